@@ -318,6 +318,158 @@ def hq_dequant_nvfp4(q: torch.Tensor, scales: torch.Tensor, s_global: torch.Tens
     return out
 
 
+# ---- products of the codes -------------------------------------------------------------------
+
+
+def _launch(device: torch.device, name: str, args: list, stream: torch.cuda.Stream | None) -> None:
+    """_call without the device switch where the device is current already: the products and norms
+    of a few rows take a few microseconds, which the switch would double."""
+    if device.index != torch.cuda.current_device():
+        _call(device, name, *args, stream=stream)
+        return
+    check(getattr(_lib.load(), name)(*args, _stream_handle(stream, device)), name)
+
+
+def _given(t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device, name: str) -> int:
+    """The address of an operand that must be there, of this shape and type, contiguous."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.device != device \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _codes(q: torch.Tensor, dims: int, name: str) -> torch.device:
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libhq has no CPU path)")
+    if q.dim() != dims or q.dtype != torch.uint8:
+        raise ValueError(f"{name} must be a {dims}-D uint8 tensor of codes")
+    return q.device
+
+
+def _tiles_bytes(rows: int, cols: int) -> int:
+    return (rows + 127) // 128 * ((cols + 3) // 4) * 512
+
+
+def _out(out: torch.Tensor | None, shape: tuple, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    if out is None:
+        if dtype not in _DTYPES:
+            raise ValueError(f"out_dtype must be float32 or bfloat16, got {dtype}")
+        return torch.empty(shape, dtype=dtype, device=device)
+    if out.dtype not in _DTYPES:
+        raise ValueError(f"out must be float32 or bfloat16, got {out.dtype}")
+    _given(out, shape, out.dtype, device, "out")
+    return out
+
+
+def _grouped_gemm(xq, xs, x_sg, wq, ws, w_sg, offsets, out, out_dtype, stream):
+    block = 16 if x_sg is not None else 32
+    dev = _codes(xq, 2, "xq")
+    _codes(wq, 3, "wq")
+    M, K2 = xq.shape
+    E, N, K = wq.shape[0], wq.shape[1], 2 * K2
+    args = [_given(xq, (M, K2), torch.uint8, dev, "xq"),
+            _given(xs, (M, K // block), torch.uint8, dev, "xs")]
+    if x_sg is not None:
+        args.append(_given(x_sg, (1,), torch.float32, dev, "x_sg"))
+    args += [_given(wq, (E, N, K2), torch.uint8, dev, "wq"),
+             _given(ws, (E, _tiles_bytes(N, K // block)), torch.uint8, dev, "ws")]
+    if x_sg is not None:
+        args.append(_given(w_sg, (E,), torch.float32, dev, "w_sg"))
+    args.append(_given(offsets, (E + 1,), torch.int32, dev, "offsets"))
+    out = _out(out, (M, N), out_dtype, dev)
+    args += [M, N, K, E, out.data_ptr(), _DTYPES[out.dtype]]
+    _launch(dev, "hq_grouped_gemm_nvfp4" if x_sg is not None else "hq_grouped_gemm_mxfp4", args, stream)
+    return out
+
+
+def hq_grouped_gemm_nvfp4(xq: torch.Tensor, xs: torch.Tensor, x_sg: torch.Tensor, wq: torch.Tensor,
+                          ws: torch.Tensor, w_sg: torch.Tensor, offsets: torch.Tensor,
+                          out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                          stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """Products grouped by expert: out [M, N], rows offsets[e] .. offsets[e + 1] of x times the
+    transpose of expert e's weights.
+
+    xq uint8 [M, K/2], xs uint8 [M, K/16], x_sg float32 [1]: the activations as hq_quantize_nvfp4
+    writes them; wq uint8 [E, N, K/2], ws uint8 [E, hq_swizzled_scales_bytes(N, K)] in the tile
+    layout (hq_swizzle_scales), w_sg float32 [E]; offsets int32 [E + 1].  Rows of no group are left
+    as they are in ``out``."""
+    if x_sg is None:
+        raise ValueError("x_sg must be a tensor (hq_grouped_gemm_mxfp4 has no per-tensor scales)")
+    return _grouped_gemm(xq, xs, x_sg, wq, ws, w_sg, offsets, out, out_dtype, stream)
+
+
+def hq_grouped_gemm_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
+                          offsets: torch.Tensor, out: torch.Tensor | None = None,
+                          out_dtype: torch.dtype = torch.bfloat16,
+                          stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """hq_grouped_gemm_nvfp4 for MXFP4 operands: xs uint8 [M, K/32] as hq_rotate_quant_mxfp4 writes it,
+    ws uint8 [E, ...] = hq_swizzle_scales of [E, N, K/32]."""
+    return _grouped_gemm(xq, xs, None, wq, ws, None, offsets, out, out_dtype, stream)
+
+
+def _grouped_wgrad(gq, gs, g_sg, xq, xs, x_sg, offsets, out, out_dtype, stream):
+    block = 16 if g_sg is not None else 32
+    dev = _codes(gq, 2, "gq")
+    _codes(xq, 2, "xq")
+    N, T2 = gq.shape
+    K, T = xq.shape[0], 2 * T2
+    args = [_given(gq, (N, T2), torch.uint8, dev, "gq"),
+            _given(gs, (_tiles_bytes(N, T // block),), torch.uint8, dev, "gs")]
+    if g_sg is not None:
+        args.append(_given(g_sg, (1,), torch.float32, dev, "g_sg"))
+    args += [_given(xq, (K, T2), torch.uint8, dev, "xq"),
+             _given(xs, (_tiles_bytes(K, T // block),), torch.uint8, dev, "xs")]
+    if g_sg is not None:
+        args.append(_given(x_sg, (1,), torch.float32, dev, "x_sg"))
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be a 1-D int32 tensor of E + 1 values")
+    E = offsets.shape[0] - 1
+    args.append(_given(offsets, (E + 1,), torch.int32, dev, "offsets"))
+    out = _out(out, (E, N, K), out_dtype, dev)
+    args += [T, N, K, E, out.data_ptr(), _DTYPES[out.dtype]]
+    _launch(dev, "hq_grouped_wgrad_nvfp4" if g_sg is not None else "hq_grouped_wgrad_mxfp4", args, stream)
+    return out
+
+
+def hq_grouped_wgrad_nvfp4(gq: torch.Tensor, gs: torch.Tensor, g_sg: torch.Tensor, xq: torch.Tensor,
+                           xs: torch.Tensor, x_sg: torch.Tensor, offsets: torch.Tensor,
+                           out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                           stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """The weights' gradients of hq_grouped_gemm: out [E, N, K], the sum over each expert's tokens.
+
+    gq uint8 [N, T/2] and xq uint8 [K, T/2]: dy and x transposed and quantized along the tokens, each
+    expert padded with zeros to a multiple of 128 tokens; gs, xs their scales in the tile layout
+    (hq_rotate_quant_nvfp4_swizzled writes it); offsets int32 [E + 1], multiples of 128."""
+    if g_sg is None:
+        raise ValueError("g_sg must be a tensor (hq_grouped_wgrad_mxfp4 has no per-tensor scales)")
+    return _grouped_wgrad(gq, gs, g_sg, xq, xs, x_sg, offsets, out, out_dtype, stream)
+
+
+def hq_grouped_wgrad_mxfp4(gq: torch.Tensor, gs: torch.Tensor, xq: torch.Tensor, xs: torch.Tensor,
+                           offsets: torch.Tensor, out: torch.Tensor | None = None,
+                           out_dtype: torch.dtype = torch.bfloat16,
+                           stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """hq_grouped_wgrad_nvfp4 for MXFP4 operands (scales through hq_swizzle_scales)."""
+    return _grouped_wgrad(gq, gs, None, xq, xs, None, offsets, out, out_dtype, stream)
+
+
+def hq_swizzle_scales(scales: torch.Tensor, out: torch.Tensor | None = None,
+                      stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """Row-major block scales uint8 [rows, cols] or [E, rows, cols] into the tile layout: uint8 [bytes]
+    or [E, bytes], bytes = ceil(rows / 128) * ceil(cols / 4) * 512."""
+    if not isinstance(scales, torch.Tensor) or not scales.is_cuda:
+        raise ValueError("scales must be a CUDA tensor (libhq has no CPU path)")
+    if scales.dim() not in (2, 3):
+        raise ValueError("scales must be [rows, cols] or [E, rows, cols]")
+    dev = scales.device
+    ptr = _given(scales, scales.shape, torch.uint8, dev, "scales")
+    rows, cols = scales.shape[-2:]
+    groups = scales.shape[0] if scales.dim() == 3 else 1
+    out = _need(out, (*scales.shape[:-2], _tiles_bytes(rows, cols)), torch.uint8, dev, "out")
+    _launch(dev, "hq_swizzle_scales", [ptr, groups, rows, cols, out.data_ptr()], stream)
+    return out
+
+
 def quantize_nvfp4(x: torch.Tensor, group: int, stream: torch.cuda.Stream | None = None):
     """Both passes: (q, scales, s_global, amax), all on x's device (hq_quantize_nvfp4)."""
     return hq_quantize_nvfp4(x, group, stream=stream)

@@ -699,6 +699,10 @@ hq_status hq_read_fault(unsigned int* fault, int clear) {
   e = hq::int8_fault_word(&int8_word, clear != 0);
   if (e != cudaSuccess) return cuda_fail(e);
   *fault |= int8_word;
+  unsigned int gemm_word = 0;  // the FP4 products' copy (hq_gemm.cu)
+  e = hq::gemm_fault_word(&gemm_word, clear != 0);
+  if (e != cudaSuccess) return cuda_fail(e);
+  *fault |= gemm_word;
   return HQ_OK;
 }
 

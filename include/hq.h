@@ -318,6 +318,84 @@ HQ_API hq_status hq_dequant_nvfp4(const uint8_t* q, const uint8_t* scales, const
                            int64_t M, int64_t K, int group, int unrotate, float* out,
                            hq_stream stream);
 
+/*
+ * Products of the codes.
+ *
+ * The calls below multiply matrices of E2M1 codes with block scales, as the quantizing calls
+ * above write them, on the tensor cores: exact products of codes and scales, fp32 sums, the
+ * product of the per-tensor scales applied in fp32, one rounding to the output's type.  A
+ * rotation of both operands by the same orthonormal symmetric H along the summed axis cancels
+ * ((x H)(w H)^T = x w^T), so operands are rotated alike or not at all.
+ *
+ * No gradient passes through the codes.  A training step's three products are three calls:
+ * y = hq_grouped_gemm(x, w); dx = hq_grouped_gemm(dy quantized along N, w^T quantized along N);
+ * dw = hq_grouped_wgrad(dy^T, x^T, both quantized along the tokens).
+ *
+ * Shared by them:
+ *   - Codes: two per byte, even element in the low nibble, rows contiguous, 16-byte aligned.
+ *   - Scales "in the tile layout" are those of hq_rotate_quant_nvfp4_swizzled, or of
+ *     hq_swizzle_scales for either format: padding entries must be 0.  32-byte aligned.
+ *   - offsets: int32 [E + 1] on the device, non-decreasing from 0: group e is the half-open range
+ *     offsets[e] .. offsets[e + 1].  Values outside the tensor are clamped to it; the host never
+ *     reads them.  E <= 1024.
+ *   - out_dtype: HQ_BF16 or HQ_F32; out is row-major and contiguous, aligned to its element.
+ *   - Sizes beyond 2^31 - 1024 return HQ_ERR_SHAPE.
+ *   - A launch may start while the kernel before it on the stream ends; it waits for that kernel
+ *     before it reads.
+ */
+
+/*
+ * hq_grouped_gemm_nvfp4 -- products grouped by expert, ragged rows (NVFP4 operands):
+ *   out[m, n] = x_sg * w_sg[e] * sum_k x[m, k] w[e, n, k]    for the rows m of group e.
+ *   Rows that belong to no group are not written.  An empty group costs nothing.
+ *
+ *   xq [M, K/2], xs [M, K/16] row-major (hq_quantize_nvfp4, hq_rotate_quant_nvfp4), x_sg 1 float;
+ *   wq [E, N, K/2], ws E buffers of hq_swizzled_scales_bytes(N, K) in the tile layout, w_sg E
+ *   floats; out [M, N].  K a multiple of 32; K == 0 zeroes out.
+ */
+HQ_API hq_status hq_grouped_gemm_nvfp4(const uint8_t* xq, const uint8_t* xs, const float* x_sg,
+                                       const uint8_t* wq, const uint8_t* ws, const float* w_sg,
+                                       const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+                                       int64_t E, void* out, hq_dtype out_dtype, hq_stream stream);
+
+/* hq_grouped_gemm_mxfp4 -- the same for MXFP4 operands: xs [M, K/32], ws E buffers of
+ * hq_swizzled_scales_bytes(N, K/2) (hq_swizzle_scales of [E, N, K/32]), no per-tensor scales. */
+HQ_API hq_status hq_grouped_gemm_mxfp4(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq,
+                                       const uint8_t* ws, const int32_t* offsets, int64_t M,
+                                       int64_t N, int64_t K, int64_t E, void* out,
+                                       hq_dtype out_dtype, hq_stream stream);
+
+/*
+ * hq_grouped_wgrad_nvfp4 -- the weights' gradients of the products above: the summed axis is the
+ * ragged one.
+ *   out[e, n, k] = g_sg * x_sg * sum_{t in group e} g[n, t] x[k, t];   0 for an empty group.
+ *
+ *   gq [N, T/2] and xq [K, T/2]: dy and x transposed, quantized (and rotated) along the tokens;
+ *   gs, xs: hq_swizzled_scales_bytes(N, T) and (K, T) in the tile layout; out [E, N, K].  Each
+ *   expert's tokens are padded with zeros to a multiple of 128, so T and the offsets are multiples
+ *   of 128 (other offsets are rounded down).
+ */
+HQ_API hq_status hq_grouped_wgrad_nvfp4(const uint8_t* gq, const uint8_t* gs, const float* g_sg,
+                                        const uint8_t* xq, const uint8_t* xs, const float* x_sg,
+                                        const int32_t* offsets, int64_t T, int64_t N, int64_t K,
+                                        int64_t E, void* out, hq_dtype out_dtype, hq_stream stream);
+
+/* hq_grouped_wgrad_mxfp4 -- the same for MXFP4 operands (scales hq_swizzled_scales_bytes(N, T/2) and
+ * (K, T/2)). */
+HQ_API hq_status hq_grouped_wgrad_mxfp4(const uint8_t* gq, const uint8_t* gs, const uint8_t* xq,
+                                        const uint8_t* xs, const int32_t* offsets, int64_t T,
+                                        int64_t N, int64_t K, int64_t E, void* out,
+                                        hq_dtype out_dtype, hq_stream stream);
+
+/*
+ * hq_swizzle_scales -- row-major block scales into the tile layout of
+ * hq_rotate_quant_nvfp4_swizzled (for weights' scales, laid out once, and for MXFP4).
+ *   scales: uint8 [groups, rows, cols], any alignment; out: groups buffers of
+ *   hq_swizzled_scales_bytes(rows, 16 * cols) bytes, every byte written, padding as 0.
+ */
+HQ_API hq_status hq_swizzle_scales(const uint8_t* scales, int64_t groups, int64_t rows,
+                                   int64_t cols, uint8_t* out, hq_stream stream);
+
 /* Human-readable name of a status code (static storage). */
 HQ_API const char* hq_status_string(hq_status status);
 
