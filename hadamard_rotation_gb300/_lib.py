@@ -109,6 +109,15 @@ def load() -> ctypes.CDLL:
         lib.hq_grouped_wgrad_mxfp4.restype = i32
         lib.hq_swizzle_scales.argtypes = [p, i64, i64, i64, p, p]
         lib.hq_swizzle_scales.restype = i32
+        f32 = ctypes.c_float
+        lib.hq_block_norm.argtypes = [p, i64, p, i64, i32, i64, i64, p, p, i32, i32, p, i64, i32, f32, f32,
+                                      p, p, p, p, i32, p, p]
+        lib.hq_block_norm.restype = i32
+        lib.hq_block_norm_bwd.argtypes = [p, i64, p, i64, p, i64, p, i64, i32, i64, i64, p, p, i32, i32, p, i64,
+                                          i32, p, p, f32, p, p, p, p, p, p, p]
+        lib.hq_block_norm_bwd.restype = i32
+        lib.hq_block_norm_bwd_workspace_bytes.argtypes = [i64, i64]
+        lib.hq_block_norm_bwd_workspace_bytes.restype = i64
         lib.hq_version.argtypes = []
         lib.hq_version.restype = i32
         _lib = lib

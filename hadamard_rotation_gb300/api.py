@@ -470,6 +470,158 @@ def hq_swizzle_scales(scales: torch.Tensor, out: torch.Tensor | None = None,
     return out
 
 
+# ---- norms before and after a block ------------------------------------------------------------
+
+_GATE_NONE, _GATE_CHANNEL, _GATE_TOKEN, _GATE_FULL = range(4)
+_NORM_POST, _NORM_PRE = 1, 2
+
+
+def _rows(t: torch.Tensor | None, like: torch.Tensor, name: str) -> tuple[int | None, int]:
+    """Address and row stride of a tensor shaped and typed like ``like`` (None: absent)."""
+    if t is None:
+        return None, like.shape[1]
+    if not isinstance(t, torch.Tensor) or t.shape != like.shape or t.dtype != like.dtype or t.device != like.device \
+            or t.stride(1) != 1:
+        raise ValueError(f"{name} must be a {like.dtype} tensor of shape {tuple(like.shape)} on {like.device} with "
+                         "contiguous rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _norm_params(h: torch.Tensor, has_y: bool, w_post, gate, w_pre, post: bool, pre: bool):
+    """(w_post, w_pre, parameter dtype, gate kind, gate, gate row stride) for the C calls."""
+    M, D = h.shape
+    dtypes = set()
+
+    def vector(w, name):
+        if w is None:
+            return None
+        if not isinstance(w, torch.Tensor) or w.shape != (D,) or w.dtype not in _DTYPES or w.device != h.device \
+                or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 or bfloat16 tensor [{D}] on {h.device}")
+        dtypes.add(w.dtype)
+        return w.data_ptr()
+
+    if not post and w_post is not None:
+        raise ValueError("w_post without post_norm")
+    if not pre and w_pre is not None:
+        raise ValueError("w_pre without pre_norm")
+    wp, wq = vector(w_post, "w_post"), vector(w_pre, "w_pre")
+    kind, g, ld = _GATE_NONE, None, 0
+    if gate is not None:
+        if not has_y:
+            raise ValueError("gate without y")
+        if not isinstance(gate, torch.Tensor):
+            raise ValueError("gate must be a tensor")
+        if gate.dim() == 1:
+            kind, g = _GATE_CHANNEL, vector(gate, "gate")
+        elif gate.shape == (M, 1) and D != 1:
+            if gate.dtype not in _DTYPES or gate.device != h.device or not gate.is_contiguous():
+                raise ValueError(f"gate [M, 1] must be a contiguous float32 or bfloat16 tensor on {h.device}")
+            dtypes.add(gate.dtype)
+            kind, g = _GATE_TOKEN, gate.data_ptr()
+        else:
+            kind = _GATE_FULL
+            g, ld = _rows(gate, h, "gate ([D], [M, 1] or [M, D])")
+    if len(dtypes) > 1:
+        raise ValueError("w_post, w_pre and a gate [D] or [M, 1] must have one dtype")
+    return wp, wq, _DTYPES[dtypes.pop()] if dtypes else HQ_F32, kind, g, ld
+
+
+def _norm_input(t: torch.Tensor, name: str) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libhq has no CPU path)")
+    if t.dim() != 2 or t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be a 2-D float32 or bfloat16 tensor [M, D]")
+
+
+def hq_block_norm(h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
+                  gate: torch.Tensor | None = None, w_pre: torch.Tensor | None = None, alpha: float = 1.0,
+                  eps: float = 1e-6, post_norm: bool = True, pre_norm: bool = True,
+                  amax_group: int | None = None, h_out: torch.Tensor | None = None,
+                  n: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """The norms after a block and before the next, with gate and residual scale, in one pass:
+    h_out = alpha * h + gate * norm(y) w_post, n = norm(h_out) w_pre.  Returns (h_out, n, r_post, r_pre),
+    None for what is not computed, and with ``amax_group`` (0, 16, 256) also the amax of n rotated, as
+    hq_rot_amax(n, amax_group) gives it.
+
+    ``gate``: [D], [M, 1] or [M, D].  ``post_norm=False``: y is added without a norm.  ``y=None``: the
+    norm of h alone (h_out is h).  Norms are x / sqrt(mean(x^2) + eps); weights default to ones."""
+    _norm_input(h, "h")
+    M, D = h.shape
+    post = post_norm and y is not None
+    hp, ld_h = _rows(h, h, "h")
+    yp, ld_y = _rows(y, h, "y")
+    wp, wq, pdt, kind, g, ld_g = _norm_params(h, y is not None, w_post, gate, w_pre, post, pre_norm)
+    if y is not None:
+        h_out = _need(h_out, (M, D), h.dtype, h.device, "h_out")
+    else:
+        h_out = h
+    n = _need(n, (M, D), h.dtype, h.device, "n") if pre_norm else None
+    r_post = torch.empty(M, dtype=torch.float32, device=h.device) if post else None
+    r_pre = torch.empty(M, dtype=torch.float32, device=h.device) if pre_norm else None
+    amax = torch.empty(1, dtype=torch.float32, device=h.device) if amax_group is not None else None
+    _launch(h.device, "hq_block_norm",
+            [hp, ld_h, yp, ld_y, _DTYPES[h.dtype], M, D, wp, wq, pdt, kind, g, ld_g,
+             (_NORM_POST if post else 0) | (_NORM_PRE if pre_norm else 0), alpha, eps,
+             h_out.data_ptr() if y is not None else None, _addr(n), _addr(r_post), _addr(r_pre), amax_group or 0,
+             _addr(amax)], stream)
+    return (h_out, n, r_post, r_pre) if amax is None else (h_out, n, r_post, r_pre, amax)
+
+
+def hq_block_norm_bwd_workspace_bytes(M: int, D: int) -> int:
+    """Bytes of the workspace of hq_block_norm_bwd (which this binding allocates itself)."""
+    n = _lib.load().hq_block_norm_bwd_workspace_bytes(M, D)
+    if n < 0:
+        raise ValueError("hq_block_norm_bwd_workspace_bytes: M >= 0, D a multiple of 16 up to 32768")
+    return n
+
+
+def hq_block_norm_bwd(dh_out: torch.Tensor | None, dn: torch.Tensor | None, h_out: torch.Tensor,
+                      y: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
+                      gate: torch.Tensor | None = None, w_pre: torch.Tensor | None = None,
+                      r_post: torch.Tensor | None = None, r_pre: torch.Tensor | None = None,
+                      alpha: float = 1.0, post_norm: bool = True, pre_norm: bool = True,
+                      stream: torch.cuda.Stream | None = None):
+    """Gradients of hq_block_norm: (dh, dy, dw_post, dgate, dw_pre), None for what has none.
+
+    ``dh_out`` (None: zeros) and ``dn`` are the gradients at h_out and n; h_out, r_post and r_pre are what
+    the forward call returned (h itself where y is None).  dw_post, dw_pre and the gradients of gates [D]
+    and [M, 1] are float32, summed over the rows in a fixed order; that of a gate [M, D] has its dtype."""
+    _norm_input(h_out, "h_out")
+    M, D = h_out.shape
+    dev = h_out.device
+    post = post_norm and y is not None
+    if pre_norm and (dn is None or r_pre is None):
+        raise ValueError("dn and r_pre are needed with pre_norm")
+    if not pre_norm and (dn is not None or dh_out is None):
+        raise ValueError("without pre_norm there is no dn, and dh_out is needed")
+    if post and r_post is None:
+        raise ValueError("r_post is needed with post_norm")
+    (dhp, ld_dh), (dnp, ld_dn) = _rows(dh_out, h_out, "dh_out"), _rows(dn, h_out, "dn")
+    (hp, ld_h), (yp, ld_y) = _rows(h_out, h_out, "h_out"), _rows(y, h_out, "y")
+    wp, wq, pdt, kind, g, ld_g = _norm_params(h_out, y is not None, w_post, gate, w_pre, post, pre_norm)
+    rp = _given(r_post, (M,), torch.float32, dev, "r_post") if post else None
+    rq = _given(r_pre, (M,), torch.float32, dev, "r_pre") if pre_norm else None
+    dh = torch.empty((M, D), dtype=h_out.dtype, device=dev)
+    dy = torch.empty((M, D), dtype=h_out.dtype, device=dev) if y is not None else None
+    dw_post = torch.empty(D, dtype=torch.float32, device=dev) if w_post is not None else None
+    dw_pre = torch.empty(D, dtype=torch.float32, device=dev) if w_pre is not None else None
+    dgate = None if kind == _GATE_NONE else torch.empty(
+        gate.shape, dtype=h_out.dtype if kind == _GATE_FULL else torch.float32, device=dev)
+    work = torch.empty(hq_block_norm_bwd_workspace_bytes(M, D), dtype=torch.uint8, device=dev)
+    if stream is not None:
+        work.record_stream(stream)  # freed when this call returns: not before the stream is done with it
+    _launch(dev, "hq_block_norm_bwd",
+            [dhp, ld_dh, dnp, ld_dn, hp, ld_h, yp, ld_y, _DTYPES[h_out.dtype], M, D, wp, wq, pdt, kind, g, ld_g,
+             (_NORM_POST if post else 0) | (_NORM_PRE if pre_norm else 0), rp, rq, alpha, dh.data_ptr(),
+             _addr(dy), _addr(dw_post), _addr(dgate), _addr(dw_pre), work.data_ptr()], stream)
+    return dh, dy, dw_post, dgate, dw_pre
+
+
+def _addr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
 def quantize_nvfp4(x: torch.Tensor, group: int, stream: torch.cuda.Stream | None = None):
     """Both passes: (q, scales, s_global, amax), all on x's device (hq_quantize_nvfp4)."""
     return hq_quantize_nvfp4(x, group, stream=stream)

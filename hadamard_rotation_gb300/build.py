@@ -14,10 +14,10 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, "hq.cu"), os.path.join(CSRC, "hq_int8.cu"),
-           os.path.join(CSRC, "hq_gemm.cu"),
+           os.path.join(CSRC, "hq_gemm.cu"), os.path.join(CSRC, "hq_norm.cu"),
            os.path.join(CSRC, "hq_host.cu"), os.path.join(CSRC, "hq_noalloc.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "hq_kernels.cuh"), os.path.join(CSRC, "hq_int8.cuh"),
-                  os.path.join(CSRC, "hq_gemm.cuh"),
+                  os.path.join(CSRC, "hq_gemm.cuh"), os.path.join(CSRC, "hq_norm.cuh"),
                   os.path.join(CSRC, "hq_internal.h"),
                   os.path.join(INCLUDE, "hq.h")]
 LIB = os.path.join(PKG, "libhq.so")

@@ -703,6 +703,10 @@ hq_status hq_read_fault(unsigned int* fault, int clear) {
   e = hq::gemm_fault_word(&gemm_word, clear != 0);
   if (e != cudaSuccess) return cuda_fail(e);
   *fault |= gemm_word;
+  unsigned int norm_word = 0;  // the norms' copy (hq_norm.cu)
+  e = hq::norm_fault_word(&norm_word, clear != 0);
+  if (e != cudaSuccess) return cuda_fail(e);
+  *fault |= norm_word;
   return HQ_OK;
 }
 

@@ -18,6 +18,8 @@ cudaError_t int8_fault_word(unsigned int* fault, bool clear);
 
 // The same for the FP4 products' translation unit (hq_gemm.cu).
 cudaError_t gemm_fault_word(unsigned int* fault, bool clear);
+// And for the norms' (hq_norm.cu).
+cudaError_t norm_fault_word(unsigned int* fault, bool clear);
 
 // Launch the bounded-wait self-test kernel of the int8 translation unit on `stream`.
 cudaError_t int8_selftest_bounded_wait(cudaStream_t stream);

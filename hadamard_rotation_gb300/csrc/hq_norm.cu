@@ -1,0 +1,283 @@
+// hq_norm.cu -- C ABI of the norms before and after a block (include/hq.h) and their launch logic.
+// The kernels are in hq_norm.cuh.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "hq.h"
+#include "hq_internal.h"
+#include "hq_norm.cuh"
+
+namespace {
+
+using hq::cuda_fail;
+using hq::NormParams;
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+constexpr int64_t kMaxD = 32768;
+constexpr int kSmemBytes = 216 * 1024;  // ring and parameters, of the 227 KB a CTA may have
+
+// Columns per CTA: two units per thread, and no more than leave room for two stages.
+struct Shape {
+  int ranks, cols, tpr, units, rows, stages;
+  size_t smem;
+};
+
+Shape shape_of(int64_t M, int D, int es, int tensors, int sms) {
+  Shape s;
+  const int most = tensors == 4 && es == 4 ? 4096 : 8192;
+  s.ranks = (D + most - 1) / most;
+  s.cols = ((D + s.ranks - 1) / s.ranks + 255) / 256 * 256;  // whole rotation groups
+  if (s.ranks == 1) s.cols = D;
+  const int u = (s.cols + 7) / 8;
+  s.units = u > hq::kNormThreads ? 2 : 1;
+  s.tpr = ((u + s.units - 1) / s.units + 31) / 32 * 32;
+  // narrow rows: several per step, while every SM still gets a step
+  int64_t rows = s.ranks > 1 ? 1 : hq::kNormThreads / s.tpr;
+  if (rows > (M + sms - 1) / sms) rows = (M + sms - 1) / sms;
+  s.rows = static_cast<int>(rows);
+  const size_t stage = static_cast<size_t>(tensors) * s.rows * s.cols * es, params = 8 * static_cast<size_t>(s.cols);
+  size_t n = (kSmemBytes - params) / stage;
+  s.stages = static_cast<int>(n > hq::kNormMaxStages ? hq::kNormMaxStages : n);
+  s.smem = params + s.stages * stage;
+  if (s.smem < 2 * params) s.smem = 2 * params;  // the backward kernel's column sums lie over the ring
+  return s;
+}
+
+template <typename Kernel>
+cudaError_t launch(Kernel kernel, const NormParams& p, const Shape& s, int clusters, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(s.smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * s.ranks));
+  cfg.blockDim = dim3(static_cast<unsigned>(s.tpr * s.rows));
+  cfg.dynamicSmemBytes = s.smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(s.ranks);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+cudaError_t sm_count(int* sms) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) : e;
+}
+
+int clusters_of(const Shape& s, int64_t M, int sms) {
+  const int64_t steps = (M + s.rows - 1) / s.rows;
+  int64_t n = sms / s.ranks;
+  if (n > hq::kNormMaxPartials) n = hq::kNormMaxPartials;
+  if (n > steps) n = steps;
+  return static_cast<int>(n < 1 ? 1 : n);
+}
+
+hq_status check_sizes(hq_dtype dt, hq_dtype params, int64_t M, int64_t D, hq_gate_kind kind, const void* gate,
+                      bool has_y) {
+  if ((dt != HQ_F32 && dt != HQ_BF16) || (params != HQ_F32 && params != HQ_BF16)) return HQ_ERR_DTYPE;
+  if (M < 0 || D <= 0 || D > kMaxD || D % 16 != 0 || M > INT64_MAX / (D * 4)) return HQ_ERR_SHAPE;
+  if (kind < HQ_GATE_NONE || kind > HQ_GATE_FULL) return HQ_ERR_SHAPE;
+  if (kind != HQ_GATE_NONE && !has_y) return HQ_ERR_NULL;
+  if (kind != HQ_GATE_NONE && !gate && M > 0) return HQ_ERR_NULL;
+  return HQ_OK;
+}
+
+// A tensor [M, D] with row stride ld (elements).
+hq_status check_rows(const void* x, int64_t M, int64_t D, int64_t ld, int es) {
+  if (ld < D || ld > INT64_MAX / es || (M > 1 && ld > INT64_MAX / es / M)) return HQ_ERR_SHAPE;
+  if (!aligned(x, 16) || (M > 1 && ld * es % 16 != 0)) return HQ_ERR_ALIGN;
+  return HQ_OK;
+}
+
+hq_status check_params(hq_gate_kind kind, const void* gate, int64_t M, int64_t D, int64_t ld_gate, int es,
+                       const void* w_post, const void* w_pre, int ps) {
+  if (!aligned(w_post, ps) || !aligned(w_pre, ps)) return HQ_ERR_ALIGN;
+  if (kind == HQ_GATE_FULL) return check_rows(gate, M, D, ld_gate, es);
+  return kind != HQ_GATE_NONE && !aligned(gate, ps) ? HQ_ERR_ALIGN : HQ_OK;
+}
+
+}  // namespace
+
+cudaError_t hq::norm_fault_word(unsigned int* fault, bool clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(fault, g_hq_fault, sizeof(unsigned int));
+  if (e == cudaSuccess && clear && *fault) {
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_hq_fault, &zero, sizeof(unsigned int));
+  }
+  return e;
+}
+
+extern "C" {
+
+hq_status hq_block_norm(const void* h, int64_t ld_h, const void* y, int64_t ld_y, hq_dtype dtype, int64_t M, int64_t D,
+                        const void* w_post, const void* w_pre, hq_dtype param_dtype, hq_gate_kind gate_kind,
+                        const void* gate, int64_t ld_gate, int norms, float alpha, float eps, void* h_out, void* n,
+                        float* r_post, float* r_pre, int group, float* amax, hq_stream stream) {
+  const bool post = norms & HQ_NORM_POST, pre = norms & HQ_NORM_PRE;
+  hq_status st = check_sizes(dtype, param_dtype, M, D, gate_kind, gate, y != nullptr || M == 0);
+  if (st != HQ_OK) return st;
+  if (norms & ~(HQ_NORM_POST | HQ_NORM_PRE)) return HQ_ERR_SHAPE;
+  if (amax && group != 0 && group != 16 && group != 256) return HQ_ERR_GROUP;
+  if (amax && D % (group ? group : 16) != 0) return HQ_ERR_SHAPE;
+  if (amax && (!pre || !aligned(amax, 4))) return pre ? HQ_ERR_ALIGN : HQ_ERR_NULL;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    const cudaError_t e = amax ? cudaMemsetAsync(amax, 0, 4, cs) : cudaSuccess;
+    return e == cudaSuccess ? HQ_OK : cuda_fail(e);
+  }
+  if (!h || (post && !y) || (!y && !pre) || (y && !h_out) || (post && !r_post) || (pre && (!n || !r_pre)))
+    return HQ_ERR_NULL;
+  const int es = dtype == HQ_BF16 ? 2 : 4, ps = param_dtype == HQ_BF16 ? 2 : 4;
+  if ((st = check_rows(h, M, D, ld_h, es)) != HQ_OK) return st;
+  if (y && (st = check_rows(y, M, D, ld_y, es)) != HQ_OK) return st;
+  if ((st = check_params(gate_kind, gate, M, D, ld_gate, es, w_post, w_pre, ps)) != HQ_OK) return st;
+  if (!aligned(h_out, 16) || !aligned(n, 16) || !aligned(r_post, 4) || !aligned(r_pre, 4)) return HQ_ERR_ALIGN;
+
+  NormParams p = {};
+  p.in[0] = static_cast<const uint8_t*>(h);
+  p.in[1] = static_cast<const uint8_t*>(y);
+  p.ld[0] = ld_h * es;
+  p.ld[1] = ld_y * es;
+  p.w_post = w_post;
+  p.w_pre = w_pre;
+  p.gate = gate;
+  p.ld_gate = ld_gate * es;
+  p.params_bf16 = param_dtype == HQ_BF16;
+  p.gate_kind = gate_kind;
+  p.post = post;
+  p.pre = pre;
+  p.has_y = y != nullptr;
+  p.M = M;
+  p.D = static_cast<int>(D);
+  p.alpha = alpha;
+  p.eps = eps;
+  p.h_out = h_out;
+  p.n = n;
+  p.r_post = r_post;
+  p.r_pre = r_pre;
+  p.group = amax ? group : -1;
+  p.amax = reinterpret_cast<unsigned*>(amax);
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  const Shape s = shape_of(M, p.D, es, 2, sms);
+  p.cols = s.cols;
+  p.tpr = s.tpr;
+  p.rows = s.rows;
+  p.stages = s.stages;
+  if (amax && (e = cudaMemsetAsync(amax, 0, 4, cs)) != cudaSuccess) return cuda_fail(e);
+  const int n_cl = clusters_of(s, M, sms);
+  if (dtype == HQ_BF16)
+    e = s.units == 1 ? launch(hq::k_block_norm<true, 1>, p, s, n_cl, cs) : launch(hq::k_block_norm<true, 2>, p, s, n_cl, cs);
+  else
+    e = s.units == 1 ? launch(hq::k_block_norm<false, 1>, p, s, n_cl, cs) : launch(hq::k_block_norm<false, 2>, p, s, n_cl, cs);
+  return e == cudaSuccess ? HQ_OK : cuda_fail(e);
+}
+
+int64_t hq_block_norm_bwd_workspace_bytes(int64_t M, int64_t D) {
+  if (M < 0 || D <= 0 || D > kMaxD || D % 16 != 0) return -1;
+  return 8 * D * (M < hq::kNormMaxPartials ? M : hq::kNormMaxPartials);
+}
+
+hq_status hq_block_norm_bwd(const void* dh_out, int64_t ld_dh, const void* dn, int64_t ld_dn, const void* h_out,
+                            int64_t ld_h, const void* y, int64_t ld_y, hq_dtype dtype, int64_t M, int64_t D,
+                            const void* w_post, const void* w_pre, hq_dtype param_dtype, hq_gate_kind gate_kind,
+                            const void* gate, int64_t ld_gate, int norms, const float* r_post, const float* r_pre,
+                            float alpha, void* dh, void* dy, float* dw_post, void* dgate, float* dw_pre,
+                            void* workspace, hq_stream stream) {
+  const bool post = norms & HQ_NORM_POST, pre = norms & HQ_NORM_PRE;
+  hq_status st = check_sizes(dtype, param_dtype, M, D, gate_kind, gate, y != nullptr || M == 0);
+  if (st != HQ_OK) return st;
+  if (norms & ~(HQ_NORM_POST | HQ_NORM_PRE)) return HQ_ERR_SHAPE;
+  const bool channel = gate_kind == HQ_GATE_CHANNEL;
+  if (!aligned(dw_post, 4) || !aligned(dw_pre, 4) || !aligned(dgate, gate_kind == HQ_GATE_FULL ? 16 : 4)) return HQ_ERR_ALIGN;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (M == 0) {  // empty sums
+    if (dw_post) e = cudaMemsetAsync(dw_post, 0, D * 4, cs);
+    if (e == cudaSuccess && dw_pre) e = cudaMemsetAsync(dw_pre, 0, D * 4, cs);
+    if (e == cudaSuccess && dgate && channel) e = cudaMemsetAsync(dgate, 0, D * 4, cs);
+    return e == cudaSuccess ? HQ_OK : cuda_fail(e);
+  }
+  if ((!dh_out && !pre) || (pre && (!dn || !h_out || !r_pre)) || (post && (!y || !r_post)) || !dh || (y && !dy) ||
+      (gate_kind != HQ_GATE_NONE && !dgate) || !workspace)
+    return HQ_ERR_NULL;
+  const int es = dtype == HQ_BF16 ? 2 : 4, ps = param_dtype == HQ_BF16 ? 2 : 4;
+  if (dh_out && (st = check_rows(dh_out, M, D, ld_dh, es)) != HQ_OK) return st;
+  if (pre && (st = check_rows(dn, M, D, ld_dn, es)) != HQ_OK) return st;
+  if (pre && (st = check_rows(h_out, M, D, ld_h, es)) != HQ_OK) return st;
+  if (y && (st = check_rows(y, M, D, ld_y, es)) != HQ_OK) return st;
+  if ((st = check_params(gate_kind, gate, M, D, ld_gate, es, w_post, w_pre, ps)) != HQ_OK) return st;
+  if (!aligned(dh, 16) || !aligned(dy, 16) || !aligned(workspace, 16) || !aligned(r_post, 4) || !aligned(r_pre, 4))
+    return HQ_ERR_ALIGN;
+
+  NormParams p = {};
+  p.in[0] = pre ? static_cast<const uint8_t*>(h_out) : nullptr;
+  p.in[1] = pre ? static_cast<const uint8_t*>(dn) : nullptr;
+  p.in[2] = static_cast<const uint8_t*>(dh_out);
+  p.in[3] = static_cast<const uint8_t*>(y);
+  p.ld[0] = ld_h * es;
+  p.ld[1] = ld_dn * es;
+  p.ld[2] = ld_dh * es;
+  p.ld[3] = ld_y * es;
+  p.w_post = w_post;
+  p.w_pre = w_pre;
+  p.gate = gate;
+  p.ld_gate = ld_gate * es;
+  p.params_bf16 = param_dtype == HQ_BF16;
+  p.gate_kind = gate_kind;
+  p.post = post;
+  p.pre = pre;
+  p.has_y = y != nullptr;
+  p.M = M;
+  p.D = static_cast<int>(D);
+  p.alpha = y ? alpha : 1.0f;
+  p.r_post_in = r_post;
+  p.r_pre_in = r_pre;
+  p.dh = dh;
+  p.dy = dy;
+  p.dgate = dgate;
+  p.partial = static_cast<float*>(workspace);
+  int sms = 0;
+  if ((e = sm_count(&sms)) != cudaSuccess) return cuda_fail(e);
+  const Shape s = shape_of(M, p.D, es, 4, sms);
+  p.cols = s.cols;
+  p.tpr = s.tpr;
+  p.rows = s.rows;
+  p.stages = s.stages;
+  const int n_cl = clusters_of(s, M, sms);
+  if (dtype == HQ_BF16)
+    e = s.units == 1 ? launch(hq::k_block_norm_bwd<true, 1>, p, s, n_cl, cs)
+                     : launch(hq::k_block_norm_bwd<true, 2>, p, s, n_cl, cs);
+  else  // at most 4096 columns per CTA: one unit per thread
+    e = launch(hq::k_block_norm_bwd<false, 1>, p, s, n_cl, cs);
+  if (e != cudaSuccess) return cuda_fail(e);
+  float* const to_pre = pre ? dw_pre : nullptr;
+  float* const to_post = post ? dw_post : nullptr;
+  float* const to_gate = channel ? static_cast<float*>(dgate) : nullptr;
+  if (!to_pre && !to_post && !to_gate) return HQ_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((D + 31) / 32));
+  cfg.blockDim = dim3(256);
+  cfg.stream = cs;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, hq::k_norm_columns, const_cast<const float*>(p.partial), n_cl, p.D,
+                         post ? w_post : static_cast<const void*>(nullptr),
+                         channel ? gate : static_cast<const void*>(nullptr), p.params_bf16, to_pre, to_post, to_gate);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? HQ_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -396,6 +396,64 @@ HQ_API hq_status hq_grouped_wgrad_mxfp4(const uint8_t* gq, const uint8_t* gs, co
 HQ_API hq_status hq_swizzle_scales(const uint8_t* scales, int64_t groups, int64_t rows,
                                    int64_t cols, uint8_t* out, hq_stream stream);
 
+/*
+ * hq_block_norm -- the norms after a block and before the next one, with the block's gate and the
+ * residual scale: what makes the tensor that is quantized next, in one pass.
+ *   u = y * r_post * w_post,  r_post = 1 / sqrt(mean(y^2) + eps)   (HQ_NORM_POST; u = y without)
+ *   h_out = alpha * h + gate * u
+ *   n = h_out * r_pre * w_pre,  r_pre = 1 / sqrt(mean(h_out^2) + eps)   (HQ_NORM_PRE)
+ *   In fp32 throughout; h_out and n are each rounded once, n from the h_out before its rounding.
+ *
+ *   h, y    : [M, D] of dtype, row strides ld_h, ld_y elements; 16-byte aligned rows.  y NULL: h_out
+ *             is h and is not written (a first block's norm); then norms is HQ_NORM_PRE.
+ *   D       : a multiple of 16, at most 32768.
+ *   w_post, w_pre : [D] of param_dtype, or NULL for ones.
+ *   gate    : by gate_kind NULL, [D] or [M] of param_dtype, or [M, D] of dtype (row stride ld_gate).
+ *   h_out, n: [M, D] of dtype, contiguous, 16-byte aligned; may not overlap the inputs, except that
+ *             h_out may be h itself (ld_h == D).
+ *   r_post, r_pre : float [M], the rows' reciprocal norms for hq_block_norm_bwd.
+ *   amax    : NULL, or 1 float that receives max |n . H_group / sqrt(group)| exactly as hq_rot_amax(n)
+ *             would, so that n is quantized with one pass (hq_rotate_quant_nvfp4).  Needs HQ_NORM_PRE;
+ *             D a multiple of group.
+ */
+typedef enum {
+  HQ_GATE_NONE = 0,
+  HQ_GATE_CHANNEL = 1, /* gate [D] */
+  HQ_GATE_TOKEN = 2,   /* gate [M] */
+  HQ_GATE_FULL = 3     /* gate [M, D] */
+} hq_gate_kind;
+#define HQ_NORM_POST 1
+#define HQ_NORM_PRE 2
+
+HQ_API hq_status hq_block_norm(const void* h, int64_t ld_h, const void* y, int64_t ld_y,
+                               hq_dtype dtype, int64_t M, int64_t D, const void* w_post,
+                               const void* w_pre, hq_dtype param_dtype, hq_gate_kind gate_kind,
+                               const void* gate, int64_t ld_gate, int norms, float alpha, float eps,
+                               void* h_out, void* n, float* r_post, float* r_pre, int group,
+                               float* amax, hq_stream stream);
+
+/*
+ * hq_block_norm_bwd -- the gradients of hq_block_norm.
+ *   dh_out, dn : gradients at h_out and n, [M, D] of dtype (dh_out NULL: zeros; dn is read with
+ *                HQ_NORM_PRE).  h_out, r_post, r_pre: what the forward call wrote (h where y is NULL).
+ *   dh, dy     : [M, D] of dtype, contiguous, 16-byte aligned (dy where y is given).
+ *   dw_post, dw_pre : float [D], or NULL to skip.  Sums over the rows in fp32 in a fixed order.
+ *   dgate      : float [D] (HQ_GATE_CHANNEL), float [M] (HQ_GATE_TOKEN), [M, D] of dtype (HQ_GATE_FULL).
+ *   workspace  : hq_block_norm_bwd_workspace_bytes(M, D) bytes, 16-byte aligned; contents need no
+ *                preparation.  Calls that may run at the same time need different ones.
+ */
+HQ_API hq_status hq_block_norm_bwd(const void* dh_out, int64_t ld_dh, const void* dn, int64_t ld_dn,
+                                   const void* h_out, int64_t ld_h, const void* y, int64_t ld_y,
+                                   hq_dtype dtype, int64_t M, int64_t D, const void* w_post,
+                                   const void* w_pre, hq_dtype param_dtype, hq_gate_kind gate_kind,
+                                   const void* gate, int64_t ld_gate, int norms, const float* r_post,
+                                   const float* r_pre, float alpha, void* dh, void* dy,
+                                   float* dw_post, void* dgate, float* dw_pre, void* workspace,
+                                   hq_stream stream);
+
+/* Bytes of hq_block_norm_bwd's workspace (-1 for sizes it refuses). */
+HQ_API int64_t hq_block_norm_bwd_workspace_bytes(int64_t M, int64_t D);
+
 /* Human-readable name of a status code (static storage). */
 HQ_API const char* hq_status_string(hq_status status);
 
