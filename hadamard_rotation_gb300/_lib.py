@@ -107,6 +107,12 @@ def load() -> ctypes.CDLL:
         lib.hq_grouped_wgrad_nvfp4.restype = i32
         lib.hq_grouped_wgrad_mxfp4.argtypes = [p] * 5 + [i64] * 4 + [p, i32, p]
         lib.hq_grouped_wgrad_mxfp4.restype = i32
+        lib.hq_lora_gemm_nvfp4.argtypes = [p] * 7 + [i64] + [p] * 4 + [i64] * 5 + [p, i32, p, p]
+        lib.hq_lora_gemm_nvfp4.restype = i32
+        lib.hq_lora_gemm_mxfp4.argtypes = [p] * 5 + [i64] + [p] * 4 + [i64] * 5 + [p, i32, p, p]
+        lib.hq_lora_gemm_mxfp4.restype = i32
+        lib.hq_lora_gemm_workspace_bytes.argtypes = [i64, i64]
+        lib.hq_lora_gemm_workspace_bytes.restype = i64
         lib.hq_swizzle_scales.argtypes = [p, i64, i64, i64, p, p]
         lib.hq_swizzle_scales.restype = i32
         f32 = ctypes.c_float

@@ -453,6 +453,73 @@ def hq_grouped_wgrad_mxfp4(gq: torch.Tensor, gs: torch.Tensor, xq: torch.Tensor,
     return _grouped_wgrad(gq, gs, None, xq, xs, None, offsets, out, out_dtype, stream)
 
 
+def hq_lora_gemm_workspace_bytes(M: int, R: int) -> int:
+    """Bytes of the workspace of hq_lora_gemm_* (which this binding allocates itself)."""
+    n = _lib.load().hq_lora_gemm_workspace_bytes(M, R)
+    if n < 0:
+        raise ValueError("hq_lora_gemm_workspace_bytes: M >= 0, R a multiple of 8 up to 128")
+    return n
+
+
+def _lora_gemm(xq, xs, x_sg, wq, ws, w_sg, x, lora_a, lora_b, scaling, row_adapter, out, out_dtype, stream):
+    block = 16 if x_sg is not None else 32
+    dev = _codes(xq, 2, "xq")
+    _codes(wq, 2, "wq")
+    M, K2 = xq.shape
+    N, K = wq.shape[0], 2 * K2
+    args = [_given(xq, (M, K2), torch.uint8, dev, "xq"),
+            _given(xs, (M, K // block), torch.uint8, dev, "xs")]
+    if x_sg is not None:
+        args.append(_given(x_sg, (1,), torch.float32, dev, "x_sg"))
+    args += [_given(wq, (N, K2), torch.uint8, dev, "wq"),
+             _given(ws, (_tiles_bytes(N, K // block),), torch.uint8, dev, "ws")]
+    if x_sg is not None:
+        args.append(_given(w_sg, (1,), torch.float32, dev, "w_sg"))
+    if not isinstance(x, torch.Tensor) or x.shape != (M, K) or x.dtype != torch.bfloat16 or x.device != dev \
+            or x.stride(1) != 1:
+        raise ValueError(f"x must be a bfloat16 tensor of shape {(M, K)} on {dev} with contiguous rows")
+    if not isinstance(lora_a, torch.Tensor) or lora_a.dim() != 3:
+        raise ValueError("lora_a must be [adapters, R, K]")
+    n, R = lora_a.shape[:2]
+    args += [x.data_ptr(), x.stride(0) if M > 1 else K,
+             _given(lora_a, (n, R, K), torch.bfloat16, dev, "lora_a"),
+             _given(lora_b, (n, N, R), torch.bfloat16, dev, "lora_b"),
+             _given(scaling, (n,), torch.float32, dev, "scaling"),
+             _given(row_adapter, (M,), torch.int32, dev, "row_adapter")]
+    out = _out(out, (M, N), out_dtype, dev)
+    work = torch.empty(hq_lora_gemm_workspace_bytes(M, R), dtype=torch.uint8, device=dev)
+    if stream is not None:
+        work.record_stream(stream)  # freed when this call returns: not before the stream is done with it
+    args += [M, N, K, n, R, out.data_ptr(), _DTYPES[out.dtype], work.data_ptr()]
+    _launch(dev, "hq_lora_gemm_nvfp4" if x_sg is not None else "hq_lora_gemm_mxfp4", args, stream)
+    return out
+
+
+def hq_lora_gemm_nvfp4(xq: torch.Tensor, xs: torch.Tensor, x_sg: torch.Tensor, wq: torch.Tensor,
+                       ws: torch.Tensor, w_sg: torch.Tensor, x: torch.Tensor, lora_a: torch.Tensor,
+                       lora_b: torch.Tensor, scaling: torch.Tensor, row_adapter: torch.Tensor,
+                       out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                       stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """A shared projection with the low-rank adapters of many requests: out [M, N] =
+    x_q w_q^T + scaling[a] (x lora_a[a]^T) lora_b[a]^T, a = row_adapter[m] (none where it is negative).
+
+    xq, xs, x_sg: x quantized (hq_quantize_nvfp4); wq uint8 [N, K/2], ws its scales in the tile layout,
+    w_sg float32 [1]; x bfloat16 [M, K]; lora_a bfloat16 [n, R, K], lora_b bfloat16 [n, N, R], scaling
+    float32 [n]; row_adapter int32 [M].  R a multiple of 8 up to 128."""
+    if x_sg is None:
+        raise ValueError("x_sg must be a tensor (hq_lora_gemm_mxfp4 has no per-tensor scales)")
+    return _lora_gemm(xq, xs, x_sg, wq, ws, w_sg, x, lora_a, lora_b, scaling, row_adapter, out, out_dtype, stream)
+
+
+def hq_lora_gemm_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, x: torch.Tensor,
+                       lora_a: torch.Tensor, lora_b: torch.Tensor, scaling: torch.Tensor,
+                       row_adapter: torch.Tensor, out: torch.Tensor | None = None,
+                       out_dtype: torch.dtype = torch.bfloat16,
+                       stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """hq_lora_gemm_nvfp4 beside an MXFP4 projection."""
+    return _lora_gemm(xq, xs, None, wq, ws, None, x, lora_a, lora_b, scaling, row_adapter, out, out_dtype, stream)
+
+
 def hq_swizzle_scales(scales: torch.Tensor, out: torch.Tensor | None = None,
                       stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """Row-major block scales uint8 [rows, cols] or [E, rows, cols] into the tile layout: uint8 [bytes]

@@ -73,10 +73,10 @@ struct Codes {
   int64_t row_bytes, rows, groups;
 };
 
-template <int KIND, bool MX, int T>
+template <int KIND, bool MX, int T, bool LORA = false>
 hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t most_tiles, hq_stream stream) {
-  using S = hq::GemmShape<MX, T>;
-  auto kernel = hq::k_fp4_gemm<KIND, MX, T>;
+  using S = hq::GemmShape<MX, T, LORA>;
+  auto kernel = hq::k_fp4_gemm<KIND, MX, T, LORA>;
   CUtensorMap ma, mb;
   if (!encode_codes(&ma, a.q, a.row_bytes, a.rows, a.groups, hq::kGemmLanes, 3) ||
       !encode_codes(&mb, b.q, b.row_bytes, b.rows, 1, S::kBox, 2))
@@ -84,13 +84,13 @@ hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t most_tile
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);
-  const size_t smem = hq::gemm_smem_bytes(S::kStageBytes, S::kStages, p.groups);
+  const size_t smem = hq::gemm_smem_bytes(S::kSmemBytes, p.groups);
   if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) !=
       cudaSuccess)
     return cuda_fail(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(most_tiles < sms ? most_tiles : sms));
-  cfg.blockDim = dim3(hq::kGemmThreads);
+  cfg.blockDim = dim3(hq::kGemmThreads + (LORA ? hq::kLoraThreads : 0));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr;
@@ -111,6 +111,30 @@ hq_status out_zero(void* out, int64_t n, hq_dtype dt, hq_stream stream) {
   return e == cudaSuccess ? HQ_OK : cuda_fail(e);
 }
 
+// What grouped_gemm and lora_gemm share: the operands of a product with ragged rows.
+template <bool MX>
+GemmParams rows_params(const uint8_t* xs, const float* x_sg, const uint8_t* ws, const float* w_sg, int64_t M, int64_t N,
+                       int64_t K, int64_t groups, void* out, hq_dtype dt) {
+  GemmParams p = {};
+  p.k_tiles = static_cast<int>((K + (MX ? 127 : 63)) / (MX ? 128 : 64));
+  p.tiles_a = static_cast<int>((N + 127) / 128);
+  p.sfa = ws;
+  p.sfa_group_bytes = static_cast<int64_t>(p.tiles_a) * p.k_tiles * 512;
+  p.sfb = xs;
+  p.sfb_row_bytes = static_cast<int>(K / (MX ? 32 : 16));
+  p.sfb_vec = MX ? 8 : 16;
+  while (p.sfb_row_bytes % p.sfb_vec || !aligned(xs, p.sfb_vec)) p.sfb_vec /= 2;
+  p.sg_a = w_sg;
+  p.sg_b = x_sg;
+  p.groups = static_cast<int>(groups);
+  p.extent = static_cast<int>(M);
+  p.na = static_cast<int>(N);
+  p.k = static_cast<int>(K);
+  p.out = out;
+  p.out_f32 = dt == HQ_F32;
+  return p;
+}
+
 template <bool MX>
 hq_status grouped_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, const uint8_t* wq, const uint8_t* ws,
                        const float* w_sg, const int32_t* offsets, int64_t M, int64_t N, int64_t K, int64_t E, void* out,
@@ -129,24 +153,8 @@ hq_status grouped_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, 
   if (!xq || !xs || !wq || !ws || (!MX && (!x_sg || !w_sg))) return HQ_ERR_NULL;
   if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(ws, 32) || (!MX && (!aligned(x_sg, 4) || !aligned(w_sg, 4))))
     return HQ_ERR_ALIGN;
-  GemmParams p = {};
-  p.k_tiles = static_cast<int>((K + (MX ? 127 : 63)) / (MX ? 128 : 64));
-  p.sfa = ws;
-  p.sfa_group_bytes = tiles_a * p.k_tiles * 512;
-  p.sfb = xs;
-  p.sfb_row_bytes = static_cast<int>(K / (MX ? 32 : 16));
-  p.sfb_vec = MX ? 8 : 16;
-  while (p.sfb_row_bytes % p.sfb_vec || !aligned(xs, p.sfb_vec)) p.sfb_vec /= 2;
-  p.sg_a = w_sg;
-  p.sg_b = x_sg;
+  GemmParams p = rows_params<MX>(xs, x_sg, ws, w_sg, M, N, K, E, out, dt);
   p.offsets = offsets;
-  p.groups = static_cast<int>(E);
-  p.extent = static_cast<int>(M);
-  p.na = static_cast<int>(N);
-  p.k = static_cast<int>(K);
-  p.tiles_a = static_cast<int>(tiles_a);
-  p.out = out;
-  p.out_f32 = dt == HQ_F32;
   const Codes a = {wq, K / 2, N, E}, b = {xq, K / 2, M, 1};
   return narrow ? launch<hq::kGemmRows, MX, 64>(p, a, b, tiles, stream)
                 : launch<hq::kGemmRows, MX, 192>(p, a, b, tiles, stream);
@@ -186,6 +194,96 @@ hq_status grouped_wgrad(const uint8_t* gq, const uint8_t* gs, const float* g_sg,
   p.out_f32 = dt == HQ_F32;
   const Codes a = {xq, T / 2, K, 1}, b = {gq, T / 2, N, 1};
   return launch<hq::kGemmContr, MX, 192>(p, a, b, E * tiles_a * tiles_b, stream);
+}
+
+template <int NB, int TG>
+cudaError_t launch_shrink(hq::ShrinkParams p, int sms, cudaStream_t stream) {
+  const int tiles = (p.rows + 32 * TG - 1) / (32 * TG), chunks = p.K / 32;
+  // As many slices of k as keep every warp a chunk, up to a portable cluster; then, where few
+  // rows leave multiprocessors idle, several CTAs share a tile's adapters.
+  p.slices = 1;
+  while (p.slices < 8 && p.slices * 2 * (8 / TG) <= chunks && tiles * p.slices < 2 * sms) p.slices *= 2;
+  p.jobs = 1;
+  while (p.jobs < 32 && tiles * p.slices * p.jobs < sms) p.jobs *= 2;
+  auto kernel = hq::k_lora_shrink<NB, TG>;
+  const size_t smem = sizeof(float) * (8 / TG) * (32 * TG) * (16 * NB);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles) * p.slices * p.jobs);
+  cfg.blockDim = dim3(hq::kShrinkThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.slices);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <int TG>
+cudaError_t launch_shrink(const hq::ShrinkParams& p, int sms, cudaStream_t stream) {
+  return p.rank <= 16   ? launch_shrink<1, TG>(p, sms, stream)
+         : p.rank <= 32 ? launch_shrink<2, TG>(p, sms, stream)
+                        : launch_shrink<4, TG>(p, sms, stream);
+}
+
+template <bool MX>
+hq_status lora_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, const uint8_t* wq, const uint8_t* ws,
+                    const float* w_sg, const void* x, int64_t ldx, const void* a, const void* b, const float* scaling,
+                    const int32_t* ids, int64_t M, int64_t N, int64_t K, int64_t n, int64_t R, void* out, hq_dtype dt,
+                    void* workspace, hq_stream stream) {
+  if (dt != HQ_F32 && dt != HQ_BF16) return HQ_ERR_DTYPE;
+  if (M < 0 || N < 0 || K <= 0 || n < 0 || K % 32 != 0 || R < 8 || R > 128 || R % 8 != 0 || ldx < K)
+    return HQ_ERR_SHAPE;
+  if (M > kMaxExtent || N > kMaxExtent || K > kMaxExtent || n > kMaxExtent || ldx > INT64_MAX / 2 / (M ? M : 1))
+    return HQ_ERR_SHAPE;
+  if (M == 0 || N == 0) return HQ_OK;
+  if (!out || !xq || !xs || !wq || !ws || !x || !ids || !workspace || (n > 0 && (!a || !b || !scaling)) ||
+      (!MX && (!x_sg || !w_sg)))
+    return HQ_ERR_NULL;
+  if (!aligned(out, dt == HQ_F32 ? 4 : 2) || !aligned(xq, 16) || !aligned(wq, 16) || !aligned(ws, 32) ||
+      !aligned(x, 16) || (M > 1 && ldx % 8 != 0) || !aligned(a, 16) || !aligned(b, 16) || !aligned(scaling, 4) ||
+      !aligned(ids, 4) || !aligned(workspace, 16) || !aligned(x_sg, 4) || !aligned(w_sg, 4))
+    return HQ_ERR_ALIGN;
+  const bool narrow = M <= 64;
+  const int64_t tiles = (M + (narrow ? 63 : 191)) / (narrow ? 64 : 192) * ((N + 127) / 128);
+  if (tiles > kMaxExtent) return HQ_ERR_SHAPE;
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  hq::ShrinkParams s = {};
+  s.x = static_cast<const uint8_t*>(x);
+  s.ldx = ldx * 2;
+  s.a = static_cast<const uint8_t*>(a);
+  s.scaling = scaling;
+  s.sg_a = w_sg;
+  s.sg_b = x_sg;
+  s.ids = ids;
+  s.t = static_cast<uint8_t*>(workspace);
+  s.rows = static_cast<int>(M);
+  s.K = static_cast<int>(K);
+  s.adapters = static_cast<int>(n);
+  s.rank = static_cast<int>(R);
+  if (n > 0) {
+    e = M <= 32 ? launch_shrink<1>(s, sms, static_cast<cudaStream_t>(stream))
+                : launch_shrink<2>(s, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  GemmParams p = rows_params<MX>(xs, x_sg, ws, w_sg, M, N, K, 1, out, dt);
+  p.lora_b = static_cast<const uint8_t*>(b);
+  p.lora_t = s.t;
+  p.lora_ids = ids;
+  p.adapters = s.adapters;
+  p.rank = s.rank;
+  const Codes ca = {wq, K / 2, N, 1}, cb = {xq, K / 2, M, 1};
+  return narrow ? launch<hq::kGemmRows, MX, 64, true>(p, ca, cb, tiles, stream)
+                : launch<hq::kGemmRows, MX, 192, true>(p, ca, cb, tiles, stream);
 }
 
 // Row-major scale bytes [groups, rows, cols] -> the tile layout, a 16-byte row of a tile per thread.
@@ -246,6 +344,28 @@ hq_status hq_grouped_wgrad_mxfp4(const uint8_t* gq, const uint8_t* gs, const uin
                                  const int32_t* offsets, int64_t T, int64_t N, int64_t K, int64_t E, void* out,
                                  hq_dtype out_dtype, hq_stream stream) {
   return grouped_wgrad<true>(gq, gs, nullptr, xq, xs, nullptr, offsets, T, N, K, E, out, out_dtype, stream);
+}
+
+int64_t hq_lora_gemm_workspace_bytes(int64_t M, int64_t R) {
+  if (M < 0 || M > kMaxExtent || R < 8 || R > 128 || R % 8 != 0) return -1;
+  return 4 * M * R;
+}
+
+hq_status hq_lora_gemm_nvfp4(const uint8_t* xq, const uint8_t* xs, const float* x_sg, const uint8_t* wq,
+                             const uint8_t* ws, const float* w_sg, const void* x, int64_t ldx, const void* lora_a,
+                             const void* lora_b, const float* scaling, const int32_t* row_adapter, int64_t M,
+                             int64_t N, int64_t K, int64_t adapters, int64_t R, void* out, hq_dtype out_dtype,
+                             void* workspace, hq_stream stream) {
+  return lora_gemm<false>(xq, xs, x_sg, wq, ws, w_sg, x, ldx, lora_a, lora_b, scaling, row_adapter, M, N, K, adapters,
+                          R, out, out_dtype, workspace, stream);
+}
+
+hq_status hq_lora_gemm_mxfp4(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const uint8_t* ws, const void* x,
+                             int64_t ldx, const void* lora_a, const void* lora_b, const float* scaling,
+                             const int32_t* row_adapter, int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t R,
+                             void* out, hq_dtype out_dtype, void* workspace, hq_stream stream) {
+  return lora_gemm<true>(xq, xs, nullptr, wq, ws, nullptr, x, ldx, lora_a, lora_b, scaling, row_adapter, M, N, K,
+                         adapters, R, out, out_dtype, workspace, stream);
 }
 
 hq_status hq_swizzle_scales(const uint8_t* scales, int64_t groups, int64_t rows, int64_t cols, uint8_t* out,

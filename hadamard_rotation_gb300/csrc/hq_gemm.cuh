@@ -28,12 +28,23 @@
 //   warps 4..7    epilogue: tensor memory -> registers -> * a -> global
 //   warps 8..11   (ROWS) the tokens' scales: row-major in global memory, since a group starts at
 //                 any row; moved through registers into the tile layout
+//   warps 12..15  (adapters) the operands of the adapters' second product, below
 // Shared memory holds a ring of kStages stages (256 steps of the summed axis each); tensor
 // memory holds two accumulators, so the epilogue of a tile runs under the products of the next.
+//
+// Adapters (the shared projection of hq_lora_gemm): out += s_a (x A_a^T) B_a^T for the rows of adapter
+// a.  The first, thin product is a kernel of its own (k_lora_shrink) that leaves t = s_a x A_a^T / a in
+// two bf16 terms per value, t = hi + lo, so nothing is lost to the type (2^-17).  The second product
+// is more steps of the same accumulator: 16 bf16 columns ("a slot") hold 16 ranks of one adapter, B_a on the
+// lanes' side and t -- zero in the rows of other adapters -- on the columns' side, hi and lo in turn.
+// Four slots make a chunk; a tile takes as many as its rows have distinct adapters, so a tile of
+// one request pays for one adapter and a tile of 64 requests for those that occur.  Chunks are
+// multiplied at fixed places of the main loop: the order of the sum does not depend on timing.
 #pragma once
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <limits.h>
 
 #include "hq_kernels.cuh"
 
@@ -64,12 +75,17 @@ struct GemmParams {
   int sfb_vec;              // ROWS: bytes per load of them (rows aligned to it)
   void* out;                // ROWS: [extent, na]; CONTR: [groups, nb, na]
   int out_f32;
+  // adapters
+  const uint8_t* lora_b;    // bf16 [adapters, na, rank]
+  const uint8_t* lora_t;    // bf16 [extent][hi, lo][rank]
+  const int32_t* lora_ids;  // [extent]
+  int adapters, rank;
 };
 
 // ---------------------------------------------------------------------------
 // Geometry of one kernel instance.  T: columns of a tile (tokens, or rows of G).
 // ---------------------------------------------------------------------------
-template <bool MX, int T>
+template <bool MX, int T, bool LORA>
 struct GemmShape {
   static constexpr int kTilesPerBlock = MX ? 2 : 4;  // scale tiles along K per stage
   static constexpr int kRowTilesB = (T + 127) / 128;
@@ -80,7 +96,13 @@ struct GemmShape {
   static constexpr int kBytesSfb = kRowTilesB * kTilesPerBlock * 512;
   static constexpr int kStageBytes = kBytesA + kBytesB + kBytesSfa + kBytesSfb;
   static_assert(kStageBytes % 1024 == 0, "stages stay aligned to the swizzle atom");
-  static constexpr int kStages = (200 * 1024) / kStageBytes < 8 ? (200 * 1024) / kStageBytes : 8;
+  // adapters: chunks of 64 bf16 columns: B_a of 128 lanes, then t's hi and lo of T rows
+  static constexpr int kChunkBytes = LORA ? kGemmLanes * 128 + 2 * T * 128 : 0;
+  static constexpr int kChunks = T >= 128 ? 1 : 2;
+  static constexpr int kRingBytes = 206 * 1024 - kChunks * kChunkBytes;
+  static constexpr int kStages = kRingBytes / kStageBytes < 8 ? kRingBytes / kStageBytes : 8;
+  static constexpr int kChunkGap = T >= 128 ? 5 : 2;  // stages between two chunks of a tile
+  static constexpr int kSmemBytes = kStages * kStageBytes + kChunks * kChunkBytes;
   // tensor memory columns: two accumulators, then two sets of scales (stage parity)
   static constexpr int kColsSfa = kTilesPerBlock * 4;
   static constexpr int kColsSfb = kTilesPerBlock * kRowTilesB * 4;
@@ -94,14 +116,15 @@ struct GemmBars {
   uint64_t full[8], empty[8];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
+  uint64_t chunk_full[2], chunk_empty[2];
+  int chunk_steps[2], chunk_last[2];  // 16-column steps of a chunk; whether the tile ends with it
+  int next_id[2][4];
+  int32_t ids[192];
   uint32_t tmem;
-  int failed;
   int tiles;
 };
 
-inline size_t gemm_smem_bytes(int stage_bytes, int stages, int groups) {
-  return 1024 + static_cast<size_t>(stage_bytes) * stages + 12 * static_cast<size_t>(groups + 1);
-}
+inline size_t gemm_smem_bytes(int bytes, int groups) { return 1024 + static_cast<size_t>(bytes) + 12 * static_cast<size_t>(groups + 1); }
 
 // ---------------------------------------------------------------------------
 // PTX.
@@ -164,6 +187,14 @@ __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uin
   }
 }
 
+__device__ __forceinline__ void umma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc)
+      : "memory");
+}
+
 // Shared-memory matrix descriptors.  Codes: rows of 128 bytes, 128-byte swizzle, 8-row groups
 // 1024 bytes apart.  Scale tiles: unswizzled, 8-row groups of 16-byte rows 128 bytes apart.
 __device__ __forceinline__ uint64_t desc_codes(uint32_t addr) {
@@ -181,6 +212,11 @@ template <bool MX>
 __device__ __forceinline__ uint32_t umma_idesc(int n, int pair) {
   return (static_cast<uint32_t>(pair) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
          ((MX ? 1u : 0u) << 23) | (1u << 27) | (static_cast<uint32_t>(pair) << 29);
+}
+
+// The same for bf16 x bf16 into fp32.
+__device__ __forceinline__ uint32_t umma_idesc_bf16(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 
 // Order tensor-memory operations across a barrier between threads.
@@ -291,23 +327,40 @@ __device__ __forceinline__ void load_scale_row(const uint8_t* src, int left, int
   }
 }
 
+// The adapters' warps among themselves.
+__device__ __forceinline__ void lora_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ bool lora_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(ok))
+      : "memory");
+  return r;
+}
+
 // ---------------------------------------------------------------------------
 // The kernel.
 // ---------------------------------------------------------------------------
 constexpr int kGemmThreads = 384;
 constexpr int kScaleThreads = 128;
 
-template <int KIND, bool MX, int T>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+constexpr int kLoraThreads = 128;
+
+template <int KIND, bool MX, int T, bool LORA>
+__global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
     k_fp4_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                const __grid_constant__ GemmParams p) {
-  using S = GemmShape<MX, T>;
+  using S = GemmShape<MX, T, LORA>;
   constexpr int kTpb = S::kTilesPerBlock;
   constexpr int kScaleK = MX ? 128 : 64;  // summed elements of one scale tile
   extern __shared__ uint8_t gemm_smem_raw[];
   __shared__ GemmBars bars;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(gemm_smem_raw) + 1023) & ~uintptr_t{1023});
-  int* start = reinterpret_cast<int*>(smem + S::kStages * S::kStageBytes);
+  uint8_t* const chunks = smem + S::kStages * S::kStageBytes;
+  int* start = reinterpret_cast<int*>(smem + S::kSmemBytes);
   int* lo = start + p.groups + 1;
   int* hi = lo + p.groups + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -326,9 +379,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&bars.acc_full[i]), 1);
       mbar_init(smem_addr(&bars.acc_empty[i]), 4);
+      mbar_init(smem_addr(&bars.chunk_full[i]), kLoraThreads / 32);
+      mbar_init(smem_addr(&bars.chunk_empty[i]), 1);
     }
     mbar_init(smem_addr(&bars.drain), 1);
-    bars.failed = 0;
     fence_mbar_init();
   }
   // The kernel before this one on the stream wrote the operands.
@@ -424,6 +478,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       int acc = 0;
       uint32_t acc_phase = 0;
       uint32_t parity = 0;
+      GemmRing chunk;
       for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
         const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, tile);
         const int blocks = (t.k + kGemmKBlock - 1) / kGemmKBlock;
@@ -434,7 +489,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         umma_fence_after();
         const uint32_t d = tmem + acc * T;
         const uint32_t shift = KIND == kGemmContr ? (t.b0 % 128) / 32 : 0;
+        bool chunks_left = LORA;
+        auto take_chunk = [&]() {
+          if (!mbar_wait(smem_addr(&bars.chunk_full[chunk.s]), chunk.phase)) {
+            ok = false;
+            return;
+          }
+          umma_fence_after();
+          const int steps = bars.chunk_steps[chunk.s];
+          chunks_left = !bars.chunk_last[chunk.s];
+          const uint32_t ch = smem_addr(chunks + chunk.s * S::kChunkBytes);
+          for (int part = 0; part < 2; ++part)  // hi, lo
+            for (int j = 0; j < steps; ++j)
+              umma_bf16(d, desc_codes(ch + 32 * j), desc_codes(ch + kGemmLanes * 128 + part * T * 128 + 32 * j),
+                        umma_idesc_bf16(t.n));
+          umma_commit(smem_addr(&bars.chunk_empty[chunk.s]));
+          chunk.next(S::kChunks);
+        };
         for (int kb = 0; kb < blocks; ++kb) {
+          if (LORA && chunks_left && kb % S::kChunkGap == S::kChunkGap - 1) take_chunk();
+          if (!ok) break;
           if (!mbar_wait(smem_addr(&bars.full[ring.s]), ring.phase)) {
             ok = false;
             break;
@@ -461,6 +535,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           parity ^= 1;
           ring.next(S::kStages);
         }
+        while (LORA && chunks_left && ok) take_chunk();
         if (!ok) break;
         umma_commit(smem_addr(&bars.acc_full[acc]));
         acc ^= 1;
@@ -517,7 +592,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
-  } else if (KIND == kGemmRows && warp >= 8) {
+  } else if (KIND == kGemmRows && warp >= 8 && warp < 12) {
     constexpr int kRowsPerThread = (T + kScaleThreads - 1) / kScaleThreads;
     constexpr int kAhead = 4;  // stages whose scales are loaded together
     constexpr int kBlockBytes = MX ? 8 : 16;
@@ -562,8 +637,107 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
     }
   }
+  if constexpr (LORA) {
+    if (warp >= 12) {
+      const int tid = threadIdx.x - kGemmThreads;
+      const int rank_steps = (p.rank + 15) / 16;
+      GemmRing chunk;
+      int turn = 0;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, tile);
+        lora_barrier();  // the last tile's ids have been read
+        for (int r = tid; r < t.n; r += kLoraThreads) {
+          const int id = r < t.valid ? __ldg(p.lora_ids + t.b0 + r) : -1;
+          bars.ids[r] = id < p.adapters ? id : -1;
+        }
+        lora_barrier();
+        // the smallest adapter of the tile's rows above `a`
+        auto next_above = [&](int a) {
+          int m = INT_MAX;
+          for (int r = tid; r < t.n; r += kLoraThreads) {
+            const int id = bars.ids[r];
+            if (id > a) m = min(m, id);
+          }
+          m = __reduce_min_sync(0xFFFFFFFFu, m);
+          if (lane == 0) bars.next_id[turn][tid >> 5] = m;
+          lora_barrier();
+          m = min(min(bars.next_id[turn][0], bars.next_id[turn][1]), min(bars.next_id[turn][2], bars.next_id[turn][3]));
+          turn ^= 1;
+          return m;
+        };
+        int a = next_above(-1), step = 0;
+        do {
+          int slot_a[4], slot_r[4], steps = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            slot_a[i] = -1, slot_r[i] = 0;
+            if (a == INT_MAX) continue;
+            slot_a[i] = a, slot_r[i] = step * 16;
+            steps = i + 1;
+            if (++step == rank_steps) {
+              step = 0;
+              a = next_above(a);
+            }
+          }
+          // all four warps go on, or none: they meet at barriers
+          ok = lora_all(mbar_wait(smem_addr(&bars.chunk_empty[chunk.s]), chunk.phase ^ 1));
+          if (!ok) break;
+          uint8_t* const ch = chunks + chunk.s * S::kChunkBytes;
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          {  // B_a of this thread's lane
+            const int n = t.a0 + tid;
+            uint4 v[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const int r = slot_r[i] + 8 * q;
+                v[i][q] = zero;
+                if (slot_a[i] >= 0 && n < p.na && r < p.rank)
+                  v[i][q] = __ldg(reinterpret_cast<const uint4*>(
+                      p.lora_b + ((static_cast<int64_t>(slot_a[i]) * p.na + n) * p.rank + r) * 2));
+              }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+                *reinterpret_cast<uint4*>(ch + tid * 128 + (((2 * i + q) ^ (tid & 7)) << 4)) = v[i][q];
+          }
+          for (int r = tid; r < t.n; r += kLoraThreads) {  // t of a row: zero outside its adapter
+            const int id = bars.ids[r];
+            const uint8_t* src = p.lora_t + static_cast<int64_t>(t.b0 + r) * p.rank * 4;
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              uint4 v[4][2];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  const int k = slot_r[i] + 8 * q;
+                  v[i][q] = zero;
+                  if (slot_a[i] >= 0 && slot_a[i] == id && k < p.rank)
+                    v[i][q] = __ldg(reinterpret_cast<const uint4*>(src + (part * p.rank + k) * 2));
+                }
+              uint8_t* dst = ch + kGemmLanes * 128 + part * T * 128 + r * 128;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) *reinterpret_cast<uint4*>(dst + (((2 * i + q) ^ (r & 7)) << 4)) = v[i][q];
+            }
+          }
+          if (tid == 0) {
+            bars.chunk_steps[chunk.s] = steps;
+            bars.chunk_last[chunk.s] = a == INT_MAX;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&bars.chunk_full[chunk.s]));
+          chunk.next(S::kChunks);
+        } while (a != INT_MAX);
+      }
+    }
+  }
   if (!ok) {
-    bars.failed = 1;
     if (lane == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);
   }
   __syncwarp();
@@ -572,6 +746,166 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   umma_fence_after();
   if (warp == 2)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// The adapters' first product: t[m, r] = scaling[a] / (x_sg w_sg) sum_k x[m, k] A_a[r, k] for row m of
+// adapter a, in two bf16 terms.  (The division undoes what the epilogue multiplies the whole
+// accumulator by.)
+//
+// A CTA takes a tile of 32 or 64 rows and a slice of k; the slices of a tile are a cluster, which adds
+// their sums in distributed shared memory in a fixed order.  It goes through the tile's distinct adapters
+// (of several CTAs per slice every `jobs`-th one), so each adapter's A is read once per row tile: when
+// every row has its own, once per row, which is the least.  mma.sync m16n8k16 with ranks as its
+// rows and tokens as its columns: the operands come straight from global memory, 16 bytes per
+// thread and row, with the same permutation of k on both sides.  Bound by the reads of x and A; the
+// tensor cores are idle most of the time, so the shape of the instruction does not matter.
+// ---------------------------------------------------------------------------
+constexpr int kShrinkThreads = 256;
+
+struct ShrinkParams {
+  const uint8_t* x;        // bf16 [rows, K], row stride ldx bytes
+  int64_t ldx;
+  const uint8_t* a;        // bf16 [adapters, rank, K]
+  const float* scaling;    // [adapters]
+  const float* sg_a;       // NULL: 1
+  const float* sg_b;
+  const int32_t* ids;
+  uint8_t* t;              // bf16 [rows][hi, lo][rank]
+  int rows, K, adapters, rank, slices, jobs;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float load_cluster(const float* p, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+      "ld.shared::cluster.f32 %0, [a];\n\t}"
+      : "=f"(v)
+      : "r"(smem_addr(p)), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// NB: blocks of 16 ranks at a time.  TG: groups of 32 rows in a tile (the 8 warps are TG x 8 / TG
+// interleaved parts of the slice).
+template <int NB, int TG>
+__global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const __grid_constant__ ShrinkParams p) {
+  constexpr int kRows = 32 * TG, kParts = 8 / TG, kRanks = 16 * NB;
+  extern __shared__ float shrink_sum[];  // [parts][rows][ranks]
+  __shared__ int ids[kRows];
+  __shared__ int leaders[kRows];         // the tile's distinct adapters, in the order of their first row
+  __shared__ int n_leaders;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tg = warp % TG, part = warp / TG;
+  const int slice = blockIdx.x % p.slices, job = blockIdx.x / p.slices % p.jobs;
+  const int row0 = blockIdx.x / p.slices / p.jobs * kRows;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x < kRows) {
+    const int id = row0 + threadIdx.x < p.rows ? __ldg(p.ids + row0 + threadIdx.x) : -1;
+    ids[threadIdx.x] = id < p.adapters ? id : -1;
+  }
+  if (threadIdx.x == 0) n_leaders = 0;
+  __syncthreads();
+  if (warp == 0) {
+    int n = 0;
+    for (int r0 = 0; r0 < kRows; r0 += 32) {
+      const int id = ids[r0 + lane];
+      bool first = id >= 0;
+      for (int j = 0; j < r0 + lane && first; ++j) first = ids[j] != id;
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, first);
+      if (first) leaders[n + __popc(m & ((1u << lane) - 1))] = id;
+      n += __popc(m);
+    }
+    if (lane == 0) n_leaders = n;
+  }
+  __syncthreads();
+  float inv = 1.0f;
+  if (p.sg_a) inv = __fdiv_rn(1.0f, __fmul_rn(__ldg(p.sg_a), __ldg(p.sg_b)));
+  const int chunks = p.K / 32;  // of 32 summed elements: 16 bytes per thread and row
+  const int per = (chunks + p.slices - 1) / p.slices;
+  const int c_end = min(chunks, (slice + 1) * per);
+  const int g = lane >> 2, q = lane & 3;
+
+  for (int li = job; li < n_leaders; li += p.jobs) {
+    const int id = leaders[li];
+    const bool mine = __ballot_sync(0xFFFFFFFFu, ids[tg * 32 + lane] == id) != 0;
+    for (int rb = 0; rb < p.rank; rb += kRanks) {
+      float acc[NB][4][4];
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.0f;
+      if (mine) {
+#pragma unroll 2
+        for (int c = slice * per + part; c < c_end; c += kParts) {
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          uint4 a[NB][2], x[4];
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int r = rb + 16 * i + 8 * h + g;
+              a[i][h] = r < p.rank ? __ldg(reinterpret_cast<const uint4*>(
+                                         p.a + ((static_cast<int64_t>(id) * p.rank + r) * p.K + int64_t{32} * c) * 2 + 16 * q))
+                                   : zero;
+            }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int m = row0 + tg * 32 + 8 * j + g;
+            x[j] = m < p.rows ? __ldg(reinterpret_cast<const uint4*>(p.x + m * p.ldx + int64_t{64} * c + 16 * q)) : zero;
+          }
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              mma_bf16(acc[i][j], a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, x[j].x, x[j].y);
+              mma_bf16(acc[i][j], a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, x[j].z, x[j].w);
+            }
+        }
+      }
+      // accumulator: ranks g and g + 8, rows 2 q and 2 q + 1 of a block of 8
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            shrink_sum[(part * kRows + tg * 32 + 8 * j + 2 * q + (k & 1)) * kRanks + 16 * i + g + 8 * (k >> 1)] =
+                acc[i][j][k];
+      __syncthreads();
+      for (int e = threadIdx.x; e < kRows * kRanks; e += kShrinkThreads) {
+        float v = shrink_sum[e];
+#pragma unroll
+        for (int k = 1; k < kParts; ++k) v += shrink_sum[k * kRows * kRanks + e];
+        shrink_sum[e] = v;
+      }
+      cluster_sync();
+      // each CTA of the cluster finishes every slices-th value
+      for (int e = threadIdx.x * p.slices + slice; e < kRows * kRanks; e += kShrinkThreads * p.slices) {
+        const int m = e / kRanks, r = rb + e % kRanks;
+        if (ids[m] != id || r >= p.rank) continue;
+        float v = 0.0f;
+        for (int k = 0; k < p.slices; ++k) v += load_cluster(shrink_sum + e, k);
+        v *= __ldg(p.scaling + id) * inv;
+        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+        __nv_bfloat16* t = reinterpret_cast<__nv_bfloat16*>(p.t) + static_cast<int64_t>(row0 + m) * 2 * p.rank;
+        t[r] = hi;
+        t[p.rank + r] = __float2bfloat16_rn(v - __bfloat162float(hi));
+      }
+      cluster_sync();  // the sums have been read
+    }
+  }
 }
 
 }  // namespace hq

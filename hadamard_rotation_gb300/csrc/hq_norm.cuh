@@ -138,19 +138,6 @@ __device__ __forceinline__ int param_slot(int units, int col) {
   return ((col & 4) ? 4 * units : 0) + (col >> 3) * 4 + (col & 3);
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // A float into the same shared variable of CTA `rank` of the cluster.
 __device__ __forceinline__ void store_cluster(const float* p, uint32_t rank, float v) {
   asm volatile(

@@ -388,6 +388,43 @@ HQ_API hq_status hq_grouped_wgrad_mxfp4(const uint8_t* gq, const uint8_t* gs, co
                                         hq_dtype out_dtype, hq_stream stream);
 
 /*
+ * hq_lora_gemm_nvfp4 -- a shared projection with the low-rank adapters of many requests (NVFP4
+ * projection, bf16 adapters):
+ *   out[m, n] = x_sg * w_sg * sum_k xq[m, k] wq[n, k] + scaling[a] * sum_r (sum_k x[m, k] A_a[r, k]) B_a[n, r]
+ *   with a = row_adapter[m]; no second term where a is negative or not below `adapters`.
+ *   Both terms are added in fp32 before the one rounding to out_dtype; the inner sums of the second
+ *   are carried in two bf16 terms (to 2^-17).  x_sg * w_sg must be a normal fp32 number.
+ *
+ *   xq [M, K/2], xs [M, K/16] row-major, x_sg 1 float: x as quantized (rotated along K like the
+ *   weights); x bf16 [M, K], row stride ldx: x itself, which the adapters read; wq [N, K/2], ws
+ *   hq_swizzled_scales_bytes(N, K) in the tile layout, w_sg 1 float; lora_a bf16 [adapters, R, K],
+ *   lora_b bf16 [adapters, N, R], scaling float [adapters]; row_adapter int32 [M] on the device, rows in
+ *   any order (rows of one request next to one another cost least).  R a multiple of 8 up to 128
+ *   (adapters of a smaller rank padded with zeros), K a multiple of 32.  x, lora_a, lora_b and x's rows
+ *   16-byte aligned.
+ *   workspace : hq_lora_gemm_workspace_bytes(M, R) bytes, 16-byte aligned; contents need no
+ *               preparation.  Calls that may run at the same time need different ones.
+ */
+HQ_API hq_status hq_lora_gemm_nvfp4(const uint8_t* xq, const uint8_t* xs, const float* x_sg,
+                                    const uint8_t* wq, const uint8_t* ws, const float* w_sg,
+                                    const void* x, int64_t ldx, const void* lora_a,
+                                    const void* lora_b, const float* scaling,
+                                    const int32_t* row_adapter, int64_t M, int64_t N, int64_t K,
+                                    int64_t adapters, int64_t R, void* out, hq_dtype out_dtype,
+                                    void* workspace, hq_stream stream);
+
+/* hq_lora_gemm_mxfp4 -- the same beside an MXFP4 projection (no per-tensor scales). */
+HQ_API hq_status hq_lora_gemm_mxfp4(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq,
+                                    const uint8_t* ws, const void* x, int64_t ldx,
+                                    const void* lora_a, const void* lora_b, const float* scaling,
+                                    const int32_t* row_adapter, int64_t M, int64_t N, int64_t K,
+                                    int64_t adapters, int64_t R, void* out, hq_dtype out_dtype,
+                                    void* workspace, hq_stream stream);
+
+/* Bytes of hq_lora_gemm's workspace (-1 for sizes it refuses). */
+HQ_API int64_t hq_lora_gemm_workspace_bytes(int64_t M, int64_t R);
+
+/*
  * hq_swizzle_scales -- row-major block scales into the tile layout of
  * hq_rotate_quant_nvfp4_swizzled (for weights' scales, laid out once, and for MXFP4).
  *   scales: uint8 [groups, rows, cols], any alignment; out: groups buffers of
