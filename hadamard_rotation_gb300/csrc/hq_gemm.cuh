@@ -158,6 +158,21 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// One lane of a converged warp.  The asynchronous instructions are issued under this predicate, in code
+// that the whole warp runs, rather than in a branch on the lane: the compiler then knows that their
+// operands are the warp's and keeps them in uniform registers (a stage's 12 tensor-core
+// instructions took 1700 cycles to issue from a branch on lane 0).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+
+// A wait of the whole warp: every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
+}
+
 // Arrive on `bar` once every tensor-core operation this thread has issued is complete.
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
@@ -363,7 +378,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
   int* start = reinterpret_cast<int*>(smem + S::kSmemBytes);
   int* lo = start + p.groups + 1;
   int* hi = lo + p.groups + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bars.tmem)),
@@ -428,123 +443,129 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
   bool ok = true;
 
   if (warp == 0) {
-    if (lane == 0) {
-      GemmRing ring;
-      long long fills = 0;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, tile);
-        const int blocks = (t.k + kGemmKBlock - 1) / kGemmKBlock;
-        const int boxes = (t.n + S::kBox - 1) / S::kBox;
-        const int kt0 = t.k0 / kScaleK;
-        const uint8_t* sfa = p.sfa + (KIND == kGemmRows ? t.g * p.sfa_group_bytes : 0) +
-                             (static_cast<int64_t>(t.a0 / 128) * p.k_tiles + kt0) * 512;
-        int row_tiles = 0;
-        const uint8_t* sfb = nullptr;
-        if constexpr (KIND == kGemmContr) {
-          const int first = t.b0 / 128;
-          row_tiles = min((t.b0 + t.valid + 127) / 128 - first, S::kRowTilesB);
-          sfb = p.sfb + (static_cast<int64_t>(first) * p.k_tiles + kt0) * 512;
-        }
-        for (int kb = 0; kb < blocks; ++kb) {
-          const uint32_t bar = smem_addr(&bars.full[ring.s]);
-          if (!mbar_wait(smem_addr(&bars.empty[ring.s]), ring.phase ^ 1)) {
-            ok = false;
-            break;
-          }
-          const uint32_t st = smem_addr(smem + ring.s * S::kStageBytes);
-          const uint32_t sa = st + S::kBytesA + S::kBytesB;
-          const int sf_tiles = min(kTpb, p.k_tiles - kt0 - kb * kTpb);
+    GemmRing ring;
+    long long fills = 0;
+    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, tile);
+      const int blocks = (t.k + kGemmKBlock - 1) / kGemmKBlock;
+      const int boxes = (t.n + S::kBox - 1) / S::kBox;
+      const int kt0 = t.k0 / kScaleK;
+      const uint8_t* sfa = p.sfa + (KIND == kGemmRows ? t.g * p.sfa_group_bytes : 0) +
+                           (static_cast<int64_t>(t.a0 / 128) * p.k_tiles + kt0) * 512;
+      int row_tiles = 0;
+      const uint8_t* sfb = nullptr;
+      if constexpr (KIND == kGemmContr) {
+        const int first = t.b0 / 128;
+        row_tiles = min((t.b0 + t.valid + 127) / 128 - first, S::kRowTilesB);
+        sfb = p.sfb + (static_cast<int64_t>(first) * p.k_tiles + kt0) * 512;
+      }
+      for (int kb = 0; kb < blocks; ++kb) {
+        ok = warp_wait(smem_addr(&bars.empty[ring.s]), ring.phase ^ 1);
+        if (!ok) break;
+        const uint32_t bar = smem_addr(&bars.full[ring.s]);
+        const uint32_t st = smem_addr(smem) + ring.s * S::kStageBytes;
+        const uint32_t sa = st + S::kBytesA + S::kBytesB;
+        const int sf_tiles = min(kTpb, p.k_tiles - kt0 - kb * kTpb);
+        const int kx = (t.k0 + kb * kGemmKBlock) / 2;
+        if (elect_one()) {
           mbar_expect_tx(bar, S::kBytesA + boxes * S::kBox * 128 + sf_tiles * 512 * (1 + row_tiles));
-          const int kx = (t.k0 + kb * kGemmKBlock) / 2;
           tma_tile3(st, &map_a, kx, t.a0, KIND == kGemmRows ? t.g : 0, bar);
+          tma_bulk(sa, sfa + static_cast<int64_t>(kb) * kTpb * 512, sf_tiles * 512, bar);
           for (int i = 0; i < boxes; ++i)
             tma_tile2(st + S::kBytesA + i * S::kBox * 128, &map_b, kx, t.b0 + i * S::kBox, bar);
-          tma_bulk(sa, sfa + static_cast<int64_t>(kb) * kTpb * 512, sf_tiles * 512, bar);
           for (int i = 0; i < row_tiles; ++i)
             tma_bulk(sa + S::kBytesSfa + i * kTpb * 512,
                      sfb + (static_cast<int64_t>(i) * p.k_tiles + kb * kTpb) * 512, sf_tiles * 512, bar);
-          ++fills;
-          ring.next(S::kStages);
         }
-      }
-      if (!ok) {  // let the copies in flight land (bounded) before the CTA may end
-        for (long long f = fills > S::kStages ? fills - S::kStages : 0; f < fills; ++f)
-          mbar_wait(smem_addr(&bars.full[f % S::kStages]), (f / S::kStages) & 1);
+        __syncwarp();
+        ++fills;
+        ring.next(S::kStages);
       }
     }
+    if (!ok) {  // let the copies in flight land (bounded) before the CTA may end
+      for (long long f = fills > S::kStages ? fills - S::kStages : 0; f < fills; ++f)
+        mbar_wait(smem_addr(&bars.full[f % S::kStages]), (f / S::kStages) & 1);
+    }
   } else if (warp == 1) {
-    if (lane == 0) {
-      GemmRing ring;
-      int acc = 0;
-      uint32_t acc_phase = 0;
-      uint32_t parity = 0;
-      GemmRing chunk;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, tile);
-        const int blocks = (t.k + kGemmKBlock - 1) / kGemmKBlock;
-        if (!mbar_wait(smem_addr(&bars.acc_empty[acc]), acc_phase ^ 1)) {
-          ok = false;
-          break;
-        }
+    GemmRing ring;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    uint32_t parity = 0;
+    GemmRing chunk;
+    const uint64_t codes0 = desc_codes(smem_addr(smem)), scales0 = desc_scales(smem_addr(smem));
+    const uint64_t chunk0 = desc_codes(smem_addr(chunks));
+    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, tile);
+      const int blocks = (t.k + kGemmKBlock - 1) / kGemmKBlock;
+      ok = warp_wait(smem_addr(&bars.acc_empty[acc]), acc_phase ^ 1);
+      if (!ok) break;
+      umma_fence_after();
+      const uint32_t d = tmem + acc * T;
+      const uint32_t shift = KIND == kGemmContr ? (t.b0 % 128) / 32 : 0;
+      const int row_tiles = (shift * 32 + t.n + 127) / 128;
+      const uint32_t idesc0 = umma_idesc<MX>(t.n, 0), idesc1 = umma_idesc<MX>(t.n, MX ? 2 : 0);
+      bool chunks_left = LORA;
+      auto take_chunk = [&]() {
+        ok = warp_wait(smem_addr(&bars.chunk_full[chunk.s]), chunk.phase);
+        if (!ok) return;
         umma_fence_after();
-        const uint32_t d = tmem + acc * T;
-        const uint32_t shift = KIND == kGemmContr ? (t.b0 % 128) / 32 : 0;
-        bool chunks_left = LORA;
-        auto take_chunk = [&]() {
-          if (!mbar_wait(smem_addr(&bars.chunk_full[chunk.s]), chunk.phase)) {
-            ok = false;
-            return;
-          }
-          umma_fence_after();
-          const int steps = bars.chunk_steps[chunk.s];
-          chunks_left = !bars.chunk_last[chunk.s];
-          const uint32_t ch = smem_addr(chunks + chunk.s * S::kChunkBytes);
+        const int steps = bars.chunk_steps[chunk.s];
+        chunks_left = !bars.chunk_last[chunk.s];
+        const uint64_t ch = chunk0 + chunk.s * (S::kChunkBytes >> 4);
+        if (elect_one()) {
           for (int part = 0; part < 2; ++part)  // hi, lo
             for (int j = 0; j < steps; ++j)
-              umma_bf16(d, desc_codes(ch + 32 * j), desc_codes(ch + kGemmLanes * 128 + part * T * 128 + 32 * j),
-                        umma_idesc_bf16(t.n));
+              umma_bf16(d, ch + 2 * j, ch + ((kGemmLanes * 128 + part * T * 128) >> 4) + 2 * j, umma_idesc_bf16(t.n));
           umma_commit(smem_addr(&bars.chunk_empty[chunk.s]));
-          chunk.next(S::kChunks);
-        };
-        for (int kb = 0; kb < blocks; ++kb) {
-          if (LORA && chunks_left && kb % S::kChunkGap == S::kChunkGap - 1) take_chunk();
-          if (!ok) break;
-          if (!mbar_wait(smem_addr(&bars.full[ring.s]), ring.phase)) {
-            ok = false;
-            break;
+        }
+        __syncwarp();
+        chunk.next(S::kChunks);
+      };
+      for (int kb = 0; kb < blocks; ++kb) {
+        if (LORA && chunks_left && kb % S::kChunkGap == S::kChunkGap - 1) take_chunk();
+        if (!ok) break;
+        ok = warp_wait(smem_addr(&bars.full[ring.s]), ring.phase);
+        if (!ok) break;
+        umma_fence_after();
+        const uint64_t st = codes0 + ring.s * (S::kStageBytes >> 4);
+        const uint64_t sa = scales0 + ((ring.s * S::kStageBytes + S::kBytesA + S::kBytesB) >> 4);
+        const uint32_t ca = tmem + S::kColSf + parity * (S::kColsSfa + S::kColsSfb), cb = ca + S::kColsSfa;
+        const int steps = min(4, (t.k - kb * kGemmKBlock + 63) / 64);
+        const int sf_tiles = (steps * 64 + kScaleK - 1) / kScaleK;
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < kTpb; ++j) {
+            if (j >= sf_tiles) break;
+            umma_copy_scales(ca + 4 * j, sa + 32 * j);
+#pragma unroll
+            for (int i = 0; i < S::kRowTilesB; ++i)
+              if (i < row_tiles)
+                umma_copy_scales(cb + (j * S::kRowTilesB + i) * 4, sa + (S::kBytesSfa >> 4) + (i * kTpb + j) * 32);
           }
-          umma_fence_after();
-          const uint32_t st = smem_addr(smem + ring.s * S::kStageBytes);
-          const uint32_t sa = st + S::kBytesA + S::kBytesB, sb = sa + S::kBytesSfa;
-          const uint32_t ca = tmem + S::kColSf + parity * (S::kColsSfa + S::kColsSfb), cb = ca + S::kColsSfa;
-          const int steps = min(4, (t.k - kb * kGemmKBlock + 63) / 64);
-          const int sf_tiles = (steps * 64 + kScaleK - 1) / kScaleK;
-          const int row_tiles = (shift * 32 + t.n + 127) / 128;
-          for (int j = 0; j < sf_tiles; ++j) {
-            umma_copy_scales(ca + 4 * j, desc_scales(sa + 512 * j));
-            for (int i = 0; i < row_tiles; ++i)
-              umma_copy_scales(cb + (j * S::kRowTilesB + i) * 4, desc_scales(sb + (i * kTpb + j) * 512));
-          }
-          for (int j = 0; j < steps; ++j) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j >= steps) break;
             const int sj = MX ? j / 2 : j;
-            umma_fp4<MX>(d, desc_codes(st + 32 * j), desc_codes(st + S::kBytesA + 32 * j),
-                         umma_idesc<MX>(t.n, MX ? 2 * (j & 1) : 0), ca + 4 * sj,
+            umma_fp4<MX>(d, st + 2 * j, st + (S::kBytesA >> 4) + 2 * j, (j & 1) ? idesc1 : idesc0, ca + 4 * sj,
                          cb + sj * S::kRowTilesB * 4 + shift, (kb | j) != 0);
           }
           umma_commit(smem_addr(&bars.empty[ring.s]));
-          parity ^= 1;
-          ring.next(S::kStages);
         }
-        while (LORA && chunks_left && ok) take_chunk();
-        if (!ok) break;
-        umma_commit(smem_addr(&bars.acc_full[acc]));
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1;
+        __syncwarp();
+        parity ^= 1;
+        ring.next(S::kStages);
       }
-      if (!ok) {  // let the products in flight finish (bounded) before tensor memory is freed
-        umma_commit(smem_addr(&bars.drain));
-        mbar_wait(smem_addr(&bars.drain), 0);
-      }
+      while (LORA && chunks_left && ok) take_chunk();
+      if (!ok) break;
+      if (elect_one()) umma_commit(smem_addr(&bars.acc_full[acc]));
+      __syncwarp();
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
+    if (!ok) {  // let the products in flight finish (bounded) before tensor memory is freed
+      if (elect_one()) umma_commit(smem_addr(&bars.drain));
+      __syncwarp();
+      mbar_wait(smem_addr(&bars.drain), 0);
     }
   } else if (warp >= 4 && warp < 8) {
     const int quarter = warp & 3;
