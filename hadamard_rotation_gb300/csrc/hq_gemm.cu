@@ -52,6 +52,14 @@ bool encode_codes(CUtensorMap* map, const uint8_t* q, int64_t row_bytes, int64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Bytes per store into rows of n elements at `out`: the alignment that every row has, up to 16.
+int store_bytes(const void* out, int64_t n, hq_dtype dt) {
+  const int64_t es = dt == HQ_F32 ? 4 : 2;
+  int v = 16;
+  while (n * es % v || !aligned(out, v)) v /= 2;
+  return v;
+}
+
 // Multiprocessors of the current device, asked for once per device.
 cudaError_t sm_count(int* sms) {
   static int known[64] = {};
@@ -75,7 +83,7 @@ struct Codes {
 
 template <int KIND, bool MX, int T, bool LORA = false>
 hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t most_tiles, hq_stream stream) {
-  using S = hq::GemmShape<MX, T, LORA>;
+  using S = hq::GemmShape<KIND, MX, T, LORA>;
   auto kernel = hq::k_fp4_gemm<KIND, MX, T, LORA>;
   CUtensorMap ma, mb;
   if (!encode_codes(&ma, a.q, a.row_bytes, a.rows, a.groups, hq::kGemmLanes, 3) ||
@@ -122,8 +130,10 @@ GemmParams rows_params(const uint8_t* xs, const float* x_sg, const uint8_t* ws, 
   p.sfa_group_bytes = static_cast<int64_t>(p.tiles_a) * p.k_tiles * 512;
   p.sfb = xs;
   p.sfb_row_bytes = static_cast<int>(K / (MX ? 32 : 16));
-  p.sfb_vec = MX ? 8 : 16;
-  while (p.sfb_row_bytes % p.sfb_vec || !aligned(xs, p.sfb_vec)) p.sfb_vec /= 2;
+  p.sfb_mode = p.sfb_row_bytes % 16 == 0 && aligned(xs, 16) ? 16
+               : p.sfb_row_bytes % 8 == 0 && aligned(xs, 8) ? 8
+               : aligned(xs, 4)                             ? 4
+                                                            : 1;
   p.sg_a = w_sg;
   p.sg_b = x_sg;
   p.groups = static_cast<int>(groups);
@@ -132,6 +142,7 @@ GemmParams rows_params(const uint8_t* xs, const float* x_sg, const uint8_t* ws, 
   p.k = static_cast<int>(K);
   p.out = out;
   p.out_f32 = dt == HQ_F32;
+  p.out_vec = store_bytes(out, N, dt);
   return p;
 }
 
@@ -192,6 +203,7 @@ hq_status grouped_wgrad(const uint8_t* gq, const uint8_t* gs, const float* g_sg,
   p.tiles_b = static_cast<int>(tiles_b);
   p.out = out;
   p.out_f32 = dt == HQ_F32;
+  p.out_vec = store_bytes(out, K, dt);
   const Codes a = {xq, T / 2, K, 1}, b = {gq, T / 2, N, 1};
   return launch<hq::kGemmContr, MX, 192>(p, a, b, E * tiles_a * tiles_b, stream);
 }

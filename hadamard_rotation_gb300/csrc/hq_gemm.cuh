@@ -25,7 +25,7 @@
 //                 already the order that tensor memory wants)
 //   warp 1        copies the scales to tensor memory (tcgen05.cp) and issues the products
 //   warp 2        allocates tensor memory
-//   warps 4..7    epilogue: tensor memory -> registers -> * a -> global
+//   warps 4..7    epilogue: tensor memory -> registers -> * a -> shared memory -> global (CONTR: 4..11)
 //   warps 8..11   (ROWS) the tokens' scales: row-major in global memory, since a group starts at
 //                 any row; moved through registers into the tile layout
 //   warps 12..15  (adapters) the operands of the adapters' second product, below
@@ -52,7 +52,7 @@ namespace hq {
 
 constexpr int kGemmLanes = 128;      // rows of operand A per tile (lanes of tensor memory)
 constexpr int kGemmKBlock = 256;     // summed elements per stage: 128 bytes of codes per row
-constexpr int kGemmMaxGroups = 1024;
+constexpr int kGemmMaxGroups = 512;
 
 enum GemmKind { kGemmRows = 0, kGemmContr = 1 };
 
@@ -72,9 +72,10 @@ struct GemmParams {
   int tiles_b;              // CONTR: ceil(nb / T)
   int k_tiles;              // 512-byte scale tiles per 128 rows
   int sfb_row_bytes;        // ROWS: bytes of one row of scales
-  int sfb_vec;              // ROWS: bytes per load of them (rows aligned to it)
+  int sfb_mode;             // ROWS: how they are read (load_scales)
   void* out;                // ROWS: [extent, na]; CONTR: [groups, nb, na]
   int out_f32;
+  int out_vec;              // bytes per store: what the rows of out are aligned to, up to 16
   // adapters
   const uint8_t* lora_b;    // bf16 [adapters, na, rank]
   const uint8_t* lora_t;    // bf16 [extent][hi, lo][rank]
@@ -85,7 +86,7 @@ struct GemmParams {
 // ---------------------------------------------------------------------------
 // Geometry of one kernel instance.  T: columns of a tile (tokens, or rows of G).
 // ---------------------------------------------------------------------------
-template <bool MX, int T, bool LORA>
+template <int KIND, bool MX, int T, bool LORA>
 struct GemmShape {
   static constexpr int kTilesPerBlock = MX ? 2 : 4;  // scale tiles along K per stage
   static constexpr int kRowTilesB = (T + 127) / 128;
@@ -99,10 +100,13 @@ struct GemmShape {
   // adapters: chunks of 64 bf16 columns: B_a of 128 lanes, then t's hi and lo of T rows
   static constexpr int kChunkBytes = LORA ? kGemmLanes * 128 + 2 * T * 128 : 0;
   static constexpr int kChunks = T >= 128 ? 1 : 2;
-  static constexpr int kRingBytes = 206 * 1024 - kChunks * kChunkBytes;
-  static constexpr int kStages = kRingBytes / kStageBytes < 8 ? kRingBytes / kStageBytes : 8;
   static constexpr int kChunkGap = T >= 128 ? 5 : 2;  // stages between two chunks of a tile
-  static constexpr int kSmemBytes = kStages * kStageBytes + kChunks * kChunkBytes;
+  static constexpr int kEpilogues = KIND == kGemmContr ? 2 : 1;  // groups of 128 threads
+  static constexpr int kOuts = kEpilogues * 2 * 8 * 1024;        // their output buffers
+  static constexpr int kRingBytes = 218 * 1024 - kChunks * kChunkBytes - kOuts;
+  static constexpr int kStages = kRingBytes / kStageBytes < 7 ? kRingBytes / kStageBytes : 7;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kChunks * kChunkBytes + kOuts;
+  static_assert(kSmemBytes + 1024 + 12 * (kGemmMaxGroups + 1) + 1280 <= 227 * 1024, "a CTA has 227 KB");
   // tensor memory columns: two accumulators, then two sets of scales (stage parity)
   static constexpr int kColsSfa = kTilesPerBlock * 4;
   static constexpr int kColsSfb = kTilesPerBlock * kRowTilesB * 4;
@@ -238,12 +242,25 @@ __device__ __forceinline__ uint32_t umma_idesc_bf16(int n) {
 __device__ __forceinline__ void umma_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void umma_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+// Columns of the thread's lane into registers; the wait is part of the statement, so nothing reads
+// the registers before it.
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
         "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(taddr)
       : "memory");
 }
@@ -308,52 +325,155 @@ struct GemmRing {
 };
 
 // ---------------------------------------------------------------------------
-// The scales of a row of X for one stage: `bytes` of them from `src`, zero past the row's end.
+// The scales of a row of X for a batch of stages, as words in registers: W words, of which the thread
+// takes what lies in its row when it writes them.  `mode`: 16, 8: rows aligned to that many bytes;
+// 4: rows at any byte of a 4-byte aligned tensor, read as the aligned words around them (one more,
+// shifted when they are written); 1: a tensor at any byte.  The loads are volatile so that they stay
+// ahead of the batch written before them.
 // ---------------------------------------------------------------------------
-template <int BYTES>
-__device__ __forceinline__ void load_scale_row(const uint8_t* src, int left, int vec, uint32_t (&w)[4]) {
+__device__ __forceinline__ uint32_t ld_word(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
+struct ScaleRow {
+  int shift;  // bits to drop from the first word
+  int left;   // bytes of the row from the batch's first one on; <= 0: nothing
+};
+
+template <int W>
+__device__ __forceinline__ ScaleRow load_scales(const GemmParams& p, int64_t row, bool live, int at, uint32_t (&w)[W + 1]) {
+  ScaleRow s{0, live ? p.sfb_row_bytes - at : 0};
+  if (p.sfb_mode >= 8) {
+    const int vec = p.sfb_mode;
+    const uint8_t* src = p.sfb + (s.left > 0 ? row * p.sfb_row_bytes + at : 0);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = 0;
-  if (vec == 16) {  // rows of whole stages' scales (NVFP4: K a multiple of 256)
-    if (left >= 16) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    }
-  } else if (vec == 8) {
-#pragma unroll
-    for (int i = 0; i < BYTES / 8; ++i)
-      if (left >= 8 * i + 8) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src) + i);
-        w[2 * i] = v.x, w[2 * i + 1] = v.y;
+    for (int i = 0; i < W; i += 4) {  // past the row's end: its first bytes again, dropped later
+      const uint8_t* q = src + (4 * i < s.left ? 4 * i : 0);
+      if (vec == 16) {
+        asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                     : "l"(q));
+      } else {
+        const uint8_t* q2 = src + (4 * i + 8 < s.left ? 4 * i + 8 : 0);
+        asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(w[i]), "=r"(w[i + 1]) : "l"(q));
+        asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(w[i + 2]), "=r"(w[i + 3]) : "l"(q2));
       }
-  } else if (vec == 4) {
+    }
+    return s;
+  }
+  const int64_t first = row * p.sfb_row_bytes + at, end = static_cast<int64_t>(p.extent) * p.sfb_row_bytes;
+  if (p.sfb_mode == 4 && (s.left <= 0 || first + s.left <= (end & ~int64_t{3}))) {
+    // every word that holds a byte of the row lies inside the tensor; later words: the first again
+    const int64_t base = s.left > 0 ? first & ~int64_t{3} : 0;
+    s.shift = s.left > 0 ? static_cast<int>(first & 3) * 8 : 0;
+    const int words = s.left > 0 ? (s.left + s.shift / 8 + 3) / 4 : (end >= 4 ? 1 : 0);
 #pragma unroll
-    for (int i = 0; i < BYTES / 4; ++i)
-      if (left >= 4 * i + 4) w[i] = __ldg(reinterpret_cast<const uint32_t*>(src) + i);
-  } else if (vec == 2) {
+    for (int i = 0; i <= W; ++i) w[i] = words > 0 ? ld_word(p.sfb + base + (i < words ? 4 * i : 0)) : 0;
+    return s;
+  }
 #pragma unroll
-    for (int i = 0; i < BYTES / 2; ++i)
-      if (left >= 2 * i + 2)
-        w[i / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(src) + i)) << (16 * (i % 2));
-  } else {
+  for (int i = 0; i <= W; ++i) {  // the tensor's last bytes, or an unaligned tensor
+    w[i] = 0;
 #pragma unroll
-    for (int i = 0; i < BYTES; ++i)
-      if (left > i) w[i / 4] |= static_cast<uint32_t>(__ldg(src + i)) << (8 * (i % 4));
+    for (int b = 0; b < 4; ++b)
+      if (4 * i + b < s.left) w[i] |= static_cast<uint32_t>(__ldg(p.sfb + first + 4 * i + b)) << (8 * b);
+  }
+  return s;
+}
+
+// Word i of a loaded row, zero past its end.
+template <int W>
+__device__ __forceinline__ uint32_t scale_word(const uint32_t (&w)[W + 1], const ScaleRow& s, int i) {
+  const uint32_t v = __funnelshift_r(w[i], w[i + 1], s.shift);
+  const int left = s.left - 4 * i;
+  return left >= 4 ? v : left <= 0 ? 0u : v & ((1u << (8 * left)) - 1);
+}
+
+// Barriers among 128 threads of a role (1: adapters, 2, 3: epilogue); the second tells all of them
+// whether `ok` held for all: a wait that ran out for one warp must not leave the others at a barrier.
+template <int ID>
+__device__ __forceinline__ void role_sync() {
+  asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory");
+}
+template <int ID>
+__device__ __forceinline__ bool role_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(ok)), "n"(ID)
+      : "memory");
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// Epilogue: accumulator columns [0, valid) of 128 lanes, times a, to rows of `out`.
+//
+// In tensor memory a thread holds one lane, and lanes are consecutive elements of an output row: stored
+// as they come, a warp writes 64 bytes of a row at a time (bf16), which took 12,000 cycles for 192
+// columns, more than a tile's products.  So a chunk of columns goes through shared memory, where 16
+// threads pick up the 256 bytes of a row (VEC bytes each, or less where the rows are not aligned).
+// Two buffers: one barrier per chunk.
+// ---------------------------------------------------------------------------
+constexpr int kOutBytes = 8 * 1024;  // one buffer: 128 lanes x 32 columns of bf16 or 16 of fp32
+
+// Up to ROWS rows of ROW bytes in the buffer, the first `bytes` of each, to global rows `stride` bytes
+// apart: all reads before the writes.
+template <typename V, int ROW, int ROWS>
+__device__ __forceinline__ void store_rows(const uint8_t* buf, uint8_t* out, int64_t stride, int rows, int bytes,
+                                           int tid) {
+  constexpr int kPerRow = ROW / sizeof(V);
+  if constexpr (kPerRow <= 128) {
+    constexpr int kStep = 128 / kPerRow, kTimes = ROWS / kStep, kBatch = kTimes < 8 ? kTimes : 8;
+    const int at = tid % kPerRow * static_cast<int>(sizeof(V)), r0 = tid / kPerRow;
+    if (at >= bytes) return;
+#pragma unroll 1
+    for (int i0 = 0; i0 < kTimes; i0 += kBatch) {
+      V v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) v[i] = *reinterpret_cast<const V*>(buf + (r0 + (i0 + i) * kStep) * ROW + at);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + (i0 + i) * kStep;
+        if (r < rows) *reinterpret_cast<V*>(out + r * stride + at) = v[i];
+      }
+    }
   }
 }
 
-// The adapters' warps among themselves.
-__device__ __forceinline__ void lora_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+template <int ROW, int ROWS>
+__device__ __forceinline__ void store_rows(int vec, const uint8_t* buf, uint8_t* out, int64_t stride, int rows,
+                                           int bytes, int tid) {
+  if (vec == 16) store_rows<uint4, ROW, ROWS>(buf, out, stride, rows, bytes, tid);
+  else if (vec == 8) store_rows<uint2, ROW, ROWS>(buf, out, stride, rows, bytes, tid);
+  else if (vec == 4) store_rows<uint32_t, ROW, ROWS>(buf, out, stride, rows, bytes, tid);
+  else store_rows<uint16_t, ROW, ROWS>(buf, out, stride, rows, bytes, tid);  // (bf16 only)
+}
 
-__device__ __forceinline__ bool lora_all(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(ok))
-      : "memory");
-  return r;
+// A chunk of the accumulator's columns of this thread's lane, times a, into a buffer.
+template <typename O, int N>
+__device__ __forceinline__ void fetch_chunk(uint32_t from, float a, bool none, uint8_t* buf, int tid) {
+  uint32_t v[N];
+  tmem_load(from, v);
+  if (none)
+#pragma unroll
+    for (int c = 0; c < N; ++c) v[c] = 0;
+  O* o = reinterpret_cast<O*>(buf) + tid;
+#pragma unroll
+  for (int c = 0; c < N; c += 2) {
+    const float x = __fmul_rn(__uint_as_float(v[c]), a), y = __fmul_rn(__uint_as_float(v[c + 1]), a);
+    if constexpr (sizeof(O) == 4) {
+      o[c * 128] = x;
+      o[(c + 1) * 128] = y;
+    } else {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+      o[c * 128] = b.x;
+      o[(c + 1) * 128] = b.y;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -368,13 +488,15 @@ template <int KIND, bool MX, int T, bool LORA>
 __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
     k_fp4_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                const __grid_constant__ GemmParams p) {
-  using S = GemmShape<MX, T, LORA>;
+  using S = GemmShape<KIND, MX, T, LORA>;
   constexpr int kTpb = S::kTilesPerBlock;
   constexpr int kScaleK = MX ? 128 : 64;  // summed elements of one scale tile
+  constexpr int kEpilogues = S::kEpilogues;
   extern __shared__ uint8_t gemm_smem_raw[];
   __shared__ GemmBars bars;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(gemm_smem_raw) + 1023) & ~uintptr_t{1023});
   uint8_t* const chunks = smem + S::kStages * S::kStageBytes;
+  uint8_t* const outs = chunks + S::kChunks * S::kChunkBytes;
   int* start = reinterpret_cast<int*>(smem + S::kSmemBytes);
   int* lo = start + p.groups + 1;
   int* hi = lo + p.groups + 1;
@@ -393,13 +515,14 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&bars.acc_full[i]), 1);
-      mbar_init(smem_addr(&bars.acc_empty[i]), 4);
+      mbar_init(smem_addr(&bars.acc_empty[i]), 4 * kEpilogues);
       mbar_init(smem_addr(&bars.chunk_full[i]), kLoraThreads / 32);
       mbar_init(smem_addr(&bars.chunk_empty[i]), 1);
     }
     mbar_init(smem_addr(&bars.drain), 1);
     fence_mbar_init();
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // The kernel before this one on the stream wrote the operands.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 0) {  // where each group's tiles begin
@@ -567,95 +690,128 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
       __syncwarp();
       mbar_wait(smem_addr(&bars.drain), 0);
     }
-  } else if (warp >= 4 && warp < 8) {
-    const int quarter = warp & 3;
-    int acc = 0;
+  } else if (warp >= 4 && warp < 4 + 4 * kEpilogues) {
+    // Group `half` of 128 threads takes every kEpilogues-th chunk.  (CONTR: the sums are short, two
+    // groups keep up with them.)
+    const int half = (warp - 4) / 4, quarter = warp & 3, tid = threadIdx.x & 127;
+    int acc = 0, buf = 0;
     uint32_t acc_phase = 0;
+    const int es = p.out_f32 ? 4 : 2, step = p.out_f32 ? 16 : 32;
+    uint8_t* const my_outs = outs + half * 2 * kOutBytes;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
       const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, tile);
       float a = 1.0f;
       if (!MX) a = __fmul_rn(__ldg(p.sg_a + (KIND == kGemmRows ? t.g : 0)), __ldg(p.sg_b));
-      ok = mbar_wait(smem_addr(&bars.acc_full[acc]), acc_phase);
-      if (!__all_sync(0xFFFFFFFFu, ok)) {
-        ok = false;
-        break;
-      }
+      const bool full = mbar_wait(smem_addr(&bars.acc_full[acc]), acc_phase);
+      ok = half == 0 ? role_all<2>(full) : role_all<3>(full);
+      if (!ok) break;
       umma_fence_after();
-      const int n = t.a0 + quarter * 32 + lane;
       const int64_t row0 = KIND == kGemmRows ? t.b0 : static_cast<int64_t>(t.g) * p.nb + t.b0;
-      const int64_t at = row0 * p.na + n;
-      const bool live = n < p.na;
+      const int64_t stride = static_cast<int64_t>(p.na) * es;
+      uint8_t* const out = static_cast<uint8_t*>(p.out) + row0 * stride + static_cast<int64_t>(t.a0) * es;
+      const int bytes = min(128, p.na - t.a0) * es;
       const bool none = t.k == 0;  // an empty sum: no product wrote the accumulator
-      for (int c0 = 0; c0 < t.valid; c0 += 16) {
-        uint32_t v[16];
-        tmem_ld16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * T + c0, v);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        if (live) {
-          if (p.out_f32) {
-            float* o = static_cast<float*>(p.out) + at + static_cast<int64_t>(c0) * p.na;
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              if (c0 + c < t.valid)
-                o[static_cast<int64_t>(c) * p.na] = none ? 0.0f : __fmul_rn(__uint_as_float(v[c]), a);
-          } else {
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at + static_cast<int64_t>(c0) * p.na;
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              if (c0 + c < t.valid)
-                o[static_cast<int64_t>(c) * p.na] =
-                    __float2bfloat16_rn(none ? 0.0f : __fmul_rn(__uint_as_float(v[c]), a));
-          }
+      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * T;
+      bool held = true;
+      for (int c0 = half * step; c0 < t.valid; c0 += kEpilogues * step) {
+        uint8_t* const o = my_outs + buf * kOutBytes;
+        if (p.out_f32) fetch_chunk<float, 16>(from + c0, a, none, o, tid);
+        else fetch_chunk<__nv_bfloat16, 32>(from + c0, a, none, o, tid);
+        if (c0 + kEpilogues * step >= t.valid) {  // the group's last chunk: its part has been read
+          umma_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&bars.acc_empty[acc]));
+          held = false;
         }
+        if (half == 0) role_sync<2>();
+        else role_sync<3>();
+        if (p.out_f32)
+          store_rows<512, 16>(p.out_vec, o, out + c0 * stride, stride, min(16, t.valid - c0), bytes, tid);
+        else
+          store_rows<256, 32>(p.out_vec, o, out + c0 * stride, stride, min(32, t.valid - c0), bytes, tid);
+        buf ^= 1;
       }
-      umma_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&bars.acc_empty[acc]));
+      if (held) {  // no chunk for this group
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&bars.acc_empty[acc]));
+      }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
   } else if (KIND == kGemmRows && warp >= 8 && warp < 12) {
     constexpr int kRowsPerThread = (T + kScaleThreads - 1) / kScaleThreads;
-    constexpr int kAhead = 4;  // stages whose scales are loaded together
+    constexpr int kAhead = 4;  // stages whose scales are loaded together: a batch
     constexpr int kBlockBytes = MX ? 8 : 16;
     const int tid = threadIdx.x - 256;
+    const int blocks = (p.k + kGemmKBlock - 1) / kGemmKBlock;
     GemmRing ring;
-    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, tile);
-      const int blocks = (t.k + kGemmKBlock - 1) / kGemmKBlock;
-      for (int kb0 = 0; kb0 < blocks && ok; kb0 += kAhead) {
-        uint32_t w[kRowsPerThread][kAhead][4];
+    struct Batch {
+      int tile, kb, b0, valid, n;
+    };
+    auto enter = [&](Batch& b) {  // a tile's first batch
+      if (b.tile >= tiles) return;
+      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, b.tile);
+      b.kb = 0, b.b0 = t.b0, b.valid = t.valid, b.n = t.n;
+    };
+    auto after = [&](const Batch& b) {
+      Batch c = b;
+      c.kb += kAhead;
+      if (c.kb >= blocks) {
+        c.tile += gridDim.x;
+        enter(c);
+      }
+      return c;
+    };
+    constexpr int kWords = kAhead * kBlockBytes / 4;
+    struct Loaded {
+      uint32_t w[kRowsPerThread][kWords + 1];
+      ScaleRow row[kRowsPerThread];
+    };
+    auto load = [&](const Batch& b, Loaded& l) {
+      if (b.tile >= tiles) return;
+#pragma unroll
+      for (int i = 0; i < kRowsPerThread; ++i) {
+        const int r = tid + kScaleThreads * i;
+        l.row[i] = load_scales<kWords>(p, b.b0 + r, r < b.valid, b.kb * kBlockBytes, l.w[i]);
+      }
+    };
+    // The next batch is loaded after this one's first stage is written: its words have arrived by then
+    // (waiting for them later would wait for the newer loads too), and there is the time of the
+    // other stages for the new ones.
+    auto write = [&](const Batch& b, const Loaded& l, const Batch& next, Loaded& into) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (b.kb + j >= blocks || !ok) break;
+        ok = warp_wait(smem_addr(&bars.empty[ring.s]), ring.phase ^ 1);
+        if (!ok) break;
+        uint8_t* sb = smem + ring.s * S::kStageBytes + S::kBytesA + S::kBytesB + S::kBytesSfa;
 #pragma unroll
         for (int i = 0; i < kRowsPerThread; ++i) {
           const int r = tid + kScaleThreads * i;
-          const uint8_t* src = p.sfb + static_cast<int64_t>(t.b0 + r) * p.sfb_row_bytes;
+          if (r < b.n) {
+            uint8_t* dst = sb + (r / 128) * kTpb * 512 + (r % 32) * 16 + ((r % 128) / 32) * 4;
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-            const int at = (kb0 + j) * kBlockBytes;
-            load_scale_row<kBlockBytes>(src + at, r < t.valid ? p.sfb_row_bytes - at : 0, p.sfb_vec, w[i][j]);
+            for (int q = 0; q < kTpb; ++q)
+              *reinterpret_cast<uint32_t*>(dst + 512 * q) = scale_word<kWords>(l.w[i], l.row[i], j * kTpb + q);
           }
         }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          if (kb0 + j >= blocks || !ok) break;
-          ok = mbar_wait(smem_addr(&bars.empty[ring.s]), ring.phase ^ 1);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          uint8_t* sb = smem + ring.s * S::kStageBytes + S::kBytesA + S::kBytesB + S::kBytesSfa;
-#pragma unroll
-          for (int i = 0; i < kRowsPerThread; ++i) {
-            const int r = tid + kScaleThreads * i;
-            if (r < t.n) {
-              uint8_t* dst = sb + (r / 128) * kTpb * 512 + (r % 32) * 16 + ((r % 128) / 32) * 4;
-#pragma unroll
-              for (int q = 0; q < kTpb; ++q) *reinterpret_cast<uint32_t*>(dst + 512 * q) = w[i][j][q];
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&bars.full[ring.s]));
-          ring.next(S::kStages);
-        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&bars.full[ring.s]));
+        ring.next(S::kStages);
+        if (j == 0) load(next, into);
       }
+    };
+    Loaded w0, w1;
+    Batch b0{static_cast<int>(blockIdx.x)}, b1;
+    enter(b0);
+    load(b0, w0);
+    while (b0.tile < tiles && ok) {
+      b1 = after(b0);
+      write(b0, w0, b1, w1);
+      if (b1.tile >= tiles || !ok) break;
+      b0 = after(b1);
+      write(b1, w1, b0, w0);
     }
   }
   if constexpr (LORA) {
@@ -666,12 +822,12 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
       int turn = 0;
       for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
         const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, tile);
-        lora_barrier();  // the last tile's ids have been read
+        role_sync<1>();  // the last tile's ids have been read
         for (int r = tid; r < t.n; r += kLoraThreads) {
           const int id = r < t.valid ? __ldg(p.lora_ids + t.b0 + r) : -1;
           bars.ids[r] = id < p.adapters ? id : -1;
         }
-        lora_barrier();
+        role_sync<1>();
         // the smallest adapter of the tile's rows above `a`
         auto next_above = [&](int a) {
           int m = INT_MAX;
@@ -681,7 +837,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
           }
           m = __reduce_min_sync(0xFFFFFFFFu, m);
           if (lane == 0) bars.next_id[turn][tid >> 5] = m;
-          lora_barrier();
+          role_sync<1>();
           m = min(min(bars.next_id[turn][0], bars.next_id[turn][1]), min(bars.next_id[turn][2], bars.next_id[turn][3]));
           turn ^= 1;
           return m;
@@ -701,7 +857,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
             }
           }
           // all four warps go on, or none: they meet at barriers
-          ok = lora_all(mbar_wait(smem_addr(&bars.chunk_empty[chunk.s]), chunk.phase ^ 1));
+          ok = role_all<1>(mbar_wait(smem_addr(&bars.chunk_empty[chunk.s]), chunk.phase ^ 1));
           if (!ok) break;
           uint8_t* const ch = chunks + chunk.s * S::kChunkBytes;
           const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -829,6 +985,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const __grid_con
   const int tg = warp % TG, part = warp / TG;
   const int slice = blockIdx.x % p.slices, job = blockIdx.x / p.slices % p.jobs;
   const int row0 = blockIdx.x / p.slices / p.jobs * kRows;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x < kRows) {
     const int id = row0 + threadIdx.x < p.rows ? __ldg(p.ids + row0 + threadIdx.x) : -1;

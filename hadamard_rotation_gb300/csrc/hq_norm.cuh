@@ -280,6 +280,7 @@ struct RowRing {
   RowRing<BF16, NT> ring{p, norm_smem + 8 * static_cast<size_t>(p.cols), sh, cluster, clusters,       \
                          cluster < all_steps ? (all_steps - cluster + clusters - 1) / clusters : 0,   \
                          col0, my_cols * kEs};                                                        \
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");                                     \
   if (threadIdx.x == 0) {                                                                             \
     for (int i = 0; i < p.stages; ++i) mbar_init(smem_addr(&sh.full[i]), 1);                          \
     fence_mbar_init();                                                                                \

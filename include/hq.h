@@ -337,7 +337,7 @@ HQ_API hq_status hq_dequant_nvfp4(const uint8_t* q, const uint8_t* scales, const
  *     hq_swizzle_scales for either format: padding entries must be 0.  32-byte aligned.
  *   - offsets: int32 [E + 1] on the device, non-decreasing from 0: group e is the half-open range
  *     offsets[e] .. offsets[e + 1].  Values outside the tensor are clamped to it; the host never
- *     reads them.  E <= 1024.
+ *     reads them.  E <= 512.
  *   - out_dtype: HQ_BF16 or HQ_F32; out is row-major and contiguous, aligned to its element.
  *   - Sizes beyond 2^31 - 1024 return HQ_ERR_SHAPE.
  *   - A launch may start while the kernel before it on the stream ends; it waits for that kernel
