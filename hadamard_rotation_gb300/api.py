@@ -377,7 +377,8 @@ def _grouped_gemm(xq, xs, x_sg, wq, ws, w_sg, offsets, out, out_dtype, stream):
         args.append(_given(w_sg, (E,), torch.float32, dev, "w_sg"))
     args.append(_given(offsets, (E + 1,), torch.int32, dev, "offsets"))
     out = _out(out, (M, N), out_dtype, dev)
-    args += [M, N, K, E, out.data_ptr(), _DTYPES[out.dtype]]
+    work = _work(hq_grouped_gemm_workspace_bytes(M, K, E), dev, stream)
+    args += [M, N, K, E, out.data_ptr(), _DTYPES[out.dtype], _addr(work)]
     _launch(dev, "hq_grouped_gemm_nvfp4" if x_sg is not None else "hq_grouped_gemm_mxfp4", args, stream)
     return out
 
@@ -453,12 +454,30 @@ def hq_grouped_wgrad_mxfp4(gq: torch.Tensor, gs: torch.Tensor, xq: torch.Tensor,
     return _grouped_wgrad(gq, gs, None, xq, xs, None, offsets, out, out_dtype, stream)
 
 
-def hq_lora_gemm_workspace_bytes(M: int, R: int) -> int:
-    """Bytes of the workspace of hq_lora_gemm_* (which this binding allocates itself)."""
-    n = _lib.load().hq_lora_gemm_workspace_bytes(M, R)
+def hq_grouped_gemm_workspace_bytes(M: int, K: int, E: int) -> int:
+    """Bytes of the workspace of hq_grouped_gemm_* (which this binding allocates itself)."""
+    n = _lib.load().hq_grouped_gemm_workspace_bytes(M, K, E)
     if n < 0:
-        raise ValueError("hq_lora_gemm_workspace_bytes: M >= 0, R a multiple of 8 up to 128")
+        raise ValueError("hq_grouped_gemm_workspace_bytes: M >= 0, K a multiple of 32, 0 <= E <= 512")
     return n
+
+
+def hq_lora_gemm_workspace_bytes(M: int, K: int, R: int) -> int:
+    """Bytes of the workspace of hq_lora_gemm_* (which this binding allocates itself)."""
+    n = _lib.load().hq_lora_gemm_workspace_bytes(M, K, R)
+    if n < 0:
+        raise ValueError("hq_lora_gemm_workspace_bytes: M >= 0, K a multiple of 32, R a multiple of 8 up to 128")
+    return n
+
+
+def _work(nbytes: int, device: torch.device, stream: torch.cuda.Stream | None) -> torch.Tensor | None:
+    """A workspace for one call; freed when the call returns, so not before ``stream`` is done with it."""
+    if nbytes == 0:
+        return None
+    work = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        work.record_stream(stream)
+    return work
 
 
 def _lora_gemm(xq, xs, x_sg, wq, ws, w_sg, x, lora_a, lora_b, scaling, row_adapter, out, out_dtype, stream):
@@ -487,10 +506,8 @@ def _lora_gemm(xq, xs, x_sg, wq, ws, w_sg, x, lora_a, lora_b, scaling, row_adapt
              _given(scaling, (n,), torch.float32, dev, "scaling"),
              _given(row_adapter, (M,), torch.int32, dev, "row_adapter")]
     out = _out(out, (M, N), out_dtype, dev)
-    work = torch.empty(hq_lora_gemm_workspace_bytes(M, R), dtype=torch.uint8, device=dev)
-    if stream is not None:
-        work.record_stream(stream)  # freed when this call returns: not before the stream is done with it
-    args += [M, N, K, n, R, out.data_ptr(), _DTYPES[out.dtype], work.data_ptr()]
+    work = _work(hq_lora_gemm_workspace_bytes(M, K, R), dev, stream)
+    args += [M, N, K, n, R, out.data_ptr(), _DTYPES[out.dtype], _addr(work)]
     _launch(dev, "hq_lora_gemm_nvfp4" if x_sg is not None else "hq_lora_gemm_mxfp4", args, stream)
     return out
 
@@ -675,13 +692,11 @@ def hq_block_norm_bwd(dh_out: torch.Tensor | None, dn: torch.Tensor | None, h_ou
     dw_pre = torch.empty(D, dtype=torch.float32, device=dev) if w_pre is not None else None
     dgate = None if kind == _GATE_NONE else torch.empty(
         gate.shape, dtype=h_out.dtype if kind == _GATE_FULL else torch.float32, device=dev)
-    work = torch.empty(hq_block_norm_bwd_workspace_bytes(M, D), dtype=torch.uint8, device=dev)
-    if stream is not None:
-        work.record_stream(stream)  # freed when this call returns: not before the stream is done with it
+    work = _work(hq_block_norm_bwd_workspace_bytes(M, D), dev, stream)
     _launch(dev, "hq_block_norm_bwd",
             [dhp, ld_dh, dnp, ld_dn, hp, ld_h, yp, ld_y, _DTYPES[h_out.dtype], M, D, wp, wq, pdt, kind, g, ld_g,
              (_NORM_POST if post else 0) | (_NORM_PRE if pre_norm else 0), rp, rq, alpha, dh.data_ptr(),
-             _addr(dy), _addr(dw_post), _addr(dgate), _addr(dw_pre), work.data_ptr()], stream)
+             _addr(dy), _addr(dw_post), _addr(dgate), _addr(dw_pre), _addr(work)], stream)
     return dh, dy, dw_post, dgate, dw_pre
 
 

@@ -75,6 +75,19 @@ cudaError_t sm_count(int* sms) {
   return e;
 }
 
+// bf16 output [groups, rows, n], rows contiguous, in boxes of 32 rows x 64 elements, 128-byte swizzle.
+bool encode_out(CUtensorMap* map, void* out, int64_t n, int64_t rows, int64_t groups) {
+  const EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t size[3] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(groups)};
+  const cuuint64_t stride[2] = {static_cast<cuuint64_t>(n * 2), static_cast<cuuint64_t>(n * rows * 2)};
+  const cuuint32_t box[3] = {64, 32, 1}, step[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, out, size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // One operand's codes as the launch needs them.
 struct Codes {
   const uint8_t* q;
@@ -85,10 +98,12 @@ template <int KIND, bool MX, int T, bool LORA = false>
 hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t most_tiles, hq_stream stream) {
   using S = hq::GemmShape<KIND, MX, T, LORA>;
   auto kernel = hq::k_fp4_gemm<KIND, MX, T, LORA>;
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, mo = {};
   if (!encode_codes(&ma, a.q, a.row_bytes, a.rows, a.groups, hq::kGemmLanes, 3) ||
       !encode_codes(&mb, b.q, b.row_bytes, b.rows, 1, S::kBox, 2))
     return cuda_fail(cudaErrorInvalidValue);
+  p.out_tma = !p.out_f32 && p.out_vec == 16 &&
+              encode_out(&mo, p.out, p.na, KIND == hq::kGemmRows ? p.extent : p.nb, KIND == hq::kGemmRows ? 1 : p.groups);
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -106,9 +121,66 @@ hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t most_tile
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, p);
+  e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, mo, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? HQ_OK : cuda_fail(e);
+}
+
+// The scales of ragged rows in the tile layout, each group's rows from a multiple of 64 on (units of 64
+// rows: a tile of the wide kernel starts at one).  A CTA per 128 rows; padding rows are not written
+// (the products of their columns are not stored).
+__global__ void __launch_bounds__(256) k_group_scales(const uint8_t* __restrict__ s, const int32_t* offsets, int groups,
+                                                      int rows, int row_bytes, int col_tiles, uint4* __restrict__ out) {
+  __shared__ int first[2], count[2];  // of the CTA's two units: the first row of x, how many
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x < 2) count[threadIdx.x] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int base = 0;
+    for (int g0 = 0; g0 < groups && base < 2 * static_cast<int>(blockIdx.x) + 2; g0 += 32) {
+      const int g = g0 + lane;
+      int a = 0, b = 0;
+      if (g < groups) {
+        a = offsets ? offsets[g] : 0;
+        b = offsets ? offsets[g + 1] : rows;
+        a = max(0, min(a, rows));
+        b = max(a, min(b, rows));
+      }
+      const int u = (b - a + 63) / 64, sum = hq::warp_scan(u, lane);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int at = 2 * static_cast<int>(blockIdx.x) + q - (base + sum - u);  // the unit within this group
+        if (at >= 0 && at < u) {
+          first[q] = a + 64 * at;
+          count[q] = min(64, b - a - 64 * at);
+        }
+      }
+      base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+  }
+  __syncthreads();
+  if (count[0] + count[1] == 0) return;
+  const int r = threadIdx.x & 31;
+  for (int ct = threadIdx.x >> 5; ct < col_tiles; ct += 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      w[q] = 0;
+      const int at = (q & 1) * 32 + r;
+      if (at >= count[q >> 1]) continue;
+      const uint8_t* src = s + static_cast<int64_t>(first[q >> 1] + at) * row_bytes + 4 * ct;
+      if (row_bytes % 4 == 0 && reinterpret_cast<uintptr_t>(s) % 4 == 0) {
+        w[q] = __ldg(reinterpret_cast<const uint32_t*>(src));
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (4 * ct + c < row_bytes) w[q] |= static_cast<uint32_t>(__ldg(src + c)) << (8 * c);
+      }
+    }
+    out[(static_cast<int64_t>(blockIdx.x) * col_tiles + ct) * 32 + r] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 constexpr int64_t kMaxExtent = (int64_t{1} << 31) - 1024;  // sizes and row indexes are ints in the kernel
@@ -116,6 +188,36 @@ constexpr int64_t kMaxExtent = (int64_t{1} << 31) - 1024;  // sizes and row inde
 hq_status out_zero(void* out, int64_t n, hq_dtype dt, hq_stream stream) {
   const cudaError_t e = cudaMemsetAsync(out, 0, static_cast<size_t>(n) * (dt == HQ_F32 ? 4 : 2),
                                         static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? HQ_OK : cuda_fail(e);
+}
+
+// Tiles of 64 or of 192 columns: the narrow ones read the tokens' scales as they are and have more stages
+// in flight per byte of operand, the wide ones read the weights half or a third as often.
+bool narrow_rows(int64_t M, int64_t E) { return M <= 64 * E; }
+
+// 128-row tiles of k_group_scales' output, and its bytes.
+int64_t group_scale_tiles(int64_t M, int64_t groups) {
+  return ((M + 63) / 64 + (groups < M ? groups : M) + 1) / 2;
+}
+int64_t group_scale_bytes(int64_t M, int64_t K, int64_t groups, bool mx) {
+  return group_scale_tiles(M, groups) * ((K + (mx ? 127 : 63)) / (mx ? 128 : 64)) * 512;
+}
+
+// Lay the scales of ragged rows out for the wide kernel and point `p` at them.
+hq_status tile_scales(GemmParams& p, uint8_t* work, hq_stream stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(group_scale_tiles(p.extent, p.groups)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, k_group_scales, p.sfb, p.offsets, p.groups, p.extent, p.sfb_row_bytes,
+                                     p.k_tiles, reinterpret_cast<uint4*>(work));
+  if (e == cudaSuccess) e = cudaGetLastError();
+  p.sfb = work;
   return e == cudaSuccess ? HQ_OK : cuda_fail(e);
 }
 
@@ -149,7 +251,7 @@ GemmParams rows_params(const uint8_t* xs, const float* x_sg, const uint8_t* ws, 
 template <bool MX>
 hq_status grouped_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, const uint8_t* wq, const uint8_t* ws,
                        const float* w_sg, const int32_t* offsets, int64_t M, int64_t N, int64_t K, int64_t E, void* out,
-                       hq_dtype dt, hq_stream stream) {
+                       hq_dtype dt, void* workspace, hq_stream stream) {
   if (dt != HQ_F32 && dt != HQ_BF16) return HQ_ERR_DTYPE;
   if (M < 0 || N < 0 || K < 0 || E < 0 || K % 32 != 0) return HQ_ERR_SHAPE;
   if (M > kMaxExtent || N > kMaxExtent || K > kMaxExtent || E > hq::kGemmMaxGroups) return HQ_ERR_SHAPE;
@@ -157,7 +259,7 @@ hq_status grouped_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, 
   if (!out || !offsets) return HQ_ERR_NULL;
   if (!aligned(out, dt == HQ_F32 ? 4 : 2) || !aligned(offsets, 4)) return HQ_ERR_ALIGN;
   const int64_t tiles_a = (N + 127) / 128;
-  const bool narrow = M <= 64 * E;
+  const bool narrow = narrow_rows(M, E);
   const int64_t tiles = ((M + (narrow ? 63 : 191)) / (narrow ? 64 : 192) + (E < M ? E : M)) * tiles_a;
   if (tiles > kMaxExtent) return HQ_ERR_SHAPE;
   if (K == 0) return out_zero(out, M * N, dt, stream);
@@ -167,6 +269,12 @@ hq_status grouped_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, 
   GemmParams p = rows_params<MX>(xs, x_sg, ws, w_sg, M, N, K, E, out, dt);
   p.offsets = offsets;
   const Codes a = {wq, K / 2, N, E}, b = {xq, K / 2, M, 1};
+  if (!narrow) {
+    if (!workspace) return HQ_ERR_NULL;
+    if (!aligned(workspace, 32)) return HQ_ERR_ALIGN;
+    const hq_status st = tile_scales(p, static_cast<uint8_t*>(workspace), stream);
+    if (st != HQ_OK) return st;
+  }
   return narrow ? launch<hq::kGemmRows, MX, 64>(p, a, b, tiles, stream)
                 : launch<hq::kGemmRows, MX, 192>(p, a, b, tiles, stream);
 }
@@ -245,6 +353,8 @@ cudaError_t launch_shrink(const hq::ShrinkParams& p, int sms, cudaStream_t strea
                         : launch_shrink<4, TG>(p, sms, stream);
 }
 
+int64_t lora_t_bytes(int64_t M, int64_t R) { return (4 * M * R + 31) / 32 * 32; }
+
 template <bool MX>
 hq_status lora_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, const uint8_t* wq, const uint8_t* ws,
                     const float* w_sg, const void* x, int64_t ldx, const void* a, const void* b, const float* scaling,
@@ -261,9 +371,9 @@ hq_status lora_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, con
     return HQ_ERR_NULL;
   if (!aligned(out, dt == HQ_F32 ? 4 : 2) || !aligned(xq, 16) || !aligned(wq, 16) || !aligned(ws, 32) ||
       !aligned(x, 16) || (M > 1 && ldx % 8 != 0) || !aligned(a, 16) || !aligned(b, 16) || !aligned(scaling, 4) ||
-      !aligned(ids, 4) || !aligned(workspace, 16) || !aligned(x_sg, 4) || !aligned(w_sg, 4))
+      !aligned(ids, 4) || !aligned(workspace, 32) || !aligned(x_sg, 4) || !aligned(w_sg, 4))
     return HQ_ERR_ALIGN;
-  const bool narrow = M <= 64;
+  const bool narrow = narrow_rows(M, 1);
   const int64_t tiles = (M + (narrow ? 63 : 191)) / (narrow ? 64 : 192) * ((N + 127) / 128);
   if (tiles > kMaxExtent) return HQ_ERR_SHAPE;
   int sms = 0;
@@ -293,6 +403,10 @@ hq_status lora_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, con
   p.lora_ids = ids;
   p.adapters = s.adapters;
   p.rank = s.rank;
+  if (!narrow) {
+    const hq_status st = tile_scales(p, s.t + lora_t_bytes(M, R), stream);
+    if (st != HQ_OK) return st;
+  }
   const Codes ca = {wq, K / 2, N, 1}, cb = {xq, K / 2, M, 1};
   return narrow ? launch<hq::kGemmRows, MX, 64, true>(p, ca, cb, tiles, stream)
                 : launch<hq::kGemmRows, MX, 192, true>(p, ca, cb, tiles, stream);
@@ -336,14 +450,14 @@ extern "C" {
 
 hq_status hq_grouped_gemm_nvfp4(const uint8_t* xq, const uint8_t* xs, const float* x_sg, const uint8_t* wq,
                                 const uint8_t* ws, const float* w_sg, const int32_t* offsets, int64_t M, int64_t N,
-                                int64_t K, int64_t E, void* out, hq_dtype out_dtype, hq_stream stream) {
-  return grouped_gemm<false>(xq, xs, x_sg, wq, ws, w_sg, offsets, M, N, K, E, out, out_dtype, stream);
+                                int64_t K, int64_t E, void* out, hq_dtype out_dtype, void* workspace, hq_stream stream) {
+  return grouped_gemm<false>(xq, xs, x_sg, wq, ws, w_sg, offsets, M, N, K, E, out, out_dtype, workspace, stream);
 }
 
 hq_status hq_grouped_gemm_mxfp4(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const uint8_t* ws,
                                 const int32_t* offsets, int64_t M, int64_t N, int64_t K, int64_t E, void* out,
-                                hq_dtype out_dtype, hq_stream stream) {
-  return grouped_gemm<true>(xq, xs, nullptr, wq, ws, nullptr, offsets, M, N, K, E, out, out_dtype, stream);
+                                hq_dtype out_dtype, void* workspace, hq_stream stream) {
+  return grouped_gemm<true>(xq, xs, nullptr, wq, ws, nullptr, offsets, M, N, K, E, out, out_dtype, workspace, stream);
 }
 
 hq_status hq_grouped_wgrad_nvfp4(const uint8_t* gq, const uint8_t* gs, const float* g_sg, const uint8_t* xq,
@@ -358,9 +472,14 @@ hq_status hq_grouped_wgrad_mxfp4(const uint8_t* gq, const uint8_t* gs, const uin
   return grouped_wgrad<true>(gq, gs, nullptr, xq, xs, nullptr, offsets, T, N, K, E, out, out_dtype, stream);
 }
 
-int64_t hq_lora_gemm_workspace_bytes(int64_t M, int64_t R) {
-  if (M < 0 || M > kMaxExtent || R < 8 || R > 128 || R % 8 != 0) return -1;
-  return 4 * M * R;
+int64_t hq_grouped_gemm_workspace_bytes(int64_t M, int64_t K, int64_t E) {
+  if (M < 0 || K < 0 || E < 0 || M > kMaxExtent || K > kMaxExtent || E > hq::kGemmMaxGroups || K % 32 != 0) return -1;
+  return M == 0 || E == 0 || narrow_rows(M, E) ? 0 : group_scale_bytes(M, K, E, false);
+}
+
+int64_t hq_lora_gemm_workspace_bytes(int64_t M, int64_t K, int64_t R) {
+  if (M < 0 || M > kMaxExtent || K < 0 || K > kMaxExtent || K % 32 != 0 || R < 8 || R > 128 || R % 8 != 0) return -1;
+  return lora_t_bytes(M, R) + (narrow_rows(M, 1) ? 0 : group_scale_bytes(M, K, 1, false));
 }
 
 hq_status hq_lora_gemm_nvfp4(const uint8_t* xq, const uint8_t* xs, const float* x_sg, const uint8_t* wq,

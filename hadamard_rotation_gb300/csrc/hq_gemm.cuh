@@ -25,9 +25,10 @@
 //                 already the order that tensor memory wants)
 //   warp 1        copies the scales to tensor memory (tcgen05.cp) and issues the products
 //   warp 2        allocates tensor memory
-//   warps 4..7    epilogue: tensor memory -> registers -> * a -> shared memory -> global (CONTR: 4..11)
-//   warps 8..11   (ROWS) the tokens' scales: row-major in global memory, since a group starts at
-//                 any row; moved through registers into the tile layout
+//   warps 4..7    epilogue: tensor memory -> registers -> * a -> shared memory -> global (4..11 where
+//                 the next does not apply)
+//   warps 8..11   (ROWS, narrow tiles) the tokens' scales: row-major in global memory, since a group
+//                 starts at any row; moved through registers into the tile layout
 //   warps 12..15  (adapters) the operands of the adapters' second product, below
 // Shared memory holds a ring of kStages stages (256 steps of the summed axis each); tensor
 // memory holds two accumulators, so the epilogue of a tile runs under the products of the next.
@@ -59,7 +60,7 @@ enum GemmKind { kGemmRows = 0, kGemmContr = 1 };
 struct GemmParams {
   const uint8_t* sfa;       // scales of A in the tile layout
   int64_t sfa_group_bytes;  // bytes of one group's scales of A (ROWS)
-  const uint8_t* sfb;       // scales of B: row-major (ROWS), tile layout (CONTR)
+  const uint8_t* sfb;       // scales of B: row-major (narrow ROWS), or in the tile layout
   const float* sg_a;        // per-tensor scales (ROWS: one per group; CONTR: one); NULL: 1
   const float* sg_b;
   const int32_t* offsets;   // groups + 1; NULL: one group of all `extent` rows
@@ -71,10 +72,11 @@ struct GemmParams {
   int tiles_a;              // ceil(na / 128)
   int tiles_b;              // CONTR: ceil(nb / T)
   int k_tiles;              // 512-byte scale tiles per 128 rows
-  int sfb_row_bytes;        // ROWS: bytes of one row of scales
-  int sfb_mode;             // ROWS: how they are read (load_scales)
+  int sfb_row_bytes;        // bytes of one row of row-major scales
+  int sfb_mode;             // how they are read (load_scales)
   void* out;                // ROWS: [extent, na]; CONTR: [groups, nb, na]
   int out_f32;
+  int out_tma;              // bf16 rows aligned to 16 bytes: map_out is valid
   int out_vec;              // bytes per store: what the rows of out are aligned to, up to 16
   // adapters
   const uint8_t* lora_b;    // bf16 [adapters, na, rank]
@@ -101,12 +103,13 @@ struct GemmShape {
   static constexpr int kChunkBytes = LORA ? kGemmLanes * 128 + 2 * T * 128 : 0;
   static constexpr int kChunks = T >= 128 ? 1 : 2;
   static constexpr int kChunkGap = T >= 128 ? 5 : 2;  // stages between two chunks of a tile
-  static constexpr int kEpilogues = KIND == kGemmContr ? 2 : 1;  // groups of 128 threads
-  static constexpr int kOuts = kEpilogues * 2 * 8 * 1024;        // their output buffers
+  static constexpr bool kTiledB = KIND == kGemmContr || T >= 128;  // B's scales come in the tile layout
+  static constexpr int kEpilogues = kTiledB && !LORA ? 2 : 1;      // groups of 128 threads
+  static constexpr int kOuts = kEpilogues * 2 * 8 * 1024;          // their output buffers
   static constexpr int kRingBytes = 218 * 1024 - kChunks * kChunkBytes - kOuts;
   static constexpr int kStages = kRingBytes / kStageBytes < 7 ? kRingBytes / kStageBytes : 7;
   static constexpr int kSmemBytes = kStages * kStageBytes + kChunks * kChunkBytes + kOuts;
-  static_assert(kSmemBytes + 1024 + 12 * (kGemmMaxGroups + 1) + 1280 <= 227 * 1024, "a CTA has 227 KB");
+  static_assert(kSmemBytes + 1024 + 16 * (LORA ? 2 : kGemmMaxGroups + 1) + 1280 <= 227 * 1024, "a CTA has 227 KB");
   // tensor memory columns: two accumulators, then two sets of scales (stage parity)
   static constexpr int kColsSfa = kTilesPerBlock * 4;
   static constexpr int kColsSfb = kTilesPerBlock * kRowTilesB * 4;
@@ -128,7 +131,7 @@ struct GemmBars {
   int tiles;
 };
 
-inline size_t gemm_smem_bytes(int bytes, int groups) { return 1024 + static_cast<size_t>(bytes) + 12 * static_cast<size_t>(groups + 1); }
+inline size_t gemm_smem_bytes(int bytes, int groups) { return 1024 + static_cast<size_t>(bytes) + 16 * static_cast<size_t>(groups + 1); }
 
 // ---------------------------------------------------------------------------
 // PTX.
@@ -253,14 +256,13 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&v)[16]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&v)[32]) {
+// 16 lanes x 32 columns in the shape of matrix fragments.
+__device__ __forceinline__ void tmem_load_fragments(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(taddr)
       : "memory");
 }
@@ -275,11 +277,12 @@ struct GemmTile {
   int valid;   // columns that exist
   int n;       // columns of the instruction (valid rounded up to 16)
   int k0, k;   // summed range
+  int s0;      // first row of B's scales in the tile layout, a multiple of 64
 };
 
 template <int KIND, int T>
 __device__ __forceinline__ GemmTile gemm_tile(const GemmParams& p, const int* start, const int* lo, const int* hi,
-                                              int tile) {
+                                              const int* units, int tile) {
   int l = 0, r = p.groups;  // the last group that starts at or before `tile`
   while (r - l > 1) {
     const int m = (l + r) >> 1;
@@ -293,23 +296,35 @@ __device__ __forceinline__ GemmTile gemm_tile(const GemmParams& p, const int* st
   if constexpr (KIND == kGemmRows) {
     // equal widths rather than one narrow last tile
     const int parts = (span + T - 1) / T;
-    const int width = ((span + parts - 1) / parts + 15) & ~15;
-    const int bt = local % parts;
-    t.a0 = (local / parts) * kGemmLanes;
+    constexpr int kStep = T >= 128 ? 64 : 16;
+    const int width = ((span + parts - 1) / parts + kStep - 1) & ~(kStep - 1);
+    const int at = local / parts, bt = local - at * parts;
+    t.a0 = at * kGemmLanes;
     t.b0 = lo[l] + bt * width;
     t.valid = min(width, hi[l] - t.b0);
+    t.s0 = T >= 128 ? units[l] * 64 + bt * width : 0;
     t.k0 = 0;
     t.k = p.k;
   } else {
-    const int bt = local % p.tiles_b;
-    t.a0 = (local / p.tiles_b) * kGemmLanes;
-    t.b0 = bt * T;
+    const int at = local / p.tiles_b, bt = local - at * p.tiles_b;
+    t.a0 = at * kGemmLanes;
+    t.b0 = t.s0 = bt * T;
     t.valid = min(T, p.nb - t.b0);
     t.k0 = lo[l];
     t.k = span;
   }
   t.n = (t.valid + 15) & ~15;
   return t;
+}
+
+// Sums of v over the lanes up to this one.
+__device__ __forceinline__ int warp_scan(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
 }
 
 // The ring position of a role: stage s, and the parity of its current pass.
@@ -414,27 +429,40 @@ __device__ __forceinline__ bool role_all(bool ok) {
 //
 // In tensor memory a thread holds one lane, and lanes are consecutive elements of an output row: stored
 // as they come, a warp writes 64 bytes of a row at a time (bf16), which took 12,000 cycles for 192
-// columns, more than a tile's products.  So a chunk of columns goes through shared memory, where 16
-// threads pick up the 256 bytes of a row (VEC bytes each, or less where the rows are not aligned).
-// Two buffers: one barrier per chunk.
+// columns, more than a tile's products.  So a chunk of columns goes through shared memory, as
+// rows of the output (two buffers, one barrier per chunk), and from there
+//   bf16   read from tensor memory in the matrix-fragment shape (16x256b), packed in pairs and stored
+//          transposed by stmatrix, 4 stores per 32 columns in place of 32; a whole chunk leaves by TMA
+//          (two boxes of 64 elements x 32 rows, 128-byte swizzle), a chunk that the group's rows end
+//          in, and rows not aligned to 16 bytes, by plain stores;
+//   fp32   one store per element and plain stores.
 // ---------------------------------------------------------------------------
 constexpr int kOutBytes = 8 * 1024;  // one buffer: 128 lanes x 32 columns of bf16 or 16 of fp32
 
-// Up to ROWS rows of ROW bytes in the buffer, the first `bytes` of each, to global rows `stride` bytes
-// apart: all reads before the writes.
-template <typename V, int ROW, int ROWS>
+// Byte `at` of row r of a buffer.  bf16: two halves of 32 rows x 128 bytes, 16-byte pieces swizzled by the
+// row.  fp32: 16 rows x 512 bytes.
+template <bool F32>
+__device__ __forceinline__ int out_place(int r, int at) {
+  if constexpr (F32) return r * 512 + at;
+  return (at >> 7) * 4096 + r * 128 + ((((at >> 4) & 7) ^ (r & 7)) << 4) + (at & 15);
+}
+
+// The buffer's first `rows` rows, the first `bytes` of each, to global rows `stride` bytes apart: all
+// reads before the writes.
+template <typename V, bool F32>
 __device__ __forceinline__ void store_rows(const uint8_t* buf, uint8_t* out, int64_t stride, int rows, int bytes,
                                            int tid) {
-  constexpr int kPerRow = ROW / sizeof(V);
+  constexpr int kPerRow = (F32 ? 512 : 256) / sizeof(V), kRows = F32 ? 16 : 32;
   if constexpr (kPerRow <= 128) {
-    constexpr int kStep = 128 / kPerRow, kTimes = ROWS / kStep, kBatch = kTimes < 8 ? kTimes : 8;
+    constexpr int kStep = 128 / kPerRow, kTimes = kRows / kStep, kBatch = kTimes < 8 ? kTimes : 8;
     const int at = tid % kPerRow * static_cast<int>(sizeof(V)), r0 = tid / kPerRow;
     if (at >= bytes) return;
 #pragma unroll 1
     for (int i0 = 0; i0 < kTimes; i0 += kBatch) {
       V v[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) v[i] = *reinterpret_cast<const V*>(buf + (r0 + (i0 + i) * kStep) * ROW + at);
+      for (int i = 0; i < kBatch; ++i)
+        v[i] = *reinterpret_cast<const V*>(buf + out_place<F32>(r0 + (i0 + i) * kStep, at));
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int r = r0 + (i0 + i) * kStep;
@@ -444,36 +472,56 @@ __device__ __forceinline__ void store_rows(const uint8_t* buf, uint8_t* out, int
   }
 }
 
-template <int ROW, int ROWS>
+template <bool F32>
 __device__ __forceinline__ void store_rows(int vec, const uint8_t* buf, uint8_t* out, int64_t stride, int rows,
                                            int bytes, int tid) {
-  if (vec == 16) store_rows<uint4, ROW, ROWS>(buf, out, stride, rows, bytes, tid);
-  else if (vec == 8) store_rows<uint2, ROW, ROWS>(buf, out, stride, rows, bytes, tid);
-  else if (vec == 4) store_rows<uint32_t, ROW, ROWS>(buf, out, stride, rows, bytes, tid);
-  else store_rows<uint16_t, ROW, ROWS>(buf, out, stride, rows, bytes, tid);  // (bf16 only)
+  if (vec == 16) store_rows<uint4, F32>(buf, out, stride, rows, bytes, tid);
+  else if (vec == 8) store_rows<uint2, F32>(buf, out, stride, rows, bytes, tid);
+  else if (vec == 4) store_rows<uint32_t, F32>(buf, out, stride, rows, bytes, tid);
+  else if constexpr (!F32) store_rows<uint16_t, F32>(buf, out, stride, rows, bytes, tid);
 }
 
-// A chunk of the accumulator's columns of this thread's lane, times a, into a buffer.
-template <typename O, int N>
-__device__ __forceinline__ void fetch_chunk(uint32_t from, float a, bool none, uint8_t* buf, int tid) {
-  uint32_t v[N];
+// A chunk of the accumulator's columns (32 of bf16, 16 of fp32), times a, into a buffer.  `from`: the
+// address of the warp's 32 lanes and the first column.
+__device__ __forceinline__ void fetch_chunk_f32(uint32_t from, float a, bool none, uint8_t* buf, int tid) {
+  uint32_t v[16];
   tmem_load(from, v);
+  float* o = reinterpret_cast<float*>(buf) + tid;
+#pragma unroll
+  for (int c = 0; c < 16; ++c) o[c * 128] = none ? 0.0f : __fmul_rn(__uint_as_float(v[c]), a);
+}
+
+__device__ __forceinline__ void fetch_chunk_bf16(uint32_t from, float a, bool none, uint8_t* buf, int quarter, int lane) {
+  // v[h][4 i + 0..3]: lanes 16 h + lane / 4 and + 8, columns 8 i + 2 (lane % 4) and + 1
+  uint32_t v[2][16];
+  tmem_load_fragments(from, v[0]);
+  tmem_load_fragments(from + (16u << 16), v[1]);
   if (none)
 #pragma unroll
-    for (int c = 0; c < N; ++c) v[c] = 0;
-  O* o = reinterpret_cast<O*>(buf) + tid;
+    for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0;
+  // matrix m = lane / 8 of a store is lanes 8 m .. 8 m + 7 of the warp; its row lane % 8 a column
+  const int place = quarter * 64 + (lane >> 3) * 16, r = lane & 7;
 #pragma unroll
-  for (int c = 0; c < N; c += 2) {
-    const float x = __fmul_rn(__uint_as_float(v[c]), a), y = __fmul_rn(__uint_as_float(v[c + 1]), a);
-    if constexpr (sizeof(O) == 4) {
-      o[c * 128] = x;
-      o[(c + 1) * 128] = y;
-    } else {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
-      o[c * 128] = b.x;
-      o[(c + 1) * 128] = b.y;
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const uint32_t* f = &v[m >> 1][4 * i + 2 * (m & 1)];
+      const __nv_bfloat162 b = __floats2bfloat162_rn(__fmul_rn(__uint_as_float(f[0]), a), __fmul_rn(__uint_as_float(f[1]), a));
+      w[m] = *reinterpret_cast<const uint32_t*>(&b);
     }
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                     smem_addr(buf + out_place<false>(8 * i + r, place))),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
   }
+}
+
+__device__ __forceinline__ void tma_store3(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -487,7 +535,7 @@ constexpr int kLoraThreads = 128;
 template <int KIND, bool MX, int T, bool LORA>
 __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
     k_fp4_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-               const __grid_constant__ GemmParams p) {
+               const __grid_constant__ CUtensorMap map_out, const __grid_constant__ GemmParams p) {
   using S = GemmShape<KIND, MX, T, LORA>;
   constexpr int kTpb = S::kTilesPerBlock;
   constexpr int kScaleK = MX ? 128 : 64;  // summed elements of one scale tile
@@ -500,6 +548,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
   int* start = reinterpret_cast<int*>(smem + S::kSmemBytes);
   int* lo = start + p.groups + 1;
   int* hi = lo + p.groups + 1;
+  int* units = hi + p.groups + 1;  // (tiled scales of ragged rows) 64-row units of scales before a group's
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (warp == 2) {
@@ -510,7 +559,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
   }
   if (warp == 1 && lane == 0) {
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(smem_addr(&bars.full[i]), KIND == kGemmRows ? 1 + kScaleThreads / 32 : 1);
+      mbar_init(smem_addr(&bars.full[i]), S::kTiledB ? 1 : 1 + kScaleThreads / 32);
       mbar_init(smem_addr(&bars.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -526,7 +575,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
   // The kernel before this one on the stream wrote the operands.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 0) {  // where each group's tiles begin
-    int base = 0;
+    int base = 0, unit_base = 0;
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
       const int g = g0 + lane;
       int a = 0, b = 0, n = 0;
@@ -543,18 +592,18 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
           n = p.tiles_a * ((b - a + T - 1) / T);
         }
       }
-      int incl = n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-        if (lane >= d) incl += o;
-      }
+      const int incl = warp_scan(n, lane);
       if (g < p.groups) {
         start[g] = base + incl - n;
         lo[g] = a;
         hi[g] = b;
       }
       base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+      if constexpr (KIND == kGemmRows && S::kTiledB) {
+        const int u = (b - a + 63) / 64, sum = warp_scan(u, lane);
+        if (g < p.groups) units[g] = unit_base + sum - u;
+        unit_base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+      }
     }
     if (lane == 0) bars.tiles = base;
   }
@@ -569,7 +618,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
     GemmRing ring;
     long long fills = 0;
     for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, tile);
+      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, units, tile);
       const int blocks = (t.k + kGemmKBlock - 1) / kGemmKBlock;
       const int boxes = (t.n + S::kBox - 1) / S::kBox;
       const int kt0 = t.k0 / kScaleK;
@@ -577,9 +626,9 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
                            (static_cast<int64_t>(t.a0 / 128) * p.k_tiles + kt0) * 512;
       int row_tiles = 0;
       const uint8_t* sfb = nullptr;
-      if constexpr (KIND == kGemmContr) {
-        const int first = t.b0 / 128;
-        row_tiles = min((t.b0 + t.valid + 127) / 128 - first, S::kRowTilesB);
+      if constexpr (S::kTiledB) {
+        const int first = t.s0 / 128;
+        row_tiles = (t.s0 + t.valid + 127) / 128 - first;  // (at most kRowTilesB: s0 is a multiple of 64)
         sfb = p.sfb + (static_cast<int64_t>(first) * p.k_tiles + kt0) * 512;
       }
       for (int kb = 0; kb < blocks; ++kb) {
@@ -618,13 +667,13 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
     const uint64_t codes0 = desc_codes(smem_addr(smem)), scales0 = desc_scales(smem_addr(smem));
     const uint64_t chunk0 = desc_codes(smem_addr(chunks));
     for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, tile);
+      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, units, tile);
       const int blocks = (t.k + kGemmKBlock - 1) / kGemmKBlock;
       ok = warp_wait(smem_addr(&bars.acc_empty[acc]), acc_phase ^ 1);
       if (!ok) break;
       umma_fence_after();
       const uint32_t d = tmem + acc * T;
-      const uint32_t shift = KIND == kGemmContr ? (t.b0 % 128) / 32 : 0;
+      const uint32_t shift = S::kTiledB ? (t.s0 % 128) / 32 : 0;
       const int row_tiles = (shift * 32 + t.n + 127) / 128;
       const uint32_t idesc0 = umma_idesc<MX>(t.n, 0), idesc1 = umma_idesc<MX>(t.n, MX ? 2 : 0);
       bool chunks_left = LORA;
@@ -699,7 +748,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
     const int es = p.out_f32 ? 4 : 2, step = p.out_f32 ? 16 : 32;
     uint8_t* const my_outs = outs + half * 2 * kOutBytes;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, tile);
+      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, units, tile);
       float a = 1.0f;
       if (!MX) a = __fmul_rn(__ldg(p.sg_a + (KIND == kGemmRows ? t.g : 0)), __ldg(p.sg_b));
       const bool full = mbar_wait(smem_addr(&bars.acc_full[acc]), acc_phase);
@@ -715,20 +764,33 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
       bool held = true;
       for (int c0 = half * step; c0 < t.valid; c0 += kEpilogues * step) {
         uint8_t* const o = my_outs + buf * kOutBytes;
-        if (p.out_f32) fetch_chunk<float, 16>(from + c0, a, none, o, tid);
-        else fetch_chunk<__nv_bfloat16, 32>(from + c0, a, none, o, tid);
+        const int rows = min(step, t.valid - c0);
+        if (p.out_f32) fetch_chunk_f32(from + c0, a, none, o, tid);
+        else fetch_chunk_bf16(from + c0, a, none, o, quarter, lane);
         if (c0 + kEpilogues * step >= t.valid) {  // the group's last chunk: its part has been read
           umma_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_addr(&bars.acc_empty[acc]));
           held = false;
         }
+        // (CONTR: rows past nb are past the tensor map's end and not written)
+        const bool by_tma = p.out_tma && (KIND == kGemmContr || rows == 32);
+        fence_proxy_async_smem();
+        if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the other buffer is free
         if (half == 0) role_sync<2>();
         else role_sync<3>();
-        if (p.out_f32)
-          store_rows<512, 16>(p.out_vec, o, out + c0 * stride, stride, min(16, t.valid - c0), bytes, tid);
-        else
-          store_rows<256, 32>(p.out_vec, o, out + c0 * stride, stride, min(32, t.valid - c0), bytes, tid);
+        if (by_tma) {
+          if (tid == 0) {
+            const int y = t.b0 + c0, z = KIND == kGemmRows ? 0 : t.g;
+            tma_store3(&map_out, smem_addr(o), t.a0, y, z);
+            if (t.a0 + 64 < p.na) tma_store3(&map_out, smem_addr(o) + 4096, t.a0 + 64, y, z);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else if (p.out_f32) {
+          store_rows<true>(p.out_vec, o, out + c0 * stride, stride, rows, bytes, tid);
+        } else {
+          store_rows<false>(p.out_vec, o, out + c0 * stride, stride, rows, bytes, tid);
+        }
         buf ^= 1;
       }
       if (held) {  // no chunk for this group
@@ -738,7 +800,8 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
-  } else if (KIND == kGemmRows && warp >= 8 && warp < 12) {
+    if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  } else if (!S::kTiledB && warp >= 8 && warp < 12) {
     constexpr int kRowsPerThread = (T + kScaleThreads - 1) / kScaleThreads;
     constexpr int kAhead = 4;  // stages whose scales are loaded together: a batch
     constexpr int kBlockBytes = MX ? 8 : 16;
@@ -750,7 +813,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
     };
     auto enter = [&](Batch& b) {  // a tile's first batch
       if (b.tile >= tiles) return;
-      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, b.tile);
+      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, units, b.tile);
       b.kb = 0, b.b0 = t.b0, b.valid = t.valid, b.n = t.n;
     };
     auto after = [&](const Batch& b) {
@@ -821,7 +884,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
       GemmRing chunk;
       int turn = 0;
       for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, tile);
+        const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, units, tile);
         role_sync<1>();  // the last tile's ids have been read
         for (int r = tid; r < t.n; r += kLoraThreads) {
           const int id = r < t.valid ? __ldg(p.lora_ids + t.b0 + r) : -1;
