@@ -256,14 +256,17 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&v)[16]) {
       : "r"(taddr)
       : "memory");
 }
-// 16 lanes x 32 columns in the shape of matrix fragments.
-__device__ __forceinline__ void tmem_load_fragments(uint32_t taddr, uint32_t (&v)[16]) {
+// A warp's 32 lanes x 32 columns in the shape of matrix fragments: v[h] is lanes 16 h .. 16 h + 15.
+__device__ __forceinline__ void tmem_load_fragments(uint32_t taddr, uint32_t (&v)[2][16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr)
+      : "=r"(v[0][0]), "=r"(v[0][1]), "=r"(v[0][2]), "=r"(v[0][3]), "=r"(v[0][4]), "=r"(v[0][5]), "=r"(v[0][6]), "=r"(v[0][7]),
+        "=r"(v[0][8]), "=r"(v[0][9]), "=r"(v[0][10]), "=r"(v[0][11]), "=r"(v[0][12]), "=r"(v[0][13]), "=r"(v[0][14]), "=r"(v[0][15]),
+        "=r"(v[1][0]), "=r"(v[1][1]), "=r"(v[1][2]), "=r"(v[1][3]), "=r"(v[1][4]), "=r"(v[1][5]), "=r"(v[1][6]), "=r"(v[1][7]),
+        "=r"(v[1][8]), "=r"(v[1][9]), "=r"(v[1][10]), "=r"(v[1][11]), "=r"(v[1][12]), "=r"(v[1][13]), "=r"(v[1][14]), "=r"(v[1][15])
+      : "r"(taddr), "r"(taddr + (16u << 16))
       : "memory");
 }
 
@@ -494,8 +497,7 @@ __device__ __forceinline__ void fetch_chunk_f32(uint32_t from, float a, bool non
 __device__ __forceinline__ void fetch_chunk_bf16(uint32_t from, float a, bool none, uint8_t* buf, int quarter, int lane) {
   // v[h][4 i + 0..3]: lanes 16 h + lane / 4 and + 8, columns 8 i + 2 (lane % 4) and + 1
   uint32_t v[2][16];
-  tmem_load_fragments(from, v[0]);
-  tmem_load_fragments(from + (16u << 16), v[1]);
+  tmem_load_fragments(from, v);
   if (none)
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0;
@@ -776,11 +778,13 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
         // (CONTR: rows past nb are past the tensor map's end and not written)
         const bool by_tma = p.out_tma && (KIND == kGemmContr || rows == 32);
         fence_proxy_async_smem();
-        if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the other buffer is free
+        // (the group's first warp issues the copies, by the same elected lane each time)
+        if (quarter == 0 && elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the other buffer is free
+        __syncwarp();
         if (half == 0) role_sync<2>();
         else role_sync<3>();
         if (by_tma) {
-          if (tid == 0) {
+          if (quarter == 0 && elect_one()) {
             const int y = t.b0 + c0, z = KIND == kGemmRows ? 0 : t.g;
             tma_store3(&map_out, smem_addr(o), t.a0, y, z);
             if (t.a0 + 64 < p.na) tma_store3(&map_out, smem_addr(o) + 4096, t.a0 + 64, y, z);
@@ -800,7 +804,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
-    if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (quarter == 0 && elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else if (!S::kTiledB && warp >= 8 && warp < 12) {
     constexpr int kRowsPerThread = (T + kScaleThreads - 1) / kScaleThreads;
     constexpr int kAhead = 4;  // stages whose scales are loaded together: a batch
