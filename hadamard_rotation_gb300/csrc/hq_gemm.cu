@@ -75,6 +75,18 @@ cudaError_t sm_count(int* sms) {
   return e;
 }
 
+// Scale tiles [row_tiles][k_tiles] of 512 bytes, as words: boxes of `box` tiles along k.
+bool encode_scales(CUtensorMap* map, const uint8_t* s, int64_t k_tiles, int64_t row_tiles, int box) {
+  const EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t size[3] = {128, static_cast<cuuint64_t>(k_tiles), static_cast<cuuint64_t>(row_tiles)};
+  const cuuint64_t stride[2] = {512, static_cast<cuuint64_t>(k_tiles * 512)};
+  const cuuint32_t dim[3] = {128, static_cast<cuuint32_t>(box), 1}, step[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(s), size, stride, dim, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // bf16 output [groups, rows, n], rows contiguous, in boxes of 32 rows x 64 elements, 128-byte swizzle.
 bool encode_out(CUtensorMap* map, void* out, int64_t n, int64_t rows, int64_t groups) {
   const EncodeTiledFn fn = encode_tiled();
@@ -95,12 +107,15 @@ struct Codes {
 };
 
 template <int KIND, bool MX, int T, bool LORA = false>
-hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t most_tiles, hq_stream stream) {
+hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t b_scale_row_tiles, int64_t most_tiles,
+                 hq_stream stream) {
   using S = hq::GemmShape<KIND, MX, T, LORA>;
   auto kernel = hq::k_fp4_gemm<KIND, MX, T, LORA>;
-  CUtensorMap ma, mb, mo = {};
+  CUtensorMap ma, mb, msa, msb = {}, mo = {};
   if (!encode_codes(&ma, a.q, a.row_bytes, a.rows, a.groups, hq::kGemmLanes, 3) ||
-      !encode_codes(&mb, b.q, b.row_bytes, b.rows, 1, S::kBox, 2))
+      !encode_codes(&mb, b.q, b.row_bytes, b.rows, 1, S::kBox, 2) ||
+      !encode_scales(&msa, p.sfa, p.k_tiles, a.groups * p.a_row_tiles, S::kTilesPerBlock) ||
+      (S::kWide && !encode_scales(&msb, p.sfb, p.k_tiles, b_scale_row_tiles, S::kTilesPerBlock)))
     return cuda_fail(cudaErrorInvalidValue);
   p.out_tma = !p.out_f32 && p.out_vec == 16 &&
               encode_out(&mo, p.out, p.na, KIND == hq::kGemmRows ? p.extent : p.nb, KIND == hq::kGemmRows ? 1 : p.groups);
@@ -112,16 +127,20 @@ hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t most_tile
       cudaSuccess)
     return cuda_fail(e);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(most_tiles < sms ? most_tiles : sms));
-  cfg.blockDim = dim3(hq::kGemmThreads + (LORA ? hq::kLoraThreads : 0));
+  const int64_t most = sms / S::kCtas;
+  cfg.gridDim = dim3(static_cast<unsigned>((most_tiles < most ? most_tiles : most) * S::kCtas));
+  cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, mo, p);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = S::kCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = S::kWide ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, msa, msb, mo, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? HQ_OK : cuda_fail(e);
 }
@@ -227,9 +246,9 @@ GemmParams rows_params(const uint8_t* xs, const float* x_sg, const uint8_t* ws, 
                        int64_t K, int64_t groups, void* out, hq_dtype dt) {
   GemmParams p = {};
   p.k_tiles = static_cast<int>((K + (MX ? 127 : 63)) / (MX ? 128 : 64));
-  p.tiles_a = static_cast<int>((N + 127) / 128);
+  p.a_row_tiles = static_cast<int>((N + 127) / 128);
+  p.tiles_a = static_cast<int>(narrow_rows(M, groups) ? (N + 127) / 128 : (N + 255) / 256);
   p.sfa = ws;
-  p.sfa_group_bytes = static_cast<int64_t>(p.tiles_a) * p.k_tiles * 512;
   p.sfb = xs;
   p.sfb_row_bytes = static_cast<int>(K / (MX ? 32 : 16));
   p.sfb_mode = p.sfb_row_bytes % 16 == 0 && aligned(xs, 16) ? 16
@@ -258,8 +277,8 @@ hq_status grouped_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, 
   if (M == 0 || N == 0 || E == 0) return HQ_OK;
   if (!out || !offsets) return HQ_ERR_NULL;
   if (!aligned(out, dt == HQ_F32 ? 4 : 2) || !aligned(offsets, 4)) return HQ_ERR_ALIGN;
-  const int64_t tiles_a = (N + 127) / 128;
   const bool narrow = narrow_rows(M, E);
+  const int64_t tiles_a = narrow ? (N + 127) / 128 : (N + 255) / 256;
   const int64_t tiles = ((M + (narrow ? 63 : 191)) / (narrow ? 64 : 192) + (E < M ? E : M)) * tiles_a;
   if (tiles > kMaxExtent) return HQ_ERR_SHAPE;
   if (K == 0) return out_zero(out, M * N, dt, stream);
@@ -275,8 +294,8 @@ hq_status grouped_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, 
     const hq_status st = tile_scales(p, static_cast<uint8_t*>(workspace), stream);
     if (st != HQ_OK) return st;
   }
-  return narrow ? launch<hq::kGemmRows, MX, 64>(p, a, b, tiles, stream)
-                : launch<hq::kGemmRows, MX, 192>(p, a, b, tiles, stream);
+  return narrow ? launch<hq::kGemmRows, MX, 64>(p, a, b, 0, tiles, stream)
+                : launch<hq::kGemmRows, MX, 192>(p, a, b, group_scale_tiles(M, E), tiles, stream);
 }
 
 template <bool MX>
@@ -289,7 +308,7 @@ hq_status grouped_wgrad(const uint8_t* gq, const uint8_t* gs, const float* g_sg,
   if (N == 0 || K == 0 || E == 0) return HQ_OK;
   if (!out || !offsets) return HQ_ERR_NULL;
   if (!aligned(out, dt == HQ_F32 ? 4 : 2) || !aligned(offsets, 4)) return HQ_ERR_ALIGN;
-  const int64_t tiles_a = (K + 127) / 128, tiles_b = (N + 191) / 192;
+  const int64_t tiles_a = (K + 255) / 256, tiles_b = (N + 191) / 192;
   if (tiles_a * tiles_b > kMaxExtent / E) return HQ_ERR_SHAPE;
   if (T == 0) return out_zero(out, E * N * K, dt, stream);
   if (!gq || !gs || !xq || !xs || (!MX && (!g_sg || !x_sg))) return HQ_ERR_NULL;
@@ -307,13 +326,14 @@ hq_status grouped_wgrad(const uint8_t* gq, const uint8_t* gs, const float* g_sg,
   p.extent = static_cast<int>(T);
   p.na = static_cast<int>(K);
   p.nb = static_cast<int>(N);
+  p.a_row_tiles = static_cast<int>((K + 127) / 128);
   p.tiles_a = static_cast<int>(tiles_a);
   p.tiles_b = static_cast<int>(tiles_b);
   p.out = out;
   p.out_f32 = dt == HQ_F32;
   p.out_vec = store_bytes(out, K, dt);
   const Codes a = {xq, T / 2, K, 1}, b = {gq, T / 2, N, 1};
-  return launch<hq::kGemmContr, MX, 192>(p, a, b, E * tiles_a * tiles_b, stream);
+  return launch<hq::kGemmContr, MX, 192>(p, a, b, (N + 127) / 128, E * tiles_a * tiles_b, stream);
 }
 
 template <int NB, int TG>
@@ -374,7 +394,7 @@ hq_status lora_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, con
       !aligned(ids, 4) || !aligned(workspace, 32) || !aligned(x_sg, 4) || !aligned(w_sg, 4))
     return HQ_ERR_ALIGN;
   const bool narrow = narrow_rows(M, 1);
-  const int64_t tiles = (M + (narrow ? 63 : 191)) / (narrow ? 64 : 192) * ((N + 127) / 128);
+  const int64_t tiles = narrow ? (M + 63) / 64 * ((N + 127) / 128) : (M + 191) / 192 * ((N + 255) / 256);
   if (tiles > kMaxExtent) return HQ_ERR_SHAPE;
   int sms = 0;
   cudaError_t e = sm_count(&sms);
@@ -408,8 +428,8 @@ hq_status lora_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, con
     if (st != HQ_OK) return st;
   }
   const Codes ca = {wq, K / 2, N, 1}, cb = {xq, K / 2, M, 1};
-  return narrow ? launch<hq::kGemmRows, MX, 64, true>(p, ca, cb, tiles, stream)
-                : launch<hq::kGemmRows, MX, 192, true>(p, ca, cb, tiles, stream);
+  return narrow ? launch<hq::kGemmRows, MX, 64, true>(p, ca, cb, 0, tiles, stream)
+                : launch<hq::kGemmRows, MX, 192, true>(p, ca, cb, group_scale_tiles(M, 1), tiles, stream);
 }
 
 // Row-major scale bytes [groups, rows, cols] -> the tile layout, a 16-byte row of a tile per thread.

@@ -17,7 +17,13 @@
 // whose width is chosen per tile in steps of 16 columns: an expert with 5 rows costs one
 // 16-column instruction per step, not a 128-row tile.
 //
-// One CTA per SM takes tiles (128 lanes x up to T columns) from a static cyclic order; the
+// Small groups are taken by single CTAs in tiles of 128 lanes x up to 64 columns.  Large ones, and the
+// CONTR form, by pairs of CTAs (cta_group::2) in tiles of 256 lanes x up to 192 columns: each CTA keeps its
+// 128 lanes of A and half of B's rows, so a stage brings 34 KB into a CTA for what 46 KB would be
+// needed alone.  An SM's shared memory moves 128 bytes a cycle; the FP4 products of 128 x 192 alone read
+// 107 and their loads write 120.
+//
+// One CTA per SM takes tiles from a static cyclic order; the
 // group sizes are read on the device, so the call does not wait for the host to know them.
 // Roles of a CTA:
 //   warp 0        TMA: codes of both operands (128-byte swizzled boxes of 256 codes per row) and
@@ -25,11 +31,11 @@
 //                 already the order that tensor memory wants)
 //   warp 1        copies the scales to tensor memory (tcgen05.cp) and issues the products
 //   warp 2        allocates tensor memory
-//   warps 4..7    epilogue: tensor memory -> registers -> * a -> shared memory -> global (4..11 where
-//                 the next does not apply)
+//   warps 4..7    epilogue: tensor memory -> registers -> * a -> shared memory -> global (wide: 4..15,
+//                 with adapters 4..11)
 //   warps 8..11   (ROWS, narrow tiles) the tokens' scales: row-major in global memory, since a group
 //                 starts at any row; moved through registers into the tile layout
-//   warps 12..15  (adapters) the operands of the adapters' second product, below
+//   then 4 warps  (adapters) the operands of the adapters' second product, below
 // Shared memory holds a ring of kStages stages (256 steps of the summed axis each); tensor
 // memory holds two accumulators, so the epilogue of a tile runs under the products of the next.
 //
@@ -59,7 +65,7 @@ enum GemmKind { kGemmRows = 0, kGemmContr = 1 };
 
 struct GemmParams {
   const uint8_t* sfa;       // scales of A in the tile layout
-  int64_t sfa_group_bytes;  // bytes of one group's scales of A (ROWS)
+  int a_row_tiles;          // its 128-row tiles per group (ROWS)
   const uint8_t* sfb;       // scales of B: row-major (narrow ROWS), or in the tile layout
   const float* sg_a;        // per-tensor scales (ROWS: one per group; CONTR: one); NULL: 1
   const float* sg_b;
@@ -69,7 +75,7 @@ struct GemmParams {
   int na;                   // rows of A (per group for ROWS)
   int nb;                   // CONTR: rows of B
   int k;                    // ROWS: summed elements
-  int tiles_a;              // ceil(na / 128)
+  int tiles_a;              // tiles over na: of 128 lanes, or 256 (pairs)
   int tiles_b;              // CONTR: ceil(nb / T)
   int k_tiles;              // 512-byte scale tiles per 128 rows
   int sfb_row_bytes;        // bytes of one row of row-major scales
@@ -90,23 +96,29 @@ struct GemmParams {
 // ---------------------------------------------------------------------------
 template <int KIND, bool MX, int T, bool LORA>
 struct GemmShape {
+  static constexpr bool kWide = KIND == kGemmContr || T >= 128;  // pairs of CTAs; B's scales in the tile layout
+  static constexpr int kCtas = kWide ? 2 : 1;
+  static constexpr int kTileLanes = kCtas * kGemmLanes;
+  static constexpr int kRowsB = T / kCtas;           // rows of B in a CTA's shared memory
   static constexpr int kTilesPerBlock = MX ? 2 : 4;  // scale tiles along K per stage
   static constexpr int kRowTilesB = (T + 127) / 128;
-  static constexpr int kBox = T >= 128 ? 64 : 16;    // rows of B per TMA box
+  static constexpr int kBox = kWide ? 32 : 16;       // rows of B per TMA box
+  static constexpr int kStepN = 16 * kCtas;          // columns of an instruction come in steps of this
   static constexpr int kBytesA = kGemmLanes * 128;
-  static constexpr int kBytesB = T * 128;
+  static constexpr int kBytesB = kRowsB * 128;
   static constexpr int kBytesSfa = kTilesPerBlock * 512;
   static constexpr int kBytesSfb = kRowTilesB * kTilesPerBlock * 512;
   static constexpr int kStageBytes = kBytesA + kBytesB + kBytesSfa + kBytesSfb;
   static_assert(kStageBytes % 1024 == 0, "stages stay aligned to the swizzle atom");
-  // adapters: chunks of 64 bf16 columns: B_a of 128 lanes, then t's hi and lo of T rows
-  static constexpr int kChunkBytes = LORA ? kGemmLanes * 128 + 2 * T * 128 : 0;
-  static constexpr int kChunks = T >= 128 ? 1 : 2;
-  static constexpr int kChunkGap = T >= 128 ? 5 : 2;  // stages between two chunks of a tile
-  static constexpr bool kTiledB = KIND == kGemmContr || T >= 128;  // B's scales come in the tile layout
-  static constexpr int kEpilogues = kTiledB && !LORA ? 2 : 1;      // groups of 128 threads
-  static constexpr int kOuts = kEpilogues * 2 * 8 * 1024;          // their output buffers
-  static constexpr int kRingBytes = 218 * 1024 - kChunks * kChunkBytes - kOuts;
+  // adapters: chunks of 64 bf16 columns: B_a of 128 lanes, then t's hi and lo of kRowsB rows
+  static constexpr int kChunkBytes = LORA ? kGemmLanes * 128 + 2 * kRowsB * 128 : 0;
+  static constexpr int kChunks = kWide ? 1 : 2;
+  static constexpr int kChunkGap = kWide ? 5 : 2;         // stages between two chunks of a tile
+  static constexpr int kEpilogues = !kWide ? 1 : LORA ? 2 : 3;  // groups of 128 threads
+  static constexpr int kOuts = kEpilogues * 8 * 1024;           // their output buffers
+  static constexpr int kLoraWarp = 4 + 4 * (kWide ? kEpilogues : 2);  // the adapters' first warp
+  static constexpr int kThreads = 32 * (kLoraWarp + (LORA ? 4 : 0));
+  static constexpr int kRingBytes = 216 * 1024 - kChunks * kChunkBytes - kOuts;
   static constexpr int kStages = kRingBytes / kStageBytes < 7 ? kRingBytes / kStageBytes : 7;
   static constexpr int kSmemBytes = kStages * kStageBytes + kChunks * kChunkBytes + kOuts;
   static_assert(kSmemBytes + 1024 + 16 * (LORA ? 2 : kGemmMaxGroups + 1) + 1280 <= 227 * 1024, "a CTA has 227 KB");
@@ -136,29 +148,52 @@ inline size_t gemm_smem_bytes(int bytes, int groups) { return 1024 + static_cast
 // ---------------------------------------------------------------------------
 // PTX.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void tma_tile3(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
+// Tensor copies into this CTA's shared memory.  PAIR: `bar` is a cluster address, of either CTA of the pair.
+template <bool PAIR>
+__device__ __forceinline__ void tma_tile3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void tma_tile2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
 
-// A bulk copy whose bytes have been announced on `bar` already.
-__device__ __forceinline__ void tma_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
+// The cluster address of a shared variable of CTA `rank`, and an arrival there.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same without waiting for this thread's stores (2000 cycles with output rows in flight): for an
+// arrival that hands over tensor memory, which the tcgen05 fence orders.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
@@ -180,41 +215,73 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
 }
 
-// Arrive on `bar` once every tensor-core operation this thread has issued is complete.
+// Tensor-core operations, of this CTA or (PAIR) of the pair, issued by its first CTA: operands and
+// scales lie at the same addresses of both CTAs' shared and tensor memory.
+
+// Arrive on `bar` (PAIR: of both CTAs) once every operation this thread has issued is complete.
+template <bool PAIR>
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // One 512-byte scale tile -> 4 columns of tensor memory, repeated for the 4 groups of 32 lanes.
+template <bool PAIR>
 __device__ __forceinline__ void umma_copy_scales(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+  if constexpr (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
-template <bool MX>
+template <bool PAIR, bool MX>
 __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                          uint32_t sfb, uint32_t accumulate) {
-  if constexpr (MX) {
+  if constexpr (PAIR && MX)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else if constexpr (MX)
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
-  } else {
+  else
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
-  }
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void umma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc)
+        : "memory");
 }
 
 // Shared-memory matrix descriptors.  Codes: rows of 128 bytes, 128-byte swizzle, 8-row groups
@@ -228,17 +295,18 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
          (uint64_t{1} << 46);
 }
 
-// Instruction descriptor: E2M1 x E2M1, both operands along K, M = 128, N columns; which pair of
+// Instruction descriptor: E2M1 x E2M1, both operands along K, M lanes, N columns; which pair of
 // a 4-byte scale word MXFP4 takes (0 or 2; NVFP4 takes all four).
 template <bool MX>
-__device__ __forceinline__ uint32_t umma_idesc(int n, int pair) {
+__device__ __forceinline__ uint32_t umma_idesc(int m, int n, int pair) {
   return (static_cast<uint32_t>(pair) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
-         ((MX ? 1u : 0u) << 23) | (1u << 27) | (static_cast<uint32_t>(pair) << 29);
+         ((MX ? 1u : 0u) << 23) | (static_cast<uint32_t>(m >> 4) << 24) | (static_cast<uint32_t>(pair) << 29);
 }
 
 // The same for bf16 x bf16 into fp32.
-__device__ __forceinline__ uint32_t umma_idesc_bf16(int n) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+__device__ __forceinline__ uint32_t umma_idesc_bf16(int m, int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
 }
 
 // Order tensor-memory operations across a barrier between threads.
@@ -275,10 +343,10 @@ __device__ __forceinline__ void tmem_load_fragments(uint32_t taddr, uint32_t (&v
 // ---------------------------------------------------------------------------
 struct GemmTile {
   int g;       // group
-  int a0;      // first row of A
+  int a0;      // first row of A (of the pair)
   int b0;      // first row of B (ROWS: a row of X)
   int valid;   // columns that exist
-  int n;       // columns of the instruction (valid rounded up to 16)
+  int n;       // columns of the instruction (valid rounded up to 16, pairs: 32)
   int k0, k;   // summed range
   int s0;      // first row of B's scales in the tile layout, a multiple of 64
 };
@@ -302,7 +370,7 @@ __device__ __forceinline__ GemmTile gemm_tile(const GemmParams& p, const int* st
     constexpr int kStep = T >= 128 ? 64 : 16;
     const int width = ((span + parts - 1) / parts + kStep - 1) & ~(kStep - 1);
     const int at = local / parts, bt = local - at * parts;
-    t.a0 = at * kGemmLanes;
+    t.a0 = at * (T >= 128 ? 2 * kGemmLanes : kGemmLanes);
     t.b0 = lo[l] + bt * width;
     t.valid = min(width, hi[l] - t.b0);
     t.s0 = T >= 128 ? units[l] * 64 + bt * width : 0;
@@ -310,13 +378,13 @@ __device__ __forceinline__ GemmTile gemm_tile(const GemmParams& p, const int* st
     t.k = p.k;
   } else {
     const int at = local / p.tiles_b, bt = local - at * p.tiles_b;
-    t.a0 = at * kGemmLanes;
+    t.a0 = at * 2 * kGemmLanes;
     t.b0 = t.s0 = bt * T;
     t.valid = min(T, p.nb - t.b0);
     t.k0 = lo[l];
     t.k = span;
   }
-  t.n = (t.valid + 15) & ~15;
+  t.n = T >= 128 ? (t.valid + 31) & ~31 : (t.valid + 15) & ~15;
   return t;
 }
 
@@ -409,7 +477,7 @@ __device__ __forceinline__ uint32_t scale_word(const uint32_t (&w)[W + 1], const
   return left >= 4 ? v : left <= 0 ? 0u : v & ((1u << (8 * left)) - 1);
 }
 
-// Barriers among 128 threads of a role (1: adapters, 2, 3: epilogue); the second tells all of them
+// Barriers among 128 threads of a role (1: adapters, 2 to 4: epilogue); the second tells all of them
 // whether `ok` held for all: a wait that ran out for one warp must not leave the others at a barrier.
 template <int ID>
 __device__ __forceinline__ void role_sync() {
@@ -433,7 +501,7 @@ __device__ __forceinline__ bool role_all(bool ok) {
 // In tensor memory a thread holds one lane, and lanes are consecutive elements of an output row: stored
 // as they come, a warp writes 64 bytes of a row at a time (bf16), which took 12,000 cycles for 192
 // columns, more than a tile's products.  So a chunk of columns goes through shared memory, as
-// rows of the output (two buffers, one barrier per chunk), and from there
+// rows of the output, and from there
 //   bf16   read from tensor memory in the matrix-fragment shape (16x256b), packed in pairs and stored
 //          transposed by stmatrix, 4 stores per 32 columns in place of 32; a whole chunk leaves by TMA
 //          (two boxes of 64 elements x 32 rows, 128-byte swizzle), a chunk that the group's rows end
@@ -484,39 +552,42 @@ __device__ __forceinline__ void store_rows(int vec, const uint8_t* buf, uint8_t*
   else if constexpr (!F32) store_rows<uint16_t, F32>(buf, out, stride, rows, bytes, tid);
 }
 
-// A chunk of the accumulator's columns (32 of bf16, 16 of fp32), times a, into a buffer.  `from`: the
-// address of the warp's 32 lanes and the first column.
-__device__ __forceinline__ void fetch_chunk_f32(uint32_t from, float a, bool none, uint8_t* buf, int tid) {
-  uint32_t v[16];
-  tmem_load(from, v);
-  float* o = reinterpret_cast<float*>(buf) + tid;
+// A chunk of the accumulator's columns (32 of bf16, 16 of fp32), times a, into registers as they are
+// stored (16 words), and from there into the buffer.  `from`: the address of the warp's 32 lanes and the
+// first column.
+__device__ __forceinline__ void fetch_f32(uint32_t from, float a, bool none, uint32_t (&w)[16]) {
+  tmem_load(from, w);
 #pragma unroll
-  for (int c = 0; c < 16; ++c) o[c * 128] = none ? 0.0f : __fmul_rn(__uint_as_float(v[c]), a);
+  for (int c = 0; c < 16; ++c) w[c] = none ? 0u : __float_as_uint(__fmul_rn(__uint_as_float(w[c]), a));
 }
 
-__device__ __forceinline__ void fetch_chunk_bf16(uint32_t from, float a, bool none, uint8_t* buf, int quarter, int lane) {
+__device__ __forceinline__ void put_f32(uint8_t* buf, const uint32_t (&w)[16], int tid) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) reinterpret_cast<uint32_t*>(buf)[c * 128 + tid] = w[c];
+}
+
+__device__ __forceinline__ void fetch_bf16(uint32_t from, float a, bool none, uint32_t (&w)[16]) {
   // v[h][4 i + 0..3]: lanes 16 h + lane / 4 and + 8, columns 8 i + 2 (lane % 4) and + 1
   uint32_t v[2][16];
   tmem_load_fragments(from, v);
-  if (none)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0;
-  // matrix m = lane / 8 of a store is lanes 8 m .. 8 m + 7 of the warp; its row lane % 8 a column
-  const int place = quarter * 64 + (lane >> 3) * 16, r = lane & 7;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t w[4];
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const uint32_t* f = &v[m >> 1][4 * i + 2 * (m & 1)];
       const __nv_bfloat162 b = __floats2bfloat162_rn(__fmul_rn(__uint_as_float(f[0]), a), __fmul_rn(__uint_as_float(f[1]), a));
-      w[m] = *reinterpret_cast<const uint32_t*>(&b);
+      w[4 * i + m] = none ? 0u : *reinterpret_cast<const uint32_t*>(&b);
     }
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                     smem_addr(buf + out_place<false>(8 * i + r, place))),
-                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+}
+
+__device__ __forceinline__ void put_bf16(uint8_t* buf, const uint32_t (&w)[16], int quarter, int lane) {
+  // matrix m = lane / 8 of a store is lanes 8 m .. 8 m + 7 of the warp; its row lane % 8 a column
+  const uint32_t to = smem_addr(buf) + out_place<false>(lane & 7, quarter * 64 + (lane >> 3) * 16);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1, %2, %3, %4};" ::"r"(to + 1024 * i),
+                 "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
                  : "memory");
-  }
 }
 
 __device__ __forceinline__ void tma_store3(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
@@ -529,19 +600,20 @@ __device__ __forceinline__ void tma_store3(const CUtensorMap* map, uint32_t src,
 // ---------------------------------------------------------------------------
 // The kernel.
 // ---------------------------------------------------------------------------
-constexpr int kGemmThreads = 384;
 constexpr int kScaleThreads = 128;
 
 constexpr int kLoraThreads = 128;
 
 template <int KIND, bool MX, int T, bool LORA>
-__global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
+__global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
     k_fp4_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+               const __grid_constant__ CUtensorMap map_sfa, const __grid_constant__ CUtensorMap map_sfb,
                const __grid_constant__ CUtensorMap map_out, const __grid_constant__ GemmParams p) {
   using S = GemmShape<KIND, MX, T, LORA>;
   constexpr int kTpb = S::kTilesPerBlock;
   constexpr int kScaleK = MX ? 128 : 64;  // summed elements of one scale tile
-  constexpr int kEpilogues = S::kEpilogues;
+  constexpr int kEpilogues = S::kEpilogues, kCtas = S::kCtas;
+  constexpr bool kPair = S::kWide;
   extern __shared__ uint8_t gemm_smem_raw[];
   __shared__ GemmBars bars;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(gemm_smem_raw) + 1023) & ~uintptr_t{1023});
@@ -553,21 +625,30 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
   int* units = hi + p.groups + 1;  // (tiled scales of ragged rows) 64-row units of scales before a group's
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
+  const uint32_t rank = kPair ? cluster_rank() : 0;  // of the pair; CTA 0 issues the products
+
   if (warp == 2) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bars.tmem)),
-                 "r"(S::kCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (kPair) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bars.tmem)),
+                   "r"(S::kCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bars.tmem)),
+                   "r"(S::kCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   if (warp == 1 && lane == 0) {
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(smem_addr(&bars.full[i]), S::kTiledB ? 1 : 1 + kScaleThreads / 32);
+      mbar_init(smem_addr(&bars.full[i]), S::kWide ? 1 : 1 + kScaleThreads / 32);
       mbar_init(smem_addr(&bars.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&bars.acc_full[i]), 1);
-      mbar_init(smem_addr(&bars.acc_empty[i]), 4 * kEpilogues);
-      mbar_init(smem_addr(&bars.chunk_full[i]), kLoraThreads / 32);
+      mbar_init(smem_addr(&bars.acc_empty[i]), 4 * kEpilogues * kCtas);
+      mbar_init(smem_addr(&bars.chunk_full[i]), kLoraThreads / 32 * kCtas);
       mbar_init(smem_addr(&bars.chunk_empty[i]), 1);
     }
     mbar_init(smem_addr(&bars.drain), 1);
@@ -601,7 +682,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
         hi[g] = b;
       }
       base += __shfl_sync(0xFFFFFFFFu, incl, 31);
-      if constexpr (KIND == kGemmRows && S::kTiledB) {
+      if constexpr (KIND == kGemmRows && S::kWide) {
         const int u = (b - a + 63) / 64, sum = warp_scan(u, lane);
         if (g < p.groups) units[g] = unit_base + sum - u;
         unit_base += __shfl_sync(0xFFFFFFFFu, sum, 31);
@@ -611,73 +692,83 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
   }
   umma_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // the peer's barriers are there
   umma_fence_after();
   const uint32_t tmem = bars.tmem;
+  const int first_tile = blockIdx.x / kCtas, tile_step = gridDim.x / kCtas;
   const int tiles = bars.tiles;
   bool ok = true;
+  // Arrivals on a barrier of the CTA that issues the products.
+  auto arrive_first = [&](uint32_t bar) {
+    if (rank) mbar_arrive_cluster(cluster_addr(bar, 0));
+    else mbar_arrive(bar);
+  };
+  auto release_acc = [&](uint32_t bar) {
+    if (rank) mbar_arrive_cluster_relaxed(cluster_addr(bar, 0));
+    else mbar_arrive(bar);
+  };
 
   if (warp == 0) {
     GemmRing ring;
     long long fills = 0;
-    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+    for (int tile = first_tile; tile < tiles && ok; tile += tile_step) {
       const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, units, tile);
       const int blocks = (t.k + kGemmKBlock - 1) / kGemmKBlock;
-      const int boxes = (t.n + S::kBox - 1) / S::kBox;
+      const int rows_b = t.n / kCtas, boxes = (rows_b + S::kBox - 1) / S::kBox;
+      const int a0 = t.a0 + static_cast<int>(rank) * kGemmLanes, b0 = t.b0 + static_cast<int>(rank) * rows_b;
       const int kt0 = t.k0 / kScaleK;
-      const uint8_t* sfa = p.sfa + (KIND == kGemmRows ? t.g * p.sfa_group_bytes : 0) +
-                           (static_cast<int64_t>(t.a0 / 128) * p.k_tiles + kt0) * 512;
-      int row_tiles = 0;
-      const uint8_t* sfb = nullptr;
-      if constexpr (S::kTiledB) {
-        const int first = t.s0 / 128;
-        row_tiles = (t.s0 + t.valid + 127) / 128 - first;  // (at most kRowTilesB: s0 is a multiple of 64)
-        sfb = p.sfb + (static_cast<int64_t>(first) * p.k_tiles + kt0) * 512;
-      }
+      // scale tiles of this CTA's lanes and of all the tile's columns
+      const int64_t ta = (KIND == kGemmRows ? static_cast<int64_t>(t.g) * p.a_row_tiles : 0) + a0 / 128;
+      const int first = S::kWide ? t.s0 / 128 : 0;
+      const int row_tiles = S::kWide ? (t.s0 + t.valid + 127) / 128 - first : 0;  // (<= kRowTilesB: s0 % 64 == 0)
       for (int kb = 0; kb < blocks; ++kb) {
         ok = warp_wait(smem_addr(&bars.empty[ring.s]), ring.phase ^ 1);
         if (!ok) break;
-        const uint32_t bar = smem_addr(&bars.full[ring.s]);
+        const uint32_t full = smem_addr(&bars.full[ring.s]);
+        const uint32_t bar = kPair ? cluster_addr(full, 0) : full;
         const uint32_t st = smem_addr(smem) + ring.s * S::kStageBytes;
         const uint32_t sa = st + S::kBytesA + S::kBytesB;
-        const int sf_tiles = min(kTpb, p.k_tiles - kt0 - kb * kTpb);
         const int kx = (t.k0 + kb * kGemmKBlock) / 2;
+        const int kt = kt0 + kb * kTpb;
         if (elect_one()) {
-          mbar_expect_tx(bar, S::kBytesA + boxes * S::kBox * 128 + sf_tiles * 512 * (1 + row_tiles));
-          tma_tile3(st, &map_a, kx, t.a0, KIND == kGemmRows ? t.g : 0, bar);
-          tma_bulk(sa, sfa + static_cast<int64_t>(kb) * kTpb * 512, sf_tiles * 512, bar);
+          if (rank == 0)
+            mbar_expect_tx(full, kCtas * (S::kBytesA + boxes * S::kBox * 128 + S::kBytesSfa * (1 + row_tiles)));
+          tma_tile3<kPair>(st, &map_a, kx, a0, KIND == kGemmRows ? t.g : 0, bar);
+          tma_tile3<kPair>(sa, &map_sfa, 0, kt, static_cast<int>(ta), bar);
           for (int i = 0; i < boxes; ++i)
-            tma_tile2(st + S::kBytesA + i * S::kBox * 128, &map_b, kx, t.b0 + i * S::kBox, bar);
+            tma_tile2<kPair>(st + S::kBytesA + i * S::kBox * 128, &map_b, kx, b0 + i * S::kBox, bar);
           for (int i = 0; i < row_tiles; ++i)
-            tma_bulk(sa + S::kBytesSfa + i * kTpb * 512,
-                     sfb + (static_cast<int64_t>(i) * p.k_tiles + kb * kTpb) * 512, sf_tiles * 512, bar);
+            tma_tile3<kPair>(sa + S::kBytesSfa + i * kTpb * 512, &map_sfb, 0, kt, first + i, bar);
         }
         __syncwarp();
         ++fills;
         ring.next(S::kStages);
       }
     }
-    if (!ok) {  // let the copies in flight land (bounded) before the CTA may end
+    if (!ok && rank == 0) {  // let the copies in flight land (bounded) before the CTA (the pair) may end
       for (long long f = fills > S::kStages ? fills - S::kStages : 0; f < fills; ++f)
         mbar_wait(smem_addr(&bars.full[f % S::kStages]), (f / S::kStages) & 1);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 && rank == 0) {
     GemmRing ring;
     int acc = 0;
     uint32_t acc_phase = 0;
     uint32_t parity = 0;
     GemmRing chunk;
-    const uint64_t codes0 = desc_codes(smem_addr(smem)), scales0 = desc_scales(smem_addr(smem));
+    const uint64_t codes0 = desc_codes(smem_addr(smem));
+    const uint64_t scales0 = desc_scales(smem_addr(smem) + S::kBytesA + S::kBytesB);
     const uint64_t chunk0 = desc_codes(smem_addr(chunks));
-    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+    for (int tile = first_tile; tile < tiles && ok; tile += tile_step) {
       const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, units, tile);
       const int blocks = (t.k + kGemmKBlock - 1) / kGemmKBlock;
       ok = warp_wait(smem_addr(&bars.acc_empty[acc]), acc_phase ^ 1);
       if (!ok) break;
       umma_fence_after();
       const uint32_t d = tmem + acc * T;
-      const uint32_t shift = S::kTiledB ? (t.s0 % 128) / 32 : 0;
+      const uint32_t shift = S::kWide ? (t.s0 % 128) / 32 : 0;
       const int row_tiles = (shift * 32 + t.n + 127) / 128;
-      const uint32_t idesc0 = umma_idesc<MX>(t.n, 0), idesc1 = umma_idesc<MX>(t.n, MX ? 2 : 0);
+      const uint32_t idesc0 = umma_idesc<MX>(S::kTileLanes, t.n, 0);
+      const uint32_t idesc1 = umma_idesc<MX>(S::kTileLanes, t.n, MX ? 2 : 0);
       bool chunks_left = LORA;
       auto take_chunk = [&]() {
         ok = warp_wait(smem_addr(&bars.chunk_full[chunk.s]), chunk.phase);
@@ -689,8 +780,9 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
         if (elect_one()) {
           for (int part = 0; part < 2; ++part)  // hi, lo
             for (int j = 0; j < steps; ++j)
-              umma_bf16(d, ch + 2 * j, ch + ((kGemmLanes * 128 + part * T * 128) >> 4) + 2 * j, umma_idesc_bf16(t.n));
-          umma_commit(smem_addr(&bars.chunk_empty[chunk.s]));
+              umma_bf16<kPair>(d, ch + 2 * j, ch + ((kGemmLanes * 128 + part * S::kRowsB * 128) >> 4) + 2 * j,
+                               umma_idesc_bf16(S::kTileLanes, t.n));
+          umma_commit<kPair>(smem_addr(&bars.chunk_empty[chunk.s]));
         }
         __syncwarp();
         chunk.next(S::kChunks);
@@ -701,29 +793,42 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
         ok = warp_wait(smem_addr(&bars.full[ring.s]), ring.phase);
         if (!ok) break;
         umma_fence_after();
-        const uint64_t st = codes0 + ring.s * (S::kStageBytes >> 4);
-        const uint64_t sa = scales0 + ((ring.s * S::kStageBytes + S::kBytesA + S::kBytesB) >> 4);
+        const uint32_t at = ring.s * (S::kStageBytes >> 4);  // (descriptor addresses are in 16 bytes)
+        const uint64_t st = codes0 + at, sa = scales0 + at;
         const uint32_t ca = tmem + S::kColSf + parity * (S::kColsSfa + S::kColsSfb), cb = ca + S::kColsSfa;
-        const int steps = min(4, (t.k - kb * kGemmKBlock + 63) / 64);
-        const int sf_tiles = (steps * 64 + kScaleK - 1) / kScaleK;
+        const uint32_t more = kb != 0;
+        auto copy_scales = [&](int j) {
+          umma_copy_scales<kPair>(ca + 4 * j, sa + 32 * j);
+          umma_copy_scales<kPair>(cb + j * S::kRowTilesB * 4, sa + (S::kBytesSfa >> 4) + 32 * j);
+        };
+        auto copy_scales2 = [&](int j) {  // the second 128 columns
+          umma_copy_scales<kPair>(cb + (j * S::kRowTilesB + 1) * 4, sa + (S::kBytesSfa >> 4) + (kTpb + j) * 32);
+        };
+        auto multiply = [&](int j) {
+          const int sj = MX ? j / 2 : j;
+          umma_fp4<kPair, MX>(d, st + 2 * j, st + (S::kBytesA >> 4) + 2 * j, (j & 1) ? idesc1 : idesc0, ca + 4 * sj,
+                              cb + sj * S::kRowTilesB * 4 + shift, j ? 1u : more);
+        };
+        const int left = t.k - kb * kGemmKBlock;
         if (elect_one()) {
+          if (left >= kGemmKBlock - 63) {  // all four steps
 #pragma unroll
-          for (int j = 0; j < kTpb; ++j) {
-            if (j >= sf_tiles) break;
-            umma_copy_scales(ca + 4 * j, sa + 32 * j);
+            for (int j = 0; j < kTpb; ++j) copy_scales(j);
+            if (S::kRowTilesB > 1 && row_tiles > 1) {
 #pragma unroll
-            for (int i = 0; i < S::kRowTilesB; ++i)
-              if (i < row_tiles)
-                umma_copy_scales(cb + (j * S::kRowTilesB + i) * 4, sa + (S::kBytesSfa >> 4) + (i * kTpb + j) * 32);
+              for (int j = 0; j < kTpb; ++j) copy_scales2(j);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) multiply(j);
+          } else {
+            const int steps = (left + 63) / 64;
+            for (int j = 0; j * kScaleK < left; ++j) {
+              copy_scales(j);
+              if (S::kRowTilesB > 1 && row_tiles > 1) copy_scales2(j);
+            }
+            for (int j = 0; j < steps; ++j) multiply(j);
           }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (j >= steps) break;
-            const int sj = MX ? j / 2 : j;
-            umma_fp4<MX>(d, st + 2 * j, st + (S::kBytesA >> 4) + 2 * j, (j & 1) ? idesc1 : idesc0, ca + 4 * sj,
-                         cb + sj * S::kRowTilesB * 4 + shift, (kb | j) != 0);
-          }
-          umma_commit(smem_addr(&bars.empty[ring.s]));
+          umma_commit<kPair>(smem_addr(&bars.empty[ring.s]));
         }
         __syncwarp();
         parity ^= 1;
@@ -731,81 +836,90 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
       }
       while (LORA && chunks_left && ok) take_chunk();
       if (!ok) break;
-      if (elect_one()) umma_commit(smem_addr(&bars.acc_full[acc]));
+      if (elect_one()) umma_commit<kPair>(smem_addr(&bars.acc_full[acc]));
       __syncwarp();
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
     if (!ok) {  // let the products in flight finish (bounded) before tensor memory is freed
-      if (elect_one()) umma_commit(smem_addr(&bars.drain));
+      if (elect_one()) umma_commit<kPair>(smem_addr(&bars.drain));
       __syncwarp();
       mbar_wait(smem_addr(&bars.drain), 0);
     }
   } else if (warp >= 4 && warp < 4 + 4 * kEpilogues) {
-    // Group `half` of 128 threads takes every kEpilogues-th chunk.  (CONTR: the sums are short, two
-    // groups keep up with them.)
-    const int half = (warp - 4) / 4, quarter = warp & 3, tid = threadIdx.x & 127;
-    int acc = 0, buf = 0;
+    // Group `part` of 128 threads takes every kEpilogues-th chunk.  (With short sums the output is most of
+    // the work: a chunk takes 1000 cycles, mostly latencies, and a wide tile has six.)
+    const int part = (warp - 4) / 4, quarter = warp & 3, tid = threadIdx.x & 127;
+    auto sync = [&]() {
+      if (part == 0) role_sync<2>();
+      else if (part == 1) role_sync<3>();
+      else role_sync<4>();
+    };
+    int acc = 0;
     uint32_t acc_phase = 0;
     const int es = p.out_f32 ? 4 : 2, step = p.out_f32 ? 16 : 32;
-    uint8_t* const my_outs = outs + half * 2 * kOutBytes;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    uint8_t* const buf = outs + part * kOutBytes;
+    for (int tile = first_tile; tile < tiles; tile += tile_step) {
       const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, units, tile);
       float a = 1.0f;
       if (!MX) a = __fmul_rn(__ldg(p.sg_a + (KIND == kGemmRows ? t.g : 0)), __ldg(p.sg_b));
       const bool full = mbar_wait(smem_addr(&bars.acc_full[acc]), acc_phase);
-      ok = half == 0 ? role_all<2>(full) : role_all<3>(full);
+      ok = part == 0 ? role_all<2>(full) : part == 1 ? role_all<3>(full) : role_all<4>(full);
       if (!ok) break;
       umma_fence_after();
       const int64_t row0 = KIND == kGemmRows ? t.b0 : static_cast<int64_t>(t.g) * p.nb + t.b0;
       const int64_t stride = static_cast<int64_t>(p.na) * es;
-      uint8_t* const out = static_cast<uint8_t*>(p.out) + row0 * stride + static_cast<int64_t>(t.a0) * es;
-      const int bytes = min(128, p.na - t.a0) * es;
+      const int a0 = t.a0 + static_cast<int>(rank) * kGemmLanes;
+      uint8_t* const out = static_cast<uint8_t*>(p.out) + row0 * stride + static_cast<int64_t>(a0) * es;
+      const int bytes = min(128, p.na - a0) * es;  // (not positive: the pair's second CTA has no lanes here)
       const bool none = t.k == 0;  // an empty sum: no product wrote the accumulator
       const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * T;
       bool held = true;
-      for (int c0 = half * step; c0 < t.valid; c0 += kEpilogues * step) {
-        uint8_t* const o = my_outs + buf * kOutBytes;
+      for (int c0 = part * step; c0 < t.valid; c0 += kEpilogues * step) {
         const int rows = min(step, t.valid - c0);
-        if (p.out_f32) fetch_chunk_f32(from + c0, a, none, o, tid);
-        else fetch_chunk_bf16(from + c0, a, none, o, quarter, lane);
+        uint32_t w[16];
+        if (p.out_f32) fetch_f32(from + c0, a, none, w);
+        else fetch_bf16(from + c0, a, none, w);
         if (c0 + kEpilogues * step >= t.valid) {  // the group's last chunk: its part has been read
           umma_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&bars.acc_empty[acc]));
+          if (lane == 0) release_acc(smem_addr(&bars.acc_empty[acc]));
           held = false;
         }
+        // (the group's first warp issues the copies, by the same elected lane each time)
+        if (quarter == 0) {
+          if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+        }
+        sync();  // the last chunk has left the buffer
+        if (p.out_f32) put_f32(buf, w, tid);
+        else put_bf16(buf, w, quarter, lane);
         // (CONTR: rows past nb are past the tensor map's end and not written)
         const bool by_tma = p.out_tma && (KIND == kGemmContr || rows == 32);
         fence_proxy_async_smem();
-        // (the group's first warp issues the copies, by the same elected lane each time)
-        if (quarter == 0 && elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the other buffer is free
-        __syncwarp();
-        if (half == 0) role_sync<2>();
-        else role_sync<3>();
+        sync();
         if (by_tma) {
           if (quarter == 0 && elect_one()) {
             const int y = t.b0 + c0, z = KIND == kGemmRows ? 0 : t.g;
-            tma_store3(&map_out, smem_addr(o), t.a0, y, z);
-            if (t.a0 + 64 < p.na) tma_store3(&map_out, smem_addr(o) + 4096, t.a0 + 64, y, z);
+            if (a0 < p.na) tma_store3(&map_out, smem_addr(buf), a0, y, z);
+            if (a0 + 64 < p.na) tma_store3(&map_out, smem_addr(buf) + 4096, a0 + 64, y, z);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         } else if (p.out_f32) {
-          store_rows<true>(p.out_vec, o, out + c0 * stride, stride, rows, bytes, tid);
+          store_rows<true>(p.out_vec, buf, out + c0 * stride, stride, rows, bytes, tid);
         } else {
-          store_rows<false>(p.out_vec, o, out + c0 * stride, stride, rows, bytes, tid);
+          store_rows<false>(p.out_vec, buf, out + c0 * stride, stride, rows, bytes, tid);
         }
-        buf ^= 1;
       }
       if (held) {  // no chunk for this group
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&bars.acc_empty[acc]));
+        if (lane == 0) release_acc(smem_addr(&bars.acc_empty[acc]));
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
     if (quarter == 0 && elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-  } else if (!S::kTiledB && warp >= 8 && warp < 12) {
+  } else if (!S::kWide && warp >= 8 && warp < 12) {
     constexpr int kRowsPerThread = (T + kScaleThreads - 1) / kScaleThreads;
     constexpr int kAhead = 4;  // stages whose scales are loaded together: a batch
     constexpr int kBlockBytes = MX ? 8 : 16;
@@ -824,7 +938,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
       Batch c = b;
       c.kb += kAhead;
       if (c.kb >= blocks) {
-        c.tile += gridDim.x;
+        c.tile += tile_step;
         enter(c);
       }
       return c;
@@ -870,7 +984,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
       }
     };
     Loaded w0, w1;
-    Batch b0{static_cast<int>(blockIdx.x)}, b1;
+    Batch b0{first_tile}, b1;
     enter(b0);
     load(b0, w0);
     while (b0.tile < tiles && ok) {
@@ -882,12 +996,12 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
     }
   }
   if constexpr (LORA) {
-    if (warp >= 12) {
-      const int tid = threadIdx.x - kGemmThreads;
+    if (warp >= S::kLoraWarp) {
+      const int tid = threadIdx.x - 32 * S::kLoraWarp;
       const int rank_steps = (p.rank + 15) / 16;
       GemmRing chunk;
       int turn = 0;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      for (int tile = first_tile; tile < tiles && ok; tile += tile_step) {
         const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, units, tile);
         role_sync<1>();  // the last tile's ids have been read
         for (int r = tid; r < t.n; r += kLoraThreads) {
@@ -929,7 +1043,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
           uint8_t* const ch = chunks + chunk.s * S::kChunkBytes;
           const uint4 zero = make_uint4(0, 0, 0, 0);
           {  // B_a of this thread's lane
-            const int n = t.a0 + tid;
+            const int n = t.a0 + static_cast<int>(rank) * kGemmLanes + tid;
             uint4 v[4][2];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -947,9 +1061,10 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
               for (int q = 0; q < 2; ++q)
                 *reinterpret_cast<uint4*>(ch + tid * 128 + (((2 * i + q) ^ (tid & 7)) << 4)) = v[i][q];
           }
-          for (int r = tid; r < t.n; r += kLoraThreads) {  // t of a row: zero outside its adapter
-            const int id = bars.ids[r];
-            const uint8_t* src = p.lora_t + static_cast<int64_t>(t.b0 + r) * p.rank * 4;
+          const int rows_b = t.n / kCtas, r0 = static_cast<int>(rank) * rows_b;
+          for (int r = tid; r < rows_b; r += kLoraThreads) {  // t of this CTA's rows: zero outside their adapter
+            const int id = bars.ids[r0 + r];
+            const uint8_t* src = p.lora_t + static_cast<int64_t>(t.b0 + r0 + r) * p.rank * 4;
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
               uint4 v[4][2];
@@ -962,7 +1077,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
                   if (slot_a[i] >= 0 && slot_a[i] == id && k < p.rank)
                     v[i][q] = __ldg(reinterpret_cast<const uint4*>(src + (part * p.rank + k) * 2));
                 }
-              uint8_t* dst = ch + kGemmLanes * 128 + part * T * 128 + r * 128;
+              uint8_t* dst = ch + kGemmLanes * 128 + part * S::kRowsB * 128 + r * 128;
 #pragma unroll
               for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -975,7 +1090,7 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&bars.chunk_full[chunk.s]));
+          if (lane == 0) arrive_first(smem_addr(&bars.chunk_full[chunk.s]));
           chunk.next(S::kChunks);
         } while (a != INT_MAX);
       }
@@ -987,9 +1102,14 @@ __global__ void __launch_bounds__(kGemmThreads + (LORA ? kLoraThreads : 0), 1)
   __syncwarp();
   umma_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // nothing of the pair reads or signals this CTA any more
   umma_fence_after();
-  if (warp == 2)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols) : "memory");
+  if (warp == 2) {
+    if constexpr (kPair)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols) : "memory");
+  }
 }
 
 // ---------------------------------------------------------------------------
