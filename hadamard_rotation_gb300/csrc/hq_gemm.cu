@@ -75,13 +75,13 @@ cudaError_t sm_count(int* sms) {
   return e;
 }
 
-// Scale tiles [row_tiles][k_tiles] of 512 bytes, as words: boxes of `box` tiles along k.
-bool encode_scales(CUtensorMap* map, const uint8_t* s, int64_t k_tiles, int64_t row_tiles, int box) {
+// Scale tiles [row_tiles][k_tiles] of 512 bytes, as words: boxes of `box` tiles along k, `box_rows` of rows.
+bool encode_scales(CUtensorMap* map, const uint8_t* s, int64_t k_tiles, int64_t row_tiles, int box, int box_rows) {
   const EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   const cuuint64_t size[3] = {128, static_cast<cuuint64_t>(k_tiles), static_cast<cuuint64_t>(row_tiles)};
   const cuuint64_t stride[2] = {512, static_cast<cuuint64_t>(k_tiles * 512)};
-  const cuuint32_t dim[3] = {128, static_cast<cuuint32_t>(box), 1}, step[3] = {1, 1, 1};
+  const cuuint32_t dim[3] = {128, static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(box_rows)}, step[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(s), size, stride, dim, step,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -114,8 +114,8 @@ hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t b_scale_r
   CUtensorMap ma, mb, msa, msb = {}, mo = {};
   if (!encode_codes(&ma, a.q, a.row_bytes, a.rows, a.groups, hq::kGemmLanes, 3) ||
       !encode_codes(&mb, b.q, b.row_bytes, b.rows, 1, S::kBox, 2) ||
-      !encode_scales(&msa, p.sfa, p.k_tiles, a.groups * p.a_row_tiles, S::kTilesPerBlock) ||
-      (S::kWide && !encode_scales(&msb, p.sfb, p.k_tiles, b_scale_row_tiles, S::kTilesPerBlock)))
+      !encode_scales(&msa, p.sfa, p.k_tiles, a.groups * p.a_row_tiles, S::kTilesPerBlock, 1) ||
+      (S::kWide && !encode_scales(&msb, p.sfb, p.k_tiles, b_scale_row_tiles, S::kTilesPerBlock, S::kRowTilesB)))
     return cuda_fail(cudaErrorInvalidValue);
   p.out_tma = !p.out_f32 && p.out_vec == 16 &&
               encode_out(&mo, p.out, p.na, KIND == hq::kGemmRows ? p.extent : p.nb, KIND == hq::kGemmRows ? 1 : p.groups);

@@ -102,8 +102,7 @@ struct GemmShape {
   static constexpr int kRowsB = T / kCtas;           // rows of B in a CTA's shared memory
   static constexpr int kTilesPerBlock = MX ? 2 : 4;  // scale tiles along K per stage
   static constexpr int kRowTilesB = (T + 127) / 128;
-  static constexpr int kBox = kWide ? 32 : 16;       // rows of B per TMA box
-  static constexpr int kStepN = 16 * kCtas;          // columns of an instruction come in steps of this
+  static constexpr int kBox = kWide ? kRowsB : 16;   // rows of B per TMA box
   static constexpr int kBytesA = kGemmLanes * 128;
   static constexpr int kBytesB = kRowsB * 128;
   static constexpr int kBytesSfa = kTilesPerBlock * 512;
@@ -115,7 +114,9 @@ struct GemmShape {
   static constexpr int kChunks = kWide ? 1 : 2;
   static constexpr int kChunkGap = kWide ? 5 : 2;         // stages between two chunks of a tile
   static constexpr int kEpilogues = !kWide ? 1 : LORA ? 2 : 3;  // groups of 128 threads
-  static constexpr int kOuts = kEpilogues * 8 * 1024;           // their output buffers
+  // 32-column blocks of the output per chunk.  CONTR: two, three groups then take a tile in one chunk each.
+  static constexpr int kBlocks = KIND == kGemmContr ? 2 : 1;
+  static constexpr int kOuts = kEpilogues * kBlocks * 8 * 1024;  // the groups' output buffers
   static constexpr int kLoraWarp = 4 + 4 * (kWide ? kEpilogues : 2);  // the adapters' first warp
   static constexpr int kThreads = 32 * (kLoraWarp + (LORA ? 4 : 0));
   static constexpr int kRingBytes = 216 * 1024 - kChunks * kChunkBytes - kOuts;
@@ -398,6 +399,33 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {
   return v;
 }
 
+// The tiles of a CTA in their order, for one warp: 32 are worked out at a time, one per lane (the search and
+// the divisions take 500 cycles), and handed out by shuffles.
+template <int KIND, int T>
+struct GemmTiles {
+  const GemmParams& p;
+  const int *start, *lo, *hi, *units;
+  int tiles, step;
+  int next;      // the next tile
+  int count = 0;  // handed out since the last 32 were worked out
+  GemmTile mine;
+
+  // The next tile into t; false: there is none.
+  __device__ __forceinline__ bool get(GemmTile& t) {
+    if (next >= tiles) return false;
+    if ((count & 31) == 0) {
+      const int tile = next + static_cast<int>(threadIdx.x & 31) * step;
+      mine = gemm_tile<KIND, T>(p, start, lo, hi, units, tile < tiles ? tile : next);
+    }
+    const int from = count & 31;
+    auto pick = [&](int v) { return __shfl_sync(0xFFFFFFFFu, v, from); };
+    t = {pick(mine.g), pick(mine.a0), pick(mine.b0), pick(mine.valid), pick(mine.n), pick(mine.k0), pick(mine.k), pick(mine.s0)};
+    ++count;
+    next += step;
+    return true;
+  }
+};
+
 // The ring position of a role: stage s, and the parity of its current pass.
 struct GemmRing {
   int s = 0;
@@ -508,9 +536,9 @@ __device__ __forceinline__ bool role_all(bool ok) {
 //          in, and rows not aligned to 16 bytes, by plain stores;
 //   fp32   one store per element and plain stores.
 // ---------------------------------------------------------------------------
-constexpr int kOutBytes = 8 * 1024;  // one buffer: 128 lanes x 32 columns of bf16 or 16 of fp32
+constexpr int kOutBytes = 8 * 1024;  // a block: 128 lanes x 32 columns of bf16 or 16 of fp32
 
-// Byte `at` of row r of a buffer.  bf16: two halves of 32 rows x 128 bytes, 16-byte pieces swizzled by the
+// Byte `at` of row r of a block.  bf16: two halves of 32 rows x 128 bytes, 16-byte pieces swizzled by the
 // row.  fp32: 16 rows x 512 bytes.
 template <bool F32>
 __device__ __forceinline__ int out_place(int r, int at) {
@@ -518,7 +546,7 @@ __device__ __forceinline__ int out_place(int r, int at) {
   return (at >> 7) * 4096 + r * 128 + ((((at >> 4) & 7) ^ (r & 7)) << 4) + (at & 15);
 }
 
-// The buffer's first `rows` rows, the first `bytes` of each, to global rows `stride` bytes apart: all
+// The block's first `rows` rows, the first `bytes` of each, to global rows `stride` bytes apart: all
 // reads before the writes.
 template <typename V, bool F32>
 __device__ __forceinline__ void store_rows(const uint8_t* buf, uint8_t* out, int64_t stride, int rows, int bytes,
@@ -552,7 +580,7 @@ __device__ __forceinline__ void store_rows(int vec, const uint8_t* buf, uint8_t*
   else if constexpr (!F32) store_rows<uint16_t, F32>(buf, out, stride, rows, bytes, tid);
 }
 
-// A chunk of the accumulator's columns (32 of bf16, 16 of fp32), times a, into registers as they are
+// A block of the accumulator's columns (32 of bf16, 16 of fp32), times a, into registers as they are
 // stored (16 words), and from there into the buffer.  `from`: the address of the warp's 32 lanes and the
 // first column.
 __device__ __forceinline__ void fetch_f32(uint32_t from, float a, bool none, uint32_t (&w)[16]) {
@@ -612,7 +640,7 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
   using S = GemmShape<KIND, MX, T, LORA>;
   constexpr int kTpb = S::kTilesPerBlock;
   constexpr int kScaleK = MX ? 128 : 64;  // summed elements of one scale tile
-  constexpr int kEpilogues = S::kEpilogues, kCtas = S::kCtas;
+  constexpr int kEpilogues = S::kEpilogues, kBlocks = S::kBlocks, kCtas = S::kCtas;
   constexpr bool kPair = S::kWide;
   extern __shared__ uint8_t gemm_smem_raw[];
   __shared__ GemmBars bars;
@@ -695,8 +723,9 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
   if constexpr (kPair) cluster_sync();  // the peer's barriers are there
   umma_fence_after();
   const uint32_t tmem = bars.tmem;
-  const int first_tile = blockIdx.x / kCtas, tile_step = gridDim.x / kCtas;
   const int tiles = bars.tiles;
+  GemmTiles<KIND, T> order{p, start, lo, hi, units, tiles, static_cast<int>(gridDim.x) / kCtas,
+                           static_cast<int>(blockIdx.x) / kCtas};
   bool ok = true;
   // Arrivals on a barrier of the CTA that issues the products.
   auto arrive_first = [&](uint32_t bar) {
@@ -711,16 +740,15 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
   if (warp == 0) {
     GemmRing ring;
     long long fills = 0;
-    for (int tile = first_tile; tile < tiles && ok; tile += tile_step) {
-      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, units, tile);
+    GemmTile t;
+    while (ok && order.get(t)) {
       const int blocks = (t.k + kGemmKBlock - 1) / kGemmKBlock;
-      const int rows_b = t.n / kCtas, boxes = (rows_b + S::kBox - 1) / S::kBox;
+      const int rows_b = t.n / kCtas, boxes = S::kWide ? 1 : (rows_b + S::kBox - 1) / S::kBox;
       const int a0 = t.a0 + static_cast<int>(rank) * kGemmLanes, b0 = t.b0 + static_cast<int>(rank) * rows_b;
       const int kt0 = t.k0 / kScaleK;
       // scale tiles of this CTA's lanes and of all the tile's columns
-      const int64_t ta = (KIND == kGemmRows ? static_cast<int64_t>(t.g) * p.a_row_tiles : 0) + a0 / 128;
-      const int first = S::kWide ? t.s0 / 128 : 0;
-      const int row_tiles = S::kWide ? (t.s0 + t.valid + 127) / 128 - first : 0;  // (<= kRowTilesB: s0 % 64 == 0)
+      const int ta = (KIND == kGemmRows ? t.g * p.a_row_tiles : 0) + a0 / 128, tb = S::kWide ? t.s0 / 128 : 0;
+      const uint32_t bytes = kCtas * (S::kBytesA + boxes * S::kBox * 128 + S::kBytesSfa + (S::kWide ? S::kBytesSfb : 0));
       for (int kb = 0; kb < blocks; ++kb) {
         ok = warp_wait(smem_addr(&bars.empty[ring.s]), ring.phase ^ 1);
         if (!ok) break;
@@ -732,13 +760,12 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
         const int kt = kt0 + kb * kTpb;
         if (elect_one()) {
           if (rank == 0)
-            mbar_expect_tx(full, kCtas * (S::kBytesA + boxes * S::kBox * 128 + S::kBytesSfa * (1 + row_tiles)));
+            mbar_expect_tx(full, bytes);
           tma_tile3<kPair>(st, &map_a, kx, a0, KIND == kGemmRows ? t.g : 0, bar);
-          tma_tile3<kPair>(sa, &map_sfa, 0, kt, static_cast<int>(ta), bar);
+          tma_tile3<kPair>(sa, &map_sfa, 0, kt, ta, bar);
           for (int i = 0; i < boxes; ++i)
             tma_tile2<kPair>(st + S::kBytesA + i * S::kBox * 128, &map_b, kx, b0 + i * S::kBox, bar);
-          for (int i = 0; i < row_tiles; ++i)
-            tma_tile3<kPair>(sa + S::kBytesSfa + i * kTpb * 512, &map_sfb, 0, kt, first + i, bar);
+          if constexpr (S::kWide) tma_tile3<kPair>(sa + S::kBytesSfa, &map_sfb, 0, kt, tb, bar);
         }
         __syncwarp();
         ++fills;
@@ -758,8 +785,8 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
     const uint64_t codes0 = desc_codes(smem_addr(smem));
     const uint64_t scales0 = desc_scales(smem_addr(smem) + S::kBytesA + S::kBytesB);
     const uint64_t chunk0 = desc_codes(smem_addr(chunks));
-    for (int tile = first_tile; tile < tiles && ok; tile += tile_step) {
-      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, units, tile);
+    GemmTile t;
+    while (ok && order.get(t)) {
       const int blocks = (t.k + kGemmKBlock - 1) / kGemmKBlock;
       ok = warp_wait(smem_addr(&bars.acc_empty[acc]), acc_phase ^ 1);
       if (!ok) break;
@@ -847,8 +874,8 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
       mbar_wait(smem_addr(&bars.drain), 0);
     }
   } else if (warp >= 4 && warp < 4 + 4 * kEpilogues) {
-    // Group `part` of 128 threads takes every kEpilogues-th chunk.  (With short sums the output is most of
-    // the work: a chunk takes 1000 cycles, mostly latencies, and a wide tile has six.)
+    // Group `part` of 128 threads takes every kEpilogues-th chunk of kBlocks blocks.  (With short sums the
+    // output is most of the work: a chunk takes 1000 cycles, mostly latencies.)
     const int part = (warp - 4) / 4, quarter = warp & 3, tid = threadIdx.x & 127;
     auto sync = [&]() {
       if (part == 0) role_sync<2>();
@@ -857,10 +884,10 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
     };
     int acc = 0;
     uint32_t acc_phase = 0;
-    const int es = p.out_f32 ? 4 : 2, step = p.out_f32 ? 16 : 32;
-    uint8_t* const buf = outs + part * kOutBytes;
-    for (int tile = first_tile; tile < tiles; tile += tile_step) {
-      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, units, tile);
+    const int es = p.out_f32 ? 4 : 2, block = p.out_f32 ? 16 : 32, step = kBlocks * block;
+    uint8_t* const buf = outs + part * kBlocks * kOutBytes;
+    GemmTile t;
+    while (order.get(t)) {
       float a = 1.0f;
       if (!MX) a = __fmul_rn(__ldg(p.sg_a + (KIND == kGemmRows ? t.g : 0)), __ldg(p.sg_b));
       const bool full = mbar_wait(smem_addr(&bars.acc_full[acc]), acc_phase);
@@ -876,40 +903,50 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
       const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * T;
       bool held = true;
       for (int c0 = part * step; c0 < t.valid; c0 += kEpilogues * step) {
-        const int rows = min(step, t.valid - c0);
-        uint32_t w[16];
-        if (p.out_f32) fetch_f32(from + c0, a, none, w);
-        else fetch_bf16(from + c0, a, none, w);
+        uint32_t w[kBlocks][16];
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {  // (past t.valid: columns of the accumulator that are not stored)
+          if (p.out_f32) fetch_f32(from + c0 + i * block, a, none, w[i]);
+          else fetch_bf16(from + c0 + i * block, a, none, w[i]);
+        }
         if (c0 + kEpilogues * step >= t.valid) {  // the group's last chunk: its part has been read
           umma_fence_before();
           __syncwarp();
           if (lane == 0) release_acc(smem_addr(&bars.acc_empty[acc]));
           held = false;
         }
-        // (the group's first warp issues the copies, by the same elected lane each time)
-        if (quarter == 0) {
+        // (The copies of a block's two halves are issued by two warps, by the same elected lane each time.)
+        if (quarter < 2 * kBlocks) {
           if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           __syncwarp();
         }
         sync();  // the last chunk has left the buffer
-        if (p.out_f32) put_f32(buf, w, tid);
-        else put_bf16(buf, w, quarter, lane);
-        // (CONTR: rows past nb are past the tensor map's end and not written)
-        const bool by_tma = p.out_tma && (KIND == kGemmContr || rows == 32);
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          if (p.out_f32) put_f32(buf + i * kOutBytes, w[i], tid);
+          else put_bf16(buf + i * kOutBytes, w[i], quarter, lane);
+        }
         fence_proxy_async_smem();
         sync();
-        if (by_tma) {
-          if (quarter == 0 && elect_one()) {
-            const int y = t.b0 + c0, z = KIND == kGemmRows ? 0 : t.g;
-            if (a0 < p.na) tma_store3(&map_out, smem_addr(buf), a0, y, z);
-            if (a0 + 64 < p.na) tma_store3(&map_out, smem_addr(buf) + 4096, a0 + 64, y, z);
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          const int c = c0 + i * block, rows = min(block, t.valid - c);
+          if (rows <= 0) break;
+          const uint8_t* const b = buf + i * kOutBytes;
+          // (CONTR: rows past nb are past the tensor map's end and not written)
+          if (p.out_tma && (KIND == kGemmContr || rows == 32)) {
+            const int half = quarter - 2 * i, x = a0 + 64 * half;
+            if (half >= 0 && half < 2 && x < p.na && elect_one()) {
+              tma_store3(&map_out, smem_addr(b) + 4096 * half, x, t.b0 + c, KIND == kGemmRows ? 0 : t.g);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+          } else if (p.out_f32) {
+            store_rows<true>(p.out_vec, b, out + c * stride, stride, rows, bytes, tid);
+          } else {
+            store_rows<false>(p.out_vec, b, out + c * stride, stride, rows, bytes, tid);
           }
-        } else if (p.out_f32) {
-          store_rows<true>(p.out_vec, buf, out + c0 * stride, stride, rows, bytes, tid);
-        } else {
-          store_rows<false>(p.out_vec, buf, out + c0 * stride, stride, rows, bytes, tid);
         }
+        __syncwarp();
       }
       if (held) {  // no chunk for this group
         __syncwarp();
@@ -918,7 +955,7 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
-    if (quarter == 0 && elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   } else if (!S::kWide && warp >= 8 && warp < 12) {
     constexpr int kRowsPerThread = (T + kScaleThreads - 1) / kScaleThreads;
     constexpr int kAhead = 4;  // stages whose scales are loaded together: a batch
@@ -927,20 +964,18 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
     const int blocks = (p.k + kGemmKBlock - 1) / kGemmKBlock;
     GemmRing ring;
     struct Batch {
-      int tile, kb, b0, valid, n;
+      bool live;  // there is one
+      int kb, b0, valid, n;
     };
-    auto enter = [&](Batch& b) {  // a tile's first batch
-      if (b.tile >= tiles) return;
-      const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, units, b.tile);
-      b.kb = 0, b.b0 = t.b0, b.valid = t.valid, b.n = t.n;
+    auto enter = [&](Batch& b) {  // the next tile's first batch
+      GemmTile t;
+      b.live = order.get(t);
+      if (b.live) b.kb = 0, b.b0 = t.b0, b.valid = t.valid, b.n = t.n;
     };
     auto after = [&](const Batch& b) {
       Batch c = b;
       c.kb += kAhead;
-      if (c.kb >= blocks) {
-        c.tile += tile_step;
-        enter(c);
-      }
+      if (c.live && c.kb >= blocks) enter(c);
       return c;
     };
     constexpr int kWords = kAhead * kBlockBytes / 4;
@@ -949,7 +984,7 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
       ScaleRow row[kRowsPerThread];
     };
     auto load = [&](const Batch& b, Loaded& l) {
-      if (b.tile >= tiles) return;
+      if (!b.live) return;
 #pragma unroll
       for (int i = 0; i < kRowsPerThread; ++i) {
         const int r = tid + kScaleThreads * i;
@@ -984,13 +1019,13 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
       }
     };
     Loaded w0, w1;
-    Batch b0{first_tile}, b1;
+    Batch b0, b1;
     enter(b0);
     load(b0, w0);
-    while (b0.tile < tiles && ok) {
+    while (b0.live && ok) {
       b1 = after(b0);
       write(b0, w0, b1, w1);
-      if (b1.tile >= tiles || !ok) break;
+      if (!b1.live || !ok) break;
       b0 = after(b1);
       write(b1, w1, b0, w0);
     }
@@ -1001,8 +1036,8 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
       const int rank_steps = (p.rank + 15) / 16;
       GemmRing chunk;
       int turn = 0;
-      for (int tile = first_tile; tile < tiles && ok; tile += tile_step) {
-        const GemmTile t = gemm_tile<KIND, T>(p, start, lo, hi, units, tile);
+      GemmTile t;
+      while (ok && order.get(t)) {
         role_sync<1>();  // the last tile's ids have been read
         for (int r = tid; r < t.n; r += kLoraThreads) {
           const int id = r < t.valid ? __ldg(p.lora_ids + t.b0 + r) : -1;
