@@ -16,9 +16,9 @@ using hq::NormParams;
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 constexpr int64_t kMaxD = 32768;
-constexpr int kSmemBytes = 216 * 1024;  // ring and parameters, of the 227 KB a CTA may have
+constexpr int kSmemBytes = 216 * 1024;  // the ring, of the 227 KB a CTA may have
 
-// Columns per CTA: two units per thread, and no more than leave room for two stages.
+// Columns per CTA: two units per thread, and no more than leave room for three stages.
 struct Shape {
   int ranks, cols, tpr, units, rows, stages;
   size_t smem;
@@ -37,11 +37,11 @@ Shape shape_of(int64_t M, int D, int es, int tensors, int sms) {
   int64_t rows = s.ranks > 1 ? 1 : hq::kNormThreads / s.tpr;
   if (rows > (M + sms - 1) / sms) rows = (M + sms - 1) / sms;
   s.rows = static_cast<int>(rows);
-  const size_t stage = static_cast<size_t>(tensors) * s.rows * s.cols * es, params = 8 * static_cast<size_t>(s.cols);
-  size_t n = (kSmemBytes - params) / stage;
+  const size_t stage = static_cast<size_t>(tensors) * s.rows * s.cols * es;
+  const size_t n = kSmemBytes / stage;  // at least 3
   s.stages = static_cast<int>(n > hq::kNormMaxStages ? hq::kNormMaxStages : n);
-  s.smem = params + s.stages * stage;
-  if (s.smem < 2 * params) s.smem = 2 * params;  // the backward kernel's column sums lie over the ring
+  s.smem = s.stages * stage;
+  if (s.smem < 8 * static_cast<size_t>(s.cols)) s.smem = 8 * s.cols;  // the column sums lie over the ring
   return s;
 }
 

@@ -20,11 +20,14 @@
 // times gate and times w_post, so two column sums are kept, not three.
 //
 // Bound by memory: 8 bytes per element forward, 12 backward (bf16).  A CTA keeps its columns for all
-// its rows, so the column sums stay in registers and the parameters in shared memory; rows arrive
-// through a ring of bulk copies (cp.async.bulk), so the loads of the next rows run under a row's
-// reduction.  Rows of more columns than a CTA holds are split over a cluster, which adds its row sums
-// in distributed shared memory; narrow rows are taken several at a time.  Column sums end as one
-// partial row per cluster, added in a fixed order by k_norm_columns: no atomics, the same bits each time.
+// its rows, so the column sums and the parameters stay in registers; rows arrive through a ring of
+// bulk copies (cp.async.bulk).  A row's phases are spread over the steps of the loop -- forward: the sum
+// over y; h' and the sum over it; n -- so that a step works on three rows (backward: two) and has one
+// barrier, behind which the sums of all of them travel: with one row at a time a CTA waited for its
+// reductions half of the time (bf16 [16384, 8192] forward 313 us).  Rows of more columns than a CTA
+// holds are split over a cluster, whose warps write their sums into every CTA's shared memory;
+// narrow rows are taken several at a time.  Column sums end as one partial row per cluster, added in
+// a fixed order by k_norm_columns: no atomics, the same bits each time.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -34,7 +37,7 @@
 namespace hq {
 
 constexpr int kNormThreads = 512;    // most threads of a CTA
-constexpr int kNormMaxStages = 4;
+constexpr int kNormMaxStages = 8;
 constexpr int kNormMaxCluster = 8;
 constexpr int kNormMaxPartials = 192;  // clusters of the backward kernel, at most
 
@@ -103,8 +106,8 @@ struct Unit {
       }
     }
   }
-  // rounds to the data type (to nearest even); f becomes the rounded values
-  __device__ __forceinline__ void set(float (&f)[8]) {
+  // rounds to the data type (to nearest even)
+  __device__ __forceinline__ void set(const float (&f)[8]) {
     if constexpr (BF16) {
       uint32_t x[4];
 #pragma unroll
@@ -113,7 +116,6 @@ struct Unit {
         x[i] = *reinterpret_cast<uint32_t*>(&b);
       }
       w[0] = make_uint4(x[0], x[1], x[2], x[3]);
-      get(f);
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -128,14 +130,10 @@ __device__ __forceinline__ float norm_param(const void* w, int64_t i, int bf16) 
   return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]) : static_cast<const float*>(w)[i];
 }
 
-// A CTA's columns of a parameter in shared memory: the first halves of all units, then the second
-// halves (16-byte reads of neighbouring threads then meet no bank twice).
-__device__ __forceinline__ void read_param(const float* s, int units, int u, float (&f)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(s)[u], b = reinterpret_cast<const float4*>(s)[units + u];
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-__device__ __forceinline__ int param_slot(int units, int col) {
-  return ((col & 4) ? 4 * units : 0) + (col >> 3) * 4 + (col & 3);
+// A unit of a parameter vector (ones where it is absent; zeros outside the row).
+__device__ __forceinline__ void param_unit(const void* w, int64_t col, int bf16, bool in, float (&f)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = in ? norm_param(w, col + e, bf16) : 0.0f;
 }
 
 // A float into the same shared variable of CTA `rank` of the cluster.
@@ -149,42 +147,44 @@ __device__ __forceinline__ void store_cluster(const float* p, uint32_t rank, flo
 
 struct NormShared {
   uint64_t full[kNormMaxStages];
-  float part[2][kNormThreads / 32][3];       // a warp's sums, by parity of the reduction
-  float cluster[2][kNormMaxCluster][3];
+  // the warps' row sums, by the parity of the step that made them: [.][rank * 16 + warp]
+  float part[2][4][kNormMaxCluster * 16];
   float most[kNormThreads / 32];
 };
 
-// The row sums of NS values over the threads of a row (tpr of them) and over the cluster; every
-// thread of the CTA calls it.  Sums are added in a fixed order.
+// This warp's sums of NS values, as sums `first` .. of a step, for every CTA of the cluster.
 template <int NS>
-__device__ __forceinline__ void row_sums(NormShared& sh, int& parity, const NormParams& p, int row, uint32_t ranks,
-                                         uint32_t rank, float (&s)[NS]) {
+__device__ __forceinline__ void put_sums(NormShared& sh, int parity, int first, uint32_t ranks, uint32_t rank,
+                                         float (&s)[NS]) {
 #pragma unroll
   for (int i = 0; i < NS; ++i)
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], m);
-  if ((threadIdx.x & 31) == 0)
+  const int lane = threadIdx.x & 31, at = static_cast<int>(rank) * 16 + (threadIdx.x >> 5);
+  if (ranks == 1) {
+    if (lane == 0)
 #pragma unroll
-    for (int i = 0; i < NS; ++i) sh.part[parity][threadIdx.x >> 5][i] = s[i];
-  __syncthreads();
-  const int warps = p.tpr >> 5;
+      for (int i = 0; i < NS; ++i) sh.part[parity][first + i][at] = s[i];
+  } else if (lane < static_cast<int>(ranks)) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) store_cluster(&sh.part[parity][first + i][at], lane, s[i]);
+  }
+}
+
+// The sums of a row of an earlier step, over its warps and the cluster, in a fixed order.
+template <int NS>
+__device__ __forceinline__ void get_sums(const NormShared& sh, int parity, int first, int warps, int row, uint32_t ranks,
+                                         float (&s)[NS]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     s[i] = 0.0f;
-    for (int w = 0; w < warps; ++w) s[i] += sh.part[parity][row * warps + w][i];
-  }
-  if (ranks > 1) {  // (one row per step)
-    if (threadIdx.x < ranks)
+    if (lane < warps)
+      for (uint32_t r = 0; r < ranks; ++r) s[i] += sh.part[parity][first + i][r * 16 + row * warps + lane];
 #pragma unroll
-      for (int i = 0; i < NS; ++i) store_cluster(&sh.cluster[parity][rank][i], threadIdx.x, s[i]);
-    cluster_sync();
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      s[i] = 0.0f;
-      for (uint32_t r = 0; r < ranks; ++r) s[i] += sh.cluster[parity][r][i];
-    }
+    for (int m = 8; m >= 1; m >>= 1) s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], m);
+    s[i] = __shfl_sync(0xFFFFFFFFu, s[i], 0);
   }
-  parity ^= 1;
 }
 
 // max |x . H_G / sqrt(G)| over one unit per lane (G = 16: two lanes; G = 256: the warp), in the
@@ -216,7 +216,9 @@ __device__ __forceinline__ float rotated_absmax(float (&f)[8], int group, int la
 }
 
 // ---------------------------------------------------------------------------
-// The ring of rows.  Stage layout: tensor t, row r of the step at (t * rows + r) * cols * es.
+// The ring of rows.  Stage layout: tensor t, row r of the step at (t * rows + r) * cols * es.  Positions
+// are kept as stage numbers that are stepped along: a division per row and thread would cost as much as
+// the row.
 // ---------------------------------------------------------------------------
 template <bool BF16, int NT>
 struct RowRing {
@@ -225,15 +227,15 @@ struct RowRing {
   uint8_t* base;
   NormShared& sh;
   int64_t first, stride;  // this cluster's first step, and the step between its steps (in steps)
-  int64_t steps;
+  int steps;
   int col0, bytes;        // bytes of a row's part
 
-  __device__ __forceinline__ int stage_bytes() const { return NT * p.rows * p.cols * kEs; }
+  __device__ __forceinline__ int tensor_bytes() const { return p.rows * p.cols * kEs; }
+  __device__ __forceinline__ int next(int s) const { return s + 1 == p.stages ? 0 : s + 1; }
 
-  // Thread 0: the copies of this cluster's step i.
-  __device__ __forceinline__ void fetch(int64_t i) const {
+  // Thread 0: the copies of this cluster's step i into stage s.
+  __device__ __forceinline__ void fetch(int i, int s) const {
     if (i >= steps) return;
-    const int s = static_cast<int>(i % p.stages);
     const uint32_t bar = smem_addr(&sh.full[s]);
     const int64_t row0 = (first + i * stride) * p.rows;
     const int n = static_cast<int>(p.M - row0 < p.rows ? p.M - row0 : p.rows);
@@ -244,69 +246,82 @@ struct RowRing {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       if (!p.in[t]) continue;
+      const uint8_t* src = p.in[t] + row0 * p.ld[t] + static_cast<int64_t>(col0) * kEs;
+      uint32_t dst = smem_addr(base) + (s * NT + t) * tensor_bytes();
       for (int r = 0; r < n; ++r) {
-        const uint8_t* src = p.in[t] + (row0 + r) * p.ld[t] + static_cast<int64_t>(col0) * kEs;
-        const uint32_t dst = smem_addr(base + s * stage_bytes() + (t * p.rows + r) * p.cols * kEs);
         asm volatile(
             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
             "l"(src), "r"(static_cast<uint32_t>(bytes)), "r"(bar)
             : "memory");
+        src += p.ld[t];
+        dst += p.cols * kEs;
       }
     }
   }
-  __device__ __forceinline__ bool wait(int64_t i) const {
-    return mbar_wait(smem_addr(&sh.full[i % p.stages]), static_cast<uint32_t>((i / p.stages) & 1));
-  }
-  __device__ __forceinline__ const uint8_t* at(int64_t i, int t, int r) const {
-    return base + (i % p.stages) * stage_bytes() + (t * p.rows + r) * p.cols * kEs;
-  }
+  __device__ __forceinline__ bool wait(int s, uint32_t phase) const { return mbar_wait(smem_addr(&sh.full[s]), phase); }
 };
 
-// What both kernels set up: the ring, the parameters' columns in shared memory, the thread's place.
-// params[0]: w_pre; params[1]: w_post, times a per-channel gate.
+// What both kernels set up: the ring, the thread's place, its units of the parameters.
+// w_pre[j], w_post[j]: the j-th unit's parameters, the latter times a per-channel gate.
 #define HQ_NORM_SETUP(NT)                                                                             \
   constexpr int kEs = BF16 ? 2 : 4;                                                                   \
   extern __shared__ __align__(128) uint8_t norm_smem[];                                               \
   __shared__ NormShared sh;                                                                           \
   const uint32_t ranks = cluster_size(), rank = cluster_rank();                                       \
-  const int units = p.cols / 8;                                                                       \
-  float* const s_pre = reinterpret_cast<float*>(norm_smem);                                           \
-  float* const s_post = s_pre + p.cols;                                                               \
   const int col0 = static_cast<int>(rank) * p.cols;                                                   \
   const int my_cols = min(p.cols, p.D - col0);                                                        \
   const int my_units = my_cols / 8;                                                                   \
   const int64_t all_steps = (p.M + p.rows - 1) / p.rows;                                              \
   const int64_t cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;                           \
-  RowRing<BF16, NT> ring{p, norm_smem + 8 * static_cast<size_t>(p.cols), sh, cluster, clusters,       \
-                         cluster < all_steps ? (all_steps - cluster + clusters - 1) / clusters : 0,   \
-                         col0, my_cols * kEs};                                                        \
+  RowRing<BF16, NT> ring{p, norm_smem, sh, cluster, clusters,                                         \
+                         static_cast<int>((all_steps - cluster + clusters - 1) / clusters), col0,     \
+                         my_cols * kEs};                                                        \
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");                                     \
   if (threadIdx.x == 0) {                                                                             \
     for (int i = 0; i < p.stages; ++i) mbar_init(smem_addr(&sh.full[i]), 1);                          \
     fence_mbar_init();                                                                                \
-    asm volatile("griddepcontrol.wait;" ::: "memory");                                                \
-    for (int i = 0; i < p.stages; ++i) ring.fetch(i);                                                 \
   }                                                                                                   \
   asm volatile("griddepcontrol.wait;" ::: "memory");                                                  \
-  for (int c = threadIdx.x; c < my_cols; c += blockDim.x) {                                           \
-    const int slot = param_slot(units, c);                                                            \
-    s_pre[slot] = norm_param(p.w_pre, col0 + c, p.params_bf16);                                       \
-    float w = norm_param(p.post ? p.w_post : nullptr, col0 + c, p.params_bf16);                       \
-    if (p.gate_kind == kGateChannel) w = __fmul_rn(w, norm_param(p.gate, col0 + c, p.params_bf16));   \
-    s_post[slot] = w;                                                                                 \
+  if (threadIdx.x == 0)                                                                               \
+    for (int i = 0; i < p.stages; ++i) ring.fetch(i, i);                                              \
+  const int row = threadIdx.x / p.tpr, lane_u = threadIdx.x - row * p.tpr, warps = p.tpr >> 5;        \
+  float w_pre[V][8], w_post[V][8];                                                                    \
+  bool in[V];                                                                                         \
+  _Pragma("unroll") for (int j = 0; j < V; ++j) {                                                     \
+    const int u = j * p.tpr + lane_u;                                                                 \
+    in[j] = u < my_units;                                                                             \
+    param_unit(p.w_pre, col0 + u * 8, p.params_bf16, in[j], w_pre[j]);                                \
+    param_unit(p.post ? p.w_post : nullptr, col0 + u * 8, p.params_bf16, in[j], w_post[j]);           \
+    if (p.gate_kind == kGateChannel) {                                                                \
+      float g[8];                                                                                     \
+      param_unit(p.gate, col0 + u * 8, p.params_bf16, in[j], g);                                      \
+      _Pragma("unroll") for (int e = 0; e < 8; ++e) w_post[j][e] = __fmul_rn(w_post[j][e], g[e]);     \
+    }                                                                                                 \
   }                                                                                                   \
-  const int row = threadIdx.x / p.tpr, lane_u = threadIdx.x - row * p.tpr;                            \
-  int parity = 0;                                                                                     \
+  const float inv_d = __fdiv_rn(1.0f, static_cast<float>(p.D));                                       \
+  /* of a row in the ring: this thread's first unit of tensor 0 in stage 0; from there on, bytes */   \
+  const uint8_t* const units0 = ring.base + row * p.cols * kEs + lane_u * 8 * kEs;                    \
+  const int tensor = ring.tensor_bytes(), unit = p.tpr * 8 * kEs;                                     \
+  /* of the row of a step in an [M, D] tensor: bytes from one step to the next */                     \
+  const int64_t row_step = ring.stride * p.rows * p.D * kEs;                                          \
+  int s0 = 0, s1 = 0; /* the stages of this step's row and of the one before */                       \
+  uint32_t phase = 0;                                                                                 \
   bool ok = true;                                                                                     \
   __syncthreads();                                                                                    \
   if (ranks > 1) cluster_sync() /* the peers' shared memory is there */
+
+// The barrier of a step: sums put before it can be got after it.
+__device__ __forceinline__ void step_sync(uint32_t ranks) {
+  if (ranks > 1) cluster_sync();
+  else __syncthreads();
+}
 
 // After the last step: report a wait that ran out, with the copies in flight given time to land.
 #define HQ_NORM_FINISH()                                                                              \
   if (!ok) {                                                                                          \
     if (threadIdx.x == 0)                                                                             \
-      for (int64_t i = ring.steps > p.stages ? ring.steps - p.stages : 0; i < ring.steps; ++i)        \
-        ring.wait(i);                                                                                 \
+      for (int i = ring.steps > p.stages ? ring.steps - p.stages : 0; i < ring.steps; ++i)            \
+        ring.wait(i % p.stages, (i / p.stages) & 1);                                                  \
     if ((threadIdx.x & 31) == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);                            \
   }
 
@@ -314,100 +329,112 @@ template <bool BF16, int V>
 __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_constant__ NormParams p) {
   HQ_NORM_SETUP(2);
   float most = 0.0f;
-  for (int64_t i = 0; i < ring.steps; ++i) {
-    const int64_t m = (ring.first + i * ring.stride) * p.rows + row;
-    const bool live = m < p.M;
-    ok = ok && ring.wait(i);
-    Unit<BF16> hu[V], yu[V];
-    float ss[1] = {0.0f};
+  float t[V][8];  // h' of the row before
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int u = j * p.tpr + lane_u;
-      hu[j].zero(), yu[j].zero();
-      if (live && u < my_units) {
-        hu[j].load(ring.at(i, 0, row) + u * 8 * kEs);
-        if (p.has_y) yu[j].load(ring.at(i, 1, row) + u * 8 * kEs);
-      }
+  for (int j = 0; j < V; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[j][e] = 0.0f;
+  const int64_t stride = ring.stride * p.rows;
+  int64_t m0 = ring.first * p.rows + row;  // row of step i
+  // this thread's first unit of the output rows of steps i - 1 and i - 2
+  int64_t at1 = ((m0 - stride) * p.D + col0 + lane_u * 8) * kEs;
+  // Step i: the sum over y of its i-th row; h' of row i - 1; n of row i - 2.
+  for (int i = 0; i < ring.steps + 2; ++i) {
+    const int parity = i & 1;
+    const int64_t m1 = m0 - stride, m2 = m1 - stride;
+    const bool live1 = i >= 1 && i <= ring.steps && m1 < p.M, live2 = i >= 2 && m2 < p.M;
+    float gate = 1.0f;
+    if (p.gate_kind == kGateToken && live1) gate = norm_param(p.gate, m1, p.params_bf16);
+    if (i < ring.steps) {
+      ok = ok && ring.wait(s0, phase);
       if (p.post) {
-        float y[8];
-        yu[j].get(y);
+        float ss[1] = {0.0f};
+        const uint8_t* src = units0 + (s0 * 2 + 1) * tensor;
+        if (m0 < p.M)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss[0] = fmaf(y[e], y[e], ss[0]);
+          for (int j = 0; j < V; ++j)
+            if (in[j]) {
+              Unit<BF16> yu;
+              float y[8];
+              yu.load(src + j * unit);
+              yu.get(y);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) ss[0] = fmaf(y[e], y[e], ss[0]);
+            }
+        put_sums<1>(sh, parity, 0, ranks, rank, ss);
       }
     }
-    float r_post = 1.0f;
-    if (p.post) {
-      row_sums<1>(sh, parity, p, row, ranks, rank, ss);
-      r_post = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss[0], static_cast<float>(p.D)), p.eps));
-    } else {
-      __syncthreads();
-    }
-    if (threadIdx.x == 0) {  // every thread has its part of the stage in registers
-      fence_proxy_async_smem();
-      ring.fetch(i + p.stages);
-    }
-    if (p.post && live && lane_u == 0 && rank == 0) p.r_post[m] = r_post;
-    if (p.gate_kind == kGateToken && live) r_post *= norm_param(p.gate, m, p.params_bf16);
-    float t[V][8];
-    ss[0] = 0.0f;
+    if (p.pre && i >= 2) {  // n of row i - 2, from t
+      float ss[1];
+      get_sums<1>(sh, parity ^ 1, 1, warps, row, ranks, ss);
+      const float r_pre = rsqrtf(fmaf(ss[0], inv_d, p.eps));
+      if (live2 && lane_u == 0 && rank == 0) p.r_pre[m2] = r_pre;
+      uint8_t* const dst = static_cast<uint8_t*>(p.n) + (at1 - row_step);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int u = j * p.tpr + lane_u;
-      const bool in = live && u < my_units;
-      hu[j].get(t[j]);
-      if (p.has_y) {
-        float y[8], w[8];
-        yu[j].get(y);
-        if (in) read_param(s_post, units, u, w);
-        else
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = 0.0f;
-        if (p.gate_kind == kGateFull && in) {
-          Unit<BF16> gu;
-          float g[8];
-          gu.load(static_cast<const uint8_t*>(p.gate) + m * p.ld_gate + static_cast<int64_t>(col0 + u * 8) * kEs);
-          gu.get(g);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] *= g[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t[j][e] = fmaf(y[e] * r_post, w[e], p.alpha * t[j][e]);
-        if (in) {
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = t[j][e];
-          Unit<BF16> o;
-          o.set(f);
-          o.store(static_cast<uint8_t*>(p.h_out) + (m * p.D + col0 + u * 8) * kEs);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss[0] = fmaf(t[j][e], t[j][e], ss[0]);
-    }
-    if (!p.pre) continue;
-    row_sums<1>(sh, parity, p, row, ranks, rank, ss);
-    const float r_pre = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss[0], static_cast<float>(p.D)), p.eps));
-    if (live && lane_u == 0 && rank == 0) p.r_pre[m] = r_pre;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int u = j * p.tpr + lane_u;
-      const bool in = live && u < my_units;
-      float f[8];
-      if (in) {
-        read_param(s_pre, units, u, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= t[j][e] * r_pre;
+      for (int j = 0; j < V; ++j) {
+        float f[8];
         Unit<BF16> o;
-        o.set(f);
-        o.store(static_cast<uint8_t*>(p.n) + (m * p.D + col0 + u * 8) * kEs);
-      }
-      if (p.group >= 0) {  // (uniform over the grid: every lane takes part in the exchange)
-        if (!in)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = 0.0f;
-        most = max_nan(most, rotated_absmax(f, p.group, threadIdx.x & 31));
+        for (int e = 0; e < 8; ++e) f[e] = t[j][e] * r_pre * w_pre[j][e];
+        o.set(f);
+        if (live2 && in[j]) o.store(dst + j * unit);
+        if (p.group >= 0) {  // (the same for the grid: every lane takes part in the exchange; t is 0 outside)
+          o.get(f);
+          most = max_nan(most, rotated_absmax(f, p.group, threadIdx.x & 31));
+        }
       }
     }
+    if (i >= 1 && i <= ring.steps) {  // h' of row i - 1
+      float r_post = 1.0f, ss[1];
+      if (p.post) {
+        get_sums<1>(sh, parity ^ 1, 0, warps, row, ranks, ss);
+        r_post = rsqrtf(fmaf(ss[0], inv_d, p.eps));
+        if (live1 && lane_u == 0 && rank == 0) p.r_post[m1] = r_post;
+      }
+      r_post *= gate;
+      ss[0] = 0.0f;
+      const uint8_t* src = units0 + s1 * 2 * tensor;
+      uint8_t* const dst = static_cast<uint8_t*>(p.h_out) + at1;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        if (!live1 || !in[j]) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t[j][e] = 0.0f;
+          continue;
+        }
+        Unit<BF16> x;
+        x.load(src + j * unit);
+        x.get(t[j]);
+        if (p.has_y) {
+          float y[8], g[8];
+          x.load(src + tensor + j * unit);
+          x.get(y);
+          if (p.gate_kind == kGateFull) {
+            x.load(static_cast<const uint8_t*>(p.gate) + m1 * p.ld_gate + (col0 + lane_u * 8) * kEs + j * unit);
+            x.get(g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] *= g[e];
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t[j][e] = fmaf(y[e] * r_post, w_post[j][e], p.alpha * t[j][e]);
+          x.set(t[j]);
+          x.store(dst + j * unit);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss[0] = fmaf(t[j][e], t[j][e], ss[0]);
+      }
+      if (p.pre) put_sums<1>(sh, parity, 1, ranks, rank, ss);
+    }
+    step_sync(ranks);
+    if (threadIdx.x == 0 && i >= 1) {  // row i - 1 has left its stage
+      fence_proxy_async_smem();
+      ring.fetch(i - 1 + p.stages, s1);
+    }
+    m0 += stride;
+    at1 += row_step;
+    s1 = s0;
+    s0 = ring.next(s0);
+    if (s0 == 0) phase ^= 1;
   }
   if (p.group >= 0) {
 #pragma unroll
@@ -420,7 +447,6 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
     }
   }
   HQ_NORM_FINISH();
-  if (ranks > 1) cluster_sync();
 }
 
 template <bool BF16, int V>
@@ -431,103 +457,141 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
   for (int j = 0; j < V; ++j)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum_w[j][e] = sum_a[j][e] = 0.0f;
-  const float inv_d = __fdiv_rn(1.0f, static_cast<float>(p.D));
-  for (int64_t i = 0; i < ring.steps; ++i) {
-    const int64_t m = (ring.first + i * ring.stride) * p.rows + row;
-    const bool live = m < p.M;
-    ok = ok && ring.wait(i);
-    const float r_pre = p.pre && live ? __ldg(p.r_pre_in + m) : 0.0f;
-    const float r_post = p.post && live ? __ldg(p.r_post_in + m) : 1.0f;
-    const float tok = p.gate_kind == kGateToken && live ? norm_param(p.gate, m, p.params_bf16) : 1.0f;
-    // hu: h'; nu: dn; du: dh'; yu: y
-    Unit<BF16> hu[V], nu[V], du[V], yu[V], gu[V];
-    float s[3] = {0.0f, 0.0f, 0.0f};
+  struct RowScalars {
+    float r_pre, r_post, tok;
+  };
+  auto scalars = [&](int i, int64_t m) {
+    const bool live = i < ring.steps && m < p.M;
+    return RowScalars{p.pre && live ? __ldg(p.r_pre_in + m) : 0.0f, p.post && live ? __ldg(p.r_post_in + m) : 1.0f,
+                      p.gate_kind == kGateToken && live ? norm_param(p.gate, m, p.params_bf16) : 1.0f};
+  };
+  const int64_t stride = ring.stride * p.rows;
+  int64_t m0 = ring.first * p.rows + row;  // row of step i
+  int64_t at1 = ((m0 - stride) * p.D + col0 + lane_u * 8) * kEs;  // this thread's first unit of row i - 1
+  RowScalars next = scalars(0, m0), now = next, before = next;
+  // Step i: the sums of its i-th row; the gradients of row i - 1.
+  for (int i = 0; i < ring.steps + 1; ++i) {
+    const int parity = i & 1;
+    const int64_t m1 = m0 - stride;
+    before = now;
+    now = next;
+    next = scalars(i + 1, m0 + stride);
+    if (i < ring.steps) {
+      ok = ok && ring.wait(s0, phase);
+      float s[3] = {0.0f, 0.0f, 0.0f};
+      const uint8_t* src = units0 + s0 * 4 * tensor;
+      if (m0 < p.M)
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int u = j * p.tpr + lane_u;
-      hu[j].zero(), nu[j].zero(), du[j].zero(), yu[j].zero();
-      if (live && u < my_units) {
-        if (p.pre) hu[j].load(ring.at(i, 0, row) + u * 8 * kEs), nu[j].load(ring.at(i, 1, row) + u * 8 * kEs);
-        if (p.in[2]) du[j].load(ring.at(i, 2, row) + u * 8 * kEs);
-        float h[8], n[8], w[8];
-        hu[j].get(h), nu[j].get(n);
-        read_param(s_pre, units, u, w);
-        if (p.has_y) {
-          yu[j].load(ring.at(i, 3, row) + u * 8 * kEs);
-          float d[8], y[8], q[8];
-          du[j].get(d), yu[j].get(y);
-          read_param(s_post, units, u, q);
+        for (int j = 0; j < V; ++j) {
+          if (!in[j]) continue;
+          Unit<BF16> x;
+          float h[8], n[8];
+          x.zero();
+          if (p.pre) x.load(src + j * unit);
+          x.get(h);
+          if (p.pre) x.load(src + tensor + j * unit);
+          x.get(n);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            sum_w[j][e] = fmaf(n[e] * now.r_pre, h[e], sum_w[j][e]);
+            n[e] *= w_pre[j][e];
+            s[0] = fmaf(n[e], h[e], s[0]);
+          }
+          if (!p.has_y) continue;
+          float d[8], y[8];
+          x.zero();
+          if (p.in[2]) x.load(src + 2 * tensor + j * unit);
+          x.get(d);
+          x.load(src + 3 * tensor + j * unit);
+          x.get(y);
           if (p.gate_kind == kGateFull) {
-            gu[j].load(static_cast<const uint8_t*>(p.gate) + m * p.ld_gate + static_cast<int64_t>(col0 + u * 8) * kEs);
             float g[8];
-            gu[j].get(g);
+            x.load(static_cast<const uint8_t*>(p.gate) + m0 * p.ld_gate + (col0 + lane_u * 8) * kEs + j * unit);
+            x.get(g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] *= g[e];
+            for (int e = 0; e < 8; ++e) y[e] *= g[e];
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float gn = n[e] * w[e], qy = q[e] * y[e];
-            s[0] = fmaf(gn, h[e], s[0]);
-            s[1] = fmaf(fmaf(r_pre, gn, d[e]), qy, s[1]);
-            s[2] = fmaf(h[e], qy, s[2]);
+            const float q = w_post[j][e] * y[e];
+            s[1] = fmaf(fmaf(now.r_pre, n[e], d[e]), q, s[1]);
+            s[2] = fmaf(h[e], q, s[2]);
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s[0] = fmaf(n[e] * w[e], h[e], s[0]);
         }
-      }
+      put_sums<3>(sh, parity, 0, ranks, rank, s);
     }
-    row_sums<3>(sh, parity, p, row, ranks, rank, s);
-    if (threadIdx.x == 0) {  // every thread has its part of the stage in registers
+    if (i >= 1) {
+      float s[3];
+      get_sums<3>(sh, parity ^ 1, 0, warps, row, ranks, s);
+      const float r_pre = before.r_pre, r_post = before.r_post, tok = before.tok;
+      const float k1 = r_pre * r_pre * r_pre * (s[0] * inv_d);
+      const float dot = fmaf(-k1, s[2], s[1]);  // sum d q (a per-token gate left out)
+      const float k2 = r_post * r_post * r_post * (tok * dot * inv_d);
+      if (p.gate_kind == kGateToken && m1 < p.M && lane_u == 0 && rank == 0)
+        static_cast<float*>(p.dgate)[m1] = dot * r_post;
+      const uint8_t* src = units0 + s1 * 4 * tensor;
+      if (m1 < p.M)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          if (!in[j]) continue;
+          Unit<BF16> x;
+          float d[8], v[8], o[8];
+          x.zero();
+          if (p.in[2]) x.load(src + 2 * tensor + j * unit);
+          x.get(d);
+          if (p.pre) {
+            x.load(src + tensor + j * unit);
+            x.get(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] = fmaf(r_pre, v[e] * w_pre[j][e], d[e]);
+            x.load(src + j * unit);
+            x.get(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] = fmaf(-v[e], k1, d[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = p.alpha * d[e];
+          x.set(o);
+          x.store(static_cast<uint8_t*>(p.dh) + at1 + j * unit);
+          if (!p.has_y) continue;
+          x.load(src + 3 * tensor + j * unit);
+          x.get(v);
+          if (p.gate_kind == kGateFull) {
+            float g[8];
+            x.load(static_cast<const uint8_t*>(p.gate) + m1 * p.ld_gate + (col0 + lane_u * 8) * kEs + j * unit);
+            x.get(g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              o[e] = d[e] * (w_post[j][e] * v[e] * r_post);
+              d[e] *= g[e];
+            }
+            x.set(o);
+            x.store(static_cast<uint8_t*>(p.dgate) + at1 + j * unit);
+          }
+          const float dr = tok * r_post;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            sum_a[j][e] = fmaf(d[e] * dr, v[e], sum_a[j][e]);
+            o[e] = d[e] * w_post[j][e];
+          }
+          // (without the post norm r_post is 1 and k2 has no place)
+          const float k = p.post ? k2 : 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = fmaf(dr, o[e], -v[e] * k);
+          x.set(o);
+          x.store(static_cast<uint8_t*>(p.dy) + at1 + j * unit);
+        }
+    }
+    step_sync(ranks);
+    if (threadIdx.x == 0 && i >= 1) {  // row i - 1 has left its stage
       fence_proxy_async_smem();
-      ring.fetch(i + p.stages);
+      ring.fetch(i - 1 + p.stages, s1);
     }
-    const float k1 = r_pre * r_pre * r_pre * (s[0] * inv_d);
-    const float dot = fmaf(-k1, s[2], s[1]);  // sum d q (a per-token gate left out)
-    const float k2 = r_post * r_post * r_post * (tok * dot * inv_d);
-    if (p.gate_kind == kGateToken && live && lane_u == 0 && rank == 0) static_cast<float*>(p.dgate)[m] = dot * r_post;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int u = j * p.tpr + lane_u;
-      if (!live || u >= my_units) continue;
-      const int64_t at = (m * p.D + col0 + u * 8) * kEs;
-      float h[8], n[8], d[8], w[8], o[8];
-      hu[j].get(h), nu[j].get(n), du[j].get(d);
-      read_param(s_pre, units, u, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sum_w[j][e] = fmaf(n[e] * r_pre, h[e], sum_w[j][e]);
-        d[e] = fmaf(-h[e], k1, fmaf(r_pre, n[e] * w[e], d[e]));
-        o[e] = p.alpha * d[e];
-      }
-      Unit<BF16> out;
-      out.set(o);
-      out.store(static_cast<uint8_t*>(p.dh) + at);
-      if (!p.has_y) continue;
-      float y[8];
-      yu[j].get(y);
-      read_param(s_post, units, u, w);
-      if (p.gate_kind == kGateFull) {
-        float g[8];
-        gu[j].get(g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          o[e] = d[e] * (w[e] * y[e] * r_post);
-          d[e] *= g[e];
-        }
-        out.set(o);
-        out.store(static_cast<uint8_t*>(p.dgate) + at);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        d[e] *= tok;
-        sum_a[j][e] = fmaf(d[e] * r_post, y[e], sum_a[j][e]);
-        o[e] = d[e] * w[e];
-        if (p.post) o[e] = fmaf(r_post, o[e], -y[e] * k2);
-      }
-      out.set(o);
-      out.store(static_cast<uint8_t*>(p.dy) + at);
-    }
+    m0 += stride;
+    at1 += row_step;
+    s1 = s0;
+    s0 = ring.next(s0);
+    if (s0 == 0) phase ^= 1;
   }
   HQ_NORM_FINISH();
   // The rows of a step add their column sums one after another; the ring is free now.
@@ -537,23 +601,20 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
     if (r != row) continue;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int u = j * p.tpr + lane_u;
-      if (u >= my_units) continue;
+      if (!in[j]) continue;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int slot = param_slot(units, u * 8 + e);
-        s_sum[slot] = (r ? s_sum[slot] : 0.0f) + sum_w[j][e];
-        s_sum[p.cols + slot] = (r ? s_sum[p.cols + slot] : 0.0f) + sum_a[j][e];
+        const int c = (j * p.tpr + lane_u) * 8 + e;
+        s_sum[c] = (r ? s_sum[c] : 0.0f) + sum_w[j][e];
+        s_sum[p.cols + c] = (r ? s_sum[p.cols + c] : 0.0f) + sum_a[j][e];
       }
     }
   }
   __syncthreads();
   for (int c = threadIdx.x; c < my_cols; c += blockDim.x) {
-    const int slot = param_slot(units, c);
-    p.partial[cluster * p.D + col0 + c] = s_sum[slot];
-    p.partial[(clusters + cluster) * p.D + col0 + c] = s_sum[p.cols + slot];
+    p.partial[cluster * p.D + col0 + c] = s_sum[c];
+    p.partial[(clusters + cluster) * p.D + col0 + c] = s_sum[p.cols + c];
   }
-  if (ranks > 1) cluster_sync();
 }
 
 // The clusters' partial column sums, added in a fixed order; dw_post = gate A, dgate = w_post A.
