@@ -175,10 +175,17 @@ hq_status hq_block_norm(const void* h, int64_t ld_h, const void* y, int64_t ld_y
   p.stages = s.stages;
   if (amax && (e = cudaMemsetAsync(amax, 0, 4, cs)) != cudaSuccess) return cuda_fail(e);
   const int n_cl = clusters_of(s, M, sms);
+  const bool plain = post && pre && y && !amax && (gate_kind == HQ_GATE_NONE || gate_kind == HQ_GATE_CHANNEL);
   if (dtype == HQ_BF16)
-    e = s.units == 1 ? launch(hq::k_block_norm<true, 1>, p, s, n_cl, cs) : launch(hq::k_block_norm<true, 2>, p, s, n_cl, cs);
+    e = plain ? (s.units == 1 ? launch(hq::k_block_norm<true, 1, true>, p, s, n_cl, cs)
+                              : launch(hq::k_block_norm<true, 2, true>, p, s, n_cl, cs))
+              : (s.units == 1 ? launch(hq::k_block_norm<true, 1, false>, p, s, n_cl, cs)
+                              : launch(hq::k_block_norm<true, 2, false>, p, s, n_cl, cs));
   else
-    e = s.units == 1 ? launch(hq::k_block_norm<false, 1>, p, s, n_cl, cs) : launch(hq::k_block_norm<false, 2>, p, s, n_cl, cs);
+    e = plain ? (s.units == 1 ? launch(hq::k_block_norm<false, 1, true>, p, s, n_cl, cs)
+                              : launch(hq::k_block_norm<false, 2, true>, p, s, n_cl, cs))
+              : (s.units == 1 ? launch(hq::k_block_norm<false, 1, false>, p, s, n_cl, cs)
+                              : launch(hq::k_block_norm<false, 2, false>, p, s, n_cl, cs));
   return e == cudaSuccess ? HQ_OK : cuda_fail(e);
 }
 
@@ -254,11 +261,15 @@ hq_status hq_block_norm_bwd(const void* dh_out, int64_t ld_dh, const void* dn, i
   p.rows = s.rows;
   p.stages = s.stages;
   const int n_cl = clusters_of(s, M, sms);
+  const bool plain = post && pre && dh_out && (gate_kind == HQ_GATE_NONE || gate_kind == HQ_GATE_CHANNEL);
   if (dtype == HQ_BF16)
-    e = s.units == 1 ? launch(hq::k_block_norm_bwd<true, 1>, p, s, n_cl, cs)
-                     : launch(hq::k_block_norm_bwd<true, 2>, p, s, n_cl, cs);
+    e = plain ? (s.units == 1 ? launch(hq::k_block_norm_bwd<true, 1, true>, p, s, n_cl, cs)
+                              : launch(hq::k_block_norm_bwd<true, 2, true>, p, s, n_cl, cs))
+              : (s.units == 1 ? launch(hq::k_block_norm_bwd<true, 1, false>, p, s, n_cl, cs)
+                              : launch(hq::k_block_norm_bwd<true, 2, false>, p, s, n_cl, cs));
   else  // at most 4096 columns per CTA: one unit per thread
-    e = launch(hq::k_block_norm_bwd<false, 1>, p, s, n_cl, cs);
+    e = plain ? launch(hq::k_block_norm_bwd<false, 1, true>, p, s, n_cl, cs)
+              : launch(hq::k_block_norm_bwd<false, 1, false>, p, s, n_cl, cs);
   if (e != cudaSuccess) return cuda_fail(e);
   float* const to_pre = pre ? dw_pre : nullptr;
   float* const to_post = post ? dw_post : nullptr;

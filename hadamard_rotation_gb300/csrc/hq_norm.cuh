@@ -90,40 +90,40 @@ struct Unit {
 #pragma unroll
     for (int i = 0; i < (BF16 ? 1 : 2); ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
+  // values 2 i and 2 i + 1 in f[i]
+  __device__ __forceinline__ void get(float2 (&f)[4]) const {
     if constexpr (BF16) {
       const uint32_t x[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(x[i] << 16);
-        f[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
-      }
+      for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        f[4 * i] = __uint_as_float(w[i].x), f[4 * i + 1] = __uint_as_float(w[i].y);
-        f[4 * i + 2] = __uint_as_float(w[i].z), f[4 * i + 3] = __uint_as_float(w[i].w);
+        f[2 * i] = make_float2(__uint_as_float(w[i].x), __uint_as_float(w[i].y));
+        f[2 * i + 1] = make_float2(__uint_as_float(w[i].z), __uint_as_float(w[i].w));
       }
     }
   }
   // rounds to the data type (to nearest even)
-  __device__ __forceinline__ void set(const float (&f)[8]) {
+  __device__ __forceinline__ void set(const float2 (&f)[4]) {
     if constexpr (BF16) {
       uint32_t x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        __nv_bfloat162 b = __floats2bfloat162_rn(f[i].x, f[i].y);
         x[i] = *reinterpret_cast<uint32_t*>(&b);
       }
       w[0] = make_uint4(x[0], x[1], x[2], x[3]);
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        w[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
-                          __float_as_uint(f[4 * i + 3]));
+        w[i] = make_uint4(__float_as_uint(f[2 * i].x), __float_as_uint(f[2 * i].y), __float_as_uint(f[2 * i + 1].x),
+                          __float_as_uint(f[2 * i + 1].y));
     }
   }
 };
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 __device__ __forceinline__ float norm_param(const void* w, int64_t i, int bf16) {
   if (!w) return 1.0f;
@@ -131,9 +131,10 @@ __device__ __forceinline__ float norm_param(const void* w, int64_t i, int bf16) 
 }
 
 // A unit of a parameter vector (ones where it is absent; zeros outside the row).
-__device__ __forceinline__ void param_unit(const void* w, int64_t col, int bf16, bool in, float (&f)[8]) {
+__device__ __forceinline__ void param_unit(const void* w, int64_t col, int bf16, bool in, float2 (&f)[4]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = in ? norm_param(w, col + e, bf16) : 0.0f;
+  for (int e = 0; e < 4; ++e)
+    f[e] = in ? make_float2(norm_param(w, col + 2 * e, bf16), norm_param(w, col + 2 * e + 1, bf16)) : both(0.0f);
 }
 
 // A float into the same shared variable of CTA `rank` of the cluster.
@@ -189,7 +190,10 @@ __device__ __forceinline__ void get_sums(const NormShared& sh, int parity, int f
 
 // max |x . H_G / sqrt(G)| over one unit per lane (G = 16: two lanes; G = 256: the warp), in the
 // butterfly order of the quantizer: stages h = 1, 2, 4, ... G / 2, then the scale.
-__device__ __forceinline__ float rotated_absmax(float (&f)[8], int group, int lane) {
+__device__ __forceinline__ float rotated_absmax(const float2 (&v)[4], int group, int lane) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[2 * i] = v[i].x, f[2 * i + 1] = v[i].y;
   if (group) {
 #pragma unroll
     for (int h = 1; h < 8; h <<= 1)
@@ -285,7 +289,7 @@ struct RowRing {
   if (threadIdx.x == 0)                                                                               \
     for (int i = 0; i < p.stages; ++i) ring.fetch(i, i);                                              \
   const int row = threadIdx.x / p.tpr, lane_u = threadIdx.x - row * p.tpr, warps = p.tpr >> 5;        \
-  float w_pre[V][8], w_post[V][8];                                                                    \
+  float2 w_pre[V][4], w_post[V][4];                                                                   \
   bool in[V];                                                                                         \
   _Pragma("unroll") for (int j = 0; j < V; ++j) {                                                     \
     const int u = j * p.tpr + lane_u;                                                                 \
@@ -293,11 +297,13 @@ struct RowRing {
     param_unit(p.w_pre, col0 + u * 8, p.params_bf16, in[j], w_pre[j]);                                \
     param_unit(p.post ? p.w_post : nullptr, col0 + u * 8, p.params_bf16, in[j], w_post[j]);           \
     if (p.gate_kind == kGateChannel) {                                                                \
-      float g[8];                                                                                     \
+      float2 g[4];                                                                                    \
       param_unit(p.gate, col0 + u * 8, p.params_bf16, in[j], g);                                      \
-      _Pragma("unroll") for (int e = 0; e < 8; ++e) w_post[j][e] = __fmul_rn(w_post[j][e], g[e]);     \
+      _Pragma("unroll") for (int e = 0; e < 4; ++e) w_post[j][e] = mul2(w_post[j][e], g[e]);          \
     }                                                                                                 \
   }                                                                                                   \
+  const bool post = PLAIN || p.post, pre = PLAIN || p.pre, has_y = PLAIN || p.has_y;                  \
+  const bool by_token = !PLAIN && p.gate_kind == kGateToken, full = !PLAIN && p.gate_kind == kGateFull; \
   const float inv_d = __fdiv_rn(1.0f, static_cast<float>(p.D));                                       \
   /* of a row in the ring: this thread's first unit of tensor 0 in stage 0; from there on, bytes */   \
   const uint8_t* const units0 = ring.base + row * p.cols * kEs + lane_u * 8 * kEs;                    \
@@ -325,15 +331,17 @@ __device__ __forceinline__ void step_sync(uint32_t ranks) {
     if ((threadIdx.x & 31) == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);                            \
   }
 
-template <bool BF16, int V>
+// PLAIN: both norms, y, no gate or one per channel, no amax -- known to the compiler, which then has no
+// branch in the loop (bf16 [16384, 8192] forward 235 us without).
+template <bool BF16, int V, bool PLAIN>
 __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_constant__ NormParams p) {
   HQ_NORM_SETUP(2);
   float most = 0.0f;
-  float t[V][8];  // h' of the row before
+  float2 t[V][4];  // h' of the row before
 #pragma unroll
   for (int j = 0; j < V; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) t[j][e] = 0.0f;
+    for (int e = 0; e < 4; ++e) t[j][e] = both(0.0f);
   const int64_t stride = ring.stride * p.rows;
   int64_t m0 = ring.first * p.rows + row;  // row of step i
   // this thread's first unit of the output rows of steps i - 1 and i - 2
@@ -344,27 +352,28 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
     const int64_t m1 = m0 - stride, m2 = m1 - stride;
     const bool live1 = i >= 1 && i <= ring.steps && m1 < p.M, live2 = i >= 2 && m2 < p.M;
     float gate = 1.0f;
-    if (p.gate_kind == kGateToken && live1) gate = norm_param(p.gate, m1, p.params_bf16);
+    if (by_token && live1) gate = norm_param(p.gate, m1, p.params_bf16);
     if (i < ring.steps) {
       ok = ok && ring.wait(s0, phase);
-      if (p.post) {
-        float ss[1] = {0.0f};
+      if (post) {
+        float2 sq = both(0.0f);
         const uint8_t* src = units0 + (s0 * 2 + 1) * tensor;
         if (m0 < p.M)
 #pragma unroll
           for (int j = 0; j < V; ++j)
             if (in[j]) {
               Unit<BF16> yu;
-              float y[8];
+              float2 y[4];
               yu.load(src + j * unit);
               yu.get(y);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) ss[0] = fmaf(y[e], y[e], ss[0]);
+              for (int e = 0; e < 4; ++e) sq = fma2(y[e], y[e], sq);
             }
+        float ss[1] = {sq.x + sq.y};
         put_sums<1>(sh, parity, 0, ranks, rank, ss);
       }
     }
-    if (p.pre && i >= 2) {  // n of row i - 2, from t
+    if (pre && i >= 2) {  // n of row i - 2, from t
       float ss[1];
       get_sums<1>(sh, parity ^ 1, 1, warps, row, ranks, ss);
       const float r_pre = rsqrtf(fmaf(ss[0], inv_d, p.eps));
@@ -372,13 +381,13 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
       uint8_t* const dst = static_cast<uint8_t*>(p.n) + (at1 - row_step);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        float f[8];
+        float2 f[4];
         Unit<BF16> o;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = t[j][e] * r_pre * w_pre[j][e];
+        for (int e = 0; e < 4; ++e) f[e] = mul2(mul2(t[j][e], both(r_pre)), w_pre[j][e]);
         o.set(f);
         if (live2 && in[j]) o.store(dst + j * unit);
-        if (p.group >= 0) {  // (the same for the grid: every lane takes part in the exchange; t is 0 outside)
+        if (!PLAIN && p.group >= 0) {  // (the same for the grid: every lane takes part in the exchange; t is 0 outside)
           o.get(f);
           most = max_nan(most, rotated_absmax(f, p.group, threadIdx.x & 31));
         }
@@ -386,44 +395,46 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
     }
     if (i >= 1 && i <= ring.steps) {  // h' of row i - 1
       float r_post = 1.0f, ss[1];
-      if (p.post) {
+      if (post) {
         get_sums<1>(sh, parity ^ 1, 0, warps, row, ranks, ss);
         r_post = rsqrtf(fmaf(ss[0], inv_d, p.eps));
         if (live1 && lane_u == 0 && rank == 0) p.r_post[m1] = r_post;
       }
       r_post *= gate;
-      ss[0] = 0.0f;
+      float2 sq = both(0.0f);
       const uint8_t* src = units0 + s1 * 2 * tensor;
       uint8_t* const dst = static_cast<uint8_t*>(p.h_out) + at1;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         if (!live1 || !in[j]) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t[j][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) t[j][e] = both(0.0f);
           continue;
         }
         Unit<BF16> x;
         x.load(src + j * unit);
         x.get(t[j]);
-        if (p.has_y) {
-          float y[8], g[8];
+        if (has_y) {
+          float2 y[4], g[4];
           x.load(src + tensor + j * unit);
           x.get(y);
-          if (p.gate_kind == kGateFull) {
+          if (full) {
             x.load(static_cast<const uint8_t*>(p.gate) + m1 * p.ld_gate + (col0 + lane_u * 8) * kEs + j * unit);
             x.get(g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= g[e];
+            for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], g[e]);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t[j][e] = fmaf(y[e] * r_post, w_post[j][e], p.alpha * t[j][e]);
+          for (int e = 0; e < 4; ++e)
+            t[j][e] = fma2(mul2(y[e], both(r_post)), w_post[j][e], mul2(both(p.alpha), t[j][e]));
           x.set(t[j]);
           x.store(dst + j * unit);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss[0] = fmaf(t[j][e], t[j][e], ss[0]);
+        for (int e = 0; e < 4; ++e) sq = fma2(t[j][e], t[j][e], sq);
       }
-      if (p.pre) put_sums<1>(sh, parity, 1, ranks, rank, ss);
+      ss[0] = sq.x + sq.y;
+      if (pre) put_sums<1>(sh, parity, 1, ranks, rank, ss);
     }
     step_sync(ranks);
     if (threadIdx.x == 0 && i >= 1) {  // row i - 1 has left its stage
@@ -436,7 +447,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
     s0 = ring.next(s0);
     if (s0 == 0) phase ^= 1;
   }
-  if (p.group >= 0) {
+  if (!PLAIN && p.group >= 0) {
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) most = max_nan(most, __shfl_xor_sync(0xFFFFFFFFu, most, m));
     if ((threadIdx.x & 31) == 0) sh.most[threadIdx.x >> 5] = most;
@@ -449,21 +460,22 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
   HQ_NORM_FINISH();
 }
 
-template <bool BF16, int V>
+// PLAIN: both norms, y, dh', no gate or one per channel.
+template <bool BF16, int V, bool PLAIN>
 __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid_constant__ NormParams p) {
   HQ_NORM_SETUP(4);
-  float sum_w[V][8], sum_a[V][8];
+  float2 sum_w[V][4], sum_a[V][4];
 #pragma unroll
   for (int j = 0; j < V; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum_w[j][e] = sum_a[j][e] = 0.0f;
+    for (int e = 0; e < 4; ++e) sum_w[j][e] = sum_a[j][e] = both(0.0f);
   struct RowScalars {
     float r_pre, r_post, tok;
   };
   auto scalars = [&](int i, int64_t m) {
     const bool live = i < ring.steps && m < p.M;
-    return RowScalars{p.pre && live ? __ldg(p.r_pre_in + m) : 0.0f, p.post && live ? __ldg(p.r_post_in + m) : 1.0f,
-                      p.gate_kind == kGateToken && live ? norm_param(p.gate, m, p.params_bf16) : 1.0f};
+    return RowScalars{pre && live ? __ldg(p.r_pre_in + m) : 0.0f, post && live ? __ldg(p.r_post_in + m) : 1.0f,
+                      by_token && live ? norm_param(p.gate, m, p.params_bf16) : 1.0f};
   };
   const int64_t stride = ring.stride * p.rows;
   int64_t m0 = ring.first * p.rows + row;  // row of step i
@@ -478,46 +490,47 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
     next = scalars(i + 1, m0 + stride);
     if (i < ring.steps) {
       ok = ok && ring.wait(s0, phase);
-      float s[3] = {0.0f, 0.0f, 0.0f};
+      float2 c[3] = {both(0.0f), both(0.0f), both(0.0f)};
       const uint8_t* src = units0 + s0 * 4 * tensor;
       if (m0 < p.M)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           if (!in[j]) continue;
           Unit<BF16> x;
-          float h[8], n[8];
+          float2 h[4], n[4];
           x.zero();
-          if (p.pre) x.load(src + j * unit);
+          if (pre) x.load(src + j * unit);
           x.get(h);
-          if (p.pre) x.load(src + tensor + j * unit);
+          if (pre) x.load(src + tensor + j * unit);
           x.get(n);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            sum_w[j][e] = fmaf(n[e] * now.r_pre, h[e], sum_w[j][e]);
-            n[e] *= w_pre[j][e];
-            s[0] = fmaf(n[e], h[e], s[0]);
+          for (int e = 0; e < 4; ++e) {
+            sum_w[j][e] = fma2(mul2(n[e], both(now.r_pre)), h[e], sum_w[j][e]);
+            n[e] = mul2(n[e], w_pre[j][e]);
+            c[0] = fma2(n[e], h[e], c[0]);
           }
-          if (!p.has_y) continue;
-          float d[8], y[8];
+          if (!has_y) continue;
+          float2 d[4], y[4];
           x.zero();
-          if (p.in[2]) x.load(src + 2 * tensor + j * unit);
+          if (PLAIN || p.in[2]) x.load(src + 2 * tensor + j * unit);
           x.get(d);
           x.load(src + 3 * tensor + j * unit);
           x.get(y);
-          if (p.gate_kind == kGateFull) {
-            float g[8];
+          if (full) {
+            float2 g[4];
             x.load(static_cast<const uint8_t*>(p.gate) + m0 * p.ld_gate + (col0 + lane_u * 8) * kEs + j * unit);
             x.get(g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= g[e];
+            for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], g[e]);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float q = w_post[j][e] * y[e];
-            s[1] = fmaf(fmaf(now.r_pre, n[e], d[e]), q, s[1]);
-            s[2] = fmaf(h[e], q, s[2]);
+          for (int e = 0; e < 4; ++e) {
+            const float2 q = mul2(w_post[j][e], y[e]);
+            c[1] = fma2(fma2(both(now.r_pre), n[e], d[e]), q, c[1]);
+            c[2] = fma2(h[e], q, c[2]);
           }
         }
+      float s[3] = {c[0].x + c[0].y, c[1].x + c[1].y, c[2].x + c[2].y};
       put_sums<3>(sh, parity, 0, ranks, rank, s);
     }
     if (i >= 1) {
@@ -527,7 +540,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
       const float k1 = r_pre * r_pre * r_pre * (s[0] * inv_d);
       const float dot = fmaf(-k1, s[2], s[1]);  // sum d q (a per-token gate left out)
       const float k2 = r_post * r_post * r_post * (tok * dot * inv_d);
-      if (p.gate_kind == kGateToken && m1 < p.M && lane_u == 0 && rank == 0)
+      if (by_token && m1 < p.M && lane_u == 0 && rank == 0)
         static_cast<float*>(p.dgate)[m1] = dot * r_post;
       const uint8_t* src = units0 + s1 * 4 * tensor;
       if (m1 < p.M)
@@ -535,49 +548,47 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
         for (int j = 0; j < V; ++j) {
           if (!in[j]) continue;
           Unit<BF16> x;
-          float d[8], v[8], o[8];
+          float2 d[4], v[4], o[4];
           x.zero();
-          if (p.in[2]) x.load(src + 2 * tensor + j * unit);
+          if (PLAIN || p.in[2]) x.load(src + 2 * tensor + j * unit);
           x.get(d);
-          if (p.pre) {
+          if (pre) {
             x.load(src + tensor + j * unit);
             x.get(v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = fmaf(r_pre, v[e] * w_pre[j][e], d[e]);
+            for (int e = 0; e < 4; ++e) d[e] = fma2(both(r_pre), mul2(v[e], w_pre[j][e]), d[e]);
             x.load(src + j * unit);
             x.get(v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = fmaf(-v[e], k1, d[e]);
+            for (int e = 0; e < 4; ++e) d[e] = fma2(v[e], both(-k1), d[e]);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = p.alpha * d[e];
+          for (int e = 0; e < 4; ++e) o[e] = mul2(both(p.alpha), d[e]);
           x.set(o);
           x.store(static_cast<uint8_t*>(p.dh) + at1 + j * unit);
-          if (!p.has_y) continue;
+          if (!has_y) continue;
           x.load(src + 3 * tensor + j * unit);
           x.get(v);
-          if (p.gate_kind == kGateFull) {
-            float g[8];
+          if (full) {
+            float2 g[4];
             x.load(static_cast<const uint8_t*>(p.gate) + m1 * p.ld_gate + (col0 + lane_u * 8) * kEs + j * unit);
             x.get(g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              o[e] = d[e] * (w_post[j][e] * v[e] * r_post);
-              d[e] *= g[e];
+            for (int e = 0; e < 4; ++e) {
+              o[e] = mul2(d[e], mul2(mul2(w_post[j][e], v[e]), both(r_post)));
+              d[e] = mul2(d[e], g[e]);
             }
             x.set(o);
             x.store(static_cast<uint8_t*>(p.dgate) + at1 + j * unit);
           }
           const float dr = tok * r_post;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            sum_a[j][e] = fmaf(d[e] * dr, v[e], sum_a[j][e]);
-            o[e] = d[e] * w_post[j][e];
+          for (int e = 0; e < 4; ++e) {
+            d[e] = mul2(d[e], both(dr));
+            sum_a[j][e] = fma2(d[e], v[e], sum_a[j][e]);
+            o[e] = mul2(d[e], w_post[j][e]);
+            if (post) o[e] = fma2(v[e], both(-k2), o[e]);
           }
-          // (without the post norm r_post is 1 and k2 has no place)
-          const float k = p.post ? k2 : 0.0f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = fmaf(dr, o[e], -v[e] * k);
           x.set(o);
           x.store(static_cast<uint8_t*>(p.dy) + at1 + j * unit);
         }
@@ -603,10 +614,10 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
     for (int j = 0; j < V; ++j) {
       if (!in[j]) continue;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = (j * p.tpr + lane_u) * 8 + e;
-        s_sum[c] = (r ? s_sum[c] : 0.0f) + sum_w[j][e];
-        s_sum[p.cols + c] = (r ? s_sum[p.cols + c] : 0.0f) + sum_a[j][e];
+      for (int e = 0; e < 4; ++e) {
+        float2* const at = reinterpret_cast<float2*>(s_sum) + (j * p.tpr + lane_u) * 4 + e;
+        at[0] = add2(r ? at[0] : both(0.0f), sum_w[j][e]);
+        at[p.cols / 2] = add2(r ? at[p.cols / 2] : both(0.0f), sum_a[j][e]);
       }
     }
   }
