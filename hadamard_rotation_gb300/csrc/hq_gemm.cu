@@ -336,24 +336,44 @@ hq_status grouped_wgrad(const uint8_t* gq, const uint8_t* gs, const float* g_sg,
   return launch<hq::kGemmContr, MX, 192>(p, a, b, (N + 127) / 128, E * tiles_a * tiles_b, stream);
 }
 
-template <int NB, int TG>
-cudaError_t launch_shrink(hq::ShrinkParams p, int sms, cudaStream_t stream) {
-  const int tiles = (p.rows + 32 * TG - 1) / (32 * TG), chunks = p.K / 32;
-  // As many slices of k as keep every warp a chunk, up to a portable cluster; then, where few
-  // rows leave multiprocessors idle, several CTAs share a tile's adapters.
+// bf16 [groups, rows, cols], rows `stride` bytes apart, in boxes of box_rows rows x 64 elements, 128-byte
+// swizzle; past a group's rows or a row's end: 0.
+bool encode_bf16(CUtensorMap* map, const void* x, int64_t cols, int64_t stride_bytes, int64_t rows, int64_t groups,
+                 int box_rows, int dims) {
+  const EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t size[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(groups)};
+  const cuuint64_t stride[2] = {static_cast<cuuint64_t>(stride_bytes), static_cast<cuuint64_t>(stride_bytes * rows)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, step[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(dims), const_cast<void*>(x), size, stride,
+            box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+hq_status launch_shrink(hq::ShrinkParams p, const void* x, int64_t ldx, const void* a, hq_stream stream) {
+  CUtensorMap mx, ma;
+  if (!encode_bf16(&mx, x, p.K, ldx * 2, p.rows, 1, hq::kShrinkRows, 2) ||
+      !encode_bf16(&ma, a, p.K, int64_t{2} * p.K, p.rank, p.adapters, (p.rank + 15) / 16 * 16, 3))
+    return cuda_fail(cudaErrorInvalidValue);
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  // As many slices of k as there are places for (two CTAs per SM), up to a portable cluster; then, where
+  // few rows leave SMs idle, several CTAs share a tile's adapters.
+  const int tiles = (p.rows + hq::kShrinkRows - 1) / hq::kShrinkRows, blocks = (p.K + 63) / 64;
   p.slices = 1;
-  while (p.slices < 8 && p.slices * 2 * (8 / TG) <= chunks && tiles * p.slices < 2 * sms) p.slices *= 2;
+  while (p.slices < 8 && p.slices * 2 <= blocks && tiles * p.slices * 2 <= 2 * sms) p.slices *= 2;
   p.jobs = 1;
-  while (p.jobs < 32 && tiles * p.slices * p.jobs < sms) p.jobs *= 2;
-  auto kernel = hq::k_lora_shrink<NB, TG>;
-  const size_t smem = sizeof(float) * (8 / TG) * (32 * TG) * (16 * NB);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
+  while (p.jobs < 32 && tiles * p.slices * p.jobs * 2 <= 2 * sms) p.jobs *= 2;
+  if ((e = cudaFuncSetAttribute(hq::k_lora_shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, hq::kShrinkSmem)) !=
+      cudaSuccess)
+    return cuda_fail(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles) * p.slices * p.jobs);
   cfg.blockDim = dim3(hq::kShrinkThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
+  cfg.dynamicSmemBytes = hq::kShrinkSmem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -362,15 +382,9 @@ cudaError_t launch_shrink(hq::ShrinkParams p, int sms, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kernel, p);
-  return e == cudaSuccess ? cudaGetLastError() : e;
-}
-
-template <int TG>
-cudaError_t launch_shrink(const hq::ShrinkParams& p, int sms, cudaStream_t stream) {
-  return p.rank <= 16   ? launch_shrink<1, TG>(p, sms, stream)
-         : p.rank <= 32 ? launch_shrink<2, TG>(p, sms, stream)
-                        : launch_shrink<4, TG>(p, sms, stream);
+  e = cudaLaunchKernelEx(&cfg, hq::k_lora_shrink, mx, ma, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? HQ_OK : cuda_fail(e);
 }
 
 int64_t lora_t_bytes(int64_t M, int64_t R) { return (4 * M * R + 31) / 32 * 32; }
@@ -396,35 +410,28 @@ hq_status lora_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, con
   const bool narrow = narrow_rows(M, 1);
   const int64_t tiles = narrow ? (M + 63) / 64 * ((N + 127) / 128) : (M + 191) / 192 * ((N + 255) / 256);
   if (tiles > kMaxExtent) return HQ_ERR_SHAPE;
-  int sms = 0;
-  cudaError_t e = sm_count(&sms);
-  if (e != cudaSuccess) return cuda_fail(e);
   hq::ShrinkParams s = {};
-  s.x = static_cast<const uint8_t*>(x);
-  s.ldx = ldx * 2;
-  s.a = static_cast<const uint8_t*>(a);
   s.scaling = scaling;
   s.sg_a = w_sg;
   s.sg_b = x_sg;
   s.ids = ids;
-  s.t = static_cast<uint8_t*>(workspace);
+  s.t = static_cast<__nv_bfloat16*>(workspace);
   s.rows = static_cast<int>(M);
   s.K = static_cast<int>(K);
   s.adapters = static_cast<int>(n);
   s.rank = static_cast<int>(R);
   if (n > 0) {
-    e = M <= 32 ? launch_shrink<1>(s, sms, static_cast<cudaStream_t>(stream))
-                : launch_shrink<2>(s, sms, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e);
+    const hq_status st = launch_shrink(s, x, M > 1 ? ldx : K, a, stream);
+    if (st != HQ_OK) return st;
   }
   GemmParams p = rows_params<MX>(xs, x_sg, ws, w_sg, M, N, K, 1, out, dt);
   p.lora_b = static_cast<const uint8_t*>(b);
-  p.lora_t = s.t;
+  p.lora_t = static_cast<const uint8_t*>(workspace);
   p.lora_ids = ids;
   p.adapters = s.adapters;
   p.rank = s.rank;
   if (!narrow) {
-    const hq_status st = tile_scales(p, s.t + lora_t_bytes(M, R), stream);
+    const hq_status st = tile_scales(p, static_cast<uint8_t*>(workspace) + lora_t_bytes(M, R), stream);
     if (st != HQ_OK) return st;
   }
   const Codes ca = {wq, K / 2, N, 1}, cb = {xq, K / 2, M, 1};

@@ -270,18 +270,18 @@ __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uin
 }
 
 template <bool PAIR>
-__device__ __forceinline__ void umma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+__device__ __forceinline__ void umma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   if constexpr (PAIR)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc)
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc)
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -808,7 +808,7 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
           for (int part = 0; part < 2; ++part)  // hi, lo
             for (int j = 0; j < steps; ++j)
               umma_bf16<kPair>(d, ch + 2 * j, ch + ((kGemmLanes * 128 + part * S::kRowsB * 128) >> 4) + 2 * j,
-                               umma_idesc_bf16(S::kTileLanes, t.n));
+                               umma_idesc_bf16(S::kTileLanes, t.n), 1);
           umma_commit<kPair>(smem_addr(&bars.chunk_empty[chunk.s]));
         }
         __syncwarp();
@@ -1152,36 +1152,31 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
 // adapter a, in two bf16 terms.  (The division undoes what the epilogue multiplies the whole
 // accumulator by.)
 //
-// A CTA takes a tile of 32 or 64 rows and a slice of k; the slices of a tile are a cluster, which adds
-// their sums in distributed shared memory in a fixed order.  It goes through the tile's distinct adapters
-// (of several CTAs per slice every `jobs`-th one), so each adapter's A is read once per row tile: when
-// every row has its own, once per row, which is the least.  mma.sync m16n8k16 with ranks as its
-// rows and tokens as its columns: the operands come straight from global memory, 16 bytes per
-// thread and row, with the same permutation of k on both sides.  Bound by the reads of x and A; the
-// tensor cores are idle most of the time, so the shape of the instruction does not matter.
+// A CTA takes a tile of 128 rows (the lanes of tensor memory) and a slice of k.  The columns of one
+// instruction are the ranks of several of the tile's distinct adapters side by side, up to 128: x is
+// read once for all of them, and a row keeps the columns of its own adapter.  More adapters than
+// fit take further passes; with few row tiles, several CTAs per slice share the adapters (`jobs`).  The
+// slices of a tile are a cluster, which adds their sums in distributed shared memory in a fixed order.
+// Bound by reading x and each distinct adapter of every tile once; two CTAs per SM keep 192 KB of
+// loads in flight.  Warps 0..3: the tile's lanes; warp 4: TMA; warp 5: the products.
 // ---------------------------------------------------------------------------
-constexpr int kShrinkThreads = 256;
+constexpr int kShrinkThreads = 192;
+constexpr int kShrinkRows = 128;
+constexpr int kShrinkCols = 128;                    // columns of a pass
+constexpr int kShrinkStages = 3;
+constexpr int kShrinkStageBytes = (kShrinkRows + kShrinkCols) * 128;
+constexpr int kShrinkSmem = 1024 + kShrinkStages * kShrinkStageBytes;
+constexpr int kShrinkPitch = kShrinkRows + 1;       // of the sums [rank][row]: no bank conflict either way
+static_assert(128 * kShrinkPitch * 4 <= kShrinkStages * kShrinkStageBytes, "the sums lie over the ring");
 
 struct ShrinkParams {
-  const uint8_t* x;        // bf16 [rows, K], row stride ldx bytes
-  int64_t ldx;
-  const uint8_t* a;        // bf16 [adapters, rank, K]
   const float* scaling;    // [adapters]
   const float* sg_a;       // NULL: 1
   const float* sg_b;
   const int32_t* ids;
-  uint8_t* t;              // bf16 [rows][hi, lo][rank]
+  __nv_bfloat16* t;        // [rows][hi, lo][rank]
   int rows, K, adapters, rank, slices, jobs;
 };
-
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 __device__ __forceinline__ float load_cluster(const float* p, uint32_t rank) {
   float v;
@@ -1194,118 +1189,154 @@ __device__ __forceinline__ float load_cluster(const float* p, uint32_t rank) {
   return v;
 }
 
-// NB: blocks of 16 ranks at a time.  TG: groups of 32 rows in a tile (the 8 warps are TG x 8 / TG
-// interleaved parts of the slice).
-template <int NB, int TG>
-__global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const __grid_constant__ ShrinkParams p) {
-  constexpr int kRows = 32 * TG, kParts = 8 / TG, kRanks = 16 * NB;
-  extern __shared__ float shrink_sum[];  // [parts][rows][ranks]
-  __shared__ int ids[kRows];
-  __shared__ int leaders[kRows];         // the tile's distinct adapters, in the order of their first row
-  __shared__ int n_leaders;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tg = warp % TG, part = warp / TG;
+__global__ void __launch_bounds__(kShrinkThreads)
+    k_lora_shrink(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
+                  const __grid_constant__ ShrinkParams p) {
+  extern __shared__ uint8_t shrink_smem_raw[];
+  __shared__ struct {
+    uint64_t full[kShrinkStages], empty[kShrinkStages], done;
+    uint32_t tmem;
+    int n;                        // adapters of this CTA
+    int16_t slot[kShrinkRows];    // a row's place among them, or -1
+    int adapter[kShrinkRows];     // the tile's distinct adapters, in the order of their first row
+  } sh;
+  uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(shrink_smem_raw) + 1023) & ~uintptr_t{1023});
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int slice = blockIdx.x % p.slices, job = blockIdx.x / p.slices % p.jobs;
-  const int row0 = blockIdx.x / p.slices / p.jobs * kRows;
+  const int row0 = blockIdx.x / p.slices / p.jobs * kShrinkRows;
+  const int padded = (p.rank + 15) & ~15;
+
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
+                 "r"(kShrinkCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (threadIdx.x == 128) {
+    for (int i = 0; i < kShrinkStages; ++i) {
+      mbar_init(smem_addr(&sh.full[i]), 1);
+      mbar_init(smem_addr(&sh.empty[i]), 1);
+    }
+    mbar_init(smem_addr(&sh.done), 1);
+    fence_mbar_init();
+  }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (threadIdx.x < kRows) {
-    const int id = row0 + threadIdx.x < p.rows ? __ldg(p.ids + row0 + threadIdx.x) : -1;
-    ids[threadIdx.x] = id < p.adapters ? id : -1;
-  }
-  if (threadIdx.x == 0) n_leaders = 0;
-  __syncthreads();
-  if (warp == 0) {
+  if (warp == 0) {  // the distinct adapters; every jobs-th of them is this CTA's
     int n = 0;
-    for (int r0 = 0; r0 < kRows; r0 += 32) {
-      const int id = ids[r0 + lane];
-      bool first = id >= 0;
-      for (int j = 0; j < r0 + lane && first; ++j) first = ids[j] != id;
-      const uint32_t m = __ballot_sync(0xFFFFFFFFu, first);
-      if (first) leaders[n + __popc(m & ((1u << lane) - 1))] = id;
-      n += __popc(m);
+    for (int r0 = 0; r0 < kShrinkRows; r0 += 32) {
+      const int r = r0 + lane;
+      int id = row0 + r < p.rows ? __ldg(p.ids + row0 + r) : -1;
+      if (id >= p.adapters || id < 0) id = -1;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
+      int at = -1;
+      for (int j = 0; j < n; ++j)
+        if (sh.adapter[j] == id) at = j;
+      const bool first = id >= 0 && at < 0 && lane == __ffs(same) - 1;
+      const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, first);
+      if (id >= 0 && at < 0) at = n + __popc(firsts & ((1u << (__ffs(same) - 1)) - 1));
+      if (first) sh.adapter[at] = id;
+      sh.slot[r] = static_cast<int16_t>(at >= 0 && at % p.jobs == job ? at / p.jobs : -1);
+      n += __popc(firsts);
+      __syncwarp();
     }
-    if (lane == 0) n_leaders = n;
+    if (lane == 0) sh.n = n > job ? (n - job + p.jobs - 1) / p.jobs : 0;
   }
+  umma_fence_before();
   __syncthreads();
+  umma_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const int n = sh.n, per_pass = kShrinkCols / padded, passes = (n + per_pass - 1) / per_pass;
+  const int blocks = (p.K + 63) / 64, per = (blocks + p.slices - 1) / p.slices;
+  const int kb0 = slice * per, kb1 = min(blocks, kb0 + per);
+  bool ok = true;
   float inv = 1.0f;
   if (p.sg_a) inv = __fdiv_rn(1.0f, __fmul_rn(__ldg(p.sg_a), __ldg(p.sg_b)));
-  const int chunks = p.K / 32;  // of 32 summed elements: 16 bytes per thread and row
-  const int per = (chunks + p.slices - 1) / p.slices;
-  const int c_end = min(chunks, (slice + 1) * per);
-  const int g = lane >> 2, q = lane & 3;
+  float* const sums = reinterpret_cast<float*>(ring);
+  GemmRing at;
+  const uint64_t ring0 = desc_codes(smem_addr(ring));
+  long long fills = 0;
 
-  for (int li = job; li < n_leaders; li += p.jobs) {
-    const int id = leaders[li];
-    const bool mine = __ballot_sync(0xFFFFFFFFu, ids[tg * 32 + lane] == id) != 0;
-    for (int rb = 0; rb < p.rank; rb += kRanks) {
-      float acc[NB][4][4];
+  for (int pass = 0; pass < passes; ++pass) {  // (as many in every CTA of the cluster)
+    const int slots = min(per_pass, n - pass * per_pass);
+    if (warp == 4) {
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = ok && warp_wait(smem_addr(&sh.empty[at.s]), at.phase ^ 1);
+        const uint32_t bar = smem_addr(&sh.full[at.s]), st = smem_addr(ring) + at.s * kShrinkStageBytes;
+        if (!ok) break;
+        ++fills;
+        if (elect_one()) {
+          mbar_expect_tx(bar, (kShrinkRows + slots * padded) * 128);
+          tma_tile2<false>(st, &map_x, kb * 64, row0, bar);
+          for (int i = 0; i < slots; ++i)
+            tma_tile3<false>(st + (kShrinkRows + i * padded) * 128, &map_a, kb * 64, 0,
+                             sh.adapter[job + (pass * per_pass + i) * p.jobs], bar);
+        }
+        __syncwarp();
+        at.next(kShrinkStages);
+      }
+    } else if (warp == 5) {
+      const uint32_t idesc = umma_idesc_bf16(kShrinkRows, slots * padded);
+      for (int kb = kb0; kb < kb1 && ok; ++kb) {
+        ok = warp_wait(smem_addr(&sh.full[at.s]), at.phase);
+        umma_fence_after();
+        const uint64_t st = ring0 + at.s * (kShrinkStageBytes >> 4);
+        if (ok && elect_one()) {
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+          for (int j = 0; j < 4; ++j)
+            umma_bf16<false>(tmem, st + 2 * j, st + (kShrinkRows * 128 >> 4) + 2 * j, idesc, kb > kb0 || j > 0);
+          umma_commit<false>(smem_addr(&sh.empty[at.s]));
+        }
+        __syncwarp();
+        at.next(kShrinkStages);
+      }
+      if (elect_one()) umma_commit<false>(smem_addr(&sh.done));
+      __syncwarp();
+    }
+    // Every copy has been read and every product is complete (a failed wait: bounded here too).
+    ok = mbar_wait(smem_addr(&sh.done), pass & 1) && ok;
+    umma_fence_after();
+    __syncthreads();
+    if (warp < 4) {  // each row's own columns
+      const int row = warp * 32 + lane, mine = sh.slot[row] - pass * per_pass;
+      for (int i = 0; i < slots; ++i) {
+        if (!__any_sync(0xFFFFFFFFu, mine == i)) continue;
+        for (int r = 0; r < padded; r += 16) {
+          uint32_t v[16];
+          tmem_load(tmem + (static_cast<uint32_t>(warp * 32) << 16) + i * padded + r, v);
+          if (mine == i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.0f;
-      if (mine) {
-#pragma unroll 2
-        for (int c = slice * per + part; c < c_end; c += kParts) {
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-          uint4 a[NB][2], x[4];
-#pragma unroll
-          for (int i = 0; i < NB; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int r = rb + 16 * i + 8 * h + g;
-              a[i][h] = r < p.rank ? __ldg(reinterpret_cast<const uint4*>(
-                                         p.a + ((static_cast<int64_t>(id) * p.rank + r) * p.K + int64_t{32} * c) * 2 + 16 * q))
-                                   : zero;
-            }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int m = row0 + tg * 32 + 8 * j + g;
-            x[j] = m < p.rows ? __ldg(reinterpret_cast<const uint4*>(p.x + m * p.ldx + int64_t{64} * c + 16 * q)) : zero;
-          }
-#pragma unroll
-          for (int i = 0; i < NB; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              mma_bf16(acc[i][j], a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, x[j].x, x[j].y);
-              mma_bf16(acc[i][j], a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, x[j].z, x[j].w);
-            }
+            for (int k = 0; k < 16; ++k) sums[(r + k) * kShrinkPitch + row] = kb1 > kb0 ? __uint_as_float(v[k]) : 0.0f;
         }
       }
-      // accumulator: ranks g and g + 8, rows 2 q and 2 q + 1 of a block of 8
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            shrink_sum[(part * kRows + tg * 32 + 8 * j + 2 * q + (k & 1)) * kRanks + 16 * i + g + 8 * (k >> 1)] =
-                acc[i][j][k];
-      __syncthreads();
-      for (int e = threadIdx.x; e < kRows * kRanks; e += kShrinkThreads) {
-        float v = shrink_sum[e];
-#pragma unroll
-        for (int k = 1; k < kParts; ++k) v += shrink_sum[k * kRows * kRanks + e];
-        shrink_sum[e] = v;
-      }
-      cluster_sync();
-      // each CTA of the cluster finishes every slices-th value
-      for (int e = threadIdx.x * p.slices + slice; e < kRows * kRanks; e += kShrinkThreads * p.slices) {
-        const int m = e / kRanks, r = rb + e % kRanks;
-        if (ids[m] != id || r >= p.rank) continue;
-        float v = 0.0f;
-        for (int k = 0; k < p.slices; ++k) v += load_cluster(shrink_sum + e, k);
-        v *= __ldg(p.scaling + id) * inv;
-        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-        __nv_bfloat16* t = reinterpret_cast<__nv_bfloat16*>(p.t) + static_cast<int64_t>(row0 + m) * 2 * p.rank;
-        t[r] = hi;
-        t[p.rank + r] = __float2bfloat16_rn(v - __bfloat162float(hi));
-      }
-      cluster_sync();  // the sums have been read
+      umma_fence_before();
     }
+    cluster_sync();
+    // Each CTA of the cluster finishes every slices-th row.
+    const int rows = (kShrinkRows - slice + p.slices - 1) / p.slices;
+    for (int e = threadIdx.x; e < rows * p.rank; e += kShrinkThreads) {
+      const int row = e / p.rank * p.slices + slice, r = e % p.rank, mine = sh.slot[row] - pass * per_pass;
+      if (sh.slot[row] < 0 || mine < 0 || mine >= slots) continue;
+      float v = 0.0f;
+      for (int k = 0; k < p.slices; ++k) v += load_cluster(sums + r * kShrinkPitch + row, k);
+      v *= __ldg(p.scaling + sh.adapter[job + sh.slot[row] * p.jobs]) * inv;
+      const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+      __nv_bfloat16* const t = p.t + static_cast<int64_t>(row0 + row) * 2 * p.rank;
+      t[r] = hi;
+      t[p.rank + r] = __float2bfloat16_rn(v - __bfloat162float(hi));
+    }
+    fence_proxy_async_smem();  // the next pass's copies overwrite the sums
+    cluster_sync();
   }
+  if (!ok && warp == 4)  // let the copies in flight land (bounded)
+    for (long long f = fills > kShrinkStages ? fills - kShrinkStages : 0; f < fills; ++f)
+      mbar_wait(smem_addr(&sh.full[f % kShrinkStages]), (f / kShrinkStages) & 1);
+  if (!ok && lane == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);
+  umma_fence_before();
+  __syncthreads();
+  umma_fence_after();
+  if (warp == 5)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kShrinkCols) : "memory");
 }
 
 }  // namespace hq
