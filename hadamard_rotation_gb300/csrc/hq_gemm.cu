@@ -106,11 +106,11 @@ struct Codes {
   int64_t row_bytes, rows, groups;
 };
 
-template <int KIND, bool MX, int T, bool LORA = false>
+template <int KIND, bool MX, int T, bool LORA, bool SPLIT = false>
 hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t b_scale_row_tiles, int64_t most_tiles,
-                 hq_stream stream) {
+                 int splits, hq_stream stream) {
   using S = hq::GemmShape<KIND, MX, T, LORA>;
-  auto kernel = hq::k_fp4_gemm<KIND, MX, T, LORA>;
+  auto kernel = hq::k_fp4_gemm<KIND, MX, T, LORA, SPLIT>;
   CUtensorMap ma, mb, msa, msb = {}, mo = {};
   if (!encode_codes(&ma, a.q, a.row_bytes, a.rows, a.groups, hq::kGemmLanes, 3) ||
       !encode_codes(&mb, b.q, b.row_bytes, b.rows, 1, S::kBox, 2) ||
@@ -127,8 +127,9 @@ hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t b_scale_r
       cudaSuccess)
     return cuda_fail(e);
   cudaLaunchConfig_t cfg = {};
-  const int64_t most = sms / S::kCtas;
-  cfg.gridDim = dim3(static_cast<unsigned>((most_tiles < most ? most_tiles : most) * S::kCtas));
+  const int ctas = S::kCtas * splits;
+  const int64_t most = SPLIT ? most_tiles : sms / ctas;
+  cfg.gridDim = dim3(static_cast<unsigned>((most_tiles < most ? most_tiles : most) * ctas));
   cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
@@ -136,10 +137,10 @@ hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t b_scale_r
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = S::kCtas;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = S::kWide ? 2 : 1;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, msa, msb, mo, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? HQ_OK : cuda_fail(e);
@@ -214,6 +215,22 @@ hq_status out_zero(void* out, int64_t n, hq_dtype dt, hq_stream stream) {
 // in flight per byte of operand, the wide ones read the weights half or a third as often.
 bool narrow_rows(int64_t M, int64_t E) { return M <= 64 * E; }
 
+// Tiles of narrow groups, at most: group sizes add up to M.
+int64_t narrow_tiles(int64_t M, int64_t E, int64_t tiles_a) { return (M + 63 * (E < M ? E : M)) / 64 * tiles_a; }
+
+// The narrow kernel, its summed axis shared by a cluster where there are few tiles: as many CTAs as
+// SMs, each with two pairs of stages at least (a shorter part is mostly start and end).
+template <bool MX, bool LORA>
+hq_status launch_narrow(const GemmParams& p, const Codes& a, const Codes& b, int64_t most_tiles, hq_stream stream) {
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  int splits = 1;
+  while (splits < hq::kMaxSplits && most_tiles * splits * 2 <= sms && p.k >= splits * 2 * 4 * hq::kGemmKBlock) splits *= 2;
+  return splits > 1 ? launch<hq::kGemmRows, MX, 64, LORA, true>(p, a, b, 0, most_tiles, splits, stream)
+                    : launch<hq::kGemmRows, MX, 64, LORA>(p, a, b, 0, most_tiles, 1, stream);
+}
+
 // 128-row tiles of k_group_scales' output, and its bytes.
 int64_t group_scale_tiles(int64_t M, int64_t groups) {
   return ((M + 63) / 64 + (groups < M ? groups : M) + 1) / 2;
@@ -279,7 +296,7 @@ hq_status grouped_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, 
   if (!aligned(out, dt == HQ_F32 ? 4 : 2) || !aligned(offsets, 4)) return HQ_ERR_ALIGN;
   const bool narrow = narrow_rows(M, E);
   const int64_t tiles_a = narrow ? (N + 127) / 128 : (N + 255) / 256;
-  const int64_t tiles = ((M + (narrow ? 63 : 191)) / (narrow ? 64 : 192) + (E < M ? E : M)) * tiles_a;
+  const int64_t tiles = narrow ? narrow_tiles(M, E, tiles_a) : (M / 192 + (E < M ? E : M)) * tiles_a;
   if (tiles > kMaxExtent) return HQ_ERR_SHAPE;
   if (K == 0) return out_zero(out, M * N, dt, stream);
   if (!xq || !xs || !wq || !ws || (!MX && (!x_sg || !w_sg))) return HQ_ERR_NULL;
@@ -294,8 +311,8 @@ hq_status grouped_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, 
     const hq_status st = tile_scales(p, static_cast<uint8_t*>(workspace), stream);
     if (st != HQ_OK) return st;
   }
-  return narrow ? launch<hq::kGemmRows, MX, 64>(p, a, b, 0, tiles, stream)
-                : launch<hq::kGemmRows, MX, 192>(p, a, b, group_scale_tiles(M, E), tiles, stream);
+  return narrow ? launch_narrow<MX, false>(p, a, b, tiles, stream)
+                : launch<hq::kGemmRows, MX, 192, false>(p, a, b, group_scale_tiles(M, E), tiles, 1, stream);
 }
 
 template <bool MX>
@@ -333,7 +350,7 @@ hq_status grouped_wgrad(const uint8_t* gq, const uint8_t* gs, const float* g_sg,
   p.out_f32 = dt == HQ_F32;
   p.out_vec = store_bytes(out, K, dt);
   const Codes a = {xq, T / 2, K, 1}, b = {gq, T / 2, N, 1};
-  return launch<hq::kGemmContr, MX, 192>(p, a, b, (N + 127) / 128, E * tiles_a * tiles_b, stream);
+  return launch<hq::kGemmContr, MX, 192, false>(p, a, b, (N + 127) / 128, E * tiles_a * tiles_b, 1, stream);
 }
 
 // bf16 [groups, rows, cols], rows `stride` bytes apart, in boxes of box_rows rows x 64 elements, 128-byte
@@ -420,23 +437,31 @@ hq_status lora_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, con
   s.K = static_cast<int>(K);
   s.adapters = static_cast<int>(n);
   s.rank = static_cast<int>(R);
+  GemmParams p = rows_params<MX>(xs, x_sg, ws, w_sg, M, N, K, 1, out, dt);
+  uint8_t* const tiles_at = static_cast<uint8_t*>(workspace) + lora_t_bytes(M, R);
   if (n > 0) {
+    if (!narrow) {
+      s.scales = xs;
+      s.tiles = reinterpret_cast<uint4*>(tiles_at);
+      s.scale_row_bytes = p.sfb_row_bytes;
+      s.scale_tiles = p.k_tiles;
+      p.sfb = tiles_at;
+    }
     const hq_status st = launch_shrink(s, x, M > 1 ? ldx : K, a, stream);
     if (st != HQ_OK) return st;
   }
-  GemmParams p = rows_params<MX>(xs, x_sg, ws, w_sg, M, N, K, 1, out, dt);
   p.lora_b = static_cast<const uint8_t*>(b);
   p.lora_t = static_cast<const uint8_t*>(workspace);
   p.lora_ids = ids;
   p.adapters = s.adapters;
   p.rank = s.rank;
-  if (!narrow) {
-    const hq_status st = tile_scales(p, static_cast<uint8_t*>(workspace) + lora_t_bytes(M, R), stream);
+  if (!narrow && n == 0) {
+    const hq_status st = tile_scales(p, tiles_at, stream);
     if (st != HQ_OK) return st;
   }
   const Codes ca = {wq, K / 2, N, 1}, cb = {xq, K / 2, M, 1};
-  return narrow ? launch<hq::kGemmRows, MX, 64, true>(p, ca, cb, 0, tiles, stream)
-                : launch<hq::kGemmRows, MX, 192, true>(p, ca, cb, group_scale_tiles(M, 1), tiles, stream);
+  return narrow ? launch_narrow<MX, true>(p, ca, cb, tiles, stream)
+                : launch<hq::kGemmRows, MX, 192, true>(p, ca, cb, group_scale_tiles(M, 1), tiles, 1, stream);
 }
 
 // Row-major scale bytes [groups, rows, cols] -> the tile layout, a 16-byte row of a tile per thread.

@@ -23,6 +23,9 @@
 // needed alone.  An SM's shared memory moves 128 bytes a cycle; the FP4 products of 128 x 192 alone read
 // 107 and their loads write 120.
 //
+// With fewer tiles than SMs (a few rows and one projection) the CTAs of a cluster share a tile's summed
+// axis (SPLIT) and add their parts through distributed shared memory, always in the same order.
+//
 // One CTA per SM takes tiles from a static cyclic order; the
 // group sizes are read on the device, so the call does not wait for the host to know them.
 // Roles of a CTA:
@@ -407,6 +410,7 @@ struct GemmTiles {
   const int *start, *lo, *hi, *units;
   int tiles, step;
   int next;      // the next tile
+  int splits, part;  // the part of the summed axis that is this CTA's
   int count = 0;  // handed out since the last 32 were worked out
   GemmTile mine;
 
@@ -416,6 +420,12 @@ struct GemmTiles {
     if ((count & 31) == 0) {
       const int tile = next + static_cast<int>(threadIdx.x & 31) * step;
       mine = gemm_tile<KIND, T>(p, start, lo, hi, units, tile < tiles ? tile : next);
+      if (splits > 1) {  // parts of whole pairs of stages (16 bytes of the tokens' scales)
+        constexpr int kUnit = 2 * kGemmKBlock;
+        const int all = (mine.k + kUnit - 1) / kUnit;
+        mine.k0 = all * part / splits * kUnit;
+        mine.k = min(mine.k, all * (part + 1) / splits * kUnit) - mine.k0;
+      }
     }
     const int from = count & 31;
     auto pick = [&](int v) { return __shfl_sync(0xFFFFFFFFu, v, from); };
@@ -631,8 +641,22 @@ __device__ __forceinline__ void tma_store3(const CUtensorMap* map, uint32_t src,
 constexpr int kScaleThreads = 128;
 
 constexpr int kLoraThreads = 128;
+constexpr int kMaxSplits = 8;
 
-template <int KIND, bool MX, int T, bool LORA>
+// A float of CTA `rank` of the cluster, at the address of a shared variable of this one.
+__device__ __forceinline__ float load_cluster(const float* p, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+      "ld.shared::cluster.f32 %0, [a];\n\t}"
+      : "=f"(v)
+      : "r"(smem_addr(p)), "r"(rank)
+      : "memory");
+  return v;
+}
+
+
+template <int KIND, bool MX, int T, bool LORA, bool SPLIT>
 __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
     k_fp4_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                const __grid_constant__ CUtensorMap map_sfa, const __grid_constant__ CUtensorMap map_sfb,
@@ -653,7 +677,9 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
   int* units = hi + p.groups + 1;  // (tiled scales of ragged rows) 64-row units of scales before a group's
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
+  static_assert(!(SPLIT && kPair), "pairs do not split the sum");
   const uint32_t rank = kPair ? cluster_rank() : 0;  // of the pair; CTA 0 issues the products
+  const int splits = SPLIT ? static_cast<int>(cluster_size()) : 1, part_k = SPLIT ? static_cast<int>(cluster_rank()) : 0;
 
   if (warp == 2) {
     if constexpr (kPair) {
@@ -723,9 +749,10 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
   if constexpr (kPair) cluster_sync();  // the peer's barriers are there
   umma_fence_after();
   const uint32_t tmem = bars.tmem;
-  const int tiles = bars.tiles;
-  GemmTiles<KIND, T> order{p, start, lo, hi, units, tiles, static_cast<int>(gridDim.x) / kCtas,
-                           static_cast<int>(blockIdx.x) / kCtas};
+  // (SPLIT: the launch has a cluster for every tile; each takes one)
+  const int places = static_cast<int>(gridDim.x) / (kCtas * splits), place = static_cast<int>(blockIdx.x) / (kCtas * splits);
+  const int tiles = SPLIT ? min(bars.tiles, places) : bars.tiles;
+  GemmTiles<KIND, T> order{p, start, lo, hi, units, tiles, places, place, splits, part_k};
   bool ok = true;
   // Arrivals on a barrier of the CTA that issues the products.
   auto arrive_first = [&](uint32_t bar) {
@@ -902,6 +929,16 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
       const bool none = t.k == 0;  // an empty sum: no product wrote the accumulator
       const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * T;
       bool held = true;
+      if constexpr (SPLIT) {  // the partial sums as they are, over the ring, whose stages have been multiplied
+        float* const sums = reinterpret_cast<float*>(smem);
+        for (int c0 = 0; c0 < t.valid; c0 += 16) {
+          uint32_t v[16];
+          tmem_load(from + c0, v);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) sums[(c0 + c) * kGemmLanes + tid] = __uint_as_float(v[c]);
+        }
+        umma_fence_before();
+      } else
       for (int c0 = part * step; c0 < t.valid; c0 += kEpilogues * step) {
         uint32_t w[kBlocks][16];
 #pragma unroll
@@ -961,21 +998,23 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
     constexpr int kAhead = 4;  // stages whose scales are loaded together: a batch
     constexpr int kBlockBytes = MX ? 8 : 16;
     const int tid = threadIdx.x - 256;
-    const int blocks = (p.k + kGemmKBlock - 1) / kGemmKBlock;
     GemmRing ring;
     struct Batch {
       bool live;  // there is one
-      int kb, b0, valid, n;
+      int kb, end, b0, valid, n;  // stages [kb, end) of the rows' scales
     };
     auto enter = [&](Batch& b) {  // the next tile's first batch
       GemmTile t;
       b.live = order.get(t);
-      if (b.live) b.kb = 0, b.b0 = t.b0, b.valid = t.valid, b.n = t.n;
+      if (b.live) {
+        b.kb = t.k0 / kGemmKBlock, b.end = b.kb + (t.k + kGemmKBlock - 1) / kGemmKBlock;
+        b.b0 = t.b0, b.valid = t.valid, b.n = t.n;
+      }
     };
     auto after = [&](const Batch& b) {
       Batch c = b;
       c.kb += kAhead;
-      if (c.live && c.kb >= blocks) enter(c);
+      if (c.live && c.kb >= c.end) enter(c);
       return c;
     };
     constexpr int kWords = kAhead * kBlockBytes / 4;
@@ -997,7 +1036,7 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
     auto write = [&](const Batch& b, const Loaded& l, const Batch& next, Loaded& into) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        if (b.kb + j >= blocks || !ok) break;
+        if (b.kb + j >= b.end || !ok) break;
         ok = warp_wait(smem_addr(&bars.empty[ring.s]), ring.phase ^ 1);
         if (!ok) break;
         uint8_t* sb = smem + ring.s * S::kStageBytes + S::kBytesA + S::kBytesB + S::kBytesSfa;
@@ -1058,7 +1097,8 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
           turn ^= 1;
           return m;
         };
-        int a = next_above(-1), step = 0;
+        int a = next_above(-1), step = 0, count = 0;
+        bool more = true;
         do {
           int slot_a[4], slot_r[4], steps = 0;
 #pragma unroll
@@ -1072,6 +1112,10 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
               a = next_above(a);
             }
           }
+          // (SPLIT: the parts take the chunks in turn; each ends with an empty one)
+          const bool none = a == INT_MAX && steps == 0;
+          if (SPLIT && !none && count++ % splits != part_k) continue;
+          more = SPLIT ? !none : a != INT_MAX;
           // all four warps go on, or none: they meet at barriers
           ok = role_all<1>(mbar_wait(smem_addr(&bars.chunk_empty[chunk.s]), chunk.phase ^ 1));
           if (!ok) break;
@@ -1121,13 +1165,13 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
           }
           if (tid == 0) {
             bars.chunk_steps[chunk.s] = steps;
-            bars.chunk_last[chunk.s] = a == INT_MAX;
+            bars.chunk_last[chunk.s] = !more;
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) arrive_first(smem_addr(&bars.chunk_full[chunk.s]));
           chunk.next(S::kChunks);
-        } while (a != INT_MAX);
+        } while (more);
       }
     }
   }
@@ -1135,6 +1179,33 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
     if (lane == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);
   }
   __syncwarp();
+  if constexpr (SPLIT) {  // each CTA of the cluster finishes its share of the columns, adding the parts in order
+    cluster_sync();
+    GemmTile t;
+    GemmTiles<KIND, T> again{p, start, lo, hi, units, tiles, places, place, 1, 0};
+    if (again.get(t)) {
+      float a = 1.0f;
+      if (!MX) a = __fmul_rn(__ldg(p.sg_a + t.g), __ldg(p.sg_b));
+      const float* const sums = reinterpret_cast<const float*>(smem);
+      const int n = t.a0 + static_cast<int>(threadIdx.x & 127);
+      if (n < p.na)
+        for (int c = part_k + splits * static_cast<int>(threadIdx.x >> 7); c < t.valid;
+             c += splits * static_cast<int>(blockDim.x >> 7)) {
+          float v[kMaxSplits];
+#pragma unroll
+          for (int k = 0; k < kMaxSplits; ++k)  // all in flight before the first is added
+            v[k] = k < splits ? load_cluster(sums + c * kGemmLanes + (threadIdx.x & 127), k) : 0.0f;
+          float sum = v[0];
+#pragma unroll
+          for (int k = 1; k < kMaxSplits; ++k) sum += v[k];
+          sum = __fmul_rn(sum, a);
+          const int64_t at = static_cast<int64_t>(t.b0 + c) * p.na + n;
+          if (p.out_f32) static_cast<float*>(p.out)[at] = sum;
+          else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(sum);
+        }
+    }
+    cluster_sync();  // the peers have read this CTA's sums
+  }
   umma_fence_before();
   __syncthreads();
   if constexpr (kPair) cluster_sync();  // nothing of the pair reads or signals this CTA any more
@@ -1145,6 +1216,26 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
     else
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols) : "memory");
   }
+}
+
+// Row r (of 32) of scale tile `ct` of `rows` rows from row0 on: 4 scales each of the rows r, r + 32, r + 64,
+// r + 96; zeros past the rows and past a row's end.
+__device__ __forceinline__ uint4 scale_tile_row(const uint8_t* s, int64_t row0, int rows, int row_bytes, int ct, int r) {
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    w[q] = 0;
+    if (q * 32 + r >= rows) continue;
+    const uint8_t* src = s + (row0 + q * 32 + r) * row_bytes + 4 * ct;
+    if (row_bytes % 4 == 0 && reinterpret_cast<uintptr_t>(s) % 4 == 0) {
+      w[q] = __ldg(reinterpret_cast<const uint32_t*>(src));
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (4 * ct + c < row_bytes) w[q] |= static_cast<uint32_t>(__ldg(src + c)) << (8 * c);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // ---------------------------------------------------------------------------
@@ -1175,19 +1266,12 @@ struct ShrinkParams {
   const float* sg_b;
   const int32_t* ids;
   __nv_bfloat16* t;        // [rows][hi, lo][rank]
+  // x's scales, row-major, and where they go in the tile layout for the wide products (NULL: nowhere)
+  const uint8_t* scales;
+  uint4* tiles;
+  int scale_row_bytes, scale_tiles;
   int rows, K, adapters, rank, slices, jobs;
 };
-
-__device__ __forceinline__ float load_cluster(const float* p, uint32_t rank) {
-  float v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
-      "ld.shared::cluster.f32 %0, [a];\n\t}"
-      : "=f"(v)
-      : "r"(smem_addr(p)), "r"(rank)
-      : "memory");
-  return v;
-}
 
 __global__ void __launch_bounds__(kShrinkThreads)
     k_lora_shrink(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
@@ -1223,11 +1307,15 @@ __global__ void __launch_bounds__(kShrinkThreads)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 0) {  // the distinct adapters; every jobs-th of them is this CTA's
-    int n = 0;
-    for (int r0 = 0; r0 < kShrinkRows; r0 += 32) {
-      const int r = r0 + lane;
-      int id = row0 + r < p.rows ? __ldg(p.ids + row0 + r) : -1;
-      if (id >= p.adapters || id < 0) id = -1;
+    int ids[kShrinkRows / 32], n = 0;
+#pragma unroll
+    for (int c = 0; c < kShrinkRows / 32; ++c) {
+      const int r = row0 + 32 * c + lane;
+      ids[c] = r < p.rows ? __ldg(p.ids + r) : -1;
+    }
+#pragma unroll
+    for (int c = 0; c < kShrinkRows / 32; ++c) {
+      const int id = ids[c] >= 0 && ids[c] < p.adapters ? ids[c] : -1;
       const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
       int at = -1;
       for (int j = 0; j < n; ++j)
@@ -1236,7 +1324,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
       const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, first);
       if (id >= 0 && at < 0) at = n + __popc(firsts & ((1u << (__ffs(same) - 1)) - 1));
       if (first) sh.adapter[at] = id;
-      sh.slot[r] = static_cast<int16_t>(at >= 0 && at % p.jobs == job ? at / p.jobs : -1);
+      sh.slot[32 * c + lane] = static_cast<int16_t>(at >= 0 && at % p.jobs == job ? at / p.jobs : -1);
       n += __popc(firsts);
       __syncwarp();
     }
@@ -1256,6 +1344,11 @@ __global__ void __launch_bounds__(kShrinkThreads)
   GemmRing at;
   const uint64_t ring0 = desc_codes(smem_addr(ring));
   long long fills = 0;
+
+  if (warp < 4 && p.tiles && job == 0)  // under the products: this slice's part of the rows' scales
+    for (int ct = slice * 4 + warp; ct < p.scale_tiles; ct += 4 * p.slices)
+      p.tiles[(static_cast<int64_t>(row0 / 128) * p.scale_tiles + ct) * 32 + lane] =
+          scale_tile_row(p.scales, row0, min(128, p.rows - row0), p.scale_row_bytes, ct, lane);
 
   for (int pass = 0; pass < passes; ++pass) {  // (as many in every CTA of the cluster)
     const int slots = min(per_pass, n - pass * per_pass);
@@ -1312,18 +1405,25 @@ __global__ void __launch_bounds__(kShrinkThreads)
       umma_fence_before();
     }
     cluster_sync();
-    // Each CTA of the cluster finishes every slices-th row.
-    const int rows = (kShrinkRows - slice + p.slices - 1) / p.slices;
-    for (int e = threadIdx.x; e < rows * p.rank; e += kShrinkThreads) {
-      const int row = e / p.rank * p.slices + slice, r = e % p.rank, mine = sh.slot[row] - pass * per_pass;
-      if (sh.slot[row] < 0 || mine < 0 || mine >= slots) continue;
-      float v = 0.0f;
-      for (int k = 0; k < p.slices; ++k) v += load_cluster(sums + r * kShrinkPitch + row, k);
-      v *= __ldg(p.scaling + sh.adapter[job + sh.slot[row] * p.jobs]) * inv;
-      const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+    // Each CTA of the cluster finishes every slices-th row, a row per warp.
+    for (int row = slice + warp * p.slices; row < kShrinkRows; row += kShrinkThreads / 32 * p.slices) {
+      const int slot = sh.slot[row], mine = slot - pass * per_pass;
+      if (slot < 0 || mine < 0 || mine >= slots) continue;
+      const float scale = __ldg(p.scaling + sh.adapter[job + slot * p.jobs]) * inv;
       __nv_bfloat16* const t = p.t + static_cast<int64_t>(row0 + row) * 2 * p.rank;
-      t[r] = hi;
-      t[p.rank + r] = __float2bfloat16_rn(v - __bfloat162float(hi));
+      for (int r = lane; r < p.rank; r += 32) {
+        float part[kMaxSplits];
+#pragma unroll
+        for (int k = 0; k < kMaxSplits; ++k)  // all in flight before the first is added
+          part[k] = k < p.slices ? load_cluster(sums + r * kShrinkPitch + row, k) : 0.0f;
+        float v = part[0];
+#pragma unroll
+        for (int k = 1; k < kMaxSplits; ++k) v += part[k];
+        v *= scale;
+        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+        t[r] = hi;
+        t[p.rank + r] = __float2bfloat16_rn(v - __bfloat162float(hi));
+      }
     }
     fence_proxy_async_smem();  // the next pass's copies overwrite the sums
     cluster_sync();

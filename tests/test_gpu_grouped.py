@@ -76,6 +76,9 @@ def offsets_of(sizes):
     ([191, 192, 193, 385], 128, 512),    # around the wide tile
     ([700, 3, 0, 449], 384, 4128),       # several wide tiles per expert, 17 stages
     ([2] * 40 + [0] * 30 + [1] * 30, 72, 96),   # more groups than lanes of a warp
+    ([5], 300, 8192),                    # few tiles: the summed axis shared by a cluster of 4
+    ([0, 3, 64, 1], 130, 4640),          # of 2, uneven parts
+    ([40], 200, 16416),                  # of 8, a last part with a partial block
 ])
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
 def test_grouped_gemm(fmt, sizes, N, K, out_dtype):

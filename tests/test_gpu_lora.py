@@ -69,6 +69,8 @@ def check(fmt, p, got):
     (1, 8, 32, 1, 8, "one"),             # the smallest
     (1, 300, 544, 3, 16, "one"),
     (32, 257, 1024, 24, 16, "mixed"),    # every row its own
+    (17, 136, 8224, 9, 40, "mixed"),     # few tiles: sum and adapters shared by a cluster of 4
+    (64, 256, 4096, 64, 16, "mixed"),    # of 2, every row its own
     (33, 128, 96, 40, 8, "mixed"),       # one row past the narrow row tile of the first product
     (64, 130, 512, 5, 24, "mixed"),      # a rank that is not a multiple of 16
     (65, 100, 1056, 2, 64, "runs"),      # past the narrow tile of the projection
