@@ -7,6 +7,7 @@ Inputs must be CUDA tensors: there is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -319,68 +320,101 @@ def hq_dequant_nvfp4(q: torch.Tensor, scales: torch.Tensor, s_global: torch.Tens
 
 
 # ---- products of the codes -------------------------------------------------------------------
+#
+# A call of a few rows takes the GPU a few microseconds, so what these functions do per call counts:
+# one check per operand, the device switched only where another one is current, and addresses and
+# streams passed as plain integers.
+
+_U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+_FUNCTIONS: dict[str, object] = {}
 
 
-def _launch(device: torch.device, name: str, args: list, stream: torch.cuda.Stream | None) -> None:
-    """_call without the device switch where the device is current already: the products and norms
-    of a few rows take a few microseconds, which the switch would double."""
-    if device.index != torch.cuda.current_device():
-        _call(device, name, *args, stream=stream)
-        return
-    check(getattr(_lib.load(), name)(*args, _stream_handle(stream, device)), name)
+def _launch(index: int, name: str, args: tuple, stream: torch.cuda.Stream | None) -> None:
+    """Call the C entry point ``name`` with device ``index`` current, on ``stream`` or that device's current
+    stream; raise on a non-OK status."""
+    fn = _FUNCTIONS.get(name)
+    if fn is None:
+        fn = _FUNCTIONS[name] = getattr(_lib.load(), name)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status:
+        check(status, name)
 
 
-def _given(t: torch.Tensor, shape: tuple, dtype: torch.dtype, device: torch.device, name: str) -> int:
-    """The address of an operand that must be there, of this shape and type, contiguous."""
-    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.device != device \
-            or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
-    return t.data_ptr()
+def _given(t: torch.Tensor, shape: tuple, dtype: torch.dtype, index: int, name: str) -> int:
+    """The address of an operand that must be there, of this shape and type, contiguous, on device
+    ``index``."""
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor
+        pass
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
 
 
-def _codes(q: torch.Tensor, dims: int, name: str) -> torch.device:
+def _codes(q: torch.Tensor, dims: int, name: str) -> int:
+    """The device index of a tensor of codes."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libhq has no CPU path)")
-    if q.dim() != dims or q.dtype != torch.uint8:
+    if q.dim() != dims or q.dtype is not _U8:
         raise ValueError(f"{name} must be a {dims}-D uint8 tensor of codes")
-    return q.device
+    return q.get_device()
 
 
 def _tiles_bytes(rows: int, cols: int) -> int:
     return (rows + 127) // 128 * ((cols + 3) // 4) * 512
 
 
-def _out(out: torch.Tensor | None, shape: tuple, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+def _out(out: torch.Tensor | None, shape: tuple, dtype: torch.dtype, like: torch.Tensor) -> torch.Tensor:
     if out is None:
         if dtype not in _DTYPES:
             raise ValueError(f"out_dtype must be float32 or bfloat16, got {dtype}")
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if out.dtype not in _DTYPES:
         raise ValueError(f"out must be float32 or bfloat16, got {out.dtype}")
-    _given(out, shape, out.dtype, device, "out")
+    _given(out, shape, out.dtype, like.get_device(), "out")
     return out
 
 
-def _grouped_gemm(xq, xs, x_sg, wq, ws, w_sg, offsets, out, out_dtype, stream):
-    block = 16 if x_sg is not None else 32
-    dev = _codes(xq, 2, "xq")
-    _codes(wq, 3, "wq")
-    M, K2 = xq.shape
-    E, N, K = wq.shape[0], wq.shape[1], 2 * K2
-    args = [_given(xq, (M, K2), torch.uint8, dev, "xq"),
-            _given(xs, (M, K // block), torch.uint8, dev, "xs")]
-    if x_sg is not None:
-        args.append(_given(x_sg, (1,), torch.float32, dev, "x_sg"))
-    args += [_given(wq, (E, N, K2), torch.uint8, dev, "wq"),
-             _given(ws, (E, _tiles_bytes(N, K // block)), torch.uint8, dev, "ws")]
-    if x_sg is not None:
-        args.append(_given(w_sg, (E,), torch.float32, dev, "w_sg"))
-    args.append(_given(offsets, (E + 1,), torch.int32, dev, "offsets"))
-    out = _out(out, (M, N), out_dtype, dev)
-    work = _work(hq_grouped_gemm_workspace_bytes(M, K, E), dev, stream)
-    args += [M, N, K, E, out.data_ptr(), _DTYPES[out.dtype], _addr(work)]
-    _launch(dev, "hq_grouped_gemm_nvfp4" if x_sg is not None else "hq_grouped_gemm_mxfp4", args, stream)
-    return out
+def _addr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _work(nbytes: int, like: torch.Tensor, stream: torch.cuda.Stream | None) -> torch.Tensor | None:
+    """A workspace for one call; freed when the call returns, so not before ``stream`` is done with it."""
+    if nbytes == 0:
+        return None
+    work = torch.empty(nbytes, dtype=_U8, device=like.device)
+    if stream is not None:
+        work.record_stream(stream)
+    return work
+
+
+@functools.lru_cache(maxsize=1024)
+def hq_grouped_gemm_workspace_bytes(M: int, K: int, E: int) -> int:
+    """Bytes of the workspace of hq_grouped_gemm_* (which this binding allocates itself)."""
+    n = _lib.load().hq_grouped_gemm_workspace_bytes(M, K, E)
+    if n < 0:
+        raise ValueError("hq_grouped_gemm_workspace_bytes: M >= 0, K a multiple of 32, 0 <= E <= 512")
+    return n
+
+
+@functools.lru_cache(maxsize=1024)
+def hq_lora_gemm_workspace_bytes(M: int, K: int, R: int) -> int:
+    """Bytes of the workspace of hq_lora_gemm_* (which this binding allocates itself)."""
+    n = _lib.load().hq_lora_gemm_workspace_bytes(M, K, R)
+    if n < 0:
+        raise ValueError("hq_lora_gemm_workspace_bytes: M >= 0, K a multiple of 32, R a multiple of 8 up to 128")
+    return n
 
 
 def hq_grouped_gemm_nvfp4(xq: torch.Tensor, xs: torch.Tensor, x_sg: torch.Tensor, wq: torch.Tensor,
@@ -394,9 +428,19 @@ def hq_grouped_gemm_nvfp4(xq: torch.Tensor, xs: torch.Tensor, x_sg: torch.Tensor
     writes them; wq uint8 [E, N, K/2], ws uint8 [E, hq_swizzled_scales_bytes(N, K)] in the tile
     layout (hq_swizzle_scales), w_sg float32 [E]; offsets int32 [E + 1].  Rows of no group are left
     as they are in ``out``."""
-    if x_sg is None:
-        raise ValueError("x_sg must be a tensor (hq_grouped_gemm_mxfp4 has no per-tensor scales)")
-    return _grouped_gemm(xq, xs, x_sg, wq, ws, w_sg, offsets, out, out_dtype, stream)
+    index = _codes(xq, 2, "xq")
+    _codes(wq, 3, "wq")
+    M, K2 = xq.shape
+    E, N, _ = wq.shape
+    args = (_given(xq, (M, K2), _U8, index, "xq"), _given(xs, (M, K2 // 8), _U8, index, "xs"),
+            _given(x_sg, (1,), _F32, index, "x_sg"), _given(wq, (E, N, K2), _U8, index, "wq"),
+            _given(ws, (E, _tiles_bytes(N, K2 // 8)), _U8, index, "ws"), _given(w_sg, (E,), _F32, index, "w_sg"),
+            _given(offsets, (E + 1,), _I32, index, "offsets"))
+    out = _out(out, (M, N), out_dtype, xq)
+    work = _work(hq_grouped_gemm_workspace_bytes(M, 2 * K2, E), xq, stream)
+    _launch(index, "hq_grouped_gemm_nvfp4",
+            args + (M, N, 2 * K2, E, out.data_ptr(), _DTYPES[out.dtype], _addr(work)), stream)
+    return out
 
 
 def hq_grouped_gemm_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
@@ -405,31 +449,24 @@ def hq_grouped_gemm_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, 
                           stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """hq_grouped_gemm_nvfp4 for MXFP4 operands: xs uint8 [M, K/32] as hq_rotate_quant_mxfp4 writes it,
     ws uint8 [E, ...] = hq_swizzle_scales of [E, N, K/32]."""
-    return _grouped_gemm(xq, xs, None, wq, ws, None, offsets, out, out_dtype, stream)
+    index = _codes(xq, 2, "xq")
+    _codes(wq, 3, "wq")
+    M, K2 = xq.shape
+    E, N, _ = wq.shape
+    args = (_given(xq, (M, K2), _U8, index, "xq"), _given(xs, (M, K2 // 16), _U8, index, "xs"),
+            _given(wq, (E, N, K2), _U8, index, "wq"), _given(ws, (E, _tiles_bytes(N, K2 // 16)), _U8, index, "ws"),
+            _given(offsets, (E + 1,), _I32, index, "offsets"))
+    out = _out(out, (M, N), out_dtype, xq)
+    work = _work(hq_grouped_gemm_workspace_bytes(M, 2 * K2, E), xq, stream)
+    _launch(index, "hq_grouped_gemm_mxfp4",
+            args + (M, N, 2 * K2, E, out.data_ptr(), _DTYPES[out.dtype], _addr(work)), stream)
+    return out
 
 
-def _grouped_wgrad(gq, gs, g_sg, xq, xs, x_sg, offsets, out, out_dtype, stream):
-    block = 16 if g_sg is not None else 32
-    dev = _codes(gq, 2, "gq")
-    _codes(xq, 2, "xq")
-    N, T2 = gq.shape
-    K, T = xq.shape[0], 2 * T2
-    args = [_given(gq, (N, T2), torch.uint8, dev, "gq"),
-            _given(gs, (_tiles_bytes(N, T // block),), torch.uint8, dev, "gs")]
-    if g_sg is not None:
-        args.append(_given(g_sg, (1,), torch.float32, dev, "g_sg"))
-    args += [_given(xq, (K, T2), torch.uint8, dev, "xq"),
-             _given(xs, (_tiles_bytes(K, T // block),), torch.uint8, dev, "xs")]
-    if g_sg is not None:
-        args.append(_given(x_sg, (1,), torch.float32, dev, "x_sg"))
+def _groups(offsets: torch.Tensor) -> int:
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must be a 1-D int32 tensor of E + 1 values")
-    E = offsets.shape[0] - 1
-    args.append(_given(offsets, (E + 1,), torch.int32, dev, "offsets"))
-    out = _out(out, (E, N, K), out_dtype, dev)
-    args += [T, N, K, E, out.data_ptr(), _DTYPES[out.dtype]]
-    _launch(dev, "hq_grouped_wgrad_nvfp4" if g_sg is not None else "hq_grouped_wgrad_mxfp4", args, stream)
-    return out
+    return offsets.shape[0] - 1
 
 
 def hq_grouped_wgrad_nvfp4(gq: torch.Tensor, gs: torch.Tensor, g_sg: torch.Tensor, xq: torch.Tensor,
@@ -441,9 +478,17 @@ def hq_grouped_wgrad_nvfp4(gq: torch.Tensor, gs: torch.Tensor, g_sg: torch.Tenso
     gq uint8 [N, T/2] and xq uint8 [K, T/2]: dy and x transposed and quantized along the tokens, each
     expert padded with zeros to a multiple of 128 tokens; gs, xs their scales in the tile layout
     (hq_rotate_quant_nvfp4_swizzled writes it); offsets int32 [E + 1], multiples of 128."""
-    if g_sg is None:
-        raise ValueError("g_sg must be a tensor (hq_grouped_wgrad_mxfp4 has no per-tensor scales)")
-    return _grouped_wgrad(gq, gs, g_sg, xq, xs, x_sg, offsets, out, out_dtype, stream)
+    index = _codes(gq, 2, "gq")
+    _codes(xq, 2, "xq")
+    N, T2 = gq.shape
+    K, E = xq.shape[0], _groups(offsets)
+    args = (_given(gq, (N, T2), _U8, index, "gq"), _given(gs, (_tiles_bytes(N, T2 // 8),), _U8, index, "gs"),
+            _given(g_sg, (1,), _F32, index, "g_sg"), _given(xq, (K, T2), _U8, index, "xq"),
+            _given(xs, (_tiles_bytes(K, T2 // 8),), _U8, index, "xs"), _given(x_sg, (1,), _F32, index, "x_sg"),
+            _given(offsets, (E + 1,), _I32, index, "offsets"))
+    out = _out(out, (E, N, K), out_dtype, gq)
+    _launch(index, "hq_grouped_wgrad_nvfp4", args + (2 * T2, N, K, E, out.data_ptr(), _DTYPES[out.dtype]), stream)
+    return out
 
 
 def hq_grouped_wgrad_mxfp4(gq: torch.Tensor, gs: torch.Tensor, xq: torch.Tensor, xs: torch.Tensor,
@@ -451,65 +496,34 @@ def hq_grouped_wgrad_mxfp4(gq: torch.Tensor, gs: torch.Tensor, xq: torch.Tensor,
                            out_dtype: torch.dtype = torch.bfloat16,
                            stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """hq_grouped_wgrad_nvfp4 for MXFP4 operands (scales through hq_swizzle_scales)."""
-    return _grouped_wgrad(gq, gs, None, xq, xs, None, offsets, out, out_dtype, stream)
+    index = _codes(gq, 2, "gq")
+    _codes(xq, 2, "xq")
+    N, T2 = gq.shape
+    K, E = xq.shape[0], _groups(offsets)
+    args = (_given(gq, (N, T2), _U8, index, "gq"), _given(gs, (_tiles_bytes(N, T2 // 16),), _U8, index, "gs"),
+            _given(xq, (K, T2), _U8, index, "xq"), _given(xs, (_tiles_bytes(K, T2 // 16),), _U8, index, "xs"),
+            _given(offsets, (E + 1,), _I32, index, "offsets"))
+    out = _out(out, (E, N, K), out_dtype, gq)
+    _launch(index, "hq_grouped_wgrad_mxfp4", args + (2 * T2, N, K, E, out.data_ptr(), _DTYPES[out.dtype]), stream)
+    return out
 
 
-def hq_grouped_gemm_workspace_bytes(M: int, K: int, E: int) -> int:
-    """Bytes of the workspace of hq_grouped_gemm_* (which this binding allocates itself)."""
-    n = _lib.load().hq_grouped_gemm_workspace_bytes(M, K, E)
-    if n < 0:
-        raise ValueError("hq_grouped_gemm_workspace_bytes: M >= 0, K a multiple of 32, 0 <= E <= 512")
-    return n
-
-
-def hq_lora_gemm_workspace_bytes(M: int, K: int, R: int) -> int:
-    """Bytes of the workspace of hq_lora_gemm_* (which this binding allocates itself)."""
-    n = _lib.load().hq_lora_gemm_workspace_bytes(M, K, R)
-    if n < 0:
-        raise ValueError("hq_lora_gemm_workspace_bytes: M >= 0, K a multiple of 32, R a multiple of 8 up to 128")
-    return n
-
-
-def _work(nbytes: int, device: torch.device, stream: torch.cuda.Stream | None) -> torch.Tensor | None:
-    """A workspace for one call; freed when the call returns, so not before ``stream`` is done with it."""
-    if nbytes == 0:
-        return None
-    work = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        work.record_stream(stream)
-    return work
-
-
-def _lora_gemm(xq, xs, x_sg, wq, ws, w_sg, x, lora_a, lora_b, scaling, row_adapter, out, out_dtype, stream):
-    block = 16 if x_sg is not None else 32
-    dev = _codes(xq, 2, "xq")
+def _lora_args(xq, wq, x, lora_a, lora_b, scaling, row_adapter):
+    """(device index, M, N, K, adapters, R, the adapters' part of the C arguments)."""
+    index = _codes(xq, 2, "xq")
     _codes(wq, 2, "wq")
     M, K2 = xq.shape
     N, K = wq.shape[0], 2 * K2
-    args = [_given(xq, (M, K2), torch.uint8, dev, "xq"),
-            _given(xs, (M, K // block), torch.uint8, dev, "xs")]
-    if x_sg is not None:
-        args.append(_given(x_sg, (1,), torch.float32, dev, "x_sg"))
-    args += [_given(wq, (N, K2), torch.uint8, dev, "wq"),
-             _given(ws, (_tiles_bytes(N, K // block),), torch.uint8, dev, "ws")]
-    if x_sg is not None:
-        args.append(_given(w_sg, (1,), torch.float32, dev, "w_sg"))
-    if not isinstance(x, torch.Tensor) or x.shape != (M, K) or x.dtype != torch.bfloat16 or x.device != dev \
+    if not isinstance(x, torch.Tensor) or x.shape != (M, K) or x.dtype is not _BF16 or x.get_device() != index \
             or x.stride(1) != 1:
-        raise ValueError(f"x must be a bfloat16 tensor of shape {(M, K)} on {dev} with contiguous rows")
+        raise ValueError(f"x must be a bfloat16 tensor of shape {(M, K)} on cuda:{index} with contiguous rows")
     if not isinstance(lora_a, torch.Tensor) or lora_a.dim() != 3:
         raise ValueError("lora_a must be [adapters, R, K]")
-    n, R = lora_a.shape[:2]
-    args += [x.data_ptr(), x.stride(0) if M > 1 else K,
-             _given(lora_a, (n, R, K), torch.bfloat16, dev, "lora_a"),
-             _given(lora_b, (n, N, R), torch.bfloat16, dev, "lora_b"),
-             _given(scaling, (n,), torch.float32, dev, "scaling"),
-             _given(row_adapter, (M,), torch.int32, dev, "row_adapter")]
-    out = _out(out, (M, N), out_dtype, dev)
-    work = _work(hq_lora_gemm_workspace_bytes(M, K, R), dev, stream)
-    args += [M, N, K, n, R, out.data_ptr(), _DTYPES[out.dtype], _addr(work)]
-    _launch(dev, "hq_lora_gemm_nvfp4" if x_sg is not None else "hq_lora_gemm_mxfp4", args, stream)
-    return out
+    n, R, _ = lora_a.shape
+    args = (x.data_ptr(), x.stride(0) if M > 1 else K, _given(lora_a, (n, R, K), _BF16, index, "lora_a"),
+            _given(lora_b, (n, N, R), _BF16, index, "lora_b"), _given(scaling, (n,), _F32, index, "scaling"),
+            _given(row_adapter, (M,), _I32, index, "row_adapter"))
+    return index, M, N, K, n, R, args
 
 
 def hq_lora_gemm_nvfp4(xq: torch.Tensor, xs: torch.Tensor, x_sg: torch.Tensor, wq: torch.Tensor,
@@ -523,9 +537,15 @@ def hq_lora_gemm_nvfp4(xq: torch.Tensor, xs: torch.Tensor, x_sg: torch.Tensor, w
     xq, xs, x_sg: x quantized (hq_quantize_nvfp4); wq uint8 [N, K/2], ws its scales in the tile layout,
     w_sg float32 [1]; x bfloat16 [M, K]; lora_a bfloat16 [n, R, K], lora_b bfloat16 [n, N, R], scaling
     float32 [n]; row_adapter int32 [M].  R a multiple of 8 up to 128."""
-    if x_sg is None:
-        raise ValueError("x_sg must be a tensor (hq_lora_gemm_mxfp4 has no per-tensor scales)")
-    return _lora_gemm(xq, xs, x_sg, wq, ws, w_sg, x, lora_a, lora_b, scaling, row_adapter, out, out_dtype, stream)
+    index, M, N, K, n, R, more = _lora_args(xq, wq, x, lora_a, lora_b, scaling, row_adapter)
+    args = (_given(xq, (M, K // 2), _U8, index, "xq"), _given(xs, (M, K // 16), _U8, index, "xs"),
+            _given(x_sg, (1,), _F32, index, "x_sg"), _given(wq, (N, K // 2), _U8, index, "wq"),
+            _given(ws, (_tiles_bytes(N, K // 16),), _U8, index, "ws"), _given(w_sg, (1,), _F32, index, "w_sg"))
+    out = _out(out, (M, N), out_dtype, xq)
+    work = _work(hq_lora_gemm_workspace_bytes(M, K, R), xq, stream)
+    _launch(index, "hq_lora_gemm_nvfp4",
+            args + more + (M, N, K, n, R, out.data_ptr(), _DTYPES[out.dtype], _addr(work)), stream)
+    return out
 
 
 def hq_lora_gemm_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, x: torch.Tensor,
@@ -534,7 +554,14 @@ def hq_lora_gemm_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws:
                        out_dtype: torch.dtype = torch.bfloat16,
                        stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """hq_lora_gemm_nvfp4 beside an MXFP4 projection."""
-    return _lora_gemm(xq, xs, None, wq, ws, None, x, lora_a, lora_b, scaling, row_adapter, out, out_dtype, stream)
+    index, M, N, K, n, R, more = _lora_args(xq, wq, x, lora_a, lora_b, scaling, row_adapter)
+    args = (_given(xq, (M, K // 2), _U8, index, "xq"), _given(xs, (M, K // 32), _U8, index, "xs"),
+            _given(wq, (N, K // 2), _U8, index, "wq"), _given(ws, (_tiles_bytes(N, K // 32),), _U8, index, "ws"))
+    out = _out(out, (M, N), out_dtype, xq)
+    work = _work(hq_lora_gemm_workspace_bytes(M, K, R), xq, stream)
+    _launch(index, "hq_lora_gemm_mxfp4",
+            args + more + (M, N, K, n, R, out.data_ptr(), _DTYPES[out.dtype], _addr(work)), stream)
+    return out
 
 
 def hq_swizzle_scales(scales: torch.Tensor, out: torch.Tensor | None = None,
@@ -545,12 +572,11 @@ def hq_swizzle_scales(scales: torch.Tensor, out: torch.Tensor | None = None,
         raise ValueError("scales must be a CUDA tensor (libhq has no CPU path)")
     if scales.dim() not in (2, 3):
         raise ValueError("scales must be [rows, cols] or [E, rows, cols]")
-    dev = scales.device
-    ptr = _given(scales, scales.shape, torch.uint8, dev, "scales")
+    ptr = _given(scales, scales.shape, _U8, scales.get_device(), "scales")
     rows, cols = scales.shape[-2:]
     groups = scales.shape[0] if scales.dim() == 3 else 1
-    out = _need(out, (*scales.shape[:-2], _tiles_bytes(rows, cols)), torch.uint8, dev, "out")
-    _launch(dev, "hq_swizzle_scales", [ptr, groups, rows, cols, out.data_ptr()], stream)
+    out = _need(out, (*scales.shape[:-2], _tiles_bytes(rows, cols)), _U8, scales.device, "out")
+    _launch(scales.get_device(), "hq_swizzle_scales", (ptr, groups, rows, cols, out.data_ptr()), stream)
     return out
 
 
@@ -560,55 +586,50 @@ _GATE_NONE, _GATE_CHANNEL, _GATE_TOKEN, _GATE_FULL = range(4)
 _NORM_POST, _NORM_PRE = 1, 2
 
 
-def _rows(t: torch.Tensor | None, like: torch.Tensor, name: str) -> tuple[int | None, int]:
-    """Address and row stride of a tensor shaped and typed like ``like`` (None: absent)."""
-    if t is None:
-        return None, like.shape[1]
-    if not isinstance(t, torch.Tensor) or t.shape != like.shape or t.dtype != like.dtype or t.device != like.device \
-            or t.stride(1) != 1:
+def _rows(t: torch.Tensor, like: torch.Tensor, name: str) -> tuple[int, int]:
+    """Address and row stride of a tensor shaped and typed like ``like``."""
+    if not isinstance(t, torch.Tensor) or t.shape != like.shape or t.dtype is not like.dtype \
+            or t.get_device() != like.get_device() or t.stride(1) != 1:
         raise ValueError(f"{name} must be a {like.dtype} tensor of shape {tuple(like.shape)} on {like.device} with "
                          "contiguous rows")
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-def _norm_params(h: torch.Tensor, has_y: bool, w_post, gate, w_pre, post: bool, pre: bool):
-    """(w_post, w_pre, parameter dtype, gate kind, gate, gate row stride) for the C calls."""
+def _norm_params(h: torch.Tensor, has_y: bool, w_post, gate, w_pre, post: bool, pre: bool) -> tuple:
+    """(w_post, w_pre, parameter dtype, gate kind, gate, gate row stride) of the C calls."""
     M, D = h.shape
-    dtypes = set()
-
-    def vector(w, name):
+    index = h.get_device()
+    dtype = None  # of the parameter vectors, one for all
+    addr = [None, None, None]
+    per_channel = gate is not None and gate.dim() == 1
+    for i, (w, name) in enumerate(((w_post, "w_post"), (w_pre, "w_pre"), (gate if per_channel else None, "gate"))):
         if w is None:
-            return None
-        if not isinstance(w, torch.Tensor) or w.shape != (D,) or w.dtype not in _DTYPES or w.device != h.device \
-                or not w.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 or bfloat16 tensor [{D}] on {h.device}")
-        dtypes.add(w.dtype)
-        return w.data_ptr()
-
-    if not post and w_post is not None:
-        raise ValueError("w_post without post_norm")
-    if not pre and w_pre is not None:
+            continue
+        if dtype is None:
+            dtype = w.dtype
+            if dtype not in _DTYPES:
+                raise ValueError(f"{name} must be float32 or bfloat16, got {dtype}")
+        addr[i] = _given(w, (D,), dtype, index, name)
+    if w_post is not None and not post:
+        raise ValueError("w_post without a post norm")
+    if w_pre is not None and not pre:
         raise ValueError("w_pre without pre_norm")
-    wp, wq = vector(w_post, "w_post"), vector(w_pre, "w_pre")
-    kind, g, ld = _GATE_NONE, None, 0
+    kind, ld = _GATE_NONE, 0
     if gate is not None:
         if not has_y:
             raise ValueError("gate without y")
-        if not isinstance(gate, torch.Tensor):
-            raise ValueError("gate must be a tensor")
-        if gate.dim() == 1:
-            kind, g = _GATE_CHANNEL, vector(gate, "gate")
-        elif gate.shape == (M, 1) and D != 1:
-            if gate.dtype not in _DTYPES or gate.device != h.device or not gate.is_contiguous():
-                raise ValueError(f"gate [M, 1] must be a contiguous float32 or bfloat16 tensor on {h.device}")
-            dtypes.add(gate.dtype)
-            kind, g = _GATE_TOKEN, gate.data_ptr()
+        if per_channel:
+            kind = _GATE_CHANNEL
+        elif gate.shape == (M, 1):
+            kind = _GATE_TOKEN
+            dtype = gate.dtype if dtype is None else dtype
+            if dtype not in _DTYPES:
+                raise ValueError(f"gate must be float32 or bfloat16, got {dtype}")
+            addr[2] = _given(gate, (M, 1), dtype, index, "gate [M, 1]")
         else:
             kind = _GATE_FULL
-            g, ld = _rows(gate, h, "gate ([D], [M, 1] or [M, D])")
-    if len(dtypes) > 1:
-        raise ValueError("w_post, w_pre and a gate [D] or [M, 1] must have one dtype")
-    return wp, wq, _DTYPES[dtypes.pop()] if dtypes else HQ_F32, kind, g, ld
+            addr[2], ld = _rows(gate, h, "gate ([D], [M, 1] or [M, D])")
+    return addr[0], addr[1], HQ_F32 if dtype is None else _DTYPES[dtype], kind, addr[2], ld
 
 
 def _norm_input(t: torch.Tensor, name: str) -> None:
@@ -632,26 +653,40 @@ def hq_block_norm(h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.
     norm of h alone (h_out is h).  Norms are x / sqrt(mean(x^2) + eps); weights default to ones."""
     _norm_input(h, "h")
     M, D = h.shape
-    post = post_norm and y is not None
+    device, dtype = h.device, h.dtype
+    has_y = y is not None
+    post = post_norm and has_y
     hp, ld_h = _rows(h, h, "h")
-    yp, ld_y = _rows(y, h, "y")
-    wp, wq, pdt, kind, g, ld_g = _norm_params(h, y is not None, w_post, gate, w_pre, post, pre_norm)
-    if y is not None:
-        h_out = _need(h_out, (M, D), h.dtype, h.device, "h_out")
-    else:
+    yp, ld_y = _rows(y, h, "y") if has_y else (None, D)
+    params = _norm_params(h, has_y, w_post, gate, w_pre, post, pre_norm)
+    if not has_y:
         h_out = h
-    n = _need(n, (M, D), h.dtype, h.device, "n") if pre_norm else None
-    r_post = torch.empty(M, dtype=torch.float32, device=h.device) if post else None
-    r_pre = torch.empty(M, dtype=torch.float32, device=h.device) if pre_norm else None
-    amax = torch.empty(1, dtype=torch.float32, device=h.device) if amax_group is not None else None
-    _launch(h.device, "hq_block_norm",
-            [hp, ld_h, yp, ld_y, _DTYPES[h.dtype], M, D, wp, wq, pdt, kind, g, ld_g,
+    elif h_out is None:
+        h_out = torch.empty((M, D), dtype=dtype, device=device)
+    else:
+        _given(h_out, (M, D), dtype, h.get_device(), "h_out")
+    r_post = r_pre = amax = None
+    if pre_norm:
+        if n is None:
+            n = torch.empty((M, D), dtype=dtype, device=device)
+        else:
+            _given(n, (M, D), dtype, h.get_device(), "n")
+        r_pre = torch.empty(M, dtype=_F32, device=device)
+    else:
+        n = None
+    if post:
+        r_post = torch.empty(M, dtype=_F32, device=device)
+    if amax_group is not None:
+        amax = torch.empty(1, dtype=_F32, device=device)
+    _launch(h.get_device(), "hq_block_norm",
+            (hp, ld_h, yp, ld_y, _DTYPES[dtype], M, D, *params,
              (_NORM_POST if post else 0) | (_NORM_PRE if pre_norm else 0), alpha, eps,
-             h_out.data_ptr() if y is not None else None, _addr(n), _addr(r_post), _addr(r_pre), amax_group or 0,
-             _addr(amax)], stream)
+             h_out.data_ptr() if has_y else None, _addr(n), _addr(r_post), _addr(r_pre), amax_group or 0,
+             _addr(amax)), stream)
     return (h_out, n, r_post, r_pre) if amax is None else (h_out, n, r_post, r_pre, amax)
 
 
+@functools.lru_cache(maxsize=1024)
 def hq_block_norm_bwd_workspace_bytes(M: int, D: int) -> int:
     """Bytes of the workspace of hq_block_norm_bwd (which this binding allocates itself)."""
     n = _lib.load().hq_block_norm_bwd_workspace_bytes(M, D)
@@ -673,35 +708,36 @@ def hq_block_norm_bwd(dh_out: torch.Tensor | None, dn: torch.Tensor | None, h_ou
     and [M, 1] are float32, summed over the rows in a fixed order; that of a gate [M, D] has its dtype."""
     _norm_input(h_out, "h_out")
     M, D = h_out.shape
-    dev = h_out.device
-    post = post_norm and y is not None
+    device, dtype, index = h_out.device, h_out.dtype, h_out.get_device()
+    has_y = y is not None
+    post = post_norm and has_y
     if pre_norm and (dn is None or r_pre is None):
         raise ValueError("dn and r_pre are needed with pre_norm")
     if not pre_norm and (dn is not None or dh_out is None):
         raise ValueError("without pre_norm there is no dn, and dh_out is needed")
     if post and r_post is None:
         raise ValueError("r_post is needed with post_norm")
-    (dhp, ld_dh), (dnp, ld_dn) = _rows(dh_out, h_out, "dh_out"), _rows(dn, h_out, "dn")
-    (hp, ld_h), (yp, ld_y) = _rows(h_out, h_out, "h_out"), _rows(y, h_out, "y")
-    wp, wq, pdt, kind, g, ld_g = _norm_params(h_out, y is not None, w_post, gate, w_pre, post, pre_norm)
-    rp = _given(r_post, (M,), torch.float32, dev, "r_post") if post else None
-    rq = _given(r_pre, (M,), torch.float32, dev, "r_pre") if pre_norm else None
-    dh = torch.empty((M, D), dtype=h_out.dtype, device=dev)
-    dy = torch.empty((M, D), dtype=h_out.dtype, device=dev) if y is not None else None
-    dw_post = torch.empty(D, dtype=torch.float32, device=dev) if w_post is not None else None
-    dw_pre = torch.empty(D, dtype=torch.float32, device=dev) if w_pre is not None else None
-    dgate = None if kind == _GATE_NONE else torch.empty(
-        gate.shape, dtype=h_out.dtype if kind == _GATE_FULL else torch.float32, device=dev)
-    work = _work(hq_block_norm_bwd_workspace_bytes(M, D), dev, stream)
-    _launch(dev, "hq_block_norm_bwd",
-            [dhp, ld_dh, dnp, ld_dn, hp, ld_h, yp, ld_y, _DTYPES[h_out.dtype], M, D, wp, wq, pdt, kind, g, ld_g,
+    dhp, ld_dh = _rows(dh_out, h_out, "dh_out") if dh_out is not None else (None, D)
+    dnp, ld_dn = _rows(dn, h_out, "dn") if pre_norm else (None, D)
+    hp, ld_h = _rows(h_out, h_out, "h_out")
+    yp, ld_y = _rows(y, h_out, "y") if has_y else (None, D)
+    params = _norm_params(h_out, has_y, w_post, gate, w_pre, post, pre_norm)
+    kind = params[3]
+    rp = _given(r_post, (M,), _F32, index, "r_post") if post else None
+    rq = _given(r_pre, (M,), _F32, index, "r_pre") if pre_norm else None
+    dh = torch.empty((M, D), dtype=dtype, device=device)
+    dy = torch.empty((M, D), dtype=dtype, device=device) if has_y else None
+    dw_post = torch.empty(D, dtype=_F32, device=device) if w_post is not None else None
+    dw_pre = torch.empty(D, dtype=_F32, device=device) if w_pre is not None else None
+    dgate = None
+    if kind != _GATE_NONE:
+        dgate = torch.empty(gate.shape, dtype=dtype if kind == _GATE_FULL else _F32, device=device)
+    work = _work(hq_block_norm_bwd_workspace_bytes(M, D), h_out, stream)
+    _launch(index, "hq_block_norm_bwd",
+            (dhp, ld_dh, dnp, ld_dn, hp, ld_h, yp, ld_y, _DTYPES[dtype], M, D, *params,
              (_NORM_POST if post else 0) | (_NORM_PRE if pre_norm else 0), rp, rq, alpha, dh.data_ptr(),
-             _addr(dy), _addr(dw_post), _addr(dgate), _addr(dw_pre), _addr(work)], stream)
+             _addr(dy), _addr(dw_post), _addr(dgate), _addr(dw_pre), _addr(work)), stream)
     return dh, dy, dw_post, dgate, dw_pre
-
-
-def _addr(t: torch.Tensor | None) -> int | None:
-    return None if t is None else t.data_ptr()
 
 
 def quantize_nvfp4(x: torch.Tensor, group: int, stream: torch.cuda.Stream | None = None):
