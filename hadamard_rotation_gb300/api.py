@@ -7,7 +7,6 @@ Inputs must be CUDA tensors: there is no CPU path.
 from __future__ import annotations
 
 import ctypes
-import functools
 
 import torch
 
@@ -321,85 +320,25 @@ def hq_dequant_nvfp4(q: torch.Tensor, scales: torch.Tensor, s_global: torch.Tens
 
 # ---- products of the codes -------------------------------------------------------------------
 #
-# A call of a few rows takes the GPU a few microseconds, so what these functions do per call counts:
-# one check per operand, the device switched only where another one is current, and addresses and
-# streams passed as plain integers.
+# A call of a few rows takes the GPU a few microseconds, so the products' and norms' arguments are checked and
+# marshalled in C++ (csrc/hq_torch.cpp, built beside libhq.so); the functions here are their
+# documentation and signatures.
 
-_U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
-_FUNCTIONS: dict[str, object] = {}
-
-
-def _launch(index: int, name: str, args: tuple, stream: torch.cuda.Stream | None) -> None:
-    """Call the C entry point ``name`` with device ``index`` current, on ``stream`` or that device's current
-    stream; raise on a non-OK status."""
-    fn = _FUNCTIONS.get(name)
-    if fn is None:
-        fn = _FUNCTIONS[name] = getattr(_lib.load(), name)
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
-    elif stream.device.index != index:
-        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
-    else:
-        handle = stream.cuda_stream
-    if torch._C._cuda_getDevice() == index:
-        status = fn(*args, handle)
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args, handle)
-    if status:
-        check(status, name)
+_calls = None
 
 
-def _given(t: torch.Tensor, shape: tuple, dtype: torch.dtype, index: int, name: str) -> int:
-    """The address of an operand that must be there, of this shape and type, contiguous, on device
-    ``index``."""
+def _load_calls():
+    global _calls
+    _lib.load()
     try:
-        if t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:  # not a tensor
-        pass
-    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
+        from . import _torch_calls
+    except ImportError as e:
+        raise RuntimeError("_torch_calls.so is not built, or not for this torch; build it first "
+                           "(python -m hadamard_rotation_gb300.build, or __graft_entry__.build())") from e
+    _calls = _torch_calls
+    return _calls
 
 
-def _codes(q: torch.Tensor, dims: int, name: str) -> int:
-    """The device index of a tensor of codes."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (libhq has no CPU path)")
-    if q.dim() != dims or q.dtype is not _U8:
-        raise ValueError(f"{name} must be a {dims}-D uint8 tensor of codes")
-    return q.get_device()
-
-
-def _tiles_bytes(rows: int, cols: int) -> int:
-    return (rows + 127) // 128 * ((cols + 3) // 4) * 512
-
-
-def _out(out: torch.Tensor | None, shape: tuple, dtype: torch.dtype, like: torch.Tensor) -> torch.Tensor:
-    if out is None:
-        if dtype not in _DTYPES:
-            raise ValueError(f"out_dtype must be float32 or bfloat16, got {dtype}")
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if out.dtype not in _DTYPES:
-        raise ValueError(f"out must be float32 or bfloat16, got {out.dtype}")
-    _given(out, shape, out.dtype, like.get_device(), "out")
-    return out
-
-
-def _addr(t: torch.Tensor | None) -> int | None:
-    return None if t is None else t.data_ptr()
-
-
-def _work(nbytes: int, like: torch.Tensor, stream: torch.cuda.Stream | None) -> torch.Tensor | None:
-    """A workspace for one call; freed when the call returns, so not before ``stream`` is done with it."""
-    if nbytes == 0:
-        return None
-    work = torch.empty(nbytes, dtype=_U8, device=like.device)
-    if stream is not None:
-        work.record_stream(stream)
-    return work
-
-
-@functools.lru_cache(maxsize=1024)
 def hq_grouped_gemm_workspace_bytes(M: int, K: int, E: int) -> int:
     """Bytes of the workspace of hq_grouped_gemm_* (which this binding allocates itself)."""
     n = _lib.load().hq_grouped_gemm_workspace_bytes(M, K, E)
@@ -408,7 +347,6 @@ def hq_grouped_gemm_workspace_bytes(M: int, K: int, E: int) -> int:
     return n
 
 
-@functools.lru_cache(maxsize=1024)
 def hq_lora_gemm_workspace_bytes(M: int, K: int, R: int) -> int:
     """Bytes of the workspace of hq_lora_gemm_* (which this binding allocates itself)."""
     n = _lib.load().hq_lora_gemm_workspace_bytes(M, K, R)
@@ -428,19 +366,7 @@ def hq_grouped_gemm_nvfp4(xq: torch.Tensor, xs: torch.Tensor, x_sg: torch.Tensor
     writes them; wq uint8 [E, N, K/2], ws uint8 [E, hq_swizzled_scales_bytes(N, K)] in the tile
     layout (hq_swizzle_scales), w_sg float32 [E]; offsets int32 [E + 1].  Rows of no group are left
     as they are in ``out``."""
-    index = _codes(xq, 2, "xq")
-    _codes(wq, 3, "wq")
-    M, K2 = xq.shape
-    E, N, _ = wq.shape
-    args = (_given(xq, (M, K2), _U8, index, "xq"), _given(xs, (M, K2 // 8), _U8, index, "xs"),
-            _given(x_sg, (1,), _F32, index, "x_sg"), _given(wq, (E, N, K2), _U8, index, "wq"),
-            _given(ws, (E, _tiles_bytes(N, K2 // 8)), _U8, index, "ws"), _given(w_sg, (E,), _F32, index, "w_sg"),
-            _given(offsets, (E + 1,), _I32, index, "offsets"))
-    out = _out(out, (M, N), out_dtype, xq)
-    work = _work(hq_grouped_gemm_workspace_bytes(M, 2 * K2, E), xq, stream)
-    _launch(index, "hq_grouped_gemm_nvfp4",
-            args + (M, N, 2 * K2, E, out.data_ptr(), _DTYPES[out.dtype], _addr(work)), stream)
-    return out
+    return (_calls or _load_calls()).grouped_gemm_nvfp4(xq, xs, x_sg, wq, ws, w_sg, offsets, out, out_dtype, stream)
 
 
 def hq_grouped_gemm_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
@@ -449,24 +375,7 @@ def hq_grouped_gemm_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, 
                           stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """hq_grouped_gemm_nvfp4 for MXFP4 operands: xs uint8 [M, K/32] as hq_rotate_quant_mxfp4 writes it,
     ws uint8 [E, ...] = hq_swizzle_scales of [E, N, K/32]."""
-    index = _codes(xq, 2, "xq")
-    _codes(wq, 3, "wq")
-    M, K2 = xq.shape
-    E, N, _ = wq.shape
-    args = (_given(xq, (M, K2), _U8, index, "xq"), _given(xs, (M, K2 // 16), _U8, index, "xs"),
-            _given(wq, (E, N, K2), _U8, index, "wq"), _given(ws, (E, _tiles_bytes(N, K2 // 16)), _U8, index, "ws"),
-            _given(offsets, (E + 1,), _I32, index, "offsets"))
-    out = _out(out, (M, N), out_dtype, xq)
-    work = _work(hq_grouped_gemm_workspace_bytes(M, 2 * K2, E), xq, stream)
-    _launch(index, "hq_grouped_gemm_mxfp4",
-            args + (M, N, 2 * K2, E, out.data_ptr(), _DTYPES[out.dtype], _addr(work)), stream)
-    return out
-
-
-def _groups(offsets: torch.Tensor) -> int:
-    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
-        raise ValueError("offsets must be a 1-D int32 tensor of E + 1 values")
-    return offsets.shape[0] - 1
+    return (_calls or _load_calls()).grouped_gemm_mxfp4(xq, xs, None, wq, ws, None, offsets, out, out_dtype, stream)
 
 
 def hq_grouped_wgrad_nvfp4(gq: torch.Tensor, gs: torch.Tensor, g_sg: torch.Tensor, xq: torch.Tensor,
@@ -478,17 +387,7 @@ def hq_grouped_wgrad_nvfp4(gq: torch.Tensor, gs: torch.Tensor, g_sg: torch.Tenso
     gq uint8 [N, T/2] and xq uint8 [K, T/2]: dy and x transposed and quantized along the tokens, each
     expert padded with zeros to a multiple of 128 tokens; gs, xs their scales in the tile layout
     (hq_rotate_quant_nvfp4_swizzled writes it); offsets int32 [E + 1], multiples of 128."""
-    index = _codes(gq, 2, "gq")
-    _codes(xq, 2, "xq")
-    N, T2 = gq.shape
-    K, E = xq.shape[0], _groups(offsets)
-    args = (_given(gq, (N, T2), _U8, index, "gq"), _given(gs, (_tiles_bytes(N, T2 // 8),), _U8, index, "gs"),
-            _given(g_sg, (1,), _F32, index, "g_sg"), _given(xq, (K, T2), _U8, index, "xq"),
-            _given(xs, (_tiles_bytes(K, T2 // 8),), _U8, index, "xs"), _given(x_sg, (1,), _F32, index, "x_sg"),
-            _given(offsets, (E + 1,), _I32, index, "offsets"))
-    out = _out(out, (E, N, K), out_dtype, gq)
-    _launch(index, "hq_grouped_wgrad_nvfp4", args + (2 * T2, N, K, E, out.data_ptr(), _DTYPES[out.dtype]), stream)
-    return out
+    return (_calls or _load_calls()).grouped_wgrad_nvfp4(gq, gs, g_sg, xq, xs, x_sg, offsets, out, out_dtype, stream)
 
 
 def hq_grouped_wgrad_mxfp4(gq: torch.Tensor, gs: torch.Tensor, xq: torch.Tensor, xs: torch.Tensor,
@@ -496,34 +395,7 @@ def hq_grouped_wgrad_mxfp4(gq: torch.Tensor, gs: torch.Tensor, xq: torch.Tensor,
                            out_dtype: torch.dtype = torch.bfloat16,
                            stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """hq_grouped_wgrad_nvfp4 for MXFP4 operands (scales through hq_swizzle_scales)."""
-    index = _codes(gq, 2, "gq")
-    _codes(xq, 2, "xq")
-    N, T2 = gq.shape
-    K, E = xq.shape[0], _groups(offsets)
-    args = (_given(gq, (N, T2), _U8, index, "gq"), _given(gs, (_tiles_bytes(N, T2 // 16),), _U8, index, "gs"),
-            _given(xq, (K, T2), _U8, index, "xq"), _given(xs, (_tiles_bytes(K, T2 // 16),), _U8, index, "xs"),
-            _given(offsets, (E + 1,), _I32, index, "offsets"))
-    out = _out(out, (E, N, K), out_dtype, gq)
-    _launch(index, "hq_grouped_wgrad_mxfp4", args + (2 * T2, N, K, E, out.data_ptr(), _DTYPES[out.dtype]), stream)
-    return out
-
-
-def _lora_args(xq, wq, x, lora_a, lora_b, scaling, row_adapter):
-    """(device index, M, N, K, adapters, R, the adapters' part of the C arguments)."""
-    index = _codes(xq, 2, "xq")
-    _codes(wq, 2, "wq")
-    M, K2 = xq.shape
-    N, K = wq.shape[0], 2 * K2
-    if not isinstance(x, torch.Tensor) or x.shape != (M, K) or x.dtype is not _BF16 or x.get_device() != index \
-            or x.stride(1) != 1:
-        raise ValueError(f"x must be a bfloat16 tensor of shape {(M, K)} on cuda:{index} with contiguous rows")
-    if not isinstance(lora_a, torch.Tensor) or lora_a.dim() != 3:
-        raise ValueError("lora_a must be [adapters, R, K]")
-    n, R, _ = lora_a.shape
-    args = (x.data_ptr(), x.stride(0) if M > 1 else K, _given(lora_a, (n, R, K), _BF16, index, "lora_a"),
-            _given(lora_b, (n, N, R), _BF16, index, "lora_b"), _given(scaling, (n,), _F32, index, "scaling"),
-            _given(row_adapter, (M,), _I32, index, "row_adapter"))
-    return index, M, N, K, n, R, args
+    return (_calls or _load_calls()).grouped_wgrad_mxfp4(gq, gs, None, xq, xs, None, offsets, out, out_dtype, stream)
 
 
 def hq_lora_gemm_nvfp4(xq: torch.Tensor, xs: torch.Tensor, x_sg: torch.Tensor, wq: torch.Tensor,
@@ -537,15 +409,8 @@ def hq_lora_gemm_nvfp4(xq: torch.Tensor, xs: torch.Tensor, x_sg: torch.Tensor, w
     xq, xs, x_sg: x quantized (hq_quantize_nvfp4); wq uint8 [N, K/2], ws its scales in the tile layout,
     w_sg float32 [1]; x bfloat16 [M, K]; lora_a bfloat16 [n, R, K], lora_b bfloat16 [n, N, R], scaling
     float32 [n]; row_adapter int32 [M].  R a multiple of 8 up to 128."""
-    index, M, N, K, n, R, more = _lora_args(xq, wq, x, lora_a, lora_b, scaling, row_adapter)
-    args = (_given(xq, (M, K // 2), _U8, index, "xq"), _given(xs, (M, K // 16), _U8, index, "xs"),
-            _given(x_sg, (1,), _F32, index, "x_sg"), _given(wq, (N, K // 2), _U8, index, "wq"),
-            _given(ws, (_tiles_bytes(N, K // 16),), _U8, index, "ws"), _given(w_sg, (1,), _F32, index, "w_sg"))
-    out = _out(out, (M, N), out_dtype, xq)
-    work = _work(hq_lora_gemm_workspace_bytes(M, K, R), xq, stream)
-    _launch(index, "hq_lora_gemm_nvfp4",
-            args + more + (M, N, K, n, R, out.data_ptr(), _DTYPES[out.dtype], _addr(work)), stream)
-    return out
+    return (_calls or _load_calls()).lora_gemm_nvfp4(xq, xs, x_sg, wq, ws, w_sg, x, lora_a, lora_b, scaling,
+                                                      row_adapter, out, out_dtype, stream)
 
 
 def hq_lora_gemm_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor, x: torch.Tensor,
@@ -554,14 +419,8 @@ def hq_lora_gemm_mxfp4(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws:
                        out_dtype: torch.dtype = torch.bfloat16,
                        stream: torch.cuda.Stream | None = None) -> torch.Tensor:
     """hq_lora_gemm_nvfp4 beside an MXFP4 projection."""
-    index, M, N, K, n, R, more = _lora_args(xq, wq, x, lora_a, lora_b, scaling, row_adapter)
-    args = (_given(xq, (M, K // 2), _U8, index, "xq"), _given(xs, (M, K // 32), _U8, index, "xs"),
-            _given(wq, (N, K // 2), _U8, index, "wq"), _given(ws, (_tiles_bytes(N, K // 32),), _U8, index, "ws"))
-    out = _out(out, (M, N), out_dtype, xq)
-    work = _work(hq_lora_gemm_workspace_bytes(M, K, R), xq, stream)
-    _launch(index, "hq_lora_gemm_mxfp4",
-            args + more + (M, N, K, n, R, out.data_ptr(), _DTYPES[out.dtype], _addr(work)), stream)
-    return out
+    return (_calls or _load_calls()).lora_gemm_mxfp4(xq, xs, None, wq, ws, None, x, lora_a, lora_b, scaling,
+                                                      row_adapter, out, out_dtype, stream)
 
 
 def hq_swizzle_scales(scales: torch.Tensor, out: torch.Tensor | None = None,
@@ -572,71 +431,16 @@ def hq_swizzle_scales(scales: torch.Tensor, out: torch.Tensor | None = None,
         raise ValueError("scales must be a CUDA tensor (libhq has no CPU path)")
     if scales.dim() not in (2, 3):
         raise ValueError("scales must be [rows, cols] or [E, rows, cols]")
-    ptr = _given(scales, scales.shape, _U8, scales.get_device(), "scales")
+    scales = _need(scales, scales.shape, torch.uint8, scales.device, "scales")
     rows, cols = scales.shape[-2:]
     groups = scales.shape[0] if scales.dim() == 3 else 1
-    out = _need(out, (*scales.shape[:-2], _tiles_bytes(rows, cols)), _U8, scales.device, "out")
-    _launch(scales.get_device(), "hq_swizzle_scales", (ptr, groups, rows, cols, out.data_ptr()), stream)
+    out = _need(out, (*scales.shape[:-2], (rows + 127) // 128 * ((cols + 3) // 4) * 512), torch.uint8, scales.device,
+                "out")
+    _call(scales.device, "hq_swizzle_scales", _ptr(scales), groups, rows, cols, _ptr(out), stream=stream)
     return out
 
 
 # ---- norms before and after a block ------------------------------------------------------------
-
-_GATE_NONE, _GATE_CHANNEL, _GATE_TOKEN, _GATE_FULL = range(4)
-_NORM_POST, _NORM_PRE = 1, 2
-
-
-def _rows(t: torch.Tensor, like: torch.Tensor, name: str) -> tuple[int, int]:
-    """Address and row stride of a tensor shaped and typed like ``like``."""
-    if not isinstance(t, torch.Tensor) or t.shape != like.shape or t.dtype is not like.dtype \
-            or t.get_device() != like.get_device() or t.stride(1) != 1:
-        raise ValueError(f"{name} must be a {like.dtype} tensor of shape {tuple(like.shape)} on {like.device} with "
-                         "contiguous rows")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _norm_params(h: torch.Tensor, has_y: bool, w_post, gate, w_pre, post: bool, pre: bool) -> tuple:
-    """(w_post, w_pre, parameter dtype, gate kind, gate, gate row stride) of the C calls."""
-    M, D = h.shape
-    index = h.get_device()
-    dtype = None  # of the parameter vectors, one for all
-    addr = [None, None, None]
-    per_channel = gate is not None and gate.dim() == 1
-    for i, (w, name) in enumerate(((w_post, "w_post"), (w_pre, "w_pre"), (gate if per_channel else None, "gate"))):
-        if w is None:
-            continue
-        if dtype is None:
-            dtype = w.dtype
-            if dtype not in _DTYPES:
-                raise ValueError(f"{name} must be float32 or bfloat16, got {dtype}")
-        addr[i] = _given(w, (D,), dtype, index, name)
-    if w_post is not None and not post:
-        raise ValueError("w_post without a post norm")
-    if w_pre is not None and not pre:
-        raise ValueError("w_pre without pre_norm")
-    kind, ld = _GATE_NONE, 0
-    if gate is not None:
-        if not has_y:
-            raise ValueError("gate without y")
-        if per_channel:
-            kind = _GATE_CHANNEL
-        elif gate.shape == (M, 1):
-            kind = _GATE_TOKEN
-            dtype = gate.dtype if dtype is None else dtype
-            if dtype not in _DTYPES:
-                raise ValueError(f"gate must be float32 or bfloat16, got {dtype}")
-            addr[2] = _given(gate, (M, 1), dtype, index, "gate [M, 1]")
-        else:
-            kind = _GATE_FULL
-            addr[2], ld = _rows(gate, h, "gate ([D], [M, 1] or [M, D])")
-    return addr[0], addr[1], HQ_F32 if dtype is None else _DTYPES[dtype], kind, addr[2], ld
-
-
-def _norm_input(t: torch.Tensor, name: str) -> None:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (libhq has no CPU path)")
-    if t.dim() != 2 or t.dtype not in _DTYPES:
-        raise ValueError(f"{name} must be a 2-D float32 or bfloat16 tensor [M, D]")
 
 
 def hq_block_norm(h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
@@ -651,42 +455,10 @@ def hq_block_norm(h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.
 
     ``gate``: [D], [M, 1] or [M, D].  ``post_norm=False``: y is added without a norm.  ``y=None``: the
     norm of h alone (h_out is h).  Norms are x / sqrt(mean(x^2) + eps); weights default to ones."""
-    _norm_input(h, "h")
-    M, D = h.shape
-    device, dtype = h.device, h.dtype
-    has_y = y is not None
-    post = post_norm and has_y
-    hp, ld_h = _rows(h, h, "h")
-    yp, ld_y = _rows(y, h, "y") if has_y else (None, D)
-    params = _norm_params(h, has_y, w_post, gate, w_pre, post, pre_norm)
-    if not has_y:
-        h_out = h
-    elif h_out is None:
-        h_out = torch.empty((M, D), dtype=dtype, device=device)
-    else:
-        _given(h_out, (M, D), dtype, h.get_device(), "h_out")
-    r_post = r_pre = amax = None
-    if pre_norm:
-        if n is None:
-            n = torch.empty((M, D), dtype=dtype, device=device)
-        else:
-            _given(n, (M, D), dtype, h.get_device(), "n")
-        r_pre = torch.empty(M, dtype=_F32, device=device)
-    else:
-        n = None
-    if post:
-        r_post = torch.empty(M, dtype=_F32, device=device)
-    if amax_group is not None:
-        amax = torch.empty(1, dtype=_F32, device=device)
-    _launch(h.get_device(), "hq_block_norm",
-            (hp, ld_h, yp, ld_y, _DTYPES[dtype], M, D, *params,
-             (_NORM_POST if post else 0) | (_NORM_PRE if pre_norm else 0), alpha, eps,
-             h_out.data_ptr() if has_y else None, _addr(n), _addr(r_post), _addr(r_pre), amax_group or 0,
-             _addr(amax)), stream)
-    return (h_out, n, r_post, r_pre) if amax is None else (h_out, n, r_post, r_pre, amax)
+    return (_calls or _load_calls()).block_norm(h, y, w_post, gate, w_pre, alpha, eps, post_norm, pre_norm, amax_group,
+                                                 h_out, n, stream)
 
 
-@functools.lru_cache(maxsize=1024)
 def hq_block_norm_bwd_workspace_bytes(M: int, D: int) -> int:
     """Bytes of the workspace of hq_block_norm_bwd (which this binding allocates itself)."""
     n = _lib.load().hq_block_norm_bwd_workspace_bytes(M, D)
@@ -706,38 +478,8 @@ def hq_block_norm_bwd(dh_out: torch.Tensor | None, dn: torch.Tensor | None, h_ou
     ``dh_out`` (None: zeros) and ``dn`` are the gradients at h_out and n; h_out, r_post and r_pre are what
     the forward call returned (h itself where y is None).  dw_post, dw_pre and the gradients of gates [D]
     and [M, 1] are float32, summed over the rows in a fixed order; that of a gate [M, D] has its dtype."""
-    _norm_input(h_out, "h_out")
-    M, D = h_out.shape
-    device, dtype, index = h_out.device, h_out.dtype, h_out.get_device()
-    has_y = y is not None
-    post = post_norm and has_y
-    if pre_norm and (dn is None or r_pre is None):
-        raise ValueError("dn and r_pre are needed with pre_norm")
-    if not pre_norm and (dn is not None or dh_out is None):
-        raise ValueError("without pre_norm there is no dn, and dh_out is needed")
-    if post and r_post is None:
-        raise ValueError("r_post is needed with post_norm")
-    dhp, ld_dh = _rows(dh_out, h_out, "dh_out") if dh_out is not None else (None, D)
-    dnp, ld_dn = _rows(dn, h_out, "dn") if pre_norm else (None, D)
-    hp, ld_h = _rows(h_out, h_out, "h_out")
-    yp, ld_y = _rows(y, h_out, "y") if has_y else (None, D)
-    params = _norm_params(h_out, has_y, w_post, gate, w_pre, post, pre_norm)
-    kind = params[3]
-    rp = _given(r_post, (M,), _F32, index, "r_post") if post else None
-    rq = _given(r_pre, (M,), _F32, index, "r_pre") if pre_norm else None
-    dh = torch.empty((M, D), dtype=dtype, device=device)
-    dy = torch.empty((M, D), dtype=dtype, device=device) if has_y else None
-    dw_post = torch.empty(D, dtype=_F32, device=device) if w_post is not None else None
-    dw_pre = torch.empty(D, dtype=_F32, device=device) if w_pre is not None else None
-    dgate = None
-    if kind != _GATE_NONE:
-        dgate = torch.empty(gate.shape, dtype=dtype if kind == _GATE_FULL else _F32, device=device)
-    work = _work(hq_block_norm_bwd_workspace_bytes(M, D), h_out, stream)
-    _launch(index, "hq_block_norm_bwd",
-            (dhp, ld_dh, dnp, ld_dn, hp, ld_h, yp, ld_y, _DTYPES[dtype], M, D, *params,
-             (_NORM_POST if post else 0) | (_NORM_PRE if pre_norm else 0), rp, rq, alpha, dh.data_ptr(),
-             _addr(dy), _addr(dw_post), _addr(dgate), _addr(dw_pre), _addr(work)), stream)
-    return dh, dy, dw_post, dgate, dw_pre
+    return (_calls or _load_calls()).block_norm_bwd(dh_out, dn, h_out, y, w_post, gate, w_pre, r_post, r_pre, alpha,
+                                                     post_norm, pre_norm, stream)
 
 
 def quantize_nvfp4(x: torch.Tensor, group: int, stream: torch.cuda.Stream | None = None):

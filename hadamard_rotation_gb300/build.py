@@ -1,4 +1,5 @@
-"""Compile libhq.so (the CUDA kernels and the C ABI) in-tree for sm_103a.
+"""Compile libhq.so (the CUDA kernels and the C ABI) in-tree for sm_103a, and beside it _torch_calls.so (the
+products' and norms' calls over torch tensors, C++).
 
 No fast-math: the kernels rely on IEEE division, correctly rounded reciprocals and
 denormal support.
@@ -8,6 +9,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +23,8 @@ DEPS = SOURCES + [os.path.join(CSRC, "hq_kernels.cuh"), os.path.join(CSRC, "hq_i
                   os.path.join(CSRC, "hq_internal.h"),
                   os.path.join(INCLUDE, "hq.h")]
 LIB = os.path.join(PKG, "libhq.so")
+CALLS_SOURCE = os.path.join(CSRC, "hq_torch.cpp")
+CALLS = os.path.join(PKG, "_torch_calls.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -40,11 +44,30 @@ def nvcc_link_command(objs: list[str], out: str) -> list[str]:
     return [nvcc_path(), ARCH, "-shared", "-o", out, *objs]
 
 
+def calls_compile_command(src: str, obj: str) -> list[str]:
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c",
+            "-I", INCLUDE, "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-I", sysconfig.get_paths()["include"],
+            "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include"), "-o", obj, src]
+
+
+def calls_link_command(obj: str, out: str) -> list[str]:
+    import torch
+
+    return [shutil.which("g++") or "g++", "-shared", "-o", out, obj, "-L", os.path.dirname(LIB), "-lhq",
+            "-Wl,-rpath,$ORIGIN", "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in DEPS)
+    t, c = os.path.getmtime(LIB), os.path.getmtime(CALLS)
+    return all(os.path.getmtime(d) <= t for d in DEPS) and \
+        all(os.path.getmtime(d) <= c for d in (CALLS_SOURCE, os.path.join(INCLUDE, "hq.h")))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -52,20 +75,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     tag = f".tmp{os.getpid()}"
     objs = [os.path.join(CSRC, os.path.basename(src)[:-3] + tag + ".o") for src in SOURCES]
+    calls_obj = os.path.join(CSRC, "hq_torch" + tag + ".o")
     extra = ["-Xptxas", "-v"] if verbose else None
     try:
-        # one nvcc per translation unit, in parallel, then one link
+        # one compiler per translation unit, in parallel, then a link each
         procs = [subprocess.Popen(nvcc_compile_command(src, obj, extra))
                  for src, obj in zip(SOURCES, objs)]
+        procs.append(subprocess.Popen(calls_compile_command(CALLS_SOURCE, calls_obj)))
         rcs = [pr.wait() for pr in procs]
-        for src, rc in zip(SOURCES, rcs):
+        for src, rc in zip([*SOURCES, CALLS_SOURCE], rcs):
             if rc != 0:
-                raise subprocess.CalledProcessError(rc, f"nvcc -c {os.path.basename(src)}")
+                raise subprocess.CalledProcessError(rc, f"compiling {os.path.basename(src)}")
         tmp = LIB + tag
         subprocess.run(nvcc_link_command(objs, tmp), check=True)
         os.replace(tmp, LIB)
+        tmp = CALLS + tag
+        subprocess.run(calls_link_command(calls_obj, tmp), check=True)
+        os.replace(tmp, CALLS)
     finally:
-        for obj in objs:
+        for obj in [*objs, calls_obj]:
             if os.path.exists(obj):
                 os.remove(obj)
     return LIB
