@@ -369,10 +369,6 @@ bool encode_bf16(CUtensorMap* map, const void* x, int64_t cols, int64_t stride_b
 }
 
 hq_status launch_shrink(hq::ShrinkParams p, const void* x, int64_t ldx, const void* a, hq_stream stream) {
-  CUtensorMap mx, ma;
-  if (!encode_bf16(&mx, x, p.K, ldx * 2, p.rows, 1, hq::kShrinkRows, 2) ||
-      !encode_bf16(&ma, a, p.K, int64_t{2} * p.K, p.rank, p.adapters, (p.rank + 15) / 16 * 16, 3))
-    return cuda_fail(cudaErrorInvalidValue);
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -383,13 +379,29 @@ hq_status launch_shrink(hq::ShrinkParams p, const void* x, int64_t ldx, const vo
   while (p.slices < 8 && p.slices * 2 <= blocks && tiles * p.slices * 2 <= 2 * sms) p.slices *= 2;
   p.jobs = 1;
   while (p.jobs < 32 && tiles * p.slices * p.jobs * 2 <= 2 * sms) p.jobs *= 2;
-  if ((e = cudaFuncSetAttribute(hq::k_lora_shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, hq::kShrinkSmem)) !=
-      cudaSuccess)
+  // Stages no larger than the rows there are and the adapters a CTA can meet: beside a small CTA the
+  // products' CTA fits on the SM and starts under it.
+  const int padded = (p.rank + 15) / 16 * 16, most = p.rows < hq::kShrinkRows ? p.rows : hq::kShrinkRows;
+  const int adapters = ((p.adapters < most ? p.adapters : most) + p.jobs - 1) / p.jobs;
+  p.box_rows = (most + 7) / 8 * 8;
+  p.cols = adapters * padded < hq::kShrinkCols ? adapters * padded : hq::kShrinkCols / padded * padded;
+  const int stage = (p.box_rows + p.cols) * 128;
+  p.stages = stage <= 8 * 1024 ? hq::kShrinkMaxStages : 3;
+  // (the instruction reads 128 rows of x from a stage's start; the sums lie over the ring)
+  int bytes = p.stages * stage;
+  if (bytes < (p.stages - 1) * stage + hq::kShrinkRows * 128) bytes = (p.stages - 1) * stage + hq::kShrinkRows * 128;
+  if (bytes < hq::kShrinkRows * (padded + 1) * 4) bytes = hq::kShrinkRows * (padded + 1) * 4;
+  bytes += 1024;
+  CUtensorMap mx, ma;
+  if (!encode_bf16(&mx, x, p.K, ldx * 2, p.rows, 1, p.box_rows, 2) ||
+      !encode_bf16(&ma, a, p.K, int64_t{2} * p.K, p.rank, p.adapters, padded, 3))
+    return cuda_fail(cudaErrorInvalidValue);
+  if ((e = cudaFuncSetAttribute(hq::k_lora_shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
     return cuda_fail(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles) * p.slices * p.jobs);
   cfg.blockDim = dim3(hq::kShrinkThreads);
-  cfg.dynamicSmemBytes = hq::kShrinkSmem;
+  cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -455,6 +467,7 @@ hq_status lora_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, con
   p.lora_ids = ids;
   p.adapters = s.adapters;
   p.rank = s.rank;
+  p.after_shrink = n > 0;
   if (!narrow && n == 0) {
     const hq_status st = tile_scales(p, tiles_at, stream);
     if (st != HQ_OK) return st;

@@ -92,6 +92,7 @@ struct GemmParams {
   const uint8_t* lora_t;    // bf16 [extent][hi, lo][rank]
   const int32_t* lora_ids;  // [extent]
   int adapters, rank;
+  int after_shrink;         // narrow: the kernel before this one is k_lora_shrink, and made only lora_t
 };
 
 // ---------------------------------------------------------------------------
@@ -115,7 +116,7 @@ struct GemmShape {
   // adapters: chunks of 64 bf16 columns: B_a of 128 lanes, then t's hi and lo of kRowsB rows
   static constexpr int kChunkBytes = LORA ? kGemmLanes * 128 + 2 * kRowsB * 128 : 0;
   static constexpr int kChunks = kWide ? 1 : 2;
-  static constexpr int kChunkGap = kWide ? 5 : 2;         // stages between two chunks of a tile
+  static constexpr int kChunkGap = kWide ? 8 : 2;         // stages between two chunks of a tile
   static constexpr int kEpilogues = !kWide ? 1 : LORA ? 2 : 3;  // groups of 128 threads
   // 32-column blocks of the output per chunk.  CONTR: two, three groups then take a tile in one chunk each.
   static constexpr int kBlocks = KIND == kGemmContr ? 2 : 1;
@@ -125,7 +126,7 @@ struct GemmShape {
   static constexpr int kRingBytes = 216 * 1024 - kChunks * kChunkBytes - kOuts;
   static constexpr int kStages = kRingBytes / kStageBytes < 7 ? kRingBytes / kStageBytes : 7;
   static constexpr int kSmemBytes = kStages * kStageBytes + kChunks * kChunkBytes + kOuts;
-  static_assert(kSmemBytes + 1024 + 16 * (LORA ? 2 : kGemmMaxGroups + 1) + 1280 <= 227 * 1024, "a CTA has 227 KB");
+  static_assert(kSmemBytes + 1024 + 16 * (LORA ? 2 : kGemmMaxGroups + 1) + 2048 <= 227 * 1024, "a CTA has 227 KB");
   // tensor memory columns: two accumulators, then two sets of scales (stage parity)
   static constexpr int kColsSfa = kTilesPerBlock * 4;
   static constexpr int kColsSfb = kTilesPerBlock * kRowTilesB * 4;
@@ -141,8 +142,8 @@ struct GemmBars {
   uint64_t drain;
   uint64_t chunk_full[2], chunk_empty[2];
   int chunk_steps[2], chunk_last[2];  // 16-column steps of a chunk; whether the tile ends with it
-  int next_id[2][4];
-  int32_t ids[192];
+  int32_t ids[192], distinct[192];     // a tile's adapters by row, and each once
+  int n_distinct;
   uint32_t tmem;
   int tiles;
 };
@@ -709,8 +710,10 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
     fence_mbar_init();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // The kernel before this one on the stream wrote the operands.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The kernel before this one on the stream wrote the operands.  (Where it is the adapters' first product,
+  // which lets this kernel start once it has itself waited for what was before it: only lora_t, and only the
+  // adapters' warps wait for it.)
+  if (!(LORA && !kPair && p.after_shrink)) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 0) {  // where each group's tiles begin
     int base = 0, unit_base = 0;
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
@@ -842,7 +845,7 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
         chunk.next(S::kChunks);
       };
       for (int kb = 0; kb < blocks; ++kb) {
-        if (LORA && chunks_left && kb % S::kChunkGap == S::kChunkGap - 1) take_chunk();
+        if (LORA && chunks_left && kb % S::kChunkGap == 1) take_chunk();
         if (!ok) break;
         ok = warp_wait(smem_addr(&bars.full[ring.s]), ring.phase);
         if (!ok) break;
@@ -1074,94 +1077,101 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
       const int tid = threadIdx.x - 32 * S::kLoraWarp;
       const int rank_steps = (p.rank + 15) / 16;
       GemmRing chunk;
-      int turn = 0;
       GemmTile t;
+      bool waited = false;
+      auto wait_for_t = [&]() {
+        if (!kPair && !waited && p.after_shrink) asm volatile("griddepcontrol.wait;" ::: "memory");
+        waited = true;
+      };
       while (ok && order.get(t)) {
-        role_sync<1>();  // the last tile's ids have been read
-        for (int r = tid; r < t.n; r += kLoraThreads) {
-          const int id = r < t.valid ? __ldg(p.lora_ids + t.b0 + r) : -1;
-          bars.ids[r] = id < p.adapters ? id : -1;
+        role_sync<1>();  // the last tile's lists have been read
+        if (warp == S::kLoraWarp) {
+          int got[T / 32], n = 0;
+#pragma unroll
+          for (int c = 0; c < T / 32; ++c)  // (all in flight together)
+            got[c] = 32 * c + lane < t.valid ? __ldg(p.lora_ids + t.b0 + 32 * c + lane) : -1;
+#pragma unroll
+          for (int c = 0; c < T / 32; ++c) {
+            const int r = 32 * c + lane, id = got[c] >= 0 && got[c] < p.adapters ? got[c] : -1;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
+            bool fresh = id >= 0 && lane == __ffs(same) - 1;
+            for (int k = 0; k < n; ++k) fresh = fresh && bars.distinct[k] != id;
+            const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, fresh);
+            if (fresh) bars.distinct[n + __popc(firsts & ((1u << lane) - 1))] = id;
+            bars.ids[r] = id;
+            n += __popc(firsts);
+            __syncwarp();
+          }
+          if (lane == 0) bars.n_distinct = n;
         }
         role_sync<1>();
-        // the smallest adapter of the tile's rows above `a`
-        auto next_above = [&](int a) {
-          int m = INT_MAX;
-          for (int r = tid; r < t.n; r += kLoraThreads) {
-            const int id = bars.ids[r];
-            if (id > a) m = min(m, id);
-          }
-          m = __reduce_min_sync(0xFFFFFFFFu, m);
-          if (lane == 0) bars.next_id[turn][tid >> 5] = m;
-          role_sync<1>();
-          m = min(min(bars.next_id[turn][0], bars.next_id[turn][1]), min(bars.next_id[turn][2], bars.next_id[turn][3]));
-          turn ^= 1;
-          return m;
-        };
-        int a = next_above(-1), step = 0, count = 0;
+        // Slot q holds ranks 16 (q % rank_steps) .. of the tile's adapter q / rank_steps.  (SPLIT: the parts take
+        // the chunks in turn.)
+        const int slots = bars.n_distinct * rank_steps;
+        const int rows_b = t.n / kCtas, r0 = static_cast<int>(rank) * rows_b;
+        const int n = t.a0 + static_cast<int>(rank) * kGemmLanes + tid;  // this thread's lane
+        int first = 4 * part_k;
         bool more = true;
         do {
-          int slot_a[4], slot_r[4], steps = 0;
+          more = first + 4 * splits < slots;
+          const int steps = max(0, min(4, slots - first));
+          int slot_a[4], slot_r[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            slot_a[i] = -1, slot_r[i] = 0;
-            if (a == INT_MAX) continue;
-            slot_a[i] = a, slot_r[i] = step * 16;
-            steps = i + 1;
-            if (++step == rank_steps) {
-              step = 0;
-              a = next_above(a);
-            }
+            slot_a[i] = i < steps ? bars.distinct[(first + i) / rank_steps] : -1;
+            slot_r[i] = i < steps ? (first + i) % rank_steps * 16 : 0;
           }
-          // (SPLIT: the parts take the chunks in turn; each ends with an empty one)
-          const bool none = a == INT_MAX && steps == 0;
-          if (SPLIT && !none && count++ % splits != part_k) continue;
-          more = SPLIT ? !none : a != INT_MAX;
-          // all four warps go on, or none: they meet at barriers
-          ok = role_all<1>(mbar_wait(smem_addr(&bars.chunk_empty[chunk.s]), chunk.phase ^ 1));
-          if (!ok) break;
-          uint8_t* const ch = chunks + chunk.s * S::kChunkBytes;
+          first += 4 * splits;
           const uint4 zero = make_uint4(0, 0, 0, 0);
-          {  // B_a of this thread's lane
-            const int n = t.a0 + static_cast<int>(rank) * kGemmLanes + tid;
-            uint4 v[4][2];
+          uint4 b[4][2];  // B_a of the lane
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int r = slot_r[i] + 8 * q;
+              b[i][q] = zero;
+              if (slot_a[i] >= 0 && n < p.na && r < p.rank)
+                b[i][q] = __ldg(reinterpret_cast<const uint4*>(
+                    p.lora_b + ((static_cast<int64_t>(slot_a[i]) * p.na + n) * p.rank + r) * 2));
+            }
+          wait_for_t();
+          // t's hi or lo of one of this CTA's rows: zero outside its adapter
+          auto load_t = [&](int item, uint4 (&v)[4][2]) {
+            const int r = r0 + (item >> 1), part = item & 1, id = bars.ids[r];
+            const uint8_t* src = p.lora_t + (static_cast<int64_t>(t.b0 + r) * 2 + part) * p.rank * 2;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
-                const int r = slot_r[i] + 8 * q;
+                const int k = slot_r[i] + 8 * q;
                 v[i][q] = zero;
-                if (slot_a[i] >= 0 && n < p.na && r < p.rank)
-                  v[i][q] = __ldg(reinterpret_cast<const uint4*>(
-                      p.lora_b + ((static_cast<int64_t>(slot_a[i]) * p.na + n) * p.rank + r) * 2));
+                if (slot_a[i] >= 0 && slot_a[i] == id && k < p.rank)
+                  v[i][q] = __ldcg(reinterpret_cast<const uint4*>(src + k * 2));
               }
+          };
+          constexpr int kItems = (2 * S::kRowsB + kLoraThreads - 1) / kLoraThreads;
+          uint4 v[kItems][4][2];
+#pragma unroll
+          for (int k = 0; k < kItems; ++k)
+            if (tid + kLoraThreads * k < 2 * rows_b) load_t(tid + kLoraThreads * k, v[k]);
+          // all four warps go on, or none: they meet at barriers
+          ok = role_all<1>(mbar_wait(smem_addr(&bars.chunk_empty[chunk.s]), chunk.phase ^ 1));
+          if (!ok) break;
+          uint8_t* const ch = chunks + chunk.s * S::kChunkBytes;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              *reinterpret_cast<uint4*>(ch + tid * 128 + (((2 * i + q) ^ (tid & 7)) << 4)) = b[i][q];
+#pragma unroll
+          for (int k = 0; k < kItems; ++k) {
+            const int item = tid + kLoraThreads * k, r = item >> 1;
+            if (item >= 2 * rows_b) break;
+            uint8_t* dst = ch + kGemmLanes * 128 + (item & 1) * S::kRowsB * 128 + r * 128;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-              for (int q = 0; q < 2; ++q)
-                *reinterpret_cast<uint4*>(ch + tid * 128 + (((2 * i + q) ^ (tid & 7)) << 4)) = v[i][q];
-          }
-          const int rows_b = t.n / kCtas, r0 = static_cast<int>(rank) * rows_b;
-          for (int r = tid; r < rows_b; r += kLoraThreads) {  // t of this CTA's rows: zero outside their adapter
-            const int id = bars.ids[r0 + r];
-            const uint8_t* src = p.lora_t + static_cast<int64_t>(t.b0 + r0 + r) * p.rank * 4;
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              uint4 v[4][2];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  const int k = slot_r[i] + 8 * q;
-                  v[i][q] = zero;
-                  if (slot_a[i] >= 0 && slot_a[i] == id && k < p.rank)
-                    v[i][q] = __ldg(reinterpret_cast<const uint4*>(src + (part * p.rank + k) * 2));
-                }
-              uint8_t* dst = ch + kGemmLanes * 128 + part * S::kRowsB * 128 + r * 128;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) *reinterpret_cast<uint4*>(dst + (((2 * i + q) ^ (r & 7)) << 4)) = v[i][q];
-            }
+              for (int q = 0; q < 2; ++q) *reinterpret_cast<uint4*>(dst + (((2 * i + q) ^ (r & 7)) << 4)) = v[k][i][q];
           }
           if (tid == 0) {
             bars.chunk_steps[chunk.s] = steps;
@@ -1173,6 +1183,7 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
           chunk.next(S::kChunks);
         } while (more);
       }
+      wait_for_t();  // (a CTA without a tile too: this kernel ends after the one before)
     }
   }
   if (!ok) {
@@ -1253,11 +1264,8 @@ __device__ __forceinline__ uint4 scale_tile_row(const uint8_t* s, int64_t row0, 
 // ---------------------------------------------------------------------------
 constexpr int kShrinkThreads = 192;
 constexpr int kShrinkRows = 128;
-constexpr int kShrinkCols = 128;                    // columns of a pass
-constexpr int kShrinkStages = 3;
-constexpr int kShrinkStageBytes = (kShrinkRows + kShrinkCols) * 128;
-constexpr int kShrinkSmem = 1024 + kShrinkStages * kShrinkStageBytes;
-static_assert(kShrinkRows * 129 * 4 <= kShrinkStages * kShrinkStageBytes, "the sums lie over the ring");
+constexpr int kShrinkCols = 128;                    // columns of a pass, at most
+constexpr int kShrinkMaxStages = 4;
 
 struct ShrinkParams {
   const float* scaling;    // [adapters]
@@ -1270,6 +1278,9 @@ struct ShrinkParams {
   uint4* tiles;
   int scale_row_bytes, scale_tiles;
   int rows, K, adapters, rank, slices, jobs;
+  // rows of x in a stage (fewer than the 128 lanes where there are not so many: the others' columns are
+  // not read), columns of a pass, stages
+  int box_rows, cols, stages;
 };
 
 __global__ void __launch_bounds__(kShrinkThreads)
@@ -1277,7 +1288,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
                   const __grid_constant__ ShrinkParams p) {
   extern __shared__ uint8_t shrink_smem_raw[];
   __shared__ struct {
-    uint64_t full[kShrinkStages], empty[kShrinkStages], done;
+    uint64_t full[kShrinkMaxStages], empty[kShrinkMaxStages], done;
     uint32_t tmem;
     int n;                        // adapters of this CTA
     int16_t slot[kShrinkRows];    // a row's place among them, or -1
@@ -1296,15 +1307,16 @@ __global__ void __launch_bounds__(kShrinkThreads)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (threadIdx.x == 128) {
-    for (int i = 0; i < kShrinkStages; ++i) {
+    for (int i = 0; i < p.stages; ++i) {
       mbar_init(smem_addr(&sh.full[i]), 1);
       mbar_init(smem_addr(&sh.empty[i]), 1);
     }
     mbar_init(smem_addr(&sh.done), 1);
     fence_mbar_init();
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (after the wait: the products may start under this kernel and read what it waited for)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) {  // the distinct adapters; every jobs-th of them is this CTA's
     int ids[kShrinkRows / 32], n = 0;
 #pragma unroll
@@ -1333,7 +1345,8 @@ __global__ void __launch_bounds__(kShrinkThreads)
   __syncthreads();
   umma_fence_after();
   const uint32_t tmem = sh.tmem;
-  const int n = sh.n, per_pass = kShrinkCols / padded, passes = (n + per_pass - 1) / per_pass;
+  const int n = sh.n, per_pass = p.cols / padded, passes = (n + per_pass - 1) / per_pass;
+  const int stage_bytes = (p.box_rows + p.cols) * 128;
   const int blocks = (p.K + 63) / 64, per = (blocks + p.slices - 1) / p.slices;
   const int kb0 = slice * per, kb1 = min(blocks, kb0 + per);
   bool ok = true;
@@ -1357,33 +1370,33 @@ __global__ void __launch_bounds__(kShrinkThreads)
     if (warp == 4) {
       for (int kb = kb0; kb < kb1; ++kb) {
         ok = ok && warp_wait(smem_addr(&sh.empty[at.s]), at.phase ^ 1);
-        const uint32_t bar = smem_addr(&sh.full[at.s]), st = smem_addr(ring) + at.s * kShrinkStageBytes;
+        const uint32_t bar = smem_addr(&sh.full[at.s]), st = smem_addr(ring) + at.s * stage_bytes;
         if (!ok) break;
         ++fills;
         if (elect_one()) {
-          mbar_expect_tx(bar, (kShrinkRows + slots * padded) * 128);
+          mbar_expect_tx(bar, (p.box_rows + slots * padded) * 128);
           tma_tile2<false>(st, &map_x, kb * 64, row0, bar);
           for (int i = 0; i < slots; ++i)
-            tma_tile3<false>(st + (kShrinkRows + i * padded) * 128, &map_a, kb * 64, 0,
+            tma_tile3<false>(st + (p.box_rows + i * padded) * 128, &map_a, kb * 64, 0,
                              sh.adapter[job + (pass * per_pass + i) * p.jobs], bar);
         }
         __syncwarp();
-        at.next(kShrinkStages);
+        at.next(p.stages);
       }
     } else if (warp == 5) {
       const uint32_t idesc = umma_idesc_bf16(kShrinkRows, slots * padded);
       for (int kb = kb0; kb < kb1 && ok; ++kb) {
         ok = warp_wait(smem_addr(&sh.full[at.s]), at.phase);
         umma_fence_after();
-        const uint64_t st = ring0 + at.s * (kShrinkStageBytes >> 4);
+        const uint64_t st = ring0 + at.s * (stage_bytes >> 4);
         if (ok && elect_one()) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            umma_bf16<false>(tmem, st + 2 * j, st + (kShrinkRows * 128 >> 4) + 2 * j, idesc, kb > kb0 || j > 0);
+            umma_bf16<false>(tmem, st + 2 * j, st + (p.box_rows * 128 >> 4) + 2 * j, idesc, kb > kb0 || j > 0);
           umma_commit<false>(smem_addr(&sh.empty[at.s]));
         }
         __syncwarp();
-        at.next(kShrinkStages);
+        at.next(p.stages);
       }
       if (elect_one()) umma_commit<false>(smem_addr(&sh.done));
       __syncwarp();
@@ -1431,8 +1444,8 @@ __global__ void __launch_bounds__(kShrinkThreads)
     cluster_sync();
   }
   if (!ok && warp == 4)  // let the copies in flight land (bounded)
-    for (long long f = fills > kShrinkStages ? fills - kShrinkStages : 0; f < fills; ++f)
-      mbar_wait(smem_addr(&sh.full[f % kShrinkStages]), (f / kShrinkStages) & 1);
+    for (long long f = fills > p.stages ? fills - p.stages : 0; f < fills; ++f)
+      mbar_wait(smem_addr(&sh.full[f % p.stages]), (f / p.stages) & 1);
   if (!ok && lane == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);
   umma_fence_before();
   __syncthreads();
