@@ -111,9 +111,9 @@ def load() -> ctypes.CDLL:
         lib.hq_lora_gemm_nvfp4.restype = i32
         lib.hq_lora_gemm_mxfp4.argtypes = [p] * 5 + [i64] + [p] * 4 + [i64] * 5 + [p, i32, p, p]
         lib.hq_lora_gemm_mxfp4.restype = i32
-        lib.hq_grouped_gemm_workspace_bytes.argtypes = [i64] * 3
+        lib.hq_grouped_gemm_workspace_bytes.argtypes = [i64] * 4
         lib.hq_grouped_gemm_workspace_bytes.restype = i64
-        lib.hq_lora_gemm_workspace_bytes.argtypes = [i64] * 3
+        lib.hq_lora_gemm_workspace_bytes.argtypes = [i64] * 4
         lib.hq_lora_gemm_workspace_bytes.restype = i64
         lib.hq_swizzle_scales.argtypes = [p, i64, i64, i64, p, p]
         lib.hq_swizzle_scales.restype = i32

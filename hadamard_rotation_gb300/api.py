@@ -339,19 +339,19 @@ def _load_calls():
     return _calls
 
 
-def hq_grouped_gemm_workspace_bytes(M: int, K: int, E: int) -> int:
+def hq_grouped_gemm_workspace_bytes(M: int, N: int, K: int, E: int) -> int:
     """Bytes of the workspace of hq_grouped_gemm_* (which this binding allocates itself)."""
-    n = _lib.load().hq_grouped_gemm_workspace_bytes(M, K, E)
+    n = _lib.load().hq_grouped_gemm_workspace_bytes(M, N, K, E)
     if n < 0:
-        raise ValueError("hq_grouped_gemm_workspace_bytes: M >= 0, K a multiple of 32, 0 <= E <= 512")
+        raise ValueError("hq_grouped_gemm_workspace_bytes: M, N >= 0, K a multiple of 32, 0 <= E <= 512")
     return n
 
 
-def hq_lora_gemm_workspace_bytes(M: int, K: int, R: int) -> int:
+def hq_lora_gemm_workspace_bytes(M: int, N: int, K: int, R: int) -> int:
     """Bytes of the workspace of hq_lora_gemm_* (which this binding allocates itself)."""
-    n = _lib.load().hq_lora_gemm_workspace_bytes(M, K, R)
+    n = _lib.load().hq_lora_gemm_workspace_bytes(M, N, K, R)
     if n < 0:
-        raise ValueError("hq_lora_gemm_workspace_bytes: M >= 0, K a multiple of 32, R a multiple of 8 up to 128")
+        raise ValueError("hq_lora_gemm_workspace_bytes: M, N >= 0, K a multiple of 32, R a multiple of 8 up to 128")
     return n
 
 

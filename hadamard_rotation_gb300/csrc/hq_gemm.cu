@@ -60,21 +60,6 @@ int store_bytes(const void* out, int64_t n, hq_dtype dt) {
   return v;
 }
 
-// Multiprocessors of the current device, asked for once per device.
-cudaError_t sm_count(int* sms) {
-  static int known[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64 && known[dev]) {
-    *sms = known[dev];
-    return cudaSuccess;
-  }
-  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess && dev < 64) known[dev] = *sms;
-  return e;
-}
-
 // Scale tiles [row_tiles][k_tiles] of 512 bytes, as words: boxes of `box` tiles along k, `box_rows` of rows.
 bool encode_scales(CUtensorMap* map, const uint8_t* s, int64_t k_tiles, int64_t row_tiles, int box, int box_rows) {
   const EncodeTiledFn fn = encode_tiled();
@@ -120,11 +105,10 @@ hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t b_scale_r
   p.out_tma = !p.out_f32 && p.out_vec == 16 &&
               encode_out(&mo, p.out, p.na, KIND == hq::kGemmRows ? p.extent : p.nb, KIND == hq::kGemmRows ? 1 : p.groups);
   int sms = 0;
-  cudaError_t e = sm_count(&sms);
+  cudaError_t e = hq::sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);
   const size_t smem = hq::gemm_smem_bytes(S::kSmemBytes, p.groups);
-  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) !=
-      cudaSuccess)
+  if ((e = hq::allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem))) != cudaSuccess)
     return cuda_fail(e);
   cudaLaunchConfig_t cfg = {};
   const int ctas = S::kCtas * splits;
@@ -211,19 +195,26 @@ hq_status out_zero(void* out, int64_t n, hq_dtype dt, hq_stream stream) {
   return e == cudaSuccess ? HQ_OK : cuda_fail(e);
 }
 
-// Tiles of 64 or of 192 columns: the narrow ones read the tokens' scales as they are and have more stages
-// in flight per byte of operand, the wide ones read the weights half or a third as often.
-bool narrow_rows(int64_t M, int64_t E) { return M <= 64 * E; }
-
 // Tiles of narrow groups, at most: group sizes add up to M.
 int64_t narrow_tiles(int64_t M, int64_t E, int64_t tiles_a) { return (M + 63 * (E < M ? E : M)) / 64 * tiles_a; }
+
+// Tiles of 128 x 64 by single CTAs or of 256 x 192 by pairs.  The wide ones read each operand a half to
+// a third as often, but need the tokens' scales laid out first (3 us) and fill 76 places, not 152.  Narrow
+// where a group has a few rows, or where all its tiles take the 152 SMs some 36 stages each (4 for a tile's
+// start and end).  Measured, us narrow / wide: 8 experts 2048 x 2048, 32 rows each 6.2 / 9.9, 192 rows
+// 12.8 / 13.5, 512 rows 26.4 / 18.5; 12 of 1100 x 1056, 256 rows 12.4 / 15.1, 512 rows 18.6 / 18.6; 64 of
+// 2048 x 4096, 32 rows 46 / 48, 64 rows 67 / 55; 32 of 512 x 512, 256 rows 8.8 / 9.6, 512 rows 13.4 / 11.8.
+bool narrow_rows(int64_t M, int64_t N, int64_t K, int64_t E) {
+  return M <= 32 * E ||
+         narrow_tiles(M, E, (N + 127) / 128) <= 36 * 152 / ((K + hq::kGemmKBlock - 1) / hq::kGemmKBlock + 4);
+}
 
 // The narrow kernel, its summed axis shared by a cluster where there are few tiles: as many CTAs as
 // SMs, each with two pairs of stages at least (a shorter part is mostly start and end).
 template <bool MX, bool LORA>
 hq_status launch_narrow(const GemmParams& p, const Codes& a, const Codes& b, int64_t most_tiles, hq_stream stream) {
   int sms = 0;
-  const cudaError_t e = sm_count(&sms);
+  const cudaError_t e = hq::sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);
   int splits = 1;
   while (splits < hq::kMaxSplits && most_tiles * splits * 2 <= sms && p.k >= splits * 2 * 4 * hq::kGemmKBlock) splits *= 2;
@@ -264,7 +255,7 @@ GemmParams rows_params(const uint8_t* xs, const float* x_sg, const uint8_t* ws, 
   GemmParams p = {};
   p.k_tiles = static_cast<int>((K + (MX ? 127 : 63)) / (MX ? 128 : 64));
   p.a_row_tiles = static_cast<int>((N + 127) / 128);
-  p.tiles_a = static_cast<int>(narrow_rows(M, groups) ? (N + 127) / 128 : (N + 255) / 256);
+  p.tiles_a = static_cast<int>(narrow_rows(M, N, K, groups) ? (N + 127) / 128 : (N + 255) / 256);
   p.sfa = ws;
   p.sfb = xs;
   p.sfb_row_bytes = static_cast<int>(K / (MX ? 32 : 16));
@@ -294,7 +285,7 @@ hq_status grouped_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, 
   if (M == 0 || N == 0 || E == 0) return HQ_OK;
   if (!out || !offsets) return HQ_ERR_NULL;
   if (!aligned(out, dt == HQ_F32 ? 4 : 2) || !aligned(offsets, 4)) return HQ_ERR_ALIGN;
-  const bool narrow = narrow_rows(M, E);
+  const bool narrow = narrow_rows(M, N, K, E);
   const int64_t tiles_a = narrow ? (N + 127) / 128 : (N + 255) / 256;
   const int64_t tiles = narrow ? narrow_tiles(M, E, tiles_a) : (M / 192 + (E < M ? E : M)) * tiles_a;
   if (tiles > kMaxExtent) return HQ_ERR_SHAPE;
@@ -370,7 +361,7 @@ bool encode_bf16(CUtensorMap* map, const void* x, int64_t cols, int64_t stride_b
 
 hq_status launch_shrink(hq::ShrinkParams p, const void* x, int64_t ldx, const void* a, hq_stream stream) {
   int sms = 0;
-  cudaError_t e = sm_count(&sms);
+  cudaError_t e = hq::sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);
   // As many slices of k as there are places for (two CTAs per SM), up to a portable cluster; then, where
   // few rows leave SMs idle, several CTAs share a tile's adapters.
@@ -396,8 +387,7 @@ hq_status launch_shrink(hq::ShrinkParams p, const void* x, int64_t ldx, const vo
   if (!encode_bf16(&mx, x, p.K, ldx * 2, p.rows, 1, p.box_rows, 2) ||
       !encode_bf16(&ma, a, p.K, int64_t{2} * p.K, p.rank, p.adapters, padded, 3))
     return cuda_fail(cudaErrorInvalidValue);
-  if ((e = cudaFuncSetAttribute(hq::k_lora_shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)) != cudaSuccess)
-    return cuda_fail(e);
+  if ((e = hq::allow_smem(reinterpret_cast<const void*>(hq::k_lora_shrink), bytes)) != cudaSuccess) return cuda_fail(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles) * p.slices * p.jobs);
   cfg.blockDim = dim3(hq::kShrinkThreads);
@@ -410,7 +400,7 @@ hq_status launch_shrink(hq::ShrinkParams p, const void* x, int64_t ldx, const vo
   attr[1].val.clusterDim.x = static_cast<unsigned>(p.slices);
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = p.slices > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, hq::k_lora_shrink, mx, ma, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? HQ_OK : cuda_fail(e);
@@ -436,8 +426,8 @@ hq_status lora_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, con
       !aligned(x, 16) || (M > 1 && ldx % 8 != 0) || !aligned(a, 16) || !aligned(b, 16) || !aligned(scaling, 4) ||
       !aligned(ids, 4) || !aligned(workspace, 32) || !aligned(x_sg, 4) || !aligned(w_sg, 4))
     return HQ_ERR_ALIGN;
-  const bool narrow = narrow_rows(M, 1);
-  const int64_t tiles = narrow ? (M + 63) / 64 * ((N + 127) / 128) : (M + 191) / 192 * ((N + 255) / 256);
+  const bool narrow = narrow_rows(M, N, K, 1);
+  const int64_t tiles = narrow ? narrow_tiles(M, 1, (N + 127) / 128) : (M + 191) / 192 * ((N + 255) / 256);
   if (tiles > kMaxExtent) return HQ_ERR_SHAPE;
   hq::ShrinkParams s = {};
   s.scaling = scaling;
@@ -537,14 +527,14 @@ hq_status hq_grouped_wgrad_mxfp4(const uint8_t* gq, const uint8_t* gs, const uin
   return grouped_wgrad<true>(gq, gs, nullptr, xq, xs, nullptr, offsets, T, N, K, E, out, out_dtype, stream);
 }
 
-int64_t hq_grouped_gemm_workspace_bytes(int64_t M, int64_t K, int64_t E) {
-  if (M < 0 || K < 0 || E < 0 || M > kMaxExtent || K > kMaxExtent || E > hq::kGemmMaxGroups || K % 32 != 0) return -1;
-  return M == 0 || E == 0 || narrow_rows(M, E) ? 0 : group_scale_bytes(M, K, E, false);
+int64_t hq_grouped_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E) {
+  if (M < 0 || N < 0 || K < 0 || E < 0 || M > kMaxExtent || N > kMaxExtent || K > kMaxExtent || E > hq::kGemmMaxGroups || K % 32 != 0) return -1;
+  return M == 0 || E == 0 || narrow_rows(M, N, K, E) ? 0 : group_scale_bytes(M, K, E, false);
 }
 
-int64_t hq_lora_gemm_workspace_bytes(int64_t M, int64_t K, int64_t R) {
-  if (M < 0 || M > kMaxExtent || K < 0 || K > kMaxExtent || K % 32 != 0 || R < 8 || R > 128 || R % 8 != 0) return -1;
-  return lora_t_bytes(M, R) + (narrow_rows(M, 1) ? 0 : group_scale_bytes(M, K, 1, false));
+int64_t hq_lora_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R) {
+  if (M < 0 || N < 0 || M > kMaxExtent || N > kMaxExtent || K < 0 || K > kMaxExtent || K % 32 != 0 || R < 8 || R > 128 || R % 8 != 0) return -1;
+  return lora_t_bytes(M, R) + (narrow_rows(M, N, K, 1) ? 0 : group_scale_bytes(M, K, 1, false));
 }
 
 hq_status hq_lora_gemm_nvfp4(const uint8_t* xq, const uint8_t* xs, const float* x_sg, const uint8_t* wq,

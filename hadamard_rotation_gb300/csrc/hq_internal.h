@@ -21,6 +21,13 @@ cudaError_t gemm_fault_word(unsigned int* fault, bool clear);
 // And for the norms' (hq_norm.cu).
 cudaError_t norm_fault_word(unsigned int* fault, bool clear);
 
+// Allow `fn` `bytes` of dynamic shared memory on the current device; remembered per kernel, device and
+// context, so that a call of a few microseconds asks the runtime once.
+cudaError_t allow_smem(const void* fn, int bytes);
+
+// Multiprocessors of the current device, asked for once per device.
+cudaError_t sm_count(int* sms);
+
 // Launch the bounded-wait self-test kernel of the int8 translation unit on `stream`.
 cudaError_t int8_selftest_bounded_wait(cudaStream_t stream);
 

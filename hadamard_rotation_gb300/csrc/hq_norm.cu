@@ -47,7 +47,7 @@ Shape shape_of(int64_t M, int D, int es, int tensors, int sms) {
 
 template <typename Kernel>
 cudaError_t launch(Kernel kernel, const NormParams& p, const Shape& s, int clusters, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(s.smem));
+  cudaError_t e = hq::allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(s.smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * s.ranks));
@@ -61,15 +61,9 @@ cudaError_t launch(Kernel kernel, const NormParams& p, const Shape& s, int clust
   attr[1].val.clusterDim.x = static_cast<unsigned>(s.ranks);
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = s.ranks > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kernel, p);
   return e == cudaSuccess ? cudaGetLastError() : e;
-}
-
-cudaError_t sm_count(int* sms) {
-  int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
-  return e == cudaSuccess ? cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) : e;
 }
 
 int clusters_of(const Shape& s, int64_t M, int sms) {
@@ -166,7 +160,7 @@ hq_status hq_block_norm(const void* h, int64_t ld_h, const void* y, int64_t ld_y
   p.group = amax ? group : -1;
   p.amax = reinterpret_cast<unsigned*>(amax);
   int sms = 0;
-  cudaError_t e = sm_count(&sms);
+  cudaError_t e = hq::sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);
   const Shape s = shape_of(M, p.D, es, 2, sms);
   p.cols = s.cols;
@@ -254,7 +248,7 @@ hq_status hq_block_norm_bwd(const void* dh_out, int64_t ld_dh, const void* dn, i
   p.dgate = dgate;
   p.partial = static_cast<float*>(workspace);
   int sms = 0;
-  if ((e = sm_count(&sms)) != cudaSuccess) return cuda_fail(e);
+  if ((e = hq::sm_count(&sms)) != cudaSuccess) return cuda_fail(e);
   const Shape s = shape_of(M, p.D, es, 4, sms);
   p.cols = s.cols;
   p.tpr = s.tpr;
@@ -277,7 +271,7 @@ hq_status hq_block_norm_bwd(const void* dh_out, int64_t ld_dh, const void* dn, i
   if (!to_pre && !to_post && !to_gate) return HQ_OK;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((D + 31) / 32));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(512);
   cfg.stream = cs;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -132,6 +132,18 @@ __device__ __forceinline__ float norm_param(const void* w, int64_t i, int bf16) 
 
 // A unit of a parameter vector (ones where it is absent; zeros outside the row).
 __device__ __forceinline__ void param_unit(const void* w, int64_t col, int bf16, bool in, float2 (&f)[4]) {
+  if (in && w && (reinterpret_cast<uintptr_t>(w) & 15) == 0) {  // the usual case: two loads at most
+    if (bf16) {
+      Unit<true> u;
+      u.load(static_cast<const uint8_t*>(w) + col * 2);
+      u.get(f);
+    } else {
+      Unit<false> u;
+      u.load(static_cast<const uint8_t*>(w) + col * 4);
+      u.get(f);
+    }
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     f[e] = in ? make_float2(norm_param(w, col + 2 * e, bf16), norm_param(w, col + 2 * e + 1, bf16)) : both(0.0f);
@@ -629,26 +641,31 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
 }
 
 // The clusters' partial column sums, added in a fixed order; dw_post = gate A, dgate = w_post A.
-// 32 columns x 8 slices of the clusters per CTA.
-__global__ void __launch_bounds__(256) k_norm_columns(const float* __restrict__ partial, int clusters, int D,
+// 32 columns x 16 slices of the clusters per CTA: a thread's dozen loads are in flight together.
+__global__ void __launch_bounds__(512) k_norm_columns(const float* __restrict__ partial, int clusters, int D,
                                                       const void* w_post, const void* gate, int params_bf16,
                                                       float* dw_pre, float* dw_post, float* dgate) {
-  __shared__ float s[2][8][32];
+  constexpr int kSlices = 16, kMost = (kNormMaxPartials + kSlices - 1) / kSlices;
+  __shared__ float s[2][kSlices][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    float v = 0.0f;
-    if (c < D)
-#pragma unroll 8
-      for (int i = slice; i < clusters; i += 8) v += partial[(static_cast<int64_t>(k) * clusters + i) * D + c];
+    float x[kMost], v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      const int at = slice + i * kSlices;
+      x[i] = c < D && at < clusters ? partial[(static_cast<int64_t>(k) * clusters + at) * D + c] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) v += x[i];
     s[k][slice][threadIdx.x & 31] = v;
   }
   __syncthreads();
   if (slice < 2 && c < D) {
     float v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += s[slice][i][threadIdx.x & 31];
+    for (int i = 0; i < kSlices; ++i) v += s[slice][i][threadIdx.x & 31];
     if (slice == 0) {
       if (dw_pre) dw_pre[c] = v;
     } else {

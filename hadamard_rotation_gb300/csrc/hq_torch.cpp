@@ -209,7 +209,7 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* o = at_given<int32_t>(a[6], {E + 1}, at::kInt, index, "offsets");
     const at::Tensor out = output(a[7], a[8], {M, N}, xq);
     const Stream stream(a[9], index);
-    const at::Tensor work = workspace(hq_grouped_gemm_workspace_bytes(M, K, E), xq, stream);
+    const at::Tensor work = workspace(hq_grouped_gemm_workspace_bytes(M, N, K, E), xq, stream);
     run(index, MX ? "hq_grouped_gemm_mxfp4" : "hq_grouped_gemm_nvfp4", [&] {
       const hq_dtype dt = dtype_of(out.scalar_type());
       return MX ? hq_grouped_gemm_mxfp4(q, s, w, t, o, M, N, K, E, out.data_ptr(), dt, addr(work), stream.handle)
@@ -273,7 +273,7 @@ PyObject* lora_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t ldx = M > 1 ? x->stride(0) : K;
     const at::Tensor out = output(a[11], a[12], {M, N}, xq);
     const Stream stream(a[13], index);
-    const at::Tensor work = workspace(hq_lora_gemm_workspace_bytes(M, K, R), xq, stream);
+    const at::Tensor work = workspace(hq_lora_gemm_workspace_bytes(M, N, K, R), xq, stream);
     run(index, MX ? "hq_lora_gemm_mxfp4" : "hq_lora_gemm_nvfp4", [&] {
       const hq_dtype dt = dtype_of(out.scalar_type());
       const void* px = x->const_data_ptr();

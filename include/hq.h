@@ -352,7 +352,7 @@ HQ_API hq_status hq_dequant_nvfp4(const uint8_t* q, const uint8_t* scales, const
  *   xq [M, K/2], xs [M, K/16] row-major (hq_quantize_nvfp4, hq_rotate_quant_nvfp4), x_sg 1 float;
  *   wq [E, N, K/2], ws E buffers of hq_swizzled_scales_bytes(N, K) in the tile layout, w_sg E
  *   floats; out [M, N].  K a multiple of 32; K == 0 zeroes out.
- *   workspace : hq_grouped_gemm_workspace_bytes(M, K, E) bytes, 32-byte aligned; contents need no
+ *   workspace : hq_grouped_gemm_workspace_bytes(M, N, K, E) bytes, 32-byte aligned; contents need no
  *               preparation (large groups: x's scales in the tile layout).  Calls that may run at the
  *               same time need different ones.
  */
@@ -364,7 +364,7 @@ HQ_API hq_status hq_grouped_gemm_nvfp4(const uint8_t* xq, const uint8_t* xs, con
 
 /* Bytes of hq_grouped_gemm's workspace: 0 for a few rows per expert (workspace may then be NULL), -1
  * for sizes it refuses. */
-HQ_API int64_t hq_grouped_gemm_workspace_bytes(int64_t M, int64_t K, int64_t E);
+HQ_API int64_t hq_grouped_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E);
 
 /* hq_grouped_gemm_mxfp4 -- the same for MXFP4 operands: xs [M, K/32], ws E buffers of
  * hq_swizzled_scales_bytes(N, K/2) (hq_swizzle_scales of [E, N, K/32]), no per-tensor scales. */
@@ -410,7 +410,7 @@ HQ_API hq_status hq_grouped_wgrad_mxfp4(const uint8_t* gq, const uint8_t* gs, co
  *   any order (rows of one request next to one another cost least).  R a multiple of 8 up to 128
  *   (adapters of a smaller rank padded with zeros), K a multiple of 32.  x, lora_a, lora_b and x's rows
  *   16-byte aligned.
- *   workspace : hq_lora_gemm_workspace_bytes(M, K, R) bytes, 32-byte aligned; contents need no
+ *   workspace : hq_lora_gemm_workspace_bytes(M, N, K, R) bytes, 32-byte aligned; contents need no
  *               preparation.  Calls that may run at the same time need different ones.
  */
 HQ_API hq_status hq_lora_gemm_nvfp4(const uint8_t* xq, const uint8_t* xs, const float* x_sg,
@@ -430,7 +430,7 @@ HQ_API hq_status hq_lora_gemm_mxfp4(const uint8_t* xq, const uint8_t* xs, const 
                                     void* workspace, hq_stream stream);
 
 /* Bytes of hq_lora_gemm's workspace (-1 for sizes it refuses). */
-HQ_API int64_t hq_lora_gemm_workspace_bytes(int64_t M, int64_t K, int64_t R);
+HQ_API int64_t hq_lora_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R);
 
 /*
  * hq_swizzle_scales -- row-major block scales into the tile layout of

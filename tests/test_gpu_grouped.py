@@ -101,6 +101,20 @@ def test_grouped_gemm(fmt, sizes, N, K, out_dtype):
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("sizes,N,K", [
+    ([700, 3, 0, 449], 2100, 4128),            # several tiles per expert, a pair of lane tiles half empty
+    ([191, 192, 193, 385, 64, 65], 1290, 4640),  # around the tile's width and its steps, no 16-byte rows of out
+    ([40] * 64 + [0] * 5 + [1], 1000, 2048),   # many experts of one short tile each
+    ([1300], 4104, 1056),                      # one group, a partial block, 66- and 33-byte scale rows
+])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_grouped_gemm_large(fmt, sizes, N, K, out_dtype):
+    """Sizes that the pairs of CTAs take, whose scales are laid out in the workspace first."""
+    assert hq.hq_grouped_gemm_workspace_bytes(sum(sizes), N, K, len(sizes)) > 0
+    test_grouped_gemm(fmt, sizes, N, K, out_dtype)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 def test_rows_of_no_group_and_offsets_outside_the_tensor(fmt):
     """Rows past the last offset keep what they held; offsets beyond M are clamped to it."""
     rng = np.random.default_rng(3)
@@ -134,6 +148,31 @@ def test_unaligned_scale_rows(fmt):
         moved = buf[shift:shift + xs.numel()].view_as(xs)
         moved.copy_(xs)
         assert torch.equal(gemm(fmt, xq, moved, one, wq, ws, ones, off), want)
+    M, N, K = 1100, 2304, 4096  # and where they are laid out in a workspace
+    xq, xs = operand((M, K), fmt, rng)
+    wq, ws = operand((E, N, K), fmt, rng)
+    off = offsets_of([500, 600])
+    assert hq.hq_grouped_gemm_workspace_bytes(M, N, K, E) > 0
+    want = gemm(fmt, xq, xs, one, wq, ws, ones, off)
+    buf = torch.empty(xs.numel() + 32, dtype=torch.uint8, device="cuda")
+    moved = buf[1:1 + xs.numel()].view_as(xs)
+    moved.copy_(xs)
+    assert torch.equal(gemm(fmt, xq, moved, one, wq, ws, ones, off), want)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_large_and_small_calls_give_the_same_bits(fmt):
+    """The sum over K is made in the same steps by single CTAs and by pairs: a row's result does not depend on
+    the rows beside it."""
+    rng = np.random.default_rng(6)
+    M, N, K = 1100, 2304, 4096
+    xq, xs = operand((M, K), fmt, rng)
+    wq, ws = operand((1, N, K), fmt, rng)
+    one = torch.ones(1, device="cuda")
+    large = gemm(fmt, xq, xs, one, wq, ws, one, offsets_of([M]), out_dtype=torch.float32)
+    assert hq.hq_grouped_gemm_workspace_bytes(M, N, K, 1) > 0 == hq.hq_grouped_gemm_workspace_bytes(300, N, K, 1)
+    small = gemm(fmt, xq[:300], xs[:300], one, wq, ws, one, offsets_of([300]), out_dtype=torch.float32)
+    assert torch.equal(large[:300], small)
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])

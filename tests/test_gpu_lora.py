@@ -78,6 +78,9 @@ def check(fmt, p, got):
     (500, 200, 4128, 6, 128, "runs"),    # two rank blocks
     (391, 128, 64, 3, 40, "sorted"),     # a short sum beside many chunks
     (130, 136, 256, 4, 72, "none"),      # no row has one
+    (1100, 2304, 4128, 6, 64, "runs"),   # pairs of CTAs
+    (1030, 4104, 2048, 64, 24, "mixed"),  # as many adapters as chunks hold, several times over
+    (1300, 3336, 2080, 3, 128, "none"),
 ])
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
 def test_against_64_bits(fmt, M, N, K, n, R, order, out_dtype):
