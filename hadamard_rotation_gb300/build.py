@@ -59,7 +59,7 @@ def calls_link_command(obj: str, out: str) -> list[str]:
 
     return [shutil.which("g++") or "g++", "-shared", "-o", out, obj, "-L", os.path.dirname(LIB), "-lhq",
             "-Wl,-rpath,$ORIGIN", "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
-            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
 
 
 def up_to_date() -> bool:

@@ -205,16 +205,6 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// One lane of a converged warp.  The asynchronous instructions are issued under this predicate, in code
-// that the whole warp runs, rather than in a branch on the lane: the compiler then knows that their
-// operands are the warp's and keeps them in uniform registers (a stage's 12 tensor-core
-// instructions took 1700 cycles to issue from a branch on lane 0).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r;
-}
-
 // A wait of the whole warp: every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));

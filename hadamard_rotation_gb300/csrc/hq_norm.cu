@@ -17,6 +17,7 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 
 constexpr int64_t kMaxD = 32768;
 constexpr int kSmemBytes = 216 * 1024;  // the ring, of the 227 KB a CTA may have
+constexpr int kMinStages = 3;           // a step holds two rows' stages while the third is loaded
 
 // Columns per CTA: two units per thread, and no more than leave room for three stages.
 struct Shape {
@@ -26,22 +27,27 @@ struct Shape {
 
 Shape shape_of(int64_t M, int D, int es, int tensors, int sms) {
   Shape s;
-  const int most = tensors == 4 && es == 4 ? 4096 : 8192;
+  const int most = tensors == 4 && es == 4 ? 4096 : 8192;  // (fp32 backward: one unit per thread)
   s.ranks = (D + most - 1) / most;
   s.cols = ((D + s.ranks - 1) / s.ranks + 255) / 256 * 256;  // whole rotation groups
   if (s.ranks == 1) s.cols = D;
   const int u = (s.cols + 7) / 8;
-  s.units = u > hq::kNormThreads ? 2 : 1;
+  // Two units per thread where there are rows enough for all SMs all the same: what a step costs a thread
+  // beside its elements (the sums' way through shuffles and shared memory) is then shared by 16 of them.
+  // (bf16 [8192, 2048] forward 40.0 -> 30.1 us, backward 60.5 -> 50.9.  Not backward in fp32, whose stages leave
+  // room for half the threads then: [4096, 4096] 111 -> 186 us.)
+  const bool fp32_bwd = tensors == 4 && es == 4;
+  s.units = u > hq::kNormThreads || (u >= 64 && M >= 4 * sms && !fp32_bwd) ? 2 : 1;
   s.tpr = ((u + s.units - 1) / s.units + 31) / 32 * 32;
   // narrow rows: several per step, while every SM still gets a step
   int64_t rows = s.ranks > 1 ? 1 : hq::kNormThreads / s.tpr;
   if (rows > (M + sms - 1) / sms) rows = (M + sms - 1) / sms;
+  const int64_t row_bytes = static_cast<int64_t>(tensors) * s.cols * es;
+  if (rows > kSmemBytes / kMinStages / row_bytes) rows = kSmemBytes / kMinStages / row_bytes;  // (1 at least)
   s.rows = static_cast<int>(rows);
-  const size_t stage = static_cast<size_t>(tensors) * s.rows * s.cols * es;
-  const size_t n = kSmemBytes / stage;  // at least 3
+  const size_t stage = static_cast<size_t>(row_bytes * s.rows), n = kSmemBytes / stage;
   s.stages = static_cast<int>(n > hq::kNormMaxStages ? hq::kNormMaxStages : n);
   s.smem = s.stages * stage;
-  if (s.smem < 8 * static_cast<size_t>(s.cols)) s.smem = 8 * s.cols;  // the column sums lie over the ring
   return s;
 }
 
@@ -261,7 +267,7 @@ hq_status hq_block_norm_bwd(const void* dh_out, int64_t ld_dh, const void* dn, i
                               : launch(hq::k_block_norm_bwd<true, 2, true>, p, s, n_cl, cs))
               : (s.units == 1 ? launch(hq::k_block_norm_bwd<true, 1, false>, p, s, n_cl, cs)
                               : launch(hq::k_block_norm_bwd<true, 2, false>, p, s, n_cl, cs));
-  else  // at most 4096 columns per CTA: one unit per thread
+  else
     e = plain ? launch(hq::k_block_norm_bwd<false, 1, true>, p, s, n_cl, cs)
               : launch(hq::k_block_norm_bwd<false, 1, false>, p, s, n_cl, cs);
   if (e != cudaSuccess) return cuda_fail(e);

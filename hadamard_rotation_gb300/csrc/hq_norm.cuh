@@ -249,7 +249,7 @@ struct RowRing {
   __device__ __forceinline__ int tensor_bytes() const { return p.rows * p.cols * kEs; }
   __device__ __forceinline__ int next(int s) const { return s + 1 == p.stages ? 0 : s + 1; }
 
-  // Thread 0: the copies of this cluster's step i into stage s.
+  // One warp: the copies of this cluster's step i into stage s; rows that follow one another in one copy.
   __device__ __forceinline__ void fetch(int i, int s) const {
     if (i >= steps) return;
     const uint32_t bar = smem_addr(&sh.full[s]);
@@ -258,21 +258,27 @@ struct RowRing {
     int tensors = 0;
 #pragma unroll
     for (int t = 0; t < NT; ++t) tensors += p.in[t] != nullptr;
-    mbar_expect_tx(bar, static_cast<uint32_t>(tensors * n * bytes));
+    if (elect_one()) {
+      mbar_expect_tx(bar, static_cast<uint32_t>(tensors * n * bytes));
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (!p.in[t]) continue;
-      const uint8_t* src = p.in[t] + row0 * p.ld[t] + static_cast<int64_t>(col0) * kEs;
-      uint32_t dst = smem_addr(base) + (s * NT + t) * tensor_bytes();
-      for (int r = 0; r < n; ++r) {
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-            "l"(src), "r"(static_cast<uint32_t>(bytes)), "r"(bar)
-            : "memory");
-        src += p.ld[t];
-        dst += p.cols * kEs;
+      for (int t = 0; t < NT; ++t) {
+        if (!p.in[t]) continue;
+        const uint8_t* src = p.in[t] + row0 * p.ld[t] + static_cast<int64_t>(col0) * kEs;
+        uint32_t dst = smem_addr(base) + (s * NT + t) * tensor_bytes();
+        const bool whole = p.ld[t] == bytes;
+        const int copies = whole ? 1 : n;
+        const uint32_t size = static_cast<uint32_t>(whole ? n * bytes : bytes);
+        for (int r = 0; r < copies; ++r) {
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+              "l"(src), "r"(size), "r"(bar)
+              : "memory");
+          src += p.ld[t];
+          dst += p.cols * kEs;
+        }
       }
     }
+    __syncwarp();
   }
   __device__ __forceinline__ bool wait(int s, uint32_t phase) const { return mbar_wait(smem_addr(&sh.full[s]), phase); }
 };
@@ -293,13 +299,17 @@ struct RowRing {
                          static_cast<int>((all_steps - cluster + clusters - 1) / clusters), col0,     \
                          my_cols * kEs};                                                        \
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");                                     \
-  if (threadIdx.x == 0) {                                                                             \
+  /* the last warp fetches the rows */                                                                \
+  const bool fetches = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0) == (blockDim.x >> 5) - 1;        \
+  if (threadIdx.x == blockDim.x - 32) {                                                               \
     for (int i = 0; i < p.stages; ++i) mbar_init(smem_addr(&sh.full[i]), 1);                          \
     fence_mbar_init();                                                                                \
   }                                                                                                   \
   asm volatile("griddepcontrol.wait;" ::: "memory");                                                  \
-  if (threadIdx.x == 0)                                                                               \
+  if (fetches) {                                                                                      \
+    __syncwarp();                                                                                     \
     for (int i = 0; i < p.stages; ++i) ring.fetch(i, i);                                              \
+  }                                                                                                   \
   const int row = threadIdx.x / p.tpr, lane_u = threadIdx.x - row * p.tpr, warps = p.tpr >> 5;        \
   float2 w_pre[V][4], w_post[V][4];                                                                   \
   bool in[V];                                                                                         \
@@ -337,7 +347,7 @@ __device__ __forceinline__ void step_sync(uint32_t ranks) {
 // After the last step: report a wait that ran out, with the copies in flight given time to land.
 #define HQ_NORM_FINISH()                                                                              \
   if (!ok) {                                                                                          \
-    if (threadIdx.x == 0)                                                                             \
+    if (fetches)                                                                                      \
       for (int i = ring.steps > p.stages ? ring.steps - p.stages : 0; i < ring.steps; ++i)            \
         ring.wait(i % p.stages, (i / p.stages) & 1);                                                  \
     if ((threadIdx.x & 31) == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);                            \
@@ -449,7 +459,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
       if (pre) put_sums<1>(sh, parity, 1, ranks, rank, ss);
     }
     step_sync(ranks);
-    if (threadIdx.x == 0 && i >= 1) {  // row i - 1 has left its stage
+    if (fetches && i >= 1) {  // row i - 1 has left its stage
       fence_proxy_async_smem();
       ring.fetch(i - 1 + p.stages, s1);
     }
@@ -606,7 +616,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
         }
     }
     step_sync(ranks);
-    if (threadIdx.x == 0 && i >= 1) {  // row i - 1 has left its stage
+    if (fetches && i >= 1) {  // row i - 1 has left its stage
       fence_proxy_async_smem();
       ring.fetch(i - 1 + p.stages, s1);
     }
@@ -617,26 +627,24 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
     if (s0 == 0) phase ^= 1;
   }
   HQ_NORM_FINISH();
-  // The rows of a step add their column sums one after another; the ring is free now.
+  // The step's rows leave their column sums side by side over the ring, which is free now (8 bytes per
+  // row and column, of at least 24), and are added in their order.
   float* const s_sum = reinterpret_cast<float*>(ring.base);
-  for (int r = 0; r < p.rows; ++r) {
-    __syncthreads();
-    if (r != row) continue;
+  __syncthreads();
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (!in[j]) continue;
+  for (int j = 0; j < V; ++j) {
+    if (!in[j]) continue;
+    float2* const at = reinterpret_cast<float2*>(s_sum + row * 2 * p.cols) + (j * p.tpr + lane_u) * 4;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float2* const at = reinterpret_cast<float2*>(s_sum) + (j * p.tpr + lane_u) * 4 + e;
-        at[0] = add2(r ? at[0] : both(0.0f), sum_w[j][e]);
-        at[p.cols / 2] = add2(r ? at[p.cols / 2] : both(0.0f), sum_a[j][e]);
-      }
-    }
+    for (int e = 0; e < 4; ++e) at[e] = sum_w[j][e], at[p.cols / 2 + e] = sum_a[j][e];
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < my_cols; c += blockDim.x) {
-    p.partial[cluster * p.D + col0 + c] = s_sum[c];
-    p.partial[(clusters + cluster) * p.D + col0 + c] = s_sum[p.cols + c];
+  for (int c = threadIdx.x; c < 2 * p.cols; c += blockDim.x) {
+    const int second = c >= p.cols, col = c - second * p.cols;
+    if (col >= my_cols) continue;
+    float v = s_sum[c];
+    for (int r = 1; r < p.rows; ++r) v += s_sum[r * 2 * p.cols + c];
+    p.partial[(second * clusters + cluster) * p.D + col0 + col] = v;
   }
 }
 

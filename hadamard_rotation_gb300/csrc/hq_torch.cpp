@@ -8,7 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -84,7 +84,7 @@ hq_dtype dtype_of(at::ScalarType t) { return t == at::kFloat ? HQ_F32 : HQ_BF16;
 int64_t tiles_bytes(int64_t rows, int64_t cols) { return (rows + 127) / 128 * ((cols + 3) / 4) * 512; }
 
 at::Tensor empty(Shape shape, at::ScalarType type, const at::Tensor& like) {
-  return at::empty(shape, like.options().dtype(type));
+  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
 }
 
 // `out` as given, or a new tensor of type `out_dtype`.

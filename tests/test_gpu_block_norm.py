@@ -66,7 +66,8 @@ def close(got, want, size, name):
     assert not bad.any(), (name, int(bad.sum()), bad.nonzero()[:3].tolist(), float((got.double() - want).abs().max()))
 
 
-SHAPES = [(1, 16), (1, 4096), (3, 48), (37, 416), (5, 8192), (2, 8208), (3, 16384), (2, 32768), (700, 256), (301, 1360)]
+SHAPES = [(1, 16), (1, 4096), (3, 48), (37, 416), (5, 8192), (2, 8208), (3, 16384), (2, 32768), (700, 256), (301, 1360), (640, 4096), (1500, 2064),
+          (650, 8192)]
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
