@@ -434,8 +434,13 @@ def hq_swizzle_scales(scales: torch.Tensor, out: torch.Tensor | None = None,
     scales = _need(scales, scales.shape, torch.uint8, scales.device, "scales")
     rows, cols = scales.shape[-2:]
     groups = scales.shape[0] if scales.dim() == 3 else 1
-    out = _need(out, (*scales.shape[:-2], (rows + 127) // 128 * ((cols + 3) // 4) * 512), torch.uint8, scales.device,
-                "out")
+    shape = (*scales.shape[:-2], (rows + 127) // 128 * ((cols + 3) // 4) * 512)
+    if out is None and stream is not None:  # from the memory of the stream that writes it
+        current = torch.cuda.current_stream(scales.device)
+        with torch.cuda.stream(stream):
+            out = torch.empty(shape, dtype=torch.uint8, device=scales.device)
+        out.record_stream(current)
+    out = _need(out, shape, torch.uint8, scales.device, "out")
     _call(scales.device, "hq_swizzle_scales", _ptr(scales), groups, rows, cols, _ptr(out), stream=stream)
     return out
 

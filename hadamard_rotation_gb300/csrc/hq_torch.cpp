@@ -83,32 +83,13 @@ bool supported(at::ScalarType t) { return t == at::kFloat || t == at::kBFloat16;
 hq_dtype dtype_of(at::ScalarType t) { return t == at::kFloat ? HQ_F32 : HQ_BF16; }
 int64_t tiles_bytes(int64_t rows, int64_t cols) { return (rows + 127) / 128 * ((cols + 3) / 4) * 512; }
 
-at::Tensor empty(Shape shape, at::ScalarType type, const at::Tensor& like) {
-  return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
-}
-
-// `out` as given, or a new tensor of type `out_dtype`.
-at::Tensor output(PyObject* out, PyObject* out_dtype, Shape shape, const at::Tensor& like) {
-  if (out == Py_None) {
-    if (!THPDtype_Check(out_dtype) || !supported(reinterpret_cast<THPDtype*>(out_dtype)->scalar_type))
-      throw Refused("out_dtype must be float32 or bfloat16");
-    return empty(shape, reinterpret_cast<THPDtype*>(out_dtype)->scalar_type, like);
-  }
-  const at::Tensor* t = tensor(out);
-  if (!t || !supported(t->scalar_type())) throw Refused("out must be a float32 or bfloat16 tensor");
-  return given(out, shape, t->scalar_type(), like.get_device(), "out");
-}
-
 // The stream of a call: the one given (of the tensors' device), or that device's current one.
 struct Stream {
+  c10::cuda::CUDAStream current;
   cudaStream_t handle;
-  bool own;  // given
-  Stream(PyObject* o, int index) {
-    own = o != Py_None;
-    if (!own) {
-      handle = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream();
-      return;
-    }
+  Stream(PyObject* o, int index) : current(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index))) {
+    handle = current.stream();
+    if (o == Py_None) return;
     PyObject* d = PyObject_GetAttrString(o, "device_index");
     PyObject* s = d ? PyObject_GetAttrString(o, "cuda_stream") : nullptr;
     if (!d || !s) {
@@ -125,16 +106,33 @@ struct Stream {
   }
 };
 
-// A workspace for one call; it is freed when the call returns, so not before a given stream is done with it.
+// New memory for a call.  It comes from the memory of the call's stream: that of another stream may still be
+// in use there by what was freed last.  A result is handed to the current stream as well.
+at::Tensor empty(Shape shape, at::ScalarType type, const at::Tensor& like, const Stream& stream, bool result = true) {
+  if (stream.handle == stream.current.stream()) return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+  const c10::cuda::CUDAStreamGuard guard(
+      c10::cuda::getStreamFromExternal(stream.handle, static_cast<c10::DeviceIndex>(like.get_device())));
+  at::Tensor t = at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
+  if (result && t.numel()) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), stream.current);
+  return t;
+}
+
+// A workspace for one call, freed when the call returns: later work on its stream may have it then.
 at::Tensor workspace(int64_t bytes, const at::Tensor& like, const Stream& stream) {
   if (bytes < 0) throw Refused("sizes that the library refuses (include/hq.h)");
-  if (bytes == 0) return at::Tensor();
-  at::Tensor w = empty({bytes}, at::kByte, like);
-  if (stream.own)
-    c10::cuda::CUDACachingAllocator::recordStream(
-        w.storage().data_ptr(),
-        c10::cuda::getStreamFromExternal(stream.handle, static_cast<c10::DeviceIndex>(like.get_device())));
-  return w;
+  return bytes == 0 ? at::Tensor() : empty({bytes}, at::kByte, like, stream, false);
+}
+
+// `out` as given, or a new tensor of type `out_dtype`.
+at::Tensor output(PyObject* out, PyObject* out_dtype, Shape shape, const at::Tensor& like, const Stream& stream) {
+  if (out == Py_None) {
+    if (!THPDtype_Check(out_dtype) || !supported(reinterpret_cast<THPDtype*>(out_dtype)->scalar_type))
+      throw Refused("out_dtype must be float32 or bfloat16");
+    return empty(shape, reinterpret_cast<THPDtype*>(out_dtype)->scalar_type, like, stream);
+  }
+  const at::Tensor* t = tensor(out);
+  if (!t || !supported(t->scalar_type())) throw Refused("out must be a float32 or bfloat16 tensor");
+  return given(out, shape, t->scalar_type(), like.get_device(), "out");
 }
 
 void* addr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -207,8 +205,8 @@ PyObject* grouped_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* t = at_given<uint8_t>(a[4], {E, tiles_bytes(N, K / block)}, at::kByte, index, "ws");
     const auto* h = MX ? nullptr : at_given<float>(a[5], {E}, at::kFloat, index, "w_sg");
     const auto* o = at_given<int32_t>(a[6], {E + 1}, at::kInt, index, "offsets");
-    const at::Tensor out = output(a[7], a[8], {M, N}, xq);
     const Stream stream(a[9], index);
+    const at::Tensor out = output(a[7], a[8], {M, N}, xq, stream);
     const at::Tensor work = workspace(hq_grouped_gemm_workspace_bytes(M, N, K, E), xq, stream);
     run(index, MX ? "hq_grouped_gemm_mxfp4" : "hq_grouped_gemm_nvfp4", [&] {
       const hq_dtype dt = dtype_of(out.scalar_type());
@@ -235,8 +233,8 @@ PyObject* grouped_wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* t = at_given<uint8_t>(a[4], {tiles_bytes(K, T / block)}, at::kByte, index, "xs");
     const auto* h = MX ? nullptr : at_given<float>(a[5], {1}, at::kFloat, index, "x_sg");
     const auto* o = at_given<int32_t>(a[6], {E + 1}, at::kInt, index, "offsets");
-    const at::Tensor out = output(a[7], a[8], {E, N, K}, gq);
     const Stream stream(a[9], index);
+    const at::Tensor out = output(a[7], a[8], {E, N, K}, gq, stream);
     run(index, MX ? "hq_grouped_wgrad_mxfp4" : "hq_grouped_wgrad_nvfp4", [&] {
       const hq_dtype dt = dtype_of(out.scalar_type());
       return MX ? hq_grouped_wgrad_mxfp4(q, s, x, t, o, T, N, K, E, out.data_ptr(), dt, stream.handle)
@@ -271,8 +269,8 @@ PyObject* lora_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* sc = at_given<float>(a[9], {count}, at::kFloat, index, "scaling");
     const auto* id = at_given<int32_t>(a[10], {M}, at::kInt, index, "row_adapter");
     const int64_t ldx = M > 1 ? x->stride(0) : K;
-    const at::Tensor out = output(a[11], a[12], {M, N}, xq);
     const Stream stream(a[13], index);
+    const at::Tensor out = output(a[11], a[12], {M, N}, xq, stream);
     const at::Tensor work = workspace(hq_lora_gemm_workspace_bytes(M, N, K, R), xq, stream);
     run(index, MX ? "hq_lora_gemm_mxfp4" : "hq_lora_gemm_nvfp4", [&] {
       const hq_dtype dt = dtype_of(out.scalar_type());
@@ -379,16 +377,17 @@ PyObject* block_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
     const float alpha = number(a[5]), eps = number(a[6]);
     int group = 0;
     if (a[9] != Py_None) {
-      group = static_cast<int>(PyLong_AsLong(a[9]));
-      if (PyErr_Occurred()) throw PythonError();
+      const long v = PyLong_AsLong(a[9]);
+      if (v == -1 && PyErr_Occurred()) throw PythonError();
+      group = v < 0 || v > 256 ? -1 : static_cast<int>(v);  // (-1: refused by the library)
     }
     const Stream stream(a[12], index);
     at::Tensor h_out, n, r_post, r_pre, amax;
-    if (has_y) h_out = a[10] == Py_None ? empty({M, D}, type, h) : given(a[10], {M, D}, type, index, "h_out");
-    if (pre) n = a[11] == Py_None ? empty({M, D}, type, h) : given(a[11], {M, D}, type, index, "n");
-    if (post) r_post = empty({M}, at::kFloat, h);
-    if (pre) r_pre = empty({M}, at::kFloat, h);
-    if (a[9] != Py_None) amax = empty({1}, at::kFloat, h);
+    if (has_y) h_out = a[10] == Py_None ? empty({M, D}, type, h, stream) : given(a[10], {M, D}, type, index, "h_out");
+    if (pre) n = a[11] == Py_None ? empty({M, D}, type, h, stream) : given(a[11], {M, D}, type, index, "n");
+    if (post) r_post = empty({M}, at::kFloat, h, stream);
+    if (pre) r_pre = empty({M}, at::kFloat, h, stream);
+    if (a[9] != Py_None) amax = empty({1}, at::kFloat, h, stream);
     run(index, "hq_block_norm", [&] {
       return hq_block_norm(rh.p, rh.ld, ry.p, ry.ld, dtype_of(type), M, D, p.w_post, p.w_pre, dtype_of(p.type), p.kind,
                            p.gate, p.ld_gate, (post ? HQ_NORM_POST : 0) | (pre ? HQ_NORM_PRE : 0), alpha, eps,
@@ -419,12 +418,12 @@ PyObject* block_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t count) {
     const float* r_pre = pre ? at_given<float>(a[8], {M}, at::kFloat, index, "r_pre") : nullptr;
     const float alpha = number(a[9]);
     const Stream stream(a[12], index);
-    at::Tensor dh = empty({M, D}, type, h), dy, dw_post, dw_pre, dgate;
-    if (has_y) dy = empty({M, D}, type, h);
-    if (p.w_post) dw_post = empty({D}, at::kFloat, h);
-    if (p.w_pre) dw_pre = empty({D}, at::kFloat, h);
+    at::Tensor dh = empty({M, D}, type, h, stream), dy, dw_post, dw_pre, dgate;
+    if (has_y) dy = empty({M, D}, type, h, stream);
+    if (p.w_post) dw_post = empty({D}, at::kFloat, h, stream);
+    if (p.w_pre) dw_pre = empty({D}, at::kFloat, h, stream);
     if (p.kind != HQ_GATE_NONE)
-      dgate = empty(tensor(a[5])->sizes(), p.kind == HQ_GATE_FULL ? type : at::kFloat, h);
+      dgate = empty(tensor(a[5])->sizes(), p.kind == HQ_GATE_FULL ? type : at::kFloat, h, stream);
     const at::Tensor work = workspace(hq_block_norm_bwd_workspace_bytes(M, D), h, stream);
     run(index, "hq_block_norm_bwd", [&] {
       return hq_block_norm_bwd(rd.p, rd.ld, rn.p, rn.ld, rh.p, rh.ld, ry.p, ry.ld, dtype_of(type), M, D, p.w_post,
