@@ -131,6 +131,36 @@ cudaError_t hq::allow_smem(const void* fn, int bytes) {
   return e;
 }
 
+cudaError_t hq::clusters_at_a_time(const void* fn, const cudaLaunchConfig_t& cfg, int ranks, int* n) {
+  struct Entry {
+    unsigned long long ctx;
+    int n;
+  };
+  static std::mutex mu;
+  static Entry entries[16][17];  // [device][CTAs of a cluster]
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long ctx = hq::context_id();
+  const bool kept = ctx != 0 && dev < 16 && ranks <= 16;
+  if (kept) {
+    std::lock_guard<std::mutex> lock(mu);
+    const Entry& k = entries[dev][ranks];
+    if (k.ctx == ctx) {
+      *n = k.n;
+      return cudaSuccess;
+    }
+  }
+  e = cudaOccupancyMaxActiveClusters(n, fn, &cfg);
+  if (e != cudaSuccess) return e;
+  if (*n < 1) return cudaErrorInvalidConfiguration;
+  if (kept) {
+    std::lock_guard<std::mutex> lock(mu);
+    entries[dev][ranks] = {ctx, *n};
+  }
+  return cudaSuccess;
+}
+
 namespace {
 
 using hq::cuda_fail;

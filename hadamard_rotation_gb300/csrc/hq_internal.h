@@ -25,6 +25,10 @@ cudaError_t norm_fault_word(unsigned int* fault, bool clear);
 // context, so that a call of a few microseconds asks the runtime once.
 cudaError_t allow_smem(const void* fn, int bytes);
 
+// How many clusters of `ranks` CTAs, each alone on its SM, run at a time (not sms / ranks: the SMs of a cluster
+// lie in one part of the chip); asked for once per device, context and size.  `cfg`: a launch of them.
+cudaError_t clusters_at_a_time(const void* fn, const cudaLaunchConfig_t& cfg, int ranks, int* n);
+
 // Multiprocessors of the current device, asked for once per device.
 cudaError_t sm_count(int* sms);
 

@@ -51,33 +51,39 @@ Shape shape_of(int64_t M, int D, int es, int tensors, int sms) {
   return s;
 }
 
+// Launches as many clusters as there are steps and as run at a time (clusters of 4: 36 of them on 144 of the 152
+// SMs; two more would run after all others), and says how many.
 template <typename Kernel>
-cudaError_t launch(Kernel kernel, const NormParams& p, const Shape& s, int clusters, cudaStream_t stream) {
+cudaError_t launch(Kernel kernel, const NormParams& p, const Shape& s, int sms, int* clusters, cudaStream_t stream) {
   cudaError_t e = hq::allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(s.smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * s.ranks));
+  cfg.gridDim = dim3(static_cast<unsigned>(sms / s.ranks * s.ranks));
   cfg.blockDim = dim3(static_cast<unsigned>(s.tpr * s.rows));
   cfg.dynamicSmemBytes = s.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(s.ranks);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(s.ranks);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  int at_a_time = sms;
+  if (s.ranks > 1) {
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = hq::clusters_at_a_time(reinterpret_cast<const void*>(kernel), cfg, s.ranks, &at_a_time)) != cudaSuccess)
+      return e;
+  }
+  const int64_t steps = (p.M + s.rows - 1) / s.rows;
+  int64_t n = at_a_time < hq::kNormMaxPartials ? at_a_time : hq::kNormMaxPartials;
+  if (n > steps) n = steps;
+  *clusters = static_cast<int>(n);
+  cfg.gridDim = dim3(static_cast<unsigned>(n * s.ranks));
+  cfg.attrs = s.ranks > 1 ? attr : attr + 1;
   cfg.numAttrs = s.ranks > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kernel, p);
   return e == cudaSuccess ? cudaGetLastError() : e;
-}
-
-int clusters_of(const Shape& s, int64_t M, int sms) {
-  const int64_t steps = (M + s.rows - 1) / s.rows;
-  int64_t n = sms / s.ranks;
-  if (n > hq::kNormMaxPartials) n = hq::kNormMaxPartials;
-  if (n > steps) n = steps;
-  return static_cast<int>(n < 1 ? 1 : n);
 }
 
 hq_status check_sizes(hq_dtype dt, hq_dtype params, int64_t M, int64_t D, hq_gate_kind kind, const void* gate,
@@ -174,18 +180,18 @@ hq_status hq_block_norm(const void* h, int64_t ld_h, const void* y, int64_t ld_y
   p.rows = s.rows;
   p.stages = s.stages;
   if (amax && (e = cudaMemsetAsync(amax, 0, 4, cs)) != cudaSuccess) return cuda_fail(e);
-  const int n_cl = clusters_of(s, M, sms);
+  int n_cl = 0;
   const bool plain = post && pre && y && !amax && (gate_kind == HQ_GATE_NONE || gate_kind == HQ_GATE_CHANNEL);
   if (dtype == HQ_BF16)
-    e = plain ? (s.units == 1 ? launch(hq::k_block_norm<true, 1, true>, p, s, n_cl, cs)
-                              : launch(hq::k_block_norm<true, 2, true>, p, s, n_cl, cs))
-              : (s.units == 1 ? launch(hq::k_block_norm<true, 1, false>, p, s, n_cl, cs)
-                              : launch(hq::k_block_norm<true, 2, false>, p, s, n_cl, cs));
+    e = plain ? (s.units == 1 ? launch(hq::k_block_norm<true, 1, true>, p, s, sms, &n_cl, cs)
+                              : launch(hq::k_block_norm<true, 2, true>, p, s, sms, &n_cl, cs))
+              : (s.units == 1 ? launch(hq::k_block_norm<true, 1, false>, p, s, sms, &n_cl, cs)
+                              : launch(hq::k_block_norm<true, 2, false>, p, s, sms, &n_cl, cs));
   else
-    e = plain ? (s.units == 1 ? launch(hq::k_block_norm<false, 1, true>, p, s, n_cl, cs)
-                              : launch(hq::k_block_norm<false, 2, true>, p, s, n_cl, cs))
-              : (s.units == 1 ? launch(hq::k_block_norm<false, 1, false>, p, s, n_cl, cs)
-                              : launch(hq::k_block_norm<false, 2, false>, p, s, n_cl, cs));
+    e = plain ? (s.units == 1 ? launch(hq::k_block_norm<false, 1, true>, p, s, sms, &n_cl, cs)
+                              : launch(hq::k_block_norm<false, 2, true>, p, s, sms, &n_cl, cs))
+              : (s.units == 1 ? launch(hq::k_block_norm<false, 1, false>, p, s, sms, &n_cl, cs)
+                              : launch(hq::k_block_norm<false, 2, false>, p, s, sms, &n_cl, cs));
   return e == cudaSuccess ? HQ_OK : cuda_fail(e);
 }
 
@@ -260,16 +266,16 @@ hq_status hq_block_norm_bwd(const void* dh_out, int64_t ld_dh, const void* dn, i
   p.tpr = s.tpr;
   p.rows = s.rows;
   p.stages = s.stages;
-  const int n_cl = clusters_of(s, M, sms);
+  int n_cl = 0;
   const bool plain = post && pre && dh_out && (gate_kind == HQ_GATE_NONE || gate_kind == HQ_GATE_CHANNEL);
   if (dtype == HQ_BF16)
-    e = plain ? (s.units == 1 ? launch(hq::k_block_norm_bwd<true, 1, true>, p, s, n_cl, cs)
-                              : launch(hq::k_block_norm_bwd<true, 2, true>, p, s, n_cl, cs))
-              : (s.units == 1 ? launch(hq::k_block_norm_bwd<true, 1, false>, p, s, n_cl, cs)
-                              : launch(hq::k_block_norm_bwd<true, 2, false>, p, s, n_cl, cs));
+    e = plain ? (s.units == 1 ? launch(hq::k_block_norm_bwd<true, 1, true>, p, s, sms, &n_cl, cs)
+                              : launch(hq::k_block_norm_bwd<true, 2, true>, p, s, sms, &n_cl, cs))
+              : (s.units == 1 ? launch(hq::k_block_norm_bwd<true, 1, false>, p, s, sms, &n_cl, cs)
+                              : launch(hq::k_block_norm_bwd<true, 2, false>, p, s, sms, &n_cl, cs));
   else
-    e = plain ? launch(hq::k_block_norm_bwd<false, 1, true>, p, s, n_cl, cs)
-              : launch(hq::k_block_norm_bwd<false, 1, false>, p, s, n_cl, cs);
+    e = plain ? launch(hq::k_block_norm_bwd<false, 1, true>, p, s, sms, &n_cl, cs)
+              : launch(hq::k_block_norm_bwd<false, 1, false>, p, s, sms, &n_cl, cs);
   if (e != cudaSuccess) return cuda_fail(e);
   float* const to_pre = pre ? dw_pre : nullptr;
   float* const to_post = post ? dw_post : nullptr;

@@ -149,51 +149,82 @@ __device__ __forceinline__ void param_unit(const void* w, int64_t col, int bf16,
     f[e] = in ? make_float2(norm_param(w, col + 2 * e, bf16), norm_param(w, col + 2 * e + 1, bf16)) : both(0.0f);
 }
 
-// A float into the same shared variable of CTA `rank` of the cluster.
-__device__ __forceinline__ void store_cluster(const float* p, uint32_t rank, float v) {
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "st.shared::cluster.f32 [a], %2;\n\t}" ::"r"(smem_addr(p)),
-      "r"(rank), "f"(v)
-      : "memory");
-}
+// The row sums of four steps.  In a cluster every warp sends its sums to every CTA by asynchronous stores that
+// count on the step's mbarrier there: no barrier of the cluster, whose release would also wait for the output
+// rows' stores (bf16 [700, 28672] forward 99 us with one per step).  Four steps' slots are enough: a warp sends
+// for step j after it has all sums of step j - 2, every warp sent those after it had read the sums of step j - 4.
+constexpr int kNormSlots = 4;
 
 struct NormShared {
   uint64_t full[kNormMaxStages];
-  // the warps' row sums, by the parity of the step that made them: [.][rank * 16 + warp]
-  float part[2][4][kNormMaxCluster * 16];
+  uint64_t sums[kNormSlots];
+  float part[kNormSlots][3][kNormMaxCluster * 16];  // [.][.][rank * 16 + warp]
   float most[kNormThreads / 32];
 };
 
+// A float into the same shared variable of CTA `rank` of the cluster, counted on that CTA's barrier.
+__device__ __forceinline__ void send_cluster(const float* p, const uint64_t* bar, uint32_t rank, float v) {
+  asm volatile(
+      "{\n\t.reg .b32 a, b;\n\tmapa.shared::cluster.u32 a, %0, %2;\n\tmapa.shared::cluster.u32 b, %1, %2;\n\t"
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [a], %3, [b];\n\t}" ::"r"(smem_addr(p)),
+      "r"(smem_addr(bar)), "r"(rank), "r"(__float_as_uint(v))
+      : "memory");
+}
+
+// Waits for a step's sums, up to the limit of mbar_wait.
+__device__ __forceinline__ bool wait_sums(const NormShared& sh, int step) {
+  const uint32_t bar = smem_addr(&sh.sums[step & (kNormSlots - 1)]), parity = step / kNormSlots & 1;
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 15u) == 0) {
+      const uint64_t now = global_timer_ns();
+      if (i == 0)
+        t0 = now;
+      else if (now - t0 > kWaitLimitNs)
+        return false;
+    }
+  }
+}
+
 // This warp's sums of NS values, as sums `first` .. of a step, for every CTA of the cluster.
 template <int NS>
-__device__ __forceinline__ void put_sums(NormShared& sh, int parity, int first, uint32_t ranks, uint32_t rank,
+__device__ __forceinline__ void put_sums(NormShared& sh, int step, int first, uint32_t ranks, uint32_t rank,
                                          float (&s)[NS]) {
 #pragma unroll
   for (int i = 0; i < NS; ++i)
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], m);
   const int lane = threadIdx.x & 31, at = static_cast<int>(rank) * 16 + (threadIdx.x >> 5);
+  const int slot = step & (kNormSlots - 1);
   if (ranks == 1) {
     if (lane == 0)
 #pragma unroll
-      for (int i = 0; i < NS; ++i) sh.part[parity][first + i][at] = s[i];
+      for (int i = 0; i < NS; ++i) sh.part[slot][first + i][at] = s[i];
   } else if (lane < static_cast<int>(ranks)) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) store_cluster(&sh.part[parity][first + i][at], lane, s[i]);
+    for (int i = 0; i < NS; ++i) send_cluster(&sh.part[slot][first + i][at], &sh.sums[slot], lane, s[i]);
   }
 }
 
 // The sums of a row of an earlier step, over its warps and the cluster, in a fixed order.
 template <int NS>
-__device__ __forceinline__ void get_sums(const NormShared& sh, int parity, int first, int warps, int row, uint32_t ranks,
+__device__ __forceinline__ void get_sums(const NormShared& sh, int step, int first, int warps, int row, uint32_t ranks,
                                          float (&s)[NS]) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, slot = step & (kNormSlots - 1);
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     s[i] = 0.0f;
     if (lane < warps)
-      for (uint32_t r = 0; r < ranks; ++r) s[i] += sh.part[parity][first + i][r * 16 + row * warps + lane];
+      for (uint32_t r = 0; r < ranks; ++r) s[i] += sh.part[slot][first + i][r * 16 + row * warps + lane];
 #pragma unroll
     for (int m = 8; m >= 1; m >>= 1) s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], m);
     s[i] = __shfl_sync(0xFFFFFFFFu, s[i], 0);
@@ -303,6 +334,7 @@ struct RowRing {
   const bool fetches = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0) == (blockDim.x >> 5) - 1;        \
   if (threadIdx.x == blockDim.x - 32) {                                                               \
     for (int i = 0; i < p.stages; ++i) mbar_init(smem_addr(&sh.full[i]), 1);                          \
+    for (int i = 0; i < kNormSlots; ++i) mbar_init(smem_addr(&sh.sums[i]), 1);                        \
     fence_mbar_init();                                                                                \
   }                                                                                                   \
   asm volatile("griddepcontrol.wait;" ::: "memory");                                                  \
@@ -338,10 +370,10 @@ struct RowRing {
   __syncthreads();                                                                                    \
   if (ranks > 1) cluster_sync() /* the peers' shared memory is there */
 
-// The barrier of a step: sums put before it can be got after it.
-__device__ __forceinline__ void step_sync(uint32_t ranks) {
-  if (ranks > 1) cluster_sync();
-  else __syncthreads();
+// In a cluster: thread 0 says how many sums per warp a step will bring.
+__device__ __forceinline__ void expect_sums(const NormShared& sh, int step, int sums, uint32_t ranks, bool ok) {
+  if (ranks > 1 && threadIdx.x == 0 && ok)
+    mbar_expect_tx(smem_addr(&sh.sums[step & (kNormSlots - 1)]), sums * ranks * (blockDim.x >> 5) * 4);
 }
 
 // After the last step: report a wait that ran out, with the copies in flight given time to land.
@@ -351,7 +383,8 @@ __device__ __forceinline__ void step_sync(uint32_t ranks) {
       for (int i = ring.steps > p.stages ? ring.steps - p.stages : 0; i < ring.steps; ++i)            \
         ring.wait(i % p.stages, (i / p.stages) & 1);                                                  \
     if ((threadIdx.x & 31) == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);                            \
-  }
+  }                                                                                                   \
+  if (ranks > 1) cluster_sync() /* no CTA leaves before its peers' sums have arrived */
 
 // PLAIN: both norms, y, no gate or one per channel, no amax -- known to the compiler, which then has no
 // branch in the loop (bf16 [16384, 8192] forward 235 us without).
@@ -370,8 +403,8 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
   int64_t at1 = ((m0 - stride) * p.D + col0 + lane_u * 8) * kEs;
   // Step i: the sum over y of its i-th row; h' of row i - 1; n of row i - 2.
   for (int i = 0; i < ring.steps + 2; ++i) {
-    const int parity = i & 1;
     const int64_t m1 = m0 - stride, m2 = m1 - stride;
+    expect_sums(sh, i, (post && i < ring.steps) + (pre && i >= 1 && i <= ring.steps), ranks, ok);
     const bool live1 = i >= 1 && i <= ring.steps && m1 < p.M, live2 = i >= 2 && m2 < p.M;
     float gate = 1.0f;
     if (by_token && live1) gate = norm_param(p.gate, m1, p.params_bf16);
@@ -392,12 +425,13 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
               for (int e = 0; e < 4; ++e) sq = fma2(y[e], y[e], sq);
             }
         float ss[1] = {sq.x + sq.y};
-        put_sums<1>(sh, parity, 0, ranks, rank, ss);
+        put_sums<1>(sh, i, 0, ranks, rank, ss);
       }
     }
+    if (ranks > 1 && i >= 1) ok = ok && wait_sums(sh, i - 1);
     if (pre && i >= 2) {  // n of row i - 2, from t
       float ss[1];
-      get_sums<1>(sh, parity ^ 1, 1, warps, row, ranks, ss);
+      get_sums<1>(sh, i - 1, 1, warps, row, ranks, ss);
       const float r_pre = rsqrtf(fmaf(ss[0], inv_d, p.eps));
       if (live2 && lane_u == 0 && rank == 0) p.r_pre[m2] = r_pre;
       uint8_t* const dst = static_cast<uint8_t*>(p.n) + (at1 - row_step);
@@ -418,7 +452,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
     if (i >= 1 && i <= ring.steps) {  // h' of row i - 1
       float r_post = 1.0f, ss[1];
       if (post) {
-        get_sums<1>(sh, parity ^ 1, 0, warps, row, ranks, ss);
+        get_sums<1>(sh, i - 1, 0, warps, row, ranks, ss);
         r_post = rsqrtf(fmaf(ss[0], inv_d, p.eps));
         if (live1 && lane_u == 0 && rank == 0) p.r_post[m1] = r_post;
       }
@@ -456,9 +490,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
         for (int e = 0; e < 4; ++e) sq = fma2(t[j][e], t[j][e], sq);
       }
       ss[0] = sq.x + sq.y;
-      if (pre) put_sums<1>(sh, parity, 1, ranks, rank, ss);
+      if (pre) put_sums<1>(sh, i, 1, ranks, rank, ss);
     }
-    step_sync(ranks);
+    __syncthreads();  // one CTA's sums put before it can be got after it; and the stage is free
     if (fetches && i >= 1) {  // row i - 1 has left its stage
       fence_proxy_async_smem();
       ring.fetch(i - 1 + p.stages, s1);
@@ -505,8 +539,8 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
   RowScalars next = scalars(0, m0), now = next, before = next;
   // Step i: the sums of its i-th row; the gradients of row i - 1.
   for (int i = 0; i < ring.steps + 1; ++i) {
-    const int parity = i & 1;
     const int64_t m1 = m0 - stride;
+    expect_sums(sh, i, i < ring.steps ? 3 : 0, ranks, ok);
     before = now;
     now = next;
     next = scalars(i + 1, m0 + stride);
@@ -553,11 +587,12 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
           }
         }
       float s[3] = {c[0].x + c[0].y, c[1].x + c[1].y, c[2].x + c[2].y};
-      put_sums<3>(sh, parity, 0, ranks, rank, s);
+      put_sums<3>(sh, i, 0, ranks, rank, s);
     }
     if (i >= 1) {
+      if (ranks > 1) ok = ok && wait_sums(sh, i - 1);
       float s[3];
-      get_sums<3>(sh, parity ^ 1, 0, warps, row, ranks, s);
+      get_sums<3>(sh, i - 1, 0, warps, row, ranks, s);
       const float r_pre = before.r_pre, r_post = before.r_post, tok = before.tok;
       const float k1 = r_pre * r_pre * r_pre * (s[0] * inv_d);
       const float dot = fmaf(-k1, s[2], s[1]);  // sum d q (a per-token gate left out)
@@ -615,7 +650,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
           x.store(static_cast<uint8_t*>(p.dy) + at1 + j * unit);
         }
     }
-    step_sync(ranks);
+    __syncthreads();  // one CTA's sums put before it can be got after it; and the stage is free
     if (fetches && i >= 1) {  // row i - 1 has left its stage
       fence_proxy_async_smem();
       ring.fetch(i - 1 + p.stages, s1);
