@@ -1073,13 +1073,25 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
         if (!kPair && !waited && p.after_shrink) asm volatile("griddepcontrol.wait;" ::: "memory");
         waited = true;
       };
-      while (ok && order.get(t)) {
-        role_sync<1>();  // the last tile's lists have been read
-        if (warp == S::kLoraWarp) {
-          int got[T / 32], n = 0;
+      // Eight threads take the eight 16-byte pieces of a row (half a slot each), 16 rows at a time: a request of a
+      // warp is then four whole rows where an adapter has 64 ranks.  (A thread per row took 5000 cycles for a
+      // chunk's loads, and with two adapters per tile more than the tile's products.)
+      const int piece = tid & 7, row_of = tid >> 3;
+      constexpr int kRowsAtOnce = kLoraThreads / 8, kTimesB = kGemmLanes / kRowsAtOnce, kTimesT = S::kRowsB / kRowsAtOnce;
+      int got[T / 32];
+      auto load_ids = [&]() {
 #pragma unroll
-          for (int c = 0; c < T / 32; ++c)  // (all in flight together)
-            got[c] = 32 * c + lane < t.valid ? __ldg(p.lora_ids + t.b0 + 32 * c + lane) : -1;
+        for (int c = 0; c < T / 32; ++c)  // (all in flight together)
+          got[c] = 32 * c + lane < t.valid ? __ldg(p.lora_ids + t.b0 + 32 * c + lane) : -1;
+      };
+      bool live = order.get(t);
+      if (live && warp == S::kLoraWarp) load_ids();
+      while (ok && live) {
+        role_sync<1>();  // the last tile's lists have been read
+        const GemmTile now = t;
+        live = order.get(t);
+        if (warp == S::kLoraWarp) {
+          int n = 0;
 #pragma unroll
           for (int c = 0; c < T / 32; ++c) {
             const int r = 32 * c + lane, id = got[c] >= 0 && got[c] < p.adapters ? got[c] : -1;
@@ -1093,76 +1105,55 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
             __syncwarp();
           }
           if (lane == 0) bars.n_distinct = n;
+          if (live) load_ids();  // the next tile's
         }
         role_sync<1>();
         // Slot q holds ranks 16 (q % rank_steps) .. of the tile's adapter q / rank_steps.  (SPLIT: the parts take
         // the chunks in turn.)
         const int slots = bars.n_distinct * rank_steps;
-        const int rows_b = t.n / kCtas, r0 = static_cast<int>(rank) * rows_b;
-        const int n = t.a0 + static_cast<int>(rank) * kGemmLanes + tid;  // this thread's lane
+        const int rows_b = now.n / kCtas, r0 = static_cast<int>(rank) * rows_b;
+        const int n0 = now.a0 + static_cast<int>(rank) * kGemmLanes + row_of;  // this thread's first lane
         int first = 4 * part_k;
         bool more = true;
         do {
           more = first + 4 * splits < slots;
-          const int steps = max(0, min(4, slots - first));
-          int slot_a[4], slot_r[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            slot_a[i] = i < steps ? bars.distinct[(first + i) / rank_steps] : -1;
-            slot_r[i] = i < steps ? (first + i) % rank_steps * 16 : 0;
-          }
+          const int steps = max(0, min(4, slots - first)), slot = first + (piece >> 1);
           first += 4 * splits;
+          const int r = slot % rank_steps * 16 + (piece & 1) * 8;
+          const int a = slot < slots && r < p.rank ? bars.distinct[slot / rank_steps] : -1;
           const uint4 zero = make_uint4(0, 0, 0, 0);
-          uint4 b[4][2];  // B_a of the lane
+          uint4 b[kTimesB];  // B_a
+          const uint8_t* const src_b = p.lora_b + ((static_cast<int64_t>(a) * p.na + n0) * p.rank + r) * 2;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int r = slot_r[i] + 8 * q;
-              b[i][q] = zero;
-              if (slot_a[i] >= 0 && n < p.na && r < p.rank)
-                b[i][q] = __ldg(reinterpret_cast<const uint4*>(
-                    p.lora_b + ((static_cast<int64_t>(slot_a[i]) * p.na + n) * p.rank + r) * 2));
-            }
+          for (int k = 0; k < kTimesB; ++k) {
+            b[k] = zero;
+            if (a >= 0 && n0 + kRowsAtOnce * k < p.na)
+              b[k] = __ldg(reinterpret_cast<const uint4*>(src_b + static_cast<int64_t>(k) * kRowsAtOnce * p.rank * 2));
+          }
           wait_for_t();
-          // t's hi or lo of one of this CTA's rows: zero outside its adapter
-          auto load_t = [&](int item, uint4 (&v)[4][2]) {
-            const int r = r0 + (item >> 1), part = item & 1, id = bars.ids[r];
-            const uint8_t* src = p.lora_t + (static_cast<int64_t>(t.b0 + r) * 2 + part) * p.rank * 2;
+          uint4 v[kTimesT][2];  // t's hi and lo: zero in the rows of other adapters
+          const uint8_t* const src_t = p.lora_t + ((static_cast<int64_t>(now.b0) + r0 + row_of) * 2 * p.rank + r) * 2;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const int k = slot_r[i] + 8 * q;
-                v[i][q] = zero;
-                if (slot_a[i] >= 0 && slot_a[i] == id && k < p.rank)
-                  v[i][q] = __ldcg(reinterpret_cast<const uint4*>(src + k * 2));
-              }
-          };
-          constexpr int kItems = (2 * S::kRowsB + kLoraThreads - 1) / kLoraThreads;
-          uint4 v[kItems][4][2];
-#pragma unroll
-          for (int k = 0; k < kItems; ++k)
-            if (tid + kLoraThreads * k < 2 * rows_b) load_t(tid + kLoraThreads * k, v[k]);
+          for (int k = 0; k < kTimesT; ++k) {
+            const int row = row_of + kRowsAtOnce * k;
+            v[k][0] = v[k][1] = zero;
+            if (a < 0 || row >= rows_b || bars.ids[r0 + row] != a) continue;
+            const uint8_t* src = src_t + static_cast<int64_t>(k) * kRowsAtOnce * p.rank * 4;
+            v[k][0] = __ldcg(reinterpret_cast<const uint4*>(src));
+            v[k][1] = __ldcg(reinterpret_cast<const uint4*>(src + p.rank * 2));
+          }
           // all four warps go on, or none: they meet at barriers
           ok = role_all<1>(mbar_wait(smem_addr(&bars.chunk_empty[chunk.s]), chunk.phase ^ 1));
           if (!ok) break;
-          uint8_t* const ch = chunks + chunk.s * S::kChunkBytes;
+          // (rows 16 apart have the same place in the swizzle)
+          uint8_t* const dst = chunks + chunk.s * S::kChunkBytes + row_of * 128 + ((piece ^ (row_of & 7)) << 4);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int k = 0; k < kTimesB; ++k) *reinterpret_cast<uint4*>(dst + k * kRowsAtOnce * 128) = b[k];
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-              *reinterpret_cast<uint4*>(ch + tid * 128 + (((2 * i + q) ^ (tid & 7)) << 4)) = b[i][q];
+          for (int k = 0; k < kTimesT; ++k)
 #pragma unroll
-          for (int k = 0; k < kItems; ++k) {
-            const int item = tid + kLoraThreads * k, r = item >> 1;
-            if (item >= 2 * rows_b) break;
-            uint8_t* dst = ch + kGemmLanes * 128 + (item & 1) * S::kRowsB * 128 + r * 128;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int q = 0; q < 2; ++q) *reinterpret_cast<uint4*>(dst + (((2 * i + q) ^ (r & 7)) << 4)) = v[k][i][q];
-          }
+            for (int part = 0; part < 2; ++part)
+              *reinterpret_cast<uint4*>(dst + (kGemmLanes + part * S::kRowsB + k * kRowsAtOnce) * 128) = v[k][part];
           if (tid == 0) {
             bars.chunk_steps[chunk.s] = steps;
             bars.chunk_last[chunk.s] = !more;
