@@ -381,7 +381,7 @@ hq_status launch_shrink(hq::ShrinkParams p, const void* x, int64_t ldx, const vo
   // (the instruction reads 128 rows of x from a stage's start; the sums lie over the ring)
   int bytes = p.stages * stage;
   if (bytes < (p.stages - 1) * stage + hq::kShrinkRows * 128) bytes = (p.stages - 1) * stage + hq::kShrinkRows * 128;
-  if (bytes < hq::kShrinkRows * (padded + 1) * 4) bytes = hq::kShrinkRows * (padded + 1) * 4;
+  if (bytes < hq::kShrinkRows * (padded + hq::kShrinkPad) * 4) bytes = hq::kShrinkRows * (padded + hq::kShrinkPad) * 4;
   bytes += 1024;
   CUtensorMap mx, ma;
   if (!encode_bf16(&mx, x, p.K, ldx * 2, p.rows, 1, p.box_rows, 2) ||

@@ -646,6 +646,16 @@ __device__ __forceinline__ float load_cluster(const float* p, uint32_t rank) {
   return v;
 }
 
+__device__ __forceinline__ float4 load_cluster4(const float* p, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(smem_addr(p)), "r"(rank)
+      : "memory");
+  return v;
+}
 
 template <int KIND, bool MX, int T, bool LORA, bool SPLIT>
 __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
@@ -1247,6 +1257,7 @@ constexpr int kShrinkThreads = 192;
 constexpr int kShrinkRows = 128;
 constexpr int kShrinkCols = 128;                    // columns of a pass, at most
 constexpr int kShrinkMaxStages = 4;
+constexpr int kShrinkPad = 4;                       // floats between rows of sums
 
 struct ShrinkParams {
   const float* scaling;    // [adapters]
@@ -1333,10 +1344,10 @@ __global__ void __launch_bounds__(kShrinkThreads)
   bool ok = true;
   float inv = 1.0f;
   if (p.sg_a) inv = __fdiv_rn(1.0f, __fmul_rn(__ldg(p.sg_a), __ldg(p.sg_b)));
-  // The sums [row][rank]: an odd pitch, so that lanes (rows) write without bank conflicts; a row is read
-  // from other CTAs along its ranks (32 rows at once are 32 requests each: 20 us for 4096 rows).
+  // The sums [row][rank], in 16-byte pieces: with this pitch lanes (rows) write them without bank conflicts; a row
+  // is read from other CTAs along its ranks (32 rows at once are 32 requests each: 20 us for 4096 rows).
   float* const sums = reinterpret_cast<float*>(ring);
-  const int pitch = padded + 1;
+  const int pitch = padded + kShrinkPad;
   GemmRing at;
   const uint64_t ring0 = desc_codes(smem_addr(ring));
   long long fills = 0;
@@ -1395,31 +1406,41 @@ __global__ void __launch_bounds__(kShrinkThreads)
           tmem_load(tmem + (static_cast<uint32_t>(warp * 32) << 16) + i * padded + r, v);
           if (mine == i)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) sums[row * pitch + r + k] = kb1 > kb0 ? __uint_as_float(v[k]) : 0.0f;
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(sums + row * pitch + r + 4 * k) =
+                  kb1 > kb0 ? make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]) : make_uint4(0, 0, 0, 0);
         }
       }
       umma_fence_before();
     }
     cluster_sync();
-    // Each CTA of the cluster finishes every slices-th row, a row per warp.
-    for (int row = slice + warp * p.slices; row < kShrinkRows; row += kShrinkThreads / 32 * p.slices) {
+    // Each CTA of the cluster finishes every slices-th row, 4 ranks per thread.
+    const int quads = p.rank / 4, items = kShrinkRows / p.slices * quads;
+    for (int item = threadIdx.x; item < items; item += kShrinkThreads) {
+      const int row = slice + item / quads * p.slices, r = item % quads * 4;
       const int slot = sh.slot[row], mine = slot - pass * per_pass;
       if (slot < 0 || mine < 0 || mine >= slots) continue;
       const float scale = __ldg(p.scaling + sh.adapter[job + slot * p.jobs]) * inv;
-      __nv_bfloat16* const t = p.t + static_cast<int64_t>(row0 + row) * 2 * p.rank;
-      for (int r = lane; r < p.rank; r += 32) {
-        float part[kMaxSplits];
+      float4 part[kMaxSplits];
 #pragma unroll
-        for (int k = 0; k < kMaxSplits; ++k)  // without a condition: all in flight before the first is added
-          part[k] = load_cluster(sums + row * pitch + r, min(k, p.slices - 1));
-        float v = part[0];
+      for (int k = 0; k < kMaxSplits; ++k)  // without a condition: all in flight before the first is added
+        part[k] = load_cluster4(sums + row * pitch + r, min(k, p.slices - 1));
+      float v[4] = {part[0].x, part[0].y, part[0].z, part[0].w};
 #pragma unroll
-        for (int k = 1; k < kMaxSplits; ++k) v += k < p.slices ? part[k] : 0.0f;
-        v *= scale;
-        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-        t[r] = hi;
-        t[p.rank + r] = __float2bfloat16_rn(v - __bfloat162float(hi));
+      for (int k = 1; k < kMaxSplits; ++k) {
+        if (k >= p.slices) continue;
+        v[0] += part[k].x, v[1] += part[k].y, v[2] += part[k].z, v[3] += part[k].w;
       }
+      __nv_bfloat162 hi[2], lo[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float x = v[2 * k] * scale, y = v[2 * k + 1] * scale;
+        hi[k] = __floats2bfloat162_rn(x, y);
+        lo[k] = __floats2bfloat162_rn(x - __low2float(hi[k]), y - __high2float(hi[k]));
+      }
+      __nv_bfloat16* const t = p.t + static_cast<int64_t>(row0 + row) * 2 * p.rank + r;
+      *reinterpret_cast<uint2*>(t) = *reinterpret_cast<const uint2*>(hi);
+      *reinterpret_cast<uint2*>(t + p.rank) = *reinterpret_cast<const uint2*>(lo);
     }
     fence_proxy_async_smem();  // the next pass's copies overwrite the sums
     cluster_sync();
