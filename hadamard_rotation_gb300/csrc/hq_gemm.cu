@@ -368,14 +368,18 @@ hq_status launch_shrink(hq::ShrinkParams p, const void* x, int64_t ldx, const vo
   const int tiles = (p.rows + hq::kShrinkRows - 1) / hq::kShrinkRows, blocks = (p.K + 63) / 64;
   p.slices = 1;
   while (p.slices < 8 && p.slices * 2 <= blocks && tiles * p.slices * 2 <= 2 * sms) p.slices *= 2;
+  const int most = p.rows < hq::kShrinkRows ? p.rows : hq::kShrinkRows;
+  const int most_adapters = p.adapters < most ? p.adapters : most;
   p.jobs = 1;
   while (p.jobs < 32 && tiles * p.slices * p.jobs * 2 <= 2 * sms) p.jobs *= 2;
+  if (p.jobs > most_adapters) p.jobs = most_adapters;
   // Stages no larger than the rows there are and the adapters a CTA can meet: beside a small CTA the
   // products' CTA fits on the SM and starts under it.
-  const int padded = (p.rank + 15) / 16 * 16, most = p.rows < hq::kShrinkRows ? p.rows : hq::kShrinkRows;
-  const int adapters = ((p.adapters < most ? p.adapters : most) + p.jobs - 1) / p.jobs;
+  const int padded = (p.rank + 15) / 16 * 16, adapters = (most_adapters + p.jobs - 1) / p.jobs;
   p.box_rows = (most + 7) / 8 * 8;
   p.cols = adapters * padded < hq::kShrinkCols ? adapters * padded : hq::kShrinkCols / padded * padded;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < p.cols) p.tmem_cols *= 2;
   const int stage = (p.box_rows + p.cols) * 128;
   p.stages = stage <= 8 * 1024 ? hq::kShrinkMaxStages : 3;
   // (the instruction reads 128 rows of x from a stage's start; the sums lie over the ring)

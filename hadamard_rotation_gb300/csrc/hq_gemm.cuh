@@ -124,7 +124,8 @@ struct GemmShape {
   static constexpr int kLoraWarp = 4 + 4 * (kWide ? kEpilogues : 2);  // the adapters' first warp
   static constexpr int kThreads = 32 * (kLoraWarp + (LORA ? 4 : 0));
   static constexpr int kRingBytes = 216 * 1024 - kChunks * kChunkBytes - kOuts;
-  static constexpr int kStages = kRingBytes / kStageBytes < 7 ? kRingBytes / kStageBytes : 7;
+  static constexpr int kMostStages = LORA && !kWide ? 4 : 7;  // (4: the CTA fits beside one of the thin product)
+  static constexpr int kStages = kRingBytes / kStageBytes < kMostStages ? kRingBytes / kStageBytes : kMostStages;
   static constexpr int kSmemBytes = kStages * kStageBytes + kChunks * kChunkBytes + kOuts;
   static_assert(kSmemBytes + 1024 + 16 * (LORA ? 2 : kGemmMaxGroups + 1) + 2048 <= 227 * 1024, "a CTA has 227 KB");
   // tensor memory columns: two accumulators, then two sets of scales (stage parity)
@@ -634,18 +635,7 @@ constexpr int kScaleThreads = 128;
 constexpr int kLoraThreads = 128;
 constexpr int kMaxSplits = 8;
 
-// A float of CTA `rank` of the cluster, at the address of a shared variable of this one.
-__device__ __forceinline__ float load_cluster(const float* p, uint32_t rank) {
-  float v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
-      "ld.shared::cluster.f32 %0, [a];\n\t}"
-      : "=f"(v)
-      : "r"(smem_addr(p)), "r"(rank)
-      : "memory");
-  return v;
-}
-
+// Four floats of CTA `rank` of the cluster, at the address of shared variables of this one.
 __device__ __forceinline__ float4 load_cluster4(const float* p, uint32_t rank) {
   float4 v;
   asm volatile(
@@ -1188,22 +1178,37 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
     if (again.get(t)) {
       float a = 1.0f;
       if (!MX) a = __fmul_rn(__ldg(p.sg_a + t.g), __ldg(p.sg_b));
-      const float* const sums = reinterpret_cast<const float*>(smem);
-      const int n = t.a0 + static_cast<int>(threadIdx.x & 127);
+      // Four lanes of a column per thread.
+      const float* const sums = reinterpret_cast<const float*>(smem) + (threadIdx.x & 31) * 4;
+      const int n = t.a0 + static_cast<int>(threadIdx.x & 31) * 4, es = p.out_f32 ? 4 : 2;
       if (n < p.na)
-        for (int c = part_k + splits * static_cast<int>(threadIdx.x >> 7); c < t.valid;
-             c += splits * static_cast<int>(blockDim.x >> 7)) {
-          float v[kMaxSplits];
+        for (int c = part_k + splits * static_cast<int>(threadIdx.x >> 5); c < t.valid;
+             c += splits * static_cast<int>(blockDim.x >> 5)) {
+          float4 v[kMaxSplits];
 #pragma unroll
           for (int k = 0; k < kMaxSplits; ++k)  // without a condition: all in flight before the first is added
-            v[k] = load_cluster(sums + c * kGemmLanes + (threadIdx.x & 127), min(k, splits - 1));
-          float sum = v[0];
+            v[k] = load_cluster4(sums + c * kGemmLanes, min(k, splits - 1));
+          float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-          for (int k = 1; k < kMaxSplits; ++k) sum += k < splits ? v[k] : 0.0f;
-          sum = __fmul_rn(sum, a);
-          const int64_t at = static_cast<int64_t>(t.b0 + c) * p.na + n;
-          if (p.out_f32) static_cast<float*>(p.out)[at] = sum;
-          else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(sum);
+          for (int k = 1; k < kMaxSplits; ++k) {
+            if (k >= splits) continue;
+            sum[0] += v[k].x, sum[1] += v[k].y, sum[2] += v[k].z, sum[3] += v[k].w;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sum[k] = __fmul_rn(sum[k], a);
+          uint8_t* const out = static_cast<uint8_t*>(p.out) + (static_cast<int64_t>(t.b0 + c) * p.na + n) * es;
+          const __nv_bfloat162 half[2] = {__floats2bfloat162_rn(sum[0], sum[1]), __floats2bfloat162_rn(sum[2], sum[3])};
+          if (p.out_vec >= 4 * es && n + 3 < p.na) {
+            if (p.out_f32) *reinterpret_cast<float4*>(out) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+            else *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(half);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (n + k >= p.na) continue;
+              if (p.out_f32) reinterpret_cast<float*>(out)[k] = sum[k];
+              else reinterpret_cast<__nv_bfloat16*>(out)[k] = reinterpret_cast<const __nv_bfloat16*>(half)[k];
+            }
+          }
         }
     }
     cluster_sync();  // the peers have read this CTA's sums
@@ -1273,6 +1278,7 @@ struct ShrinkParams {
   // rows of x in a stage (fewer than the 128 lanes where there are not so many: the others' columns are
   // not read), columns of a pass, stages
   int box_rows, cols, stages;
+  int tmem_cols;  // columns of tensor memory: no more than needed, or the SM's next CTAs wait for them
 };
 
 __global__ void __launch_bounds__(kShrinkThreads)
@@ -1294,7 +1300,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
 
   if (warp == 5) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
-                 "r"(kShrinkCols)
+                 "r"(p.tmem_cols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -1453,7 +1459,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
   __syncthreads();
   umma_fence_after();
   if (warp == 5)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kShrinkCols) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
 }
 
 }  // namespace hq
