@@ -50,6 +50,20 @@
 // Four slots make a chunk; a tile takes as many as its rows have distinct adapters, so a tile of
 // one request pays for one adapter and a tile of 64 requests for those that occur.  Chunks are
 // multiplied at fixed places of the main loop: the order of the sum does not depend on timing.
+//
+// What bounds it, measured.
+//   A few rows per expert: the weights' bytes.  64 experts of 4096 x 2048 (MXFP4), 512 rows: 35.7 us, 5.75 TB/s of
+//   what has to move, 0.85 of a copy.  One token at 8 experts of 2048 x 4096: 9.3 us, of which 5.6 are bytes and the
+//   rest a launch's start and the sum over the cluster.
+//   Large groups: what the L2 gives the SMs.  64 experts of 2048 x 4096 (NVFP4), 32768 rows: 129 us, 4.2 PFLOP/s,
+//   tensor pipe 51% busy, 2.4 GB through the L2 for 0.48 GB of DRAM traffic; a square-ish projection without groups
+//   ([4096, 4096] x [8192, 4096]) 56 us, 4.9 PFLOP/s.  Wider tiles would read less, but tensor memory holds two
+//   accumulators of 192 columns beside the scales, and with one the epilogue (a third of a tile's time) stood alone.
+//   Weight gradients: their output.  16 experts of 2048 x 4096 bf16 from 8192 tokens: 60 us for 0.30 GB, 0.73 of a
+//   copy; an expert's sum is 2 stages long, so a tile is mostly its 98 KB of output.
+//   Adapters: [4096, 4096] x [8192, 4096] with 8 adapters of rank 64 in runs of 200 rows: 86 us = 15 us of the thin
+//   product (bound by reading x at 3.9 TB/s from its first copy to its last, then by its clusters' barriers) and 65 us;
+//   32 rows of 24 adapters of rank 16 beside 4096 x 4096: 17 us, two kernels' latencies one after the other.
 #pragma once
 
 #include <cuda.h>
@@ -1255,8 +1269,8 @@ __device__ __forceinline__ uint4 scale_tile_row(const uint8_t* s, int64_t row0, 
 // read once for all of them, and a row keeps the columns of its own adapter.  More adapters than
 // fit take further passes; with few row tiles, several CTAs per slice share the adapters (`jobs`).  The
 // slices of a tile are a cluster, which adds their sums in distributed shared memory in a fixed order.
-// Bound by reading x and each distinct adapter of every tile once; two CTAs per SM keep 192 KB of
-// loads in flight.  Warps 0..3: the tile's lanes; warp 4: TMA; warp 5: the products.
+// Bound by reading x and each distinct adapter of every tile once ([4096, 4096], 8 adapters of rank 64: 15 us for
+// 38 MB; 32 rows of 24 adapters: 7 us, latencies); two CTAs per SM keep 192 KB of loads in flight.  Warps 0..3: the tile's lanes; warp 4: TMA; warp 5: the products.
 // ---------------------------------------------------------------------------
 constexpr int kShrinkThreads = 192;
 constexpr int kShrinkRows = 128;

@@ -24,10 +24,13 @@
 // bulk copies (cp.async.bulk).  A row's phases are spread over the steps of the loop -- forward: the sum
 // over y; h' and the sum over it; n -- so that a step works on three rows (backward: two) and has one
 // barrier, behind which the sums of all of them travel: with one row at a time a CTA waited for its
-// reductions half of the time (bf16 [16384, 8192] forward 313 us).  Rows of more columns than a CTA
+// reductions half of the time (bf16 [16384, 8192] forward 313 us; 178 now, 6.0 TB/s, 0.89 of a copy).  Rows of more columns than a CTA
 // holds are split over a cluster, whose warps write their sums into every CTA's shared memory;
 // narrow rows are taken several at a time.  Column sums end as one partial row per cluster, added in
-// a fixed order by k_norm_columns: no atomics, the same bits each time.
+// a fixed order by k_norm_columns: no atomics, the same bits each time.  Backward bf16 [8192, 8192] takes 156 us,
+// 5.2 TB/s, 0.76 of a copy: 16 warps of 124 registers fill the register file and leave the schedulers idle
+// half of the time, on shared memory and barriers.  fp32 [1021, 1360] takes 19 us for 33 MB: five steps of about
+// 3 us, a launch's start and the column sums' second kernel (4 us).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -151,7 +154,7 @@ __device__ __forceinline__ void param_unit(const void* w, int64_t col, int bf16,
 
 // The row sums of four steps.  In a cluster every warp sends its sums to every CTA by asynchronous stores that
 // count on the step's mbarrier there: no barrier of the cluster, whose release would also wait for the output
-// rows' stores (bf16 [700, 28672] forward 99 us with one per step).  Four steps' slots are enough: a warp sends
+// rows' stores (bf16 [2000, 12288] forward 67 -> 51 us, 3.9 TB/s).  Four steps' slots are enough: a warp sends
 // for step j after it has all sums of step j - 2, every warp sent those after it had read the sums of step j - 4.
 constexpr int kNormSlots = 4;
 
