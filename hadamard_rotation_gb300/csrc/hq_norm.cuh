@@ -198,40 +198,45 @@ __device__ __forceinline__ bool wait_sums(const NormShared& sh, int step) {
   }
 }
 
-// This warp's sums of NS values, as sums `first` .. of a step, for every CTA of the cluster.
+// This warp's sums of two or three values, for every CTA of the cluster.  The lanes halve the values among them
+// while they halve each other: 5 or 6 shuffles, where a value at a time takes 5 each (they are a third of the
+// instructions that the step waits for); sum q ends in lanes 8 q .. 8 q + 7.
 template <int NS>
-__device__ __forceinline__ void put_sums(NormShared& sh, int step, int first, uint32_t ranks, uint32_t rank,
-                                         float (&s)[NS]) {
+__device__ __forceinline__ void put_sums(NormShared& sh, int step, uint32_t ranks, uint32_t rank, const float (&s)[NS]) {
+  static_assert(NS == 2 || NS == 3, "halved twice");
+  const int lane = threadIdx.x & 31;
+  const bool hi = lane & 16, odd = lane & 8;
+  float a = hi ? (NS == 3 ? s[2] : 0.0f) : s[0], b = hi ? 0.0f : s[1];
+  a += __shfl_xor_sync(0xFFFFFFFFu, hi ? s[0] : (NS == 3 ? s[2] : 0.0f), 16);
+  b += __shfl_xor_sync(0xFFFFFFFFu, hi ? s[1] : 0.0f, 16);
+  float v = odd ? b : a;
+  v += __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 8);
 #pragma unroll
-  for (int i = 0; i < NS; ++i)
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], m);
-  const int lane = threadIdx.x & 31, at = static_cast<int>(rank) * 16 + (threadIdx.x >> 5);
-  const int slot = step & (kNormSlots - 1);
+  for (int m = 4; m >= 1; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+  const int q = lane >> 3, at = static_cast<int>(rank) * 16 + (threadIdx.x >> 5), slot = step & (kNormSlots - 1);
+  if (q >= NS) return;
   if (ranks == 1) {
-    if (lane == 0)
-#pragma unroll
-      for (int i = 0; i < NS; ++i) sh.part[slot][first + i][at] = s[i];
-  } else if (lane < static_cast<int>(ranks)) {
-#pragma unroll
-    for (int i = 0; i < NS; ++i) send_cluster(&sh.part[slot][first + i][at], &sh.sums[slot], lane, s[i]);
+    if ((lane & 7) == 0) sh.part[slot][q][at] = v;
+  } else if ((lane & 7) < static_cast<int>(ranks)) {
+    send_cluster(&sh.part[slot][q][at], &sh.sums[slot], lane & 7, v);
   }
 }
 
-// The sums of a row of an earlier step, over its warps and the cluster, in a fixed order.
+// The sums of a row of an earlier step, over its warps and the cluster, in a fixed order: eight lanes add one.
 template <int NS>
-__device__ __forceinline__ void get_sums(const NormShared& sh, int step, int first, int warps, int row, uint32_t ranks,
+__device__ __forceinline__ void get_sums(const NormShared& sh, int step, int warps, int row, uint32_t ranks,
                                          float (&s)[NS]) {
-  const int lane = threadIdx.x & 31, slot = step & (kNormSlots - 1);
-#pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    s[i] = 0.0f;
-    if (lane < warps)
-      for (uint32_t r = 0; r < ranks; ++r) s[i] += sh.part[slot][first + i][r * 16 + row * warps + lane];
-#pragma unroll
-    for (int m = 8; m >= 1; m >>= 1) s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], m);
-    s[i] = __shfl_sync(0xFFFFFFFFu, s[i], 0);
+  const int lane = threadIdx.x & 31, q = lane >> 3, j = lane & 7;
+  const float* const part = sh.part[step & (kNormSlots - 1)][q < NS ? q : 0] + row * warps;
+  float v = 0.0f;
+  for (uint32_t r = 0; r < ranks; ++r) {
+    if (j < warps) v += part[r * 16 + j];
+    if (j + 8 < warps) v += part[r * 16 + j + 8];
   }
+#pragma unroll
+  for (int m = 4; m >= 1; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+#pragma unroll
+  for (int i = 0; i < NS; ++i) s[i] = __shfl_sync(0xFFFFFFFFu, v, 8 * i);
 }
 
 // max |x . H_G / sqrt(G)| over one unit per lane (G = 16: two lanes; G = 256: the warp), in the
@@ -387,7 +392,11 @@ __device__ __forceinline__ void expect_sums(const NormShared& sh, int step, int 
         ring.wait(i % p.stages, (i / p.stages) & 1);                                                  \
     if ((threadIdx.x & 31) == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);                            \
   }                                                                                                   \
-  if (ranks > 1) cluster_sync() /* no CTA leaves before its peers' sums have arrived */
+  if (ranks > 1) {                                                                                    \
+    cluster_sync();                                                                                   \
+    if (!ok) __nanosleep(1000000); /* sums that were not waited for land in this CTA's memory */      \
+  }                                                                                                   \
+  static_assert(true, "")
 
 // PLAIN: both norms, y, no gate or one per channel, no amax -- known to the compiler, which then has no
 // branch in the loop (bf16 [16384, 8192] forward 235 us without).
@@ -407,10 +416,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
   // Step i: the sum over y of its i-th row; h' of row i - 1; n of row i - 2.
   for (int i = 0; i < ring.steps + 2; ++i) {
     const int64_t m1 = m0 - stride, m2 = m1 - stride;
-    expect_sums(sh, i, (post && i < ring.steps) + (pre && i >= 1 && i <= ring.steps), ranks, ok);
+    if (i <= ring.steps) expect_sums(sh, i, 2, ranks, ok);
     const bool live1 = i >= 1 && i <= ring.steps && m1 < p.M, live2 = i >= 2 && m2 < p.M;
     float gate = 1.0f;
     if (by_token && live1) gate = norm_param(p.gate, m1, p.params_bf16);
+    float put[2] = {0.0f, 0.0f};  // the sum over y of this step's row; over h' of the one before
     if (i < ring.steps) {
       ok = ok && ring.wait(s0, phase);
       if (post) {
@@ -427,15 +437,16 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
 #pragma unroll
               for (int e = 0; e < 4; ++e) sq = fma2(y[e], y[e], sq);
             }
-        float ss[1] = {sq.x + sq.y};
-        put_sums<1>(sh, i, 0, ranks, rank, ss);
+        put[0] = sq.x + sq.y;
       }
     }
-    if (ranks > 1 && i >= 1) ok = ok && wait_sums(sh, i - 1);
+    float got[2] = {0.0f, 0.0f};  // of the step before
+    if (i >= 1) {
+      if (ranks > 1) ok = ok && wait_sums(sh, i - 1);
+      get_sums<2>(sh, i - 1, warps, row, ranks, got);
+    }
     if (pre && i >= 2) {  // n of row i - 2, from t
-      float ss[1];
-      get_sums<1>(sh, i - 1, 1, warps, row, ranks, ss);
-      const float r_pre = rsqrtf(fmaf(ss[0], inv_d, p.eps));
+      const float r_pre = rsqrtf(fmaf(got[1], inv_d, p.eps));
       if (live2 && lane_u == 0 && rank == 0) p.r_pre[m2] = r_pre;
       uint8_t* const dst = static_cast<uint8_t*>(p.n) + (at1 - row_step);
 #pragma unroll
@@ -453,10 +464,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
       }
     }
     if (i >= 1 && i <= ring.steps) {  // h' of row i - 1
-      float r_post = 1.0f, ss[1];
+      float r_post = 1.0f;
       if (post) {
-        get_sums<1>(sh, i - 1, 0, warps, row, ranks, ss);
-        r_post = rsqrtf(fmaf(ss[0], inv_d, p.eps));
+        r_post = rsqrtf(fmaf(got[0], inv_d, p.eps));
         if (live1 && lane_u == 0 && rank == 0) p.r_post[m1] = r_post;
       }
       r_post *= gate;
@@ -492,9 +502,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
 #pragma unroll
         for (int e = 0; e < 4; ++e) sq = fma2(t[j][e], t[j][e], sq);
       }
-      ss[0] = sq.x + sq.y;
-      if (pre) put_sums<1>(sh, i, 1, ranks, rank, ss);
+      put[1] = sq.x + sq.y;
     }
+    if (i <= ring.steps) put_sums<2>(sh, i, ranks, rank, put);  // (every sum that is sent is waited for)
     __syncthreads();  // one CTA's sums put before it can be got after it; and the stage is free
     if (fetches && i >= 1) {  // row i - 1 has left its stage
       fence_proxy_async_smem();
@@ -543,7 +553,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
   // Step i: the sums of its i-th row; the gradients of row i - 1.
   for (int i = 0; i < ring.steps + 1; ++i) {
     const int64_t m1 = m0 - stride;
-    expect_sums(sh, i, i < ring.steps ? 3 : 0, ranks, ok);
+    if (i < ring.steps) expect_sums(sh, i, 3, ranks, ok);
     before = now;
     now = next;
     next = scalars(i + 1, m0 + stride);
@@ -590,12 +600,12 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
           }
         }
       float s[3] = {c[0].x + c[0].y, c[1].x + c[1].y, c[2].x + c[2].y};
-      put_sums<3>(sh, i, 0, ranks, rank, s);
+      put_sums<3>(sh, i, ranks, rank, s);
     }
     if (i >= 1) {
       if (ranks > 1) ok = ok && wait_sums(sh, i - 1);
       float s[3];
-      get_sums<3>(sh, i - 1, 0, warps, row, ranks, s);
+      get_sums<3>(sh, i - 1, warps, row, ranks, s);
       const float r_pre = before.r_pre, r_post = before.r_post, tok = before.tok;
       const float k1 = r_pre * r_pre * r_pre * (s[0] * inv_d);
       const float dot = fmaf(-k1, s[2], s[1]);  // sum d q (a per-token gate left out)
@@ -665,6 +675,21 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
     if (s0 == 0) phase ^= 1;
   }
   HQ_NORM_FINISH();
+  if (p.rows == 1) {  // as they are
+    float* const to = p.partial + cluster * p.D + col0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if (!in[j]) continue;
+      float4* const w4 = reinterpret_cast<float4*>(to + (j * p.tpr + lane_u) * 8);
+      float4* const a4 = reinterpret_cast<float4*>(to + clusters * p.D + (j * p.tpr + lane_u) * 8);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        w4[k] = make_float4(sum_w[j][2 * k].x, sum_w[j][2 * k].y, sum_w[j][2 * k + 1].x, sum_w[j][2 * k + 1].y);
+        a4[k] = make_float4(sum_a[j][2 * k].x, sum_a[j][2 * k].y, sum_a[j][2 * k + 1].x, sum_a[j][2 * k + 1].y);
+      }
+    }
+    return;
+  }
   // The step's rows leave their column sums side by side over the ring, which is free now (8 bytes per
   // row and column, of at least 24), and are added in their order.
   float* const s_sum = reinterpret_cast<float*>(ring.base);

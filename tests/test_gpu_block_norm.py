@@ -67,7 +67,7 @@ def close(got, want, size, name):
 
 
 SHAPES = [(1, 16), (1, 4096), (3, 48), (37, 416), (5, 8192), (2, 8208), (3, 16384), (2, 32768), (700, 256), (301, 1360), (640, 4096), (1500, 2064),
-          (650, 8192)]
+          (650, 8192), (1500, 8208), (700, 16400)]
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
