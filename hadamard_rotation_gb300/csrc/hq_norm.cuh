@@ -24,13 +24,13 @@
 // bulk copies (cp.async.bulk).  A row's phases are spread over the steps of the loop -- forward: the sum
 // over y; h' and the sum over it; n -- so that a step works on three rows (backward: two) and has one
 // barrier, behind which the sums of all of them travel: with one row at a time a CTA waited for its
-// reductions half of the time (bf16 [16384, 8192] forward 313 us; 178 now, 6.0 TB/s, 0.89 of a copy).  Rows of more columns than a CTA
+// reductions half of the time (bf16 [16384, 8192] forward 313 us; 169 now, 6.4 TB/s, 0.94 of a copy).  Rows of more columns than a CTA
 // holds are split over a cluster, whose warps write their sums into every CTA's shared memory;
 // narrow rows are taken several at a time.  Column sums end as one partial row per cluster, added in
-// a fixed order by k_norm_columns: no atomics, the same bits each time.  Backward bf16 [8192, 8192] takes 156 us,
-// 5.2 TB/s, 0.76 of a copy: 16 warps of 124 registers fill the register file and leave the schedulers idle
-// half of the time, on shared memory and barriers.  fp32 [1021, 1360] takes 19 us for 33 MB: five steps of about
-// 3 us, a launch's start and the column sums' second kernel (4 us).
+// a fixed order by k_norm_columns: no atomics, the same bits each time.  Backward bf16 [8192, 8192] takes 138 us,
+// 5.8 TB/s, 0.86 of a copy: 16 warps of 128 registers fill the register file, and with no more of them what a step
+// costs beside its bytes is not all hidden.  fp32 [1021, 1360] takes 18 us for 33 MB: its first rows arrive 4 us
+// after the start, five steps take 2 us each, and the column sums have a second kernel.
 #pragma once
 
 #include <cuda_bf16.h>
