@@ -89,7 +89,27 @@ struct Unit {
 #pragma unroll
     for (int i = 0; i < (BF16 ? 1 : 2); ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
   }
+  // From a row in shared memory, where neighbouring lanes read neighbouring units.  fp32: half of the lanes read
+  // the second 16 bytes first, or lanes 4 apart would meet in the same banks.
+  __device__ __forceinline__ void load_row(const uint8_t* p) {
+    if constexpr (BF16) {
+      load(p);
+    } else {
+      const bool second = threadIdx.x & 4;
+      const uint4 a = reinterpret_cast<const uint4*>(p)[second], b = reinterpret_cast<const uint4*>(p)[!second];
+      w[0] = second ? b : a;
+      w[1] = second ? a : b;
+    }
+  }
   __device__ __forceinline__ void store(uint8_t* p) const {
+    if constexpr (!BF16) {
+      if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {  // whole sectors
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0].x), "r"(w[0].y),
+                     "r"(w[0].z), "r"(w[0].w), "r"(w[1].x), "r"(w[1].y), "r"(w[1].z), "r"(w[1].w)
+                     : "memory");
+        return;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < (BF16 ? 1 : 2); ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
   }
@@ -432,7 +452,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
             if (in[j]) {
               Unit<BF16> yu;
               float2 y[4];
-              yu.load(src + j * unit);
+              yu.load_row(src + j * unit);
               yu.get(y);
 #pragma unroll
               for (int e = 0; e < 4; ++e) sq = fma2(y[e], y[e], sq);
@@ -481,11 +501,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
           continue;
         }
         Unit<BF16> x;
-        x.load(src + j * unit);
+        x.load_row(src + j * unit);
         x.get(t[j]);
         if (has_y) {
           float2 y[4], g[4];
-          x.load(src + tensor + j * unit);
+          x.load_row(src + tensor + j * unit);
           x.get(y);
           if (full) {
             x.load(static_cast<const uint8_t*>(p.gate) + m1 * p.ld_gate + (col0 + lane_u * 8) * kEs + j * unit);
@@ -568,9 +588,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
           Unit<BF16> x;
           float2 h[4], n[4];
           x.zero();
-          if (pre) x.load(src + j * unit);
+          if (pre) x.load_row(src + j * unit);
           x.get(h);
-          if (pre) x.load(src + tensor + j * unit);
+          if (pre) x.load_row(src + tensor + j * unit);
           x.get(n);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -581,9 +601,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
           if (!has_y) continue;
           float2 d[4], y[4];
           x.zero();
-          if (PLAIN || p.in[2]) x.load(src + 2 * tensor + j * unit);
+          if (PLAIN || p.in[2]) x.load_row(src + 2 * tensor + j * unit);
           x.get(d);
-          x.load(src + 3 * tensor + j * unit);
+          x.load_row(src + 3 * tensor + j * unit);
           x.get(y);
           if (full) {
             float2 g[4];
@@ -620,14 +640,14 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
           Unit<BF16> x;
           float2 d[4], v[4], o[4];
           x.zero();
-          if (PLAIN || p.in[2]) x.load(src + 2 * tensor + j * unit);
+          if (PLAIN || p.in[2]) x.load_row(src + 2 * tensor + j * unit);
           x.get(d);
           if (pre) {
-            x.load(src + tensor + j * unit);
+            x.load_row(src + tensor + j * unit);
             x.get(v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) d[e] = fma2(both(r_pre), mul2(v[e], w_pre[j][e]), d[e]);
-            x.load(src + j * unit);
+            x.load_row(src + j * unit);
             x.get(v);
 #pragma unroll
             for (int e = 0; e < 4; ++e) d[e] = fma2(v[e], both(-k1), d[e]);
@@ -637,7 +657,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
           x.set(o);
           x.store(static_cast<uint8_t*>(p.dh) + at1 + j * unit);
           if (!has_y) continue;
-          x.load(src + 3 * tensor + j * unit);
+          x.load_row(src + 3 * tensor + j * unit);
           x.get(v);
           if (full) {
             float2 g[4];
