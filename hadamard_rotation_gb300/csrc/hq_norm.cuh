@@ -29,8 +29,8 @@
 // narrow rows are taken several at a time.  Column sums end as one partial row per cluster, added in
 // a fixed order by k_norm_columns: no atomics, the same bits each time.  Backward bf16 [8192, 8192] takes 138 us,
 // 5.8 TB/s, 0.86 of a copy: 16 warps of 128 registers fill the register file, and with no more of them what a step
-// costs beside its bytes is not all hidden.  fp32 [1021, 1360] takes 18 us for 33 MB: its first rows arrive 4 us
-// after the start, five steps take 2 us each, and the column sums have a second kernel.
+// costs beside its bytes is not all hidden.  fp32 [1021, 1360] takes 16.6 us for 33 MB: its first rows arrive 4 us
+// after the start, five steps take some 1.8 us each, and the column sums have a second kernel.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -722,12 +722,15 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
     for (int e = 0; e < 4; ++e) at[e] = sum_w[j][e], at[p.cols / 2 + e] = sum_a[j][e];
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < 2 * p.cols; c += blockDim.x) {
+  for (int c = threadIdx.x * 4; c < 2 * p.cols; c += blockDim.x * 4) {
     const int second = c >= p.cols, col = c - second * p.cols;
     if (col >= my_cols) continue;
-    float v = s_sum[c];
-    for (int r = 1; r < p.rows; ++r) v += s_sum[r * 2 * p.cols + c];
-    p.partial[(second * clusters + cluster) * p.D + col0 + col] = v;
+    float4 v = *reinterpret_cast<const float4*>(s_sum + c);
+    for (int r = 1; r < p.rows; ++r) {
+      const float4 o = *reinterpret_cast<const float4*>(s_sum + r * 2 * p.cols + c);
+      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    }
+    *reinterpret_cast<float4*>(p.partial + (second * clusters + cluster) * p.D + col0 + col) = v;
   }
 }
 
