@@ -378,8 +378,9 @@ hq_status launch_shrink(hq::ShrinkParams p, const void* x, int64_t ldx, const vo
   const int padded = (p.rank + 15) / 16 * 16, adapters = (most_adapters + p.jobs - 1) / p.jobs;
   p.box_rows = (most + 7) / 8 * 8;
   p.cols = adapters * padded < hq::kShrinkCols ? adapters * padded : hq::kShrinkCols / padded * padded;
+  const int columns = p.cols + (adapters * padded > p.cols ? padded : 0);
   p.tmem_cols = 32;
-  while (p.tmem_cols < p.cols) p.tmem_cols *= 2;
+  while (p.tmem_cols < columns) p.tmem_cols *= 2;
   const int stage = (p.box_rows + p.cols) * 128;
   p.stages = stage <= 8 * 1024 ? hq::kShrinkMaxStages : 3;
   // (the instruction reads 128 rows of x from a stage's start; the sums lie over the ring)

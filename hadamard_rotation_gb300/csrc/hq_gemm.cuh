@@ -145,6 +145,8 @@ struct GemmShape {
   static constexpr int kStages = kRingBytes / kStageBytes < kMostStages ? kRingBytes / kStageBytes : kMostStages;
   static constexpr int kSmemBytes = kStages * kStageBytes + kChunks * kChunkBytes + kOuts;
   static_assert(kSmemBytes + 1024 + 16 * (LORA ? 2 : kGemmMaxGroups + 1) + 2048 <= 227 * 1024, "a CTA has 227 KB");
+  // (its columns of tensor memory are held while it waits for the CTAs of its cluster)
+  static_assert(2 * kSmemBytes > 228 * 1024, "no two CTAs of these kernels share an SM");
   // tensor memory columns: two accumulators, then two sets of scales (stage parity)
   static constexpr int kColsSfa = kTilesPerBlock * 4;
   static constexpr int kColsSfb = kTilesPerBlock * kRowTilesB * 4;
@@ -335,6 +337,15 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&v)[16]) {
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
         "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
       : "r"(taddr)
+      : "memory");
+}
+// Registers into columns of the thread's lane; complete when the statement is.
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 // A warp's 32 lanes x 32 columns in the shape of matrix fragments: v[h] is lanes 16 h .. 16 h + 15.
@@ -701,6 +712,9 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
                    : "memory");
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    // Only now, and by this warp: the kernel after this one takes tensor memory too before it waits for this
+    // one, and must not find it free before this CTA has its own.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   }
   if (warp == 1 && lane == 0) {
     for (int i = 0; i < S::kStages; ++i) {
@@ -716,7 +730,6 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
     mbar_init(smem_addr(&bars.drain), 1);
     fence_mbar_init();
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // The kernel before this one on the stream wrote the operands.  (Where it is the adapters' first product,
   // which lets this kernel start once it has itself waited for what was before it: only lora_t, and only the
   // adapters' warps wait for it.)
@@ -1272,6 +1285,11 @@ __device__ __forceinline__ uint4 scale_tile_row(const uint8_t* s, int64_t row0, 
 // read once for all of them, and a row keeps the columns of its own adapter.  More adapters than
 // fit take further passes; with few row tiles, several CTAs per slice share the adapters (`jobs`).  The
 // slices of a tile are a cluster, which adds their sums in distributed shared memory in a fixed order.
+//
+// Tensor memory is taken after the wait for the kernel before and freed before the cluster's barriers: CTAs of
+// several launches share an SM's 512 columns in whatever order they come, and one that held columns while it waited
+// for a peer, which waits for columns elsewhere, could wait for ever.  So the sums of several passes, a row's own
+// columns of each, are gathered beside the accumulator (`own`) until the last pass is done, and exchanged once.
 // Bound by reading x and each distinct adapter of every tile once ([4096, 4096], 8 adapters of rank 64: 15 us for
 // 38 MB; 32 rows of 24 adapters: 7 us, latencies); two CTAs per SM keep 192 KB of loads in flight.  Warps 0..3: the tile's lanes; warp 4: TMA; warp 5: the products.
 // ---------------------------------------------------------------------------
@@ -1295,7 +1313,9 @@ struct ShrinkParams {
   // rows of x in a stage (fewer than the 128 lanes where there are not so many: the others' columns are
   // not read), columns of a pass, stages
   int box_rows, cols, stages;
-  int tmem_cols;  // columns of tensor memory: no more than needed, or the SM's next CTAs wait for them
+  // columns of tensor memory: those of a pass and, where there may be several, of a row's sums behind them; no more
+  // than needed, or the SM's next CTAs wait for them
+  int tmem_cols;
 };
 
 __global__ void __launch_bounds__(kShrinkThreads)
@@ -1315,12 +1335,6 @@ __global__ void __launch_bounds__(kShrinkThreads)
   const int row0 = blockIdx.x / p.slices / p.jobs * kShrinkRows;
   const int padded = (p.rank + 15) & ~15;
 
-  if (warp == 5) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
-                 "r"(p.tmem_cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
   if (threadIdx.x == 128) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(smem_addr(&sh.full[i]), 1);
@@ -1330,8 +1344,15 @@ __global__ void __launch_bounds__(kShrinkThreads)
     fence_mbar_init();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // (after the wait: the products may start under this kernel and read what it waited for)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
+                 "r"(p.tmem_cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    // After the wait, since the products may start under this kernel and read what it waited for; and with the
+    // columns in hand, since the products take theirs when they start.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
   if (warp == 0) {  // the distinct adapters; every jobs-th of them is this CTA's
     int ids[kShrinkRows / 32], n = 0;
 #pragma unroll
@@ -1371,6 +1392,13 @@ __global__ void __launch_bounds__(kShrinkThreads)
   // is read from other CTAs along its ranks (32 rows at once are 32 requests each: 20 us for 4096 rows).
   float* const sums = reinterpret_cast<float*>(ring);
   const int pitch = padded + kShrinkPad;
+  const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);  // (warps 0..3)
+  auto put_sums = [&](int r, const uint32_t (&v)[16]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<uint4*>(sums + (warp * 32 + lane) * pitch + r + 4 * k) =
+          kb1 > kb0 ? make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]) : make_uint4(0, 0, 0, 0);
+  };
   GemmRing at;
   const uint64_t ring0 = desc_codes(smem_addr(ring));
   long long fills = 0;
@@ -1421,62 +1449,75 @@ __global__ void __launch_bounds__(kShrinkThreads)
     umma_fence_after();
     __syncthreads();
     if (warp < 4) {  // each row's own columns
-      const int row = warp * 32 + lane, mine = sh.slot[row] - pass * per_pass;
+      const int mine = sh.slot[warp * 32 + lane] - pass * per_pass;
       for (int i = 0; i < slots; ++i) {
         if (!__any_sync(0xFFFFFFFFu, mine == i)) continue;
         for (int r = 0; r < padded; r += 16) {
           uint32_t v[16];
-          tmem_load(tmem + (static_cast<uint32_t>(warp * 32) << 16) + i * padded + r, v);
-          if (mine == i)
+          tmem_load(lanes + i * padded + r, v);
+          if (passes == 1) {
+            if (mine == i) put_sums(r, v);
+          } else {
+            uint32_t own[16];
+            tmem_load(lanes + p.cols + r, own);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(sums + row * pitch + r + 4 * k) =
-                  kb1 > kb0 ? make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]) : make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < 16; ++k) own[k] = mine == i ? v[k] : own[k];
+            tmem_store(lanes + p.cols + r, own);
+          }
         }
       }
-      umma_fence_before();
     }
-    cluster_sync();
-    // Each CTA of the cluster finishes every slices-th row, 4 ranks per thread.
-    const int quads = p.rank / 4, items = kShrinkRows / p.slices * quads;
-    for (int item = threadIdx.x; item < items; item += kShrinkThreads) {
-      const int row = slice + item / quads * p.slices, r = item % quads * 4;
-      const int slot = sh.slot[row], mine = slot - pass * per_pass;
-      if (slot < 0 || mine < 0 || mine >= slots) continue;
-      const float scale = __ldg(p.scaling + sh.adapter[job + slot * p.jobs]) * inv;
-      float4 part[kMaxSplits];
-#pragma unroll
-      for (int k = 0; k < kMaxSplits; ++k)  // without a condition: all in flight before the first is added
-        part[k] = load_cluster4(sums + row * pitch + r, min(k, p.slices - 1));
-      float v[4] = {part[0].x, part[0].y, part[0].z, part[0].w};
-#pragma unroll
-      for (int k = 1; k < kMaxSplits; ++k) {
-        if (k >= p.slices) continue;
-        v[0] += part[k].x, v[1] += part[k].y, v[2] += part[k].z, v[3] += part[k].w;
-      }
-      __nv_bfloat162 hi[2], lo[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float x = v[2 * k] * scale, y = v[2 * k + 1] * scale;
-        hi[k] = __floats2bfloat162_rn(x, y);
-        lo[k] = __floats2bfloat162_rn(x - __low2float(hi[k]), y - __high2float(hi[k]));
-      }
-      __nv_bfloat16* const t = p.t + static_cast<int64_t>(row0 + row) * 2 * p.rank + r;
-      *reinterpret_cast<uint2*>(t) = *reinterpret_cast<const uint2*>(hi);
-      *reinterpret_cast<uint2*>(t + p.rank) = *reinterpret_cast<const uint2*>(lo);
+    umma_fence_before();
+    __syncthreads();  // the accumulator has been read
+    umma_fence_after();
+  }
+  if (passes > 1 && warp < 4) {
+    for (int r = 0; r < padded; r += 16) {
+      uint32_t v[16];
+      tmem_load(lanes + p.cols + r, v);
+      if (sh.slot[warp * 32 + lane] >= 0) put_sums(r, v);
     }
-    fence_proxy_async_smem();  // the next pass's copies overwrite the sums
-    cluster_sync();
+    umma_fence_before();
+  }
+  if (passes > 1) __syncthreads();
+  umma_fence_after();
+  if (warp == 5)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
+  __syncwarp();
+  cluster_sync();
+  // Each CTA of the cluster finishes every slices-th row, 4 ranks per thread.
+  const int quads = p.rank / 4, items = kShrinkRows / p.slices * quads;
+  for (int item = threadIdx.x; item < items; item += kShrinkThreads) {
+    const int row = slice + item / quads * p.slices, r = item % quads * 4, slot = sh.slot[row];
+    if (slot < 0) continue;
+    const float scale = __ldg(p.scaling + sh.adapter[job + slot * p.jobs]) * inv;
+    float4 part[kMaxSplits];
+#pragma unroll
+    for (int k = 0; k < kMaxSplits; ++k)  // without a condition: all in flight before the first is added
+      part[k] = load_cluster4(sums + row * pitch + r, min(k, p.slices - 1));
+    float v[4] = {part[0].x, part[0].y, part[0].z, part[0].w};
+#pragma unroll
+    for (int k = 1; k < kMaxSplits; ++k) {
+      if (k >= p.slices) continue;
+      v[0] += part[k].x, v[1] += part[k].y, v[2] += part[k].z, v[3] += part[k].w;
+    }
+    __nv_bfloat162 hi[2], lo[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float x = v[2 * k] * scale, y = v[2 * k + 1] * scale;
+      hi[k] = __floats2bfloat162_rn(x, y);
+      lo[k] = __floats2bfloat162_rn(x - __low2float(hi[k]), y - __high2float(hi[k]));
+    }
+    __nv_bfloat16* const t = p.t + static_cast<int64_t>(row0 + row) * 2 * p.rank + r;
+    *reinterpret_cast<uint2*>(t) = *reinterpret_cast<const uint2*>(hi);
+    *reinterpret_cast<uint2*>(t + p.rank) = *reinterpret_cast<const uint2*>(lo);
   }
   if (!ok && warp == 4)  // let the copies in flight land (bounded)
     for (long long f = fills > p.stages ? fills - p.stages : 0; f < fills; ++f)
       mbar_wait(smem_addr(&sh.full[f % p.stages]), (f / p.stages) & 1);
   if (!ok && lane == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);
-  umma_fence_before();
-  __syncthreads();
-  umma_fence_after();
-  if (warp == 5)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
+  __syncwarp();
+  cluster_sync();  // the peers have read this CTA's sums
 }
 
 }  // namespace hq
