@@ -50,6 +50,9 @@
 // Four slots make a chunk; a tile takes as many as its rows have distinct adapters, so a tile of
 // one request pays for one adapter and a tile of 64 requests for those that occur.  Chunks are
 // multiplied at fixed places of the main loop: the order of the sum does not depend on timing.
+// A zero times an infinity is not zero, so an infinity or NaN in B_a goes into the product as 0, or it would reach the
+// rows of other adapters.  What it gives the rows of its own is added to the output at the end (add_special), a walk over
+// the rows and lanes that only a call with such a value pays for.
 //
 // What bounds it, measured.
 //   A few rows per expert: the weights' bytes.  64 experts of 4096 x 2048 (MXFP4), 512 rows: 35.7 us, 5.75 TB/s of
@@ -164,6 +167,7 @@ struct GemmBars {
   int chunk_steps[2], chunk_last[2];  // 16-column steps of a chunk; whether the tile ends with it
   int32_t ids[192], distinct[192];     // a tile's adapters by row, and each once
   int n_distinct;
+  int special;  // an infinity or NaN of the adapters' B was left out of a product
   uint32_t tmem;
   int tiles;
 };
@@ -675,6 +679,60 @@ __device__ __forceinline__ float4 load_cluster4(const float* p, uint32_t rank) {
   return v;
 }
 
+// A pair of bf16, each half made 0 if it is infinite or NaN.
+__device__ __forceinline__ uint32_t without_special(uint32_t w) {
+  return w & ~((((w & 0x7F807F80u) + 0x00800080u) >> 15 & 0x00010001u) * 0xFFFFu);
+}
+// zero * w + sum: NaN once there was an infinity or NaN.
+__device__ __forceinline__ __nv_bfloat162 add_zeros(uint32_t w, __nv_bfloat162 sum) {
+  return __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w), __floats2bfloat162_rn(0.0f, 0.0f), sum);
+}
+
+// What the infinities and NaN of adapter id's B add to output channel n of row m (before the multiplication by a): the
+// sum of t B over them, infinite or NaN; 0 where there are none.  Of the ranks whose slots are this CTA's: slot0 is
+// the adapter's first.
+__device__ __forceinline__ float special_sum(const GemmParams& p, int id, int64_t m, int n, int slot0, int splits,
+                                             int part) {
+  const __nv_bfloat16* const b =
+      reinterpret_cast<const __nv_bfloat16*>(p.lora_b) + (static_cast<int64_t>(id) * p.na + n) * p.rank;
+  const __nv_bfloat16* const t = reinterpret_cast<const __nv_bfloat16*>(p.lora_t) + m * 2 * p.rank;
+  float sum = 0.0f;
+  for (int r = 0; r < p.rank; ++r) {
+    const float v = __bfloat162float(b[r]);
+    if (isfinite(v) || (slot0 + r / 16) / 4 % splits != part) continue;
+    // t = hi + lo has hi's sign, and is zero, infinite or NaN where hi is
+    sum += __uint_as_float(static_cast<uint32_t>(__ldcg(reinterpret_cast<const uint16_t*>(t + r))) << 16) * v;
+  }
+  return sum;
+}
+
+// What the chunks of this CTA left out, added to the rows and lanes of its tiles, whose stores (the cluster's) are
+// complete.  Infinities and NaN: the order in which CTAs of a cluster add theirs does not matter.
+template <bool MX, int T>
+__device__ __forceinline__ void add_special(const GemmParams& p, const GemmBars& bars, GemmTiles<kGemmRows, T> order, int rank,
+                                            int splits, int part) {
+  float a = 1.0f;
+  if (!MX) a = __fmul_rn(__ldg(p.sg_a), __ldg(p.sg_b));
+  GemmTile t;
+  while (order.get(t)) {
+    const int n = t.a0 + rank * kGemmLanes + static_cast<int>(threadIdx.x % kGemmLanes);
+    if (n < p.na)
+      for (int c = threadIdx.x / kGemmLanes; c < t.valid; c += blockDim.x / kGemmLanes) {
+        const int64_t m = t.b0 + c;
+        const int id = __ldg(p.lora_ids + m);
+        if (id < 0 || id >= p.adapters) continue;
+        int at = 0;  // (one part: it has every slot)
+        if (splits > 1)
+          while (at + 1 < bars.n_distinct && bars.distinct[at] != id) ++at;
+        const float add = special_sum(p, id, m, n, at * ((p.rank + 15) / 16), splits, part);
+        if (add == 0.0f) continue;
+        if (p.out_f32) atomicAdd(static_cast<float*>(p.out) + m * p.na + n, add * a);
+        else atomicAdd(static_cast<__nv_bfloat16*>(p.out) + m * p.na + n, __float2bfloat16_rn(add * a));
+      }
+    __syncwarp();
+  }
+}
+
 template <int KIND, bool MX, int T, bool LORA, bool SPLIT>
 __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
     k_fp4_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -728,6 +786,7 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
       mbar_init(smem_addr(&bars.chunk_empty[i]), 1);
     }
     mbar_init(smem_addr(&bars.drain), 1);
+    bars.special = 0;
     fence_mbar_init();
   }
   // The kernel before this one on the stream wrote the operands.  (Where it is the adapters' first product,
@@ -1175,6 +1234,17 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
           // all four warps go on, or none: they meet at barriers
           ok = role_all<1>(mbar_wait(smem_addr(&bars.chunk_empty[chunk.s]), chunk.phase ^ 1));
           if (!ok) break;
+          // Infinities and NaN among B's values?  (Looked for here, where all loads are behind.)
+          __nv_bfloat162 zeros = __floats2bfloat162_rn(0.0f, 0.0f);
+#pragma unroll
+          for (int k = 0; k < kTimesB; ++k)
+            zeros = add_zeros(b[k].x, add_zeros(b[k].y, add_zeros(b[k].z, add_zeros(b[k].w, zeros))));
+          if (!__hbeq2(zeros, zeros)) {
+            bars.special = 1;
+#pragma unroll
+            for (int k = 0; k < kTimesB; ++k)
+              b[k] = make_uint4(without_special(b[k].x), without_special(b[k].y), without_special(b[k].z), without_special(b[k].w));
+          }
           // (rows 16 apart have the same place in the swizzle)
           uint8_t* const dst = chunks + chunk.s * S::kChunkBytes + row_of * 128 + ((piece ^ (row_of & 7)) << 4);
 #pragma unroll
@@ -1252,6 +1322,11 @@ __global__ void __launch_bounds__((GemmShape<KIND, MX, T, LORA>::kThreads), 1)
       asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols) : "memory");
     else
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kCols) : "memory");
+  }
+  if constexpr (LORA) {
+    if (bars.special)
+      add_special<MX, T>(p, bars, GemmTiles<kGemmRows, T>{p, start, lo, hi, units, tiles, places, place, 1, 0},
+                         static_cast<int>(rank), splits, part_k);
   }
 }
 

@@ -402,6 +402,7 @@ HQ_API hq_status hq_grouped_wgrad_mxfp4(const uint8_t* gq, const uint8_t* gs, co
  *   with a = row_adapter[m]; no second term where a is negative or not below `adapters`.
  *   Both terms are added in fp32 before the one rounding to out_dtype; the inner sums of the second
  *   are carried in two bf16 terms (to 2^-17).  x_sg * w_sg must be a normal fp32 number.
+ *   An infinity or NaN in x, lora_a or lora_b reaches the rows that use it and no other.
  *
  *   xq [M, K/2], xs [M, K/16] row-major, x_sg 1 float: x as quantized (rotated along K like the
  *   weights); x bf16 [M, K], row stride ldx: x itself, which the adapters read; wq [N, K/2], ws
