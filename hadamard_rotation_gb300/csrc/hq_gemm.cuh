@@ -1581,7 +1581,9 @@ __global__ void __launch_bounds__(kShrinkThreads)
     for (int k = 0; k < 2; ++k) {
       const float x = v[2 * k] * scale, y = v[2 * k + 1] * scale;
       hi[k] = __floats2bfloat162_rn(x, y);
-      lo[k] = __floats2bfloat162_rn(x - __low2float(hi[k]), y - __high2float(hi[k]));
+      // (of an infinity nothing is left: inf - inf would make the sum NaN)
+      const float hx = __low2float(hi[k]), hy = __high2float(hi[k]);
+      lo[k] = __floats2bfloat162_rn(isinf(hx) ? 0.0f : x - hx, isinf(hy) ? 0.0f : y - hy);
     }
     __nv_bfloat16* const t = p.t + static_cast<int64_t>(row0 + row) * 2 * p.rank + r;
     *reinterpret_cast<uint2*>(t) = *reinterpret_cast<const uint2*>(hi);
