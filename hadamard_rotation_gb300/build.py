@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, "hq.cu"), os.path.join(CSRC, "hq_int8.cu"),
            os.path.join(CSRC, "hq_gemm.cu"), os.path.join(CSRC, "hq_norm.cu"),
-           os.path.join(CSRC, "hq_host.cu"), os.path.join(CSRC, "hq_noalloc.cu")]
+           os.path.join(CSRC, "hq_smem.cu"), os.path.join(CSRC, "hq_host.cu"), os.path.join(CSRC, "hq_noalloc.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "hq_kernels.cuh"), os.path.join(CSRC, "hq_int8.cuh"),
                   os.path.join(CSRC, "hq_gemm.cuh"), os.path.join(CSRC, "hq_norm.cuh"),
                   os.path.join(CSRC, "hq_internal.h"),

@@ -99,38 +99,6 @@ cudaError_t hq::sm_count(int* sms) {
   return e;
 }
 
-cudaError_t hq::allow_smem(const void* fn, int bytes) {
-  struct Entry {
-    const void* fn;
-    int dev, bytes;
-    unsigned long long ctx;
-  };
-  static std::mutex mu;
-  static Entry entries[64];
-  static int n = 0;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long ctx = hq::context_id();
-  if (ctx != 0) {
-    std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < n; ++i)
-      if (entries[i].fn == fn && entries[i].dev == dev && entries[i].ctx == ctx && entries[i].bytes >= bytes)
-        return cudaSuccess;
-  }
-  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  const unsigned long long now = ctx != 0 ? ctx : hq::context_id();  // (the call may have made the context)
-  if (e == cudaSuccess && now != 0) {
-    std::lock_guard<std::mutex> lock(mu);
-    int at = -1;
-    for (int i = 0; i < n; ++i)
-      if (entries[i].fn == fn && entries[i].dev == dev) at = i;  // a smaller size, or an older context's
-    if (at < 0 && n < 64) at = n++;
-    if (at >= 0) entries[at] = {fn, dev, bytes, now};
-  }
-  return e;
-}
-
 cudaError_t hq::clusters_at_a_time(const void* fn, const cudaLaunchConfig_t& cfg, int ranks, int* n) {
   struct Entry {
     unsigned long long ctx;

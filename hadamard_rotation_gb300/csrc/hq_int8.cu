@@ -70,8 +70,7 @@ hq_status launch_int8_park_ring(const hq::I8Params& p, size_t park_bytes, hq_str
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return cuda_fail(e);
   if (smem > 48 * 1024 &&
-      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(smem))) != cudaSuccess)
+      (e = hq::allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem))) != cudaSuccess)
     return cuda_fail(e);
   const int64_t n_blocks = (p.M + p.rows_per_block - 1) / p.rows_per_block;
   const unsigned grid = static_cast<unsigned>(n_blocks < sms ? n_blocks : sms);

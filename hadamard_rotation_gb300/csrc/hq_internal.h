@@ -21,8 +21,8 @@ cudaError_t gemm_fault_word(unsigned int* fault, bool clear);
 // And for the norms' (hq_norm.cu).
 cudaError_t norm_fault_word(unsigned int* fault, bool clear);
 
-// Allow `fn` `bytes` of dynamic shared memory on the current device; remembered per kernel, device and
-// context, so that a call of a few microseconds asks the runtime once.
+// Allow `fn` `bytes` of dynamic shared memory on the current device (hq_smem.cu); remembered per kernel, device and
+// context, so that a call of a few microseconds asks the runtime once.  Host threads may call it at the same time.
 cudaError_t allow_smem(const void* fn, int bytes);
 
 // How many clusters of `ranks` CTAs, each alone on its SM, run at a time (not sms / ranks: the SMs of a cluster
