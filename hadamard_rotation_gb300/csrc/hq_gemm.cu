@@ -96,6 +96,14 @@ hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t b_scale_r
                  int splits, hq_stream stream) {
   using S = hq::GemmShape<KIND, MX, T, LORA>;
   auto kernel = hq::k_fp4_gemm<KIND, MX, T, LORA, SPLIT>;
+  int sms = 0;
+  cudaError_t e = hq::sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  // (Before the tensor maps: encoding one fails in a thread that has made no CUDA call yet, and this makes the
+  // context current there.)
+  const size_t smem = hq::gemm_smem_bytes(S::kSmemBytes, p.groups);
+  if ((e = hq::allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem))) != cudaSuccess)
+    return cuda_fail(e);
   CUtensorMap ma, mb, msa, msb = {}, mo = {};
   if (!encode_codes(&ma, a.q, a.row_bytes, a.rows, a.groups, hq::kGemmLanes, 3) ||
       !encode_codes(&mb, b.q, b.row_bytes, b.rows, 1, S::kBox, 2) ||
@@ -104,12 +112,6 @@ hq_status launch(GemmParams p, const Codes& a, const Codes& b, int64_t b_scale_r
     return cuda_fail(cudaErrorInvalidValue);
   p.out_tma = !p.out_f32 && p.out_vec == 16 &&
               encode_out(&mo, p.out, p.na, KIND == hq::kGemmRows ? p.extent : p.nb, KIND == hq::kGemmRows ? 1 : p.groups);
-  int sms = 0;
-  cudaError_t e = hq::sm_count(&sms);
-  if (e != cudaSuccess) return cuda_fail(e);
-  const size_t smem = hq::gemm_smem_bytes(S::kSmemBytes, p.groups);
-  if ((e = hq::allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem))) != cudaSuccess)
-    return cuda_fail(e);
   cudaLaunchConfig_t cfg = {};
   const int ctas = S::kCtas * splits;
   const int64_t most = SPLIT ? most_tiles : sms / ctas;
@@ -388,11 +390,12 @@ hq_status launch_shrink(hq::ShrinkParams p, const void* x, int64_t ldx, const vo
   if (bytes < (p.stages - 1) * stage + hq::kShrinkRows * 128) bytes = (p.stages - 1) * stage + hq::kShrinkRows * 128;
   if (bytes < hq::kShrinkRows * (padded + hq::kShrinkPad) * 4) bytes = hq::kShrinkRows * (padded + hq::kShrinkPad) * 4;
   bytes += 1024;
+  // (before the tensor maps, as in `launch`)
+  if ((e = hq::allow_smem(reinterpret_cast<const void*>(hq::k_lora_shrink), bytes)) != cudaSuccess) return cuda_fail(e);
   CUtensorMap mx, ma;
   if (!encode_bf16(&mx, x, p.K, ldx * 2, p.rows, 1, p.box_rows, 2) ||
       !encode_bf16(&ma, a, p.K, int64_t{2} * p.K, p.rank, p.adapters, padded, 3))
     return cuda_fail(cudaErrorInvalidValue);
-  if ((e = hq::allow_smem(reinterpret_cast<const void*>(hq::k_lora_shrink), bytes)) != cudaSuccess) return cuda_fail(e);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles) * p.slices * p.jobs);
   cfg.blockDim = dim3(hq::kShrinkThreads);
