@@ -473,11 +473,13 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_con
       for (int j = 0; j < V; ++j) {
         float2 f[4];
         Unit<BF16> o;
+        // (What is not there is 0 in the amax, also times a reciprocal norm that is infinite where eps is 0.)
+        const float r = PLAIN || (live2 && in[j]) ? r_pre : 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = mul2(mul2(t[j][e], both(r_pre)), w_pre[j][e]);
+        for (int e = 0; e < 4; ++e) f[e] = mul2(mul2(t[j][e], both(r)), w_pre[j][e]);
         o.set(f);
         if (live2 && in[j]) o.store(dst + j * unit);
-        if (!PLAIN && p.group >= 0) {  // (the same for the grid: every lane takes part in the exchange; t is 0 outside)
+        if (!PLAIN && p.group >= 0) {  // (the same for the grid: every lane takes part in the exchange)
           o.get(f);
           most = max_nan(most, rotated_absmax(f, p.group, threadIdx.x & 31));
         }
