@@ -10,9 +10,9 @@
 // result is that pass's bit for bit.
 //
 // Backward, with gn = dn w_pre:
-//   d  = dh' + r_pre gn - h' k,   k = r_pre^3 / D sum(gn h')       the whole gradient at h'
+//   d  = dh' + r_pre (gn - h' k), k = r_pre^2 / D sum(gn h')       the whole gradient at h'
 //   dh = alpha d,  dgate = d u,  du = d gate
-//   dy = r_post du w_post - y r_post^3 / D sum(du w_post y)
+//   dy = r_post du w_post - (y r_post) c r_post,  c = r_post / D sum(du w_post y)
 //   dw_pre = sum_rows dn h' r_pre,  dw_post = sum_rows du y r_post
 // The second row sum contains d, which needs the first; since d is linear in k, three sums over the
 // inputs alone -- sum(gn h'), sum((dh' + r_pre gn) q), sum(h' q), q = gate w_post y -- give both, so a row
@@ -27,8 +27,8 @@
 // reductions half of the time (bf16 [16384, 8192] forward 313 us; 169 now, 6.4 TB/s, 0.94 of a copy).  Rows of more columns than a CTA
 // holds are split over a cluster, whose warps write their sums into every CTA's shared memory;
 // narrow rows are taken several at a time.  Column sums end as one partial row per cluster, added in
-// a fixed order by k_norm_columns: no atomics, the same bits each time.  Backward bf16 [8192, 8192] takes 138 us,
-// 5.8 TB/s, 0.86 of a copy: 16 warps of 128 registers fill the register file, and with no more of them what a step
+// a fixed order by k_norm_columns: no atomics, the same bits each time.  Backward bf16 [8192, 8192] takes 140 us,
+// 5.75 TB/s, 0.85 of a copy: 16 warps of 128 registers fill the register file, and with no more of them what a step
 // costs beside its bytes is not all hidden.  fp32 [1021, 1360] takes 16.6 us for 33 MB: its first rows arrive 4 us
 // after the start, five steps take some 1.8 us each, and the column sums have a second kernel.
 #pragma once
@@ -629,9 +629,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
       float s[3];
       get_sums<3>(sh, i - 1, warps, row, ranks, s);
       const float r_pre = before.r_pre, r_post = before.r_post, tok = before.tok;
-      const float k1 = r_pre * r_pre * r_pre * (s[0] * inv_d);
-      const float dot = fmaf(-k1, s[2], s[1]);  // sum d q (a per-token gate left out)
-      const float k2 = r_post * r_post * r_post * (tok * dot * inv_d);
+      // (The third powers of the reciprocal norms, which leave fp32 for rows of 1e13 and more, do not occur: one more
+      // product per pair of elements, bf16 [8192, 8192] 139 -> 140 us.)
+      const float k = r_pre * (r_pre * s[0] * inv_d);
+      const float dot = fmaf(-r_pre, k * s[2], s[1]);  // sum d q (a per-token gate left out)
+      const float c_post = r_post * (tok * dot * r_post * inv_d);
       if (by_token && m1 < p.M && lane_u == 0 && rank == 0)
         static_cast<float*>(p.dgate)[m1] = dot * r_post;
       const uint8_t* src = units0 + s1 * 4 * tensor;
@@ -646,13 +648,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
           x.get(d);
           if (pre) {
             x.load_row(src + tensor + j * unit);
-            x.get(v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d[e] = fma2(both(r_pre), mul2(v[e], w_pre[j][e]), d[e]);
+            x.get(o);
             x.load_row(src + j * unit);
             x.get(v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) d[e] = fma2(v[e], both(-k1), d[e]);
+            for (int e = 0; e < 4; ++e) d[e] = fma2(both(r_pre), fma2(v[e], both(-k), mul2(o[e], w_pre[j][e])), d[e]);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[e] = mul2(both(p.alpha), d[e]);
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm_bwd(const __grid
             d[e] = mul2(d[e], both(dr));
             sum_a[j][e] = fma2(d[e], v[e], sum_a[j][e]);
             o[e] = mul2(d[e], w_post[j][e]);
-            if (post) o[e] = fma2(v[e], both(-k2), o[e]);
+            if (post) o[e] = fma2(mul2(v[e], both(r_post)), both(-c_post), o[e]);
           }
           x.set(o);
           x.store(static_cast<uint8_t*>(p.dy) + at1 + j * unit);
