@@ -9,6 +9,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -44,11 +45,19 @@ def nvcc_link_command(objs: list[str], out: str) -> list[str]:
     return [nvcc_path(), ARCH, "-shared", "-o", out, *objs]
 
 
+def calls_built_for() -> str:
+    """What _torch_calls.so is compiled for; a copy of it is kept in the file (up_to_date)."""
+    import torch
+
+    return f"hq: torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
 def calls_compile_command(src: str, obj: str) -> list[str]:
     import torch
 
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c",
+            f'-DHQ_BUILT_FOR="{calls_built_for()}"',
             "-I", INCLUDE, "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
             "-I", sysconfig.get_paths()["include"],
             "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include"), "-o", obj, src]
@@ -62,37 +71,68 @@ def calls_link_command(obj: str, out: str) -> list[str]:
             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
+def library_up_to_date() -> bool:
+    return os.path.exists(LIB) and all(os.path.getmtime(d) <= os.path.getmtime(LIB) for d in DEPS)
+
+
+def calls_up_to_date() -> bool:
+    if not os.path.exists(CALLS):
         return False
-    t, c = os.path.getmtime(LIB), os.path.getmtime(CALLS)
-    return all(os.path.getmtime(d) <= t for d in DEPS) and \
-        all(os.path.getmtime(d) <= c for d in (CALLS_SOURCE, os.path.join(INCLUDE, "hq.h")))
+    t = os.path.getmtime(CALLS)
+    if any(os.path.getmtime(d) > t for d in (CALLS_SOURCE, os.path.join(INCLUDE, "hq.h"))):
+        return False
+    with open(CALLS, "rb") as f:
+        return calls_built_for().encode() + b"\0" in f.read()
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
+def up_to_date() -> bool:
+    return library_up_to_date() and calls_up_to_date()
+
+
+def _failed(what: str, rc: int):
+    raise subprocess.CalledProcessError(rc, what)
+
+
+def build(force: bool = False, verbose: bool = False, calls: bool = True) -> str:
+    """Builds what is not up to date and returns libhq.so's path.
+
+    libhq.so needs nvcc alone.  _torch_calls.so needs g++ and the headers of Python and of a CUDA build of torch; where it
+    cannot be built this raises, after libhq.so has been linked.  ``calls=False`` leaves it out (for callers from C)."""
+    library = force or not library_up_to_date()
+    calls = calls and (force or not calls_up_to_date())
     tag = f".tmp{os.getpid()}"
-    objs = [os.path.join(CSRC, os.path.basename(src)[:-3] + tag + ".o") for src in SOURCES]
+    objs = [os.path.join(CSRC, os.path.basename(src)[:-3] + tag + ".o") for src in SOURCES] if library else []
     calls_obj = os.path.join(CSRC, "hq_torch" + tag + ".o")
     extra = ["-Xptxas", "-v"] if verbose else None
+    no_calls = None
+    procs, calls_proc = [], None
     try:
         # one compiler per translation unit, in parallel, then a link each
-        procs = [subprocess.Popen(nvcc_compile_command(src, obj, extra))
-                 for src, obj in zip(SOURCES, objs)]
-        procs.append(subprocess.Popen(calls_compile_command(CALLS_SOURCE, calls_obj)))
+        procs = [subprocess.Popen(nvcc_compile_command(src, obj, extra)) for src, obj in zip(SOURCES, objs)]
+        if calls:
+            try:
+                calls_proc = subprocess.Popen(calls_compile_command(CALLS_SOURCE, calls_obj))
+            except (ImportError, OSError) as e:
+                no_calls = e
         rcs = [pr.wait() for pr in procs]
-        for src, rc in zip([*SOURCES, CALLS_SOURCE], rcs):
+        for src, rc in zip(SOURCES, rcs):
             if rc != 0:
-                raise subprocess.CalledProcessError(rc, f"compiling {os.path.basename(src)}")
-        tmp = LIB + tag
-        subprocess.run(nvcc_link_command(objs, tmp), check=True)
-        os.replace(tmp, LIB)
-        tmp = CALLS + tag
-        subprocess.run(calls_link_command(calls_obj, tmp), check=True)
-        os.replace(tmp, CALLS)
+                _failed(f"compiling {os.path.basename(src)}", rc)
+        if library:
+            tmp = LIB + tag
+            subprocess.run(nvcc_link_command(objs, tmp), check=True)
+            os.replace(tmp, LIB)
+        if no_calls:
+            raise no_calls
+        if calls_proc:
+            if calls_proc.wait() != 0:
+                _failed(f"compiling {os.path.basename(CALLS_SOURCE)} (libhq.so is built)", calls_proc.returncode)
+            tmp = CALLS + tag
+            subprocess.run(calls_link_command(calls_obj, tmp), check=True)
+            os.replace(tmp, CALLS)
     finally:
+        for pr in [*procs, *([calls_proc] if calls_proc else [])]:
+            pr.wait()
         for obj in [*objs, calls_obj]:
             if os.path.exists(obj):
                 os.remove(obj)
@@ -100,4 +140,4 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    print(build(force=True, verbose=True))
+    print(build(force=True, verbose=True, calls="--library" not in sys.argv[1:]))

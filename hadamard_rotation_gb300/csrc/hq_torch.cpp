@@ -20,6 +20,11 @@
 
 #include "hq.h"
 
+// Which torch and Python this file was compiled for: build.py looks for it in the built module.
+#ifdef HQ_BUILT_FOR
+__attribute__((used)) static const char built_for[] = HQ_BUILT_FOR;
+#endif
+
 namespace {
 
 // A refusal: becomes a Python ValueError.
