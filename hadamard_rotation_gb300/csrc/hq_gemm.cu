@@ -211,6 +211,11 @@ bool narrow_rows(int64_t M, int64_t N, int64_t K, int64_t E) {
          narrow_tiles(M, E, (N + 127) / 128) <= 36 * 152 / ((K + hq::kGemmKBlock - 1) / hq::kGemmKBlock + 4);
 }
 
+// Tiles of the kernel that is taken, at most.
+int64_t rows_tiles(int64_t M, int64_t N, int64_t K, int64_t E) {
+  return narrow_rows(M, N, K, E) ? narrow_tiles(M, E, (N + 127) / 128) : (M + 191 * (E < M ? E : M)) / 192 * ((N + 255) / 256);
+}
+
 // The narrow kernel, its summed axis shared by a cluster where there are few tiles: as many CTAs as
 // SMs, each with two pairs of stages at least (a shorter part is mostly start and end).
 template <bool MX, bool LORA>
@@ -277,20 +282,30 @@ GemmParams rows_params(const uint8_t* xs, const float* x_sg, const uint8_t* ws, 
   return p;
 }
 
+// The sizes that the calls and their workspace functions refuse.
+bool grouped_sizes(int64_t M, int64_t N, int64_t K, int64_t E) {
+  if (M < 0 || N < 0 || K < 0 || E < 0 || K % 32 != 0) return false;
+  if (M > kMaxExtent || N > kMaxExtent || K > kMaxExtent || E > hq::kGemmMaxGroups) return false;
+  return M == 0 || N == 0 || E == 0 || rows_tiles(M, N, K, E) <= kMaxExtent;
+}
+
+bool lora_sizes(int64_t M, int64_t N, int64_t K, int64_t R) {
+  if (M < 0 || N < 0 || K <= 0 || K % 32 != 0 || R < 8 || R > 128 || R % 8 != 0) return false;
+  if (M > kMaxExtent || N > kMaxExtent || K > kMaxExtent) return false;
+  return M == 0 || N == 0 || rows_tiles(M, N, K, 1) <= kMaxExtent;
+}
+
 template <bool MX>
 hq_status grouped_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, const uint8_t* wq, const uint8_t* ws,
                        const float* w_sg, const int32_t* offsets, int64_t M, int64_t N, int64_t K, int64_t E, void* out,
                        hq_dtype dt, void* workspace, hq_stream stream) {
   if (dt != HQ_F32 && dt != HQ_BF16) return HQ_ERR_DTYPE;
-  if (M < 0 || N < 0 || K < 0 || E < 0 || K % 32 != 0) return HQ_ERR_SHAPE;
-  if (M > kMaxExtent || N > kMaxExtent || K > kMaxExtent || E > hq::kGemmMaxGroups) return HQ_ERR_SHAPE;
+  if (!grouped_sizes(M, N, K, E)) return HQ_ERR_SHAPE;
   if (M == 0 || N == 0 || E == 0) return HQ_OK;
   if (!out || !offsets) return HQ_ERR_NULL;
   if (!aligned(out, dt == HQ_F32 ? 4 : 2) || !aligned(offsets, 4)) return HQ_ERR_ALIGN;
   const bool narrow = narrow_rows(M, N, K, E);
-  const int64_t tiles_a = narrow ? (N + 127) / 128 : (N + 255) / 256;
-  const int64_t tiles = narrow ? narrow_tiles(M, E, tiles_a) : (M / 192 + (E < M ? E : M)) * tiles_a;
-  if (tiles > kMaxExtent) return HQ_ERR_SHAPE;
+  const int64_t tiles = rows_tiles(M, N, K, E);
   if (K == 0) return out_zero(out, M * N, dt, stream);
   if (!xq || !xs || !wq || !ws || (!MX && (!x_sg || !w_sg))) return HQ_ERR_NULL;
   if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(ws, 32) || (!MX && (!aligned(x_sg, 4) || !aligned(w_sg, 4))))
@@ -422,9 +437,7 @@ hq_status lora_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, con
                     const int32_t* ids, int64_t M, int64_t N, int64_t K, int64_t n, int64_t R, void* out, hq_dtype dt,
                     void* workspace, hq_stream stream) {
   if (dt != HQ_F32 && dt != HQ_BF16) return HQ_ERR_DTYPE;
-  if (M < 0 || N < 0 || K <= 0 || n < 0 || K % 32 != 0 || R < 8 || R > 128 || R % 8 != 0 || ldx < K)
-    return HQ_ERR_SHAPE;
-  if (M > kMaxExtent || N > kMaxExtent || K > kMaxExtent || n > kMaxExtent || ldx > INT64_MAX / 2 / (M ? M : 1))
+  if (!lora_sizes(M, N, K, R) || n < 0 || n > kMaxExtent || ldx < K || ldx > INT64_MAX / 2 / (M ? M : 1))
     return HQ_ERR_SHAPE;
   if (M == 0 || N == 0) return HQ_OK;
   if (!out || !xq || !xs || !wq || !ws || !x || !ids || !workspace || (n > 0 && (!a || !b || !scaling)) ||
@@ -435,8 +448,7 @@ hq_status lora_gemm(const uint8_t* xq, const uint8_t* xs, const float* x_sg, con
       !aligned(ids, 4) || !aligned(workspace, 32) || !aligned(x_sg, 4) || !aligned(w_sg, 4))
     return HQ_ERR_ALIGN;
   const bool narrow = narrow_rows(M, N, K, 1);
-  const int64_t tiles = narrow ? narrow_tiles(M, 1, (N + 127) / 128) : (M + 191) / 192 * ((N + 255) / 256);
-  if (tiles > kMaxExtent) return HQ_ERR_SHAPE;
+  const int64_t tiles = rows_tiles(M, N, K, 1);
   hq::ShrinkParams s = {};
   s.scaling = scaling;
   s.sg_a = w_sg;
@@ -536,12 +548,12 @@ hq_status hq_grouped_wgrad_mxfp4(const uint8_t* gq, const uint8_t* gs, const uin
 }
 
 int64_t hq_grouped_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t E) {
-  if (M < 0 || N < 0 || K < 0 || E < 0 || M > kMaxExtent || N > kMaxExtent || K > kMaxExtent || E > hq::kGemmMaxGroups || K % 32 != 0) return -1;
+  if (!grouped_sizes(M, N, K, E)) return -1;
   return M == 0 || E == 0 || narrow_rows(M, N, K, E) ? 0 : group_scale_bytes(M, K, E, false);
 }
 
 int64_t hq_lora_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t R) {
-  if (M < 0 || N < 0 || M > kMaxExtent || N > kMaxExtent || K < 0 || K > kMaxExtent || K % 32 != 0 || R < 8 || R > 128 || R % 8 != 0) return -1;
+  if (!lora_sizes(M, N, K, R)) return -1;
   return lora_t_bytes(M, R) + (narrow_rows(M, N, K, 1) ? 0 : group_scale_bytes(M, K, 1, false));
 }
 
