@@ -55,18 +55,20 @@
 // the rows and lanes that only a call with such a value pays for.
 //
 // What bounds it, measured.
-//   A few rows per expert: the weights' bytes.  64 experts of 4096 x 2048 (MXFP4), 512 rows: 35.7 us, 5.75 TB/s of
-//   what has to move, 0.85 of a copy.  One token at 8 experts of 2048 x 4096: 9.3 us, of which 5.6 are bytes and the
-//   rest a launch's start and the sum over the cluster.
-//   Large groups: what the L2 gives the SMs.  64 experts of 2048 x 4096 (NVFP4), 32768 rows: 129 us, 4.2 PFLOP/s,
-//   tensor pipe 51% busy, 2.4 GB through the L2 for 0.48 GB of DRAM traffic; a square-ish projection without groups
-//   ([4096, 4096] x [8192, 4096]) 56 us, 4.9 PFLOP/s.  Wider tiles would read less, but tensor memory holds two
-//   accumulators of 192 columns beside the scales, and with one the epilogue (a third of a tile's time) stood alone.
-//   Weight gradients: their output.  16 experts of 2048 x 4096 bf16 from 8192 tokens: 60 us for 0.30 GB, 0.73 of a
+//   A few rows per expert: the weights' bytes.  64 experts of 4096 x 2048 (MXFP4), 512 rows: 34 to 38 us, 5.4 to 6.1
+//   TB/s of what has to move, 0.79 to 0.90 of a copy.  One token at 8 experts of 2048 x 4096: 9.1 to 9.7 us, of which 5.6
+//   are bytes and the rest a launch's start and the sum over the cluster.
+//   Large groups: 64 experts of 2048 x 4096 (NVFP4), 32768 rows: 134 us, 4.1 PFLOP/s.  Tensor pipe 51% busy, DRAM 50%, L2
+//   58% (2.4 GB for 0.48 GB of DRAM traffic): none is full, and which wait it is has not been settled.  (Not the L2 alone:
+//   the adapters' form takes a quarter less per second from it and keeps the pipe no busier.  The order in which warp 1
+//   issues scale copies and products was not varied.)  A square-ish projection without groups ([4096, 4096] x
+//   [8192, 4096]) 56 us, 4.9 PFLOP/s.  Wider tiles would read less, but tensor memory holds two accumulators of 192
+//   columns beside the scales, and with one the epilogue (a third of a tile's time) stood alone.
+//   Weight gradients: their output.  16 experts of 2048 x 4096 bf16 from 8192 tokens: 61 to 63 us for 0.30 GB, 0.72 of a
 //   copy; an expert's sum is 2 stages long, so a tile is mostly its 98 KB of output.
-//   Adapters: [4096, 4096] x [8192, 4096] with 8 adapters of rank 64 in runs of 200 rows: 86 us = 15 us of the thin
+//   Adapters: [4096, 4096] x [8192, 4096] with 8 adapters of rank 64 in runs of 200 rows: 80 to 89 us = 15 us of the thin
 //   product (bound by reading x at 3.9 TB/s from its first copy to its last, then by its clusters' barriers) and 65 us;
-//   32 rows of 24 adapters of rank 16 beside 4096 x 4096: 17 us, two kernels' latencies one after the other.
+//   32 rows of 24 adapters of rank 16 beside 4096 x 4096: 17.5 us, two kernels' latencies one after the other.
 #pragma once
 
 #include <cuda.h>

@@ -34,8 +34,8 @@ Shape shape_of(int64_t M, int D, int es, int tensors, int sms) {
   const int u = (s.cols + 7) / 8;
   // Two units per thread where there are rows enough for all SMs all the same: what a step costs a thread
   // beside its elements (the sums' way through shuffles and shared memory) is then shared by 16 of them.
-  // (One against two when this was chosen: bf16 [8192, 2048] forward 40.0 / 30.1 us, backward 60.5 / 50.9; now 28.4
-  // and 46.6.  Not backward in fp32, whose stages leave room for half the threads then: [4096, 4096] 111 / 186 us.)
+  // (One against two when this was chosen: bf16 [8192, 2048] forward 40.0 / 30.1 us, backward 60.5 / 50.9; now 28.6
+  // and 47.0.  Not backward in fp32, whose stages leave room for half the threads then: [4096, 4096] 111 / 186 us.)
   const bool fp32_bwd = tensors == 4 && es == 4;
   s.units = u > hq::kNormThreads || (u >= 64 && M >= 4 * sms && !fp32_bwd) ? 2 : 1;
   s.tpr = ((u + s.units - 1) / s.units + 31) / 32 * 32;

@@ -29,7 +29,7 @@
 // narrow rows are taken several at a time.  Column sums end as one partial row per cluster, added in
 // a fixed order by k_norm_columns: no atomics, the same bits each time.  Backward bf16 [8192, 8192] takes 140 us,
 // 5.75 TB/s, 0.85 of a copy: 16 warps of 128 registers fill the register file, and with no more of them what a step
-// costs beside its bytes is not all hidden.  fp32 [1021, 1360] takes 16.6 us for 33 MB: its first rows arrive 4 us
+// costs beside its bytes is not all hidden.  fp32 [1021, 1360] takes 16.8 us for 33 MB: its first rows arrive 4 us
 // after the start, five steps take some 1.8 us each, and the column sums have a second kernel.
 #pragma once
 
@@ -419,7 +419,8 @@ __device__ __forceinline__ void expect_sums(const NormShared& sh, int step, int 
   static_assert(true, "")
 
 // PLAIN: both norms, y, no gate or one per channel, no amax -- known to the compiler, which then has no
-// branch in the loop (bf16 [16384, 8192] forward 235 us without).
+// branch in the loop (bf16 [16384, 8192] forward 169 us; 235 without when this was chosen).  With the amax the same
+// call takes 214 us without a rotation, 240 with 16 and 312 with 256 points: the branches, then the exchange.
 template <bool BF16, int V, bool PLAIN>
 __global__ void __launch_bounds__(kNormThreads, 1) k_block_norm(const __grid_constant__ NormParams p) {
   HQ_NORM_SETUP(2);
