@@ -126,6 +126,19 @@ def load() -> ctypes.CDLL:
         lib.hq_block_norm_bwd.restype = i32
         lib.hq_block_norm_bwd_workspace_bytes.argtypes = [i64, i64]
         lib.hq_block_norm_bwd_workspace_bytes.restype = i64
+        lib.hq_gemm_int8.argtypes = [p] * 4 + [i64] * 3 + [p, i32, p]
+        lib.hq_gemm_int8.restype = i32
+        lib.hq_kv_page_bytes.argtypes = [i64] * 3
+        lib.hq_kv_page_bytes.restype = i64
+        lib.hq_kv_append_nvfp4.argtypes = [p, i64] * 3 + [i32] + [i64] * 4 + [p, p, i64, i64, i32, p, p, i32, p, p, p, i64, i64, p]
+        lib.hq_kv_append_nvfp4.restype = i32
+        lib.hq_kv_read_nvfp4.argtypes = [p] + [i64] * 4 + [p, i64, p, i32, p, p, i32, p]
+        lib.hq_kv_read_nvfp4.restype = i32
+        lib.hq_kv_attention_nvfp4.argtypes = [p] + [i64] * 3 + [p] + [i64] * 4 + [p, i64, i64, p, p, i64, i64, p, f32, i64, i32,
+                                              p, p, p, p]
+        lib.hq_kv_attention_nvfp4.restype = i32
+        lib.hq_kv_attention_workspace_bytes.argtypes = [i64] * 3
+        lib.hq_kv_attention_workspace_bytes.restype = i64
         lib.hq_version.argtypes = []
         lib.hq_version.restype = i32
         _lib = lib

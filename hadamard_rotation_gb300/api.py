@@ -320,7 +320,7 @@ def hq_dequant_nvfp4(q: torch.Tensor, scales: torch.Tensor, s_global: torch.Tens
 
 # ---- products of the codes -------------------------------------------------------------------
 #
-# A call of a few rows takes the GPU a few microseconds, so the products' and norms' arguments are checked and
+# A call of a few rows takes the GPU a few microseconds, so the arguments of the products, norms and caches are checked and
 # marshalled in C++ (csrc/hq_torch.cpp, built beside libhq.so); the functions here are their
 # documentation and signatures.
 
@@ -485,6 +485,76 @@ def hq_block_norm_bwd(dh_out: torch.Tensor | None, dn: torch.Tensor | None, h_ou
     and [M, 1] are float32, summed over the rows in a fixed order; that of a gate [M, D] has its dtype."""
     return (_calls or _load_calls()).block_norm_bwd(dh_out, dn, h_out, y, w_post, gate, w_pre, r_post, r_pre, alpha,
                                                      post_norm, pre_norm, stream)
+
+
+# ---- the product of INT8 codes -----------------------------------------------------------------
+
+
+def hq_gemm_int8(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w_scales: torch.Tensor,
+                 out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                 stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """The product of what hq_rotate_quant_int8 writes: out [M, N] = (xq wq^T) * x_scales[:, None] * w_scales.
+
+    xq int8 [M, K], x_scales float32 [M]; wq int8 [N, K] (weights rotated and quantized alike), w_scales float32
+    [N].  K a multiple of 16 below 2^17."""
+    return (_calls or _load_calls()).gemm_int8(xq, x_scales, wq, w_scales, out, out_dtype, stream)
+
+
+# ---- a paged NVFP4 cache of keys and values ----------------------------------------------------
+
+
+def hq_kv_page_bytes(page_size: int, kv_heads: int, D: int) -> int:
+    """Bytes of a page.  A cache is uint8 [pages, kv_heads, page_size / 16, 18 * D]."""
+    n = _lib.load().hq_kv_page_bytes(page_size, kv_heads, D)
+    if n < 0:
+        raise ValueError("hq_kv_page_bytes: page_size a multiple of 16, kv_heads up to 4096, D 64, 128 or 256")
+    return n
+
+
+def hq_kv_append_nvfp4(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cos: torch.Tensor | None,
+                       sin: torch.Tensor | None, positions: torch.Tensor | None, slots: torch.Tensor,
+                       kv_amax: torch.Tensor, cache: torch.Tensor, group: int = 16, interleaved: bool = False,
+                       q_out: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor | None:
+    """Puts T tokens into a paged NVFP4 cache, with the position rotation on the way; returns q_out, bfloat16
+    [T, q_heads, D], rotated like the keys (None without q).
+
+    q [T, q_heads, D], k, v [T, kv_heads, D] bfloat16 or float32, heads contiguous (views of a fused projection
+    will do); cos, sin float32 [rows, rotary / 2] and positions int32 [T], or None for no position rotation
+    (``interleaved``: pairs of neighbouring channels, else channels i and i + rotary / 2); slots int64 [T], page *
+    page_size + place, negative for a token that is not stored; kv_amax float32 [2], kept with the cache; cache uint8
+    [pages, kv_heads, page_size / 16, 18 * D]."""
+    return (_calls or _load_calls()).kv_append(q, k, v, cos, sin, positions, slots, kv_amax, cache, group, interleaved,
+                                                q_out, stream)
+
+
+def hq_kv_read_nvfp4(cache: torch.Tensor, slots: torch.Tensor, kv_amax: torch.Tensor, group: int = 0,
+                     out_dtype: torch.dtype = torch.bfloat16, k: torch.Tensor | None = None,
+                     v: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """The values of the cached tokens at ``slots``: (k, v) [T, kv_heads, D], zeros where a slot is none.  ``group``:
+    the rotation to undo (0: as stored)."""
+    return (_calls or _load_calls()).kv_read(cache, slots, kv_amax, group, out_dtype, k, v, stream)
+
+
+def hq_kv_attention_workspace_bytes(q_heads: int, kv_heads: int, D: int) -> int:
+    """Bytes of the workspace of hq_kv_attention_nvfp4 (which this binding allocates itself)."""
+    n = _lib.load().hq_kv_attention_workspace_bytes(q_heads, kv_heads, D)
+    if n < 0:
+        raise ValueError("hq_kv_attention_workspace_bytes: q_heads a multiple of kv_heads, up to 4096, D 64, 128 or 256")
+    return n
+
+
+def hq_kv_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
+                          q_start: torch.Tensor, kv_amax: torch.Tensor, scale: float, group: int = 16, window: int = 0,
+                          max_q: int | None = None, out: torch.Tensor | None = None, return_lse: bool = False,
+                          stream: torch.cuda.Stream | None = None):
+    """Causal attention over the cache: out bfloat16 [T, q_heads, D], with ``return_lse`` (out, lse float32 [T, q_heads]).
+
+    q bfloat16 [T, q_heads, D] as hq_kv_append_nvfp4 returns it; page_table int32 [S, pages of a sequence], kv_len int32
+    [S], q_start int32 [S + 1]: sequence s has the queries q_start[s] .. q_start[s + 1] - 1, which are the last of its
+    kv_len[s] tokens.  ``group``: the cache's rotation.  ``window``: keys that a query sees at most (0: all).
+    ``max_q``: the most queries of a sequence, if known.  Rows of no sequence are left as they are in ``out``."""
+    return (_calls or _load_calls()).kv_attention(q, cache, page_table, kv_len, q_start, kv_amax, scale, group, window,
+                                                   -1 if max_q is None else max_q, out, return_lse, stream)
 
 
 def quantize_nvfp4(x: torch.Tensor, group: int, stream: torch.cuda.Stream | None = None):

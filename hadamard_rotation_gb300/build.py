@@ -1,5 +1,5 @@
 """Compile libhq.so (the CUDA kernels and the C ABI) in-tree for sm_103a, and beside it _torch_calls.so (the
-products' and norms' calls over torch tensors, C++).
+products', norms' and caches' calls over torch tensors, C++).
 
 No fast-math: the kernels rely on IEEE division, correctly rounded reciprocals and
 denormal support.
@@ -18,9 +18,12 @@ INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, "hq.cu"), os.path.join(CSRC, "hq_int8.cu"),
            os.path.join(CSRC, "hq_gemm.cu"), os.path.join(CSRC, "hq_norm.cu"),
+           os.path.join(CSRC, "hq_gemm8.cu"), os.path.join(CSRC, "hq_kv.cu"),
            os.path.join(CSRC, "hq_smem.cu"), os.path.join(CSRC, "hq_host.cu"), os.path.join(CSRC, "hq_noalloc.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "hq_kernels.cuh"), os.path.join(CSRC, "hq_int8.cuh"),
                   os.path.join(CSRC, "hq_gemm.cuh"), os.path.join(CSRC, "hq_norm.cuh"),
+                  os.path.join(CSRC, "hq_gemm8.cuh"), os.path.join(CSRC, "hq_kv.cuh"),
+                  os.path.join(CSRC, "hq_kv_attend.cuh"),
                   os.path.join(CSRC, "hq_internal.h"),
                   os.path.join(INCLUDE, "hq.h")]
 LIB = os.path.join(PKG, "libhq.so")

@@ -748,6 +748,13 @@ hq_status hq_read_fault(unsigned int* fault, int clear) {
   e = hq::norm_fault_word(&norm_word, clear != 0);
   if (e != cudaSuccess) return cuda_fail(e);
   *fault |= norm_word;
+  unsigned int word = 0;  // the INT8 product's (hq_gemm8.cu) and the cache's (hq_kv.cu)
+  e = hq::gemm8_fault_word(&word, clear != 0);
+  if (e != cudaSuccess) return cuda_fail(e);
+  *fault |= word;
+  e = hq::kv_fault_word(&word, clear != 0);
+  if (e != cudaSuccess) return cuda_fail(e);
+  *fault |= word;
   return HQ_OK;
 }
 

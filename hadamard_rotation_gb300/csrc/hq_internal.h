@@ -20,6 +20,9 @@ cudaError_t int8_fault_word(unsigned int* fault, bool clear);
 cudaError_t gemm_fault_word(unsigned int* fault, bool clear);
 // And for the norms' (hq_norm.cu).
 cudaError_t norm_fault_word(unsigned int* fault, bool clear);
+// And for the INT8 product's (hq_gemm8.cu) and the cache's (hq_kv.cu).
+cudaError_t gemm8_fault_word(unsigned int* fault, bool clear);
+cudaError_t kv_fault_word(unsigned int* fault, bool clear);
 
 // Allow `fn` `bytes` of dynamic shared memory on the current device (hq_smem.cu); remembered per kernel, device and
 // context, so that a call of a few microseconds asks the runtime once.  Host threads may call it at the same time.

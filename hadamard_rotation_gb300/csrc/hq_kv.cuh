@@ -1,0 +1,281 @@
+// hq_kv.cuh -- device code of the paged NVFP4 cache of keys and values (sm_103a): appending to it, reading it back,
+// and attention over it for few queries per sequence (hq_kv_prompt.cuh: for many).
+//
+// The cache is made of records: 16 tokens of one head, 18 D bytes in one piece,
+//   K codes [16, D / 2] | V codes [16, D / 2] | K scales [16, D / 16] | V scales [16, D / 16],
+// so that everything a step of the attention reads of 16 tokens is one contiguous copy, whatever the page size (a
+// multiple of 16) is.  A page is [kv_heads][page_size / 16] records.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "hq_kernels.cuh"
+
+namespace hq {
+
+constexpr int kKvUnit = 16;  // tokens of a record
+
+template <int D>
+struct KvRecord {
+  static constexpr int kCodes = 16 * D / 2;   // K's (V's) code bytes
+  static constexpr int kScales = 16 * D / 16;
+  static constexpr int kV = kCodes, kKs = 2 * kCodes, kVs = 2 * kCodes + kScales;
+  static constexpr int kBytes = 2 * kCodes + 2 * kScales;
+  static_assert(kBytes == 18 * D, "a record");
+};
+
+// s_global of amax, as the quantizer has it.
+__device__ __forceinline__ float kv_global_scale(float amax) {
+  const float s = __fdiv_rn(amax, 2688.0f);
+  return s == 0.0f ? 1.0f : s;
+}
+
+// ---------------------------------------------------------------------------
+// Appending.
+//
+// A thread takes 16 channels of a head of a token: position rotation (two products and a sum, each rounded, as the
+// definition in hq.h has them), butterfly, then for K and V the block scale and codes exactly as
+// hq_rotate_quant_nvfp4.
+// ---------------------------------------------------------------------------
+struct KvAppendParams {
+  const uint8_t* in[3];  // q, k, v
+  int64_t ld[3];         // bytes between tokens
+  int heads[3];
+  int64_t T;
+  const float *cos_t, *sin_t;
+  int64_t rows;          // of the tables
+  int rotary, interleaved;
+  const int32_t* positions;
+  const int64_t* slots;
+  const float* kv_amax;
+  __nv_bfloat16* q_out;
+  uint8_t* cache;
+  int64_t n_slots;       // pages * page_size
+  int page_units;        // records of a page and head
+  int kv_heads;
+};
+
+template <bool BF16>
+__device__ __forceinline__ void kv_load8(const uint8_t* p, float (&f)[8]) {
+  if constexpr (BF16) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  } else {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+}
+
+// The rotation's butterfly over 16 channels of a thread, and (G = 256) over 16 lanes.
+template <int G>
+__device__ __forceinline__ void kv_rotate(float (&x)[16]) {
+  if constexpr (G != 0) {
+#pragma unroll
+    for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if ((i & h) == 0) {
+          const float a = x[i], b = x[i + h];
+          x[i] = __fadd_rn(a, b);
+          x[i + h] = __fsub_rn(a, b);
+        }
+    if constexpr (G == 256) {
+      const int lane = threadIdx.x & 31;
+#pragma unroll
+      for (int m = 1; m < 16; m <<= 1)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float o = __shfl_xor_sync(0xFFFFFFFFu, x[i], m);
+          x[i] = (lane & m) ? __fsub_rn(o, x[i]) : __fadd_rn(x[i], o);
+        }
+    }
+    constexpr float c = inv_sqrt_g<G>();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], c);
+  }
+}
+
+// The record that holds slot `slot`, and the token's place in it.
+template <int D>
+__device__ __forceinline__ int64_t kv_record(int64_t slot, int head, int kv_heads, int page_units, int& at) {
+  const int64_t unit = slot / kKvUnit, page = unit / page_units;
+  at = static_cast<int>(slot % kKvUnit);
+  return ((page * kv_heads + head) * page_units + (unit - page * page_units)) * KvRecord<D>::kBytes;
+}
+
+template <int D, int G, bool BF16>
+__global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ KvAppendParams p) {
+  using R = KvRecord<D>;
+  constexpr int kBlocks = D / 16, es = BF16 ? 2 : 4;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int heads = p.heads[0] + 2 * p.kv_heads;
+  const int64_t rows = p.T * heads;
+  const int b = threadIdx.x % kBlocks;
+  const float sg[2] = {kv_global_scale(__ldg(p.kv_amax)), kv_global_scale(__ldg(p.kv_amax + 1))};
+  // (every lane of a warp goes on while one does: the lanes exchange values)
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * (256 / kBlocks); r0 < rows; r0 += static_cast<int64_t>(gridDim.x) * (256 / kBlocks)) {
+    const int64_t r = r0 + threadIdx.x / kBlocks;
+    const bool live = r < rows;
+    const int64_t t = live ? r / heads : 0;
+    int head = live ? static_cast<int>(r - t * heads) : 0, which = 0;
+    if (head >= p.heads[0]) {
+      which = 1 + (head - p.heads[0]) / p.kv_heads;
+      head = (head - p.heads[0]) % p.kv_heads;
+    }
+    const int64_t slot = which ? __ldg(p.slots + t) : 0;
+    const bool store = live && slot >= 0 && (which == 0 || slot < p.n_slots);
+    const uint8_t* const src = p.in[which] + t * p.ld[which] + static_cast<int64_t>(head) * D * es;
+    float x[16];
+    {
+      float lo[8], hi[8];
+      kv_load8<BF16>(src + 16 * b * es, lo);
+      kv_load8<BF16>(src + (16 * b + 8) * es, hi);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = lo[i], x[8 + i] = hi[i];
+    }
+    if (which < 2 && p.rotary > 0) {
+      int64_t pos = __ldg(p.positions + t);
+      pos = pos < 0 ? 0 : pos >= p.rows ? p.rows - 1 : pos;
+      const int half = p.rotary / 2;
+      const float *ct = p.cos_t + pos * half, *st = p.sin_t + pos * half;
+      if (p.interleaved) {
+        if (16 * b < p.rotary) {
+          float c[8], s[8];
+          kv_load8<false>(reinterpret_cast<const uint8_t*>(ct + 8 * b), c);
+          kv_load8<false>(reinterpret_cast<const uint8_t*>(st + 8 * b), s);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x1 = x[2 * i], x2 = x[2 * i + 1];
+            x[2 * i] = __fsub_rn(__fmul_rn(x1, c[i]), __fmul_rn(x2, s[i]));
+            x[2 * i + 1] = __fadd_rn(__fmul_rn(x2, c[i]), __fmul_rn(x1, s[i]));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {  // 8 channels: in the first half of the pairs, in the second, or behind them
+          const int c0 = 16 * b + 8 * q;
+          if (c0 < p.rotary) {
+            const bool second = c0 >= half;
+            const int at = second ? c0 - half : c0;
+            float c[8], s[8], o[8];
+            kv_load8<false>(reinterpret_cast<const uint8_t*>(ct + at), c);
+            kv_load8<false>(reinterpret_cast<const uint8_t*>(st + at), s);
+            kv_load8<BF16>(src + (second ? at : c0 + half) * es, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float mine = __fmul_rn(x[8 * q + i], c[i]), other = __fmul_rn(o[i], s[i]);
+              x[8 * q + i] = second ? __fadd_rn(mine, other) : __fsub_rn(mine, other);
+            }
+          }
+        }
+      }
+    }
+    kv_rotate<G>(x);
+    if (!store) continue;
+    if (which == 0) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      uint4* const dst = reinterpret_cast<uint4*>(p.q_out + ((t * p.heads[0] + head) * D + 16 * b));
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      continue;
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max_nan(top, fabsf(x[i]));
+    const float g = sg[which - 1];
+    const uint32_t sb = e4m3x2(__fdiv_rn(__fdiv_rn(top, 6.0f), g), 0.0f) & 0xFFu;
+    const float sf = __fmul_rn(e4m3x2_to_f32(sb).x, g);
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = sf == 0.0f ? 0.0f : __fdiv_rn(x[i], sf);
+    int at;
+    uint8_t* const rec = p.cache + kv_record<D>(slot, head, p.kv_heads, p.page_units, at);
+    *reinterpret_cast<uint2*>(rec + (which == 1 ? 0 : R::kV) + at * (D / 2) + 8 * b) =
+        make_uint2(e2m1x8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]),
+                   e2m1x8(v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]));
+    rec[(which == 1 ? R::kKs : R::kVs) + at * kBlocks + b] = static_cast<uint8_t>(sb);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Reading back: the values of the tokens at `slots`, zeros where a slot is none.
+// ---------------------------------------------------------------------------
+struct KvReadParams {
+  const uint8_t* cache;
+  const int64_t* slots;
+  const float* kv_amax;
+  int64_t T, n_slots;
+  int page_units, kv_heads;
+  void *k, *v;  // [T, kv_heads, D]
+};
+
+template <int D, int G, bool BF16>
+__global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ KvReadParams p) {
+  using R = KvRecord<D>;
+  constexpr int kBlocks = D / 16;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t rows = p.T * p.kv_heads;
+  const int b = threadIdx.x % kBlocks;
+  const float sg[2] = {kv_global_scale(__ldg(p.kv_amax)), kv_global_scale(__ldg(p.kv_amax + 1))};
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * (256 / kBlocks); r0 < rows; r0 += static_cast<int64_t>(gridDim.x) * (256 / kBlocks)) {
+    const int64_t r = r0 + threadIdx.x / kBlocks;
+    const bool live = r < rows;
+    const int64_t t = live ? r / p.kv_heads : 0;
+    const int head = live ? static_cast<int>(r - t * p.kv_heads) : 0;
+    const int64_t slot = __ldg(p.slots + t);
+    const bool there = slot >= 0 && slot < p.n_slots;
+    int at;
+    const uint8_t* const rec = p.cache + kv_record<D>(there ? slot : 0, head, p.kv_heads, p.page_units, at);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      float x[16];
+      uint2 w = make_uint2(0, 0);
+      uint32_t sb = 0;
+      if (there) {
+        w = *reinterpret_cast<const uint2*>(rec + (which ? R::kV : 0) + at * (D / 2) + 8 * b);
+        sb = rec[(which ? R::kVs : R::kKs) + at * kBlocks + b];
+      }
+      const float sf = __fmul_rn(e4m3x2_to_f32(sb).x, sg[which]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 c = e2m1x2_to_f32((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+        x[2 * i] = __fmul_rn(c.x, sf);
+        x[2 * i + 1] = __fmul_rn(c.y, sf);
+      }
+      kv_rotate<G>(x);
+      if (!live) continue;
+      void* const dst = which ? p.v : p.k;
+      const int64_t to = r * D + 16 * b;
+      if constexpr (BF16) {
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+          o[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        uint4* const d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dst) + to);
+        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      } else {
+        float4* const d = reinterpret_cast<float4*>(static_cast<float*>(dst) + to);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+      }
+    }
+  }
+}
+
+}  // namespace hq

@@ -1,4 +1,4 @@
-// hq_torch.cpp -- the Python calls of the products and norms over torch tensors, in C++.
+// hq_torch.cpp -- the Python calls of the products, norms and caches over torch tensors, in C++.
 //
 // These calls take the GPU as little as 4 us (a token through the norms), and checking a dozen tensors,
 // allocating outputs and marshalling 25 arguments takes Python 10 to 30 us.  Here it is done through
@@ -15,6 +15,7 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <exception>
 #include <string>
 
@@ -46,7 +47,9 @@ std::string shape_text(Shape s) {
 const char* type_text(at::ScalarType t) {
   switch (t) {
     case at::kByte: return "torch.uint8";
+    case at::kChar: return "torch.int8";
     case at::kInt: return "torch.int32";
+    case at::kLong: return "torch.int64";
     case at::kFloat: return "torch.float32";
     case at::kBFloat16: return "torch.bfloat16";
     default: return "a type that is not supported";
@@ -289,6 +292,175 @@ PyObject* lora_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (xq, x_scales, wq, w_scales, out, out_dtype, stream)
+PyObject* gemm_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 7, [&] {
+    const at::Tensor &xq = cuda_tensor(a[0], "xq"), &wq = cuda_tensor(a[2], "wq");
+    if (xq.dim() != 2 || wq.dim() != 2) throw Refused("xq must be [M, K] and wq [N, K]");
+    const int index = static_cast<int>(xq.get_device());
+    const int64_t M = xq.size(0), K = xq.size(1), N = wq.size(0);
+    const auto* x = at_given<int8_t>(a[0], {M, K}, at::kChar, index, "xq");
+    const auto* xs = at_given<float>(a[1], {M}, at::kFloat, index, "x_scales");
+    const auto* w = at_given<int8_t>(a[2], {N, K}, at::kChar, index, "wq");
+    const auto* ws = at_given<float>(a[3], {N}, at::kFloat, index, "w_scales");
+    const Stream stream(a[6], index);
+    const at::Tensor out = output(a[4], a[5], {M, N}, xq, stream);
+    run(index, "hq_gemm_int8", [&] {
+      return hq_gemm_int8(x, xs, w, ws, M, N, K, out.data_ptr(), dtype_of(out.scalar_type()), stream.handle);
+    });
+    return wrap(out);
+  });
+}
+
+// ---- the paged cache -------------------------------------------------------------------------------
+
+long whole(PyObject* o) {
+  const long v = PyLong_AsLong(o);
+  if (v == -1 && PyErr_Occurred()) throw PythonError();
+  return v;
+}
+
+// uint8 [pages, kv_heads, page_size / 16, 18 D]
+struct Cache {
+  const at::Tensor& t;
+  int index;
+  int64_t pages, kv_heads, page_size, D;
+  explicit Cache(PyObject* o) : t(cuda_tensor(o, "cache")) {
+    if (t.dim() != 4 || t.scalar_type() != at::kByte || !t.is_contiguous() || t.size(3) % 18 != 0)
+      throw Refused("cache must be a contiguous uint8 tensor [pages, kv_heads, page_size / 16, 18 * D]");
+    index = static_cast<int>(t.get_device());
+    pages = t.size(0), kv_heads = t.size(1), page_size = 16 * t.size(2), D = t.size(3) / 18;
+  }
+};
+
+// [T, heads, D] with contiguous heads; ld: elements between tokens.
+struct Heads {
+  const at::Tensor* t;
+  int64_t ld;
+  Heads(PyObject* o, int64_t tokens, int64_t heads, const Cache& cache, const char* name) : t(tensor(o)) {
+    if (!t || t->dim() != 3 || (tokens >= 0 && t->size(0) != tokens) || (heads >= 0 && t->size(1) != heads) ||
+        t->size(2) != cache.D || !supported(t->scalar_type()) || !t->is_cuda() || t->get_device() != cache.index ||
+        t->stride(2) != 1 || (t->size(1) > 1 && t->stride(1) != cache.D))
+      throw Refused(std::string(name) + " must be a bfloat16 or float32 tensor [T, " +
+                    (heads >= 0 ? std::to_string(heads) : std::string("heads")) + ", " + std::to_string(cache.D) +
+                    "] on cuda:" + std::to_string(cache.index) + " with contiguous heads");
+    ld = t->size(0) > 1 ? t->stride(0) : t->size(1) * cache.D;
+  }
+};
+
+// (q, k, v, cos, sin, positions, slots, kv_amax, cache, group, interleaved, q_out, stream)
+PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&] {
+    const Cache cache(a[8]);
+    const Heads k(a[1], -1, cache.kv_heads, cache, "k");
+    const int64_t T = k.t->size(0);
+    const Heads v(a[2], T, cache.kv_heads, cache, "v");
+    const at::ScalarType type = k.t->scalar_type();
+    const void* pq = nullptr;
+    int64_t ld_q = 0, heads = 0;
+    if (a[0] != Py_None) {
+      const Heads q(a[0], T, -1, cache, "q");
+      if (q.t->scalar_type() != type) throw Refused("q, k and v must be of one type");
+      pq = q.t->const_data_ptr(), ld_q = q.ld, heads = q.t->size(1);
+    }
+    if (v.t->scalar_type() != type) throw Refused("q, k and v must be of one type");
+    const float *cos = nullptr, *sin = nullptr;
+    const int32_t* positions = nullptr;
+    int64_t rows = 0, rotary = 0;
+    if (a[3] != Py_None || a[4] != Py_None || a[5] != Py_None) {
+      const at::Tensor* c = tensor(a[3]);
+      if (!c || c->dim() != 2) throw Refused("cos, sin and positions are given together; cos must be [rows, rotary / 2]");
+      rows = c->size(0), rotary = 2 * c->size(1);
+      cos = at_given<float>(a[3], {rows, rotary / 2}, at::kFloat, cache.index, "cos");
+      sin = at_given<float>(a[4], {rows, rotary / 2}, at::kFloat, cache.index, "sin");
+      positions = at_given<int32_t>(a[5], {T}, at::kInt, cache.index, "positions");
+    }
+    const auto* slots = at_given<int64_t>(a[6], {T}, at::kLong, cache.index, "slots");
+    const auto* amax = at_given<float>(a[7], {2}, at::kFloat, cache.index, "kv_amax");
+    const int group = static_cast<int>(std::min(std::max(whole(a[9]), -1l), 257l));  // (others: refused by the library)
+    const int pairs = PyObject_IsTrue(a[10]);
+    if (pairs < 0) throw PythonError();
+    const Stream stream(a[12], cache.index);
+    at::Tensor out;
+    if (a[0] == Py_None) {
+      if (a[11] != Py_None) throw Refused("q_out without q");
+    } else {
+      out = a[11] == Py_None ? empty({T, heads, cache.D}, at::kBFloat16, cache.t, stream)
+                             : given(a[11], {T, heads, cache.D}, at::kBFloat16, cache.index, "q_out");
+    }
+    run(cache.index, "hq_kv_append_nvfp4", [&] {
+      return hq_kv_append_nvfp4(pq, ld_q, k.t->const_data_ptr(), k.ld, v.t->const_data_ptr(), v.ld, dtype_of(type), T, heads,
+                                cache.kv_heads, cache.D, cos, sin, rows, rotary, pairs, positions, slots, group, amax,
+                                addr(out), static_cast<uint8_t*>(cache.t.data_ptr()), cache.pages, cache.page_size,
+                                stream.handle);
+    });
+    return wrap(out);
+  });
+}
+
+// (cache, slots, kv_amax, group, out_dtype, k, v, stream)
+PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&] {
+    const Cache cache(a[0]);
+    const at::Tensor* s = tensor(a[1]);
+    if (!s || s->dim() != 1) throw Refused("slots must be a 1-D int64 tensor");
+    const int64_t T = s->size(0);
+    const auto* slots = at_given<int64_t>(a[1], {T}, at::kLong, cache.index, "slots");
+    const auto* amax = at_given<float>(a[2], {2}, at::kFloat, cache.index, "kv_amax");
+    const int group = static_cast<int>(std::min(std::max(whole(a[3]), -1l), 257l));
+    const Stream stream(a[7], cache.index);
+    const at::Tensor k = output(a[5], a[4], {T, cache.kv_heads, cache.D}, cache.t, stream);
+    const at::Tensor v = output(a[6], a[4], {T, cache.kv_heads, cache.D}, cache.t, stream);
+    if (k.scalar_type() != v.scalar_type()) throw Refused("k and v must be of one type");
+    run(cache.index, "hq_kv_read_nvfp4", [&] {
+      return hq_kv_read_nvfp4(static_cast<const uint8_t*>(cache.t.const_data_ptr()), cache.pages, cache.page_size,
+                              cache.kv_heads, cache.D, slots, T, amax, group, k.data_ptr(), v.data_ptr(),
+                              dtype_of(k.scalar_type()), stream.handle);
+    });
+    return tuple({wrap(k), wrap(v)});
+  });
+}
+
+// (q, cache, page_table, kv_len, q_start, kv_amax, scale, group, window, max_q, out, return_lse, stream)
+PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&] {
+    const Cache cache(a[1]);
+    const Heads q(a[0], -1, -1, cache, "q");
+    if (q.t->scalar_type() != at::kBFloat16) throw Refused("q must be bfloat16");
+    const int64_t T = q.t->size(0), heads = q.t->size(1);
+    const at::Tensor* table = tensor(a[2]);
+    if (!table || table->dim() != 2 || table->scalar_type() != at::kInt || !table->is_cuda() ||
+        table->get_device() != cache.index || (table->size(1) > 1 && table->stride(1) != 1))
+      throw Refused("page_table must be an int32 tensor [S, pages] on cuda:" + std::to_string(cache.index) +
+                    " with contiguous rows");
+    const int64_t S = table->size(0), pages = table->size(1), ld = S > 1 ? table->stride(0) : pages;
+    const auto* lens = at_given<int32_t>(a[3], {S}, at::kInt, cache.index, "kv_len");
+    const auto* starts = at_given<int32_t>(a[4], {S + 1}, at::kInt, cache.index, "q_start");
+    const auto* amax = at_given<float>(a[5], {2}, at::kFloat, cache.index, "kv_amax");
+    const double scale = PyFloat_AsDouble(a[6]);
+    if (scale == -1.0 && PyErr_Occurred()) throw PythonError();
+    const int group = static_cast<int>(std::min(std::max(whole(a[7]), -1l), 257l));
+    const long window = whole(a[8]), max_q = whole(a[9]);
+    if (window < 0) throw Refused("window must be 0 (none) or positive");
+    const int with_lse = PyObject_IsTrue(a[11]);
+    if (with_lse < 0) throw PythonError();
+    const Stream stream(a[12], cache.index);
+    const at::Tensor out = a[10] == Py_None ? empty({T, heads, cache.D}, at::kBFloat16, cache.t, stream)
+                                            : given(a[10], {T, heads, cache.D}, at::kBFloat16, cache.index, "out");
+    at::Tensor lse;
+    if (with_lse) lse = empty({T, heads}, at::kFloat, cache.t, stream);
+    const at::Tensor work = workspace(hq_kv_attention_workspace_bytes(heads, cache.kv_heads, cache.D), cache.t, stream);
+    run(cache.index, "hq_kv_attention_nvfp4", [&] {
+      return hq_kv_attention_nvfp4(q.t->const_data_ptr(), q.ld, T, heads, static_cast<const uint8_t*>(cache.t.const_data_ptr()),
+                                   cache.pages, cache.page_size, cache.kv_heads, cache.D,
+                                   static_cast<const int32_t*>(table->const_data_ptr()), ld, pages, lens, starts, S,
+                                   max_q < 0 ? T : max_q, amax, static_cast<float>(scale), window, group, out.data_ptr(),
+                                   static_cast<float*>(addr(lse)), addr(work), stream.handle);
+    });
+    return with_lse ? tuple({wrap(out), wrap(lse)}) : wrap(out);
+  });
+}
+
 // ---- norms ------------------------------------------------------------------------------------------
 
 const at::Tensor& norm_input(PyObject* o, const char* name) {
@@ -451,12 +623,16 @@ PyMethodDef methods[] = {
     HQ_METHOD("grouped_wgrad_mxfp4", grouped_wgrad<true>),
     HQ_METHOD("lora_gemm_nvfp4", lora_gemm<false>),
     HQ_METHOD("lora_gemm_mxfp4", lora_gemm<true>),
+    HQ_METHOD("gemm_int8", gemm_int8),
+    HQ_METHOD("kv_append", kv_append),
+    HQ_METHOD("kv_read", kv_read),
+    HQ_METHOD("kv_attention", kv_attention),
     HQ_METHOD("block_norm", block_norm),
     HQ_METHOD("block_norm_bwd", block_norm_bwd),
     {nullptr, nullptr, 0, nullptr},
 };
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", "The products and norms of libhq over torch tensors.", -1,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", "The products, norms and caches of libhq over torch tensors.", -1,
                       methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -500,6 +500,103 @@ HQ_API hq_status hq_block_norm_bwd(const void* dh_out, int64_t ld_dh, const void
 /* Bytes of hq_block_norm_bwd's workspace (-1 for sizes it refuses). */
 HQ_API int64_t hq_block_norm_bwd_workspace_bytes(int64_t M, int64_t D);
 
+/*
+ * hq_gemm_int8 -- the product that reads what hq_rotate_quant_int8 writes: INT8 codes with a scale per token and per
+ * channel.
+ *   out[m, n] = (sum_k xq[m, k] wq[n, k]) * x_scales[m] * w_scales[n]
+ *   The sum is exact while its partial sums stay below 2^24 in magnitude (fp32 sums of exact products beyond); then
+ *   two fp32 products in this order and one rounding to out_dtype.
+ *
+ *   xq int8 [M, K], x_scales float [M]: activations; wq int8 [N, K], w_scales float [N]: weights, rotated like them.
+ *   Rows contiguous, xq and wq 16-byte aligned.  K a multiple of 16 below 2^17; K == 0 gives zeros.
+ *   out [M, N] of out_dtype, contiguous, aligned to its element.
+ */
+HQ_API hq_status hq_gemm_int8(const int8_t* xq, const float* x_scales, const int8_t* wq,
+                              const float* w_scales, int64_t M, int64_t N, int64_t K, void* out,
+                              hq_dtype out_dtype, hq_stream stream);
+
+/*
+ * A paged NVFP4 cache of keys and values.
+ *
+ *   cache : uint8 [pages][kv_heads][page_size / 16][18 D], 16-byte aligned, owned by the caller.  A record of 18 D bytes
+ *           holds 16 tokens of a head: K codes [16, D/2], V codes [16, D/2], K scales [16, D/16], V scales [16, D/16],
+ *           codes and E4M3 scales as hq_rotate_quant_nvfp4 writes them.  D is 64, 128 or 256; page_size a multiple
+ *           of 16.  Any contents are allowed where no token has been stored.
+ *   slot  : int64, page * page_size + place in the page.
+ *   kv_amax : 2 floats on the device, the amax of K and of V that stand behind s_global (amax / 2688, as in
+ *           hq_rotate_quant_nvfp4).  They are kept with the cache: every call on it takes the same two.  Blocks larger than
+ *           they allow saturate.
+ *   group : rotation of each head's channels, as in hq_rotate_quant_nvfp4; 256 needs D == 256.  q and K are rotated alike,
+ *           so scores do not change; V is rotated and the attention's output rotated back.
+ *   Each launch may start while the kernel before it on the stream ends; it waits for that kernel before it reads.
+ */
+
+/* Bytes of a page: kv_heads * page_size / 16 * 18 D (-1 for sizes that the calls refuse). */
+HQ_API int64_t hq_kv_page_bytes(int64_t page_size, int64_t kv_heads, int64_t D);
+
+/*
+ * hq_kv_append_nvfp4 -- the way of T tokens into the cache, with the position rotation on it.
+ *   q, k : pairs of channels (a, b) -> (a cos - b sin, b cos + a sin), each product and sum rounded to fp32; pair i is
+ *          channels i and i + rotary/2, or 2i and 2i + 1 (interleaved); channels from `rotary` on stay.
+ *   then q, k, v: y = x . H_group / sqrt(group) (fp32 butterfly); q_out = y rounded to bf16; k and v quantized as
+ *          hq_rotate_quant_nvfp4 with amax = kv_amax[0], kv_amax[1], and stored at the token's slot.
+ *
+ *   q [T, q_heads, D], k, v [T, kv_heads, D] of dtype: heads contiguous, ld_* elements between tokens, 16-byte aligned
+ *          tokens (parts of one fused projection qualify).  q_heads == 0: no queries.
+ *   cos, sin : float [table_rows, rotary/2], 16-byte aligned.  rotary: a multiple of 16 up to D, 0 for none.
+ *   positions : int32 [T] on the device, rows of the tables (others are clamped to them).
+ *   slots : int64 [T] on the device; a token whose slot is negative or behind the last page is not stored.  Two
+ *          tokens with one slot leave it with parts of either.
+ *   q_out : bf16 [T, q_heads, D], contiguous, 16-byte aligned; may not overlap the inputs.
+ */
+HQ_API hq_status hq_kv_append_nvfp4(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                                    int64_t ld_v, hq_dtype dtype, int64_t T, int64_t q_heads,
+                                    int64_t kv_heads, int64_t D, const float* cos, const float* sin,
+                                    int64_t table_rows, int64_t rotary, int interleaved,
+                                    const int32_t* positions, const int64_t* slots, int group,
+                                    const float* kv_amax, void* q_out, uint8_t* cache, int64_t pages,
+                                    int64_t page_size, hq_stream stream);
+
+/*
+ * hq_kv_read_nvfp4 -- the values of cached tokens (to hand a prefix on, or to check): k, v [T, kv_heads, D] of
+ * out_dtype, contiguous, 16-byte aligned; code * (scale * s_global) in fp32, then the rotation by `group` again (0:
+ * as stored), one rounding.  Tokens without a slot (negative, behind the last page) are zeros.
+ */
+HQ_API hq_status hq_kv_read_nvfp4(const uint8_t* cache, int64_t pages, int64_t page_size, int64_t kv_heads,
+                                  int64_t D, const int64_t* slots, int64_t T, const float* kv_amax,
+                                  int group, void* k, void* v, hq_dtype out_dtype, hq_stream stream);
+
+/*
+ * hq_kv_attention_nvfp4 -- causal attention of S sequences over the cache.
+ *   Sequence s has the queries q_start[s] .. q_start[s + 1] - 1, the last of its kv_len[s] tokens: its i-th of n
+ *   queries sees the keys j <= p = kv_len[s] - n + i, with a window only the `window` last of them (j > p - window).
+ *   out = (softmax(scale q K^T) V) . H_group / sqrt(group);  query head h reads key head h / (q_heads / kv_heads).
+ *   lse = the natural logarithm of the sum of exp(scale q K^T).  A query without keys gets out = 0, lse = -inf.
+ *   Scores are exact up to their fp32 sums; weights are carried in 11 bits into sums in fp32; one rounding to bf16.
+ *
+ *   q, out : bf16 [T, q_heads, D]; q as hq_kv_append_nvfp4 leaves it, ld_q elements between tokens, 16-byte aligned
+ *          tokens; out contiguous, 16-byte aligned.  Rows of no sequence are not written.  q_heads a multiple of
+ *          kv_heads.
+ *   page_table : int32 [S, table_pages] on the device, rows ld_table apart: page of the tokens page_size * i .. of the
+ *          sequence (others than 0 .. pages - 1 are clamped).  Entries behind a sequence's last page are not read.
+ *   kv_len int32 [S], q_start int32 [S + 1] on the device, clamped to table_pages * page_size and to 0 .. T.
+ *   max_q : the most queries of a sequence, as far as the host knows (T is always right).  It chooses the kernel;
+ *          the result is defined for any value.
+ *   window : 0 for none.    lse : float [T, q_heads], or NULL.
+ *   workspace : hq_kv_attention_workspace_bytes(q_heads, kv_heads, D) bytes, 16-byte aligned; contents need no
+ *          preparation.  Calls that may run at the same time need different ones.
+ */
+HQ_API hq_status hq_kv_attention_nvfp4(const void* q, int64_t ld_q, int64_t T, int64_t q_heads,
+                                       const uint8_t* cache, int64_t pages, int64_t page_size,
+                                       int64_t kv_heads, int64_t D, const int32_t* page_table,
+                                       int64_t ld_table, int64_t table_pages, const int32_t* kv_len,
+                                       const int32_t* q_start, int64_t S, int64_t max_q,
+                                       const float* kv_amax, float scale, int64_t window, int group,
+                                       void* out, float* lse, void* workspace, hq_stream stream);
+
+/* Bytes of hq_kv_attention_nvfp4's workspace (-1 for sizes it refuses). */
+HQ_API int64_t hq_kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t D);
+
 /* Human-readable name of a status code (static storage). */
 HQ_API const char* hq_status_string(hq_status status);
 
