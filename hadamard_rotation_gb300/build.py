@@ -21,7 +21,8 @@ SOURCES = [os.path.join(CSRC, "hq.cu"), os.path.join(CSRC, "hq_int8.cu"),
            os.path.join(CSRC, "hq_gemm8.cu"), os.path.join(CSRC, "hq_kv.cu"),
            os.path.join(CSRC, "hq_smem.cu"), os.path.join(CSRC, "hq_host.cu"), os.path.join(CSRC, "hq_noalloc.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "hq_kernels.cuh"), os.path.join(CSRC, "hq_int8.cuh"),
-                  os.path.join(CSRC, "hq_gemm.cuh"), os.path.join(CSRC, "hq_norm.cuh"),
+                  os.path.join(CSRC, "hq_gemm.cuh"), os.path.join(CSRC, "hq_tcgen05.cuh"),
+                  os.path.join(CSRC, "hq_tensor_map.h"), os.path.join(CSRC, "hq_norm.cuh"),
                   os.path.join(CSRC, "hq_gemm8.cuh"), os.path.join(CSRC, "hq_kv.cuh"),
                   os.path.join(CSRC, "hq_kv_attend.cuh"),
                   os.path.join(CSRC, "hq_internal.h"),

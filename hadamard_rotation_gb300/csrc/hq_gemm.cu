@@ -7,34 +7,19 @@
 #include "hq.h"
 #include "hq_gemm.cuh"
 #include "hq_internal.h"
+#include "hq_tensor_map.h"
 
 namespace {
 
 using hq::cuda_fail;
+using hq::encode_out;
+using hq::encode_tiled;
+using hq::EncodeTiledFn;
+using hq::store_bytes;
 using hq::GemmKind;
 using hq::GemmParams;
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// cuTensorMapEncodeTiled through the runtime's driver entry points (the library does not link
-// the driver library).
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-  static const EncodeTiledFn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      return static_cast<EncodeTiledFn>(nullptr);
-    }
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  return fn;
-}
 
 // Codes [groups, rows, row_bytes] in boxes of box_rows rows x 128 bytes, 128-byte swizzle; what a
 // box reaches past the rows of its group or past a row's end reads as code 0.
@@ -52,14 +37,6 @@ bool encode_codes(CUtensorMap* map, const uint8_t* q, int64_t row_bytes, int64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Bytes per store into rows of n elements at `out`: the alignment that every row has, up to 16.
-int store_bytes(const void* out, int64_t n, hq_dtype dt) {
-  const int64_t es = dt == HQ_F32 ? 4 : 2;
-  int v = 16;
-  while (n * es % v || !aligned(out, v)) v /= 2;
-  return v;
-}
-
 // Scale tiles [row_tiles][k_tiles] of 512 bytes, as words: boxes of `box` tiles along k, `box_rows` of rows.
 bool encode_scales(CUtensorMap* map, const uint8_t* s, int64_t k_tiles, int64_t row_tiles, int box, int box_rows) {
   const EncodeTiledFn fn = encode_tiled();
@@ -69,19 +46,6 @@ bool encode_scales(CUtensorMap* map, const uint8_t* s, int64_t k_tiles, int64_t 
   const cuuint32_t dim[3] = {128, static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(box_rows)}, step[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(s), size, stride, dim, step,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// bf16 output [groups, rows, n], rows contiguous, in boxes of 32 rows x 64 elements, 128-byte swizzle.
-bool encode_out(CUtensorMap* map, void* out, int64_t n, int64_t rows, int64_t groups) {
-  const EncodeTiledFn fn = encode_tiled();
-  if (!fn) return false;
-  const cuuint64_t size[3] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(rows),
-                              static_cast<cuuint64_t>(groups)};
-  const cuuint64_t stride[2] = {static_cast<cuuint64_t>(n * 2), static_cast<cuuint64_t>(n * rows * 2)};
-  const cuuint32_t box[3] = {64, 32, 1}, step[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, out, size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -7,6 +7,7 @@
 #include "hq.h"
 #include "hq_gemm8.cuh"
 #include "hq_internal.h"
+#include "hq_tensor_map.h"
 
 namespace {
 
@@ -16,6 +17,80 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 
 constexpr int64_t kMaxExtent = (int64_t{1} << 31) - 1024;  // sizes and row indexes are ints in the kernel
 constexpr int64_t kMaxK = int64_t{1} << 17;
+
+// Codes [rows, K] in boxes of box_rows rows x 128 codes, 128-byte swizzle; past the last row or a row's end: 0.
+bool encode_rows(CUtensorMap* map, const int8_t* q, int64_t K, int64_t rows, int box_rows) {
+  const hq::EncodeTiledFn fn = hq::encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t size[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(K)};
+  const cuuint32_t box[2] = {hq::kGemm8Block, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(q), size, stride, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a product is cut: wide tiles by pairs of CTAs or narrow ones, and how many CTAs share a narrow tile's sum.
+struct Plan {
+  bool wide;
+  int splits;
+  int tiles_a, tiles_b, width;
+};
+
+Plan plan_of(int64_t M, int64_t N, int64_t K, int sms) {
+  const int64_t stages = (K + hq::kGemm8Block - 1) / hq::kGemm8Block;
+  Plan best = {};
+  int64_t least = INT64_MAX;
+  for (int wide = 0; wide < 2; ++wide) {
+    const int64_t T = wide ? 256 : 64, lanes = wide ? 256 : 128, unit = wide ? 32 : 16;
+    const int64_t parts = (M + T - 1) / T, width = ((M + parts - 1) / parts + unit - 1) / unit * unit;
+    const int64_t tiles_a = (N + lanes - 1) / lanes, tiles = tiles_a * parts;
+    for (int s = 1; s <= (wide ? 1 : hq::kGemm8MaxSplits); s *= 2) {
+      if (s > 1 && stages < 2 * s) break;
+      const int64_t places = sms / ((wide ? 2 : 1) * s), waves = (tiles + places - 1) / places;
+      // cycles of a stage, of a tile's end, of a launch's start
+      const int64_t stage = wide ? 4 * width + 60 : 330, end = wide ? 3500 : s > 1 ? 4500 : 1200, start = 4000;
+      const int64_t cost = waves * ((stages + s - 1) / s * stage + end) + start;
+      if (cost < least) {
+        least = cost;
+        best = {wide != 0, s, static_cast<int>(tiles_a), static_cast<int>(parts), static_cast<int>(width)};
+      }
+    }
+  }
+  return best;
+}
+
+template <bool WIDE, bool SPLIT>
+hq_status launch(hq::Gemm8Params p, const Plan& plan, const int8_t* x, const int8_t* w, int sms, cudaStream_t stream) {
+  using S = hq::Gemm8Shape<WIDE>;
+  auto kernel = hq::k_gemm8<WIDE, SPLIT>;
+  const size_t smem = S::kSmemBytes + 1024;
+  // (Before the tensor maps: encoding one fails in a thread that has made no CUDA call yet, and this makes the context
+  // current there.)
+  cudaError_t e = hq::allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
+  if (e != cudaSuccess) return cuda_fail(e);
+  p.box_b = plan.width / S::kCtas;
+  CUtensorMap mw, mx, mo = {};
+  if (!encode_rows(&mw, w, p.K, p.N, 128) || !encode_rows(&mx, x, p.K, p.M, p.box_b)) return cuda_fail(cudaErrorInvalidValue);
+  p.out_tma = !p.out_f32 && p.out_vec == 16 && hq::encode_out(&mo, p.out, p.N, p.M, 1);
+  cudaLaunchConfig_t cfg = {};
+  const int64_t ctas = S::kCtas * plan.splits, tiles = static_cast<int64_t>(p.tiles_a) * p.tiles_b, places = sms / ctas;
+  cfg.gridDim = dim3(static_cast<unsigned>((SPLIT || tiles < places ? tiles : places) * ctas));
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, mw, mx, mo, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? HQ_OK : cuda_fail(e);
+}
 
 }  // namespace
 
@@ -32,31 +107,35 @@ extern "C" hq_status hq_gemm_int8(const int8_t* xq, const float* x_scales, const
                                   int64_t M, int64_t N, int64_t K, void* out, hq_dtype out_dtype, hq_stream stream) {
   if (out_dtype != HQ_F32 && out_dtype != HQ_BF16) return HQ_ERR_DTYPE;
   if (M < 0 || N < 0 || K < 0 || K % 16 != 0 || K >= kMaxK || M > kMaxExtent || N > kMaxExtent) return HQ_ERR_SHAPE;
+  if ((M + 63) / 64 * ((N + 127) / 128) > kMaxExtent) return HQ_ERR_SHAPE;  // tiles
   if (M == 0 || N == 0) return HQ_OK;
   if (!out || !x_scales || !w_scales || (K > 0 && (!xq || !wq))) return HQ_ERR_NULL;
   if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) ||
       !aligned(out, out_dtype == HQ_F32 ? 4 : 2))
     return HQ_ERR_ALIGN;
+  const int es = out_dtype == HQ_F32 ? 4 : 2;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (K == 0) {
+    const cudaError_t e = cudaMemsetAsync(out, 0, static_cast<size_t>(M * N) * es, cs);
+    return e == cudaSuccess ? HQ_OK : cuda_fail(e);
+  }
+  int sms = 0;
+  const cudaError_t e = hq::sm_count(&sms);
+  if (e != cudaSuccess) return cuda_fail(e);
+  const Plan plan = plan_of(M, N, K, sms);
   hq::Gemm8Params p = {};
-  p.x = xq;
-  p.w = wq;
   p.xs = x_scales;
   p.ws = w_scales;
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N);
   p.K = static_cast<int>(K);
+  p.tiles_a = plan.tiles_a;
+  p.tiles_b = plan.tiles_b;
+  p.width = plan.width;
   p.out = out;
   p.out_f32 = out_dtype == HQ_F32;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((N + 63) / 64), static_cast<unsigned>((M + 63) / 64));
-  cfg.blockDim = dim3(256);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, hq::k_gemm8, p);
-  if (e == cudaSuccess) e = cudaGetLastError();
-  return e == cudaSuccess ? HQ_OK : cuda_fail(e);
+  p.out_vec = hq::store_bytes(out, N, out_dtype);
+  return plan.wide         ? launch<true, false>(p, plan, xq, wq, sms, cs)
+         : plan.splits > 1 ? launch<false, true>(p, plan, xq, wq, sms, cs)
+                           : launch<false, false>(p, plan, xq, wq, sms, cs);
 }
