@@ -18,15 +18,16 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 constexpr int64_t kMaxExtent = (int64_t{1} << 31) - 1024;  // sizes and row indexes are ints in the kernel
 constexpr int64_t kMaxK = int64_t{1} << 17;
 
-// Codes [rows, K] in boxes of box_rows rows x 128 codes, 128-byte swizzle; past the last row or a row's end: 0.
-bool encode_rows(CUtensorMap* map, const int8_t* q, int64_t K, int64_t rows, int box_rows) {
+// Codes [rows, K] in boxes of box_rows rows x `block` codes (64, 128), swizzle of as many bytes; past the last row or a row's end: 0.
+bool encode_rows(CUtensorMap* map, const int8_t* q, int64_t K, int64_t rows, int box_rows, int block) {
   const hq::EncodeTiledFn fn = hq::encode_tiled();
   if (!fn) return false;
   const cuuint64_t size[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
   const cuuint64_t stride[1] = {static_cast<cuuint64_t>(K)};
-  const cuuint32_t box[2] = {hq::kGemm8Block, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(block), static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(q), size, stride, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, block == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -38,7 +39,7 @@ struct Plan {
 };
 
 Plan plan_of(int64_t M, int64_t N, int64_t K, int sms) {
-  const int64_t stages = (K + hq::kGemm8Block - 1) / hq::kGemm8Block;
+  const int64_t stages = (K + 127) / 128;  // (of 128 codes)
   Plan best = {};
   int64_t least = INT64_MAX;
   for (int wide = 0; wide < 2; ++wide) {
@@ -71,7 +72,7 @@ hq_status launch(hq::Gemm8Params p, const Plan& plan, const int8_t* x, const int
   if (e != cudaSuccess) return cuda_fail(e);
   p.box_b = plan.width / S::kCtas;
   CUtensorMap mw, mx, mo = {};
-  if (!encode_rows(&mw, w, p.K, p.N, 128) || !encode_rows(&mx, x, p.K, p.M, p.box_b)) return cuda_fail(cudaErrorInvalidValue);
+  if (!encode_rows(&mw, w, p.K, p.N, 128, S::kBlock) || !encode_rows(&mx, x, p.K, p.M, p.box_b, S::kBlock)) return cuda_fail(cudaErrorInvalidValue);
   p.out_tma = !p.out_f32 && p.out_vec == 16 && hq::encode_out(&mo, p.out, p.N, p.M, 1);
   cudaLaunchConfig_t cfg = {};
   const int64_t ctas = S::kCtas * plan.splits, tiles = static_cast<int64_t>(p.tiles_a) * p.tiles_b, places = sms / ctas;

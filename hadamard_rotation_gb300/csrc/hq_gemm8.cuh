@@ -7,14 +7,14 @@
 // are exact, and so is the fp32 sum while it stays below 2^24.
 //
 // The weights' channels are the M side of the instruction and lie in tensor memory; the tokens are its N side and lie in
-// shared memory.  Both come from global memory as they are (TMA, 128 codes of a row, 128-byte swizzle), are read
+// shared memory.  Both come from global memory as they are (TMA, 64 or 128 codes of a row, swizzled), are read
 // a row per thread, widened, and written: channels by tcgen05.st, tokens by 16-byte stores in the swizzle that the
 // instruction reads.  Widening: a code with its sign bit flipped, as the low byte of f16 0x64.., is 1024 + 128 +
 // code; one subtraction of pairs gives code.
 //
 // Large products are taken by pairs of CTAs (WIDE, cta_group::2) in tiles of 256 channels x up to 256 tokens: each CTA
-// widens 128 rows of each side for 4.2 M products of 16 bits, and an SM's shared memory moves 128 KB in the 1024 cycles
-// of a stage, of 131 KB that it can.  With the channels in shared memory too it would be 192.
+// widens 128 rows of each side, and its shared memory moves 64 KB in the 512 cycles of a stage, of 66 KB that it can.
+// With the channels in shared memory too it would be 96.
 // Few tokens: single CTAs, 128 channels x up to 64 tokens; with fewer tiles than SMs the CTAs of a cluster share the
 // summed axis (SPLIT) and add their parts through distributed shared memory in a fixed order.
 //
@@ -22,9 +22,9 @@
 //   warp 0         TMA
 //   warp 1         issues the products
 //   warp 2         allocates tensor memory
-//   warps 4..7     widen the channels (the warp's quarter of the lanes)
-//   warps 8..11    widen the tokens
-//   warps 12..     epilogue, groups of four warps: tensor memory -> registers -> scales -> shared memory -> global
+//   sets of 8      four warps widen the channels (a quarter of the lanes each), four the tokens; the sets take stages in
+//                  turn, for a stage's way through one warp is mostly latency
+//   the last       epilogue, groups of four warps: tensor memory -> registers -> scales -> shared memory -> global
 #pragma once
 
 #include <cuda_fp16.h>
@@ -45,24 +45,30 @@ struct Gemm8Params {
   int out_vec;  // bytes per store: what the rows of out are aligned to, up to 16
 };
 
-constexpr int kGemm8Block = 128;  // summed codes per stage
 constexpr int kGemm8MaxSplits = 8;
 
 template <bool WIDE>
 struct Gemm8Shape {
   static constexpr int kCtas = WIDE ? 2 : 1;
   static constexpr int T = WIDE ? 256 : 64;     // tokens of a tile, at most
+  static constexpr int kBlock = WIDE ? 64 : 128;  // summed codes per stage
   static constexpr int kRowsB = T / kCtas;      // in a CTA
   static constexpr int kTileLanes = 128 * kCtas;
-  static constexpr int kRawA = 128 * 128, kRawB = kRowsB * 128, kRawBytes = kRawA + kRawB;
-  static constexpr int kRaw = WIDE ? 3 : 5;     // stages of codes
-  static constexpr int kWideBytes = kRowsB * 256;
-  static constexpr int kWides = WIDE ? 3 : 4;   // stages of widened operands
+  static constexpr int kRawA = 128 * kBlock, kRawB = kRowsB * kBlock, kRawBytes = kRawA + kRawB;
+  static constexpr int kRaw = 6;                // stages of codes
+  static constexpr int kWideBytes = kRowsB * kBlock * 2;
+  static constexpr int kWides = WIDE ? 6 : 3;   // stages of widened operands
   static constexpr int kAccs = WIDE ? 1 : 2;
-  static constexpr int kColA = kAccs * T;       // the channels' columns of tensor memory: 64 per stage
-  static_assert(kColA + 64 * kWides <= 512, "tensor memory has 512 columns");
+  static constexpr int kColA = kAccs * T;       // the channels' columns of tensor memory: kBlock / 2 per stage
+  static_assert(kColA + kBlock / 2 * kWides <= 512, "tensor memory has 512 columns");
   static constexpr int kEpilogues = WIDE ? 2 : 1;
-  static constexpr int kThreads = 32 * (12 + 4 * kEpilogues);
+  // Sets of eight warps (four for the channels, four for the tokens) that widen stages in turn.
+  static constexpr int kSets = WIDE ? 2 : 3;
+  // A place is used by the same set each time.  Otherwise a set could come to a place two uses ahead of the copy that
+  // another set still waits for, where the parity says that its own has landed.
+  static_assert(kRaw % kSets == 0 && kWides % kSets == 0, "a place belongs to one set");
+  static constexpr int kEpilogueWarp = 4 + 8 * kSets;
+  static constexpr int kThreads = 32 * (kEpilogueWarp + 4 * kEpilogues);
   static constexpr int kWideAt = kRaw * kRawBytes, kOutAt = kWideAt + kWides * kWideBytes;
   static constexpr int kSmemBytes = kOutAt + kEpilogues * kOutBytes;
   static_assert(kSmemBytes + 1024 + 4096 <= 227 * 1024, "a CTA has 227 KB");
@@ -71,8 +77,8 @@ struct Gemm8Shape {
 };
 
 struct Gemm8Bars {
-  uint64_t raw_full[5], raw_empty[5];
-  uint64_t wide_full[4], wide_empty[4];
+  uint64_t raw_full[6], raw_empty[6];
+  uint64_t wide_full[6], wide_empty[6];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   float xs[2][256];  // a tile's token scales, by epilogue group
@@ -110,9 +116,11 @@ __device__ __forceinline__ uint2 widen8(uint32_t w) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// Sixteen codes, 16-byte piece `j` of row r of a stage.
+// Sixteen codes, 16-byte piece `j` of row r of a stage: rows of BLOCK bytes, swizzled by the copy.
+template <int BLOCK>
 __device__ __forceinline__ void widen_piece(const uint8_t* rows, int r, int j, uint32_t (&v)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(rows + r * 128 + ((j ^ (r & 7)) << 4));
+  const int at = BLOCK == 128 ? j ^ (r & 7) : j ^ ((r >> 1) & 3);
+  const uint4 w = *reinterpret_cast<const uint4*>(rows + r * BLOCK + (at << 4));
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__((Gemm8Shape<WIDE>::kThreads), 1)
   const int group = kCtas * splits, step = static_cast<int>(gridDim.x) / group, first = static_cast<int>(blockIdx.x) / group;
   const int tiles = p.tiles_a * p.tiles_b;
   // this CTA's part of the summed axis, in stages
-  const int all = (p.K + kGemm8Block - 1) / kGemm8Block;
+  const int all = (p.K + S::kBlock - 1) / S::kBlock;
   const int kb0 = all * part_k / splits, kb1 = all * (part_k + 1) / splits;
   bool ok = true;
 
@@ -237,9 +245,9 @@ __global__ void __launch_bounds__((Gemm8Shape<WIDE>::kThreads), 1)
         if (!ok) break;
         const uint32_t full = smem_addr(&bars.raw_full[ring.s]), st = smem_addr(smem) + ring.s * S::kRawBytes;
         if (elect_one()) {
-          mbar_expect_tx(full, S::kRawA + p.box_b * 128);
-          tma_tile2<false>(st, &map_w, kb * kGemm8Block, a0, full);
-          tma_tile2<false>(st + S::kRawA, &map_x, kb * kGemm8Block, b0, full);
+          mbar_expect_tx(full, S::kRawA + p.box_b * S::kBlock);
+          tma_tile2<false>(st, &map_w, kb * S::kBlock, a0, full);
+          tma_tile2<false>(st + S::kRawA, &map_x, kb * S::kBlock, b0, full);
         }
         __syncwarp();
         ++fills;
@@ -265,10 +273,10 @@ __global__ void __launch_bounds__((Gemm8Shape<WIDE>::kThreads), 1)
         if (!ok) break;
         umma_fence_after();
         if (elect_one()) {
-          const uint32_t a = tmem + S::kColA + 64 * ring.s;
+          const uint32_t a = tmem + S::kColA + S::kBlock / 2 * ring.s;
           const uint64_t b = b_desc + ring.s * (S::kWideBytes >> 4);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)  // 16 codes each; four in a row of the swizzle
+          for (int j = 0; j < S::kBlock / 16; ++j)  // 16 codes each; four in a row of the swizzle
             umma_f16_ts<WIDE>(d, a + 8 * j, b + (j / 4) * (S::kRowsB * 128 >> 4) + 2 * (j % 4), idesc, kb > kb0 || j > 0);
           umma_commit<WIDE>(smem_addr(&bars.wide_empty[ring.s]));
         }
@@ -288,28 +296,33 @@ __global__ void __launch_bounds__((Gemm8Shape<WIDE>::kThreads), 1)
       __syncwarp();
       mbar_wait(smem_addr(&bars.drain), 0);
     }
-  } else if (warp >= 4 && warp < 12) {
-    const bool channels = warp < 8;
+  } else if (warp >= 4 && warp < S::kEpilogueWarp) {
+    const int set = (warp - 4) / 8;
+    const bool channels = ((warp - 4) & 4) == 0;
     // (64 tokens at most: two threads a row, each half of a stage's codes)
     const int r = (channels || WIDE ? warp & 3 : warp & 1) * 32 + lane, half0 = channels || WIDE ? 0 : (warp & 2) * 2;
-    constexpr int kPieces = WIDE ? 8 : 4;
+    constexpr int kPieces = S::kBlock / 16, kPiecesB = WIDE ? kPieces : kPieces / 2;
     GemmRing raw, ring;
+    int turn = 0;
     for (int tile = first; ok && tile < tiles; tile += step) {
       const Gemm8Tile t = gemm8_tile<WIDE>(p, tile);
       const int rows_b = t.n / kCtas;
       const bool mine = channels || r < rows_b;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb, raw.next(S::kRaw), ring.next(S::kWides)) {
+        const bool another = turn != set;
+        if (++turn == S::kSets) turn = 0;
+        if (another) continue;
         ok = warp_wait(smem_addr(&bars.raw_full[raw.s]), raw.phase) && warp_wait(smem_addr(&bars.wide_empty[ring.s]), ring.phase ^ 1);
         if (!ok) break;
         const uint8_t* const rows = smem + raw.s * S::kRawBytes + (channels ? 0 : S::kRawA);
         if (channels) {
           umma_fence_after();
-          const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + S::kColA + 64 * ring.s;
+          const uint32_t to = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + S::kColA + S::kBlock / 2 * ring.s;
 #pragma unroll
-          for (int j = 0; j < 8; j += 2) {
+          for (int j = 0; j < kPieces; j += 2) {
             uint32_t v[16];
-            widen_piece(rows, r, j, *reinterpret_cast<uint32_t(*)[8]>(v));
-            widen_piece(rows, r, j + 1, *reinterpret_cast<uint32_t(*)[8]>(v + 8));
+            widen_piece<S::kBlock>(rows, r, j, *reinterpret_cast<uint32_t(*)[8]>(v));
+            widen_piece<S::kBlock>(rows, r, j + 1, *reinterpret_cast<uint32_t(*)[8]>(v + 8));
             tmem_store_nowait(to + 8 * j, v);
           }
           tmem_store_wait();
@@ -317,10 +330,10 @@ __global__ void __launch_bounds__((Gemm8Shape<WIDE>::kThreads), 1)
         } else if (mine) {
           uint8_t* const to = wide + ring.s * S::kWideBytes + r * 128;
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) {
+          for (int i = 0; i < kPiecesB; ++i) {
             const int j = half0 + i, at = 2 * (i % 4);
             uint32_t v[8];
-            widen_piece(rows, r, j, v);
+            widen_piece<S::kBlock>(rows, r, j, v);
             uint8_t* const half = to + (j / 4) * (S::kRowsB * 128);
             *reinterpret_cast<uint4*>(half + ((at ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
             *reinterpret_cast<uint4*>(half + (((at + 1) ^ (r & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
@@ -333,12 +346,10 @@ __global__ void __launch_bounds__((Gemm8Shape<WIDE>::kThreads), 1)
           if (rank) mbar_arrive_cluster(cluster_addr(smem_addr(&bars.wide_full[ring.s]), 0));
           else mbar_arrive(smem_addr(&bars.wide_full[ring.s]));
         }
-        raw.next(S::kRaw);
-        ring.next(S::kWides);
       }
     }
-  } else if (warp >= 12) {
-    const int part = (warp - 12) / 4, quarter = warp & 3, tid = threadIdx.x & 127;
+  } else if (warp >= S::kEpilogueWarp) {
+    const int part = (warp - S::kEpilogueWarp) / 4, quarter = warp & 3, tid = threadIdx.x & 127;
     auto sync = [&]() {
       if (part == 0) role_sync<2>();
       else role_sync<3>();

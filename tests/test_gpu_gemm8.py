@@ -56,6 +56,16 @@ def test_sizes(M, N, K, out):
     check(x, xs, w, ws, hq.hq_gemm_int8(x, xs, w, ws, out_dtype=out))
 
 
+@pytest.mark.parametrize("M,N,K", [(48, 28672, 8192), (300, 40000, 4096), (4096, 4096, 8192), (1000, 9000, 2048), (40, 4096, 16384)])
+def test_long_sums_over_more_tiles_than_places(M, N, K):
+    """Stages go round the rings many times under a loaded memory, whose copies land in any order; again and again."""
+    x, xs, w, ws = problem(M, N, K, 3, most=20)  # (400 * K < 2^24: exact)
+    sums = torch.cat([x.double() @ v.double().t() for v in w.split(4096)], 1)
+    want = ((sums.float() * xs[:, None]) * ws).to(torch.bfloat16)
+    for _ in range(5):
+        assert torch.equal(hq.hq_gemm_int8(x, xs, w, ws), want)
+
+
 def test_every_code():
     """All pairs of codes, -128 among them (which the quantizer does not write)."""
     v = torch.arange(-128, 128, device="cuda", dtype=torch.int8)
