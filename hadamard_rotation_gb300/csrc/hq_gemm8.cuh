@@ -15,8 +15,9 @@
 // Large products are taken by pairs of CTAs (WIDE, cta_group::2) in tiles of 256 channels x up to 256 tokens: each CTA
 // widens 128 rows of each side, and its shared memory moves 64 KB in the 512 cycles of a stage, of 66 KB that it can.
 // With the channels in shared memory too it would be 96.
-// Few tokens: single CTAs, 128 channels x up to 64 tokens; with fewer tiles than SMs the CTAs of a cluster share the
-// summed axis (SPLIT) and add their parts through distributed shared memory in a fixed order.
+// Few tokens: single CTAs, up to 128 channels x up to 64 tokens (fewer channels where that evens out what the SMs get; the
+// instruction's other lanes hold whatever lies there and are not stored); with fewer tiles than SMs the CTAs of a cluster
+// share the summed axis (SPLIT) and add their parts through distributed shared memory in a fixed order.
 //
 // Roles of a CTA:
 //   warp 0         TMA
@@ -37,6 +38,7 @@ struct Gemm8Params {
   const float *xs, *ws;
   int M, N, K;
   int tiles_a, tiles_b;  // over the channels, over the tokens
+  int lanes;             // channels of a tile (of the pair's CTA: 128)
   int width;             // tokens of a tile
   int box_b;             // rows of a copy of tokens
   void* out;
@@ -57,13 +59,13 @@ struct Gemm8Shape {
   static constexpr int kRawA = 128 * kBlock, kRawB = kRowsB * kBlock, kRawBytes = kRawA + kRawB;
   static constexpr int kRaw = 6;                // stages of codes
   static constexpr int kWideBytes = kRowsB * kBlock * 2;
-  static constexpr int kWides = WIDE ? 6 : 3;   // stages of widened operands
+  static constexpr int kWides = WIDE ? 6 : 4;   // stages of widened operands
   static constexpr int kAccs = WIDE ? 1 : 2;
   static constexpr int kColA = kAccs * T;       // the channels' columns of tensor memory: kBlock / 2 per stage
   static_assert(kColA + kBlock / 2 * kWides <= 512, "tensor memory has 512 columns");
   static constexpr int kEpilogues = WIDE ? 2 : 1;
   // Sets of eight warps (four for the channels, four for the tokens) that widen stages in turn.
-  static constexpr int kSets = WIDE ? 2 : 3;
+  static constexpr int kSets = 2;
   // A place is used by the same set each time.  Otherwise a set could come to a place two uses ahead of the copy that
   // another set still waits for, where the parity says that its own has landed.
   static_assert(kRaw % kSets == 0 && kWides % kSets == 0, "a place belongs to one set");
@@ -77,8 +79,8 @@ struct Gemm8Shape {
 };
 
 struct Gemm8Bars {
-  uint64_t raw_full[6], raw_empty[6];
-  uint64_t wide_full[6], wide_empty[6];
+  uint64_t raw_full[12], raw_empty[12];
+  uint64_t wide_full[12], wide_empty[12];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   float xs[2][256];  // a tile's token scales, by epilogue group
@@ -139,6 +141,13 @@ __device__ __forceinline__ void tmem_store_nowait(uint32_t taddr, const uint32_t
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// An arrival on a barrier of the pair's first CTA that releases what this CTA's threads wrote to their own shared and
+// tensor memory: there the tensor core reads it, and the fences in front have made it visible to it.  (Released to the whole
+// cluster, an arrival waits for 1000 cycles and more: [8192, 8192] x 8192 1094 us in place of 657.)
+__device__ __forceinline__ void mbar_arrive_cta(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 struct Gemm8Tile {
   int a0, b0;    // first channel and token (of the pair)
   int valid, n;  // tokens that exist, columns of the instruction
@@ -148,7 +157,7 @@ template <bool WIDE>
 __device__ __forceinline__ Gemm8Tile gemm8_tile(const Gemm8Params& p, int tile) {
   const int at = tile / p.tiles_b, bt = tile - at * p.tiles_b;
   Gemm8Tile t;
-  t.a0 = at * Gemm8Shape<WIDE>::kTileLanes;
+  t.a0 = at * (WIDE ? 256 : p.lanes);
   t.b0 = bt * p.width;
   t.valid = min(p.width, p.M - t.b0);
   t.n = WIDE ? (t.valid + 31) & ~31 : (t.valid + 15) & ~15;
@@ -245,7 +254,7 @@ __global__ void __launch_bounds__((Gemm8Shape<WIDE>::kThreads), 1)
         if (!ok) break;
         const uint32_t full = smem_addr(&bars.raw_full[ring.s]), st = smem_addr(smem) + ring.s * S::kRawBytes;
         if (elect_one()) {
-          mbar_expect_tx(full, S::kRawA + p.box_b * S::kBlock);
+          mbar_expect_tx(full, (p.lanes + p.box_b) * S::kBlock);
           tma_tile2<false>(st, &map_w, kb * S::kBlock, a0, full);
           tma_tile2<false>(st + S::kRawA, &map_x, kb * S::kBlock, b0, full);
         }
@@ -300,8 +309,9 @@ __global__ void __launch_bounds__((Gemm8Shape<WIDE>::kThreads), 1)
     const int set = (warp - 4) / 8;
     const bool channels = ((warp - 4) & 4) == 0;
     // (64 tokens at most: two threads a row, each half of a stage's codes)
-    const int r = (channels || WIDE ? warp & 3 : warp & 1) * 32 + lane, half0 = channels || WIDE ? 0 : (warp & 2) * 2;
+    const int r = (channels || WIDE ? warp & 3 : warp & 1) * 32 + lane;
     constexpr int kPieces = S::kBlock / 16, kPiecesB = WIDE ? kPieces : kPieces / 2;
+    const int half0 = !WIDE && (warp & 2) ? kPiecesB : 0;
     GemmRing raw, ring;
     int turn = 0;
     for (int tile = first; ok && tile < tiles; tile += step) {
@@ -312,7 +322,7 @@ __global__ void __launch_bounds__((Gemm8Shape<WIDE>::kThreads), 1)
         const bool another = turn != set;
         if (++turn == S::kSets) turn = 0;
         if (another) continue;
-        ok = warp_wait(smem_addr(&bars.raw_full[raw.s]), raw.phase) && warp_wait(smem_addr(&bars.wide_empty[ring.s]), ring.phase ^ 1);
+        ok = warp_wait(smem_addr(&bars.wide_empty[ring.s]), ring.phase ^ 1) && warp_wait(smem_addr(&bars.raw_full[raw.s]), raw.phase);
         if (!ok) break;
         const uint8_t* const rows = smem + raw.s * S::kRawBytes + (channels ? 0 : S::kRawA);
         if (channels) {
@@ -331,7 +341,7 @@ __global__ void __launch_bounds__((Gemm8Shape<WIDE>::kThreads), 1)
           uint8_t* const to = wide + ring.s * S::kWideBytes + r * 128;
 #pragma unroll
           for (int i = 0; i < kPiecesB; ++i) {
-            const int j = half0 + i, at = 2 * (i % 4);
+            const int j = half0 + i, at = 2 * (j % 4);
             uint32_t v[8];
             widen_piece<S::kBlock>(rows, r, j, v);
             uint8_t* const half = to + (j / 4) * (S::kRowsB * 128);
@@ -343,7 +353,7 @@ __global__ void __launch_bounds__((Gemm8Shape<WIDE>::kThreads), 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_addr(&bars.raw_empty[raw.s]));
-          if (rank) mbar_arrive_cluster(cluster_addr(smem_addr(&bars.wide_full[ring.s]), 0));
+          if (rank) mbar_arrive_cta(cluster_addr(smem_addr(&bars.wide_full[ring.s]), 0));
           else mbar_arrive(smem_addr(&bars.wide_full[ring.s]));
         }
       }
@@ -376,7 +386,7 @@ __global__ void __launch_bounds__((Gemm8Shape<WIDE>::kThreads), 1)
       umma_fence_after();
       const int64_t stride = static_cast<int64_t>(p.N) * es;
       uint8_t* const out = static_cast<uint8_t*>(p.out) + t.b0 * stride + static_cast<int64_t>(a0) * es;
-      const int bytes = min(128, p.N - a0) * es;  // (not positive: the pair's second CTA has no channels here)
+      const int bytes = min(p.lanes, p.N - a0) * es;  // (not positive: the pair's second CTA has no channels here)
       const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * S::T;
       bool held = true;
       if constexpr (SPLIT) {  // the partial sums as they are, over the widened tokens, which have been multiplied
@@ -451,7 +461,7 @@ __global__ void __launch_bounds__((Gemm8Shape<WIDE>::kThreads), 1)
       float ws[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) ws[k] = n + k < p.N ? __ldg(p.ws + n + k) : 0.0f;
-      if (n < p.N)
+      if (n < p.N && lane * 4 < p.lanes)
         for (int c = part_k + splits * warp; c < t.valid; c += splits * static_cast<int>(blockDim.x >> 5)) {
           float4 v[kGemm8MaxSplits];
           const float x = __ldg(p.xs + t.b0 + c);
