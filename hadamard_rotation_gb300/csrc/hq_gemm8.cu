@@ -44,7 +44,7 @@ struct Plan {
 // wide tile ends with an epilogue of 3500 that nothing hides, a split one with the cluster's sum, and each split
 // tile starts anew.  Measured, us: 48 x 28672 x 8192 with 128 channels per tile (224 tiles on 152 SMs) 52.6, with 96
 // (299) 43.6; [777, 1056] x 1100 narrow 7.9, wide 14.
-Plan plan_of(int64_t M, int64_t N, int64_t K, int sms) {
+Plan plan_of(int64_t M, int64_t N, int64_t K, int sms, const int (&clusters)[9]) {
   const int64_t stages = (K + 127) / 128;
   Plan best = {};
   int64_t least = INT64_MAX;
@@ -55,7 +55,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int sms) {
       const int64_t tiles_a = (N + lanes * (1 + wide) - 1) / (lanes * (1 + wide)), tiles = tiles_a * parts;
       for (int64_t s = 1; s <= (wide ? 1 : hq::kGemm8MaxSplits); s *= 2) {
         if (s > 1 && stages < 2 * s) break;
-        const int64_t places = sms / ((1 + wide) * s), waves = (tiles + places - 1) / places;
+        const int64_t places = wide ? sms / 2 : s > 1 ? clusters[s] : sms, waves = (tiles + places - 1) / places;
         const int64_t stage = wide ? 1300 : lanes * 11 / 2 > 330 ? lanes * 11 / 2 : 330;
         const int64_t cost = waves * ((stages + s - 1) / s * stage + (wide ? 3500 : s > 1 ? 2500 : 1200));
         if (cost < least) {
@@ -67,6 +67,27 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int sms) {
     }
   }
   return best;
+}
+
+// How many clusters of 2, 4 and 8 CTAs that share a sum run at a time.
+cudaError_t clusters_of(int sms, int (&n)[9]) {
+  auto kernel = hq::k_gemm8<false, true>;
+  const size_t smem = hq::Gemm8Shape<false>::kSmemBytes + 1024;
+  cudaError_t e = hq::allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
+  for (int s = 2; s <= hq::kGemm8MaxSplits && e == cudaSuccess; s *= 2) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sms / s * s));
+    cfg.blockDim = dim3(hq::Gemm8Shape<false>::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(s);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = hq::clusters_at_a_time(reinterpret_cast<const void*>(kernel), cfg, s, &n[s]);
+  }
+  return e;
 }
 
 template <bool WIDE, bool SPLIT>
@@ -129,9 +150,11 @@ extern "C" hq_status hq_gemm_int8(const int8_t* xq, const float* x_scales, const
     return e == cudaSuccess ? HQ_OK : cuda_fail(e);
   }
   int sms = 0;
-  const cudaError_t e = hq::sm_count(&sms);
+  cudaError_t e = hq::sm_count(&sms);
+  int clusters[9] = {};
+  if (e == cudaSuccess) e = clusters_of(sms, clusters);
   if (e != cudaSuccess) return cuda_fail(e);
-  const Plan plan = plan_of(M, N, K, sms);
+  const Plan plan = plan_of(M, N, K, sms, clusters);
   hq::Gemm8Params p = {};
   p.xs = x_scales;
   p.ws = w_scales;
