@@ -137,7 +137,7 @@ def load() -> ctypes.CDLL:
         lib.hq_kv_attention_nvfp4.argtypes = [p] + [i64] * 3 + [p] + [i64] * 4 + [p, i64, i64, p, p, i64, i64, p, f32, i64, i32,
                                               p, p, p, p]
         lib.hq_kv_attention_nvfp4.restype = i32
-        lib.hq_kv_attention_workspace_bytes.argtypes = [i64] * 3
+        lib.hq_kv_attention_workspace_bytes.argtypes = [i64] * 5
         lib.hq_kv_attention_workspace_bytes.restype = i64
         lib.hq_version.argtypes = []
         lib.hq_version.restype = i32

@@ -535,9 +535,9 @@ def hq_kv_read_nvfp4(cache: torch.Tensor, slots: torch.Tensor, kv_amax: torch.Te
     return (_calls or _load_calls()).kv_read(cache, slots, kv_amax, group, out_dtype, k, v, stream)
 
 
-def hq_kv_attention_workspace_bytes(q_heads: int, kv_heads: int, D: int) -> int:
+def hq_kv_attention_workspace_bytes(q_heads: int, kv_heads: int, D: int, T: int, max_q: int) -> int:
     """Bytes of the workspace of hq_kv_attention_nvfp4 (which this binding allocates itself)."""
-    n = _lib.load().hq_kv_attention_workspace_bytes(q_heads, kv_heads, D)
+    n = _lib.load().hq_kv_attention_workspace_bytes(q_heads, kv_heads, D, T, max_q)
     if n < 0:
         raise ValueError("hq_kv_attention_workspace_bytes: q_heads a multiple of kv_heads, up to 4096, D 64, 128 or 256")
     return n

@@ -24,7 +24,7 @@ DEPS = SOURCES + [os.path.join(CSRC, "hq_kernels.cuh"), os.path.join(CSRC, "hq_i
                   os.path.join(CSRC, "hq_gemm.cuh"), os.path.join(CSRC, "hq_tcgen05.cuh"),
                   os.path.join(CSRC, "hq_tensor_map.h"), os.path.join(CSRC, "hq_norm.cuh"),
                   os.path.join(CSRC, "hq_gemm8.cuh"), os.path.join(CSRC, "hq_kv.cuh"),
-                  os.path.join(CSRC, "hq_kv_attend.cuh"),
+                  os.path.join(CSRC, "hq_kv_attend.cuh"), os.path.join(CSRC, "hq_kv_prompt.cuh"),
                   os.path.join(CSRC, "hq_internal.h"),
                   os.path.join(INCLUDE, "hq.h")]
 LIB = os.path.join(PKG, "libhq.so")

@@ -1,5 +1,5 @@
 // hq_kv.cu -- C ABI of the paged NVFP4 cache of keys and values (include/hq.h) and its launch logic.  The kernels are
-// in hq_kv.cuh and hq_kv_attend.cuh.
+// in hq_kv.cuh, hq_kv_attend.cuh and hq_kv_prompt.cuh.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -8,6 +8,7 @@
 #include "hq_internal.h"
 #include "hq_kv.cuh"
 #include "hq_kv_attend.cuh"
+#include "hq_kv_prompt.cuh"
 
 namespace {
 
@@ -17,6 +18,7 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 
 constexpr int64_t kMaxTokens = (int64_t{1} << 31) - 1024;  // token counts are ints in the kernels
 constexpr int64_t kMaxHeads = 4096;
+constexpr int64_t kFewRows = 32;
 
 // Heads, head size, rotation group, pages.
 hq_status check_cache(int64_t kv_heads, int64_t D, int group, int64_t pages, int64_t page_size) {
@@ -29,9 +31,9 @@ hq_status check_cache(int64_t kv_heads, int64_t D, int group, int64_t pages, int
 }
 
 template <typename Kernel, typename... Args>
-cudaError_t launch(Kernel kernel, int64_t grid, int block, size_t smem, cudaStream_t stream, Args... args) {
+cudaError_t launch(Kernel kernel, dim3 grid, int block, size_t smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(block));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -62,9 +64,9 @@ cudaError_t with_sizes(int64_t D, int group, bool bf16, F f) {
 }
 
 // CTAs for rows of D channels, 16 per thread: as many as there are, up to what fills the SMs.
-int64_t row_grid(int64_t rows, int64_t D, int sms) {
+dim3 row_grid(int64_t rows, int64_t D, int sms) {
   const int64_t per = 256 / (D / 16), most = int64_t{16} * sms;
-  return (rows + per - 1) / per < most ? (rows + per - 1) / per : most;
+  return dim3(static_cast<unsigned>((rows + per - 1) / per < most ? (rows + per - 1) / per : most));
 }
 
 template <int D, int NT>
@@ -74,9 +76,24 @@ cudaError_t launch_attend(const hq::KvAttendParams& p, int sms, cudaStream_t str
   cudaError_t e = hq::allow_smem(reinterpret_cast<const void*>(kernel), S::kSmemBytes);
   if (e != cudaSuccess) return e;
   const int ctas = sms < hq::kKvMaxCtas ? sms : hq::kKvMaxCtas;
-  if ((e = launch(kernel, ctas, S::kThreads, S::kSmemBytes, stream, p)) != cudaSuccess) return e;
-  return launch(hq::k_kv_combine<D, NT>, ctas, 256, 0, stream, p, ctas);
+  if ((e = launch(kernel, dim3(ctas), S::kThreads, S::kSmemBytes, stream, p)) != cudaSuccess) return e;
+  return launch(hq::k_kv_combine<D, NT>, dim3(ctas), 256, 0, stream, p, ctas);
 }
+
+template <int D>
+cudaError_t launch_prompt(const hq::KvAttendParams& p, int sms, cudaStream_t stream) {
+  using S = hq::KvPromptShape<D>;
+  auto kernel = hq::k_kv_prompt<D>;
+  const size_t smem = S::kSmemBytes + 1024;
+  cudaError_t e = hq::allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const int ctas = sms < hq::kKvMaxCtas ? sms : hq::kKvMaxCtas;
+  if ((e = launch(kernel, dim3(ctas), S::kThreads, smem, stream, p)) != cudaSuccess) return e;
+  return launch(hq::k_kv_prompt_combine<D>, dim3(ctas, 8), 256, 0, stream, p);
+}
+
+// The kernel for few rows (query tokens x heads that share a key head) of a sequence, or the one for many.
+bool few_rows(int64_t T, int64_t max_q, int64_t share) { return (max_q < T ? max_q : T) <= kFewRows / share; }
 
 }  // namespace
 
@@ -180,9 +197,10 @@ hq_status hq_kv_read_nvfp4(const uint8_t* cache, int64_t pages, int64_t page_siz
   return e == cudaSuccess ? HQ_OK : cuda_fail(e);
 }
 
-int64_t hq_kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t D) {
+int64_t hq_kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t D, int64_t T, int64_t max_q) {
   if (check_cache(kv_heads, D, 0, 0, 16) != HQ_OK || q_heads < 1 || q_heads > kMaxHeads || q_heads % kv_heads != 0) return -1;
-  return hq::kv_part_bytes(static_cast<int>(D), 16);
+  if (T < 0 || T * (q_heads / kv_heads) > kMaxTokens || T > kMaxTokens || max_q < 0) return -1;
+  return few_rows(T, max_q, q_heads / kv_heads) ? hq::kv_part_bytes(static_cast<int>(D), 16) : hq::kv_prompt_bytes(static_cast<int>(D));
 }
 
 hq_status hq_kv_attention_nvfp4(const void* q, int64_t ld_q, int64_t T, int64_t q_heads, const uint8_t* cache, int64_t pages,
@@ -230,10 +248,12 @@ hq_status hq_kv_attention_nvfp4(const void* q, int64_t ld_q, int64_t T, int64_t 
   cudaError_t e = hq::sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const bool few = (max_q < T ? max_q : T) * p.share <= 8;  // rows of a sequence
-  if (D == 64) e = few ? launch_attend<64, 1>(p, sms, cs) : launch_attend<64, 2>(p, sms, cs);
-  else if (D == 128) e = few ? launch_attend<128, 1>(p, sms, cs) : launch_attend<128, 2>(p, sms, cs);
-  else e = few ? launch_attend<256, 1>(p, sms, cs) : launch_attend<256, 2>(p, sms, cs);
+  if (!few_rows(T, max_q, p.share))
+    e = D == 64 ? launch_prompt<64>(p, sms, cs) : D == 128 ? launch_prompt<128>(p, sms, cs) : launch_prompt<256>(p, sms, cs);
+  else if ((max_q < T ? max_q : T) * p.share <= 8)
+    e = D == 64 ? launch_attend<64, 1>(p, sms, cs) : D == 128 ? launch_attend<128, 1>(p, sms, cs) : launch_attend<256, 1>(p, sms, cs);
+  else
+    e = D == 64 ? launch_attend<64, 2>(p, sms, cs) : D == 128 ? launch_attend<128, 2>(p, sms, cs) : launch_attend<256, 2>(p, sms, cs);
   return e == cudaSuccess ? HQ_OK : cuda_fail(e);
 }
 

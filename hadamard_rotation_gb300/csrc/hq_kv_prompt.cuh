@@ -1,0 +1,710 @@
+// hq_kv_prompt.cuh -- attention of many queries per sequence over the paged NVFP4 cache (prompts, chunks of prompts), on
+// the 5th-generation tensor cores.
+//
+// The mathematics and the number formats are those of hq_kv_attend.cuh: codes widened exactly to f16, q scaled by a power of
+// two per row, p in f16 scaled by 2^7 against a reference that moves only when a score exceeds it by 2^8.
+//
+// A CTA takes 128 rows (query token, head of the group that shares a key head) per tile of the tensor core and, up to D =
+// 128, two such tiles at once, so that the scores of one are multiplied while the other's are exponentiated.  Keys come
+// in tiles of 128 (64 for D = 256), widened once for both:
+//   S = Q K^T   Q and K in shared memory along the channels, S in tensor memory
+//   O += P V    P in tensor memory over S's columns, V in shared memory as it comes (the instruction takes it across)
+// Roles of a CTA:
+//   warp 0        issues the products
+//   warp 1        allocates tensor memory
+//   warps 4..7    widen keys and values: a token per thread, from global memory through registers (the next tile's
+//                 bytes are on their way meanwhile) into the swizzle that the products read
+//   warps 8..     softmax, a row per thread, four warps per tile; they also load and scale Q, correct O when a reference
+//                 moves, and finish the rows
+// In the order of issue, the product that writes S of a tile follows the one that reads its P, so neither needs a barrier
+// against the other; and when S of a tile is complete, so is the O that the correction changes.
+//
+// The work, in key tiles, is laid end to end (sequence, head, rows) and cut into equal parts, one per CTA; what a cut
+// goes through is finished by k_kv_prompt_combine from parts in the workspace, in the order of the parts.
+#pragma once
+
+#include "hq_kv_attend.cuh"
+#include "hq_tcgen05.cuh"
+
+namespace hq {
+
+template <int D>
+struct KvPromptShape {
+  static constexpr int kSub = D == 256 ? 1 : 2;       // tiles of 128 rows
+  static constexpr int kRows = 128 * kSub;
+  static constexpr int kKeys = D == 256 ? 64 : 128;   // of a tile
+  static constexpr int kQBytes = 128 * D * 2;         // of a tile of rows
+  static constexpr int kKvBytes = kKeys * D * 2;      // of a tile of keys or values
+  static constexpr int kAtomQ = 128 * 128, kAtomK = kKeys * 128;  // 64 channels
+  static constexpr int kQAt = 0, kKAt = kSub * kQBytes, kVAt = kKAt + 2 * kKvBytes;
+  static constexpr int kUsed = kVAt + 2 * kKvBytes;
+  static constexpr int kSmemBytes = kUsed < 116 * 1024 ? 116 * 1024 : kUsed;  // (a CTA takes all of tensor memory)
+  static constexpr int kThreads = 32 * (8 + 4 * kSub);
+  static constexpr int kColO = kSub * kKeys;          // tensor memory: S of each tile, then O of each
+  static_assert(kColO + kSub * D <= 512, "tensor memory has 512 columns");
+  static_assert(kSmemBytes + 1024 + 8192 <= 227 * 1024 && 2 * (kSmemBytes + 1024) > 228 * 1024, "one CTA per SM");
+  static constexpr int kPerToken = 128 / kKeys;       // threads that widen a token
+  static constexpr int kWords = D / 8 / kPerToken;    // words of codes of a thread, and a quarter as many pairs of scales
+  static constexpr int kPartFloats = kRows * (D + 2);
+};
+
+// Bytes of the workspace: parts of items that were cut, 2 per CTA, and a record per CTA of the item it begins and
+// does not end.
+inline int64_t kv_prompt_bytes(int D) {
+  return int64_t{2} * kKvMaxCtas * (D == 256 ? 128 : 256) * (D + 2) * 4 + kKvMaxCtas * 32;
+}
+
+struct KvCut {
+  int s, tile, head, last;  // the item; the CTA that has its end (-1: none)
+  int pad[4];
+};
+
+constexpr int64_t kKvMinTiles = 4;  // key tiles per CTA at least
+
+// Key tiles of the rows `tile` of a sequence: [first, first + n) of `keys` keys.
+struct KvReach {
+  int first, n;
+};
+template <int ROWS, int KEYS>
+__device__ __forceinline__ KvReach kv_reach(const KvAttendParams& p, const KvSeq& s, int tile) {
+  const int i0 = tile * ROWS / p.share, i1 = min(s.nq - 1, (tile * ROWS + ROWS - 1) / p.share);
+  const int hi = max(0, min(s.n, s.n - s.nq + i1 + 1));
+  const int lo = p.window ? max(0, s.n - s.nq + i0 + 1 - p.window) : 0;
+  return lo < hi ? KvReach{lo / KEYS, (hi + KEYS - 1) / KEYS - lo / KEYS} : KvReach{0, 0};
+}
+template <int ROWS>
+__device__ __forceinline__ int kv_row_tiles(const KvAttendParams& p, const KvSeq& s) {
+  return (s.nq * p.share + ROWS - 1) / ROWS;
+}
+
+// Where a CTA's share begins.
+struct KvStart {
+  int64_t at, end;  // of the work
+  int64_t per;
+  int s, head, tile;
+  int64_t item;     // the work before the item
+};
+
+// The plan of a launch, by all threads of a CTA: sums of the sequences by the warps in turn, the start by each thread.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ KvStart kv_plan(const KvAttendParams& p, int64_t (&sums)[512], int ctas, int cta) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = static_cast<int>(blockDim.x >> 5);
+  auto fill = [&](int s0) {  // per head
+    for (int s = s0 + warp; s < p.S && s < s0 + 512; s += warps) {
+      const KvSeq q = kv_seq(p, s);
+      const int tiles = kv_row_tiles<ROWS>(p, q);
+      int64_t sum = 0;
+      for (int t = lane; t < tiles; t += 32) sum += max(1, kv_reach<ROWS, KEYS>(p, q, t).n);
+#pragma unroll
+      for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
+      if (lane == 0) sums[s - s0] = sum;
+    }
+    __syncthreads();
+  };
+  int64_t total = 0;
+  for (int s0 = 0; s0 < p.S; s0 += 512) {
+    if (s0) __syncthreads();
+    fill(s0);
+    int64_t sum = 0;
+    for (int s = s0 + lane; s < p.S && s < s0 + 512; s += 32) sum += sums[s - s0];
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
+    total += sum * p.kv_heads;
+  }
+  KvStart r = {};
+  int64_t use = (total + kKvMinTiles - 1) / kKvMinTiles;
+  use = use < 1 ? 1 : use > ctas ? ctas : use;
+  r.per = (total + use - 1) / use;
+  r.at = r.per * cta < total ? r.per * cta : total;
+  r.end = r.at + r.per < total ? r.at + r.per : total;
+  // the sequence
+  int64_t before = 0, mine = 0;
+  bool found = r.at >= r.end;
+  for (int s0 = 0; s0 < p.S; s0 += 512) {  // (to the end in any case: the threads meet in `fill`)
+    if (p.S > 512) {
+      __syncthreads();
+      fill(s0);
+    }
+    for (int b = s0; b < p.S && b < s0 + 512 && !found; b += 32) {
+      const int64_t v = b + lane < p.S && b + lane < s0 + 512 ? sums[b + lane - s0] : 0;
+      int64_t sum = v * p.kv_heads;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d) sum += o;
+      }
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + sum > r.at);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        found = true;
+        r.s = b + l;
+        mine = __shfl_sync(0xFFFFFFFFu, v, l);
+        before += __shfl_sync(0xFFFFFFFFu, sum - v * p.kv_heads, l);
+      } else {
+        before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+      }
+    }
+  }
+  if (r.at >= r.end) return r;
+  // its head and rows
+  r.head = static_cast<int>((r.at - before) / mine);
+  r.item = before + r.head * mine;
+  const KvSeq q = kv_seq(p, r.s);
+  for (int t0 = 0;; t0 += 32) {  // (ends: the rows' work adds up to `mine`)
+    const int v = t0 + lane < kv_row_tiles<ROWS>(p, q) ? max(1, kv_reach<ROWS, KEYS>(p, q, t0 + lane).n) : 0;
+    int64_t sum = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, r.item + sum > r.at);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      r.tile = t0 + l;
+      r.item += __shfl_sync(0xFFFFFFFFu, sum - v, l);
+      return r;
+    }
+    r.item += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    if (t0 > kv_row_tiles<ROWS>(p, q)) return r;
+  }
+}
+
+// The segments of a share: an item each, or the part of one that lies in the share.
+template <int ROWS, int KEYS>
+struct KvPromptWalk {
+  const KvAttendParams& p;
+  int64_t at, end, item;
+  int s, head, tile;
+  KvSeq seq;
+  KvReach reach;
+
+  struct Segment {
+    int s, head, tile;
+    KvSeq seq;
+    int j0, j1;  // key tiles
+    bool starts, ends;
+    int64_t stop;  // the work up to the item's end
+  };
+
+  __device__ __forceinline__ KvPromptWalk(const KvAttendParams& p, const KvStart& b)
+      : p(p), at(b.at), end(b.end), item(b.item), s(b.s), head(b.head), tile(b.tile), seq{0, 0, 0}, reach{0, 0} {
+    if (at >= end) return;
+    seq = kv_seq(p, s);
+    reach = kv_reach<ROWS, KEYS>(p, seq, tile);
+  }
+
+  __device__ __forceinline__ bool next(Segment& g) {
+    if (at >= end) return false;
+    const int64_t stop = item + max(1, reach.n);
+    g.s = s, g.head = head, g.tile = tile, g.seq = seq;
+    g.starts = at == item;
+    g.ends = stop <= end;
+    g.stop = stop;
+    g.j0 = reach.first + static_cast<int>(at - item);
+    g.j1 = reach.first + min(reach.n, static_cast<int>((g.ends ? stop : end) - item));
+    at = item = stop;
+    if (at < end) {
+      if (++tile == kv_row_tiles<ROWS>(p, seq)) {
+        tile = 0;
+        if (++head == p.kv_heads) {
+          head = 0;
+          do seq = kv_seq(p, ++s);
+          while (seq.nq == 0);  // (there is work left, so a sequence with rows)
+        }
+      }
+      reach = kv_reach<ROWS, KEYS>(p, seq, tile);
+    }
+    return true;
+  }
+};
+
+// The key tiles that rows [128 sub, 128 sub + 128) of a segment's rows see of it, and what of them needs no mask.
+struct KvSub {
+  int j0, j1;
+  int first_end, last_start;  // keys below the one and from the other on are seen by all rows that exist
+  int live;                   // rows that exist
+};
+template <int ROWS, int KEYS, typename Segment>
+__device__ __forceinline__ KvSub kv_sub(const KvAttendParams& p, const Segment& g, int sub) {
+  KvSub r;
+  const int row0 = g.tile * ROWS + 128 * sub;
+  r.live = max(0, min(128, g.seq.nq * p.share - row0));
+  const int i0 = row0 / p.share, i1 = (row0 + max(1, r.live) - 1) / p.share, base = g.seq.n - g.seq.nq + 1;
+  const int hi = max(0, min(g.seq.n, base + i1)), lo = p.window ? max(0, base + i0 - p.window) : 0;
+  r.first_end = base + i0;
+  r.last_start = p.window ? base + i1 - p.window : 0;
+  r.j0 = r.j1 = g.j0;
+  if (r.live > 0 && lo < hi) {
+    r.j0 = max(g.j0, lo / KEYS);
+    r.j1 = max(r.j0, min(g.j1, (hi + KEYS - 1) / KEYS));
+  }
+  return r;
+}
+
+struct KvPromptBars {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t drain;
+  uint32_t tmem;
+};
+
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
+        "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]),
+        "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// f16 x f16 into fp32; `across`: B has its columns, not the summed axis, along its rows.
+__device__ __forceinline__ uint32_t kv_idesc(int n, bool across) {
+  return (1u << 4) | (static_cast<uint32_t>(across) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  umma_bf16<false>(d, a, b, idesc, accumulate);  // (the kind is the same, the types are the descriptor's)
+}
+// Values: rows of 64 channels (128 bytes, swizzled), 8-token groups 1024 bytes apart, the next 64 channels `atom` bytes on.
+__device__ __forceinline__ uint64_t desc_across(uint32_t addr, int atom) {
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(atom >> 4) << 16) | (uint64_t{1024 >> 4} << 32) |
+         (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+
+// Sixteen columns of the thread's row through the rotation's butterfly.
+__device__ __forceinline__ void kv_butterfly(uint32_t (&w)[16], float c) {
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(w[i]);
+#pragma unroll
+  for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if ((i & h) == 0) {
+        const float a = x[i], b = x[i + h];
+        x[i] = a + b;
+        x[i + h] = a - b;
+      }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(x[i] * c);
+}
+
+template <int D>
+__global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(const __grid_constant__ KvAttendParams p) {
+  using S = KvPromptShape<D>;
+  using R = KvRecord<D>;
+  constexpr int kSub = S::kSub, kRows = S::kRows, kKeys = S::kKeys;
+  using Walk = KvPromptWalk<kRows, kKeys>;
+  using Segment = typename Walk::Segment;
+  extern __shared__ uint8_t kv_prompt_raw[];
+  __shared__ KvPromptBars bars;
+  __shared__ int64_t sums[512];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(kv_prompt_raw) + 1023) & ~uintptr_t{1023});
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&bars.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&bars.k_full[i]), 4);
+      mbar_init(smem_addr(&bars.k_empty[i]), 1);
+      mbar_init(smem_addr(&bars.v_full[i]), 4);
+      mbar_init(smem_addr(&bars.v_empty[i]), 1);
+      mbar_init(smem_addr(&bars.q_full[i]), 4);
+      mbar_init(smem_addr(&bars.s_full[i]), 1);
+      mbar_init(smem_addr(&bars.p_full[i]), 4);
+      mbar_init(smem_addr(&bars.o_full[i]), 1);
+    }
+    mbar_init(smem_addr(&bars.drain), 1);
+    fence_mbar_init();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (by the warp that has taken tensor memory: the kernel after this one may take some before it waits for this one)
+  if (warp == 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  umma_fence_before();
+  __syncthreads();
+  umma_fence_after();
+  const uint32_t tmem = bars.tmem;
+  const KvStart start = kv_plan<kRows, kKeys>(p, sums, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x));
+  Walk walk(p, start);
+  Segment g;
+  bool ok = true;
+
+  if (warp == 0) {
+    GemmRing kv;  // the place of key tile j + 1's keys; values follow one tile behind
+    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};  // (rows that see nothing of a segment take no part in it)
+    const uint64_t q_desc = desc_codes(smem_addr(smem)), k_desc = desc_codes(smem_addr(smem) + S::kKAt);
+    const uint64_t v_desc = desc_across(smem_addr(smem) + S::kVAt, S::kAtomK);
+    while (ok && walk.next(g)) {
+      KvSub sub[kSub];
+#pragma unroll
+      for (int t = 0; t < kSub; ++t) sub[t] = kv_sub<kRows, kKeys>(p, g, t);
+      GemmRing vr = kv;
+      for (int j = g.j0 - 1; ok && j < g.j1; ++j) {
+        bool have_k = false, have_v = false;
+#pragma unroll
+        for (int t = 0; t < kSub; ++t) {
+          if (j >= sub[t].j0 && j < sub[t].j1) {  // O += P V
+            if (!have_v) ok = ok && warp_wait(smem_addr(&bars.v_full[vr.s]), vr.phase);
+            have_v = true;
+            ok = ok && warp_wait(smem_addr(&bars.p_full[t]), p_phase[t]);
+            if (!ok) break;
+            p_phase[t] ^= 1;
+            umma_fence_after();
+            if (elect_one()) {
+              const uint64_t v = v_desc + vr.s * (S::kKvBytes >> 4);
+#pragma unroll
+              for (int i = 0; i < kKeys / 16; ++i)
+                umma_f16_ts<false>(tmem + S::kColO + t * D, tmem + t * kKeys + 8 * i, v + i * (2048 >> 4), kv_idesc(D, true),
+                                   j > sub[t].j0 || i > 0);
+              if (j + 1 == sub[t].j1) umma_commit<false>(smem_addr(&bars.o_full[t]));
+            }
+            __syncwarp();
+          }
+          if (j + 1 >= sub[t].j0 && j + 1 < sub[t].j1) {  // S = Q K^T
+            if (j + 1 == sub[t].j0) {
+              ok = ok && warp_wait(smem_addr(&bars.q_full[t]), q_phase[t]);
+              q_phase[t] ^= 1;
+            }
+            if (!have_k) ok = ok && warp_wait(smem_addr(&bars.k_full[kv.s]), kv.phase);
+            have_k = true;
+            if (!ok) break;
+            umma_fence_after();
+            if (elect_one()) {
+              const uint64_t q = q_desc + t * (S::kQBytes >> 4), k = k_desc + kv.s * (S::kKvBytes >> 4);
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i)
+                umma_f16_ss(tmem + t * kKeys, q + (i / 4) * (S::kAtomQ >> 4) + 2 * (i % 4), k + (i / 4) * (S::kAtomK >> 4) + 2 * (i % 4),
+                            kv_idesc(kKeys, false), i > 0);
+              umma_commit<false>(smem_addr(&bars.s_full[t]));
+            }
+            __syncwarp();
+          }
+        }
+        if (!ok) break;
+        if (j >= g.j0) {
+          if (!have_v) ok = warp_wait(smem_addr(&bars.v_full[vr.s]), vr.phase);  // (a tile that no rows see)
+          if (elect_one()) umma_commit<false>(smem_addr(&bars.v_empty[vr.s]));
+          __syncwarp();
+          vr.next(2);
+        }
+        if (j + 1 < g.j1) {
+          if (!have_k) ok = ok && warp_wait(smem_addr(&bars.k_full[kv.s]), kv.phase);
+          if (elect_one()) umma_commit<false>(smem_addr(&bars.k_empty[kv.s]));
+          __syncwarp();
+          kv.next(2);
+        }
+      }
+    }
+    if (!ok) {  // let the products in flight finish (bounded) before tensor memory is freed
+      if (elect_one()) umma_commit<false>(smem_addr(&bars.drain));
+      __syncwarp();
+      mbar_wait(smem_addr(&bars.drain), 0);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    constexpr int kWords = S::kWords;
+    const int tid = threadIdx.x - 128, t = tid % kKeys, half = tid / kKeys;  // (half of the channels, for D = 256)
+    GemmRing ring;
+    struct Bytes {
+      uint32_t k[kWords], v[kWords];
+      uint2 ks, vs;  // (8 scales; 4 of them for D = 64)
+      bool live;
+    };
+    // The token's record: nothing past the sequence's end is read.
+    auto find = [&](int j) -> const uint8_t* {
+      const int key = j * kKeys + t;
+      if (j >= g.j1 || key >= g.seq.n) return nullptr;
+      const int u = key / kKvUnit, page = u / p.page_units;
+      int64_t at = __ldg(p.table + g.s * p.ld_table + page);
+      at = at < 0 ? 0 : at >= p.pages ? p.pages - 1 : at;
+      return p.cache + ((at * p.kv_heads + g.head) * p.page_units + (u - page * p.page_units)) * R::kBytes;
+    };
+    auto load = [&](const uint8_t* rec, int j, Bytes& b) {
+      b.live = rec != nullptr;
+      if (!b.live) return;
+      const int at = (j * kKeys + t) % kKvUnit;
+      const uint4* const k = reinterpret_cast<const uint4*>(rec + at * (D / 2) + half * (4 * kWords));
+      const uint4* const v = reinterpret_cast<const uint4*>(rec + R::kV + at * (D / 2) + half * (4 * kWords));
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 a = __ldg(k + i), c = __ldg(v + i);
+        b.k[4 * i] = a.x, b.k[4 * i + 1] = a.y, b.k[4 * i + 2] = a.z, b.k[4 * i + 3] = a.w;
+        b.v[4 * i] = c.x, b.v[4 * i + 1] = c.y, b.v[4 * i + 2] = c.z, b.v[4 * i + 3] = c.w;
+      }
+      const uint8_t *const ks = rec + R::kKs + at * (D / 16) + half * 8, *const vs = rec + R::kVs + at * (D / 16) + half * 8;
+      if constexpr (D == 64) {
+        b.ks.x = __ldg(reinterpret_cast<const uint32_t*>(ks));
+        b.vs.x = __ldg(reinterpret_cast<const uint32_t*>(vs));
+      } else {
+        b.ks = __ldg(reinterpret_cast<const uint2*>(ks));
+        b.vs = __ldg(reinterpret_cast<const uint2*>(vs));
+      }
+    };
+    auto widen = [&](uint8_t* to, const uint32_t (&w)[kWords], uint2 scales, bool live) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        __half2 h[4];
+        kv_widen(w[i], h);
+        const __half2 two = kv_scales((i < 8 ? scales.x : scales.y) >> (16 * ((i / 4) & 1)));
+        const __half2 sc = (i / 2) & 1 ? __high2half2(two) : __low2half2(two);
+        uint4 o = make_uint4(0, 0, 0, 0);
+        if (live) o = make_uint4(bits_of(__hmul2(h[0], sc)), bits_of(__hmul2(h[1], sc)), bits_of(__hmul2(h[2], sc)), bits_of(__hmul2(h[3], sc)));
+        const int c = half * kWords + i;  // 8 channels
+        *reinterpret_cast<uint4*>(to + (c / 8) * S::kAtomK + t * 128 + (((c % 8) ^ (t & 7)) << 4)) = o;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    while (ok && walk.next(g)) {
+      if (g.j0 >= g.j1) continue;
+      Bytes now;
+      load(find(g.j0), g.j0, now);
+      const uint8_t* ahead = find(g.j0 + 1);
+      for (int j = g.j0; j < g.j1; ++j) {
+        Bytes next;
+        load(ahead, j + 1, next);
+        ahead = find(j + 2);
+        ok = warp_wait(smem_addr(&bars.k_empty[ring.s]), ring.phase ^ 1);
+        if (!ok) break;
+        widen(smem + S::kKAt + ring.s * S::kKvBytes, now.k, now.ks, now.live);
+        if (lane == 0) mbar_arrive(smem_addr(&bars.k_full[ring.s]));
+        ok = warp_wait(smem_addr(&bars.v_empty[ring.s]), ring.phase ^ 1);
+        if (!ok) break;
+        widen(smem + S::kVAt + ring.s * S::kKvBytes, now.v, now.vs, now.live);
+        if (lane == 0) mbar_arrive(smem_addr(&bars.v_full[ring.s]));
+        ring.next(2);
+        now = next;
+      }
+    }
+  } else if (warp >= 8) {
+    const int t = (warp - 8) / 4, quarter = warp & 3, r = quarter * 32 + lane;  // the thread's row of its tile
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t ts = tmem + lanes + t * kKeys, to = tmem + lanes + S::kColO + t * D;
+    const float k_sg = kv_global_scale(__ldg(p.kv_amax)), v_sg = kv_global_scale(__ldg(p.kv_amax + 1));
+    const float to_log2 = fabsf(p.scale) * 1.4426950408889634f * k_sg;
+    uint32_t s_phase = 0, o_phase = 0;
+    while (ok && walk.next(g)) {
+      const KvSub sub = kv_sub<kRows, kKeys>(p, g, t);
+      const bool live = r < sub.live;
+      const int at = g.tile * kRows + 128 * t + r, i = at / p.share;
+      const int64_t token = g.seq.q0 + i;
+      const int head = g.head * p.share + (at - i * p.share);
+      // Q
+      float mult;
+      {
+        const uint4* const src = reinterpret_cast<const uint4*>(p.q + token * p.ld_q + static_cast<int64_t>(head) * D);
+        float top = 0.0f;
+        if (live && sub.j0 < sub.j1)
+#pragma unroll 8
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = __ldg(src + c);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xFFFF0000u))));
+          }
+        const float2 f = kv_row_factor(top);
+        const float factor = p.scale < 0.0f ? -f.x : f.x;
+        mult = fmaxf(f.y * to_log2, 1e-37f);  // (not 0: a masked score is -inf times it)
+        if (sub.j0 < sub.j1) {
+          uint8_t* const row = smem + t * S::kQBytes + r * 128;
+#pragma unroll 8
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              o[k] = bits_of(__floats2half2_rn(__uint_as_float(u[k] << 16) * factor, __uint_as_float(u[k] & 0xFFFF0000u) * factor));
+            *reinterpret_cast<uint4*>(row + (c / 8) * S::kAtomQ + (((c % 8) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&bars.q_full[t]));
+        }
+      }
+      const int end = live ? g.seq.n - g.seq.nq + i + 1 : 0, begin = p.window ? end - p.window : 0;
+      float m = kKvNone, l = 0.0f;
+      for (int j = sub.j0; j < sub.j1; ++j) {
+        ok = warp_wait(smem_addr(&bars.s_full[t]), s_phase);
+        if (!ok) break;
+        s_phase ^= 1;
+        umma_fence_after();
+        const int key = j * kKeys;
+        const bool masked = key < sub.last_start || key + kKeys > sub.first_end;
+        const int lo = begin - key, hi = end - key;  // columns [lo, hi) are seen
+        float top = -INFINITY;
+#pragma unroll
+        for (int c0 = 0; c0 < kKeys; c0 += 32) {
+          float v[32];
+          tmem_load32(ts + c0, v);
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] = c0 + c >= lo && c0 + c < hi ? v[c] : -INFINITY;
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) top = fmaxf(top, fmaxf(v[c], v[c + 1]));
+        }
+        top = top == -INFINITY ? top : top * mult;  // (0 * inf is no score)
+        const bool above = top > m + kKvSlack;
+        if (__any_sync(0xFFFFFFFFu, above)) {
+          const float moved = above ? top : m;
+          if (j > sub.j0) {
+            const float f = exp2_fast(m - moved);
+            l *= f;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              uint32_t w[16];
+              tmem_load(to + c0, w);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) w[c] = __float_as_uint(__uint_as_float(w[c]) * f);
+              tmem_store(to + c0, w);
+            }
+          }
+          m = moved;
+        }
+        const float off = kKvShift - m;
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int c0 = 0; c0 < kKeys; c0 += 32) {
+          float v[32];
+          tmem_load32(ts + c0, v);
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] = c0 + c >= lo && c0 + c < hi ? v[c] : -INFINITY;
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float2 e = fma2(make_float2(v[2 * c], v[2 * c + 1]), make_float2(mult, mult), make_float2(off, off));
+            e = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+            sum = add2(sum, e);
+            w[c] = bits_of(__floats2half2_rn(e.x, e.y));
+          }
+          tmem_store_nowait(ts + c0 / 2, w);  // (over columns that have been read)
+        }
+        l += sum.x + sum.y;
+        tmem_store_wait();
+        umma_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&bars.p_full[t]));
+      }
+      if (!ok) break;
+      const bool some = sub.j0 < sub.j1;
+      if (some) {
+        ok = warp_wait(smem_addr(&bars.o_full[t]), o_phase);
+        if (!ok) break;
+        o_phase ^= 1;
+        umma_fence_after();
+      }
+      if (g.starts && g.ends) {
+        const float f = l > 0.0f || l != l ? __fdiv_rn(v_sg, l) : 0.0f;
+        __nv_bfloat16* const out = p.out + (token * p.heads + head) * D;
+        if (D == 256 && p.group == 256 && some) {  // the butterfly across the blocks of 16, in place
+#pragma unroll 1
+          for (int c = 0; c < 16; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(w[k]) : "r"(to + (16 * k + c) % D) : "memory");
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+            for (int k = 0; k < 16; ++k) asm volatile("" : "+r"(w[k]));  // (not used before the wait)
+            kv_butterfly(w, 0.25f);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(to + (16 * k + c) % D), "r"(w[k]) : "memory");
+            tmem_store_wait();
+          }
+        }
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          uint32_t w[16] = {};
+          if (some) tmem_load(to + c0, w);
+          if (p.group) kv_butterfly(w, 0.25f);
+          uint32_t o[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(w[2 * c]) * f, __uint_as_float(w[2 * c + 1]) * f);
+            o[c] = l == 0.0f ? 0u : *reinterpret_cast<const uint32_t*>(&h);
+          }
+          if (live) {
+            reinterpret_cast<uint4*>(out + c0)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            reinterpret_cast<uint4*>(out + c0)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+        if (p.lse && live)
+          p.lse[token * p.heads + head] = l > 0.0f || l != l ? (m - kKvShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      } else {  // (an item that began before is the share's first segment, one that goes on its last)
+        float* const part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + g.starts) * S::kPartFloats;
+        const int row = 128 * t + r;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          uint32_t w[16] = {};
+          if (some) tmem_load(to + c0, w);
+#pragma unroll
+          for (int c = 0; c < 16; c += 4)
+            *reinterpret_cast<uint4*>(part + static_cast<int64_t>(row) * D + c0 + c) = make_uint4(w[c], w[c + 1], w[c + 2], w[c + 3]);
+        }
+        part[kRows * D + row] = m;
+        part[kRows * D + kRows + row] = l;
+      }
+      umma_fence_before();  // (the tile's next product into O follows this warp's next arrival)
+    }
+  } else if (warp == 2) {  // what this CTA begins and does not end
+    KvCut cut{0, 0, 0, -1, {}};
+    while (walk.next(g))
+      if (g.starts && !g.ends) cut = KvCut{g.s, g.tile, g.head, static_cast<int>((g.stop - 1) / start.per), {}};
+    KvCut* const cuts = reinterpret_cast<KvCut*>(p.part + static_cast<int64_t>(2) * kKvMaxCtas * S::kPartFloats);
+    if (lane == 0) cuts[blockIdx.x] = cut;
+  }
+  if (!ok && lane == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);
+  __syncwarp();
+  umma_fence_before();
+  __syncthreads();
+  umma_fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Items that were cut: blockIdx.x the CTA that an item begins in, blockIdx.y a slice of its rows.
+template <int D>
+__global__ void __launch_bounds__(256) k_kv_prompt_combine(const __grid_constant__ KvAttendParams p) {
+  using S = KvPromptShape<D>;
+  constexpr int kRows = S::kRows, kLanes = D / 8;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int cta = static_cast<int>(blockIdx.x);
+  const KvCut* const cuts = reinterpret_cast<const KvCut*>(p.part + static_cast<int64_t>(2) * kKvMaxCtas * S::kPartFloats);
+  const int4 cut = __ldcg(reinterpret_cast<const int4*>(cuts + cta));
+  const int last = cut.w;
+  if (last < 0) return;
+  const KvSeq seq = kv_seq(p, cut.x);
+  const float v_sg = kv_global_scale(__ldg(p.kv_amax + 1));
+  auto part = [&](int k) { return p.part + (static_cast<int64_t>(k) * 2 + (k == cta)) * S::kPartFloats; };
+  for (int task = blockIdx.y * 256 + threadIdx.x; task < kRows * kLanes; task += 256 * gridDim.y) {
+    const int row = task / kLanes, e = task % kLanes;
+    float top = kKvNone;
+    for (int k = cta; k <= last; ++k) top = fmaxf(top, __ldcg(part(k) + kRows * D + row));
+    float sum = 0.0f, v[8] = {};
+#pragma unroll 4
+    for (int k = cta; k <= last; ++k) {
+      const float* const from = part(k);
+      const float f = exp2_fast(__ldcg(from + kRows * D + row) - top);
+      sum += __ldcg(from + kRows * D + kRows + row) * f;
+      const float4* const src = reinterpret_cast<const float4*>(from + row * D + 8 * e);
+      const float4 a = __ldcg(src), b = __ldcg(src + 1);
+      v[0] += a.x * f, v[1] += a.y * f, v[2] += a.z * f, v[3] += a.w * f;
+      v[4] += b.x * f, v[5] += b.y * f, v[6] += b.z * f, v[7] += b.w * f;
+    }
+    const int at = cut.y * kRows + row;
+    kv_finish<D>(p, v, top, sum, v_sg, seq.q0 + at / p.share, cut.z * p.share + at % p.share, e, at < seq.nq * p.share);
+  }
+}
+
+}  // namespace hq

@@ -449,7 +449,7 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                             : given(a[10], {T, heads, cache.D}, at::kBFloat16, cache.index, "out");
     at::Tensor lse;
     if (with_lse) lse = empty({T, heads}, at::kFloat, cache.t, stream);
-    const at::Tensor work = workspace(hq_kv_attention_workspace_bytes(heads, cache.kv_heads, cache.D), cache.t, stream);
+    const at::Tensor work = workspace(hq_kv_attention_workspace_bytes(heads, cache.kv_heads, cache.D, T, max_q < 0 ? T : max_q), cache.t, stream);
     run(cache.index, "hq_kv_attention_nvfp4", [&] {
       return hq_kv_attention_nvfp4(q.t->const_data_ptr(), q.ld, T, heads, static_cast<const uint8_t*>(cache.t.const_data_ptr()),
                                    cache.pages, cache.page_size, cache.kv_heads, cache.D,

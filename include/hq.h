@@ -583,8 +583,8 @@ HQ_API hq_status hq_kv_read_nvfp4(const uint8_t* cache, int64_t pages, int64_t p
  *   max_q : the most queries of a sequence, as far as the host knows (T is always right).  It chooses the kernel;
  *          the result is defined for any value.
  *   window : 0 for none.    lse : float [T, q_heads], or NULL.
- *   workspace : hq_kv_attention_workspace_bytes(q_heads, kv_heads, D) bytes, 16-byte aligned; contents need no
- *          preparation.  Calls that may run at the same time need different ones.
+ *   workspace : hq_kv_attention_workspace_bytes(q_heads, kv_heads, D, T, max_q) bytes, 16-byte aligned; contents need
+ *          no preparation.  Calls that may run at the same time need different ones.
  */
 HQ_API hq_status hq_kv_attention_nvfp4(const void* q, int64_t ld_q, int64_t T, int64_t q_heads,
                                        const uint8_t* cache, int64_t pages, int64_t page_size,
@@ -595,7 +595,8 @@ HQ_API hq_status hq_kv_attention_nvfp4(const void* q, int64_t ld_q, int64_t T, i
                                        void* out, float* lse, void* workspace, hq_stream stream);
 
 /* Bytes of hq_kv_attention_nvfp4's workspace (-1 for sizes it refuses). */
-HQ_API int64_t hq_kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t D);
+HQ_API int64_t hq_kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t D, int64_t T,
+                                               int64_t max_q);
 
 /* Human-readable name of a status code (static storage). */
 HQ_API const char* hq_status_string(hq_status status);

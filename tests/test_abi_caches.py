@@ -103,8 +103,9 @@ def test_sizes(lib):
         assert lib.hq_kv_page_bytes(*bad) == -1
         with pytest.raises(ValueError):
             hq.hq_kv_page_bytes(*bad)
-    assert lib.hq_kv_attention_workspace_bytes(8, 2, 128) > 0
-    for bad in ((0, 1, 64), (7, 2, 64), (8, 2, 96), (8, 0, 64), (5000, 1, 64)):
+    assert lib.hq_kv_attention_workspace_bytes(8, 2, 128, 100, 100) > lib.hq_kv_attention_workspace_bytes(8, 2, 128, 100, 1) > 0
+    for bad in ((0, 1, 64, 1, 1), (7, 2, 64, 1, 1), (8, 2, 96, 1, 1), (8, 0, 64, 1, 1), (5000, 1, 64, 1, 1), (8, 2, 64, -1, 1), (8, 2, 64, 1, -1),
+                (8, 2, 64, 1 << 31, 1)):
         assert lib.hq_kv_attention_workspace_bytes(*bad) == -1
         with pytest.raises(ValueError):
             hq.hq_kv_attention_workspace_bytes(*bad)
