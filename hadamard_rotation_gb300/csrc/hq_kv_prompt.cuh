@@ -59,7 +59,9 @@ struct KvCut {
   int pad[4];
 };
 
-constexpr int64_t kKvMinTiles = 4;  // key tiles per CTA at least
+constexpr int64_t kKvMinTiles = 6;  // of work per CTA at least
+// What an item costs beside its key tiles (Q, the first scores, the rows' end), as work of this many tiles before its first.
+constexpr int kKvItemTiles = 2;
 
 // Key tiles of the rows `tile` of a sequence: [first, first + n) of `keys` keys.
 struct KvReach {
@@ -94,7 +96,7 @@ __device__ __forceinline__ KvStart kv_plan(const KvAttendParams& p, int64_t (&su
       const KvSeq q = kv_seq(p, s);
       const int tiles = kv_row_tiles<ROWS>(p, q);
       int64_t sum = 0;
-      for (int t = lane; t < tiles; t += 32) sum += max(1, kv_reach<ROWS, KEYS>(p, q, t).n);
+      for (int t = lane; t < tiles; t += 32) sum += kv_reach<ROWS, KEYS>(p, q, t).n + kKvItemTiles;
 #pragma unroll
       for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
       if (lane == 0) sums[s - s0] = sum;
@@ -151,7 +153,7 @@ __device__ __forceinline__ KvStart kv_plan(const KvAttendParams& p, int64_t (&su
   r.item = before + r.head * mine;
   const KvSeq q = kv_seq(p, r.s);
   for (int t0 = 0;; t0 += 32) {  // (ends: the rows' work adds up to `mine`)
-    const int v = t0 + lane < kv_row_tiles<ROWS>(p, q) ? max(1, kv_reach<ROWS, KEYS>(p, q, t0 + lane).n) : 0;
+    const int v = t0 + lane < kv_row_tiles<ROWS>(p, q) ? kv_reach<ROWS, KEYS>(p, q, t0 + lane).n + kKvItemTiles : 0;
     int64_t sum = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -196,13 +198,13 @@ struct KvPromptWalk {
 
   __device__ __forceinline__ bool next(Segment& g) {
     if (at >= end) return false;
-    const int64_t stop = item + max(1, reach.n);
+    const int64_t stop = item + reach.n + kKvItemTiles;
     g.s = s, g.head = head, g.tile = tile, g.seq = seq;
     g.starts = at == item;
     g.ends = stop <= end;
     g.stop = stop;
-    g.j0 = reach.first + static_cast<int>(at - item);
-    g.j1 = reach.first + min(reach.n, static_cast<int>((g.ends ? stop : end) - item));
+    g.j0 = reach.first + max(0, static_cast<int>(at - item) - kKvItemTiles);
+    g.j1 = reach.first + max(0, static_cast<int>((g.ends ? stop : end) - item) - kKvItemTiles);
     at = item = stop;
     if (at < end) {
       if (++tile == kv_row_tiles<ROWS>(p, seq)) {
@@ -249,17 +251,24 @@ struct KvPromptBars {
   uint32_t tmem;
 };
 
-__device__ __forceinline__ void tmem_load32(uint32_t taddr, float (&v)[32]) {
+// Columns of the thread's row, on their way until tmem_load_wait.
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, float* v) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
         "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
         "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]),
         "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr)
       : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_load_wait(float (&v)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));  // (not used before the wait)
 }
 
 // f16 x f16 into fp32; `across`: B has its columns, not the summed axis, along its rows.
@@ -336,70 +345,64 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
   Segment g;
   bool ok = true;
 
+  if (warp < 4) {
   if (warp == 0) {
     GemmRing kv;  // the place of key tile j + 1's keys; values follow one tile behind
-    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};  // (rows that see nothing of a segment take no part in it)
+    uint32_t q_phase = 0, p_phase = 0;  // a bit per tile of rows (rows that see nothing of a segment take no part in it)
     const uint64_t q_desc = desc_codes(smem_addr(smem)), k_desc = desc_codes(smem_addr(smem) + S::kKAt);
     const uint64_t v_desc = desc_across(smem_addr(smem) + S::kVAt, S::kAtomK);
     while (ok && walk.next(g)) {
-      KvSub sub[kSub];
-#pragma unroll
-      for (int t = 0; t < kSub; ++t) sub[t] = kv_sub<kRows, kKeys>(p, g, t);
+      const KvSub first = kv_sub<kRows, kKeys>(p, g, 0), second = kSub > 1 ? kv_sub<kRows, kKeys>(p, g, 1) : first;
       GemmRing vr = kv;
       for (int j = g.j0 - 1; ok && j < g.j1; ++j) {
-        bool have_k = false, have_v = false;
-#pragma unroll
-        for (int t = 0; t < kSub; ++t) {
-          if (j >= sub[t].j0 && j < sub[t].j1) {  // O += P V
-            if (!have_v) ok = ok && warp_wait(smem_addr(&bars.v_full[vr.s]), vr.phase);
-            have_v = true;
-            ok = ok && warp_wait(smem_addr(&bars.p_full[t]), p_phase[t]);
+        if (j >= g.j0) ok = warp_wait(smem_addr(&bars.v_full[vr.s]), vr.phase);
+        if (j + 1 < g.j1) ok = ok && warp_wait(smem_addr(&bars.k_full[kv.s]), kv.phase);
+#pragma unroll 1  // (short code: the roles share the instruction cache)
+        for (int t = 0; t < kSub && ok; ++t) {
+          const int t0 = t ? second.j0 : first.j0, t1 = t ? second.j1 : first.j1;
+          if (j >= t0 && j < t1) {  // O += P V
+            ok = warp_wait(smem_addr(&bars.p_full[t]), p_phase >> t & 1);
+            p_phase ^= 1u << t;
             if (!ok) break;
-            p_phase[t] ^= 1;
             umma_fence_after();
+            const uint64_t v = v_desc + vr.s * (S::kKvBytes >> 4);
             if (elect_one()) {
-              const uint64_t v = v_desc + vr.s * (S::kKvBytes >> 4);
-#pragma unroll
+#pragma unroll 4
               for (int i = 0; i < kKeys / 16; ++i)
                 umma_f16_ts<false>(tmem + S::kColO + t * D, tmem + t * kKeys + 8 * i, v + i * (2048 >> 4), kv_idesc(D, true),
-                                   j > sub[t].j0 || i > 0);
-              if (j + 1 == sub[t].j1) umma_commit<false>(smem_addr(&bars.o_full[t]));
+                                   j > t0 || i > 0);
+              if (j + 1 == t1) umma_commit<false>(smem_addr(&bars.o_full[t]));
             }
             __syncwarp();
           }
-          if (j + 1 >= sub[t].j0 && j + 1 < sub[t].j1) {  // S = Q K^T
-            if (j + 1 == sub[t].j0) {
-              ok = ok && warp_wait(smem_addr(&bars.q_full[t]), q_phase[t]);
-              q_phase[t] ^= 1;
+          if (j + 1 >= t0 && j + 1 < t1) {  // S = Q K^T
+            if (j + 1 == t0) {
+              ok = warp_wait(smem_addr(&bars.q_full[t]), q_phase >> t & 1);
+              q_phase ^= 1u << t;
+              if (!ok) break;
             }
-            if (!have_k) ok = ok && warp_wait(smem_addr(&bars.k_full[kv.s]), kv.phase);
-            have_k = true;
-            if (!ok) break;
             umma_fence_after();
+            const uint64_t q = q_desc + t * (S::kQBytes >> 4), k = k_desc + kv.s * (S::kKvBytes >> 4);
             if (elect_one()) {
-              const uint64_t q = q_desc + t * (S::kQBytes >> 4), k = k_desc + kv.s * (S::kKvBytes >> 4);
+#pragma unroll 1
+              for (int i = 0; i < D / 64; ++i)
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i)
-                umma_f16_ss(tmem + t * kKeys, q + (i / 4) * (S::kAtomQ >> 4) + 2 * (i % 4), k + (i / 4) * (S::kAtomK >> 4) + 2 * (i % 4),
-                            kv_idesc(kKeys, false), i > 0);
+                for (int c = 0; c < 4; ++c)
+                  umma_f16_ss(tmem + t * kKeys, q + i * (S::kAtomQ >> 4) + 2 * c, k + i * (S::kAtomK >> 4) + 2 * c,
+                              kv_idesc(kKeys, false), i > 0 || c > 0);
               umma_commit<false>(smem_addr(&bars.s_full[t]));
             }
             __syncwarp();
           }
         }
         if (!ok) break;
-        if (j >= g.j0) {
-          if (!have_v) ok = warp_wait(smem_addr(&bars.v_full[vr.s]), vr.phase);  // (a tile that no rows see)
-          if (elect_one()) umma_commit<false>(smem_addr(&bars.v_empty[vr.s]));
-          __syncwarp();
-          vr.next(2);
+        if (elect_one()) {
+          if (j >= g.j0) umma_commit<false>(smem_addr(&bars.v_empty[vr.s]));
+          if (j + 1 < g.j1) umma_commit<false>(smem_addr(&bars.k_empty[kv.s]));
         }
-        if (j + 1 < g.j1) {
-          if (!have_k) ok = ok && warp_wait(smem_addr(&bars.k_full[kv.s]), kv.phase);
-          if (elect_one()) umma_commit<false>(smem_addr(&bars.k_empty[kv.s]));
-          __syncwarp();
-          kv.next(2);
-        }
+        __syncwarp();
+        if (j >= g.j0) vr.next(2);
+        if (j + 1 < g.j1) kv.next(2);
       }
     }
     if (!ok) {  // let the products in flight finish (bounded) before tensor memory is freed
@@ -407,54 +410,51 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
       __syncwarp();
       mbar_wait(smem_addr(&bars.drain), 0);
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp == 2) {  // what this CTA begins and does not end
+    KvCut cut{0, 0, 0, -1, {}};
+    while (walk.next(g))
+      if (g.starts && !g.ends) cut = KvCut{g.s, g.tile, g.head, static_cast<int>((g.stop - 1) / start.per), {}};
+    KvCut* const cuts = reinterpret_cast<KvCut*>(p.part + static_cast<int64_t>(2) * kKvMaxCtas * S::kPartFloats);
+    if (lane == 0) cuts[blockIdx.x] = cut;
+  }
+  } else if (warp < 8) {
     constexpr int kWords = S::kWords;
     const int tid = threadIdx.x - 128, t = tid % kKeys, half = tid / kKeys;  // (half of the channels, for D = 256)
     GemmRing ring;
-    struct Bytes {
-      uint32_t k[kWords], v[kWords];
-      uint2 ks, vs;  // (8 scales; 4 of them for D = 64)
-      bool live;
-    };
-    // The token's record: nothing past the sequence's end is read.
-    auto find = [&](int j) -> const uint8_t* {
+    // The page of the token in key tile j, -1 where the sequence has none: nothing past its end is read.  (These loads
+    // are volatile so that they stay a tile ahead of what waits for them.)
+    auto page_of = [&](int j) {
       const int key = j * kKeys + t;
-      if (j >= g.j1 || key >= g.seq.n) return nullptr;
-      const int u = key / kKvUnit, page = u / p.page_units;
-      int64_t at = __ldg(p.table + g.s * p.ld_table + page);
-      at = at < 0 ? 0 : at >= p.pages ? p.pages - 1 : at;
-      return p.cache + ((at * p.kv_heads + g.head) * p.page_units + (u - page * p.page_units)) * R::kBytes;
+      int page = -1;
+      if (j < g.j1 && key < g.seq.n)
+        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(page) : "l"(p.table + g.s * p.ld_table + key / (kKvUnit * p.page_units)));
+      return j < g.j1 && key < g.seq.n ? max(0, page) : -1;
     };
-    auto load = [&](const uint8_t* rec, int j, Bytes& b) {
-      b.live = rec != nullptr;
-      if (!b.live) return;
-      const int at = (j * kKeys + t) % kKvUnit;
-      const uint4* const k = reinterpret_cast<const uint4*>(rec + at * (D / 2) + half * (4 * kWords));
-      const uint4* const v = reinterpret_cast<const uint4*>(rec + R::kV + at * (D / 2) + half * (4 * kWords));
+    auto load16 = [](uint32_t* to, const uint8_t* from) {
+      asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(to[0]), "=r"(to[1]), "=r"(to[2]), "=r"(to[3]) : "l"(from));
+    };
+    // Its K (which = 0) or V: the codes of the thread and their scales (8; 4 for D = 64).
+    auto load = [&](int page, int j, int which, uint32_t (&w)[kWords], uint2& scales) {
+      scales = make_uint2(0, 0);  // (widened to zeros)
+      if (page < 0) return;
+      const int u = (j * kKeys + t) / kKvUnit % p.page_units, at = t % kKvUnit;
+      const int64_t pg = min(static_cast<int64_t>(page), p.pages - 1);
+      const uint8_t* const rec = p.cache + ((pg * p.kv_heads + g.head) * p.page_units + u) * R::kBytes;
+      const uint8_t* const codes = rec + which * R::kV + at * (D / 2) + half * (4 * kWords);
 #pragma unroll
-      for (int i = 0; i < kWords / 4; ++i) {
-        const uint4 a = __ldg(k + i), c = __ldg(v + i);
-        b.k[4 * i] = a.x, b.k[4 * i + 1] = a.y, b.k[4 * i + 2] = a.z, b.k[4 * i + 3] = a.w;
-        b.v[4 * i] = c.x, b.v[4 * i + 1] = c.y, b.v[4 * i + 2] = c.z, b.v[4 * i + 3] = c.w;
-      }
-      const uint8_t *const ks = rec + R::kKs + at * (D / 16) + half * 8, *const vs = rec + R::kVs + at * (D / 16) + half * 8;
-      if constexpr (D == 64) {
-        b.ks.x = __ldg(reinterpret_cast<const uint32_t*>(ks));
-        b.vs.x = __ldg(reinterpret_cast<const uint32_t*>(vs));
-      } else {
-        b.ks = __ldg(reinterpret_cast<const uint2*>(ks));
-        b.vs = __ldg(reinterpret_cast<const uint2*>(vs));
-      }
+      for (int i = 0; i < kWords; i += 4) load16(w + i, codes + 4 * i);
+      const uint8_t* const sc = rec + R::kKs + which * R::kScales + at * (D / 16) + half * 8;
+      if constexpr (D == 64) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(scales.x) : "l"(sc));
+      else asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(scales.x), "=r"(scales.y) : "l"(sc));
     };
-    auto widen = [&](uint8_t* to, const uint32_t (&w)[kWords], uint2 scales, bool live) {
+    auto widen = [&](uint8_t* to, const uint32_t (&w)[kWords], uint2 scales) {
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         __half2 h[4];
         kv_widen(w[i], h);
         const __half2 two = kv_scales((i < 8 ? scales.x : scales.y) >> (16 * ((i / 4) & 1)));
         const __half2 sc = (i / 2) & 1 ? __high2half2(two) : __low2half2(two);
-        uint4 o = make_uint4(0, 0, 0, 0);
-        if (live) o = make_uint4(bits_of(__hmul2(h[0], sc)), bits_of(__hmul2(h[1], sc)), bits_of(__hmul2(h[2], sc)), bits_of(__hmul2(h[3], sc)));
+        const uint4 o = make_uint4(bits_of(__hmul2(h[0], sc)), bits_of(__hmul2(h[1], sc)), bits_of(__hmul2(h[2], sc)), bits_of(__hmul2(h[3], sc)));
         const int c = half * kWords + i;  // 8 channels
         *reinterpret_cast<uint4*>(to + (c / 8) * S::kAtomK + t * 128 + (((c % 8) ^ (t & 7)) << 4)) = o;
       }
@@ -463,26 +463,28 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
     };
     while (ok && walk.next(g)) {
       if (g.j0 >= g.j1) continue;
-      Bytes now;
-      load(find(g.j0), g.j0, now);
-      const uint8_t* ahead = find(g.j0 + 1);
+      uint32_t k[kWords] = {}, v[kWords] = {};
+      uint2 ks, vs;
+      int page = page_of(g.j0), ahead = page_of(g.j0 + 1);
+      load(page, g.j0, 0, k, ks);
+      load(page, g.j0, 1, v, vs);
       for (int j = g.j0; j < g.j1; ++j) {
-        Bytes next;
-        load(ahead, j + 1, next);
-        ahead = find(j + 2);
+        page = ahead;
+        ahead = page_of(j + 2);
         ok = warp_wait(smem_addr(&bars.k_empty[ring.s]), ring.phase ^ 1);
         if (!ok) break;
-        widen(smem + S::kKAt + ring.s * S::kKvBytes, now.k, now.ks, now.live);
+        widen(smem + S::kKAt + ring.s * S::kKvBytes, k, ks);
         if (lane == 0) mbar_arrive(smem_addr(&bars.k_full[ring.s]));
+        load(page, j + 1, 0, k, ks);
         ok = warp_wait(smem_addr(&bars.v_empty[ring.s]), ring.phase ^ 1);
         if (!ok) break;
-        widen(smem + S::kVAt + ring.s * S::kKvBytes, now.v, now.vs, now.live);
+        widen(smem + S::kVAt + ring.s * S::kKvBytes, v, vs);
         if (lane == 0) mbar_arrive(smem_addr(&bars.v_full[ring.s]));
+        load(page, j + 1, 1, v, vs);
         ring.next(2);
-        now = next;
       }
     }
-  } else if (warp >= 8) {
+  } else {
     const int t = (warp - 8) / 4, quarter = warp & 3, r = quarter * 32 + lane;  // the thread's row of its tile
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + lanes + t * kKeys, to = tmem + lanes + S::kColO + t * D;
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
         const uint4* const src = reinterpret_cast<const uint4*>(p.q + token * p.ld_q + static_cast<int64_t>(head) * D);
         float top = 0.0f;
         if (live && sub.j0 < sub.j1)
-#pragma unroll 8
+#pragma unroll 4
           for (int c = 0; c < D / 8; ++c) {
             const uint4 v = __ldg(src + c);
             const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
         mult = fmaxf(f.y * to_log2, 1e-37f);  // (not 0: a masked score is -inf times it)
         if (sub.j0 < sub.j1) {
           uint8_t* const row = smem + t * S::kQBytes + r * 128;
-#pragma unroll 8
+#pragma unroll 4
           for (int c = 0; c < D / 8; ++c) {
             const uint4 v = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
             const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -539,18 +541,33 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
         const int key = j * kKeys;
         const bool masked = key < sub.last_start || key + kKeys > sub.first_end;
         const int lo = begin - key, hi = end - key;  // columns [lo, hi) are seen
-        float top = -INFINITY;
+        if (masked) {  // (seldom, so apart from the rest and short)
+#pragma unroll 1
+          for (int c0 = 0; c0 < kKeys; c0 += 16) {
+            uint32_t w[16];
+            tmem_load(ts + c0, w);
 #pragma unroll
-        for (int c0 = 0; c0 < kKeys; c0 += 32) {
-          float v[32];
-          tmem_load32(ts + c0, v);
-          if (masked) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = c0 + c >= lo && c0 + c < hi ? v[c] : -INFINITY;
+            for (int c = 0; c < 16; ++c) w[c] = c0 + c >= lo && c0 + c < hi ? w[c] : 0xFF800000u;  // -inf
+            tmem_store(ts + c0, w);
           }
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) top = fmaxf(top, fmaxf(v[c], v[c + 1]));
         }
+        // (64 columns at a time, and twice: a thread has 128 registers)
+        float v[64];
+        auto fetch = [&](int c0) {
+          tmem_load32(ts + c0, v);
+          tmem_load32(ts + c0 + 32, v + 32);
+          tmem_load_wait(v);
+        };
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c0 = 0; c0 < kKeys; c0 += 64) {
+          fetch(c0);
+#pragma unroll
+          for (int c = 0; c < 64; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], fmaxf(v[c + k], v[c + k + 4]));
+        }
+        float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         top = top == -INFINITY ? top : top * mult;  // (0 * inf is no score)
         const bool above = top > m + kKvSlack;
         if (__any_sync(0xFFFFFFFFu, above)) {
@@ -570,26 +587,32 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
           m = moved;
         }
         const float off = kKvShift - m;
-        float2 sum = make_float2(0.0f, 0.0f);
+        uint32_t kept[kKeys > 64 ? 32 : 1];
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-        for (int c0 = 0; c0 < kKeys; c0 += 32) {
-          float v[32];
-          tmem_load32(ts + c0, v);
-          if (masked) {
+        for (int c0 = kKeys - 64; c0 >= 0; c0 -= 64) {  // (the last columns are still there)
+          if (c0 < kKeys - 64) fetch(c0);
+          uint32_t w[2][16];
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = c0 + c >= lo && c0 + c < hi ? v[c] : -INFINITY;
-          }
-          uint32_t w[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
+          for (int c = 0; c < 32; ++c) {
             float2 e = fma2(make_float2(v[2 * c], v[2 * c + 1]), make_float2(mult, mult), make_float2(off, off));
             e = make_float2(exp2_fast(e.x), exp2_fast(e.y));
-            sum = add2(sum, e);
-            w[c] = bits_of(__floats2half2_rn(e.x, e.y));
+            sum[c & 1] = add2(sum[c & 1], e);
+            w[c / 16][c % 16] = bits_of(__floats2half2_rn(e.x, e.y));
           }
-          tmem_store_nowait(ts + c0 / 2, w);  // (over columns that have been read)
+          if (kKeys > 64 && c0 > 0) {  // P goes over the first columns: kept until those have been read
+#pragma unroll
+            for (int k = 0; k < 32; ++k) kept[k] = w[k / 16][k % 16];
+          } else {
+            tmem_store_nowait(ts, w[0]);
+            tmem_store_nowait(ts + 16, w[1]);
+          }
         }
-        l += sum.x + sum.y;
+        if constexpr (kKeys > 64) {
+          tmem_store_nowait(ts + 32, *reinterpret_cast<const uint32_t(*)[16]>(kept));
+          tmem_store_nowait(ts + 48, *reinterpret_cast<const uint32_t(*)[16]>(kept + 16));
+        }
+        l += sum[0].x + sum[0].y + (sum[1].x + sum[1].y);
         tmem_store_wait();
         umma_fence_before();
         __syncwarp();
@@ -657,12 +680,6 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
       }
       umma_fence_before();  // (the tile's next product into O follows this warp's next arrival)
     }
-  } else if (warp == 2) {  // what this CTA begins and does not end
-    KvCut cut{0, 0, 0, -1, {}};
-    while (walk.next(g))
-      if (g.starts && !g.ends) cut = KvCut{g.s, g.tile, g.head, static_cast<int>((g.stop - 1) / start.per), {}};
-    KvCut* const cuts = reinterpret_cast<KvCut*>(p.part + static_cast<int64_t>(2) * kKvMaxCtas * S::kPartFloats);
-    if (lane == 0) cuts[blockIdx.x] = cut;
   }
   if (!ok && lane == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);
   __syncwarp();
