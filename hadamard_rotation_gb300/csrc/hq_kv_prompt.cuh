@@ -16,8 +16,9 @@
 //                 bytes are on their way meanwhile) into the swizzle that the products read
 //   warps 8..     softmax, a row per thread, four warps per tile; they also load and scale Q, correct O when a reference
 //                 moves, and finish the rows
-// In the order of issue, the product that writes S of a tile follows the one that reads its P, so neither needs a barrier
-// against the other; and when S of a tile is complete, so is the O that the correction changes.
+// Products into different columns need not end in the order of their issue, so what a product writes is never what an
+// earlier one may still read; but a commit covers all products before it: with two tiles of rows, when S of a tile is
+// complete, so is the O that the correction changes.
 //
 // The work, in key tiles, is laid end to end (sequence, head, rows) and cut into equal parts, one per CTA; what a cut
 // goes through is finished by k_kv_prompt_combine from parts in the workspace, in the order of the parts.
@@ -40,8 +41,10 @@ struct KvPromptShape {
   static constexpr int kUsed = kVAt + 2 * kKvBytes;
   static constexpr int kSmemBytes = kUsed < 116 * 1024 ? 116 * 1024 : kUsed;  // (a CTA takes all of tensor memory)
   static constexpr int kThreads = 32 * (8 + 4 * kSub);
-  static constexpr int kColO = kSub * kKeys;          // tensor memory: S of each tile, then O of each
-  static_assert(kColO + kSub * D <= 512, "tensor memory has 512 columns");
+  // Tensor memory: two of S, O of each tile, two of P; for D = 128 there is no room for P but in S's first columns.
+  static constexpr int kColO = 2 * kKeys, kColP = D == 128 ? 0 : kColO + kSub * D;
+  static constexpr int kStepP = D == 128 ? kKeys : kKeys / 2;  // columns from one P to the other
+  static_assert(kColO + kSub * D <= 512 && kColP + 2 * (kKeys / 2) <= 512, "tensor memory has 512 columns");
   static_assert(kSmemBytes + 1024 + 8192 <= 227 * 1024 && 2 * (kSmemBytes + 1024) > 228 * 1024, "one CTA per SM");
   static constexpr int kPerToken = 128 / kKeys;       // threads that widen a token
   static constexpr int kWords = D / 8 / kPerToken;    // words of codes of a thread, and a quarter as many pairs of scales
@@ -348,61 +351,102 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
   if (warp < 4) {
   if (warp == 0) {
     GemmRing kv;  // the place of key tile j + 1's keys; values follow one tile behind
-    uint32_t q_phase = 0, p_phase = 0;  // a bit per tile of rows (rows that see nothing of a segment take no part in it)
+    uint32_t q_phase = 0, p_phase = 0, o_phase = 0;  // a bit per barrier (rows that see nothing of a segment take no part in it)
     const uint64_t q_desc = desc_codes(smem_addr(smem)), k_desc = desc_codes(smem_addr(smem) + S::kKAt);
     const uint64_t v_desc = desc_across(smem_addr(smem) + S::kVAt, S::kAtomK);
     while (ok && walk.next(g)) {
-      const KvSub first = kv_sub<kRows, kKeys>(p, g, 0), second = kSub > 1 ? kv_sub<kRows, kKeys>(p, g, 1) : first;
       GemmRing vr = kv;
-      for (int j = g.j0 - 1; ok && j < g.j1; ++j) {
-        if (j >= g.j0) ok = warp_wait(smem_addr(&bars.v_full[vr.s]), vr.phase);
-        if (j + 1 < g.j1) ok = ok && warp_wait(smem_addr(&bars.k_full[kv.s]), kv.phase);
-#pragma unroll 1  // (short code: the roles share the instruction cache)
-        for (int t = 0; t < kSub && ok; ++t) {
-          const int t0 = t ? second.j0 : first.j0, t1 = t ? second.j1 : first.j1;
-          if (j >= t0 && j < t1) {  // O += P V
-            ok = warp_wait(smem_addr(&bars.p_full[t]), p_phase >> t & 1);
-            p_phase ^= 1u << t;
-            if (!ok) break;
-            umma_fence_after();
-            const uint64_t v = v_desc + vr.s * (S::kKvBytes >> 4);
-            if (elect_one()) {
-#pragma unroll 4
-              for (int i = 0; i < kKeys / 16; ++i)
-                umma_f16_ts<false>(tmem + S::kColO + t * D, tmem + t * kKeys + 8 * i, v + i * (2048 >> 4), kv_idesc(D, true),
-                                   j > t0 || i > 0);
-              if (j + 1 == t1) umma_commit<false>(smem_addr(&bars.o_full[t]));
-            }
-            __syncwarp();
-          }
-          if (j + 1 >= t0 && j + 1 < t1) {  // S = Q K^T
-            if (j + 1 == t0) {
-              ok = warp_wait(smem_addr(&bars.q_full[t]), q_phase >> t & 1);
-              q_phase ^= 1u << t;
-              if (!ok) break;
-            }
-            umma_fence_after();
-            const uint64_t q = q_desc + t * (S::kQBytes >> 4), k = k_desc + kv.s * (S::kKvBytes >> 4);
-            if (elect_one()) {
+      // S = Q K^T; `over`: into columns whose P the last product into O may still read.  Then the keys' second half goes first,
+      // whose scores lie beside P, and the first half's wait for that product costs nothing.
+      auto scores = [&](int t, int buffer, bool over) {
+        umma_fence_after();
+        const uint64_t q = q_desc + t * (S::kQBytes >> 4), k = k_desc + kv.s * (S::kKvBytes >> 4);
+        constexpr int kParts = D == 128 ? 2 : 1, kN = kKeys / kParts;
 #pragma unroll 1
-              for (int i = 0; i < D / 64; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                  umma_f16_ss(tmem + t * kKeys, q + i * (S::kAtomQ >> 4) + 2 * c, k + i * (S::kAtomK >> 4) + 2 * c,
-                              kv_idesc(kKeys, false), i > 0 || c > 0);
-              umma_commit<false>(smem_addr(&bars.s_full[t]));
-            }
-            __syncwarp();
+        for (int part = kParts - 1; part >= 0; --part) {
+          if (kParts > 1 && part == 0 && over) {
+            ok = warp_wait(smem_addr(&bars.o_full[t]), o_phase >> t & 1 ^ 1);
+            if (!ok) return;
+            umma_fence_after();
           }
+          if (elect_one()) {
+#pragma unroll 1
+            for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                umma_f16_ss(tmem + buffer * kKeys + part * kN, q + i * (S::kAtomQ >> 4) + 2 * c,
+                            k + i * (S::kAtomK >> 4) + part * (kN * 128 >> 4) + 2 * c, kv_idesc(kN, false), i > 0 || c > 0);
+            if (part == 0) umma_commit<false>(smem_addr(&bars.s_full[buffer]));
+          }
+          __syncwarp();
         }
-        if (!ok) break;
+      };
+      auto values = [&](int t, int buffer, bool more) {  // O += P V
+        umma_fence_after();
+        const uint64_t v = v_desc + vr.s * (S::kKvBytes >> 4);
         if (elect_one()) {
-          if (j >= g.j0) umma_commit<false>(smem_addr(&bars.v_empty[vr.s]));
-          if (j + 1 < g.j1) umma_commit<false>(smem_addr(&bars.k_empty[kv.s]));
+#pragma unroll 4
+          for (int i = 0; i < kKeys / 16; ++i)
+            umma_f16_ts<false>(tmem + S::kColO + t * D, tmem + S::kColP + buffer * S::kStepP + 8 * i, v + i * (2048 >> 4),
+                               kv_idesc(D, true), more || i > 0);
+          umma_commit<false>(smem_addr(&bars.o_full[t]));
         }
         __syncwarp();
-        if (j >= g.j0) vr.next(2);
-        if (j + 1 < g.j1) kv.next(2);
+        o_phase ^= 1u << t;
+      };
+      auto wait_bit = [&](uint64_t* bar, int t, uint32_t& phases) {
+        ok = ok && warp_wait(smem_addr(bar + t), phases >> t & 1);
+        phases ^= 1u << t;
+        return ok;
+      };
+      if constexpr (kSub == 1) {
+        // One tile of rows: two of S in turn, so the next scores are multiplied while these are exponentiated.
+        for (int j = g.j0 - 1; ok && j < g.j1; ++j) {
+          if (j + 1 < g.j1) {
+            if (j < g.j0 && !wait_bit(bars.q_full, 0, q_phase)) break;
+            ok = warp_wait(smem_addr(&bars.k_full[kv.s]), kv.phase);
+            if (!ok) break;
+            scores(0, (j + 1) & 1, false);
+            if (elect_one()) umma_commit<false>(smem_addr(&bars.k_empty[kv.s]));
+            __syncwarp();
+            kv.next(2);
+          }
+          if (j >= g.j0) {
+            ok = warp_wait(smem_addr(&bars.v_full[vr.s]), vr.phase);
+            if (!wait_bit(bars.p_full, j & 1, p_phase)) break;
+            values(0, j & 1, j > g.j0);
+            if (elect_one()) umma_commit<false>(smem_addr(&bars.v_empty[vr.s]));
+            __syncwarp();
+            vr.next(2);
+          }
+        }
+      } else {
+        const KvSub first = kv_sub<kRows, kKeys>(p, g, 0), second = kv_sub<kRows, kKeys>(p, g, 1);
+        for (int j = g.j0 - 1; ok && j < g.j1; ++j) {
+          if (j >= g.j0) ok = warp_wait(smem_addr(&bars.v_full[vr.s]), vr.phase);
+          if (j + 1 < g.j1) ok = ok && warp_wait(smem_addr(&bars.k_full[kv.s]), kv.phase);
+#pragma unroll 1  // (short code: the roles share the instruction cache)
+          for (int t = 0; t < kSub && ok; ++t) {
+            const int t0 = t ? second.j0 : first.j0, t1 = t ? second.j1 : first.j1;
+            if (j >= t0 && j < t1) {
+              if (!wait_bit(bars.p_full, t, p_phase)) break;
+              values(t, t, j > t0);
+            }
+            if (j + 1 >= t0 && j + 1 < t1) {
+              if (j + 1 == t0 && !wait_bit(bars.q_full, t, q_phase)) break;
+              scores(t, t, j >= t0);
+              if (!ok) break;
+            }
+          }
+          if (!ok) break;
+          if (elect_one()) {
+            if (j >= g.j0) umma_commit<false>(smem_addr(&bars.v_empty[vr.s]));
+            if (j + 1 < g.j1) umma_commit<false>(smem_addr(&bars.k_empty[kv.s]));
+          }
+          __syncwarp();
+          if (j >= g.j0) vr.next(2);
+          if (j + 1 < g.j1) kv.next(2);
+        }
       }
     }
     if (!ok) {  // let the products in flight finish (bounded) before tensor memory is freed
@@ -421,29 +465,35 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
     constexpr int kWords = S::kWords;
     const int tid = threadIdx.x - 128, t = tid % kKeys, half = tid / kKeys;  // (half of the channels, for D = 256)
     GemmRing ring;
-    // The page of the token in key tile j, -1 where the sequence has none: nothing past its end is read.  (These loads
-    // are volatile so that they stay a tile ahead of what waits for them.)
-    auto page_of = [&](int j) {
+    // (The loads are volatile so that they stay a tile ahead of what waits for them.)
+    struct Place {
+      int page;  // of the table's row
+      int unit;  // record in the page
+      int id;    // the page, as the table has it
+      bool live; // nothing past the sequence's end is read
+    };
+    auto look = [&](Place& at, int j) {  // the token of key tile j
       const int key = j * kKeys + t;
-      int page = -1;
-      if (j < g.j1 && key < g.seq.n)
-        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(page) : "l"(p.table + g.s * p.ld_table + key / (kKvUnit * p.page_units)));
-      return j < g.j1 && key < g.seq.n ? max(0, page) : -1;
+      at.live = j < g.j1 && key < g.seq.n;
+      if (at.live) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(at.id) : "l"(p.table + g.s * p.ld_table + at.page));
+    };
+    auto step = [&](Place& at) {
+      at.unit += kKeys / kKvUnit;
+      while (at.unit >= p.page_units) at.unit -= p.page_units, ++at.page;
     };
     auto load16 = [](uint32_t* to, const uint8_t* from) {
       asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(to[0]), "=r"(to[1]), "=r"(to[2]), "=r"(to[3]) : "l"(from));
     };
     // Its K (which = 0) or V: the codes of the thread and their scales (8; 4 for D = 64).
-    auto load = [&](int page, int j, int which, uint32_t (&w)[kWords], uint2& scales) {
+    auto load = [&](const Place& at, int which, uint32_t (&w)[kWords], uint2& scales) {
       scales = make_uint2(0, 0);  // (widened to zeros)
-      if (page < 0) return;
-      const int u = (j * kKeys + t) / kKvUnit % p.page_units, at = t % kKvUnit;
-      const int64_t pg = min(static_cast<int64_t>(page), p.pages - 1);
-      const uint8_t* const rec = p.cache + ((pg * p.kv_heads + g.head) * p.page_units + u) * R::kBytes;
-      const uint8_t* const codes = rec + which * R::kV + at * (D / 2) + half * (4 * kWords);
+      if (!at.live) return;
+      const int64_t page = min(static_cast<int64_t>(max(at.id, 0)), p.pages - 1);
+      const uint8_t* const rec = p.cache + ((page * p.kv_heads + g.head) * p.page_units + at.unit) * R::kBytes;
+      const uint8_t* const codes = rec + which * R::kV + t % kKvUnit * (D / 2) + half * (4 * kWords);
 #pragma unroll
       for (int i = 0; i < kWords; i += 4) load16(w + i, codes + 4 * i);
-      const uint8_t* const sc = rec + R::kKs + which * R::kScales + at * (D / 16) + half * 8;
+      const uint8_t* const sc = rec + R::kKs + which * R::kScales + t % kKvUnit * (D / 16) + half * 8;
       if constexpr (D == 64) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(scales.x) : "l"(sc));
       else asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(scales.x), "=r"(scales.y) : "l"(sc));
     };
@@ -465,78 +515,102 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
       if (g.j0 >= g.j1) continue;
       uint32_t k[kWords] = {}, v[kWords] = {};
       uint2 ks, vs;
-      int page = page_of(g.j0), ahead = page_of(g.j0 + 1);
-      load(page, g.j0, 0, k, ks);
-      load(page, g.j0, 1, v, vs);
+      Place now, ahead;
+      const int unit = (g.j0 * kKeys + t) / kKvUnit;
+      now.page = unit / p.page_units;
+      now.unit = unit - now.page * p.page_units;
+      now.id = ahead.id = 0;
+      look(now, g.j0);
+      load(now, 0, k, ks);
+      load(now, 1, v, vs);
+      ahead = now;
+      step(ahead);
+      look(ahead, g.j0 + 1);
       for (int j = g.j0; j < g.j1; ++j) {
-        page = ahead;
-        ahead = page_of(j + 2);
         ok = warp_wait(smem_addr(&bars.k_empty[ring.s]), ring.phase ^ 1);
         if (!ok) break;
         widen(smem + S::kKAt + ring.s * S::kKvBytes, k, ks);
         if (lane == 0) mbar_arrive(smem_addr(&bars.k_full[ring.s]));
-        load(page, j + 1, 0, k, ks);
+        // The next tile's place has landed with this tile's bytes.  (Used right after newer loads it would wait for those.)
+        now = ahead;
+        step(ahead);
+        look(ahead, j + 2);
+        load(now, 0, k, ks);
         ok = warp_wait(smem_addr(&bars.v_empty[ring.s]), ring.phase ^ 1);
         if (!ok) break;
         widen(smem + S::kVAt + ring.s * S::kKvBytes, v, vs);
         if (lane == 0) mbar_arrive(smem_addr(&bars.v_full[ring.s]));
-        load(page, j + 1, 1, v, vs);
+        load(now, 1, v, vs);
         ring.next(2);
       }
     }
   } else {
     const int t = (warp - 8) / 4, quarter = warp & 3, r = quarter * 32 + lane;  // the thread's row of its tile
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t ts = tmem + lanes + t * kKeys, to = tmem + lanes + S::kColO + t * D;
+    const uint32_t to = tmem + lanes + S::kColO + t * D;
     const float k_sg = kv_global_scale(__ldg(p.kv_amax)), v_sg = kv_global_scale(__ldg(p.kv_amax + 1));
     const float to_log2 = fabsf(p.scale) * 1.4426950408889634f * k_sg;
     uint32_t s_phase = 0, o_phase = 0;
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+    // 16 bytes of a row of the warp in the tile's Q; later the same of its output.
+    auto piece = [&](int row, int c) {
+      return smem + t * S::kQBytes + (c / 8) * S::kAtomQ + (quarter * 32 + row) * 128 + (((c % 8) ^ (row & 7)) << 4);
+    };
     while (ok && walk.next(g)) {
       const KvSub sub = kv_sub<kRows, kKeys>(p, g, t);
       const bool live = r < sub.live;
       const int at = g.tile * kRows + 128 * t + r, i = at / p.share;
       const int64_t token = g.seq.q0 + i;
       const int head = g.head * p.share + (at - i * p.share);
-      // Q
-      float mult;
-      {
-        const uint4* const src = reinterpret_cast<const uint4*>(p.q + token * p.ld_q + static_cast<int64_t>(head) * D);
-        float top = 0.0f;
-        if (live && sub.j0 < sub.j1)
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = __ldg(src + c);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      const bool some = sub.j0 < sub.j1;
+      // Q: the warp's rows along their channels, kLanes lanes a row.
+      float mult = 0.0f;
+      if (some) {
+        const int64_t mine = token * p.ld_q + static_cast<int64_t>(head) * D;
+        const int left = sub.live - quarter * 32;  // of the warp's rows
+#pragma unroll 1
+        for (int b = 0; b < kLanes; b += 8) {
+          uint4 v[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xFFFF0000u))));
+          for (int k = 0; k < 8; ++k) {
+            const int row = (b + k) * kAtOnce + lane / kLanes;
+            const int64_t from = __shfl_sync(0xFFFFFFFFu, mine, row);
+            v[k] = row < left ? __ldg(reinterpret_cast<const uint4*>(p.q + from) + lane % kLanes) : make_uint4(0, 0, 0, 0);
           }
-        const float2 f = kv_row_factor(top);
-        const float factor = p.scale < 0.0f ? -f.x : f.x;
-        mult = fmaxf(f.y * to_log2, 1e-37f);  // (not 0: a masked score is -inf times it)
-        if (sub.j0 < sub.j1) {
-          uint8_t* const row = smem + t * S::kQBytes + r * 128;
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int row = (b + k) * kAtOnce + lane / kLanes;
+            const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            float top = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[c] << 16)), fabsf(__uint_as_float(u[c] & 0xFFFF0000u))));
+#pragma unroll
+            for (int x = 1; x < kLanes; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+            const float2 f = kv_row_factor(top);
+            const float back = __shfl_sync(0xFFFFFFFFu, f.y, lane % kAtOnce * kLanes);
+            if (lane / kAtOnce == b + k) mult = back;
+            const float factor = p.scale < 0.0f ? -f.x : f.x;
             uint32_t o[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              o[k] = bits_of(__floats2half2_rn(__uint_as_float(u[k] << 16) * factor, __uint_as_float(u[k] & 0xFFFF0000u) * factor));
-            *reinterpret_cast<uint4*>(row + (c / 8) * S::kAtomQ + (((c % 8) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int c = 0; c < 4; ++c)
+              o[c] = bits_of(__floats2half2_rn(__uint_as_float(u[c] << 16) * factor, __uint_as_float(u[c] & 0xFFFF0000u) * factor));
+            *reinterpret_cast<uint4*>(piece(row, lane % kLanes)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&bars.q_full[t]));
         }
+        mult = fmaxf(mult * to_log2, 1e-37f);  // (not 0: a masked score is -inf times it)
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&bars.q_full[t]));
       }
       const int end = live ? g.seq.n - g.seq.nq + i + 1 : 0, begin = p.window ? end - p.window : 0;
       float m = kKvNone, l = 0.0f;
       for (int j = sub.j0; j < sub.j1; ++j) {
-        ok = warp_wait(smem_addr(&bars.s_full[t]), s_phase);
+        const int buffer = kSub == 1 ? j & 1 : t;
+        const uint32_t ts = tmem + lanes + buffer * kKeys, tp = tmem + lanes + S::kColP + buffer * S::kStepP;
+        ok = warp_wait(smem_addr(&bars.s_full[buffer]), s_phase >> buffer & 1);
         if (!ok) break;
-        s_phase ^= 1;
+        s_phase ^= 1u << buffer;
         umma_fence_after();
         const int key = j * kKeys;
         const bool masked = key < sub.last_start || key + kKeys > sub.first_end;
@@ -569,6 +643,11 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
         }
         float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         top = top == -INFINITY ? top : top * mult;  // (0 * inf is no score)
+        if (kSub == 1 && j > sub.j0) {  // (these scores did not wait for the product into O before this tile's)
+          ok = warp_wait(smem_addr(&bars.o_full[0]), o_phase ^ 1);
+          if (!ok) break;
+          umma_fence_after();
+        }
         const bool above = top > m + kKvSlack;
         if (__any_sync(0xFFFFFFFFu, above)) {
           const float moved = above ? top : m;
@@ -587,7 +666,7 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
           m = moved;
         }
         const float off = kKvShift - m;
-        uint32_t kept[kKeys > 64 ? 32 : 1];
+        uint32_t kept[D == 128 ? 32 : 1];
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
         for (int c0 = kKeys - 64; c0 >= 0; c0 -= 64) {  // (the last columns are still there)
@@ -600,35 +679,33 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
             sum[c & 1] = add2(sum[c & 1], e);
             w[c / 16][c % 16] = bits_of(__floats2half2_rn(e.x, e.y));
           }
-          if (kKeys > 64 && c0 > 0) {  // P goes over the first columns: kept until those have been read
+          if (D == 128 && c0 > 0) {  // P goes over S's first columns: kept until those have been read
 #pragma unroll
             for (int k = 0; k < 32; ++k) kept[k] = w[k / 16][k % 16];
           } else {
-            tmem_store_nowait(ts, w[0]);
-            tmem_store_nowait(ts + 16, w[1]);
+            tmem_store_nowait(tp + c0 / 2, w[0]);
+            tmem_store_nowait(tp + c0 / 2 + 16, w[1]);
           }
         }
-        if constexpr (kKeys > 64) {
-          tmem_store_nowait(ts + 32, *reinterpret_cast<const uint32_t(*)[16]>(kept));
-          tmem_store_nowait(ts + 48, *reinterpret_cast<const uint32_t(*)[16]>(kept + 16));
+        if constexpr (D == 128) {
+          tmem_store_nowait(tp + 32, *reinterpret_cast<const uint32_t(*)[16]>(kept));
+          tmem_store_nowait(tp + 48, *reinterpret_cast<const uint32_t(*)[16]>(kept + 16));
         }
         l += sum[0].x + sum[0].y + (sum[1].x + sum[1].y);
         tmem_store_wait();
         umma_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&bars.p_full[t]));
+        if (lane == 0) mbar_arrive(smem_addr(&bars.p_full[buffer]));
+        o_phase ^= 1;
       }
       if (!ok) break;
-      const bool some = sub.j0 < sub.j1;
       if (some) {
-        ok = warp_wait(smem_addr(&bars.o_full[t]), o_phase);
+        ok = warp_wait(smem_addr(&bars.o_full[t]), o_phase ^ 1);
         if (!ok) break;
-        o_phase ^= 1;
         umma_fence_after();
       }
       if (g.starts && g.ends) {
         const float f = l > 0.0f || l != l ? __fdiv_rn(v_sg, l) : 0.0f;
-        __nv_bfloat16* const out = p.out + (token * p.heads + head) * D;
         if (D == 256 && p.group == 256 && some) {  // the butterfly across the blocks of 16, in place
 #pragma unroll 1
           for (int c = 0; c < 16; ++c) {
@@ -657,11 +734,19 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
             const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(w[2 * c]) * f, __uint_as_float(w[2 * c + 1]) * f);
             o[c] = l == 0.0f ? 0u : *reinterpret_cast<const uint32_t*>(&h);
           }
-          if (live) {
-            reinterpret_cast<uint4*>(out + c0)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            reinterpret_cast<uint4*>(out + c0)[1] = make_uint4(o[4], o[5], o[6], o[7]);
-          }
+          *reinterpret_cast<uint4*>(piece(lane, c0 / 8)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(piece(lane, c0 / 8 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
+        __syncwarp();
+        const int64_t mine = (token * p.heads + head) * D;  // rows leave along their channels
+#pragma unroll 4
+        for (int b = 0; b < kLanes; ++b) {
+          const int row = b * kAtOnce + lane / kLanes;
+          const int64_t to_row = __shfl_sync(0xFFFFFFFFu, mine, row);
+          if (row < sub.live - quarter * 32)
+            reinterpret_cast<uint4*>(p.out + to_row)[lane % kLanes] = *reinterpret_cast<const uint4*>(piece(row, lane % kLanes));
+        }
+        __syncwarp();
         if (p.lse && live)
           p.lse[token * p.heads + head] = l > 0.0f || l != l ? (m - kKvShift + log2f(l)) * 0.6931471805599453f : -INFINITY;
       } else {  // (an item that began before is the share's first segment, one that goes on its last)
