@@ -12,9 +12,10 @@
 // Roles of a CTA:
 //   warp 0        issues the products
 //   warp 1        allocates tensor memory
-//   warps 4..7    widen keys and values: a token per thread, from global memory through registers (the next tile's
-//                 bytes are on their way meanwhile) into the swizzle that the products read
-//   warps 8..     softmax, a row per thread, four warps per tile; they also load and scale Q, correct O when a reference
+//   warp 2        the segments of the CTA's share, one after another, for the other roles
+//   warps 4..11   widen keys (4..7) and values: a token per thread, from global memory through registers (the next
+//                 tile's bytes are on their way meanwhile) into the swizzle that the products read
+//   warps 12..    softmax, a row per thread, four warps per tile; they also load and scale Q, correct O when a reference
 //                 moves, and finish the rows
 // Products into different columns need not end in the order of their issue, so what a product writes is never what an
 // earlier one may still read; but a commit covers all products before it: with two tiles of rows, when S of a tile is
@@ -40,12 +41,16 @@ struct KvPromptShape {
   static constexpr int kQAt = 0, kKAt = kSub * kQBytes, kVAt = kKAt + 2 * kKvBytes;
   static constexpr int kUsed = kVAt + 2 * kKvBytes;
   static constexpr int kSmemBytes = kUsed < 116 * 1024 ? 116 * 1024 : kUsed;  // (a CTA takes all of tensor memory)
-  static constexpr int kThreads = 32 * (8 + 4 * kSub);
+  static constexpr int kThreads = 32 * (12 + 4 * kSub);
   // Tensor memory: two of S, O of each tile, two of P; for D = 128 there is no room for P but in S's first columns.
   static constexpr int kColO = 2 * kKeys, kColP = D == 128 ? 0 : kColO + kSub * D;
   static constexpr int kStepP = D == 128 ? kKeys : kKeys / 2;  // columns from one P to the other
   static_assert(kColO + kSub * D <= 512 && kColP + 2 * (kKeys / 2) <= 512, "tensor memory has 512 columns");
   static_assert(kSmemBytes + 1024 + 8192 <= 227 * 1024 && 2 * (kSmemBytes + 1024) > 228 * 1024, "one CTA per SM");
+  // Registers of a thread: at the launch, and by role.
+  static constexpr int kRegsLaunch = kSub == 1 ? 128 : 96, kRegsControl = kSub == 1 ? 80 : 64, kRegsWiden = kSub == 1 ? 80 : 64;
+  static constexpr int kRegsSoftmax = kSub == 1 ? 184 : 144;
+  static_assert(128 * kRegsControl + 256 * kRegsWiden + 128 * kSub * kRegsSoftmax <= kThreads * kRegsLaunch, "what the launch has");
   static constexpr int kPerToken = 128 / kKeys;       // threads that widen a token
   static constexpr int kWords = D / 8 / kPerToken;    // words of codes of a thread, and a quarter as many pairs of scales
   static constexpr int kPartFloats = kRows * (D + 2);
@@ -247,7 +252,21 @@ __device__ __forceinline__ KvSub kv_sub(const KvAttendParams& p, const Segment& 
   return r;
 }
 
+// A segment as the roles see it, handed to them through a ring in shared memory: worked out once, by a warp of its own,
+// instead of in every role's registers and code.
+struct KvTask {
+  const int32_t* table;  // the sequence's pages; NULL: there are no more segments
+  KvSeq seq;
+  int head, tile;
+  int j0, j1;            // key tiles
+  int starts, ends;
+  KvSub sub[2];
+};
+constexpr int kKvTasks = 8;
+
 struct KvPromptBars {
+  uint64_t task_full[kKvTasks], task_empty[kKvTasks];
+  KvTask tasks[kKvTasks];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
   uint64_t drain;
@@ -333,6 +352,10 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
       mbar_init(smem_addr(&bars.p_full[i]), 4);
       mbar_init(smem_addr(&bars.o_full[i]), 1);
     }
+    for (int i = 0; i < kKvTasks; ++i) {
+      mbar_init(smem_addr(&bars.task_full[i]), 1);
+      mbar_init(smem_addr(&bars.task_empty[i]), 9 + 4 * kSub);  // (the warps of the roles)
+    }
     mbar_init(smem_addr(&bars.drain), 1);
     fence_mbar_init();
   }
@@ -344,42 +367,49 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
   umma_fence_after();
   const uint32_t tmem = bars.tmem;
   const KvStart start = kv_plan<kRows, kKeys>(p, sums, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x));
-  Walk walk(p, start);
-  Segment g;
+  GemmRing turn;  // of the tasks
   bool ok = true;
+  // The next segment, for a warp of a role; it is copied, and its place free, before the role goes on.
+  auto next = [&](KvTask& g) {
+    ok = ok && warp_wait(smem_addr(&bars.task_full[turn.s]), turn.phase);
+    if (!ok) return false;
+    g = bars.tasks[turn.s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&bars.task_empty[turn.s]));
+    turn.next(kKvTasks);
+    return g.table != nullptr;
+  };
 
+  // Registers where they are used: a thread of the softmax holds half a row of a key tile.
   if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsControl));
   if (warp == 0) {
     GemmRing kv;  // the place of key tile j + 1's keys; values follow one tile behind
     uint32_t q_phase = 0, p_phase = 0, o_phase = 0;  // a bit per barrier (rows that see nothing of a segment take no part in it)
     const uint64_t q_desc = desc_codes(smem_addr(smem)), k_desc = desc_codes(smem_addr(smem) + S::kKAt);
     const uint64_t v_desc = desc_across(smem_addr(smem) + S::kVAt, S::kAtomK);
-    while (ok && walk.next(g)) {
+    KvTask g;
+    while (ok && next(g)) {
       GemmRing vr = kv;
-      // S = Q K^T; `over`: into columns whose P the last product into O may still read.  Then the keys' second half goes first,
-      // whose scores lie beside P, and the first half's wait for that product costs nothing.
+      // S = Q K^T; `over`: into columns whose P the last product into O may still read.  (In two halves, of which only the
+      // one over P waits, the products of 64 columns take as long as those of 128: 778 us for four prompts in place of XXX.)
       auto scores = [&](int t, int buffer, bool over) {
+        if (D == 128 && over) {
+          ok = warp_wait(smem_addr(&bars.o_full[t]), o_phase >> t & 1 ^ 1);
+          if (!ok) return;
+        }
         umma_fence_after();
         const uint64_t q = q_desc + t * (S::kQBytes >> 4), k = k_desc + kv.s * (S::kKvBytes >> 4);
-        constexpr int kParts = D == 128 ? 2 : 1, kN = kKeys / kParts;
+        if (elect_one()) {
 #pragma unroll 1
-        for (int part = kParts - 1; part >= 0; --part) {
-          if (kParts > 1 && part == 0 && over) {
-            ok = warp_wait(smem_addr(&bars.o_full[t]), o_phase >> t & 1 ^ 1);
-            if (!ok) return;
-            umma_fence_after();
-          }
-          if (elect_one()) {
-#pragma unroll 1
-            for (int i = 0; i < D / 64; ++i)
+          for (int i = 0; i < D / 64; ++i)
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                umma_f16_ss(tmem + buffer * kKeys + part * kN, q + i * (S::kAtomQ >> 4) + 2 * c,
-                            k + i * (S::kAtomK >> 4) + part * (kN * 128 >> 4) + 2 * c, kv_idesc(kN, false), i > 0 || c > 0);
-            if (part == 0) umma_commit<false>(smem_addr(&bars.s_full[buffer]));
-          }
-          __syncwarp();
+            for (int c = 0; c < 4; ++c)
+              umma_f16_ss(tmem + buffer * kKeys, q + i * (S::kAtomQ >> 4) + 2 * c, k + i * (S::kAtomK >> 4) + 2 * c,
+                          kv_idesc(kKeys, false), i > 0 || c > 0);
+          umma_commit<false>(smem_addr(&bars.s_full[buffer]));
         }
+        __syncwarp();
       };
       auto values = [&](int t, int buffer, bool more) {  // O += P V
         umma_fence_after();
@@ -421,13 +451,12 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
           }
         }
       } else {
-        const KvSub first = kv_sub<kRows, kKeys>(p, g, 0), second = kv_sub<kRows, kKeys>(p, g, 1);
         for (int j = g.j0 - 1; ok && j < g.j1; ++j) {
           if (j >= g.j0) ok = warp_wait(smem_addr(&bars.v_full[vr.s]), vr.phase);
           if (j + 1 < g.j1) ok = ok && warp_wait(smem_addr(&bars.k_full[kv.s]), kv.phase);
 #pragma unroll 1  // (short code: the roles share the instruction cache)
           for (int t = 0; t < kSub && ok; ++t) {
-            const int t0 = t ? second.j0 : first.j0, t1 = t ? second.j1 : first.j1;
+            const int t0 = t ? g.sub[1].j0 : g.sub[0].j0, t1 = t ? g.sub[1].j1 : g.sub[0].j1;
             if (j >= t0 && j < t1) {
               if (!wait_bit(bars.p_full, t, p_phase)) break;
               values(t, t, j > t0);
@@ -454,17 +483,43 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
       __syncwarp();
       mbar_wait(smem_addr(&bars.drain), 0);
     }
-  } else if (warp == 2) {  // what this CTA begins and does not end
+  } else if (warp == 2) {  // the segments; and of the items that this CTA begins the one that it does not end
+    Walk walk(p, start);
+    Segment g;
     KvCut cut{0, 0, 0, -1, {}};
-    while (walk.next(g))
-      if (g.starts && !g.ends) cut = KvCut{g.s, g.tile, g.head, static_cast<int>((g.stop - 1) / start.per), {}};
+    for (bool more = true; more;) {
+      more = walk.next(g);
+      if (more && g.starts && !g.ends) cut = KvCut{g.s, g.tile, g.head, static_cast<int>((g.stop - 1) / start.per), {}};
+      ok = warp_wait(smem_addr(&bars.task_empty[turn.s]), turn.phase ^ 1);
+      if (!ok) break;
+      KvTask& to = bars.tasks[turn.s];
+      if (lane == 0) {
+        to.table = more ? p.table + g.s * p.ld_table : nullptr;
+        if (more) {
+          to.seq = g.seq;
+          to.head = g.head, to.tile = g.tile;
+          to.j0 = g.j0, to.j1 = g.j1;
+          to.starts = g.starts, to.ends = g.ends;
+        }
+      } else if (more && lane <= kSub) {
+        to.sub[lane - 1] = kv_sub<kRows, kKeys>(p, g, lane - 1);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&bars.task_full[turn.s]));
+      turn.next(kKvTasks);
+    }
     KvCut* const cuts = reinterpret_cast<KvCut*>(p.part + static_cast<int64_t>(2) * kKvMaxCtas * S::kPartFloats);
     if (lane == 0) cuts[blockIdx.x] = cut;
   }
-  } else if (warp < 8) {
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsWiden));
     constexpr int kWords = S::kWords;
-    const int tid = threadIdx.x - 128, t = tid % kKeys, half = tid / kKeys;  // (half of the channels, for D = 256)
+    const int which = warp >= 8;  // K or V
+    const int tid = threadIdx.x & 127, t = tid % kKeys, half = tid / kKeys;  // (half of the channels, for D = 256)
+    uint64_t *const full = which ? bars.v_full : bars.k_full, *const empty = which ? bars.v_empty : bars.k_empty;
+    uint8_t* const tiles = smem + (which ? S::kVAt : S::kKAt);
     GemmRing ring;
+    KvTask g = {};
     // (The loads are volatile so that they stay a tile ahead of what waits for them.)
     struct Place {
       int page;  // of the table's row
@@ -475,7 +530,7 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
     auto look = [&](Place& at, int j) {  // the token of key tile j
       const int key = j * kKeys + t;
       at.live = j < g.j1 && key < g.seq.n;
-      if (at.live) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(at.id) : "l"(p.table + g.s * p.ld_table + at.page));
+      if (at.live) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(at.id) : "l"(g.table + at.page));
     };
     auto step = [&](Place& at) {
       at.unit += kKeys / kKvUnit;
@@ -484,8 +539,8 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
     auto load16 = [](uint32_t* to, const uint8_t* from) {
       asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(to[0]), "=r"(to[1]), "=r"(to[2]), "=r"(to[3]) : "l"(from));
     };
-    // Its K (which = 0) or V: the codes of the thread and their scales (8; 4 for D = 64).
-    auto load = [&](const Place& at, int which, uint32_t (&w)[kWords], uint2& scales) {
+    // The codes of the thread and their scales (8; 4 for D = 64).
+    auto load = [&](const Place& at, uint32_t (&w)[kWords], uint2& scales) {
       scales = make_uint2(0, 0);  // (widened to zeros)
       if (!at.live) return;
       const int64_t page = min(static_cast<int64_t>(max(at.id, 0)), p.pages - 1);
@@ -511,41 +566,36 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
       fence_proxy_async_smem();
       __syncwarp();
     };
-    while (ok && walk.next(g)) {
+    while (ok && next(g)) {
       if (g.j0 >= g.j1) continue;
-      uint32_t k[kWords] = {}, v[kWords] = {};
-      uint2 ks, vs;
+      uint32_t codes[kWords] = {};
+      uint2 scales;
       Place now, ahead;
       const int unit = (g.j0 * kKeys + t) / kKvUnit;
       now.page = unit / p.page_units;
       now.unit = unit - now.page * p.page_units;
       now.id = ahead.id = 0;
       look(now, g.j0);
-      load(now, 0, k, ks);
-      load(now, 1, v, vs);
+      load(now, codes, scales);
       ahead = now;
       step(ahead);
       look(ahead, g.j0 + 1);
       for (int j = g.j0; j < g.j1; ++j) {
-        ok = warp_wait(smem_addr(&bars.k_empty[ring.s]), ring.phase ^ 1);
+        ok = warp_wait(smem_addr(empty + ring.s), ring.phase ^ 1);
         if (!ok) break;
-        widen(smem + S::kKAt + ring.s * S::kKvBytes, k, ks);
-        if (lane == 0) mbar_arrive(smem_addr(&bars.k_full[ring.s]));
+        widen(tiles + ring.s * S::kKvBytes, codes, scales);
+        if (lane == 0) mbar_arrive(smem_addr(full + ring.s));
+        ring.next(2);
         // The next tile's place has landed with this tile's bytes.  (Used right after newer loads it would wait for those.)
         now = ahead;
         step(ahead);
         look(ahead, j + 2);
-        load(now, 0, k, ks);
-        ok = warp_wait(smem_addr(&bars.v_empty[ring.s]), ring.phase ^ 1);
-        if (!ok) break;
-        widen(smem + S::kVAt + ring.s * S::kKvBytes, v, vs);
-        if (lane == 0) mbar_arrive(smem_addr(&bars.v_full[ring.s]));
-        load(now, 1, v, vs);
-        ring.next(2);
+        load(now, codes, scales);
       }
     }
   } else {
-    const int t = (warp - 8) / 4, quarter = warp & 3, r = quarter * 32 + lane;  // the thread's row of its tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsSoftmax));
+    const int t = (warp - 12) / 4, quarter = warp & 3, r = quarter * 32 + lane;  // the thread's row of its tile
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t to = tmem + lanes + S::kColO + t * D;
     const float k_sg = kv_global_scale(__ldg(p.kv_amax)), v_sg = kv_global_scale(__ldg(p.kv_amax + 1));
@@ -556,8 +606,9 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
     auto piece = [&](int row, int c) {
       return smem + t * S::kQBytes + (c / 8) * S::kAtomQ + (quarter * 32 + row) * 128 + (((c % 8) ^ (row & 7)) << 4);
     };
-    while (ok && walk.next(g)) {
-      const KvSub sub = kv_sub<kRows, kKeys>(p, g, t);
+    KvTask g;
+    while (ok && next(g)) {
+      const KvSub sub = t ? g.sub[1] : g.sub[0];
       const bool live = r < sub.live;
       const int at = g.tile * kRows + 128 * t + r, i = at / p.share;
       const int64_t token = g.seq.q0 + i;
@@ -634,7 +685,7 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
         };
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c0 = 0; c0 < kKeys; c0 += 64) {
+        for (int c0 = kKeys - 64; c0 >= 0; c0 -= 64) {
           fetch(c0);
 #pragma unroll
           for (int c = 0; c < 64; c += 8)
@@ -666,30 +717,23 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
           m = moved;
         }
         const float off = kKvShift - m;
-        uint32_t kept[D == 128 ? 32 : 1];
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-        for (int c0 = kKeys - 64; c0 >= 0; c0 -= 64) {  // (the last columns are still there)
-          if (c0 < kKeys - 64) fetch(c0);
-          uint32_t w[2][16];
+        for (int c0 = 0; c0 < kKeys; c0 += 64) {  // (the first columns are still there)
+          if (c0 > 0) fetch(c0);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            float2 e = fma2(make_float2(v[2 * c], v[2 * c + 1]), make_float2(mult, mult), make_float2(off, off));
-            e = make_float2(exp2_fast(e.x), exp2_fast(e.y));
-            sum[c & 1] = add2(sum[c & 1], e);
-            w[c / 16][c % 16] = bits_of(__floats2half2_rn(e.x, e.y));
-          }
-          if (D == 128 && c0 > 0) {  // P goes over S's first columns: kept until those have been read
+          for (int half = 0; half < 2; ++half) {
+            uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) kept[k] = w[k / 16][k % 16];
-          } else {
-            tmem_store_nowait(tp + c0 / 2, w[0]);
-            tmem_store_nowait(tp + c0 / 2 + 16, w[1]);
+            for (int c = 0; c < 16; ++c) {
+              const int at = 32 * half + 2 * c;
+              float2 e = fma2(make_float2(v[at], v[at + 1]), make_float2(mult, mult), make_float2(off, off));
+              e = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+              sum[c & 1] = add2(sum[c & 1], e);
+              w[c] = bits_of(__floats2half2_rn(e.x, e.y));
+            }
+            tmem_store_nowait(tp + c0 / 2 + 16 * half, w);  // (D = 128: over columns of S that have been read)
           }
-        }
-        if constexpr (D == 128) {
-          tmem_store_nowait(tp + 32, *reinterpret_cast<const uint32_t(*)[16]>(kept));
-          tmem_store_nowait(tp + 48, *reinterpret_cast<const uint32_t(*)[16]>(kept + 16));
         }
         l += sum[0].x + sum[0].y + (sum[1].x + sum[1].y);
         tmem_store_wait();
