@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
           tmem_load_wait(v);
         };
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
         for (int c0 = kKeys - 64; c0 >= 0; c0 -= 64) {
           fetch(c0);
 #pragma unroll
@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
         }
         const float off = kKvShift - m;
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < kKeys; c0 += 64) {  // (the first columns are still there)
           if (c0 > 0) fetch(c0);
 #pragma unroll
