@@ -2,7 +2,7 @@
 // the 5th-generation tensor cores.
 //
 // The mathematics and the number formats are those of hq_kv_attend.cuh: codes widened exactly to f16, q scaled by a power of
-// two per row, p in f16 scaled by 2^7 against a reference that moves only when a score exceeds it by 2^8.
+// two per row, p in f16 scaled by 2^7 against a reference that moves only when a score exceeds it by 2^8 (and then by a power of two).
 //
 // A CTA takes 128 rows (query token, head of the group that shares a key head) per tile of the tensor core and, up to D =
 // 128, two such tiles at once, so that the scores of one are multiplied while the other's are exponentiated.  Keys come
@@ -69,7 +69,7 @@ struct KvCut {
 
 constexpr int64_t kKvMinTiles = 6;  // of work per CTA at least
 // What an item costs beside its key tiles (Q, the first scores, the rows' end), as work of this many tiles before its first.
-constexpr int kKvItemTiles = 2;
+constexpr int kKvItemTiles = 3;
 
 // Key tiles of the rows `tile` of a sequence: [first, first + n) of `keys` keys.
 struct KvReach {
@@ -262,7 +262,7 @@ struct KvTask {
   int starts, ends;
   KvSub sub[2];
 };
-constexpr int kKvTasks = 8;
+constexpr int kKvTasks = 3;
 
 struct KvPromptBars {
   uint64_t task_full[kKvTasks], task_empty[kKvTasks];
@@ -306,22 +306,25 @@ __device__ __forceinline__ uint64_t desc_across(uint32_t addr, int atom) {
          (uint64_t{1} << 46) | (uint64_t{2} << 61);
 }
 
-// Sixteen columns of the thread's row through the rotation's butterfly.
-__device__ __forceinline__ void kv_butterfly(uint32_t (&w)[16], float c) {
-  float x[16];
+// Sixteen columns of the thread's row through the rotation's butterfly (not yet divided by 4).
+__device__ __forceinline__ void kv_butterfly(uint32_t (&w)[16]) {
+  float2 x[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(w[i]);
+  for (int i = 0; i < 8; ++i) {
+    const float a = __uint_as_float(w[2 * i]), b = __uint_as_float(w[2 * i + 1]);
+    x[i] = make_float2(a + b, a - b);
+  }
 #pragma unroll
-  for (int h = 1; h < 16; h <<= 1)
+  for (int h = 1; h < 8; h <<= 1)
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 8; ++i)
       if ((i & h) == 0) {
-        const float a = x[i], b = x[i + h];
-        x[i] = a + b;
-        x[i + h] = a - b;
+        const float2 a = x[i], b = x[i + h];
+        x[i] = add2(a, b);
+        x[i + h] = sub2(a, b);
       }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(x[i] * c);
+  for (int i = 0; i < 8; ++i) w[2 * i] = __float_as_uint(x[i].x), w[2 * i + 1] = __float_as_uint(x[i].y);
 }
 
 template <int D>
@@ -507,6 +510,12 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&bars.task_full[turn.s]));
       turn.next(kKvTasks);
+      if (more && g.j0 < g.j1)  // its rows of Q into the L2: they are read once, with nothing else to do
+        for (int r = g.tile * kRows + lane; r < min((g.tile + 1) * kRows, g.seq.nq * p.share); r += 32) {
+          const __nv_bfloat16* const row = p.q + (g.seq.q0 + r / p.share) * p.ld_q + (static_cast<int64_t>(g.head) * p.share + r % p.share) * D;
+#pragma unroll
+          for (int c = 0; c < D; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
+        }
     }
     KvCut* const cuts = reinterpret_cast<KvCut*>(p.part + static_cast<int64_t>(2) * kKvMaxCtas * S::kPartFloats);
     if (lane == 0) cuts[blockIdx.x] = cut;
@@ -676,51 +685,51 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
             tmem_store(ts + c0, w);
           }
         }
-        // (64 columns at a time, and twice: a thread has 128 registers)
-        float v[64];
-        auto fetch = [&](int c0) {
-          tmem_load32(ts + c0, v);
-          tmem_load32(ts + c0 + 32, v + 32);
-          tmem_load_wait(v);
-        };
-        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-        for (int c0 = kKeys - 64; c0 >= 0; c0 -= 64) {
-          fetch(c0);
-#pragma unroll
-          for (int c = 0; c < 64; c += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], fmaxf(v[c + k], v[c + k + 4]));
-        }
-        float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-        top = top == -INFINITY ? top : top * mult;  // (0 * inf is no score)
         if (kSub == 1 && j > sub.j0) {  // (these scores did not wait for the product into O before this tile's)
           ok = warp_wait(smem_addr(&bars.o_full[0]), o_phase ^ 1);
           if (!ok) break;
           umma_fence_after();
         }
-        const bool above = top > m + kKvSlack;
-        if (__any_sync(0xFFFFFFFFu, above)) {
-          const float moved = above ? top : m;
-          if (j > sub.j0) {
-            const float f = exp2_fast(m - moved);
-            l *= f;
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 16) {
-              uint32_t w[16];
-              tmem_load(to + c0, w);
+        // 64 columns at a time, in one pass: where a score leaves the reference's reach, what has been summed against it is
+        // scaled by a power of two, which is exact.
+#pragma unroll 1  // (short code: the roles share the instruction cache)
+        for (int c0 = 0; c0 < kKeys; c0 += 64) {
+          float v[64];
+          tmem_load32(ts + c0, v);
+          tmem_load32(ts + c0 + 32, v + 32);
+          tmem_load_wait(v);
+          float tops[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-              for (int c = 0; c < 16; ++c) w[c] = __float_as_uint(__uint_as_float(w[c]) * f);
-              tmem_store(to + c0, w);
-            }
-          }
-          m = moved;
-        }
-        const float off = kKvShift - m;
-        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+          for (int c = 4; c < 64; c += 4)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], v[c + k]);
+          float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+          top = top == -INFINITY ? top : top * mult;  // (-inf: no score)
+          const bool above = top > m + kKvSlack;
+          if (__any_sync(0xFFFFFFFFu, above)) {
+            const float moved = !above ? m : m == kKvNone ? top : m + ceilf(top - m);
+            const float f = exp2_fast(m - moved);
+            m = moved;
+            l *= f;
+            auto scale = [&](uint32_t at, int columns, auto by) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < kKeys; c0 += 64) {  // (the first columns are still there)
-          if (c0 > 0) fetch(c0);
+              for (int c = 0; c < columns; c += 16) {
+                uint32_t w[16];
+                tmem_load(at + c, w);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) w[k] = by(w[k]);
+                tmem_store(at + c, w);
+              }
+            };
+            if (j > sub.j0) scale(to, D, [&](uint32_t w) { return __float_as_uint(__uint_as_float(w) * f); });
+            if (c0 > 0)
+              scale(tp, c0 / 2, [&](uint32_t w) {
+                const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                return bits_of(__floats2half2_rn(e.x * f, e.y * f));
+              });
+          }
+          const float off = kKvShift - m;
+          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t w[16];
@@ -734,8 +743,8 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
             }
             tmem_store_nowait(tp + c0 / 2 + 16 * half, w);  // (D = 128: over columns of S that have been read)
           }
+          l += sum[0].x + sum[0].y + (sum[1].x + sum[1].y);
         }
-        l += sum[0].x + sum[0].y + (sum[1].x + sum[1].y);
         tmem_store_wait();
         umma_fence_before();
         __syncwarp();
@@ -749,7 +758,7 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
         umma_fence_after();
       }
       if (g.starts && g.ends) {
-        const float f = l > 0.0f || l != l ? __fdiv_rn(v_sg, l) : 0.0f;
+        const float f = l > 0.0f || l != l ? __fdiv_rn(v_sg, l) * (p.group == 256 ? 0.0625f : p.group ? 0.25f : 1.0f) : 0.0f;
         if (D == 256 && p.group == 256 && some) {  // the butterfly across the blocks of 16, in place
 #pragma unroll 1
           for (int c = 0; c < 16; ++c) {
@@ -760,18 +769,18 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
             for (int k = 0; k < 16; ++k) asm volatile("" : "+r"(w[k]));  // (not used before the wait)
-            kv_butterfly(w, 0.25f);
+            kv_butterfly(w);
 #pragma unroll
             for (int k = 0; k < 16; ++k)
               asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(to + (16 * k + c) % D), "r"(w[k]) : "memory");
             tmem_store_wait();
           }
         }
-#pragma unroll 1
+#pragma unroll 2
         for (int c0 = 0; c0 < D; c0 += 16) {
           uint32_t w[16] = {};
           if (some) tmem_load(to + c0, w);
-          if (p.group) kv_butterfly(w, 0.25f);
+          if (p.group) kv_butterfly(w);
           uint32_t o[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
