@@ -25,6 +25,8 @@
 // (cp.async.bulk, one per record), and the other warps take them in turn.
 #pragma once
 
+#include <type_traits>
+
 #include "hq_kv.cuh"
 
 namespace hq {
@@ -57,12 +59,15 @@ constexpr float kKvSlack = 8.0f, kKvShift = 7.0f;
 template <int D, int NT>
 struct KvAttendShape {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kWarps = D == 256 ? (NT == 1 ? 8 : 4) : (NT == 1 || D == 64) ? 12 : 8;  // that multiply
+  static constexpr int kWarps = D == 256 ? (NT == 1 ? 11 : 7) : NT == 1 ? 15 : D == 64 ? 15 : 11;  // that multiply
   static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kUnit = KvRecord<D>::kBytes;
   static constexpr int kPitch = D + 4;  // floats of a row of the warps' sums
   static constexpr int kMergeBytes = kWarps * kRows * kPitch * 4;
-  static constexpr int kSlots = (222 * 1024 - kMergeBytes) / kUnit < 96 ? (222 * 1024 - kMergeBytes) / kUnit : 96;
+  // Places of the ring; each belongs to one warp.  (Else a warp could come to a place whose copy before its own has not
+  // landed for another warp, where the parity says that its own has.)
+  static constexpr int kFit = (222 * 1024 - kMergeBytes) / kUnit, kSlots = (kFit < 96 ? kFit : 96) / kWarps * kWarps;
+  static_assert(kSlots >= 2 * kWarps, "copies ahead of every warp");
   static constexpr int kSmemBytes = kSlots * kUnit + kMergeBytes;
   static constexpr int kPartFloats = kRows * (D + 2);
 };
@@ -413,19 +418,31 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
         l[nt][0] = l[nt][1] = 0.0f;
       }
       const int skip = (warp + kWarps - static_cast<int>(k0 % kWarps)) % kWarps;
-      for (int u = g.u0 + skip; u < g.u1; u += kWarps) {
-        if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&full[slot]), pass));
-        if (!ok) break;
-        const uint8_t* const rec = kv_smem + slot * S::kUnit;
-        // S^T
-        float s[NT][4];
-        {
+      // U records at once, kWarps apart: what comes with a step is shared by them, and their chains run side by side.
+      auto take = [&](int u, auto count) {
+        constexpr int U = decltype(count)::value;
+        const uint8_t* rec[U];
+        uint32_t done[U];
+#pragma unroll
+        for (int x = 0; x < U; ++x) {
+          ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&full[slot]), pass));
+          rec[x] = kv_smem + slot * S::kUnit;
+          done[x] = smem_addr(&empty[slot]);
+          if ((slot += kWarps) >= kSlots) {
+            slot -= kSlots;
+            pass ^= 1;
+          }
+        }
+        if (!ok) return;
+        float s[U][NT][4];  // S^T
+#pragma unroll
+        for (int x = 0; x < U; ++x) {
           uint32_t kw[2][kWordsK];
           uint32_t sb[2][(kWordsK + 1) / 2];  // scale bytes, by two
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint8_t* const row = rec + (t_k + 8 * h) * (D / 2);
-            const uint8_t* const sc = rec + R::kKs + (t_k + 8 * h) * (D / 16);
+            const uint8_t* const row = rec[x] + (t_k + 8 * h) * (D / 2);
+            const uint8_t* const sc = rec[x] + R::kKs + (t_k + 8 * h) * (D / 16);
             if constexpr (D == 64) {
               const uint2 v = *reinterpret_cast<const uint2*>(row + 8 * c);
               kw[h][0] = v.x, kw[h][1] = v.y;
@@ -465,31 +482,37 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[nt][i] = (acc[nt][0][i] + acc[nt][1][i]) * mult[nt][i & 1];
+            for (int i = 0; i < 4; ++i) s[x][nt][i] = (acc[nt][0][i] + acc[nt][1][i]) * mult[nt][i & 1];
         }
-        const int key = u * kKvUnit;
-        if (key < last_start || key + kKvUnit > first_end) {
+        const int key = u * kKvUnit, last = (u + (U - 1) * kWarps) * kKvUnit;
+        if (key < last_start || last + kKvUnit > first_end) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int x = 0; x < U; ++x)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int t = key + t_k + 8 * (i >> 1);
-              if (t < lo[nt][i & 1] || t >= hi[nt][i & 1]) s[nt][i] = -INFINITY;
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int t = key + x * (kWarps * kKvUnit) + t_k + 8 * (i >> 1);
+                if (t < lo[nt][i & 1] || t >= hi[nt][i & 1]) s[x][nt][i] = -INFINITY;
+              }
         }
         bool above = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int x = 0; x < U; ++x)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) above |= s[nt][i] > m[nt][i & 1] + kKvSlack;
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) above |= s[x][nt][i] > m[nt][i & 1] + kKvSlack;
         if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              float top = fmaxf(m[nt][h], fmaxf(s[nt][h], s[nt][h + 2]));
+              float top = m[nt][h];
 #pragma unroll
-              for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+              for (int x = 0; x < U; ++x) top = fmaxf(top, fmaxf(s[x][nt][h], s[x][nt][h + 2]));
+#pragma unroll
+              for (int y = 4; y < 32; y <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, y));
               const float f = exp2_fast(m[nt][h] - top);
               m[nt][h] = top;
               l[nt][h] *= f;
@@ -500,26 +523,27 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
               }
             }
         }
-        uint32_t pb[NT][2];
+        uint32_t pb[U][NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float e[4];
+        for (int x = 0; x < U; ++x)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = exp2_fast(s[nt][i] - (m[nt][i & 1] - kKvShift));
-          l[nt][0] += e[0] + e[2];
-          l[nt][1] += e[1] + e[3];
-          pb[nt][0] = transposed8(bits_of(__floats2half2_rn(e[0], e[1])));
-          pb[nt][1] = transposed8(bits_of(__floats2half2_rn(e[2], e[3])));
-        }
-        // O^T
-        {
+          for (int nt = 0; nt < NT; ++nt) {
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = exp2_fast(s[x][nt][i] - (m[nt][i & 1] - kKvShift));
+            l[nt][0] += e[0] + e[2];
+            l[nt][1] += e[1] + e[3];
+            pb[x][nt][0] = transposed8(bits_of(__floats2half2_rn(e[0], e[1])));
+            pb[x][nt][1] = transposed8(bits_of(__floats2half2_rn(e[2], e[3])));
+          }
+#pragma unroll
+        for (int x = 0; x < U; ++x) {  // O^T
           uint32_t even[2][kWordsV], odd[2][kWordsV];
-          __half2 sc[2][D == 256 ? 2 : 1];
-          const int left = g.seq.n - key;  // (scales behind the sequence's end may be NaN)
+          uint32_t sv[2][D == 256 ? 2 : 1];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t wa[kWordsV], wb[kWordsV];
-            const uint8_t *const ra = rec + R::kV + (t_a + 8 * h) * (D / 2) + gq * (D / 16), *const rb = ra + (t_b - t_a) * (D / 2);
+            const uint8_t *const ra = rec[x] + R::kV + (t_a + 8 * h) * (D / 2) + gq * (D / 16), *const rb = ra + (t_b - t_a) * (D / 2);
             if constexpr (kWordsV == 1) {
               wa[0] = *reinterpret_cast<const uint32_t*>(ra);
               wb[0] = *reinterpret_cast<const uint32_t*>(rb);
@@ -535,14 +559,26 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
               even[h][w] = (wa[w] & 0x0F0F0F0Fu) | ((wb[w] & 0x0F0F0F0Fu) << 4);
               odd[h][w] = ((wa[w] >> 4) & 0x0F0F0F0Fu) | (wb[w] & 0xF0F0F0F0u);
             }
-            const uint8_t *const va = rec + R::kVs + (t_a + 8 * h) * (D / 16), *const vb = rec + R::kVs + (t_b + 8 * h) * (D / 16);
-            const bool a_in = t_a + 8 * h < left, b_in = t_b + 8 * h < left;
+            const uint8_t *const va = rec[x] + R::kVs + (t_a + 8 * h) * (D / 16), *const vb = rec[x] + R::kVs + (t_b + 8 * h) * (D / 16);
 #pragma unroll
             for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {
               const int block = D == 64 ? gq / 2 : D == 128 ? gq : 2 * gq + i;
-              sc[h][i] = kv_scales((a_in ? va[block] : 0u) | (b_in ? vb[block] : 0u) << 8);
+              sv[h][i] = va[block] | static_cast<uint32_t>(vb[block]) << 8;
             }
           }
+          const int left = g.seq.n - key - x * (kWarps * kKvUnit);
+          if (left < kKvUnit) {  // (scales behind the sequence's end may be NaN)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < (D == 256 ? 2 : 1); ++i)
+                sv[h][i] &= (t_a + 8 * h < left ? 0xFFu : 0u) | (t_b + 8 * h < left ? 0xFF00u : 0u);
+          }
+          __half2 sc[2][D == 256 ? 2 : 1];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < (D == 256 ? 2 : 1); ++i) sc[h][i] = kv_scales(sv[h][i]);
 #pragma unroll
           for (int w = 0; w < kWordsV; ++w) {  // 8 channels per thread: four products
             __half2 a[2][2][4];
@@ -561,16 +597,19 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 mma_f16(o[nt][4 * w + i], bits_of(a[0][0][i]), bits_of(a[0][1][i]), bits_of(a[1][0][i]), bits_of(a[1][1][i]),
-                        pb[nt][0], pb[nt][1]);
+                        pb[x][nt][0], pb[x][nt][1]);
           }
         }
         __syncwarp();
-        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[slot])) : "memory");
-        if ((slot += kWarps) >= kSlots) {
-          slot -= kSlots;
-          pass ^= 1;
+        if (lane == 0) {
+#pragma unroll
+          for (int x = 0; x < U; ++x) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(done[x]) : "memory");
         }
-      }
+      };
+      int u = g.u0 + skip;
+      if constexpr (D * NT <= 128)  // (more would not fit the registers)
+        for (; ok && u + kWarps < g.u1; u += 2 * kWarps) take(u, std::integral_constant<int, 2>());
+      for (; ok && u < g.u1; u += kWarps) take(u, std::integral_constant<int, 1>());
       // The warps' sums, one after another.
       float* const mine = merge + warp * kRows * S::kPitch;
 #pragma unroll
