@@ -25,6 +25,8 @@
 // (cp.async.bulk, one per record), and the other warps take them in turn.
 #pragma once
 
+#include <limits.h>
+
 #include <type_traits>
 
 #include "hq_kv.cuh"
@@ -52,7 +54,7 @@ struct KvAttendParams {
 };
 
 constexpr int kKvMaxCtas = 160;
-constexpr int kKvMinUnits = 24;  // records per CTA at least: fewer CTAs rather than emptier ones
+constexpr int kKvMinUnits = 24;  // records per CTA at least where items have as many: fewer CTAs rather than emptier ones
 constexpr float kKvNone = -1e30f;
 constexpr float kKvSlack = 8.0f, kKvShift = 7.0f;
 
@@ -88,6 +90,21 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttendParams& p, int s) {
   return {a, b - a, max(0, min(n, p.most))};
 }
 
+// The same for a whole warp that goes through the sequences in order: 32 are fetched at a time.
+struct KvSeqs {
+  int base = INT_MIN;
+  KvSeq mine;
+  __device__ __forceinline__ KvSeq get(const KvAttendParams& p, int s) {
+    if (s < base || s >= base + 32) {
+      base = s;
+      const int lane = threadIdx.x & 31;
+      mine = s + lane < p.S ? kv_seq(p, s + lane) : KvSeq{0, 0, 0};
+    }
+    const int l = s - base;
+    return {__shfl_sync(0xFFFFFFFFu, mine.q0, l), __shfl_sync(0xFFFFFFFFu, mine.nq, l), __shfl_sync(0xFFFFFFFFu, mine.n, l)};
+  }
+};
+
 // Items of a sequence per head; records per item (the same for all of its rows, at least 1 so that every row is
 // written) and the first of them.
 template <int ROWS>
@@ -102,15 +119,25 @@ struct KvSpan {
   __device__ __forceinline__ int64_t work(const KvAttendParams& p) const { return static_cast<int64_t>(tiles) * units * p.kv_heads; }
 };
 
-// All work; and the sequence at `at` of it, with the work before that sequence.  For a whole warp.
+// All work and its items; and the sequence at `at` of it, with the work before that sequence.  For a whole warp.
+struct KvTotal {
+  int64_t work, items;
+};
 template <int ROWS>
-__device__ __forceinline__ int64_t kv_total(const KvAttendParams& p) {
+__device__ __forceinline__ KvTotal kv_total(const KvAttendParams& p) {
   const int lane = threadIdx.x & 31;
-  int64_t sum = 0;
-  for (int s = lane; s < p.S; s += 32) sum += KvSpan<ROWS>(p, kv_seq(p, s)).work(p);
+  KvTotal t = {0, 0};
+  for (int s = lane; s < p.S; s += 32) {
+    const KvSpan<ROWS> span(p, kv_seq(p, s));
+    t.work += span.work(p);
+    t.items += static_cast<int64_t>(span.tiles) * p.kv_heads;
+  }
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
-  return sum;
+  for (int m = 16; m > 0; m >>= 1) {
+    t.work += __shfl_xor_sync(0xFFFFFFFFu, t.work, m);
+    t.items += __shfl_xor_sync(0xFFFFFFFFu, t.items, m);
+  }
+  return t;
 }
 
 template <int ROWS>
@@ -143,10 +170,12 @@ struct KvShare {
 template <int ROWS>
 __device__ __forceinline__ KvShare kv_share(const KvAttendParams& p, int ctas, int cta) {
   KvShare s;
-  s.total = kv_total<ROWS>(p);
-  int64_t use = (s.total + kKvMinUnits - 1) / kKvMinUnits;
-  use = use < 1 ? 1 : use > ctas ? ctas : use;
-  s.per = (s.total + use - 1) / use;
+  const KvTotal t = kv_total<ROWS>(p);
+  s.total = t.work;
+  // As many shares as CTAs, but none much shorter than an item or, where items are long, than kKvMinUnits.
+  const int64_t item = t.items ? (t.work + t.items - 1) / t.items : 1, least = item < kKvMinUnits ? item : kKvMinUnits;
+  s.per = (s.total + ctas - 1) / ctas;
+  if (s.per < least) s.per = least;
   s.w0 = s.per * cta < s.total ? s.per * cta : s.total;
   s.w1 = s.w0 + s.per < s.total ? s.w0 + s.per : s.total;
   return s;
@@ -159,6 +188,7 @@ struct KvWalk {
   int64_t at, end;   // the next segment's start, the share's end
   int s, tile, head; // the item at `at`
   int64_t item;      // its start
+  KvSeqs seqs;
   KvSeq seq;
   KvSpan<ROWS> span;
 
@@ -175,7 +205,7 @@ struct KvWalk {
       : p(p), at(w0), end(w1), s(0), tile(0), head(0), item(0), seq{0, 0, 0}, span(p, seq) {
     if (at >= end) return;
     s = kv_find<ROWS>(p, at, item);
-    seq = kv_seq(p, s);
+    seq = seqs.get(p, s);
     span = KvSpan<ROWS>(p, seq);
     const int64_t local = (at - item) / span.units;
     tile = static_cast<int>(local / p.kv_heads);
@@ -204,7 +234,7 @@ struct KvWalk {
       if (++tile == span.tiles) {
         tile = 0;
         do {
-          seq = kv_seq(p, ++s);
+          seq = seqs.get(p, ++s);
           span = KvSpan<ROWS>(p, seq);
         } while (span.tiles == 0);  // (there is work left, so a sequence with rows)
       }
@@ -310,6 +340,10 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
   using Walk = KvWalk<kRows>;
   extern __shared__ __align__(128) uint8_t kv_smem[];
   __shared__ uint64_t full[kSlots], empty[kSlots];
+  // Segments, from the producer to the other warps: kept here, not in every warp's registers.
+  constexpr int kTasks = 8;
+  __shared__ uint64_t task_full[kTasks], task_empty[kTasks], met[2];
+  __shared__ typename KvWalk<kRows>::Segment tasks[kTasks];
   __shared__ float merge_m[kWarps][kRows], merge_l[kWarps][kRows];
   float* const merge = reinterpret_cast<float*>(kv_smem + kSlots * S::kUnit);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -318,21 +352,36 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
       mbar_init(smem_addr(&full[i]), 1);
       mbar_init(smem_addr(&empty[i]), 1);
     }
+    for (int i = 0; i < kTasks; ++i) {
+      mbar_init(smem_addr(&task_full[i]), 1);
+      mbar_init(smem_addr(&task_empty[i]), kWarps);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&met[i]), kWarps);
     fence_mbar_init();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // (after the wait: k_kv_combine reads lengths before it has waited for this kernel)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
-  const KvShare share = kv_share<kRows>(p, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x));
-  Walk walk(p, share.w0, share.w1);
-  typename Walk::Segment g;
   bool ok = true;
 
   if (warp == kWarps) {  // the producer: lane l copies every 32nd record
     uint32_t k = 0;      // records so far
     const uint64_t policy = l2_stream_policy();
-    while (walk.next(g)) {
+    const KvShare share = kv_share<kRows>(p, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x));
+    Walk walk(p, share.w0, share.w1);
+    typename Walk::Segment g;
+    int turn = 0;
+    for (bool more = true; more;) {
+      more = walk.next(g);
+      if (!more) g.s = -1, g.u0 = g.u1 = 0;
+      ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(smem_addr(&task_empty[turn % kTasks]), turn / kTasks & 1 ^ 1));
+      if (!ok) break;
+      if (lane == 0) {
+        tasks[turn % kTasks] = g;
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&task_full[turn % kTasks])) : "memory");
+      }
+      ++turn;
       for (int u0 = g.u0; u0 < g.u1; u0 += 32) {
         const int u = u0 + lane;
         const bool mine = u < g.u1;
@@ -368,8 +417,23 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
     uint32_t k0 = 0;  // records of the segments before
     int slot = warp;  // of this warp's next record, and its pass
     uint32_t pass = 0;
-    while (walk.next(g)) {
-      // Q's fragments: row 8 nt + gq, channels as K's.
+    // Segment `round`; false: there is none.
+    const typename Walk::Segment* task = tasks;
+    auto find = [&](int round) {
+      ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&task_full[round % kTasks]), round / kTasks & 1));
+      task = tasks + round % kTasks;
+      return ok && task->s >= 0;
+    };
+    // All multiplying warps; a wait that runs out for one of them must not leave the others waiting for ever.
+    auto meet = [&](int which, int round) {
+      __syncwarp();
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&met[which])) : "memory");
+      ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&met[which]), round & 1));
+      return ok;
+    };
+    for (int round = 0; find(round); ++round) {
+      const typename Walk::Segment& g = *task;
+      // Their fragments.
       uint32_t qf[NT][kSteps][2];
       float mult[NT][2];
       int lo[NT][2], hi[NT][2];
@@ -378,14 +442,14 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
       for (int nt = 0; nt < NT; ++nt) {
         const int r = 8 * nt + gq, at = g.tile * kRows + r;
         const int64_t i = g.seq.q0 + at / p.share;
-        const __nv_bfloat16* const src = p.q + i * p.ld_q + (static_cast<int64_t>(g.head) * p.share + at % p.share) * D;
+        const __nv_bfloat16* const src = r < live ? p.q + i * p.ld_q + (static_cast<int64_t>(g.head) * p.share + at % p.share) * D : nullptr;
         uint32_t w[kSteps * 2];
         float top = 0.0f;
 #pragma unroll
-        for (int j = 0; j < kSteps; j += 2) {  // 8 channels
+        for (int j = 0; j < kSteps; j += 2) {  // 8 channels, as K's
           constexpr int kPer = kPiece / 2;     // steps of a piece
           const int ch = j / kPer * (8 * kPiece) + c * (2 * kPiece) + (j % kPer) * 4;
-          const uint4 v = r < live ? __ldg(reinterpret_cast<const uint4*>(src + ch)) : make_uint4(0, 0, 0, 0);
+          const uint4 v = src ? __ldg(reinterpret_cast<const uint4*>(src + ch)) : make_uint4(0, 0, 0, 0);
           w[2 * j] = v.x, w[2 * j + 1] = v.y, w[2 * j + 2] = v.z, w[2 * j + 3] = v.w;
         }
 #pragma unroll
@@ -610,7 +674,8 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
       if constexpr (D * NT <= 128)  // (more would not fit the registers)
         for (; ok && u + kWarps < g.u1; u += 2 * kWarps) take(u, std::integral_constant<int, 2>());
       for (; ok && u < g.u1; u += kWarps) take(u, std::integral_constant<int, 1>());
-      // The warps' sums, one after another.
+      // The warps' sums, one after another, once those of the segment before have been read.
+      if (!meet(0, round)) break;
       float* const mine = merge + warp * kRows * S::kPitch;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -628,26 +693,28 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
           for (int j = 0; j < kSteps; ++j)
             *reinterpret_cast<float2*>(mine + row * S::kPitch + gq * (D / 8) + 2 * j) = make_float2(o[nt][j][h], o[nt][j][h + 2]);
         }
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-      constexpr int kLanes = D / 8;  // threads of a row
-      for (int task = threadIdx.x; task < kRows * kLanes; task += 32 * kWarps) {
-        const int row = task / kLanes, e = task % kLanes;
+      k0 += max(0, g.u1 - g.u0);
+      if (!meet(1, round)) break;
+      // Each time by other warps: the rest are in the next segment.
+      constexpr int kLanes = D / 8, kParts = kRows * kLanes / 32;  // threads of a row; warps' worth of rows
+      for (int part = (warp + kWarps - round * kParts % kWarps) % kWarps; part < kParts; part += kWarps) {
+        const int task = part * 32 + lane, row = task / kLanes, e = task % kLanes;
         float top = kKvNone;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, merge_m[w][row]);
         float sum = 0.0f, v[8] = {};
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float f = exp2_fast(merge_m[w][row] - top);
-          sum += merge_l[w][row] * f;
+          const float by = exp2_fast(merge_m[w][row] - top);
+          sum += merge_l[w][row] * by;
           const float4* const src = reinterpret_cast<const float4*>(merge + (w * kRows + row) * S::kPitch + 8 * e);
           const float4 a = src[0], b = src[1];
-          v[0] += a.x * f, v[1] += a.y * f, v[2] += a.z * f, v[3] += a.w * f;
-          v[4] += b.x * f, v[5] += b.y * f, v[6] += b.z * f, v[7] += b.w * f;
+          v[0] += a.x * by, v[1] += a.y * by, v[2] += a.z * by, v[3] += a.w * by;
+          v[4] += b.x * by, v[5] += b.y * by, v[6] += b.z * by, v[7] += b.w * by;
         }
+        const int at = g.tile * kRows + row;
         if (g.starts && g.ends) {
-          const int at = g.tile * kRows + row;
-          kv_finish<D>(p, v, top, sum, v_sg, g.seq.q0 + at / p.share, g.head * p.share + at % p.share, e, row < live);
+          kv_finish<D>(p, v, top, sum, v_sg, g.seq.q0 + at / p.share, g.head * p.share + at % p.share, e, at < g.seq.nq * p.share);
         } else {  // (an item that began before is the share's first segment, one that goes on its last)
           float* const to = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + g.starts) * S::kPartFloats;
           float4* const dst = reinterpret_cast<float4*>(to + row * D + 8 * e);
@@ -659,8 +726,8 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
           }
         }
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-      k0 += max(0, g.u1 - g.u0);
+      __syncwarp();
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&task_empty[round % kTasks])) : "memory");
     }
   }
   if (!__all_sync(0xFFFFFFFFu, ok) && lane == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);
@@ -700,9 +767,10 @@ __global__ void __launch_bounds__(256) k_kv_combine(const __grid_constant__ KvAt
   for (int task = threadIdx.x; task < kRows * kLanes; task += 256) {
     const int row = task / kLanes, e = task % kLanes;
     float top = kKvNone;
+#pragma unroll 8
     for (int k = cta; k <= last; ++k) top = fmaxf(top, __ldcg(part(k) + kRows * D + row));
     float sum = 0.0f, v[8] = {};
-#pragma unroll 4
+#pragma unroll 8
     for (int k = cta; k <= last; ++k) {
       const float* const from = part(k);
       const float f = exp2_fast(__ldcg(from + kRows * D + row) - top);
