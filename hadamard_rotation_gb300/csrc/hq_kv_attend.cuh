@@ -54,7 +54,10 @@ struct KvAttendParams {
 };
 
 constexpr int kKvMaxCtas = 160;
-constexpr int kKvMinUnits = 24;  // records per CTA at least where items have as many: fewer CTAs rather than emptier ones
+constexpr int kKvMinUnits = 60;  // work per CTA at least where items have as many: fewer CTAs rather than emptier ones
+// What an item costs beside its records (Q, the joining of the warps' sums), as work of this many before its first.
+// (Without, CTAs with many short items ended last: 37 sequences of 12 heads and some 60 records each 42 us, with it XXX.)
+constexpr int kKvItemUnits = 28;
 constexpr float kKvNone = -1e30f;
 constexpr float kKvSlack = 8.0f, kKvShift = 7.0f;
 
@@ -110,13 +113,15 @@ struct KvSeqs {
 template <int ROWS>
 struct KvSpan {
   int tiles, units, first;
+  int64_t cost;  // of an item
   __device__ __forceinline__ KvSpan(const KvAttendParams& p, const KvSeq& s) {
     tiles = (s.nq * p.share + ROWS - 1) / ROWS;
     const int lo = p.window ? max(0, s.n - s.nq - p.window + 1) : 0;
     first = lo / kKvUnit;
     units = max(1, (s.n + kKvUnit - 1) / kKvUnit - first);
+    cost = units + kKvItemUnits;
   }
-  __device__ __forceinline__ int64_t work(const KvAttendParams& p) const { return static_cast<int64_t>(tiles) * units * p.kv_heads; }
+  __device__ __forceinline__ int64_t work(const KvAttendParams& p) const { return tiles * cost * p.kv_heads; }
 };
 
 // All work and its items; and the sequence at `at` of it, with the work before that sequence.  For a whole warp.
@@ -207,20 +212,20 @@ struct KvWalk {
     s = kv_find<ROWS>(p, at, item);
     seq = seqs.get(p, s);
     span = KvSpan<ROWS>(p, seq);
-    const int64_t local = (at - item) / span.units;
+    const int64_t local = (at - item) / span.cost;
     tile = static_cast<int>(local / p.kv_heads);
     head = static_cast<int>(local - static_cast<int64_t>(tile) * p.kv_heads);
-    item += local * span.units;
+    item += local * span.cost;
   }
 
   __device__ __forceinline__ bool next(Segment& g) {
     if (at >= end) return false;
-    const int64_t stop = item + span.units;
+    const int64_t stop = item + span.cost;
     g.s = s, g.tile = tile, g.head = head, g.seq = seq;
     g.starts = at == item;
     g.ends = stop <= end;
-    const int from = span.first + static_cast<int>(at - item);
-    const int to = span.first + static_cast<int>((g.ends ? stop : end) - item);
+    const int from = span.first + max(0, static_cast<int>(at - item) - kKvItemUnits);
+    const int to = span.first + max(0, static_cast<int>((g.ends ? stop : end) - item) - kKvItemUnits);
     g.i0 = tile * ROWS / p.share;
     g.i1 = min(seq.nq - 1, (tile * ROWS + ROWS - 1) / p.share);
     const int hi = max(0, min(seq.n, seq.n - seq.nq + g.i1 + 1));
@@ -341,9 +346,9 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
   extern __shared__ __align__(128) uint8_t kv_smem[];
   __shared__ uint64_t full[kSlots], empty[kSlots];
   // Segments, from the producer to the other warps: kept here, not in every warp's registers.
-  constexpr int kTasks = 8;
-  __shared__ uint64_t task_full[kTasks], task_empty[kTasks], met[2];
-  __shared__ typename KvWalk<kRows>::Segment tasks[kTasks];
+  constexpr int kRing = 8;
+  __shared__ uint64_t task_full[kRing], task_empty[kRing], met[2];
+  __shared__ typename KvWalk<kRows>::Segment tasks[kRing];
   __shared__ float merge_m[kWarps][kRows], merge_l[kWarps][kRows];
   float* const merge = reinterpret_cast<float*>(kv_smem + kSlots * S::kUnit);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
       mbar_init(smem_addr(&full[i]), 1);
       mbar_init(smem_addr(&empty[i]), 1);
     }
-    for (int i = 0; i < kTasks; ++i) {
+    for (int i = 0; i < kRing; ++i) {
       mbar_init(smem_addr(&task_full[i]), 1);
       mbar_init(smem_addr(&task_empty[i]), kWarps);
     }
@@ -370,38 +375,43 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
     const uint64_t policy = l2_stream_policy();
     const KvShare share = kv_share<kRows>(p, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x));
     Walk walk(p, share.w0, share.w1);
+    // Batches of 32 records; the pages of the next one are looked up while this one's copies are issued.
     typename Walk::Segment g;
-    int turn = 0;
-    for (bool more = true; more;) {
-      more = walk.next(g);
-      if (!more) g.s = -1, g.u0 = g.u1 = 0;
-      ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(smem_addr(&task_empty[turn % kTasks]), turn / kTasks & 1 ^ 1));
-      if (!ok) break;
-      if (lane == 0) {
-        tasks[turn % kTasks] = g;
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&task_full[turn % kTasks])) : "memory");
-      }
-      ++turn;
-      for (int u0 = g.u0; u0 < g.u1; u0 += 32) {
-        const int u = u0 + lane;
-        const bool mine = u < g.u1;
-        const uint8_t* src = nullptr;
-        if (mine) {
-          const int page = u / p.page_units;
-          int64_t at = __ldg(p.table + g.s * p.ld_table + page);
-          at = at < 0 ? 0 : at >= p.pages ? p.pages - 1 : at;
-          src = p.cache + ((at * p.kv_heads + g.head) * p.page_units + (u - page * p.page_units)) * R::kBytes;
+    int turn = 0, u0 = 0, id = 0;
+    g.u0 = g.u1 = 0;
+    auto advance = [&]() {  // to the next batch; false: there is none
+      u0 += 32;
+      while (u0 >= g.u1) {
+        const bool more = walk.next(g);
+        if (!more) g.s = -1, g.u0 = g.u1 = 0;
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(smem_addr(&task_empty[turn % kRing]), turn / kRing & 1 ^ 1));
+        if (!ok) return false;
+        if (lane == 0) {
+          tasks[turn % kRing] = g;
+          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&task_full[turn % kRing])) : "memory");
         }
-        const uint32_t slot = (k + lane) % kSlots, pass = (k + lane) / kSlots & 1;
-        for (int part = 0; part < 4; ++part) {  // eight at a time: the first are on their way before the last have a slot
-          if (mine && lane / 8 == part && ok) {
-            ok = mbar_wait(smem_addr(&empty[slot]), pass ^ 1);
-            if (ok) tma_load(smem_addr(kv_smem) + slot * S::kUnit, src, R::kBytes, smem_addr(&full[slot]), policy);
-          }
-          __syncwarp();
-        }
-        k += min(32, g.u1 - u0);
+        ++turn;
+        if (!more) return false;
+        u0 = g.u0;
       }
+      if (u0 + lane < g.u1)
+        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(id) : "l"(p.table + g.s * p.ld_table + (u0 + lane) / p.page_units));
+      return true;
+    };
+    for (bool more = advance(); more;) {
+      const int u = u0 + lane, n = min(32, g.u1 - u0), head = g.head, page = id;
+      more = advance();
+      const int64_t at = min(static_cast<int64_t>(max(page, 0)), p.pages - 1);
+      const uint8_t* const src = p.cache + ((at * p.kv_heads + head) * p.page_units + u % p.page_units) * R::kBytes;
+      const uint32_t slot = (k + lane) % kSlots, pass = (k + lane) / kSlots & 1;
+      for (int part = 0; part < 4; ++part) {  // eight at a time: the first are on their way before the last have a slot
+        if (lane < n && lane / 8 == part && ok) {
+          ok = mbar_wait(smem_addr(&empty[slot]), pass ^ 1);
+          if (ok) tma_load(smem_addr(kv_smem) + slot * S::kUnit, src, R::kBytes, smem_addr(&full[slot]), policy);
+        }
+        __syncwarp();
+      }
+      k += n;
     }
     // what is on its way lands before the CTA may end
     for (uint32_t i = lane; i < kSlots && i < k; i += 32) {
@@ -420,8 +430,8 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
     // Segment `round`; false: there is none.
     const typename Walk::Segment* task = tasks;
     auto find = [&](int round) {
-      ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&task_full[round % kTasks]), round / kTasks & 1));
-      task = tasks + round % kTasks;
+      ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(&task_full[round % kRing]), round / kRing & 1));
+      task = tasks + round % kRing;
       return ok && task->s >= 0;
     };
     // All multiplying warps; a wait that runs out for one of them must not leave the others waiting for ever.
@@ -727,7 +737,7 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
         }
       }
       __syncwarp();
-      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&task_empty[round % kTasks])) : "memory");
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&task_empty[round % kRing])) : "memory");
     }
   }
   if (!__all_sync(0xFFFFFFFFu, ok) && lane == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);
@@ -751,11 +761,11 @@ __global__ void __launch_bounds__(256) k_kv_combine(const __grid_constant__ KvAt
     s = kv_find<kRows>(p, share.w1 - 1, item);
     seq = kv_seq(p, s);
     const KvSpan<kRows> span(p, seq);
-    const int64_t local = (share.w1 - 1 - item) / span.units;
+    const int64_t local = (share.w1 - 1 - item) / span.cost;
     tile = static_cast<int>(local / p.kv_heads);
     head = static_cast<int>(local - static_cast<int64_t>(tile) * p.kv_heads);
-    item += local * span.units;
-    stop = item + span.units;
+    item += local * span.cost;
+    stop = item + span.cost;
     mine = item >= share.w0 && stop > share.w1;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
