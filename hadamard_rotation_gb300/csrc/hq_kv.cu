@@ -77,7 +77,7 @@ cudaError_t launch_attend(const hq::KvAttendParams& p, int sms, cudaStream_t str
   if (e != cudaSuccess) return e;
   const int ctas = sms < hq::kKvMaxCtas ? sms : hq::kKvMaxCtas;
   if ((e = launch(kernel, dim3(ctas), S::kThreads, S::kSmemBytes, stream, p)) != cudaSuccess) return e;
-  return launch(hq::k_kv_combine<D, NT>, dim3(ctas), 256, 0, stream, p, ctas);
+  return launch(hq::k_kv_combine<D, NT>, dim3(ctas, S::kRows), 256, 0, stream, p);
 }
 
 template <int D>
@@ -200,7 +200,7 @@ hq_status hq_kv_read_nvfp4(const uint8_t* cache, int64_t pages, int64_t page_siz
 int64_t hq_kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t D, int64_t T, int64_t max_q) {
   if (check_cache(kv_heads, D, 0, 0, 16) != HQ_OK || q_heads < 1 || q_heads > kMaxHeads || q_heads % kv_heads != 0) return -1;
   if (T < 0 || T * (q_heads / kv_heads) > kMaxTokens || T > kMaxTokens || max_q < 0) return -1;
-  return few_rows(T, max_q, q_heads / kv_heads) ? hq::kv_part_bytes(static_cast<int>(D), 16) : hq::kv_prompt_bytes(static_cast<int>(D));
+  return few_rows(T, max_q, q_heads / kv_heads) ? hq::kv_part_bytes(static_cast<int>(D)) : hq::kv_prompt_bytes(static_cast<int>(D));
 }
 
 hq_status hq_kv_attention_nvfp4(const void* q, int64_t ld_q, int64_t T, int64_t q_heads, const uint8_t* cache, int64_t pages,

@@ -77,7 +77,18 @@ struct KvAttendShape {
   static constexpr int kPartFloats = kRows * (D + 2);
 };
 
-inline int64_t kv_part_bytes(int D, int rows) { return int64_t{2} * kKvMaxCtas * rows * (D + 2) * 4; }
+// Bytes of the workspace: parts of items that were cut, 2 per CTA, and a record per CTA of the item it begins and does not
+// end, behind the parts of 16 rows.
+inline int64_t kv_part_bytes(int D) { return int64_t{2} * kKvMaxCtas * 16 * (D + 2) * 4 + kKvMaxCtas * 32; }
+
+struct KvCut {
+  int s, tile, head, last;  // the item; the CTA that has its end (-1: none)
+  int pad[4];
+};
+template <int D>
+__device__ __forceinline__ KvCut* kv_cuts(float* part) {
+  return reinterpret_cast<KvCut*>(part + static_cast<int64_t>(2) * kKvMaxCtas * 16 * (D + 2));
+}
 
 // ---------------------------------------------------------------------------
 // The work, as every warp of a launch sees it.
@@ -203,7 +214,8 @@ struct KvWalk {
     int s, tile, head, u0, u1;
     bool starts, ends;
     KvSeq seq;
-    int i0, i1;  // first and last query token of the rows
+    int i0, i1;    // first and last query token of the rows
+    int64_t stop;  // the work up to the item's end
   };
 
   __device__ __forceinline__ KvWalk(const KvAttendParams& p, int64_t w0, int64_t w1)
@@ -224,6 +236,7 @@ struct KvWalk {
     g.s = s, g.tile = tile, g.head = head, g.seq = seq;
     g.starts = at == item;
     g.ends = stop <= end;
+    g.stop = stop;
     const int from = span.first + max(0, static_cast<int>(at - item) - kKvItemUnits);
     const int to = span.first + max(0, static_cast<int>((g.ends ? stop : end) - item) - kKvItemUnits);
     g.i0 = tile * ROWS / p.share;
@@ -365,7 +378,6 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
     fence_mbar_init();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // (after the wait: k_kv_combine reads lengths before it has waited for this kernel)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
   bool ok = true;
@@ -378,12 +390,14 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
     // Batches of 32 records; the pages of the next one are looked up while this one's copies are issued.
     typename Walk::Segment g;
     int turn = 0, u0 = 0, id = 0;
+    KvCut cut{0, 0, 0, -1, {}};
     g.u0 = g.u1 = 0;
     auto advance = [&]() {  // to the next batch; false: there is none
       u0 += 32;
       while (u0 >= g.u1) {
         const bool more = walk.next(g);
         if (!more) g.s = -1, g.u0 = g.u1 = 0;
+        else if (g.starts && !g.ends) cut = KvCut{g.s, g.tile, g.head, static_cast<int>((g.stop - 1) / share.per), {}};
         ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(smem_addr(&task_empty[turn % kRing]), turn / kRing & 1 ^ 1));
         if (!ok) return false;
         if (lane == 0) {
@@ -413,6 +427,7 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
       }
       k += n;
     }
+    if (lane == 0) kv_cuts<D>(p.part)[blockIdx.x] = cut;
     // what is on its way lands before the CTA may end
     for (uint32_t i = lane; i < kSlots && i < k; i += 32) {
       const uint32_t seq = k - 1 - i;
@@ -743,55 +758,54 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
   if (!__all_sync(0xFFFFFFFFu, ok) && lane == 0) atomicOr(&g_hq_fault, kFaultWaitTimeout);
 }
 
-// Items that were cut.  CTA c finishes the one that begins in share c and goes on behind it.
+// Items that were cut: blockIdx.x the CTA that an item begins in, blockIdx.y its row.  The parts are taken by groups of
+// threads, all at once: with one thread for all parts of its channels 19 parts took 10 us.
 template <int D, int NT>
-__global__ void __launch_bounds__(256) k_kv_combine(const __grid_constant__ KvAttendParams p, int ctas) {
+__global__ void __launch_bounds__(256) k_kv_combine(const __grid_constant__ KvAttendParams p) {
   using S = KvAttendShape<D, NT>;
-  constexpr int kRows = S::kRows, kLanes = D / 8;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // (lengths and offsets were there before the kernel in front)
-  const int cta = static_cast<int>(blockIdx.x);
-  const KvShare share = kv_share<kRows>(p, ctas, cta);
-  bool mine = share.w1 > share.w0 && share.w1 < share.total;
-  int s = 0, tile = 0, head = 0;
-  int64_t stop = 0;
-  KvSeq seq{0, 0, 0};
-  if (mine) {
-    int64_t item;
-    s = kv_find<kRows>(p, share.w1 - 1, item);
-    seq = kv_seq(p, s);
-    const KvSpan<kRows> span(p, seq);
-    const int64_t local = (share.w1 - 1 - item) / span.cost;
-    tile = static_cast<int>(local / p.kv_heads);
-    head = static_cast<int>(local - static_cast<int64_t>(tile) * p.kv_heads);
-    item += local * span.cost;
-    stop = item + span.cost;
-    mine = item >= share.w0 && stop > share.w1;
-  }
+  constexpr int kRows = S::kRows, kLanes = D / 8, kGroups = 256 / kLanes;
+  __shared__ float tops[kGroups], totals[kGroups], sums[kGroups][D + 4];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!mine) return;
-  const int last = static_cast<int>((stop - 1) / share.per);  // the CTA that has the item's end
-  const float v_sg = kv_global_scale(__ldg(p.kv_amax + 1));
-  const int live = seq.nq * p.share - tile * kRows;
-  auto part = [&](int k) { return p.part + (static_cast<int64_t>(k) * 2 + (k == cta)) * S::kPartFloats; };
-  for (int task = threadIdx.x; task < kRows * kLanes; task += 256) {
-    const int row = task / kLanes, e = task % kLanes;
-    float top = kKvNone;
-#pragma unroll 8
-    for (int k = cta; k <= last; ++k) top = fmaxf(top, __ldcg(part(k) + kRows * D + row));
-    float sum = 0.0f, v[8] = {};
-#pragma unroll 8
-    for (int k = cta; k <= last; ++k) {
-      const float* const from = part(k);
-      const float f = exp2_fast(__ldcg(from + kRows * D + row) - top);
-      sum += __ldcg(from + kRows * D + kRows + row) * f;
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(from + row * D + 8 * e)), b = __ldcg(reinterpret_cast<const float4*>(from + row * D + 8 * e) + 1);
-      v[0] += a.x * f, v[1] += a.y * f, v[2] += a.z * f, v[3] += a.w * f;
-      v[4] += b.x * f, v[5] += b.y * f, v[6] += b.z * f, v[7] += b.w * f;
-    }
-    const int at = tile * kRows + row;
-    kv_finish<D>(p, v, top, sum, v_sg, seq.q0 + at / p.share, head * p.share + at % p.share, e, row < live);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int cta = static_cast<int>(blockIdx.x), row = static_cast<int>(blockIdx.y);
+  const int4 cut = __ldcg(reinterpret_cast<const int4*>(kv_cuts<D>(p.part) + cta));
+  const int last = cut.w;
+  if (last < 0) return;
+  const KvSeq seq = kv_seq(p, cut.x);
+  const int at = cut.y * kRows + row, e = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  if (at >= seq.nq * p.share) return;
+  float top = kKvNone, sum = 0.0f, v[8] = {};
+#pragma unroll 2
+  for (int k = cta + group; k <= last; k += kGroups) {
+    const float* const from = p.part + (static_cast<int64_t>(k) * 2 + (k == cta)) * S::kPartFloats;
+    const float m = __ldcg(from + kRows * D + row), l = __ldcg(from + kRows * D + kRows + row);
+    const float4 a = __ldcg(reinterpret_cast<const float4*>(from + row * D + 8 * e)), b = __ldcg(reinterpret_cast<const float4*>(from + row * D + 8 * e) + 1);
+    const float both = fmaxf(top, m), f = exp2_fast(top - both), g = exp2_fast(m - both);
+    top = both;
+    sum = sum * f + l * g;
+    v[0] = v[0] * f + a.x * g, v[1] = v[1] * f + a.y * g, v[2] = v[2] * f + a.z * g, v[3] = v[3] * f + a.w * g;
+    v[4] = v[4] * f + b.x * g, v[5] = v[5] * f + b.y * g, v[6] = v[6] * f + b.z * g, v[7] = v[7] * f + b.w * g;
   }
+  if (e == 0) tops[group] = top, totals[group] = sum;
+  *reinterpret_cast<float4*>(&sums[group][8 * e]) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(&sums[group][8 * e + 4]) = make_float4(v[4], v[5], v[6], v[7]);
+  __syncthreads();
+  if (threadIdx.x >= 32) return;  // (a whole warp for the lanes' exchange)
+  top = kKvNone;
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) top = fmaxf(top, tops[k]);
+  sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+#pragma unroll 4
+  for (int k = 0; k < kGroups; ++k) {
+    const float f = exp2_fast(tops[k] - top);
+    sum += totals[k] * f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += sums[k][8 * e + i] * f;
+  }
+  kv_finish<D>(p, v, top, sum, kv_global_scale(__ldg(p.kv_amax + 1)), seq.q0 + at / p.share, cut.z * p.share + at % p.share, e,
+               threadIdx.x < kLanes);
 }
 
 }  // namespace hq

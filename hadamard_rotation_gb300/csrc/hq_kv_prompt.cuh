@@ -62,11 +62,6 @@ inline int64_t kv_prompt_bytes(int D) {
   return int64_t{2} * kKvMaxCtas * (D == 256 ? 128 : 256) * (D + 2) * 4 + kKvMaxCtas * 32;
 }
 
-struct KvCut {
-  int s, tile, head, last;  // the item; the CTA that has its end (-1: none)
-  int pad[4];
-};
-
 constexpr int64_t kKvMinTiles = 6;  // of work per CTA at least
 // What an item costs beside its key tiles (Q, the first scores, the rows' end), as work of this many tiles before its first.
 constexpr int kKvItemTiles = 3;
