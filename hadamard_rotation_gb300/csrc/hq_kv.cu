@@ -16,7 +16,7 @@ using hq::cuda_fail;
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-constexpr int64_t kMaxTokens = (int64_t{1} << 31) - 1024;  // token counts are ints in the kernels
+constexpr int64_t kMaxTokens = (int64_t{1} << 31) - 1024;  // counts of tokens and of rows (token, head)
 constexpr int64_t kMaxHeads = 4096;
 constexpr int64_t kFewRows = 32;
 
@@ -121,6 +121,7 @@ hq_status hq_kv_append_nvfp4(const void* q, int64_t ld_q, const void* k, int64_t
   const hq_status st = check_cache(kv_heads, D, group, pages, page_size);
   if (st != HQ_OK) return st;
   if (T < 0 || T > kMaxTokens || q_heads < 0 || q_heads > kMaxHeads) return HQ_ERR_SHAPE;
+  if (T * (q_heads + 2 * kv_heads) > kMaxTokens) return HQ_ERR_SHAPE;
   if (rotary < 0 || rotary > D || rotary % 16 != 0 || (rotary > 0 && table_rows < 1)) return HQ_ERR_SHAPE;
   if (T == 0) return HQ_OK;
   const int es = dtype == HQ_BF16 ? 2 : 4;
@@ -174,7 +175,7 @@ hq_status hq_kv_read_nvfp4(const uint8_t* cache, int64_t pages, int64_t page_siz
   if (out_dtype != HQ_F32 && out_dtype != HQ_BF16) return HQ_ERR_DTYPE;
   const hq_status st = check_cache(kv_heads, D, group, pages, page_size);
   if (st != HQ_OK) return st;
-  if (T < 0 || T > kMaxTokens) return HQ_ERR_SHAPE;
+  if (T < 0 || T > kMaxTokens || T * kv_heads > kMaxTokens) return HQ_ERR_SHAPE;
   if (T == 0) return HQ_OK;
   if (!slots || !kv_amax || !k || !v || (pages > 0 && !cache)) return HQ_ERR_NULL;
   if (!aligned(cache, 16) || !aligned(slots, 8) || !aligned(kv_amax, 4) || !aligned(k, 16) || !aligned(v, 16)) return HQ_ERR_ALIGN;

@@ -9,6 +9,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <limits.h>
 
 #include "hq_kernels.cuh"
 
@@ -34,9 +35,13 @@ __device__ __forceinline__ float kv_global_scale(float amax) {
 // ---------------------------------------------------------------------------
 // Appending.
 //
-// A thread takes 16 channels of a head of a token: position rotation (two products and a sum, each rounded, as the
-// definition in hq.h has them), butterfly, then for K and V the block scale and codes exactly as
-// hq_rotate_quant_nvfp4.
+// A thread takes 16 channels of a (token, head): position rotation (two products and a sum, each rounded, as the
+// definition in hq.h has them), butterfly in pairs of channels, then for K and V the block scale and codes exactly as
+// hq_rotate_quant_nvfp4, with the quantizer's corrected quotients.  Instructions and the latency of positions and tables
+// bound it, not memory: 8192 tokens of 32 + 2 * 8 heads of 128 take 52 us (60 with a butterfly of single channels and
+// divisions), 36 without the position rotation; the bytes alone 26.  Four CTAs per SM (64 registers): a thread that
+// went over the heads of its token with cosines in registers needed 91, and took 60; the next row's position read one
+// row ahead 56.
 // ---------------------------------------------------------------------------
 struct KvAppendParams {
   const uint8_t* in[3];  // q, k, v
@@ -101,61 +106,96 @@ __device__ __forceinline__ void kv_rotate(float (&x)[16]) {
   }
 }
 
+// The same for pairs v[i] = (x[i], x[i + 8]): two channels an instruction.  Each sum and product is rounded alike.
+template <int G>
+__device__ __forceinline__ void kv_rotate(float2 (&v)[8]) {
+  if constexpr (G != 0) {
+#pragma unroll
+    for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if ((i & h) == 0) {
+          const float2 a = v[i], b = v[i + h];
+          v[i] = add2(a, b);
+          v[i + h] = sub2(a, b);
+        }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = make_float2(__fadd_rn(v[i].x, v[i].y), __fsub_rn(v[i].x, v[i].y));
+    if constexpr (G == 256) {
+      const int lane = threadIdx.x & 31;
+#pragma unroll
+      for (int m = 1; m < 16; m <<= 1) {
+        const float sign = (lane & m) ? -1.0f : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 o = make_float2(__shfl_xor_sync(0xFFFFFFFFu, v[i].x, m), __shfl_xor_sync(0xFFFFFFFFu, v[i].y, m));
+          v[i] = fma2(v[i], make_float2(sign, sign), o);  // (exact product)
+        }
+      }
+    }
+    constexpr float c = inv_sqrt_g<G>();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], make_float2(c, c));
+  }
+}
+
 // The record that holds slot `slot`, and the token's place in it.
 template <int D>
 __device__ __forceinline__ int64_t kv_record(int64_t slot, int head, int kv_heads, int page_units, int& at) {
-  const int64_t unit = slot / kKvUnit, page = unit / page_units;
+  const int64_t unit = slot / kKvUnit, page = unit < INT_MAX ? static_cast<int>(unit) / page_units : unit / page_units;
   at = static_cast<int>(slot % kKvUnit);
   return ((page * kv_heads + head) * page_units + (unit - page * page_units)) * KvRecord<D>::kBytes;
 }
 
 template <int D, int G, bool BF16>
-__global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ KvAppendParams p) {
+__global__ void __launch_bounds__(256, BF16 ? 4 : 3) k_kv_append(const __grid_constant__ KvAppendParams p) {
   using R = KvRecord<D>;
   constexpr int kBlocks = D / 16, es = BF16 ? 2 : 4;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int heads = p.heads[0] + 2 * p.kv_heads;
-  const int64_t rows = p.T * heads;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t heads = p.heads[0] + 2 * p.kv_heads, rows = static_cast<uint32_t>(p.T) * heads;  // (below 2^31)
   const int b = threadIdx.x % kBlocks;
+  const float r6 = __frcp_rn(6.0f);
   const float sg[2] = {kv_global_scale(__ldg(p.kv_amax)), kv_global_scale(__ldg(p.kv_amax + 1))};
   // (every lane of a warp goes on while one does: the lanes exchange values)
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * (256 / kBlocks); r0 < rows; r0 += static_cast<int64_t>(gridDim.x) * (256 / kBlocks)) {
-    const int64_t r = r0 + threadIdx.x / kBlocks;
+  for (uint32_t r0 = blockIdx.x * (256 / kBlocks); r0 < rows; r0 += gridDim.x * (256 / kBlocks)) {
+    const uint32_t r = r0 + threadIdx.x / kBlocks;
     const bool live = r < rows;
-    const int64_t t = live ? r / heads : 0;
-    int head = live ? static_cast<int>(r - t * heads) : 0, which = 0;
+    const uint32_t t32 = live ? r / heads : 0;
+    const int64_t t = t32;
+    int head = live ? static_cast<int>(r - t32 * heads) : 0, which = 0;
     if (head >= p.heads[0]) {
-      which = 1 + (head - p.heads[0]) / p.kv_heads;
-      head = (head - p.heads[0]) % p.kv_heads;
+      head -= p.heads[0];
+      which = head < p.kv_heads ? 1 : 2;
+      head -= (which - 1) * p.kv_heads;
     }
     const int64_t slot = which ? __ldg(p.slots + t) : 0;
     const bool store = live && slot >= 0 && (which == 0 || slot < p.n_slots);
-    const uint8_t* const src = p.in[which] + t * p.ld[which] + static_cast<int64_t>(head) * D * es;
-    float x[16];
+    const uint8_t* const src = p.in[which] + t * p.ld[which] + static_cast<int64_t>(head) * (D * es);
+    float2 x[8];  // channels k and k + 8
     {
       float lo[8], hi[8];
       kv_load8<BF16>(src + 16 * b * es, lo);
       kv_load8<BF16>(src + (16 * b + 8) * es, hi);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = lo[i], x[8 + i] = hi[i];
+      for (int i = 0; i < 8; ++i) x[i] = make_float2(lo[i], hi[i]);
     }
-    if (which < 2 && p.rotary > 0) {
+    if (which < 2 && 16 * b < p.rotary) {
       int64_t pos = __ldg(p.positions + t);
       pos = pos < 0 ? 0 : pos >= p.rows ? p.rows - 1 : pos;
       const int half = p.rotary / 2;
       const float *ct = p.cos_t + pos * half, *st = p.sin_t + pos * half;
       if (p.interleaved) {
-        if (16 * b < p.rotary) {
-          float c[8], s[8];
-          kv_load8<false>(reinterpret_cast<const uint8_t*>(ct + 8 * b), c);
-          kv_load8<false>(reinterpret_cast<const uint8_t*>(st + 8 * b), s);
+        float c[8], s[8];
+        kv_load8<false>(reinterpret_cast<const uint8_t*>(ct + 8 * b), c);
+        kv_load8<false>(reinterpret_cast<const uint8_t*>(st + 8 * b), s);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float x1 = x[2 * i], x2 = x[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(x1, c[i]), __fmul_rn(x2, s[i]));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(x2, c[i]), __fmul_rn(x1, s[i]));
-          }
+        for (int k = 0; k < 8; ++k) {  // pair k: channels 2 k and 2 k + 1
+          float& x1 = k < 4 ? x[2 * k].x : x[2 * k - 8].y;
+          float& x2 = k < 4 ? x[2 * k + 1].x : x[2 * k - 7].y;
+          const float a = x1, o = x2;
+          x1 = __fsub_rn(__fmul_rn(a, c[k]), __fmul_rn(o, s[k]));
+          x2 = __fadd_rn(__fmul_rn(o, c[k]), __fmul_rn(a, s[k]));
         }
       } else {
 #pragma unroll
@@ -170,8 +210,9 @@ __global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ KvApp
             kv_load8<BF16>(src + (second ? at : c0 + half) * es, o);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float mine = __fmul_rn(x[8 * q + i], c[i]), other = __fmul_rn(o[i], s[i]);
-              x[8 * q + i] = second ? __fadd_rn(mine, other) : __fsub_rn(mine, other);
+              float& mine = q ? x[i].y : x[i].x;
+              // (a - b is a + -b, and -(o s) is o (-s), rounded alike)
+              mine = __fadd_rn(__fmul_rn(mine, c[i]), __fmul_rn(o[i], second ? s[i] : -s[i]));
             }
           }
         }
@@ -182,9 +223,10 @@ __global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ KvApp
     if (which == 0) {
       uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      for (int k = 0; k < 4; ++k) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(x[2 * k].x, x[2 * k + 1].x), hi = __floats2bfloat162_rn(x[2 * k].y, x[2 * k + 1].y);
+        w[k] = *reinterpret_cast<const uint32_t*>(&lo);
+        w[4 + k] = *reinterpret_cast<const uint32_t*>(&hi);
       }
       uint4* const dst = reinterpret_cast<uint4*>(p.q_out + ((t * p.heads[0] + head) * D + 16 * b));
       dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -193,18 +235,36 @@ __global__ void __launch_bounds__(256) k_kv_append(const __grid_constant__ KvApp
     }
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) top = max_nan(top, fabsf(x[i]));
+    for (int k = 0; k < 8; ++k) top = max3_nan(top, fabsf(x[k].x), fabsf(x[k].y));
+    // Block scale and codes: correctly rounded quotients, by the quantizer's corrected products where its conditions hold
+    // (top and both scales far from the ends of fp32's range), else divided.
     const float g = sg[which - 1];
-    const uint32_t sb = e4m3x2(__fdiv_rn(__fdiv_rn(top, 6.0f), g), 0.0f) & 0xFFu;
+    const bool fast = top <= 0x1p60f && g >= 0x1p-60f && g <= 0x1p60f;
+    const float v = fast ? div_markstein(div_markstein(top, 6.0f, r6), g, __frcp_rn(g)) : __fdiv_rn(__fdiv_rn(top, 6.0f), g);
+    const uint32_t sb = e4m3x2(v, 0.0f) & 0xFFu;
     const float sf = __fmul_rn(e4m3x2_to_f32(sb).x, g);
-    float v[16];
+    uint2 codes = make_uint2(0, 0);
+    if (sf != 0.0f) {
+      float2 n[8];
+      uint32_t flip = 0;
+      if (fast) {  // -q, with the sign of zero; the codes' signs are turned back
+        const float nr = -__frcp_rn(sf);
+        flip = 0x88888888u;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = sf == 0.0f ? 0.0f : __fdiv_rn(x[i], sf);
+        for (int k = 0; k < 8; ++k) {
+          const float2 q0 = mul2(x[k], make_float2(nr, nr));
+          n[k] = fma2(fma2(q0, make_float2(sf, sf), x[k]), make_float2(nr, nr), q0);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) n[k] = make_float2(__fdiv_rn(x[k].x, sf), __fdiv_rn(x[k].y, sf));
+      }
+      codes = make_uint2(e2m1x8(n[0].x, n[1].x, n[2].x, n[3].x, n[4].x, n[5].x, n[6].x, n[7].x) ^ flip,
+                         e2m1x8(n[0].y, n[1].y, n[2].y, n[3].y, n[4].y, n[5].y, n[6].y, n[7].y) ^ flip);
+    }
     int at;
     uint8_t* const rec = p.cache + kv_record<D>(slot, head, p.kv_heads, p.page_units, at);
-    *reinterpret_cast<uint2*>(rec + (which == 1 ? 0 : R::kV) + at * (D / 2) + 8 * b) =
-        make_uint2(e2m1x8(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]),
-                   e2m1x8(v[8], v[9], v[10], v[11], v[12], v[13], v[14], v[15]));
+    *reinterpret_cast<uint2*>(rec + (which == 1 ? 0 : R::kV) + at * (D / 2) + 8 * b) = codes;
     rec[(which == 1 ? R::kKs : R::kVs) + at * kBlocks + b] = static_cast<uint8_t>(sb);
   }
 }
@@ -227,13 +287,13 @@ __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ KvReadP
   constexpr int kBlocks = D / 16;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t rows = p.T * p.kv_heads;
+  const uint32_t rows = static_cast<uint32_t>(p.T) * p.kv_heads;
   const int b = threadIdx.x % kBlocks;
   const float sg[2] = {kv_global_scale(__ldg(p.kv_amax)), kv_global_scale(__ldg(p.kv_amax + 1))};
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * (256 / kBlocks); r0 < rows; r0 += static_cast<int64_t>(gridDim.x) * (256 / kBlocks)) {
-    const int64_t r = r0 + threadIdx.x / kBlocks;
+  for (uint32_t r0 = blockIdx.x * (256 / kBlocks); r0 < rows; r0 += gridDim.x * (256 / kBlocks)) {
+    const uint32_t r = r0 + threadIdx.x / kBlocks;
     const bool live = r < rows;
-    const int64_t t = live ? r / p.kv_heads : 0;
+    const uint32_t t = live ? r / p.kv_heads : 0;
     const int head = live ? static_cast<int>(r - t * p.kv_heads) : 0;
     const int64_t slot = __ldg(p.slots + t);
     const bool there = slot >= 0 && slot < p.n_slots;
@@ -258,7 +318,7 @@ __global__ void __launch_bounds__(256) k_kv_read(const __grid_constant__ KvReadP
       kv_rotate<G>(x);
       if (!live) continue;
       void* const dst = which ? p.v : p.k;
-      const int64_t to = r * D + 16 * b;
+      const int64_t to = static_cast<int64_t>(r) * D + 16 * b;
       if constexpr (BF16) {
         uint32_t o[8];
 #pragma unroll

@@ -548,6 +548,7 @@ HQ_API int64_t hq_kv_page_bytes(int64_t page_size, int64_t kv_heads, int64_t D);
  *   slots : int64 [T] on the device; a token whose slot is negative or behind the last page is not stored.  Two
  *          tokens with one slot leave it with parts of either.
  *   q_out : bf16 [T, q_heads, D], contiguous, 16-byte aligned; may not overlap the inputs.
+ *   T * (q_heads + 2 kv_heads) below 2^31 - 1024.
  */
 HQ_API hq_status hq_kv_append_nvfp4(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
                                     int64_t ld_v, hq_dtype dtype, int64_t T, int64_t q_heads,
@@ -560,7 +561,8 @@ HQ_API hq_status hq_kv_append_nvfp4(const void* q, int64_t ld_q, const void* k, 
 /*
  * hq_kv_read_nvfp4 -- the values of cached tokens (to hand a prefix on, or to check): k, v [T, kv_heads, D] of
  * out_dtype, contiguous, 16-byte aligned; code * (scale * s_global) in fp32, then the rotation by `group` again (0:
- * as stored), one rounding.  Tokens without a slot (negative, behind the last page) are zeros.
+ * as stored), one rounding.  Tokens without a slot (negative, behind the last page) are zeros.  T * kv_heads below
+ * 2^31 - 1024.
  */
 HQ_API hq_status hq_kv_read_nvfp4(const uint8_t* cache, int64_t pages, int64_t page_size, int64_t kv_heads,
                                   int64_t D, const int64_t* slots, int64_t T, const float* kv_amax,

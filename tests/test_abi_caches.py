@@ -51,7 +51,7 @@ CACHE = (dict(kv_heads=0), dict(kv_heads=5000), dict(D=32), dict(D=96), dict(D=-
 def test_kv_append(lib):
     st = caller(lib, "hq_kv_append_nvfp4", APPEND)
     assert st(dt=2) == DTYPE
-    for bad in CACHE + (dict(T=-1), dict(T=1 << 31), dict(q_heads=-1), dict(q_heads=5000), dict(rotary=-16), dict(rotary=8), dict(rotary=144),
+    for bad in CACHE + (dict(T=-1), dict(T=1 << 31), dict(T=1 << 30, q_heads=2, ld_q=2 * 128), dict(q_heads=-1), dict(q_heads=5000), dict(rotary=-16), dict(rotary=8), dict(rotary=144),
                         dict(rows=0), dict(ld_q=1000), dict(ld_k=255), dict(ld_v=0), dict(ld_k=1 << 62), dict(D=64, group=256)):
         assert st(**bad) in (SHAPE, GROUP), bad
     assert st(group=8) == GROUP and st(group=256) == SHAPE and st(group=-1) == GROUP
@@ -71,7 +71,7 @@ def test_kv_append(lib):
 def test_kv_read(lib):
     st = caller(lib, "hq_kv_read_nvfp4", READ)
     assert st(dt=5) == DTYPE
-    for bad in CACHE + (dict(T=-1), dict(T=1 << 31)):
+    for bad in CACHE + (dict(T=-1), dict(T=1 << 31), dict(T=1 << 30)):
         assert st(**bad) == SHAPE, bad
     assert st(group=64) == GROUP and st(group=256) == SHAPE
     assert st(T=0, cache=None, k=None) == OK

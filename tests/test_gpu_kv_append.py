@@ -143,6 +143,34 @@ def test_values_that_saturate_vanish_and_are_zero(oracle_lib):
     check(oracle_lib, 30, 2, 2, 64, 16, 64, False, 16, torch.float32, scale=1e30, kv_amax=[3e30, 3e30], seed=7)
 
 
+@pytest.mark.parametrize("scale", [1e-38, 1e-22, 1e-3, 1e17, 1e20, 1e33])
+@pytest.mark.parametrize("amax", [1e-38, 1e-16, 1e-13, 1.0, 1e17, 1e24, 3e38])
+def test_magnitudes(oracle_lib, scale, amax):
+    """Where corrected quotients would leave fp32's range the divided ones stand in: bytes as the oracle's everywhere."""
+    check(oracle_lib, 9, 2, 2, 64, 16, 0, False, 16, torch.float32, scale=scale, kv_amax=[amax, 7 * amax if amax < 1 else amax / 7], seed=8)
+
+
+def test_values_that_are_none():
+    """NaN and infinities stay in their rotation group: the other groups' bytes are those of clean inputs."""
+    D, T = 64, 16
+    torch.manual_seed(0)
+    x = torch.randn((T, 2, D), device="cuda")
+    bad = x.clone()
+    bad[3, 0, 20], bad[5, 1, 40], bad[7, 0, 0] = float("nan"), float("inf"), -float("inf")
+    slots, amax = torch.arange(T, device="cuda"), torch.full((2,), 6.0, device="cuda")
+    got = []
+    for t in (x, bad):
+        cache = torch.zeros((1, 2, 1, 18 * D), dtype=torch.uint8, device="cuda")
+        q = hq.hq_kv_append_nvfp4(t, t, t, None, None, None, slots, amax, cache, group=16)
+        got.append((q, *hq.hq_kv_read_nvfp4(cache, slots, amax)))
+    hit = torch.zeros((T, 2, D), dtype=torch.bool, device="cuda")
+    hit[3, 0, 16:32] = hit[5, 1, 32:48] = hit[7, 0, :16] = True
+    for clean, other in zip(*got):
+        assert torch.equal(clean[~hit], other[~hit])
+    assert not torch.isfinite(got[1][0][hit]).any()
+    assert got[1][1][3, 0, 16:32].isnan().all() and got[1][2][3, 0, 16:32].isnan().all()  # (an infinite block saturates)
+
+
 def test_nothing_to_do():
     cache = torch.zeros((2, 1, 1, 18 * 64), dtype=torch.uint8, device="cuda")
     e = torch.empty((0, 1, 64), dtype=torch.bfloat16, device="cuda")
