@@ -56,7 +56,7 @@ struct KvAttendParams {
 constexpr int kKvMaxCtas = 160;
 constexpr int kKvMinUnits = 60;  // work per CTA at least where items have as many: fewer CTAs rather than emptier ones
 // What an item costs beside its records (Q, the joining of the warps' sums), as work of this many before its first.
-// (Without, CTAs with many short items ended last: 37 sequences of 12 heads and some 60 records each 42 us, with it XXX.)
+// (Without, CTAs with many short items ended last: 37 sequences of 12 heads and some 60 records each 42 us, with it 24.)
 constexpr int kKvItemUnits = 28;
 constexpr float kKvNone = -1e30f;
 constexpr float kKvSlack = 8.0f, kKvShift = 7.0f;
@@ -279,6 +279,8 @@ __device__ __forceinline__ __half2 kv_scales(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
   return *reinterpret_cast<const __half2*>(&r);
 }
+// A bit for each of four E4M3 scales that is a NaN.
+__device__ __forceinline__ uint32_t kv_nan_scales(uint32_t four) { return ((four & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -662,6 +664,36 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
 #pragma unroll
               for (int i = 0; i < (D == 256 ? 2 : 1); ++i)
                 sv[h][i] &= (t_a + 8 * h < left ? 0xFFu : 0u) | (t_b + 8 * h < left ? 0xFF00u : 0u);
+          }
+          uint32_t nan = 0;
+#pragma unroll
+          for (int i = 0; i < (D == 256 ? 2 : 1); ++i) nan |= kv_nan_scales(sv[0][i] | sv[1][i] << 16);
+          if (__any_sync(0xFFFFFFFFu, nan != 0)) {  // for the rows that see them only: the product would give them to all
+#pragma unroll
+            for (int i = 0; i < (D == 256 ? 2 : 1); ++i) {
+              uint32_t where = 0;  // tokens of the record with a NaN in the thread's channels
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                  if ((sv[h][i] >> (8 * y) & 0x7Fu) == 0x7Fu) {
+                    where |= 1u << ((y ? t_b : t_a) + 8 * h);
+                    sv[h][i] &= y ? 0x00FFu : 0xFF00u;
+                  }
+              where |= __shfl_xor_sync(0xFFFFFFFFu, where, 1);
+              where |= __shfl_xor_sync(0xFFFFFFFFu, where, 2);
+              const int first = key + x * (kWarps * kKvUnit);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int a = max(0, lo[nt][h] - first), b = min(kKvUnit, hi[nt][h] - first);
+                  if (a < b && (where & ((1u << b) - (1u << a))) != 0)
+#pragma unroll
+                    for (int j = (D == 256 ? 8 * i : 0); j < (D == 256 ? 8 * i + 8 : kSteps); ++j)
+                      o[nt][j][h] = o[nt][j][h + 2] = __int_as_float(0x7FC00000);
+                }
+            }
           }
           __half2 sc[2][D == 256 ? 2 : 1];
 #pragma unroll

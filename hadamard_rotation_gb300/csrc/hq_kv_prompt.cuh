@@ -266,6 +266,7 @@ struct KvPromptBars {
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
   uint64_t drain;
   uint32_t tmem;
+  uint32_t v_nan;  // a NaN among the values that this CTA has widened
 };
 
 // Columns of the thread's row, on their way until tmem_load_wait.
@@ -322,6 +323,34 @@ __device__ __forceinline__ void kv_butterfly(uint32_t (&w)[16]) {
   for (int i = 0; i < 8; ++i) w[2 * i] = __float_as_uint(x[i].x), w[2 * i + 1] = __float_as_uint(x[i].y);
 }
 
+// Blocks of 16 channels (a bit each) in which one of the keys [max(k0, begin), min(k1, end)) of a sequence has a NaN for a
+// value: of each lane's `begin` and `end`, by a warp.
+template <int D>
+__device__ __noinline__ uint32_t kv_nan_blocks(const KvAttendParams& p, const int32_t* table, int head, int k0, int k1, int begin,
+                                               int end) {
+  using R = KvRecord<D>;
+  const int lane = threadIdx.x & 31;
+  uint32_t mine = 0;
+  for (int base = k0; base < k1; base += 32) {
+    const int key = base + lane;
+    uint32_t bad = 0;
+    if (key < k1) {
+      const int unit = key / kKvUnit;
+      const int64_t page = min(static_cast<int64_t>(max(__ldg(table + unit / p.page_units), 0)), p.pages - 1);
+      const uint8_t* const sc = p.cache + ((page * p.kv_heads + head) * p.page_units + unit % p.page_units) * R::kBytes + R::kVs +
+                                key % kKvUnit * (D / 16);
+#pragma unroll 1
+      for (int i = 0; i < D / 16; ++i) bad |= static_cast<uint32_t>((__ldg(sc + i) & 0x7F) == 0x7F) << i;
+    }
+    for (uint32_t left = __ballot_sync(0xFFFFFFFFu, bad != 0); left; left &= left - 1) {
+      const int l = __ffs(left) - 1;
+      const uint32_t blocks = __shfl_sync(0xFFFFFFFFu, bad, l);
+      if (base + l >= begin && base + l < end) mine |= blocks;
+    }
+  }
+  return mine;
+}
+
 template <int D>
 __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(const __grid_constant__ KvAttendParams p) {
   using S = KvPromptShape<D>;
@@ -355,6 +384,7 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
       mbar_init(smem_addr(&bars.task_empty[i]), 9 + 4 * kSub);  // (the warps of the roles)
     }
     mbar_init(smem_addr(&bars.drain), 1);
+    bars.v_nan = 0;
     fence_mbar_init();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -390,7 +420,7 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
     while (ok && next(g)) {
       GemmRing vr = kv;
       // S = Q K^T; `over`: into columns whose P the last product into O may still read.  (In two halves, of which only the
-      // one over P waits, the products of 64 columns take as long as those of 128: 778 us for four prompts in place of XXX.)
+      // one over P waits, the products of 64 columns take as long as those of 128: 778 us for four prompts at a time when one piece took 682.)
       auto scores = [&](int t, int buffer, bool over) {
         if (D == 128 && over) {
           ok = warp_wait(smem_addr(&bars.o_full[t]), o_phase >> t & 1 ^ 1);
@@ -557,6 +587,12 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
       else asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(scales.x), "=r"(scales.y) : "l"(sc));
     };
     auto widen = [&](uint8_t* to, const uint32_t (&w)[kWords], uint2 scales) {
+      // A value's NaN is for the rows that see it only, but the product would give it to all: the rows' end puts it in.
+      if (which && (kv_nan_scales(scales.x) | kv_nan_scales(scales.y)) != 0) {
+        *const_cast<volatile uint32_t*>(&bars.v_nan) = 1;
+        scales.x &= ~((kv_nan_scales(scales.x) >> 7) * 0xFFu);
+        scales.y &= ~((kv_nan_scales(scales.y) >> 7) * 0xFFu);
+      }
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         __half2 h[4];
@@ -751,6 +787,18 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
         ok = warp_wait(smem_addr(&bars.o_full[t]), o_phase ^ 1);
         if (!ok) break;
         umma_fence_after();
+        if (__any_sync(0xFFFFFFFFu, *const_cast<volatile uint32_t*>(&bars.v_nan) != 0)) {
+          const uint32_t bad = kv_nan_blocks<D>(p, g.table, g.head, sub.j0 * kKeys, min(sub.j1 * kKeys, g.seq.n), begin, end);
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            if (!__any_sync(0xFFFFFFFFu, bad >> c & 1)) continue;
+            uint32_t w[16];
+            tmem_load(to + 16 * c, w);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = bad >> c & 1 ? 0x7FC00000u : w[k];
+            tmem_store(to + 16 * c, w);
+          }
+        }
       }
       if (g.starts && g.ends) {
         const float f = l > 0.0f || l != l ? __fdiv_rn(v_sg, l) * (p.group == 256 ? 0.0625f : p.group ? 0.25f : 1.0f) : 0.0f;

@@ -574,10 +574,11 @@ HQ_API hq_status hq_kv_read_nvfp4(const uint8_t* cache, int64_t pages, int64_t p
  *   queries sees the keys j <= p = kv_len[s] - n + i, with a window only the `window` last of them (j > p - window).
  *   out = (softmax(scale q K^T) V) . H_group / sqrt(group);  query head h reads key head h / (q_heads / kv_heads).
  *   lse = the natural logarithm of the sum of exp(scale q K^T).  A query without keys gets out = 0, lse = -inf.
+ *   A NaN among the stored values reaches the rows that see its token and no others.
  *   Scores are exact up to their fp32 sums; weights are carried in 11 bits into sums in fp32; one rounding to bf16.
  *
  *   q, out : bf16 [T, q_heads, D]; q as hq_kv_append_nvfp4 leaves it, ld_q elements between tokens, 16-byte aligned
- *          tokens; out contiguous, 16-byte aligned.  Rows of no sequence are not written.  q_heads a multiple of
+ *          tokens; out contiguous, 16-byte aligned, apart from q.  Rows of no sequence are not written.  q_heads a multiple of
  *          kv_heads.
  *   page_table : int32 [S, table_pages] on the device, rows ld_table apart: page of the tokens page_size * i .. of the
  *          sequence (others than 0 .. pages - 1 are clamped).  Entries behind a sequence's last page are not read.

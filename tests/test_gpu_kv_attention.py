@@ -214,6 +214,32 @@ def test_many_sequences():
     Problem([(1, 5)] * 1000, 2, 1, 64, 16, seed=10).run()
 
 
+@pytest.mark.parametrize("page_size", [272, 4096])
+def test_large_pages(page_size):
+    Problem([(1, 1), (1, 300), (2, 5000)], 4, 2, 64, page_size).run()
+    Problem([(100, 100), (40, 600)], 4, 2, 128, page_size).run()
+
+
+def test_prompts_of_many_sequences():
+    """More than the plan's sums hold at a time, most of them short or idle."""
+    seqs = [(i % 3 if i % 7 else 0, i % 40 + 3) for i in range(1100)]
+    seqs[0], seqs[600], seqs[1099] = (70, 70), (40, 300), (50, 51)
+    Problem(seqs, 2, 1, 64, 16).run()
+
+
+@pytest.mark.parametrize("seqs", [[(1, 100), (1, 900)], [(90, 300)]])
+def test_a_cache_past_4_gigabytes(seqs):
+    p = Problem(seqs, 4, 2, 128, 64)
+    want = p.call()
+    each = p.cache[0].numel()
+    big = torch.empty((2 ** 32 // each + 50 + len(p.cache), *p.cache.shape[1:]), dtype=torch.uint8, device="cuda")
+    big[-len(p.cache):] = p.cache
+    for i, (_, n) in enumerate(seqs):
+        p.table[i, :-(-n // 64)] += len(big) - len(p.cache)
+    p.cache = big
+    assert all(torch.equal(a, b) for a, b in zip(p.call(), want))
+
+
 @pytest.mark.parametrize("max_q", [0, 1, 4, 1000, 10 ** 12])
 def test_max_q_only_chooses(max_q):
     Problem([(9, 80), (1, 200), (70, 150)], 4, 2, 128, 16, seed=11).run(max_q=max_q)
@@ -233,6 +259,56 @@ def test_small_and_large_queries():
 def test_negative_and_zero_scale():
     Problem([(1, 300), (2, 90), (140, 140)], 4, 2, 128, 16, scale=-0.01, seed=14).run()
     Problem([(1, 300), (2, 90), (140, 140)], 4, 2, 128, 16, scale=0.0, seed=14).run()
+
+
+@pytest.mark.parametrize("D,group", [(64, 0), (64, 16), (128, 16), (256, 0), (256, 256)])
+@pytest.mark.parametrize("seqs,Hq,Hkv", [([(1, 50), (1, 900)], 4, 2), ([(4, 70), (2, 1500), (3, 3)], 4, 1), ([(200, 200), (300, 900), (40, 41)], 4, 2),
+                                         ([(1500, 4000)], 2, 1)])
+@pytest.mark.parametrize("window", [0, 24])
+def test_nan_reaches_the_rows_that_see_it(D, group, seqs, Hq, Hkv, window):
+    """A NaN among the stored values: its channels (rotated back, its group's) of the rows that see its token, and nothing
+    else, to the bit.  A NaN among the keys: all channels of the rows that see it, and no other row."""
+    p = Problem(seqs, Hq, Hkv, D, 32, group, window, seed=11)
+    clean, clean_lse = p.call()
+    spoiled, base = p.cache.clone(), p.cache.clone()
+    rng = np.random.default_rng(5)
+    width = group or 16
+    hit = torch.zeros_like(clean, dtype=torch.bool)
+    blind = torch.zeros(p.T, Hq, dtype=torch.bool, device="cuda")  # rows that see a NaN key
+
+    def rows(i, token):  # of the sequence, that see the token
+        nq, n = seqs[i]
+        pos = np.arange(n - nq, n)
+        return int(p.q_start[i]) + np.nonzero((token <= pos) & ((token > pos - window) if window else True))[0]
+
+    for i, (nq, n) in enumerate(seqs):
+        for token in {n - 1, n // 2, max(0, n - nq), max(0, n - nq // 2 - 1), *rng.integers(0, n, 3).tolist()}:
+            h, block = int(rng.integers(0, Hkv)), int(rng.integers(0, D // 16))
+            page = int(p.table[i, token // 32])
+            at = (page, h, token % 32 // 16, 17 * D + token % 16 * (D // 16) + block)
+            spoiled[at] = 0x7F if token % 2 else 0xFF
+            base[at] = 0  # (the rest of the row's sums, if they could be seen, are those of a zero)
+            heads = slice(h * Hq // Hkv, (h + 1) * Hq // Hkv)
+            first = block * 16 // width * width
+            for r in rows(i, token):
+                hit[r, heads, first:first + width] = True
+    p.cache = base
+    want, want_lse = p.call()
+    p.cache = spoiled
+    got, lse = p.call()
+    assert hit.any() and got[hit].isnan().all()
+    assert torch.equal(got[~hit], want[~hit]) and torch.equal(lse, want_lse)
+    p.cache = base.clone()
+    i = len(seqs) - 1
+    token = seqs[i][1] - 1 - seqs[i][0] // 3
+    p.cache[int(p.table[i, token // 32]), 0, token % 32 // 16, 16 * D + token % 16 * (D // 16)] = 0x7F
+    for r in rows(i, token):
+        blind[r, :Hq // Hkv] = True
+    got, lse = p.call()
+    assert blind.any() and got[blind].isnan().all() and lse[blind].isnan().all()
+    assert not got[~blind].isnan().any()
+    # (references move with other rows' scores: the sums differ by their rounding)
+    assert ((got - want)[~blind].abs() <= 2 ** -7 * want[~blind].abs() + 2 ** -9 * want.abs().amax()).all()
 
 
 def test_lengths_and_offsets_outside_are_clamped():
