@@ -163,7 +163,8 @@ hq_status hq_kv_append_nvfp4(const void* q, int64_t ld_q, const void* k, int64_t
   cudaError_t e = hq::sm_count(&sms);
   if (e == cudaSuccess)
     e = with_sizes(D, group, dtype == HQ_BF16, [&](auto d, auto g, auto b) {
-      return launch(hq::k_kv_append<d, g, b>, row_grid(T * (q_heads + 2 * kv_heads), D, sms), 256, 0,
+      auto kernel = rotary == D && !interleaved ? hq::k_kv_append<d, g, b, true> : hq::k_kv_append<d, g, b, false>;
+      return launch(kernel, row_grid(T * (q_heads + 2 * kv_heads), D, sms), 256, 0,
                     static_cast<cudaStream_t>(stream), p);
     });
   return e == cudaSuccess ? HQ_OK : cuda_fail(e);

@@ -107,7 +107,7 @@ __device__ __forceinline__ void kv_rotate(float (&x)[16]) {
 }
 
 // The same for pairs v[i] = (x[i], x[i + 8]): two channels an instruction.  Each sum and product is rounded alike.
-template <int G>
+template <int G, bool PAIRED>
 __device__ __forceinline__ void kv_rotate(float2 (&v)[8]) {
   if constexpr (G != 0) {
 #pragma unroll
@@ -124,7 +124,8 @@ __device__ __forceinline__ void kv_rotate(float2 (&v)[8]) {
     if constexpr (G == 256) {
       const int lane = threadIdx.x & 31;
 #pragma unroll
-      for (int m = 1; m < 16; m <<= 1) {
+      for (int k = 1; k < 16; k <<= 1) {  // blocks k apart; the lanes that hold them
+        const int m = !PAIRED ? k : k < 8 ? 2 * k : 1;
         const float sign = (lane & m) ? -1.0f : 1.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -147,14 +148,14 @@ __device__ __forceinline__ int64_t kv_record(int64_t slot, int head, int kv_head
   return ((page * kv_heads + head) * page_units + (unit - page * page_units)) * KvRecord<D>::kBytes;
 }
 
-template <int D, int G, bool BF16>
+template <int D, int G, bool BF16, bool PAIRED>
 __global__ void __launch_bounds__(256, BF16 ? 4 : 3) k_kv_append(const __grid_constant__ KvAppendParams p) {
   using R = KvRecord<D>;
   constexpr int kBlocks = D / 16, es = BF16 ? 2 : 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t heads = p.heads[0] + 2 * p.kv_heads, rows = static_cast<uint32_t>(p.T) * heads;  // (below 2^31)
-  const int b = threadIdx.x % kBlocks;
+  const int at_b = threadIdx.x % kBlocks, b = PAIRED ? at_b / 2 + at_b % 2 * (kBlocks / 2) : at_b;  // the thread's block of 16 channels
   const float r6 = __frcp_rn(6.0f);
   const float sg[2] = {kv_global_scale(__ldg(p.kv_amax)), kv_global_scale(__ldg(p.kv_amax + 1))};
   // (every lane of a warp goes on while one does: the lanes exchange values)
@@ -173,14 +174,37 @@ __global__ void __launch_bounds__(256, BF16 ? 4 : 3) k_kv_append(const __grid_co
     const bool store = live && slot >= 0 && (which == 0 || slot < p.n_slots);
     const uint8_t* const src = p.in[which] + t * p.ld[which] + static_cast<int64_t>(head) * (D * es);
     float2 x[8];  // channels k and k + 8
-    {
+    if constexpr (PAIRED) {  // 8 channels of either half turned together; then neighbours swap, for 16 in one piece each
+      float lo[8], hi[8];
+      kv_load8<BF16>(src + 8 * at_b * es, lo);
+      kv_load8<BF16>(src + (D / 2 + 8 * at_b) * es, hi);
+      if (which < 2) {
+        int64_t pos = __ldg(p.positions + t);
+        pos = pos < 0 ? 0 : pos >= p.rows ? p.rows - 1 : pos;
+        float c[8], s[8];
+        kv_load8<false>(reinterpret_cast<const uint8_t*>(p.cos_t + pos * (D / 2) + 8 * at_b), c);
+        kv_load8<false>(reinterpret_cast<const uint8_t*>(p.sin_t + pos * (D / 2) + 8 * at_b), s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x1 = lo[i], x2 = hi[i];
+          lo[i] = __fsub_rn(__fmul_rn(x1, c[i]), __fmul_rn(x2, s[i]));
+          hi[i] = __fadd_rn(__fmul_rn(x2, c[i]), __fmul_rn(x1, s[i]));
+        }
+      }
+      const bool odd = at_b & 1;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo[i] : hi[i], 1);
+        x[i] = odd ? make_float2(got, hi[i]) : make_float2(lo[i], got);
+      }
+    } else {
       float lo[8], hi[8];
       kv_load8<BF16>(src + 16 * b * es, lo);
       kv_load8<BF16>(src + (16 * b + 8) * es, hi);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = make_float2(lo[i], hi[i]);
     }
-    if (which < 2 && 16 * b < p.rotary) {
+    if (!PAIRED && which < 2 && 16 * b < p.rotary) {
       int64_t pos = __ldg(p.positions + t);
       pos = pos < 0 ? 0 : pos >= p.rows ? p.rows - 1 : pos;
       const int half = p.rotary / 2;
@@ -218,7 +242,7 @@ __global__ void __launch_bounds__(256, BF16 ? 4 : 3) k_kv_append(const __grid_co
         }
       }
     }
-    kv_rotate<G>(x);
+    kv_rotate<G, PAIRED>(x);
     if (!store) continue;
     if (which == 0) {
       uint32_t w[8];
