@@ -37,11 +37,15 @@ __device__ __forceinline__ float kv_global_scale(float amax) {
 //
 // A thread takes 16 channels of a (token, head): position rotation (two products and a sum, each rounded, as the
 // definition in hq.h has them), butterfly in pairs of channels, then for K and V the block scale and codes exactly as
-// hq_rotate_quant_nvfp4, with the quantizer's corrected quotients.  Instructions and the latency of positions and tables
-// bound it, not memory: 8192 tokens of 32 + 2 * 8 heads of 128 take 52 us (60 with a butterfly of single channels and
-// divisions), 36 without the position rotation; the bytes alone 26.  Four CTAs per SM (64 registers): a thread that
-// went over the heads of its token with cosines in registers needed 91, and took 60; the next row's position read one
-// row ahead 56.
+// hq_rotate_quant_nvfp4, with the quantizer's corrected quotients.  PAIRED (all of a head turned, halves against each
+// other): a thread loads and turns 8 channels of either half, so that each table entry and each channel is loaded once,
+// and swaps one of them with its neighbour.
+// Instructions and the latency of positions and tables bound it, not memory: 8192 tokens of 32 + 2 * 8 heads of 128 in
+// bf16 take 45 us (52 without pairs of halves; 60 with a butterfly of single channels and divisions besides), 36 without
+// the position rotation; the bytes alone 26.  CTAs per SM: five (48 registers) where that does not spill, 47 us with
+// four; the form without pairs spills at 48 (36 us without rotation become 41).  Fewer, longer threads lost: one that
+// went over the heads of its token with cosines in registers needed 91 registers and took 60 us; the next row's
+// position read one row ahead cost 4 us.
 // ---------------------------------------------------------------------------
 struct KvAppendParams {
   const uint8_t* in[3];  // q, k, v
@@ -149,7 +153,7 @@ __device__ __forceinline__ int64_t kv_record(int64_t slot, int head, int kv_head
 }
 
 template <int D, int G, bool BF16, bool PAIRED>
-__global__ void __launch_bounds__(256, BF16 ? 4 : 3) k_kv_append(const __grid_constant__ KvAppendParams p) {
+__global__ void __launch_bounds__(256, !BF16 ? 3 : PAIRED ? 5 : 4) k_kv_append(const __grid_constant__ KvAppendParams p) {
   using R = KvRecord<D>;
   constexpr int kBlocks = D / 16, es = BF16 ? 2 : 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
