@@ -40,10 +40,16 @@ struct Plan {
 };
 
 // The cheapest by this estimate, in cycles: 128 codes take a pair 1300 (two stages through its warps); a single CTA 330
-// (likewise) or 5.5 per channel (an SM's share of the memory's rate, where all of them load).  A
-// wide tile ends with an epilogue of 3500 that nothing hides, a split one with the cluster's sum, and each split
-// tile starts anew.  Measured, us: 48 x 28672 x 8192 with 128 channels per tile (224 tiles on 152 SMs) 52.6, with 96
-// (299) 43.6; [777, 1056] x 1100 narrow 7.9, wide 14.
+// (likewise) or 5.5 per channel (an SM's share of the memory's rate, where all of them load).  A wide tile ends with an
+// epilogue of 3500 that nothing hides, a split one with the cluster's sum.  Sums are split only where all clusters run at
+// once: each one after the first would start anew.
+// Measured, us, M x N x K:                  narrow   wide      wide tiles of fewer tokens take hardly less (512 x
+//   64 x 4096 x 4096                          12.3   23.7      4096 x 4096 in 32 tiles of 256 tokens 26.9, in 64 of
+//   777 x 1100 x 1056                          7.1   11.7      128 25.1): a stage's time is the channels' way through
+//   8192 x 8192 x 8192                        1221    634      the widening warps
+//   48 x 28672 x 8192    narrow tiles of 128 channels (224 on 152 SMs) 60, of 96 (299) 50
+//   64 x 4096 x 4096     sums split 12.3, whole 15.1;   1 x 4096 x 4096 8.7 and 14.3
+//   2000 x 600 x 8192    sums split in two rounds of clusters 54, whole 49
 Plan plan_of(int64_t M, int64_t N, int64_t K, int sms, const int (&clusters)[9]) {
   const int64_t stages = (K + 127) / 128;
   Plan best = {};
@@ -54,7 +60,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int sms, const int (&clusters)[9])
     for (int64_t lanes = 128; lanes >= (wide ? 128 : 64); lanes -= 16) {
       const int64_t tiles_a = (N + lanes * (1 + wide) - 1) / (lanes * (1 + wide)), tiles = tiles_a * parts;
       for (int64_t s = 1; s <= (wide ? 1 : hq::kGemm8MaxSplits); s *= 2) {
-        if (s > 1 && stages < 2 * s) break;
+        if (s > 1 && (stages < 2 * s || tiles > clusters[s])) break;
         const int64_t places = wide ? sms / 2 : s > 1 ? clusters[s] : sms, waves = (tiles + places - 1) / places;
         const int64_t stage = wide ? 1300 : lanes * 11 / 2 > 330 ? lanes * 11 / 2 : 330;
         const int64_t cost = waves * ((stages + s - 1) / s * stage + (wide ? 3500 : s > 1 ? 2500 : 1200));

@@ -117,7 +117,7 @@ __device__ __forceinline__ void widen_piece(const uint8_t* rows, int r, int j, u
 
 // An arrival on a barrier of the pair's first CTA that releases what this CTA's threads wrote to their own shared and
 // tensor memory: there the tensor core reads it, and the fences in front have made it visible to it.  (Released to the whole
-// cluster, an arrival waits for 1000 cycles and more: [8192, 8192] x 8192 1094 us in place of 657.)
+// cluster, an arrival waits for 1000 cycles and more: [8192, 8192] x 8192 1093 us in place of 666.)
 __device__ __forceinline__ void mbar_arrive_cta(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
