@@ -85,6 +85,7 @@ def test_kv_attention(lib):
     st = caller(lib, "hq_kv_attention_nvfp4", ATTEND)
     for bad in CACHE + (dict(T=-1), dict(T=1 << 31), dict(S=-1), dict(S=1 << 31), dict(q_heads=0), dict(q_heads=7), dict(q_heads=5000),
                         dict(max_q=-1), dict(window=-1), dict(table_pages=-1), dict(ld_table=4), dict(table_pages=1 << 27, ld_table=1 << 27),
+                        dict(table_pages=(1 << 20) + 1, ld_table=1 << 27),
                         dict(pages=0), dict(ld_q=1000), dict(ld_q=1 << 62), dict(ld_table=1 << 62), dict(T=1 << 29)):
         assert st(**bad) == SHAPE, bad
     assert st(group=8) == GROUP and st(group=256) == SHAPE
@@ -93,7 +94,7 @@ def test_kv_attention(lib):
         assert st(**{k: None}) == NULL, k
     for k, off in (("q", 8), ("cache", 8), ("table", 2), ("kv_len", 2), ("q_start", 1), ("amax", 2), ("out", 8), ("lse", 2), ("work", 8)):
         assert st(**{k: P + off}) == ALIGN, k
-    assert st(ld_q=1028) == ALIGN
+    assert st(ld_q=1028) == ALIGN and st(table_pages=1 << 20, ld_table=1 << 20, work=P + 8) == ALIGN
     assert st(lse=None, work=P + 8) == ALIGN and st(table_pages=0, pages=0, table=None, cache=None, work=P + 8) == ALIGN
 
 
