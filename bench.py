@@ -51,6 +51,7 @@ NCU_TRAFFIC = {
     ("4f20776c7d3b556d", "bf16_32768x28672", 16): 1879127040 + 495954176,
     ("2a825b62b2d5afe7", "bf16_32768x28672", 16): 1879130880 + 497036544,
     ("d9b288a797c75a62", "bf16_32768x28672", 16): 1879114496 + 496476160,
+    ("d0bc320196724d4a", "bf16_32768x28672", 16): 1879241728 + 496588032,
 }
 
 
