@@ -19,7 +19,6 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 constexpr int64_t kMaxTokens = (int64_t{1} << 31) - 1024;  // counts of tokens and of rows (token, head)
 constexpr int64_t kMaxHeads = 4096;
 constexpr int64_t kMaxKeys = int64_t{1} << 25;  // of a sequence: its rows' way over them ends before a wait gives up
-constexpr int64_t kFewRows = 32;
 
 // Heads, head size, rotation group, pages.
 hq_status check_cache(int64_t kv_heads, int64_t D, int group, int64_t pages, int64_t page_size) {
@@ -81,29 +80,37 @@ cudaError_t launch_attend(const hq::KvAttendParams& p, int sms, cudaStream_t str
   return launch(hq::k_kv_combine<D, NT>, dim3(ctas, S::kRows), 256, 0, stream, p);
 }
 
-template <int D>
+template <int D, int SUB>
 cudaError_t launch_prompt(const hq::KvAttendParams& p, int sms, cudaStream_t stream) {
-  using S = hq::KvPromptShape<D>;
-  auto kernel = hq::k_kv_prompt<D>;
+  using S = hq::KvPromptShape<D, SUB>;
+  auto kernel = hq::k_kv_prompt<D, SUB>;
   const size_t smem = S::kSmemBytes + 1024;
   cudaError_t e = hq::allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int ctas = sms < hq::kKvMaxCtas ? sms : hq::kKvMaxCtas;
   if ((e = launch(kernel, dim3(ctas), S::kThreads, smem, stream, p)) != cudaSuccess) return e;
-  return launch(hq::k_kv_prompt_combine<D>, dim3(ctas, 8), 256, 0, stream, p);
+  return launch(hq::k_kv_prompt_combine<D, SUB>, dim3(ctas, 8), 256, 0, stream, p);
 }
 
-// The kernel for few rows (query tokens x heads that share a key head) of a sequence, or the one for many.  The one reads
-// the keys again for every 16 rows, the other takes up to 256 at once and little less time for fewer.  Measured, us, few /
-// many, of 32 query heads over 8 key heads:
-//   rows                                     16         32         48         64
-//   16 sequences of 4096 keys, D = 64      34 / 54    51 / 54    67 / 54    82 / 54
-//                              D = 128     38 / 90    61 / 91    84 / 90   107 / 91
-//                              D = 256     62 / 112  106 / 113  151 / 114  196 / 115
-//   64 sequences of 300 keys, D = 128      39 / 56    56 / 57    77 / 57
-//   1 sequence of 65536 keys, D = 128      34 / 86    52 / 84    71 / 85
-// Up to 8 rows the few rows' kernel takes 8 at a time: 31 us for 8 (D = 128) where the form of 16 takes 35.
-bool few_rows(int64_t T, int64_t max_q, int64_t share) { return (max_q < T ? max_q : T) <= kFewRows / share; }
+// The kernel for few rows (query tokens x heads that share a key head) of a sequence, or the ones for many.  The one reads
+// the keys again for every 16 rows (or takes 8 at a time: 31 us for 8 rows, D = 128, where the form of 16 takes 35); the
+// others take 128 or 256 and little less time for fewer.  Those of 128, one tile, multiply the next scores while these are
+// exponentiated; two tiles take turns, with the keys widened once for both.  Measured, us, few / one tile / two, of 32 query
+// heads over 8 key heads:
+//   rows                                      16                 32                48             128            400
+//   16 sequences of 4096 keys, D = 64      34 / 44 / 54      51 / 44 / 54      67 / 44 / 54       44 / 54
+//                              D = 128     38 / 57 / 90      61 / 57 / 91      84 / 57 / 92       58 / 93
+//                              D = 256     62 / 112         106 / 113         151 / 114
+//   64 sequences of 300 keys, D = 128      39 / 44 / 56      56 / 45 / 57      77 / 44 / 57       46 / 60
+//   1 sequence of 65536 keys, D = 128      34 / 56 / 86      52 / 56 / 84      71 / 56 / 86       56 / 85
+//   4 sequences of 4000 keys, D = 128                                                                            55 / 55
+// and of 4 sequences of 1000 tokens behind 4000 (4000 rows) one tile 346, two 264.
+bool few_rows(int64_t T, int64_t max_q, int64_t share, int64_t D) {
+  return (max_q < T ? max_q : T) <= (D == 256 ? 32 : 16) / share;
+}
+bool one_tile(int64_t T, int64_t max_q, int64_t share, int64_t D) {
+  return D == 256 || (max_q < T ? max_q : T) <= 128 / share;
+}
 
 }  // namespace
 
@@ -212,7 +219,7 @@ hq_status hq_kv_read_nvfp4(const uint8_t* cache, int64_t pages, int64_t page_siz
 int64_t hq_kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int64_t D, int64_t T, int64_t max_q) {
   if (check_cache(kv_heads, D, 0, 0, 16) != HQ_OK || q_heads < 1 || q_heads > kMaxHeads || q_heads % kv_heads != 0) return -1;
   if (T < 0 || T * (q_heads / kv_heads) > kMaxTokens || T > kMaxTokens || max_q < 0) return -1;
-  return few_rows(T, max_q, q_heads / kv_heads) ? hq::kv_part_bytes(static_cast<int>(D)) : hq::kv_prompt_bytes(static_cast<int>(D));
+  return few_rows(T, max_q, q_heads / kv_heads, D) ? hq::kv_part_bytes(static_cast<int>(D)) : hq::kv_prompt_bytes(static_cast<int>(D));
 }
 
 hq_status hq_kv_attention_nvfp4(const void* q, int64_t ld_q, int64_t T, int64_t q_heads, const uint8_t* cache, int64_t pages,
@@ -260,8 +267,9 @@ hq_status hq_kv_attention_nvfp4(const void* q, int64_t ld_q, int64_t T, int64_t 
   cudaError_t e = hq::sm_count(&sms);
   if (e != cudaSuccess) return cuda_fail(e);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (!few_rows(T, max_q, p.share))
-    e = D == 64 ? launch_prompt<64>(p, sms, cs) : D == 128 ? launch_prompt<128>(p, sms, cs) : launch_prompt<256>(p, sms, cs);
+  if (!few_rows(T, max_q, p.share, D))
+    e = !one_tile(T, max_q, p.share, D) ? (D == 64 ? launch_prompt<64, 2>(p, sms, cs) : launch_prompt<128, 2>(p, sms, cs))
+        : D == 64 ? launch_prompt<64, 1>(p, sms, cs) : D == 128 ? launch_prompt<128, 1>(p, sms, cs) : launch_prompt<256, 1>(p, sms, cs);
   else if ((max_q < T ? max_q : T) * p.share <= 8)
     e = D == 64 ? launch_attend<64, 1>(p, sms, cs) : D == 128 ? launch_attend<128, 1>(p, sms, cs) : launch_attend<256, 1>(p, sms, cs);
   else

@@ -4,11 +4,12 @@
 // The mathematics and the number formats are those of hq_kv_attend.cuh: codes widened exactly to f16, q scaled by a power of
 // two per row, p in f16 scaled by 2^7 against a reference that moves only when a score exceeds it by 2^8 (and then by a power of two).
 //
-// A CTA takes 128 rows (query token, head of the group that shares a key head) per tile of the tensor core and, up to D =
-// 128, two such tiles at once, so that the scores of one are multiplied while the other's are exponentiated.  Keys come
-// in tiles of 128 (64 for D = 256), widened once for both:
+// A CTA takes 128 rows (query token, head of the group that shares a key head) per tile of the tensor core.  Where there are
+// more, and up to D = 128, it takes two such tiles at once (SUB = 2), so that the scores of one are multiplied while the
+// other's are exponentiated; with one, the next scores go into columns of their own.  Keys come in tiles of 128 (64 for
+// D = 256), widened once for both:
 //   S = Q K^T   Q and K in shared memory along the channels, S in tensor memory
-//   O += P V    P in tensor memory over S's columns, V in shared memory as it comes (the instruction takes it across)
+//   O += P V    P in tensor memory (two tiles, D = 128: over S's columns), V in shared memory as it comes (the instruction takes it across)
 // Roles of a CTA:
 //   warp 0        issues the products
 //   warp 1        allocates tensor memory
@@ -30,9 +31,9 @@
 
 namespace hq {
 
-template <int D>
+template <int D, int SUB>
 struct KvPromptShape {
-  static constexpr int kSub = D == 256 ? 1 : 2;       // tiles of 128 rows
+  static constexpr int kSub = SUB;                    // tiles of 128 rows
   static constexpr int kRows = 128 * kSub;
   static constexpr int kKeys = D == 256 ? 64 : 128;   // of a tile
   static constexpr int kQBytes = 128 * D * 2;         // of a tile of rows
@@ -42,9 +43,11 @@ struct KvPromptShape {
   static constexpr int kUsed = kVAt + 2 * kKvBytes;
   static constexpr int kSmemBytes = kUsed < 116 * 1024 ? 116 * 1024 : kUsed;  // (a CTA takes all of tensor memory)
   static constexpr int kThreads = 32 * (12 + 4 * kSub);
-  // Tensor memory: two of S, O of each tile, two of P; for D = 128 there is no room for P but in S's first columns.
-  static constexpr int kColO = 2 * kKeys, kColP = D == 128 ? 0 : kColO + kSub * D;
-  static constexpr int kStepP = D == 128 ? kKeys : kKeys / 2;  // columns from one P to the other
+  // Tensor memory: two of S, O of each tile, two of P; for two tiles and D = 128 there is no room for P but in S's first
+  // columns.
+  static constexpr bool kOver = D == 128 && kSub == 2;
+  static constexpr int kColO = 2 * kKeys, kColP = kOver ? 0 : kColO + kSub * D;
+  static constexpr int kStepP = kOver ? kKeys : kKeys / 2;  // columns from one P to the other
   static_assert(kColO + kSub * D <= 512 && kColP + 2 * (kKeys / 2) <= 512, "tensor memory has 512 columns");
   static_assert(kSmemBytes + 1024 + 8192 <= 227 * 1024 && 2 * (kSmemBytes + 1024) > 228 * 1024, "one CTA per SM");
   // Registers of a thread: at the launch, and by role.
@@ -351,9 +354,9 @@ __device__ __noinline__ uint32_t kv_nan_blocks(const KvAttendParams& p, const in
   return mine;
 }
 
-template <int D>
-__global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(const __grid_constant__ KvAttendParams p) {
-  using S = KvPromptShape<D>;
+template <int D, int SUB>
+__global__ void __launch_bounds__((KvPromptShape<D, SUB>::kThreads), 1) k_kv_prompt(const __grid_constant__ KvAttendParams p) {
+  using S = KvPromptShape<D, SUB>;
   using R = KvRecord<D>;
   constexpr int kSub = S::kSub, kRows = S::kRows, kKeys = S::kKeys;
   using Walk = KvPromptWalk<kRows, kKeys>;
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
       // S = Q K^T; `over`: into columns whose P the last product into O may still read.  (In two halves, of which only the
       // one over P waits, the products of 64 columns take as long as those of 128: 778 us for four prompts at a time when one piece took 682.)
       auto scores = [&](int t, int buffer, bool over) {
-        if (D == 128 && over) {
+        if (S::kOver && over) {
           ok = warp_wait(smem_addr(&bars.o_full[t]), o_phase >> t & 1 ^ 1);
           if (!ok) return;
         }
@@ -772,7 +775,7 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
               sum[c & 1] = add2(sum[c & 1], e);
               w[c] = bits_of(__floats2half2_rn(e.x, e.y));
             }
-            tmem_store_nowait(tp + c0 / 2 + 16 * half, w);  // (D = 128: over columns of S that have been read)
+            tmem_store_nowait(tp + c0 / 2 + 16 * half, w);  // (kOver: over columns of S that have been read)
           }
           l += sum[0].x + sum[0].y + (sum[1].x + sum[1].y);
         }
@@ -871,9 +874,9 @@ __global__ void __launch_bounds__(KvPromptShape<D>::kThreads, 1) k_kv_prompt(con
 }
 
 // Items that were cut: blockIdx.x the CTA that an item begins in, blockIdx.y a slice of its rows.
-template <int D>
+template <int D, int SUB>
 __global__ void __launch_bounds__(256) k_kv_prompt_combine(const __grid_constant__ KvAttendParams p) {
-  using S = KvPromptShape<D>;
+  using S = KvPromptShape<D, SUB>;
   constexpr int kRows = S::kRows, kLanes = D / 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -180,6 +180,16 @@ def test_prompts_with_a_window(D, window):
     Problem([(200, 200), (100, 700), (3, 500), (1, 90)], 4, 2, D, 48, window=window, seed=window).run()
 
 
+@pytest.mark.parametrize("D,group", [(64, 16), (128, 16), (128, 0)])
+@pytest.mark.parametrize("Hq,Hkv,q", [(4, 1, 32), (2, 2, 128), (8, 1, 9), (6, 2, 42)])
+@pytest.mark.parametrize("window", [0, 70])
+def test_rows_of_one_tile(D, group, Hq, Hkv, q, window):
+    """33 to 128 rows of a sequence have a form of their own; sequences with more go through it in several tiles."""
+    p = Problem([(q, q), (1, 700), (q - 3, 1500), (0, 9), (q, 260), (2 * q, 2 * q + 5)], Hq, Hkv, D, 32, group, window, seed=13)
+    for max_q in (q, 2 * q, 10 ** 6):
+        p.run(max_q=max_q)
+
+
 def test_more_queries_than_keys():
     """The first queries stand before the first key: nothing to see."""
     p = Problem([(5, 3), (4, 0), (1, 0), (20, 7)], 4, 2, 64, 16, seed=3)
