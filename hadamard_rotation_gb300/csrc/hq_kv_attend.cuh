@@ -349,6 +349,17 @@ __device__ __forceinline__ void kv_finish(const KvAttendParams& p, float (&o)[8]
     p.lse[row * p.heads + head] = sum > 0.0f || sum != sum ? (top - kKvShift + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
+// Is the phase of `bar` with parity `parity` complete?
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_attend(const __grid_constant__ KvAttendParams p) {
   using S = KvAttendShape<D, NT>;
@@ -389,34 +400,44 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
     const uint64_t policy = l2_stream_policy();
     const KvShare share = kv_share<kRows>(p, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x));
     Walk walk(p, share.w0, share.w1);
-    // Batches of 32 records; the pages of the next one are looked up while this one's copies are issued.
+    // Batches of 32 records.  The pages of the next one are looked up before this one's copies are issued, unless its
+    // segment has to wait for a place of the ring: that place may be held by the segment of the batch in hand, which ends only
+    // once its records are there, and segments without records take places too.
+    enum Next { kNone, kBatch, kLater };
     typename Walk::Segment g;
     int turn = 0, u0 = 0, id = 0;
+    bool more = true, told = true;  // there is a segment in `g`; the other warps know of it
     KvCut cut{0, 0, 0, -1, {}};
     g.u0 = g.u1 = 0;
-    auto advance = [&]() {  // to the next batch; false: there is none
-      u0 += 32;
-      while (u0 >= g.u1) {
-        const bool more = walk.next(g);
-        if (!more) g.s = -1, g.u0 = g.u1 = 0;
-        else if (g.starts && !g.ends) cut = KvCut{g.s, g.tile, g.head, static_cast<int>((g.stop - 1) / share.per), {}};
-        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(smem_addr(&task_empty[turn % kRing]), turn / kRing & 1 ^ 1));
-        if (!ok) return false;
+    auto advance = [&](bool wait) {  // to the next batch; kLater: its segment, `g`, would have to wait
+      if (told) u0 += 32;
+      while (!told || u0 >= g.u1) {
+        if (told) {
+          more = walk.next(g);
+          if (!more) g.s = -1, g.u0 = g.u1 = 0;
+          else if (g.starts && !g.ends) cut = KvCut{g.s, g.tile, g.head, static_cast<int>((g.stop - 1) / share.per), {}};
+          told = false;
+        }
+        const uint32_t place = smem_addr(&task_empty[turn % kRing]), parity = turn / kRing & 1 ^ 1;
+        if (!wait && !__all_sync(0xFFFFFFFFu, mbar_test(place, parity))) return kLater;
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(place, parity));
+        if (!ok) return kNone;
         if (lane == 0) {
           tasks[turn % kRing] = g;
           asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&task_full[turn % kRing])) : "memory");
         }
         ++turn;
-        if (!more) return false;
+        told = true;
+        if (!more) return kNone;
         u0 = g.u0;
       }
       if (u0 + lane < g.u1)
         asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(id) : "l"(p.table + g.s * p.ld_table + (u0 + lane) / p.page_units));
-      return true;
+      return kBatch;
     };
-    for (bool more = advance(); more;) {
+    for (Next next = advance(true); next == kBatch;) {
       const int u = u0 + lane, n = min(32, g.u1 - u0), head = g.head, page = id;
-      more = advance();
+      next = advance(false);
       const int64_t at = min(static_cast<int64_t>(max(page, 0)), p.pages - 1);
       const uint8_t* const src = p.cache + ((at * p.kv_heads + head) * p.page_units + u % p.page_units) * R::kBytes;
       const uint32_t slot = (k + lane) % kSlots, pass = (k + lane) / kSlots & 1;
@@ -428,6 +449,7 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
         __syncwarp();
       }
       k += n;
+      if (next == kLater) next = advance(true);
     }
     if (lane == 0) kv_cuts<D>(p.part)[blockIdx.x] = cut;
     // what is on its way lands before the CTA may end

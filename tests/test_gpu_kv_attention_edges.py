@@ -1,0 +1,26 @@
+"""Attention over the paged cache where its plan, its hand-overs and its numbers are at their ends.  What is not said
+here (the problems, the definition in 64 bits, the tolerances and their derivation) is in test_gpu_kv_attention.py.
+"""
+import pytest
+import torch
+
+import hadamard_rotation_gb300 as hq
+from test_gpu_kv_attention import Problem, built  # noqa: F401 (the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("seqs,Hq,Hkv,D", [
+    ([(1, 2000)] * 40 + [(1, 0)] * 24, 32, 8, 128),
+    ([(1, 1500)] * 60 + [(1, 0)] * 2 + [(1, 1500)] * 40, 8, 8, 64),
+    ([(1, 1200)] * 60 + [(1, 0)] * 60, 32, 8, 256),
+    ([(5, 2500), (5, 0), (5, 0)] * 20, 8, 8, 64),
+    ([(2, 1500)] * 60 + [(2, 0)] * 40, 40, 4, 256),
+])
+def test_queries_without_keys_among_others(seqs, Hq, Hkv, D):
+    """Runs of items without records in a share that has others: more of them than the other warps are told of ahead."""
+    p = Problem(seqs, Hq, Hkv, D, 64, seed=21)
+    out, lse = p.call(out=torch.full_like(p.q, float("nan")))
+    assert hq.hq_read_fault() == 0
+    assert torch.isfinite(out).all()  # (all rows are written; a third of them are compared)
+    p.check(out, lse, range(1, len(seqs), 3))
