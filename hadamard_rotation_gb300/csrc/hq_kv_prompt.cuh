@@ -756,11 +756,13 @@ __global__ void __launch_bounds__((KvPromptShape<D, SUB>::kThreads), 1) k_kv_pro
               }
             };
             if (j > sub.j0) scale(to, D, [&](uint32_t w) { return __float_as_uint(__uint_as_float(w) * f); });
-            if (c0 > 0)
+            if (c0 > 0) {
+              tmem_store_wait();  // (the first columns' weights are there before they are loaded again)
               scale(tp, c0 / 2, [&](uint32_t w) {
                 const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&w));
                 return bits_of(__floats2half2_rn(e.x * f, e.y * f));
               });
+            }
           }
           const float off = kKvShift - m;
           float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};

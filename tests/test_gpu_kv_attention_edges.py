@@ -24,3 +24,15 @@ def test_queries_without_keys_among_others(seqs, Hq, Hkv, D):
     assert hq.hq_read_fault() == 0
     assert torch.isfinite(out).all()  # (all rows are written; a third of them are compared)
     p.check(out, lse, range(1, len(seqs), 3))
+
+
+@pytest.mark.parametrize("D,group", [(64, 16), (128, 16)])
+@pytest.mark.parametrize("seqs", [[(30, 500), (1, 100)], [(200, 500), (40, 128)]])  # one tile of rows at a time, two
+@pytest.mark.parametrize("window", [0, 60, 400])
+def test_scores_that_rise_within_a_tile_of_keys(D, group, seqs, window):
+    """Keys 0..63 of each 128 small, the others large: references move between the halves of a tile, the first one's too;
+    with a window rows see nothing of a first half."""
+    p = Problem(seqs, 4, 1, D, 64, group=group, window=window, seed=22, scale=8 * D ** -0.5)
+    for i, (_, n) in enumerate(seqs):
+        p.cache[p.table[i, :-(-n // 64)][::2].long(), ..., 16 * D:17 * D] = 0x08  # K's scales: 2^-6
+    p.run()
