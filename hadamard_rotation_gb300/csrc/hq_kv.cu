@@ -258,7 +258,8 @@ hq_status hq_kv_attention_nvfp4(const void* q, int64_t ld_q, int64_t T, int64_t 
   p.share = static_cast<int>(q_heads / kv_heads);
   p.kv_amax = kv_amax;
   p.scale = scale;
-  p.window = static_cast<int>(window < kMaxTokens ? window : 0);  // (a window that nothing leaves)
+  // (A window that no key leaves is none; others are below 2^25, far from where differences with them would leave 32 bits.)
+  p.window = static_cast<int>(window < p.most ? window : 0);
   p.group = group;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;

@@ -36,3 +36,16 @@ def test_scores_that_rise_within_a_tile_of_keys(D, group, seqs, window):
     for i, (_, n) in enumerate(seqs):
         p.cache[p.table[i, :-(-n // 64)][::2].long(), ..., 16 * D:17 * D] = 0x08  # K's scales: 2^-6
     p.run()
+
+
+@pytest.mark.parametrize("seqs", [[(1400, 100), (1, 40)], [(3000, 2000)], [(2, 30), (1, 700)]])
+@pytest.mark.parametrize("max_q", [1, 3000])  # the kernel for few rows, that for many
+def test_windows_that_nothing_leaves(seqs, max_q):
+    """Also behind queries that far outnumber the keys: the first of them stand 1000 places and more before key 0."""
+    p = Problem(seqs, 2, 1, 64, 16, seed=23)
+    want = p.call(max_q=max_q)
+    p.check(*want)
+    for window in (max(n for _, n in seqs), 2 ** 25, 2 ** 31 - 1500, 2 ** 31 - 1026, 2 ** 31 - 1025, 2 ** 31 - 1, 2 ** 62):
+        p.window = window
+        for a, b in zip(p.call(max_q=max_q), want):
+            assert torch.equal(a, b), window
