@@ -657,6 +657,7 @@ __global__ void __launch_bounds__((KvPromptShape<D, SUB>::kThreads), 1) k_kv_pro
       const int64_t token = g.seq.q0 + i;
       const int head = g.head * p.share + (at - i * p.share);
       const bool some = sub.j0 < sub.j1;
+      const int end = live ? g.seq.n - g.seq.nq + i + 1 : 0, begin = p.window ? end - p.window : 0;
       // Q: the warp's rows along their channels, kLanes lanes a row.
       float mult = 0.0f;
       if (some) {
@@ -692,12 +693,13 @@ __global__ void __launch_bounds__((KvPromptShape<D, SUB>::kThreads), 1) k_kv_pro
             *reinterpret_cast<uint4*>(piece(row, lane % kLanes)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
-        mult = fmaxf(mult * to_log2, 1e-37f);  // (not 0: a masked score is -inf times it)
+        mult *= to_log2;
+        // (not 0: a masked score is -inf times it; a NaN is for the rows that see a key)
+        if (mult < 1e-37f || end <= 0) mult = 1e-37f;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&bars.q_full[t]));
       }
-      const int end = live ? g.seq.n - g.seq.nq + i + 1 : 0, begin = p.window ? end - p.window : 0;
       float m = kKvNone, l = 0.0f;
       for (int j = sub.j0; j < sub.j1; ++j) {
         const int buffer = kSub == 1 ? j & 1 : t;

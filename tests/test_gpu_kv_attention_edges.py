@@ -1,6 +1,8 @@
 """Attention over the paged cache where its plan, its hand-overs and its numbers are at their ends.  What is not said
 here (the problems, the definition in 64 bits, the tolerances and their derivation) is in test_gpu_kv_attention.py.
 """
+import math
+
 import pytest
 import torch
 
@@ -49,3 +51,25 @@ def test_windows_that_nothing_leaves(seqs, max_q):
         p.window = window
         for a, b in zip(p.call(max_q=max_q), want):
             assert torch.equal(a, b), window
+
+@pytest.mark.parametrize("D,group", [(64, 16), (128, 0), (256, 256)])
+@pytest.mark.parametrize("seqs", [[(2, 1), (1, 0), (1, 300), (3, 40)], [(200, 150), (40, 0), (30, 700)]])  # few rows, many
+@pytest.mark.parametrize("window", [0, 20])
+def test_amax_and_scale_that_are_none(D, group, seqs, window):
+    """A NaN amax of the keys or scale: NaN for all rows that see keys, whichever kernel takes them; of the values: the same,
+    with the sums of weights as they are.  Rows without keys stay zeros."""
+    p = Problem(seqs, 4, 2, D, 32, group=group, window=window, seed=24)
+    want, want_lse = p.call()
+    blind = want_lse == -math.inf
+    assert blind.any() and not blind.all()
+    amax, scale = p.kv_amax.clone(), p.scale
+    for which in ("K", "V", "scale"):
+        p.kv_amax, p.scale = amax.clone(), scale
+        if which == "scale":
+            p.scale = math.nan
+        else:
+            p.kv_amax["KV".index(which)] = math.nan
+        out, lse = p.call()
+        assert out[~blind].isnan().all() and not out[blind].any(), which
+        assert (lse[blind] == -math.inf).all(), which
+        assert torch.equal(lse, want_lse) if which == "V" else lse[~blind].isnan().all(), which
