@@ -25,6 +25,7 @@
 // (cp.async.bulk, one per record), and the other warps take them in turn.
 #pragma once
 
+#include <float.h>
 #include <limits.h>
 
 #include <type_traits>
@@ -58,7 +59,7 @@ constexpr int kKvMinUnits = 60;  // work per CTA at least where items have as ma
 // What an item costs beside its records (Q, the joining of the warps' sums), as work of this many before its first.
 // (Without, CTAs with many short items ended last: 37 sequences of 12 heads and some 60 records each 42 us, with it 24.)
 constexpr int kKvItemUnits = 28;
-constexpr float kKvNone = -1e30f;
+constexpr float kKvNone = -FLT_MAX;  // the reference before a row's first score, below or equal to any
 constexpr float kKvSlack = 8.0f, kKvShift = 7.0f;
 
 template <int D, int NT>

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import hadamard_rotation_gb300 as hq
-from test_gpu_kv_attention import Problem, built  # noqa: F401 (the fixture)
+from test_gpu_kv_attention import GRID, Problem, built, values  # noqa: F401 (the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -52,6 +52,7 @@ def test_windows_that_nothing_leaves(seqs, max_q):
         for a, b in zip(p.call(max_q=max_q), want):
             assert torch.equal(a, b), window
 
+
 @pytest.mark.parametrize("D,group", [(64, 16), (128, 0), (256, 256)])
 @pytest.mark.parametrize("seqs", [[(2, 1), (1, 0), (1, 300), (3, 40)], [(200, 150), (40, 0), (30, 700)]])  # few rows, many
 @pytest.mark.parametrize("window", [0, 20])
@@ -73,3 +74,33 @@ def test_amax_and_scale_that_are_none(D, group, seqs, window):
         assert out[~blind].isnan().all() and not out[blind].any(), which
         assert (lse[blind] == -math.inf).all(), which
         assert torch.equal(lse, want_lse) if which == "V" else lse[~blind].isnan().all(), which
+
+
+@pytest.mark.parametrize("size", [1e3, 3e7, 2e8, 5e9, 1e20, 2e30, 3e36])
+@pytest.mark.parametrize("D,q", [(64, 1), (128, 4), (256, 1)])
+def test_scores_of_any_magnitude(D, q, size):
+    """Scores of `size` times one of E2M1's numbers and no two largest alike: the weights are 1 and 0.  The keys' first channel has
+    the number, the queries' is the only one that is not zero, so a score is rounded as a product and not as a sum; the largest comes
+    late or early, and is positive or negative.  out is the value itself (group 0, one rounding), lse the score to 2^-20."""
+    n = 700
+    for best, low, mid, high in ((650, 15, 3, 6), (5, 15, 3, 6), (300, 1, 3, 6), (100, 0, 3, 6), (650, 15, 14, 9), (3, 15, 14, 9)):
+        p = Problem([(q, n)], 4, 2, D, 32, group=0, seed=25, scale=1.0, kv_amax=(6.0, 6.0), garbage=False)
+        rec = p.cache[p.table[0, :-(-n // 32)].long()]  # [pages, heads, units, 18 D]
+        rec[..., :8 * D] = 0
+        rec[..., 16 * D:17 * D] = 0x38  # 1
+        k = rec[..., :8 * D].unflatten(-1, (16, D // 2))  # (a view)
+        number = torch.full((len(rec) * 32,), low, dtype=torch.uint8, device="cuda")
+        number[64:90], number[best] = mid, high
+        k[..., 0] = number.view(len(rec), 1, 2, 16)
+        p.cache[p.table[0, :-(-n // 32)].long()] = rec
+        p.q.zero_()
+        p.q[..., 0] = torch.linspace(0.5, 1, p.T, device="cuda")[:, None].to(torch.bfloat16)
+        p.scale = size
+        out, lse = p.call()
+        seen = torch.arange(n - q, n, device="cuda") >= best
+        rows = seen.nonzero()[:, 0]
+        assert len(rows)
+        top = size * GRID[high] * p.q[rows, :, 0].double()
+        assert ((lse[rows].double() - top).abs() <= 2.0 ** -20 * top.abs()).all(), (best, low)
+        v = torch.stack([values(p.cache, p.table[0, :-(-n // 32)], h, n, 1, 1.0)[best] for h in (0, 0, 1, 1)])
+        assert torch.equal(out[rows].double(), v.to(torch.bfloat16).double().expand(len(rows), -1, -1)), (best, low)
