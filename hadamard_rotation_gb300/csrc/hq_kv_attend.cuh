@@ -12,8 +12,9 @@
 // 2^9), so its 8 bits are exact too, and scores are rounded only by the fp32 sums.
 //
 // p is carried in f16 (2^-11 of each p; sums of p and of p V in fp32).  The reference m moves only when a score
-// exceeds it by more than 2^8, which saves the maximum across lanes at each step; p is scaled by 2^7, so p stays
-// below 2^15 and what is flushed is below 2^-31 of the reference's.
+// exceeds it by 2^8, which saves the maximum across lanes at each step; p is scaled by 2^7, so p stays below 2^15
+// (where a step of fp32 at the score is 8, m - 7 is m - 8, and without the scores at 2^8 itself p would be 2^16) and what is
+// flushed is below 2^-31 of the reference's.
 //
 // Channels and tokens are permuted within a record so that every thread reads whole words: thread (g, c) = (lane / 4,
 // lane % 4) takes channels [D c / 4, D (c + 1) / 4) of two tokens of K, and [D g / 8, D (g + 1) / 8) of four tokens of
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) above |= s[x][nt][i] > m[nt][i & 1] + kKvSlack;
+            for (int i = 0; i < 4; ++i) above |= s[x][nt][i] >= m[nt][i & 1] + kKvSlack;
         if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)

@@ -700,6 +700,11 @@ __global__ void __launch_bounds__((KvPromptShape<D, SUB>::kThreads), 1) k_kv_pro
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&bars.q_full[t]));
       }
+      // A sum over D channels of q and K as they are multiplied is below 2^29, so with a factor up to 2^-7 scores stay below
+      // 2^22, and the reference, which is the rounding of a product, within 2^-3 of it.  Larger ones are rounded themselves first:
+      // what the reference's rounding alone left of a score could be more than f16 holds as a power of two.
+      const bool large = __any_sync(0xFFFFFFFFu, mult > 0x1p-7f);
+      const float by = large ? 1.0f : mult;
       float m = kKvNone, l = 0.0f;
       for (int j = sub.j0; j < sub.j1; ++j) {
         const int buffer = kSub == 1 ? j & 1 : t;
@@ -734,16 +739,21 @@ __global__ void __launch_bounds__((KvPromptShape<D, SUB>::kThreads), 1) k_kv_pro
           tmem_load32(ts + c0, v);
           tmem_load32(ts + c0 + 32, v + 32);
           tmem_load_wait(v);
+          if (large) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) v[c] *= mult;
+          }
           float tops[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
           for (int c = 4; c < 64; c += 4)
 #pragma unroll
             for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], v[c + k]);
           float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-          top = top == -INFINITY ? top : top * mult;  // (-inf: no score)
-          const bool above = top > m + kKvSlack;
+          top = top == -INFINITY ? top : top * by;  // (-inf: no score)
+          const bool above = top >= m + kKvSlack;
           if (__any_sync(0xFFFFFFFFu, above)) {
-            const float moved = !above ? m : m == kKvNone ? top : m + ceilf(top - m);
+            // (from 2^21 on, also at the row's first score, m + ceil(top - m) is not near top)
+            const float moved = !above ? m : fmaxf(fabsf(m), fabsf(top)) > 0x1p21f ? top : m + ceilf(top - m);
             const float f = exp2_fast(m - moved);
             m = moved;
             l *= f;
@@ -774,7 +784,7 @@ __global__ void __launch_bounds__((KvPromptShape<D, SUB>::kThreads), 1) k_kv_pro
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
               const int at = 32 * half + 2 * c;
-              float2 e = fma2(make_float2(v[at], v[at + 1]), make_float2(mult, mult), make_float2(off, off));
+              float2 e = fma2(make_float2(v[at], v[at + 1]), make_float2(by, by), make_float2(off, off));
               e = make_float2(exp2_fast(e.x), exp2_fast(e.y));
               sum[c & 1] = add2(sum[c & 1], e);
               w[c] = bits_of(__floats2half2_rn(e.x, e.y));

@@ -77,7 +77,7 @@ def test_amax_and_scale_that_are_none(D, group, seqs, window):
 
 
 @pytest.mark.parametrize("size", [1e3, 3e7, 2e8, 5e9, 1e20, 2e30, 3e36])
-@pytest.mark.parametrize("D,q", [(64, 1), (128, 4), (256, 1)])
+@pytest.mark.parametrize("D,q", [(64, 1), (128, 4), (256, 1), (64, 30), (128, 30), (128, 200), (256, 200)])
 def test_scores_of_any_magnitude(D, q, size):
     """Scores of `size` times one of E2M1's numbers and no two largest alike: the weights are 1 and 0.  The keys' first channel has
     the number, the queries' is the only one that is not zero, so a score is rounded as a product and not as a sum; the largest comes
@@ -104,3 +104,30 @@ def test_scores_of_any_magnitude(D, q, size):
         assert ((lse[rows].double() - top).abs() <= 2.0 ** -20 * top.abs()).all(), (best, low)
         v = torch.stack([values(p.cache, p.table[0, :-(-n // 32)], h, n, 1, 1.0)[best] for h in (0, 0, 1, 1)])
         assert torch.equal(out[rows].double(), v.to(torch.bfloat16).double().expand(len(rows), -1, -1)), (best, low)
+
+
+@pytest.mark.parametrize("D,q", [(64, 1), (128, 4), (256, 1), (64, 30), (128, 30), (128, 200), (256, 200)])
+def test_scores_a_step_of_fp32_apart(D, q):
+    """Scores of 2^10 to 2^33 that differ by fp32's step there, by a few of them or not at all, with one value behind every
+    key: whatever its weights are, they add up to one, so out is that value (a weight's 2^-11 does not reach the rounding of a
+    number of 5 bits to bf16's 8)."""
+    n = 700
+    p = Problem([(q, n)], 4, 2, D, 32, group=0, seed=26, scale=1.0, kv_amax=(6.0, 6.0), garbage=False)
+    rec = p.cache[p.table[0, :-(-n // 32)].long()]
+    rec[..., :8 * D] = 0
+    rec[..., 16 * D:] = 0x38  # 1
+    k, v = (rec[..., 8 * D * i:8 * D * (i + 1)].unflatten(-1, (16, D // 2)) for i in range(2))
+    g = torch.Generator("cuda").manual_seed(27)
+    # channel 0: 4, 2^10 as it is multiplied; channel 1: 0 to 6 times 2^-14, half of fp32's step there
+    k[..., 0] = 6 | torch.randint(0, 8, k.shape[:-1], generator=g, device="cuda", dtype=torch.uint8) << 4
+    v[:] = torch.randint(0, 256, (D // 2,), generator=g, device="cuda", dtype=torch.uint8)
+    p.cache[p.table[0, :-(-n // 32)].long()] = rec
+    want = values(p.cache, p.table[0, :-(-n // 32)], 0, n, 1, 1.0)[0].to(torch.bfloat16).expand(p.T, 4, D)
+    p.q.zero_()
+    p.q[..., 0] = 1.0
+    p.q[..., 1] = 2.0 ** -22  # (2^-14 where the first is 2^8: a number of f16)
+    for e in range(10, 34):
+        for m in (1.0, 1.37, 1.9):
+            p.scale = m * 2.0 ** (e - 2)
+            out, lse = p.call()
+            assert torch.equal(out, want) and torch.isfinite(lse).all(), (e, m)
