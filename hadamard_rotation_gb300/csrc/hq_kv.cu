@@ -18,6 +18,7 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 
 constexpr int64_t kMaxTokens = (int64_t{1} << 31) - 1024;  // counts of tokens and of rows (token, head)
 constexpr int64_t kMaxHeads = 4096;
+constexpr int64_t kMaxSequences = int64_t{1} << 20;  // a warp's way over idle ones ends long before a wait gives up
 constexpr int64_t kMaxKeys = int64_t{1} << 25;  // of a sequence: its rows' way over them ends before a wait gives up
 
 // Heads, head size, rotation group, pages.
@@ -229,7 +230,7 @@ hq_status hq_kv_attention_nvfp4(const void* q, int64_t ld_q, int64_t T, int64_t 
                                 void* workspace, hq_stream stream) {
   const hq_status st = check_cache(kv_heads, D, group, pages, page_size);
   if (st != HQ_OK) return st;
-  if (T < 0 || T > kMaxTokens || S < 0 || S > kMaxTokens || q_heads < 1 || q_heads > kMaxHeads || q_heads % kv_heads != 0)
+  if (T < 0 || T > kMaxTokens || S < 0 || S > kMaxSequences || q_heads < 1 || q_heads > kMaxHeads || q_heads % kv_heads != 0)
     return HQ_ERR_SHAPE;
   if (T * (q_heads / kv_heads) > kMaxTokens || max_q < 0 || window < 0) return HQ_ERR_SHAPE;
   if (table_pages < 0 || ld_table < table_pages || table_pages > kMaxKeys / page_size || (table_pages > 0 && pages == 0))

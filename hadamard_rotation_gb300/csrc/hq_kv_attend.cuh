@@ -256,7 +256,7 @@ struct KvWalk {
         do {
           seq = seqs.get(p, ++s);
           span = KvSpan<ROWS>(p, seq);
-        } while (span.tiles == 0);  // (there is work left, so a sequence with rows)
+        } while (span.tiles == 0 && s < p.S);  // (there is work left, so a sequence with rows)
       }
     }
     return true;

@@ -178,7 +178,7 @@ __device__ __forceinline__ KvStart kv_plan(const KvAttendParams& p, int64_t (&su
   }
 }
 
-// The segments of a share: an item each, or the part of one that lies in the share.
+// The segments of a share: an item each, or the part of one that lies in the share.  For a whole warp.
 template <int ROWS, int KEYS>
 struct KvPromptWalk {
   const KvAttendParams& p;
@@ -217,8 +217,15 @@ struct KvPromptWalk {
         tile = 0;
         if (++head == p.kv_heads) {
           head = 0;
-          do seq = kv_seq(p, ++s);
-          while (seq.nq == 0);  // (there is work left, so a sequence with rows)
+          // The next sequence with rows (there is work left), 32 at a time: the other roles wait for it.
+          const int lane = threadIdx.x & 31;
+          for (++s; s < p.S; s += 32) {
+            const uint32_t rows = __ballot_sync(0xFFFFFFFFu, s + lane < p.S && kv_seq(p, s + lane).nq > 0);
+            if (!rows) continue;
+            s += __ffs(rows) - 1;
+            seq = kv_seq(p, s);
+            break;
+          }
         }
       }
       reach = kv_reach<ROWS, KEYS>(p, seq, tile);

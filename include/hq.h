@@ -583,7 +583,7 @@ HQ_API hq_status hq_kv_read_nvfp4(const uint8_t* cache, int64_t pages, int64_t p
  *   page_table : int32 [S, table_pages] on the device, rows ld_table apart: page of the tokens page_size * i .. of the
  *          sequence (others than 0 .. pages - 1 are clamped).  Entries behind a sequence's last page are not read.
  *          table_pages * page_size is at most 2^25.
- *   kv_len int32 [S], q_start int32 [S + 1] on the device, clamped to table_pages * page_size and to 0 .. T.
+ *   kv_len int32 [S], q_start int32 [S + 1] on the device, clamped to table_pages * page_size and to 0 .. T.  S is at most 2^20.
  *   max_q : the most queries of a sequence, as far as the host knows (T is always right).  It chooses the kernel;
  *          the result is defined for any value.
  *   window : 0 for none.    lse : float [T, q_heads], or NULL.

@@ -131,3 +131,20 @@ def test_scores_a_step_of_fp32_apart(D, q):
             p.scale = m * 2.0 ** (e - 2)
             out, lse = p.call()
             assert torch.equal(out, want) and torch.isfinite(lse).all(), (e, m)
+
+
+@pytest.mark.parametrize("seqs", [[(1, 900), (2, 70), (1, 0), (1, 300)], [(90, 200), (1, 30), (200, 700), (3, 3)]])
+@pytest.mark.parametrize("D", [64, 256])
+def test_the_most_sequences(seqs, D):
+    """2^20 sequences, four of them with queries: the same shares and so the same bits as without the others."""
+    p = Problem(seqs, 2, 1, D, 16, seed=28)
+    want = p.call()
+    S, at = 2 ** 20, [0, 5, 2 ** 19 + 3, 2 ** 20 - 1]
+    table, kv_len = (torch.zeros((S, *t.shape[1:]), dtype=torch.int32, device="cuda") for t in (p.table, p.kv_len))
+    counts = torch.zeros(S + 1, dtype=torch.int64, device="cuda")
+    for i, s in enumerate(at):
+        table[s], kv_len[s], counts[s + 1] = p.table[i], p.kv_len[i], seqs[i][0]
+    p.table, p.kv_len, p.q_start = table, kv_len, counts.cumsum(0).int()
+    for a, b in zip(p.call(), want):
+        assert torch.equal(a, b)
+    assert hq.hq_read_fault() == 0
