@@ -398,7 +398,7 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
   bool ok = true;
 
   if (warp == kWarps) {  // the producer: lane l copies every 32nd record
-    uint32_t k = 0;      // records so far
+    uint32_t k = 0, last = 0;  // records so far, and of a batch that a wait gave up in
     const uint64_t policy = l2_stream_policy();
     const KvShare share = kv_share<kRows>(p, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x));
     Walk walk(p, share.w0, share.w1);
@@ -437,27 +437,38 @@ __global__ void __launch_bounds__((KvAttendShape<D, NT>::kThreads), 1) k_kv_atte
         asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(id) : "l"(p.table + g.s * p.ld_table + (u0 + lane) / p.page_units));
       return kBatch;
     };
-    for (Next next = advance(true); next == kBatch;) {
-      const int u = u0 + lane, n = min(32, g.u1 - u0), head = g.head, page = id;
-      next = advance(false);
+    for (Next next = kLater; next != kNone;) {
+      const int u = u0 + lane, n = next == kBatch ? min(32, g.u1 - u0) : 0, head = g.head, page = id;
+      next = advance(n == 0);
+      if (n == 0) continue;
       const int64_t at = min(static_cast<int64_t>(max(page, 0)), p.pages - 1);
       const uint8_t* const src = p.cache + ((at * p.kv_heads + head) * p.page_units + u % p.page_units) * R::kBytes;
       const uint32_t slot = (k + lane) % kSlots, pass = (k + lane) / kSlots & 1;
+      bool issued = false;
       for (int part = 0; part < 4; ++part) {  // eight at a time: the first are on their way before the last have a slot
         if (lane < n && lane / 8 == part && ok) {
           ok = mbar_wait(smem_addr(&empty[slot]), pass ^ 1);
           if (ok) tma_load(smem_addr(kv_smem) + slot * S::kUnit, src, R::kBytes, smem_addr(&full[slot]), policy);
+          issued = ok;
         }
         __syncwarp();
       }
+      if (!__all_sync(0xFFFFFFFFu, ok)) {  // a wait gave up: the last copy into each of these places lands (bounded)
+        if (issued) mbar_wait(smem_addr(&full[slot]), pass);
+        else if (lane < n && lane < kSlots && k + lane >= kSlots) mbar_wait(smem_addr(&full[slot]), pass ^ 1);
+        ok = false;
+        last = n;
+        break;
+      }
       k += n;
-      if (next == kLater) next = advance(true);
     }
     if (lane == 0) kv_cuts<D>(p.part)[blockIdx.x] = cut;
-    // what is on its way lands before the CTA may end
-    for (uint32_t i = lane; i < kSlots && i < k; i += 32) {
+    // What else is on its way lands (bounded) before the CTA may end, whoever has given up: the last copies into the other
+    // places.
+    for (uint32_t i = lane; i + last < kSlots && i < k; i += 32) {
       const uint32_t seq = k - 1 - i;
-      if (ok) ok = mbar_wait(smem_addr(&full[seq % kSlots]), seq / kSlots & 1);
+      const bool landed = mbar_wait(smem_addr(&full[seq % kSlots]), seq / kSlots & 1);
+      ok = ok && landed;
     }
   } else {
     const int gq = lane >> 2, c = lane & 3;
