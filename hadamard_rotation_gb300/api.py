@@ -516,7 +516,7 @@ def hq_kv_append_nvfp4(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
                        kv_amax: torch.Tensor, cache: torch.Tensor, group: int = 16, interleaved: bool = False,
                        q_out: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor | None:
     """Puts T tokens into a paged NVFP4 cache, with the position rotation on the way; returns q_out, bfloat16
-    [T, q_heads, D], rotated like the keys (None without q).
+    [T, q_heads, D], rotated like the keys (None without q).  q_out may not overlap q, k or v.
 
     q [T, q_heads, D], k, v [T, kv_heads, D] bfloat16 or float32, heads contiguous (views of a fused projection
     will do); cos, sin float32 [rows, rotary / 2] and positions int32 [T], or None for no position rotation
@@ -552,7 +552,8 @@ def hq_kv_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, page_table: torc
     q bfloat16 [T, q_heads, D] as hq_kv_append_nvfp4 returns it; page_table int32 [S, pages of a sequence], kv_len int32
     [S], q_start int32 [S + 1]: sequence s has the queries q_start[s] .. q_start[s + 1] - 1, which are the last of its
     kv_len[s] tokens.  ``group``: the cache's rotation.  ``window``: keys that a query sees at most (0: all).
-    ``max_q``: the most queries of a sequence, if known.  Rows of no sequence are left as they are in ``out``."""
+    ``max_q``: the most queries of a sequence, if known.  Rows of no sequence are left as they are in ``out``, which may not
+    overlap q."""
     return (_calls or _load_calls()).kv_attention(q, cache, page_table, kv_len, q_start, kv_amax, scale, group, window,
                                                    -1 if max_q is None else max_q, out, return_lse, stream)
 

@@ -346,6 +346,13 @@ struct Heads {
                     "] on cuda:" + std::to_string(cache.index) + " with contiguous heads");
     ld = t->size(0) > 1 ? t->stride(0) : t->size(1) * cache.D;
   }
+  // `out`, contiguous, reaches into what lies between its first and last element.
+  bool meets(const at::Tensor& out) const {
+    if (t->numel() == 0 || out.numel() == 0) return false;
+    const auto *a = static_cast<const char*>(t->const_data_ptr()), *b = static_cast<const char*>(out.const_data_ptr());
+    const int64_t span = (t->size(0) - 1) * ld + t->size(1) * t->size(2);
+    return a < b + out.numel() * out.element_size() && b < a + span * t->element_size();
+  }
 };
 
 // (q, k, v, cos, sin, positions, slots, kv_amax, cache, group, interleaved, q_out, stream)
@@ -387,6 +394,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else {
       out = a[11] == Py_None ? empty({T, heads, cache.D}, at::kBFloat16, cache.t, stream)
                              : given(a[11], {T, heads, cache.D}, at::kBFloat16, cache.index, "q_out");
+      if (k.meets(out) || v.meets(out) || Heads(a[0], T, -1, cache, "q").meets(out))
+        throw Refused("q_out may not overlap q, k or v");
     }
     run(cache.index, "hq_kv_append_nvfp4", [&] {
       return hq_kv_append_nvfp4(pq, ld_q, k.t->const_data_ptr(), k.ld, v.t->const_data_ptr(), v.ld, dtype_of(type), T, heads,
@@ -447,6 +456,7 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Stream stream(a[12], cache.index);
     const at::Tensor out = a[10] == Py_None ? empty({T, heads, cache.D}, at::kBFloat16, cache.t, stream)
                                             : given(a[10], {T, heads, cache.D}, at::kBFloat16, cache.index, "out");
+    if (q.meets(out)) throw Refused("out may not overlap q");
     at::Tensor lse;
     if (with_lse) lse = empty({T, heads}, at::kFloat, cache.t, stream);
     const at::Tensor work = workspace(hq_kv_attention_workspace_bytes(heads, cache.kv_heads, cache.D, T, max_q < 0 ? T : max_q), cache.t, stream);
