@@ -148,3 +148,55 @@ def test_the_most_sequences(seqs, D):
     for a, b in zip(p.call(), want):
         assert torch.equal(a, b)
     assert hq.hq_read_fault() == 0
+
+
+@pytest.mark.parametrize("D,group", [(64, 0), (64, 16), (128, 16), (256, 0), (256, 256)])
+@pytest.mark.parametrize("window", [0, 24, 700])
+@pytest.mark.parametrize("density", [0.04, 0.0003])  # of the blocks of 16 values
+def test_many_nan_values(D, group, window, density):
+    """NaN in any number of the values: the channels of the rows that see one, and nothing else, to the bit."""
+    seqs, page = [(200, 3000), (700, 1530), (40, 41), (1, 600)], 48
+    p = Problem(seqs, 2, 2, D, page, group, window, seed=29)
+    base, spoiled, width = p.cache.clone(), p.cache.clone(), group or 16
+    hit = torch.zeros((p.T, 2, D), dtype=torch.bool, device="cuda")
+    g = torch.Generator("cuda").manual_seed(30)
+    for i, (nq, n) in enumerate(seqs):
+        bad = torch.rand((n, 2, D // 16), generator=g, device="cuda") < density
+        bad[n // 2, 1, 0] = True
+        t, h, b = bad.nonzero(as_tuple=True)
+        at = (p.table[i, t // page].long(), h, t % page // 16, 17 * D + t % 16 * (D // 16) + b)
+        base[at], spoiled[at] = 0, 0x7F
+        pos, key = torch.arange(n - nq, n, device="cuda")[:, None], torch.arange(n, device="cuda")[None]
+        seen = (key <= pos) & ((key > pos - window) if window else True)
+        some = (seen.float() @ bad.flatten(1).float()).view(nq, 2, D // 16).repeat_interleave(16, -1) > 0
+        hit[int(p.q_start[i]):int(p.q_start[i + 1])] = some.unflatten(-1, (-1, width)).any(-1, keepdim=True).expand(-1, -1, -1, width).flatten(2)
+    p.cache = base
+    want, want_lse = p.call()
+    p.cache = spoiled
+    got, lse = p.call()
+    assert hit.any() and got[hit].isnan().all()
+    assert torch.equal(got[~hit], want[~hit]) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("D,share,S,nq", [(256, 32, 1, 608), (64, 4, 152, 32)])
+def test_a_nan_in_the_longest_context(D, share, S, nq):
+    """2^25 keys, whole items of them: looking for the NaN ends before the other roles' waits do."""
+    n, page = 2 ** 25, 4096
+    cache = torch.randint(0, 256, (n // page, 1, page // 16, 18 * D), dtype=torch.uint8, device="cuda")
+    cache[..., 16 * D:] = 0x38
+    table = torch.arange(n // page, device="cuda").int().repeat(S, 1)
+    q = torch.randn((S * nq, share, D), device="cuda").to(torch.bfloat16)
+    kv_len = torch.full((S,), n, dtype=torch.int32, device="cuda")
+    q_start = torch.arange(S + 1, device="cuda").int() * nq
+    amax = torch.full((2,), 6.0, device="cuda")
+    out = []
+    for scale in (0, 0x7F):
+        cache[0, 0, 0, 17 * D] = cache[-1, 0, -1, 18 * D - 1] = scale  # the first token's first block, the last one's last
+        out.append(hq.hq_kv_attention_nvfp4(q, cache, table, kv_len, q_start, amax, D ** -0.5 / 16, group=0, max_q=nq))
+    assert hq.hq_read_fault() == 0
+    hit = torch.zeros_like(q, dtype=torch.bool)
+    hit[..., :16] = True
+    hit[nq - 1::nq, :, -16:] = True
+    want, got = out
+    assert got[hit].isnan().all() and torch.isfinite(want).all()
+    assert torch.equal(got[~hit], want[~hit])
