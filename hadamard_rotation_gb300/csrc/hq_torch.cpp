@@ -394,7 +394,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else {
       out = a[11] == Py_None ? empty({T, heads, cache.D}, at::kBFloat16, cache.t, stream)
                              : given(a[11], {T, heads, cache.D}, at::kBFloat16, cache.index, "q_out");
-      if (k.meets(out) || v.meets(out) || Heads(a[0], T, -1, cache, "q").meets(out))
+      if (a[11] != Py_None && (k.meets(out) || v.meets(out) || Heads(a[0], T, -1, cache, "q").meets(out)))
         throw Refused("q_out may not overlap q, k or v");
     }
     run(cache.index, "hq_kv_append_nvfp4", [&] {
@@ -456,7 +456,7 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Stream stream(a[12], cache.index);
     const at::Tensor out = a[10] == Py_None ? empty({T, heads, cache.D}, at::kBFloat16, cache.t, stream)
                                             : given(a[10], {T, heads, cache.D}, at::kBFloat16, cache.index, "out");
-    if (q.meets(out)) throw Refused("out may not overlap q");
+    if (a[10] != Py_None && q.meets(out)) throw Refused("out may not overlap q");
     at::Tensor lse;
     if (with_lse) lse = empty({T, heads}, at::kFloat, cache.t, stream);
     const at::Tensor work = workspace(hq_kv_attention_workspace_bytes(heads, cache.kv_heads, cache.D, T, max_q < 0 ? T : max_q), cache.t, stream);
