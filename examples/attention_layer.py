@@ -45,7 +45,8 @@ class Attention:
         return (t.unflatten(1, (-1, self.D)) for t in y.split([h * self.D for h in self.heads], 1))
 
     def step(self, x, positions, slots, page_table, kv_len, q_start, max_q=None, out=None):
-        """The layer's output [T, width] for T tokens; kv_len counts them too."""
+        """The layer's output [T, width] for T tokens; kv_len counts them too.  max_q, the most tokens of a request, chooses the
+        attention's kernel for all of them: 1 for a step of single tokens (without it, they take three times as long)."""
         q = hq.hq_kv_append_nvfp4(*self.project(x), *self.tables, positions, slots, self.kv_amax, self.cache, GROUP)
         a = hq.hq_kv_attention_nvfp4(q, self.cache, page_table, kv_len, q_start, self.kv_amax, self.D ** -0.5, GROUP,
                                      max_q=max_q, out=out)
@@ -115,7 +116,7 @@ def main():
     page_table = torch.randperm(64, device="cuda").int()[:60].view(3, 20)
     before, new = [0, 0, 0], [200, 17, 64]
     x = torch.randn(sum(new), width, device="cuda").to(torch.bfloat16)
-    y = layer.step(x, *places(page_table, page_size, before, new))
+    y = layer.step(x, *places(page_table, page_size, before, new), max_q=max(new))
     print("prompts:", tuple(y.shape))
     decode = Decode(layer, 4, 20, width)
     x = y[torch.tensor(new).cumsum(0) - 1]  # (as if the layer's output were the next token)

@@ -530,8 +530,8 @@ def hq_kv_append_nvfp4(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
 def hq_kv_read_nvfp4(cache: torch.Tensor, slots: torch.Tensor, kv_amax: torch.Tensor, group: int = 0,
                      out_dtype: torch.dtype = torch.bfloat16, k: torch.Tensor | None = None,
                      v: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
-    """The values of the cached tokens at ``slots``: (k, v) [T, kv_heads, D], zeros where a slot is none.  ``group``:
-    the rotation to undo (0: as stored)."""
+    """The values of the cached tokens at ``slots``: (k, v) [T, kv_heads, D], zeros where a slot is none.  ``group``: the
+    rotation to undo, that of the call that stored them; 0, the default here and not there: as stored, still rotated."""
     return (_calls or _load_calls()).kv_read(cache, slots, kv_amax, group, out_dtype, k, v, stream)
 
 
@@ -552,7 +552,9 @@ def hq_kv_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, page_table: torc
     q bfloat16 [T, q_heads, D] as hq_kv_append_nvfp4 returns it; page_table int32 [S, pages of a sequence], kv_len int32
     [S], q_start int32 [S + 1]: sequence s has the queries q_start[s] .. q_start[s + 1] - 1, which are the last of its
     kv_len[s] tokens.  ``group``: the cache's rotation.  ``window``: keys that a query sees at most (0: all).
-    ``max_q``: the most queries of a sequence, if known.  Rows of no sequence are left as they are in ``out``, which may not
+    ``max_q``: the most queries of a sequence, the number of tokens if not given.  It chooses the kernel for the whole call: a
+    step of single tokens names it (1; without, 64 requests of some 8192 tokens take 513 us in place of 154), and single
+    tokens beside a prompt are better off in a call of their own.  Rows of no sequence are left as they are in ``out``, which may not
     overlap q."""
     return (_calls or _load_calls()).kv_attention(q, cache, page_table, kv_len, q_start, kv_amax, scale, group, window,
                                                    -1 if max_q is None else max_q, out, return_lse, stream)

@@ -105,7 +105,8 @@ cudaError_t launch_prompt(const hq::KvAttendParams& p, int sms, cudaStream_t str
 //   64 sequences of 300 keys, D = 128      39 / 44 / 56      56 / 45 / 57      77 / 44 / 57       46 / 60
 //   1 sequence of 65536 keys, D = 128      34 / 56 / 86      52 / 56 / 84      71 / 56 / 86       56 / 85
 //   4 sequences of 4000 keys, D = 128                                                                            55 / 55
-// and of 4 sequences of 1000 tokens behind 4000 (4000 rows) one tile 346, two 264.
+// and of 4 sequences of 1000 tokens behind 4000 (4000 rows) one tile 346, two 264.  One answer for all sequences of a call: 63
+// single tokens of some 8192 keys take 153 by themselves and a prompt of 2048 tokens 65, both in one call 546.
 bool few_rows(int64_t T, int64_t max_q, int64_t share, int64_t D) {
   return (max_q < T ? max_q : T) <= (D == 256 ? 32 : 16) / share;
 }

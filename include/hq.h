@@ -584,8 +584,10 @@ HQ_API hq_status hq_kv_read_nvfp4(const uint8_t* cache, int64_t pages, int64_t p
  *          sequence (others than 0 .. pages - 1 are clamped).  Entries behind a sequence's last page are not read.
  *          table_pages * page_size is at most 2^25.
  *   kv_len int32 [S], q_start int32 [S + 1] on the device, clamped to table_pages * page_size and to 0 .. T.  S is at most 2^20.
- *   max_q : the most queries of a sequence, as far as the host knows (T is always right).  It chooses the kernel;
- *          the result is defined for any value.
+ *   max_q : the most queries of a sequence, as far as the host knows (T is always right).  It chooses the kernel, one for all
+ *          sequences of the call; the result is defined for any value.  Single tokens in the kernel that prompts take cost
+ *          three times as much: a step of single tokens names its max_q of 1, and single tokens beside a prompt are better off in a
+ *          call of their own.
  *   window : 0 for none.    lse : float [T, q_heads], or NULL.
  *   workspace : hq_kv_attention_workspace_bytes(q_heads, kv_heads, D, T, max_q) bytes, 16-byte aligned; contents need
  *          no preparation.  Calls that may run at the same time need different ones.
@@ -611,9 +613,9 @@ HQ_API int hq_last_cuda_error(void);
 /*
  * hq_read_fault -- the library's device fault word on the current device (synchronous: waits
  * for all work on the device first).  0 means no kernel recorded a fault.  Bit 0 (value 1):
- * a kernel's wait for one of its own shared-memory tile copies exceeded about one second; that
- * warp stopped early, so the outputs of the affected call are incomplete.  With `clear` non-zero
- * the word is reset to 0 after reading.
+ * a kernel's wait for one of its own copies into shared memory, or for its own tensor-core products or other warps or
+ * CTAs, exceeded about one second; what waited stopped early, so the outputs of the affected call are incomplete.  With
+ * `clear` non-zero the word is reset to 0 after reading.
  */
 HQ_API hq_status hq_read_fault(unsigned int* fault, int clear);
 
